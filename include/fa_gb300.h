@@ -54,7 +54,8 @@ enum {
   FA_ERR_ARCH = -7,           /* the current device is not a compute capability 10.3 GPU     */
   FA_ERR_BAD_SCALE = -8,      /* scale is not a finite number > 0                            */
   FA_ERR_WORKSPACE = -9,      /* the workspace passed to fa_fwd_host or fa_bwd is too small  */
-  FA_ERR_SCRATCH = -10        /* the kernel needs more scratch than fa_fwd_noalloc provides  */
+  FA_ERR_SCRATCH = -10,       /* the kernel needs more scratch than fa_fwd_noalloc provides  */
+  FA_ERR_BAD_BATCH = -11      /* page_table, cu_rows or kv_lens named what is not there (reported by fa_status) */
 };
 
 /*
@@ -275,11 +276,123 @@ int fa_fwd_noalloc(const void* q, const void* k, const void* v, void* o, float* 
                    int B, int H, int N, int d, float scale, int causal, void* stream);
 
 /*
+ * Paged key/value cache.  (No counterpart in the pages, whose K and V are
+ * contiguous and of one length: these entry points are the serving form of the
+ * same attention.)
+ *
+ * A cache is a pool of pages; a page holds page_size tokens of every key/value
+ * head, as K and V [num_pages][heads][page_size][d] (a page in the place of a
+ * batch).  Element (page, h, slot, c) sits at page*s[0] + h*s[1] + slot*s[2] + c,
+ * s = k_stride / v_stride; scale (page, h, slot) at (page*heads + h)*page_size + slot.
+ *
+ * Formats: bf16 pages (k_scale = v_scale = NULL), or e4m3 pages in which a row
+ * (one token, one head) has a power-of-two scale of its own, kept as its biased
+ * exponent: real value = e4m3 value * 2^(scale - 127), scale 255 = NaN.  The
+ * scale is the smallest power of two that brings the row's largest magnitude
+ * to 448 (e4m3's largest value) or less, so dividing by it is exact, a written
+ * value is rounded once, and what is read back is exact in bf16.
+ */
+typedef struct fa_paged_cache {
+  void* k;                  /* pages of keys, bf16 or e4m3, 16-byte aligned                          */
+  void* v;                  /* pages of values                                                       */
+  unsigned char* k_scale;   /* e4m3 pages: [num_pages][heads][page_size]; bf16 pages: NULL           */
+  unsigned char* v_scale;
+  long long k_stride[3];    /* element strides {page, head, slot}, multiples of 16 bytes             */
+  long long v_stride[3];
+  int num_pages;            /* >= 1                                                                  */
+  int page_size;            /* tokens a page: 16, 32, 64, 128, 256, 512 or 1024                      */
+  int heads;                /* key/value heads                                                       */
+  int d;                    /* 32, 64, 128 or 256                                                    */
+} fa_paged_cache;
+
+/*
+ * The sequences of a call (device arrays, read on the device only, so a
+ * captured graph replays with new contents).  Sequence b has kv_lens[b] tokens,
+ * its new ones included; its rows in the token-major tensors are
+ * cu_rows[b] .. cu_rows[b+1]-1, and row cu_rows[b] + i stands for the token at
+ * position kv_lens[b] - n_b + i, n_b = cu_rows[b+1] - cu_rows[b].  Position p
+ * is held in slot p % page_size of page page_table[b*table_stride + p / page_size].
+ * Rows behind cu_rows[B] are left as they are.  A row at a negative position
+ * stands for no token: it is neither written nor read and attends to nothing.
+ *
+ * What is not there is never touched: an entry of page_table outside
+ * [0, num_pages) where a page is needed, a length beyond max_pages*page_size,
+ * rows outside [0, rows) or cu_rows that decrease.  The write skips such a row,
+ * the read leaves it, the attention rows of that sequence are unspecified, and
+ * fa_status() reports FA_ERR_BAD_BATCH.  Entries that no position needs are
+ * not looked at.
+ */
+typedef struct fa_paged_batch {
+  const int* page_table;    /* device, [B] rows of max_pages entries, table_stride ints apart        */
+  const int* cu_rows;       /* device, [B + 1], cu_rows[0] >= 0, not decreasing                      */
+  const int* kv_lens;       /* device, [B], >= 0                                                     */
+  long long table_stride;
+  int max_pages;            /* entries of a row of page_table, >= 1                                  */
+  int B;                    /* sequences, >= 1                                                       */
+  int rows;                 /* rows of the token-major tensors, >= 0 (0: nothing is done)            */
+} fa_paged_batch;
+
+/*
+ * fa_paged_write - writes the rows' K and V into the cache, where fa_paged_fwd
+ * finds them (quantised for e4m3 pages).  A row of e4m3 pages that holds an
+ * infinity or a NaN is stored as scale 255 and reads back as NaN throughout; a
+ * row of zeros has scale 0.  Two rows of one call must not name the same slot
+ * (else which of them is left, for each 32 bytes, is unspecified).
+ *
+ *   k, v      : bf16, element (row, h, c) at row*s[0] + h*s[1] + c, s = k_stride /
+ *               v_stride: {row, head} element strides, multiples of 8; 16-byte aligned.
+ *   Errors as fa_fwd_strided's.
+ */
+int fa_paged_write(const fa_paged_cache* cache, const fa_paged_batch* batch, const void* k,
+                   const long long* k_stride, const void* v, const long long* v_stride, void* stream);
+
+/*
+ * fa_paged_read - the reverse: the tokens that the rows stand for, as bf16 rows
+ * of k and v (n_b = kv_lens[b] reads whole sequences).  Values of e4m3 pages
+ * come back exactly as they are stored.
+ */
+int fa_paged_read(const fa_paged_cache* cache, const fa_paged_batch* batch, void* k, const long long* k_stride,
+                  void* v, const long long* v_stride, void* stream);
+
+/* fa_paged_fwd_workspace_bytes - size of the device workspace of fa_paged_fwd
+ * for B sequences, `heads` key/value heads and head dimension d.  It does not
+ * depend on any length.  Returns 0 for invalid shapes. */
+size_t fa_paged_fwd_workspace_bytes(int B, int heads, int d);
+
+/*
+ * fa_paged_fwd - attention of the rows (queries of the new tokens, whose K and
+ * V are in the cache already) over the cached keys of their sequences: any mix
+ * of single tokens, chunks and whole prompts.
+ *
+ *   q, o      : bf16, [rows] x q_heads x d, element (row, h, c) at row*s[0] + h*s[1] + c,
+ *               s = q_stride / o_stride as in fa_paged_write.  q_heads is a multiple of the
+ *               cache's heads, at most 128 times as many: head h reads key/value head
+ *               h / (q_heads / heads).
+ *   lse       : fp32 [q_heads][rows], contiguous: L of each row and head (natural log).
+ *   max_rows  : an upper bound of n_b, known to the host (it chooses the kernels).  Rows of a
+ *               sequence that has more are left as they are and fa_status reports FA_ERR_BAD_BATCH.
+ *   causal    : nonzero: row i sees the keys at positions <= its own.  Zero: all kv_lens[b].
+ *   workspace : 256-byte aligned, at least fa_paged_fwd_workspace_bytes bytes; contents on entry
+ *               ignored.  Calls that may run at the same time need workspaces of their own.
+ *   A row that sees no key has o = 0 and L = -infinity.  Keys that a row does not see never
+ *   reach it, whatever they hold (NaN and infinities too), nor do slots behind kv_lens[b].
+ *   o and lse must not overlap each other, q or the cache.
+ *
+ * Arithmetic: fp32 softmax state and sums; bf16 products with fp32 accumulation (e4m3 pages: see
+ * the kernels); o rounded to bf16 once at the end.  Results do not depend on what else runs:
+ * no atomics, and partial results are joined in a fixed order.
+ */
+int fa_paged_fwd(const void* q, const long long* q_stride, const fa_paged_cache* cache, const fa_paged_batch* batch,
+                 void* o, const long long* o_stride, float* lse, int q_heads, int max_rows, float scale, int causal,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * fa_status - synchronises `stream`, then reads and clears the device status
  * word of the current device, and the status word of fa_fwd_noalloc's static
  * scratch on that device.  Returns FA_OK, FA_ERR_TIMEOUT if a kernel
- * launched since the last call gave up on a bounded wait, or FA_ERR_CUDA if
- * the synchronisation itself failed.
+ * launched since the last call gave up on a bounded wait, FA_ERR_BAD_BATCH if
+ * none did but one was given a batch that names what is not there, or
+ * FA_ERR_CUDA if the synchronisation itself failed.
  */
 int fa_status(void* stream);
 

@@ -31,6 +31,10 @@ _SIGNATURES = {
     "fa_bwd": (_c_int, [_c_void_p] * 9 + [_c_int] * 4 + [_c_float, _c_int, _c_void_p, _c_size_t, _c_void_p]),
     "fa_bwd_strided": (_c_int, [_c_void_p] * 9 + [_c_int] * 5 + [_c_void_p, _c_float, _c_int, _c_void_p, _c_size_t,
                                                                   _c_void_p]),
+    "fa_paged_write": (_c_int, [_c_void_p] * 7),
+    "fa_paged_read": (_c_int, [_c_void_p] * 7),
+    "fa_paged_fwd_workspace_bytes": (_c_size_t, [_c_int] * 3),
+    "fa_paged_fwd": (_c_int, [_c_void_p] * 7 + [_c_int] * 2 + [_c_float, _c_int, _c_void_p, _c_size_t, _c_void_p]),
     "fa_status": (_c_int, [_c_void_p]),
     "fa_selftest_wait": (_c_int, [_c_void_p]),
     "fa_set_wait_limit_ms": (_c_int, [_c_int]),
@@ -152,6 +156,49 @@ def fa_bwd_strided(q, k, v, o, lse, dout, dq, dk, dv, B, H, Nq, Nk, d, strides, 
     arr = (ctypes.c_longlong * 24)(*flat)
     return load().fa_bwd_strided(q, k, v, o, lse, dout, dq, dk, dv, B, H, Nq, Nk, d, ctypes.addressof(arr), scale,
                                  int(bool(causal)), workspace, workspace_bytes, stream)
+
+
+class CPagedCache(ctypes.Structure):
+    """fa_paged_cache: the pool of pages (pointers are device addresses)."""
+
+    _fields_ = [("k", _c_void_p), ("v", _c_void_p), ("k_scale", _c_void_p), ("v_scale", _c_void_p),
+                ("k_stride", ctypes.c_longlong * 3), ("v_stride", ctypes.c_longlong * 3), ("num_pages", _c_int),
+                ("page_size", _c_int), ("heads", _c_int), ("d", _c_int)]
+
+
+class CPagedBatch(ctypes.Structure):
+    """fa_paged_batch: the sequences of a call."""
+
+    _fields_ = [("page_table", _c_void_p), ("cu_rows", _c_void_p), ("kv_lens", _c_void_p),
+                ("table_stride", ctypes.c_longlong), ("max_pages", _c_int), ("B", _c_int), ("rows", _c_int)]
+
+
+def _strides2(st):
+    return (ctypes.c_longlong * 2)(*st)
+
+
+def fa_paged_write(cache, batch, k, k_stride, v, v_stride, stream) -> int:
+    """Rows of k, v into the pages; `cache` and `batch` are CPagedCache / CPagedBatch, strides {row, head} pairs."""
+    return load().fa_paged_write(ctypes.addressof(cache), ctypes.addressof(batch), k, _strides2(k_stride), v,
+                                 _strides2(v_stride), stream)
+
+
+def fa_paged_read(cache, batch, k, k_stride, v, v_stride, stream) -> int:
+    """The tokens that the batch's rows stand for, out of the pages into k, v."""
+    return load().fa_paged_read(ctypes.addressof(cache), ctypes.addressof(batch), k, _strides2(k_stride), v,
+                                _strides2(v_stride), stream)
+
+
+def fa_paged_fwd_workspace_bytes(B, heads, d) -> int:
+    return load().fa_paged_fwd_workspace_bytes(B, heads, d)
+
+
+def fa_paged_fwd(q, q_stride, cache, batch, o, o_stride, lse, q_heads, max_rows, scale, causal, workspace,
+                 workspace_bytes, stream) -> int:
+    """Attention of the batch's rows over the pages; pointers are integers (device addresses)."""
+    return load().fa_paged_fwd(q, _strides2(q_stride), ctypes.addressof(cache), ctypes.addressof(batch), o,
+                               _strides2(o_stride), lse, q_heads, max_rows, scale, int(bool(causal)), workspace,
+                               workspace_bytes, stream)
 
 
 def fa_status(stream) -> int:
@@ -319,6 +366,183 @@ def backward(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
             name = "fa_bwd_strided"
     _check(rc, name)
     return dq, dk, dv
+
+
+class PagedCache:
+    """A pool of key/value pages: k, v [num_pages, heads, page_size, d] (any strides with a contiguous last
+    dimension), bf16, or float8_e4m3fn with k_scale, v_scale uint8 [num_pages, heads, page_size] (a row's scale is
+    2^(byte - 127)).  Holds the tensors; ``PagedCache.empty`` allocates them."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in (torch.bfloat16,
+                                                                                       torch.float8_e4m3fn):
+            raise ValueError("k and v must be [num_pages, heads, page_size, d], both bf16 or both float8_e4m3fn")
+        if not k.is_cuda or k.device != v.device:
+            raise ValueError("k and v must be CUDA tensors of one device")
+        if k.stride(3) != 1 or v.stride(3) != 1:
+            raise ValueError("the last dimension of k and v must be contiguous")
+        fp8 = k.dtype == torch.float8_e4m3fn
+        if fp8 != (k_scale is not None) or fp8 != (v_scale is not None):
+            raise ValueError("float8_e4m3fn pages need k_scale and v_scale, bf16 pages have none")
+        for s in (k_scale, v_scale) if fp8 else ():
+            if s.dtype != torch.uint8 or s.shape != k.shape[:3] or not s.is_contiguous() or s.device != k.device:
+                raise ValueError("k_scale and v_scale must be contiguous uint8 [num_pages, heads, page_size]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.heads, self.page_size, self.d = k.shape
+        self.device, self.dtype = k.device, k.dtype
+        c = CPagedCache()
+        c.k, c.v = k.data_ptr(), v.data_ptr()
+        if fp8:
+            c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+        c.k_stride[:], c.v_stride[:] = k.stride()[:3], v.stride()[:3]
+        c.num_pages, c.page_size, c.heads, c.d = self.num_pages, self.page_size, self.heads, self.d
+        self._c = c
+
+    @classmethod
+    def empty(cls, num_pages, heads, page_size, d, dtype=None, device="cuda"):
+        """A cache of uninitialised pages (bf16 unless dtype is torch.float8_e4m3fn)."""
+        import torch
+
+        dtype = torch.bfloat16 if dtype is None else dtype
+        shape = (num_pages, heads, page_size, d)
+        kv = [torch.empty(shape, dtype=dtype, device=device) for _ in range(2)]
+        if dtype == torch.float8_e4m3fn:
+            kv += [torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)]
+        return cls(*kv)
+
+
+def _paged_batch(cache, page_table, cu_rows, kv_lens, rows):
+    """CPagedBatch of int32 tensors on the cache's device."""
+    import torch
+
+    i32 = torch.int32
+    if page_table.dtype != i32 or cu_rows.dtype != i32 or kv_lens.dtype != i32:
+        raise ValueError("page_table, cu_rows and kv_lens must be int32")
+    dev = cache.device
+    if page_table.device != dev or cu_rows.device != dev or kv_lens.device != dev:
+        raise ValueError("page_table, cu_rows and kv_lens must be on the cache's device")
+    if page_table.dim() != 2 or kv_lens.dim() != 1 or cu_rows.dim() != 1:
+        raise ValueError("page_table must be [B, pages], cu_rows [B + 1] and kv_lens [B]")
+    B, width = page_table.shape
+    if B == 0 or width == 0 or kv_lens.shape[0] != B or cu_rows.shape[0] != B + 1:
+        raise ValueError("page_table must be [B, pages], cu_rows [B + 1] and kv_lens [B], B and pages at least 1")
+    if page_table.stride(1) != 1 or not kv_lens.is_contiguous() or not cu_rows.is_contiguous():
+        raise ValueError("cu_rows, kv_lens and the rows of page_table must be contiguous")
+    b = CPagedBatch()
+    b.page_table, b.cu_rows, b.kv_lens = page_table.data_ptr(), cu_rows.data_ptr(), kv_lens.data_ptr()
+    b.table_stride = page_table.stride(0) if B > 1 else width
+    b.max_pages, b.B, b.rows = width, B, rows
+    return b
+
+
+def _paged_rows(t, name, cache, heads=None):
+    """Checks a token-major bf16 tensor [rows, heads, d]; returns its {row, head} strides."""
+    import torch
+
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != cache.device or t.shape[2] != cache.d or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be a bf16 tensor [rows, heads, d] with the cache's d"
+                         f"{'' if heads is None else ' and heads'}, on its device")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    # Strides of dimensions of one element are never used; torch may report any value for them.
+    n = t.shape
+    head = s[1] if n[1] > 1 else cache.d
+    return (s[0] if n[0] > 1 else head * n[1]), head
+
+
+def paged_write(cache, k, v, page_table, cu_rows, kv_lens):
+    """Write the rows of k, v (bf16 [rows, heads, d]) into the cache's pages, quantised if they are e4m3.
+
+    page_table int32 [B, pages]: the pages of each sequence in order; kv_lens int32 [B]: its tokens, the new ones
+    included; cu_rows int32 [B + 1]: row cu_rows[b] + i is the token at position kv_lens[b] - n_b + i of sequence b,
+    n_b = cu_rows[b + 1] - cu_rows[b].  All on the cache's device (include/fa_gb300.h says what becomes of entries
+    that name nothing).  Returns the cache.  Enqueued on the current stream.
+    """
+    import torch
+
+    ks, vs = _paged_rows(k, "k", cache, cache.heads), _paged_rows(v, "v", cache, cache.heads)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same rows")
+    batch = _paged_batch(cache, page_table, cu_rows, kv_lens, k.shape[0])
+    if k.shape[0] == 0:
+        return cache
+    with torch.cuda.device(cache.device):
+        rc = fa_paged_write(cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs, _stream_handle(torch, cache.device))
+    _check(rc, "fa_paged_write")
+    return cache
+
+
+def paged_read(cache, page_table, cu_rows, kv_lens, rows=None, out=None):
+    """The tokens that the rows stand for (as in paged_write; cu_rows from kv_lens reads whole sequences), as bf16
+    (k, v) [rows, heads, d]: ``out`` = (k, v) if given, else new tensors of ``rows`` rows, whose rows behind
+    cu_rows[B] are zero.  Enqueued on the current stream."""
+    import torch
+
+    if out is None:
+        if rows is None:
+            raise ValueError("paged_read needs rows or out")
+        out = tuple(torch.zeros((rows, cache.heads, cache.d), dtype=torch.bfloat16, device=cache.device)
+                    for _ in range(2))
+    k, v = out
+    ks, vs = _paged_rows(k, "out[0]", cache, cache.heads), _paged_rows(v, "out[1]", cache, cache.heads)
+    if k.shape[0] != v.shape[0] or (rows is not None and rows != k.shape[0]):
+        raise ValueError("the tensors of out must have the same rows")
+    batch = _paged_batch(cache, page_table, cu_rows, kv_lens, k.shape[0])
+    if k.shape[0] == 0:
+        return k, v
+    with torch.cuda.device(cache.device):
+        rc = fa_paged_read(cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs, _stream_handle(torch, cache.device))
+    _check(rc, "fa_paged_read")
+    return k, v
+
+
+def paged_workspace(cache, B):
+    """A workspace for paged_forward calls of B sequences (or fewer) on this cache, one call at a time."""
+    import torch
+
+    return torch.empty(fa_paged_fwd_workspace_bytes(B, cache.heads, cache.d), dtype=torch.uint8, device=cache.device)
+
+
+def paged_forward(q, cache, page_table, cu_rows, kv_lens, max_rows=None, causal: bool = True,
+                  scale: float | None = None, out=None, lse=None, workspace=None):
+    """O, L = attention of the rows of q (bf16 [rows, q_heads, d]) over their sequences' cached keys.
+
+    page_table, cu_rows, kv_lens as in paged_write, which has put the rows' own K and V into the cache.  q_heads is a
+    multiple of the cache's heads.  ``max_rows``: an upper bound of a sequence's rows (default: all rows of q; a
+    serving step passes 1).  causal: a row sees the positions up to its own, else its whole sequence.  Returns O (like
+    q, contiguous unless ``out`` is given) and L fp32 [q_heads, rows]; rows behind cu_rows[B] are left as they are
+    (zero in new tensors).  ``workspace`` (paged_workspace) is allocated here if not given.  Enqueued on the current
+    stream.
+    """
+    import torch
+
+    qs = _paged_rows(q, "q", cache)
+    rows, heads, d = q.shape
+    o = torch.zeros((rows, heads, d), dtype=torch.bfloat16, device=q.device) if out is None else out
+    os_ = _paged_rows(o, "out", cache, heads)
+    if o.shape[0] != rows:
+        raise ValueError("out must have q's shape")
+    l = torch.zeros((heads, rows), dtype=torch.float32, device=q.device) if lse is None else lse
+    if l.shape != (heads, rows) or l.dtype != torch.float32 or not l.is_contiguous() or l.device != q.device:
+        raise ValueError("lse must be a contiguous fp32 tensor [q_heads, rows] on q's device")
+    batch = _paged_batch(cache, page_table, cu_rows, kv_lens, rows)
+    if rows == 0:
+        return o, l
+    if workspace is None:
+        workspace = paged_workspace(cache, batch.B)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    with torch.cuda.device(cache.device):
+        rc = fa_paged_fwd(q.data_ptr(), qs, cache._c, batch, o.data_ptr(), os_, l.data_ptr(), heads,
+                          rows if max_rows is None else int(max_rows), float(d ** -0.5 if scale is None else scale),
+                          causal, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                          _stream_handle(torch, cache.device))
+    _check(rc, "fa_paged_fwd")
+    return o, l
 
 
 def check_status(device=None):

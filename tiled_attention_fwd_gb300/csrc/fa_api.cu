@@ -249,6 +249,33 @@ int load_tensor_map_encoder() {
   return 0;
 }
 
+int encode_paged_map(CUtensorMap* map, const void* ptr, int elem_bytes, const long long* dims, const long long* stride,
+                     int box_cols, int box_1, int box_2, int swizzle_bytes, bool four) {
+  if (g_encode == nullptr) return -1;
+  cuuint64_t dm[4];
+  cuuint64_t strides[3];
+  const cuuint32_t rank = four ? 4 : 3;
+  for (cuuint32_t i = 0; i < rank; ++i) dm[i] = static_cast<cuuint64_t>(dims[i]);
+  for (cuuint32_t i = 0; i + 1 < rank; ++i) strides[i] = static_cast<cuuint64_t>(stride[i]) * elem_bytes;
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_1),
+                             static_cast<cuuint32_t>(box_2), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUtensorMapSwizzle swz = swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                 : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                       : CU_TENSOR_MAP_SWIZZLE_32B;
+  const CUresult r = g_encode(map, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                              rank, const_cast<void*>(ptr), dm, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -1;
+}
+
+int current_ctx(LaunchCtx* ctx, void* stream) {
+  DeviceState* s = nullptr;
+  const int rc = current_device_state(&s);
+  if (rc == FA_OK) *ctx = make_ctx(*s, stream);
+  return rc;
+}
+
 // Current time limit of the device-side waits, in nanoseconds.
 unsigned long long wait_limit_ns() { return static_cast<unsigned long long>(g_wait_limit_ms.load()) * 1000000ull; }
 
@@ -555,7 +582,8 @@ int fa_status(void* stream) {
   if (word != 0 && cudaMemset(s->status, 0, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
   const int na = fa::noalloc_take_status();
   if (na == FA_ERR_CUDA) return FA_ERR_CUDA;
-  return (word != 0 || na == FA_ERR_TIMEOUT) ? FA_ERR_TIMEOUT : FA_OK;
+  if ((word & ~fa::kBadBatchBit) != 0 || na == FA_ERR_TIMEOUT) return FA_ERR_TIMEOUT;
+  return word != 0 ? FA_ERR_BAD_BATCH : FA_OK;
 }
 
 int fa_selftest_wait(void* stream) {
@@ -583,6 +611,7 @@ const char* fa_strerror(int code) {
     case FA_ERR_BAD_SCALE: return "FA_ERR_BAD_SCALE: scale (and every dequantisation factor) must be finite and > 0";
     case FA_ERR_WORKSPACE: return "FA_ERR_WORKSPACE: workspace too small";
     case FA_ERR_SCRATCH: return "FA_ERR_SCRATCH: the kernel needs more scratch than fa_fwd_noalloc's static array holds";
+    case FA_ERR_BAD_BATCH: return "FA_ERR_BAD_BATCH: page_table, cu_rows or kv_lens named what is not there";
     default: return "unknown fa_gb300 error code";
   }
 }

@@ -125,6 +125,7 @@ enum : int {
   kStatusTimeoutMma = 1 << 1,
   kStatusTimeoutSoftmax = 1 << 2,
   kStatusTimeoutDrain = 1 << 3,
+  kStatusBadBatch = 1 << 4,  // paged cache: page_table, cu_rows or kv_lens name what is not there
 };
 
 // Shared state of the bounded waits of one CTA.
