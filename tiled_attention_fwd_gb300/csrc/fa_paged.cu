@@ -4,7 +4,7 @@
 #include <cmath>
 
 #include "../../include/fa_gb300.h"
-#include "fa_paged.cuh"
+#include "fa_paged_plan.cuh"
 
 namespace fa {
 namespace {
@@ -227,10 +227,7 @@ __global__ void __launch_bounds__(kPlainWarps * 32) fa_paged_plain_kernel(const 
   const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, b, bad);
   if (bad && lane == 0) atomicOr(status, kStatusBadBatch);
   if (t < s.row0 || t >= s.row0 + s.n) return;
-  if (s.n > a.max_rows) {
-    if (lane == 0) atomicOr(status, kStatusBadBatch);
-    return;
-  }
+  if (s.n > a.max_rows || static_cast<long long>(s.n) * a.group <= kFewRows) return;
   for (int c = lane; c < D; c += 32) s_q[warp][c] = __bfloat162float(a.q[t * a.qs[0] + hq * a.qs[1] + c]);
   __syncwarp();
   const int see = a.causal ? s.len - s.n + (t - s.row0) + 1 : s.len;  // keys 0 .. see - 1
@@ -318,6 +315,14 @@ int launch_plain_d(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   else
     fa_paged_plain_kernel<D, false><<<grid, kPlainWarps * 32, 0, ctx.stream>>>(a, ctx.status);
   return static_cast<int>(cudaGetLastError());
+}
+
+// Sequences of few rows, then the others (unless max_rows says that there are none).
+template <int D>
+int launch_fwd_d(const PagedFwdArgs& a, const LaunchCtx& ctx) {
+  const int e = launch_paged_few<D>(a, ctx);
+  if (e != 0 || static_cast<long long>(a.max_rows) * a.group <= kFewRows) return e;
+  return launch_plain_d<D>(a, ctx);
 }
 
 // ------------------------------------------------------------------ checks
@@ -419,7 +424,7 @@ int fa_paged_read(const fa_paged_cache* cache, const fa_paged_batch* batch, void
 
 size_t fa_paged_fwd_workspace_bytes(int B, int heads, int d) {
   if (B < 1 || heads < 1 || heads > 65535 || (d != 32 && d != 64 && d != 128 && d != 256)) return 0;
-  return 256;
+  return fa::paged_ws_bytes(d);
 }
 
 int fa_paged_fwd(const void* q, const long long* q_stride, const fa_paged_cache* cache, const fa_paged_batch* batch,
@@ -457,10 +462,10 @@ int fa_paged_fwd(const void* q, const long long* q_stride, const fa_paged_cache*
   a.workspace = static_cast<char*>(workspace);
   int e;
   switch (a.d) {
-    case 32: e = fa::launch_plain_d<32>(a, ctx); break;
-    case 64: e = fa::launch_plain_d<64>(a, ctx); break;
-    case 128: e = fa::launch_plain_d<128>(a, ctx); break;
-    default: e = fa::launch_plain_d<256>(a, ctx); break;
+    case 32: e = fa::launch_fwd_d<32>(a, ctx); break;
+    case 64: e = fa::launch_fwd_d<64>(a, ctx); break;
+    case 128: e = fa::launch_fwd_d<128>(a, ctx); break;
+    default: e = fa::launch_fwd_d<256>(a, ctx); break;
   }
   return e == 0 ? FA_OK : FA_ERR_CUDA;
 }

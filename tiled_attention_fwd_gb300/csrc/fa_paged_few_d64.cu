@@ -1,0 +1,6 @@
+// Paged attention of few rows, head dimension 64.
+#include "fa_paged_few.cuh"
+
+namespace fa {
+template int launch_paged_few<64>(const PagedFwdArgs& a, const LaunchCtx& ctx);
+}
