@@ -77,7 +77,7 @@ int encode_e4m3_map(CUtensorMap* map, const void* ptr, int BH, int N, int D, int
 // The same over the tensors of the paged operators (elements of 2 bytes, bf16,
 // or 1): `dims` and boxes {box_cols, box_1, box_2[, 1]} of 4 (or 3) dimensions,
 // innermost first, `stride` the element strides of dimensions 1 .. and swizzle
-// spans of 32, 64 or 128 bytes.  Returns 0 on success.
+// spans of 0 (none), 32, 64 or 128 bytes.  Returns 0 on success.
 int encode_paged_map(CUtensorMap* map, const void* ptr, int elem_bytes, const long long* dims, const long long* stride,
                      int box_cols, int box_1, int box_2, int swizzle_bytes, bool four);
 

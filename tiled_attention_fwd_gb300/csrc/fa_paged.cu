@@ -205,124 +205,164 @@ int launch_move(MoveArgs& a, int d, bool e4m3, const LaunchCtx& ctx) {
   return e == 0 ? FA_OK : FA_ERR_CUDA;
 }
 
-// ------------------------------------------------------------------ attention, plain
-// One warp per (row, query head): 32 keys at a time, a key per lane for the
-// logits (q from shared memory), then the lanes share out the d columns of V.
-// Reads K and V once per row: right for every case, bound by the cache's reads.
-constexpr int kPlainWarps = 4;
+// ------------------------------------------------------------------ attention, mending
+// The chunk kernel multiplies whole tiles: P = 0 where a row does not see a key,
+// and 0 times an infinity or a NaN in that key's V is NaN.  The few-row kernel
+// looks through the new tokens' V (a key that some rows of its sequence see and
+// others do not is a new token); where it met such a value, this kernel computes
+// the rows before it again, plainly.  One warp per (row, query head): 32 keys at
+// a time, a key per lane for the logits (q from shared memory), then the lanes
+// share out the d columns of V.  It is launched behind every causal chunk call and
+// leaves at once where there is nothing to mend.
+constexpr int kMendWarps = 4;
+
+struct MendParams {
+  PagedFwdArgs a;
+  const int* odd;
+  int n_odd;
+};
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kPlainWarps * 32) fa_paged_plain_kernel(const PagedFwdArgs a, int* status) {
-  __shared__ float s_q[kPlainWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * kPlainWarps + warp;
-  if (blockIdx.x == 0) paged_report(a.pb, a.kv.ps_log2, status);
-  if (unit >= static_cast<long long>(a.pb.rows) * a.q_heads) return;
-  const int t = static_cast<int>(unit / a.q_heads), hq = static_cast<int>(unit % a.q_heads);
-  const int hk = hq / a.group;
-  int b = 0;
-  while (b < a.pb.B && a.pb.cu_rows[b + 1] <= t) ++b;
-  if (b == a.pb.B) return;
-  bool bad;
-  const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, b, bad);
-  if (bad && lane == 0) atomicOr(status, kStatusBadBatch);
-  if (t < s.row0 || t >= s.row0 + s.n) return;
-  if (s.n > a.max_rows || static_cast<long long>(s.n) * a.group <= kFewRows) return;
-  for (int c = lane; c < D; c += 32) s_q[warp][c] = __bfloat162float(a.q[t * a.qs[0] + hq * a.qs[1] + c]);
-  __syncwarp();
-  const int see = a.causal ? s.len - s.n + (t - s.row0) + 1 : s.len;  // keys 0 .. see - 1
-  const float sl2 = a.scale * 1.4426950408889634f;
-  constexpr int CPL = D / 32;  // columns a lane
-  float acc[CPL] = {};
-  float m = -INFINITY, l = 0.f;
-  for (int j0 = 0; j0 < see; j0 += 32) {
-    const int j = j0 + lane;
-    float x = -INFINITY;
-    int page = -1;
-    if (j < see) {
-      page = paged_page(a.pb, a.kv, b, j);
-      const int slot = j & ((1 << a.kv.ps_log2) - 1);
-      float dot = 0.f;
-      if (page < 0) {
-        atomicOr(status, kStatusBadBatch);
-      } else if constexpr (E4M3) {
-        const uint8_t* k = static_cast<const uint8_t*>(a.kv.k) + page * a.kv.ks[0] + hk * a.kv.ks[1] + slot * a.kv.ks[2];
-        for (int c = 0; c < D; c += 2) {
-          const uint32_t h2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(k + c));
-          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-          dot = fmaf(s_q[warp][c], y.x, fmaf(s_q[warp][c + 1], y.y, dot));
-        }
-        dot *= scale_of_byte(a.kv.k_scale[((static_cast<long long>(page) * a.kv.heads + hk) << a.kv.ps_log2) + slot]);
-      } else {
-        const __nv_bfloat16* k =
-            static_cast<const __nv_bfloat16*>(a.kv.k) + page * a.kv.ks[0] + hk * a.kv.ks[1] + slot * a.kv.ks[2];
-        for (int c = 0; c < D; c += 2) {
-          const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(k + c));
-          dot = fmaf(s_q[warp][c], y.x, fmaf(s_q[warp][c + 1], y.y, dot));
-        }
-      }
-      x = dot * sl2;
-    }
-    float top = x;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    const float m_new = fmaxf(m, top);
-    const float alpha = m_new == m ? 1.f : ex2(m - m_new);
-    const float p = j < see ? ex2(x - (m_new == -INFINITY ? 0.f : m_new)) : 0.f;
-    float sum = p;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    l = l * alpha + sum;
-    m = m_new;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) acc[c] *= alpha;
-    const int nk = min(32, see - j0);
-    for (int i = 0; i < nk; ++i) {
-      const float pi = __shfl_sync(0xffffffffu, p, i);
-      const int pg = __shfl_sync(0xffffffffu, page, i);
-      if (pg < 0) continue;
-      const int slot = (j0 + i) & ((1 << a.kv.ps_log2) - 1);
-      const long long off = pg * a.kv.vs[0] + hk * a.kv.vs[1] + slot * a.kv.vs[2];
-      if constexpr (E4M3) {
-        const float f =
-            scale_of_byte(a.kv.v_scale[((static_cast<long long>(pg) * a.kv.heads + hk) << a.kv.ps_log2) + slot]);
-        const uint8_t* v = static_cast<const uint8_t*>(a.kv.v) + off;
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-          const uint32_t h2 = e4m3x2_to_f16x2(v[c * 32 + lane]);
-          acc[c] = fmaf(pi, __low2float(*reinterpret_cast<const __half2*>(&h2)) * f, acc[c]);
-        }
-      } else {
-        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.kv.v) + off;
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) acc[c] = fmaf(pi, __bfloat162float(v[c * 32 + lane]), acc[c]);
-      }
-    }
+__device__ __forceinline__ bool row_is_odd(const PagedKv& kv, int page, int head, int slot) {
+  const uint8_t* v = static_cast<const uint8_t*>(kv.v) +
+                     (page * kv.vs[0] + head * kv.vs[1] + slot * kv.vs[2]) * (E4M3 ? 1 : 2);
+  bool odd = E4M3 && kv.v_scale[((static_cast<long long>(page) * kv.heads + head) << kv.ps_log2) + slot] == 255;
+  for (int i = 0; i < D * (E4M3 ? 1 : 2) / 4; ++i) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(v)[i];
+    odd = odd || (E4M3 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u)) != 0;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int c = 0; c < CPL; ++c)
-    a.o[t * a.os[0] + hq * a.os[1] + c * 32 + lane] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[c] * inv);
-  if (lane == 0)
-    a.lse[static_cast<long long>(hq) * a.pb.rows + t] = (m + log2f(l)) * 0.69314718055994531f;
+  return odd;
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kMendWarps * 32) fa_paged_mend_kernel(const __grid_constant__ MendParams p) {
+  __shared__ float s_q[kMendWarps][D];
+  pdl_wait();
+  const PagedFwdArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool any = false;
+  for (int i = lane; i < p.n_odd; i += 32) any = any || p.odd[i] != 0;
+  if (!__any_sync(0xffffffffu, any)) return;
+  const long long units = static_cast<long long>(a.pb.rows) * a.q_heads;
+  for (long long unit = static_cast<long long>(blockIdx.x) * kMendWarps + warp; unit < units;
+       unit += static_cast<long long>(gridDim.x) * kMendWarps) {
+    const int t = static_cast<int>(unit / a.q_heads), hq = static_cast<int>(unit % a.q_heads);
+    const int hk = hq / a.group;
+    const int b = find_seq(a.pb.cu_rows, a.pb.B, t, lane);
+    if (b >= a.pb.B) continue;
+    bool bad;
+    const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, b, bad);
+    if (t < s.row0 || t >= s.row0 + s.n || s.n > a.max_rows || static_cast<long long>(s.n) * a.group <= kFewRows) continue;
+    const int see = s.len - s.n + (t - s.row0) + 1;  // keys 0 .. see - 1
+    bool odd = false;
+    for (int j = max(see, 0) + lane; j < s.len; j += 32) {
+      const int page = paged_page(a.pb, a.kv, b, j);
+      odd = odd || (page >= 0 && row_is_odd<D, E4M3>(a.kv, page, hk, j & ((1 << a.kv.ps_log2) - 1)));
+    }
+    if (!__any_sync(0xffffffffu, odd)) continue;
+    __syncwarp();
+    for (int c = lane; c < D; c += 32) s_q[warp][c] = __bfloat162float(a.q[t * a.qs[0] + hq * a.qs[1] + c]);
+    __syncwarp();
+    const float sl2 = a.scale * 1.4426950408889634f;
+    constexpr int CPL = D / 32;  // columns a lane
+    float acc[CPL] = {};
+    float m = -INFINITY, l = 0.f;
+    for (int j0 = 0; j0 < see; j0 += 32) {
+      const int j = j0 + lane;
+      float x = -INFINITY;
+      int page = -1;
+      if (j < see) {
+        page = paged_page(a.pb, a.kv, b, j);
+        const int slot = j & ((1 << a.kv.ps_log2) - 1);
+        float dot = 0.f;
+        if (page < 0) {
+          // (reported by the kernels before)
+        } else if constexpr (E4M3) {
+          const uint8_t* k = static_cast<const uint8_t*>(a.kv.k) + page * a.kv.ks[0] + hk * a.kv.ks[1] + slot * a.kv.ks[2];
+          for (int c = 0; c < D; c += 2) {
+            const uint32_t h2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(k + c));
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+            dot = fmaf(s_q[warp][c], y.x, fmaf(s_q[warp][c + 1], y.y, dot));
+          }
+          dot *= scale_of_byte(a.kv.k_scale[((static_cast<long long>(page) * a.kv.heads + hk) << a.kv.ps_log2) + slot]);
+        } else {
+          const __nv_bfloat16* k =
+              static_cast<const __nv_bfloat16*>(a.kv.k) + page * a.kv.ks[0] + hk * a.kv.ks[1] + slot * a.kv.ks[2];
+          for (int c = 0; c < D; c += 2) {
+            const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(k + c));
+            dot = fmaf(s_q[warp][c], y.x, fmaf(s_q[warp][c + 1], y.y, dot));
+          }
+        }
+        x = dot * sl2;
+      }
+      float top = x;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      const float m_new = fmaxf(m, top);
+      const float alpha = m_new == m ? 1.f : ex2(m - m_new);
+      const float p = j < see ? ex2(x - (m_new == -INFINITY ? 0.f : m_new)) : 0.f;
+      float sum = p;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+      l = l * alpha + sum;
+      m = m_new;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) acc[c] *= alpha;
+      const int nk = min(32, see - j0);
+      for (int i = 0; i < nk; ++i) {
+        const float pi = __shfl_sync(0xffffffffu, p, i);
+        const int pg = __shfl_sync(0xffffffffu, page, i);
+        if (pg < 0) continue;
+        const int slot = (j0 + i) & ((1 << a.kv.ps_log2) - 1);
+        const long long off = pg * a.kv.vs[0] + hk * a.kv.vs[1] + slot * a.kv.vs[2];
+        if constexpr (E4M3) {
+          const float f =
+              scale_of_byte(a.kv.v_scale[((static_cast<long long>(pg) * a.kv.heads + hk) << a.kv.ps_log2) + slot]);
+          const uint8_t* v = static_cast<const uint8_t*>(a.kv.v) + off;
+#pragma unroll
+          for (int c = 0; c < CPL; ++c) {
+            const uint32_t h2 = e4m3x2_to_f16x2(v[c * 32 + lane]);
+            acc[c] = fmaf(pi, __low2float(*reinterpret_cast<const __half2*>(&h2)) * f, acc[c]);
+          }
+        } else {
+          const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.kv.v) + off;
+#pragma unroll
+          for (int c = 0; c < CPL; ++c) acc[c] = fmaf(pi, __bfloat162float(v[c * 32 + lane]), acc[c]);
+        }
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int c = 0; c < CPL; ++c)
+      a.o[t * a.os[0] + hq * a.os[1] + c * 32 + lane] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[c] * inv);
+    if (lane == 0)
+      a.lse[static_cast<long long>(hq) * a.pb.rows + t] = (m + log2f(l)) * 0.69314718055994531f;
+  }
 }
 
 template <int D>
-int launch_plain_d(const PagedFwdArgs& a, const LaunchCtx& ctx) {
-  const long long units = static_cast<long long>(a.pb.rows) * a.q_heads;
-  const unsigned grid = static_cast<unsigned>((units + kPlainWarps - 1) / kPlainWarps);
-  if (a.e4m3)
-    fa_paged_plain_kernel<D, true><<<grid, kPlainWarps * 32, 0, ctx.stream>>>(a, ctx.status);
-  else
-    fa_paged_plain_kernel<D, false><<<grid, kPlainWarps * 32, 0, ctx.stream>>>(a, ctx.status);
-  return static_cast<int>(cudaGetLastError());
+int launch_mend(const PagedFwdArgs& a, const LaunchCtx& ctx) {
+  const int ctas = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
+  const MendParams p{a, paged_ws(a.workspace, D).odd, ctas};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas * 4);
+  cfg.blockDim = dim3(kMendWarps * 32);
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(a.e4m3 ? cudaLaunchKernelEx(&cfg, fa_paged_mend_kernel<D, true>, p)
+                                 : cudaLaunchKernelEx(&cfg, fa_paged_mend_kernel<D, false>, p));
 }
 
 // Sequences of few rows, then the others (unless max_rows says that there are none).
 template <int D>
 int launch_fwd_d(const PagedFwdArgs& a, const LaunchCtx& ctx) {
-  const int e = launch_paged_few<D>(a, ctx);
+  int e = launch_paged_few<D>(a, ctx);
   if (e != 0 || static_cast<long long>(a.max_rows) * a.group <= kFewRows) return e;
-  return launch_plain_d<D>(a, ctx);
+  e = launch_paged_chunk<D>(a, ctx);
+  return e != 0 || !a.causal ? e : launch_mend<D>(a, ctx);
 }
 
 // ------------------------------------------------------------------ checks

@@ -1,0 +1,1132 @@
+// Attention of chunks and prompts over a paged cache: sequences with more rows
+// than the few-row kernel takes.  The forward kernel's pipeline (fa_fwd_tc.cuh:
+// TMA, tcgen05.mma, S / P and O in tensor memory, softmax and correction
+// warpgroups, lazy row maximum) on work that is found on the device:
+//
+//  * Rows.  A 128-row tile holds 128 / G tokens (rounded down) of the G query
+//    heads that share a key/value head, token by token, so a chunk of few
+//    tokens fills tiles and K and V are read once for all G heads; Q comes in by one
+//    3-D TMA box {columns, G heads, tokens}.  A query block is two tiles
+//    (d = 256: one).
+//  * Work.  The key tiles of all (sequence, query block, head) units form one
+//    line that is cut into equal shares (fa_paged_plan.cuh).  The load warp walks
+//    this CTA's share and hands segments (a run of key tiles of one unit) to
+//    the other warps through a ring in shared memory.
+//  * Pages.  A key tile is loaded page by page (boxes of min(page, tile) rows);
+//    only boxes that hold keys of the sequence are.  V rows behind the last token
+//    are set to zero before the tensor core reads them: such slots hold anything,
+//    and 0 times NaN is NaN.
+//  * e4m3 pages.  The load warp brings codes and scales into a small ring, two
+//    warps turn them into the bf16 tiles that the tensor core reads (exact: a
+//    code has 4 significant bits and a scale is a power of two), so the rest of
+//    the pipeline is the same.
+//  * Output.  A unit held whole is written as it is finished; of others O and
+//    the log-sum (base 2) go to the workspace in fp32 and the joining kernel
+//    adds them up: O = sum 2^(L_i - L) O_i, L = log2 sum 2^L_i.
+#pragma once
+
+#include <atomic>
+
+#include "fa_fwd_tc.cuh"
+#include "fa_paged_plan.cuh"
+
+namespace fa {
+
+constexpr int kSegRing = 4;
+
+// A run of key tiles of one unit.
+struct alignas(16) ChunkSeg {
+  int valid;
+  int b;
+  int head;   // key/value head
+  int row0;   // row of the block's first token
+  int ntok;   // tokens of the block
+  int pos0;   // position of its first token
+  int len;    // tokens of the sequence
+  int j0;     // first key tile
+  int n0;     // key tiles of query tile 0 in this segment (they start at j0)
+  int n1;     // of query tile 1
+  int nmax;   // the larger
+  int out;    // 0: the unit is whole; 1, 2: part 0, part 1 of this CTA
+};
+static_assert(sizeof(ChunkSeg) == 48, "segment size");
+
+template <int D, bool E4M3>
+struct ChunkCfg : TcCfg<D> {
+  using T = TcCfg<D>;
+  // e4m3: ring of half key tiles (codes) where the contiguous kernel stages its output.
+  static constexpr int SLOT_ROWS = T::BK / 2;
+  static constexpr int SLOT = SLOT_ROWS * D;
+  static constexpr int NSLOT = T::OST / SLOT > 4 ? 4 : T::OST / SLOT;
+  static constexpr int OFF_SEG = T::OFF_MISC + 6672;
+  static constexpr int OFF_SCALE = OFF_SEG + kSegRing * static_cast<int>(sizeof(ChunkSeg));  // [NSLOT][SLOT_ROWS]
+  static constexpr int OFF_PLAN = T::OFF_ALPHA;  // before the roles start
+  static constexpr int CONV_WARPS = E4M3 ? 2 : 0;
+  static constexpr int CONV_WARP0 = T::LOAD_WARP + 1;
+  static constexpr int SEG_READERS = T::SOFTMAX_WARPS + 4 + 1 + CONV_WARPS;
+  static constexpr int ROWS = T::NQT * 128;
+  static_assert(T::OFF_ABORT + 4 <= OFF_SEG && OFF_SEG % 16 == 0, "misc area");
+  static_assert(OFF_SCALE + NSLOT * SLOT_ROWS <= T::OFF_MISC + T::MISC, "misc area");
+  static_assert(NSLOT >= 2 && sizeof(PlanScratch) <= 2048, "rings");
+};
+
+template <int D, bool E4M3>
+struct ChunkBars : TcBars<D, TcCfg<D>::NQT, kVarBf16> {
+  using Base = TcBars<D, TcCfg<D>::NQT, kVarBf16>;
+  __device__ __forceinline__ uint32_t seg_full(int i) const { return this->b0 + 256 + 8u * i; }
+  __device__ __forceinline__ uint32_t seg_empty(int i) const { return this->b0 + 288 + 8u * i; }
+  __device__ __forceinline__ uint32_t slot_full(int i) const { return this->b0 + 320 + 8u * i; }
+  __device__ __forceinline__ uint32_t slot_empty(int i) const { return this->b0 + 352 + 8u * i; }
+  static_assert(Base::COUNT * 8 <= 256, "barrier area");
+};
+
+struct ChunkParams {
+  PagedFwdArgs a;
+  PagedWs ws;
+  int* status;
+  unsigned long long limit_ns;
+  float scale_log2;
+  int tpt;      // tokens of a 128-row tile: 128 / group
+  int box;      // rows of a K/V box
+};
+
+// sum over i in [0, n) of floor((a i + b) / m), a, b >= 0 (Euclid's way down).
+__host__ __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long top = a * n + b;
+    if (top < m) break;
+    n = top / m;
+    b = top % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// The query blocks of a sequence (TQ tokens each) and the key tiles they visit.
+struct ChunkBlocks {
+  int n, len, tq, bk;
+  bool causal;
+  __host__ __device__ __forceinline__ int count() const { return (n + tq - 1) / tq; }
+  // Key tiles of the first `ntok` tokens of block q: those up to the last token's position (one at least).
+  __host__ __device__ __forceinline__ int tiles(int q, int ntok) const {
+    int end = len;
+    if (causal) {
+      const int pos = len - n + q * tq + ntok;
+      end = pos < len ? pos : len;
+    }
+    return end <= bk ? 1 : (end + bk - 1) / bk;
+  }
+  __host__ __device__ __forceinline__ int tokens(int q) const { return n - q * tq < tq ? n - q * tq : tq; }
+  // Key tiles of blocks 0 .. k - 1.
+  __host__ __device__ __forceinline__ long long before(int k) const {
+    if (k == 0) return 0;
+    const long long last = tiles(k - 1, tokens(k - 1));
+    if (!causal) return k * last;
+    // Block i < k - 1 ends behind position x_i = len - n + (i + 1) tq < len; the first `one` of them have x_i <= 0.
+    const int past = len - n;
+    int one = past < 0 ? -past / tq : 0;
+    one = one < k - 1 ? one : k - 1;
+    return one + floor_sum(k - 1 - one, bk, tq, static_cast<long long>(past) + static_cast<long long>(one + 1) * tq + bk - 1) + last;
+  }
+};
+
+template <int D>
+__device__ __forceinline__ ChunkBlocks chunk_blocks(const ChunkParams& p, const PagedSeq& s) {
+  ChunkBlocks c;
+  const bool mine = s.n >= 1 && s.n <= p.a.max_rows && (s.n > kFewRows || s.n * p.a.group > kFewRows);
+  c.n = mine ? s.n : 0;
+  c.len = s.len;
+  c.tq = p.tpt * TcCfg<D>::NQT;
+  c.bk = TcCfg<D>::BK;
+  c.causal = p.a.causal;
+  return c;
+}
+
+// ------------------------------------------------------------------ segments
+// The load warp's walk over its CTA's share.
+template <int D, bool E4M3>
+struct ChunkWalk {
+  using C = ChunkCfg<D, E4M3>;
+  int b, q, head, j, nt;
+  PagedSeq s;
+  ChunkBlocks c;
+  long long left;
+  __device__ __forceinline__ void load(const ChunkParams& p) {
+    bool bad;
+    s = paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad);
+    c = chunk_blocks<D>(p, s);
+  }
+  __device__ __forceinline__ ChunkSeg next(const ChunkParams& p) {
+    ChunkSeg g = {};
+    if (left == 0) return g;
+    const int ntok = c.tokens(q);
+    const int n = left < nt - j ? static_cast<int>(left) : nt - j;
+    g.valid = 1;
+    g.b = b;
+    g.head = head;
+    g.row0 = s.row0 + q * c.tq;
+    g.ntok = ntok;
+    g.pos0 = s.len - s.n + q * c.tq;
+    g.len = s.len;
+    g.j0 = j;
+    g.nmax = n;
+    g.n0 = n;
+    if (ntok > p.tpt) {
+      // Tile 0's tokens come first: they may be done with their keys before tile 1's.
+      const int first = c.tiles(q, p.tpt) - j;
+      g.n0 = first < 0 ? 0 : first < n ? first : n;
+      g.n1 = n;
+    }
+    g.out = n == nt ? 0 : j == 0 ? 2 : 1;
+    left -= n;
+    j += n;
+    if (left > 0 && j == nt) {
+      j = 0;
+      if (++head == p.a.kv.heads) {
+        head = 0;
+        ++q;
+        while (q == c.count()) {
+          ++b;
+          q = 0;
+          load(p);
+        }
+        nt = c.tiles(q, c.tokens(q));
+      }
+    }
+    return g;
+  }
+};
+
+template <int D, bool E4M3>
+__device__ __forceinline__ ChunkSeg* seg_slot(uint8_t* gbase, int k) {
+  return reinterpret_cast<ChunkSeg*>(gbase + ChunkCfg<D, E4M3>::OFF_SEG) + (k % kSegRing);
+}
+
+// Segment k, read by a whole warp of a role other than the load warp.
+template <int D, bool E4M3>
+__device__ __forceinline__ bool seg_read(ChunkSeg& g, int k, uint8_t* gbase, const ChunkBars<D, E4M3>& bar,
+                                         const WaitGuard& guard) {
+  if (!warp_wait_bar(bar.seg_full(k % kSegRing), (k / kSegRing) & 1, guard, kStatusTimeoutLoad)) return false;
+  const int4* src = reinterpret_cast<const int4*>(seg_slot<D, E4M3>(gbase, k));
+  int4* dst = reinterpret_cast<int4*>(&g);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) dst[i] = src[i];
+  warp_arrive(bar.seg_empty(k % kSegRing));
+  return true;
+}
+
+// A K or V tile of the stream.
+struct ChunkTile {
+  int kind;  // 0: none, 1: K, 2: V
+  int b, head, key0, len;
+};
+template <int D>
+__device__ __forceinline__ ChunkTile chunk_tile(int kind, const ChunkSeg& g, int j) {
+  return ChunkTile{kind, g.b, g.head, (g.j0 + j) * TcCfg<D>::BK, g.len};
+}
+
+// The order in which stages are filled and read (see tc_producer): get(k, seg)
+// fetches segment k, unit(seg, k) is called where segment k's Q may be loaded,
+// stage(t0, t1) for every stage with the tiles at its positions 0 and 1.
+template <int D, class Get, class Unit, class Stage>
+__device__ __forceinline__ bool chunk_stream(const Get& get, const Unit& unit, const Stage& stage) {
+  using C = TcCfg<D>;
+  const ChunkTile none{0, 0, 0, 0, 0};
+  ChunkSeg w;
+  if (!get(0, w)) return false;
+  if constexpr (C::NQT == 2) {
+    if (!w.valid) return true;
+    if (!unit(w, 0) || !stage(chunk_tile<D>(1, w, 0), none)) return false;
+    for (int k = 0;; ++k) {
+      ChunkSeg wn;
+      if (!get(k + 1, wn)) return false;
+      for (int j = 0; j < w.nmax; ++j) {
+        const ChunkTile kt = j + 1 < w.nmax ? chunk_tile<D>(1, w, j + 1) : wn.valid ? chunk_tile<D>(1, wn, 0) : none;
+        if (!stage(chunk_tile<D>(2, w, j), kt)) return false;
+      }
+      if (!wn.valid) return true;
+      if (!unit(wn, k + 1)) return false;
+      w = wn;
+    }
+  } else {
+    for (int k = 0; w.valid; ++k) {
+      if (!unit(w, k)) return false;
+      if (!stage(chunk_tile<D>(1, w, 0), 1 < w.nmax ? chunk_tile<D>(1, w, 1) : none)) return false;
+      for (int j = 0; j < w.nmax; ++j)
+        if (!stage(chunk_tile<D>(2, w, j), j + C::LA < w.nmax ? chunk_tile<D>(1, w, j + C::LA) : none)) return false;
+      if (!get(k + 1, w)) return false;
+    }
+    return true;
+  }
+}
+
+// ------------------------------------------------------------------ load warp
+template <int D, bool E4M3>
+__device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                           const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint32_t base,
+                                           uint8_t* gbase, const PlanShare& share, const WaitGuard& g) {
+  using C = ChunkCfg<D, E4M3>;
+  const int lane = threadIdx.x & 31;
+  const uint64_t pol_q = policy_evict_first();
+  const uint64_t pol_kv = policy_evict_last();
+  uint32_t pos = 0;          // stages (e4m3: half tiles) filled so far
+  uint32_t issued = 0;       // bit i: stage or slot i has been loaded
+  uint32_t last_par = 0;     // bit i: parity of its latest load
+  int last_q = -1;           // latest segment whose Q tiles were loaded
+  bool recorded = false;
+
+  ChunkWalk<D, E4M3> walk;
+  walk.left = share.end - share.start;
+  if (walk.left > 0) {
+    walk.b = share.b;
+    walk.load(p);
+    // The block that holds the share's first tile: 32 candidates at a time.
+    for (int q0 = 0;; q0 += 32) {
+      const int q = q0 + lane;
+      bool here = false;
+      long long first = 0;
+      int nt = 0;
+      if (q < walk.c.count()) {
+        nt = walk.c.tiles(q, walk.c.tokens(q));
+        first = p.a.kv.heads * walk.c.before(q);
+        here = first <= share.offset && share.offset < first + static_cast<long long>(p.a.kv.heads) * nt;
+      }
+      const uint32_t who = __ballot_sync(0xffffffffu, here);
+      if (who != 0) {
+        const int from = __ffs(who) - 1;
+        walk.q = q0 + from;
+        walk.nt = __shfl_sync(0xffffffffu, nt, from);
+        const long long in = share.offset - __shfl_sync(0xffffffffu, first, from);
+        walk.head = static_cast<int>(in / walk.nt);
+        walk.j = static_cast<int>(in - static_cast<long long>(walk.head) * walk.nt);
+        break;
+      }
+      if (q0 + 32 >= walk.c.count()) {  // cannot be: the share lies within the sequence's tiles
+        walk.left = 0;
+        break;
+      }
+    }
+  }
+
+  auto get = [&](int k, ChunkSeg& w) -> bool {
+    const int i = k % kSegRing;
+    if (!warp_wait_bar(bar.seg_empty(i), ((k / kSegRing) & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
+    w = walk.next(p);
+    if (lane == 0) {
+      *seg_slot<D, E4M3>(gbase, k) = w;
+      if (w.out == 2) {  // this unit's first part: who holds the rest
+        const long long last = share.end - 1 + (walk.nt - w.nmax);
+        p.ws.chunk_rec[blockIdx.x] = PlanRecord{w.b, w.head, walk.q, plan_cta_of(last, share.total, share.ctas) - static_cast<int>(blockIdx.x)};
+      }
+    }
+    recorded = recorded || w.out == 2;
+    warp_arrive(bar.seg_full(i));
+    return true;
+  };
+  auto unit = [&](const ChunkSeg& w, int k) -> bool {
+    for (int t = 0; t < C::NQT; ++t) {
+      if (!warp_wait_bar(bar.q_empty(t), (k & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar.q_full(t), p.tpt * p.a.group * D * 2);
+        for (int r = 0; r < C::NR; ++r)
+          tma_load_3d(base + C::OFF_Q + t * C::Q_TILE + r * C::Q_REGION, tm_q, bar.q_full(t), r * C::RC,
+                      w.head * p.a.group, w.row0 + t * p.tpt, pol_q);
+      }
+    }
+    last_q = k;
+    return true;
+  };
+  // Boxes of up to `rows` keys from key0 on, one lane each: those that begin before the sequence's end.
+  auto boxes = [&](const ChunkTile& t, int key0, int rows) -> int {
+    const int n = min(rows, t.len - key0);
+    return n <= 0 ? 0 : (n + p.box - 1) / p.box;
+  };
+  auto page_of = [&](const ChunkTile& t, int key) -> int {
+    const int page = paged_page(p.a.pb, p.a.kv, t.b, key);
+    if (page < 0) atomicOr(p.status, kStatusBadBatch);
+    return page < 0 ? p.a.kv.num_pages : page;  // a coordinate outside the tensor reads as zeros
+  };
+  const int slot_mask = (1 << p.a.kv.ps_log2) - 1;
+  auto stage = [&](const ChunkTile& t0, const ChunkTile& t1) -> bool {
+    if constexpr (!E4M3) {
+      const int st = pos % C::NST;
+      const uint32_t par = (pos / C::NST) & 1;
+      if (!warp_wait_bar(bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
+      const uint32_t full = bar.kv_full(st);
+      const int n0 = boxes(t0, t0.key0, C::BK), n1 = t1.kind ? boxes(t1, t1.key0, C::BK) : 0;
+      if (lane == 0) mbar_arrive_expect_tx(full, (n0 + n1) * p.box * D * 2);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const ChunkTile& t = i == 0 ? t0 : t1;
+        if (lane < (i == 0 ? n0 : n1)) {
+          const int key = t.key0 + lane * p.box;
+          const int page = page_of(t, key);
+          const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE + lane * p.box * C::SWB;
+          for (int r = 0; r < C::NR; ++r)
+            tma_load_4d(dst + r * C::K_REGION, t.kind == 1 ? tm_k : tm_v, full, r * C::RC, key & slot_mask, t.head, page,
+                        pol_kv);
+        }
+      }
+      issued |= 1u << st;
+      last_par = (last_par & ~(1u << st)) | (par << st);
+      ++pos;
+    } else {
+      for (int i = 0; i < 2; ++i) {
+        const ChunkTile& t = i == 0 ? t0 : t1;
+        if (t.kind == 0) continue;
+        for (int h = 0; h < 2; ++h) {
+          const int st = pos % C::NSLOT;
+          const uint32_t par = (pos / C::NSLOT) & 1;
+          if (!warp_wait_bar(bar.slot_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
+          const uint32_t full = bar.slot_full(st);
+          const int key0 = t.key0 + h * C::SLOT_ROWS;
+          const int n = boxes(t, key0, C::SLOT_ROWS);
+          if (lane == 0) mbar_arrive_expect_tx(full, n * p.box * (D + 1));
+          __syncwarp();
+          if (lane < n) {
+            const int key = key0 + lane * p.box;
+            const int page = page_of(t, key);
+            const uint32_t sc = base + C::OFF_SCALE + st * C::SLOT_ROWS + lane * p.box;
+            tma_load_4d(base + C::OFF_OST + st * C::SLOT + lane * p.box * D, t.kind == 1 ? tm_k : tm_v, full, 0,
+                        key & slot_mask, t.head, page, pol_kv);
+            // (For a page that is not there any scales do.)
+            const long long pg = page == p.a.kv.num_pages ? 0 : page;
+            bulk_load(sc, (t.kind == 1 ? p.a.kv.k_scale : p.a.kv.v_scale) +
+                              (((pg * p.a.kv.heads + t.head) << p.a.kv.ps_log2) + (key & slot_mask)), p.box, full);
+          }
+          issued |= 1u << st;
+          last_par = (last_par & ~(1u << st)) | (par << st);
+          ++pos;
+        }
+      }
+    }
+    return true;
+  };
+  chunk_stream<D>(get, unit, stage);
+  if (lane == 0 && !recorded) p.ws.chunk_rec[blockIdx.x].b = -1;
+  // Every issued copy must land before the CTA may exit.
+  for (int i = 0; i < (E4M3 ? C::NSLOT : C::NST); ++i)
+    if (issued & (1u << i)) wait_bar_drain(E4M3 ? bar.slot_full(i) : bar.kv_full(i), (last_par >> i) & 1, g);
+  for (int t = 0; t < C::NQT; ++t)
+    if (last_q >= 0) wait_bar_drain(bar.q_full(t), last_q & 1, g);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ e4m3 -> bf16
+// Eight codes (two words) to eight bf16, times the scale: the bits of a code are
+// put where bf16 has them (sign; 4 exponent bits below bf16's 8; 3 mantissa
+// bits), which is the value times 2^-120, also for denormals; one multiplication
+// by 2^(120 + e) makes it right (two where that power is beyond bf16).
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t x, uint32_t f, uint32_t& lo, uint32_t& hi) {
+  const uint32_t h = (x & 0x80808080u) | ((x >> 4) & 0x07070707u);  // high bytes: sign, upper 3 exponent bits
+  const uint32_t l = (x << 4) & 0xf0f0f0f0u;                        // low bytes: lowest exponent bit, mantissa
+  lo = mul_bf16x2(__byte_perm(l, h, 0x5140), f);
+  hi = mul_bf16x2(__byte_perm(l, h, 0x7362), f);
+}
+
+// Two warps: every half tile that the load warp brought, into the stages.
+template <int D, bool E4M3>
+__device__ __forceinline__ void chunk_convert(const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint32_t base,
+                                              uint8_t* gbase, int cw, const WaitGuard& g) {
+  using C = ChunkCfg<D, E4M3>;
+  const int lane = threadIdx.x & 31;
+  uint32_t pos = 0, half = 0;
+  auto get = [&](int k, ChunkSeg& w) -> bool { return seg_read<D, E4M3>(w, k, gbase, bar, g); };
+  auto unit = [&](const ChunkSeg&, int) -> bool { return true; };
+  auto stage = [&](const ChunkTile& t0, const ChunkTile& t1) -> bool {
+    const int st = pos % C::NST;
+    if (!warp_wait_bar(bar.kv_empty(st), ((pos / C::NST) & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
+    ++pos;
+    for (int i = 0; i < 2; ++i) {
+      const ChunkTile& t = i == 0 ? t0 : t1;
+      if (t.kind == 0) continue;
+      for (int h = 0; h < 2; ++h, ++half) {
+        const int sl = half % C::NSLOT;
+        if (!warp_wait_bar(bar.slot_full(sl), (half / C::NSLOT) & 1, g, kStatusTimeoutLoad)) return false;
+        const uint8_t* codes = gbase + C::OFF_OST + sl * C::SLOT;
+        const uint8_t* scales = gbase + C::OFF_SCALE + sl * C::SLOT_ROWS;
+        const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE;
+        const int end = t.len - (t.key0 + h * C::SLOT_ROWS);  // rows of this half that are keys
+        constexpr int UPR = D / 8;                             // 16-byte units of a bf16 row
+        constexpr int UNITS = C::SLOT_ROWS * UPR;
+#pragma unroll 4
+        for (int u0 = 0; u0 < UNITS; u0 += 64) {
+          const int u = u0 + cw * 32 + lane;
+          const int row = u / UPR, unit16 = u % UPR;
+          const uint2 x = *reinterpret_cast<const uint2*>(codes + u * 8);
+          const uint32_t byte = scales[row];
+          uint32_t f = byte > 134u ? 254u << 7 : (byte + 120u) << 7;  // 2^(120 + e), 2^127 at most
+          f = byte == 255u ? 0x7fc0u : f;
+          f |= f << 16;
+          uint32_t w[4];
+          e4m3x4_to_bf16x4(x.x, f, w[0], w[1]);
+          e4m3x4_to_bf16x4(x.y, f, w[2], w[3]);
+          if (byte > 134u) {
+            uint32_t f2 = byte == 255u ? 0x3f80u : (byte - 7u) << 7;  // 2^(e - 7)
+            f2 |= f2 << 16;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = mul_bf16x2(w[k], f2);
+          }
+          if (row >= end) w[0] = w[1] = w[2] = w[3] = 0u;
+          const int trow = h * C::SLOT_ROWS + row;
+          constexpr int UR = C::SWB / 16;
+          const uint32_t sw = C::SWB == 128 ? trow & 7 : (trow >> 1) & 3;
+          st_shared_v4(dst + (unit16 / UR) * C::K_REGION + trow * C::SWB + (((unit16 % UR) ^ sw) << 4), w[0], w[1], w[2],
+                       w[3]);
+        }
+        warp_arrive(bar.slot_empty(sl));
+      }
+    }
+    fence_proxy_async_smem();  // before the tensor core reads them
+    warp_arrive(bar.kv_full(st));
+    return true;
+  };
+  chunk_stream<D>(get, unit, stage);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ MMA issuer
+// tc_mma's order of products, segment by segment.
+template <int D, bool E4M3>
+__device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint32_t base,
+                                          uint8_t* gbase, uint32_t tmem, const WaitGuard& g) {
+  using C = ChunkCfg<D, E4M3>;
+  const TcMma<D, C::NQT, kVarBf16> M(tmem, base);
+  const int lane = threadIdx.x & 31;
+  auto wait = [&](uint32_t b, uint32_t par) -> bool {
+    const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
+    return __all_sync(0xffffffffu, r);
+  };
+  uint32_t pos = 0;
+  uint32_t go0 = 0, go1 = 0;
+  bool ok = true;
+  auto stage_acquire = [&](uint32_t& st) -> bool {
+    st = pos % C::NST;
+    const bool r = wait(bar.kv_full(st), (pos / C::NST) & 1);
+    ++pos;
+    if (r) tc_fence_after();
+    return r;
+  };
+  // V rows behind the sequence's end in the tile at stage st (key tile j of w): zeros.
+  auto clear_tail = [&](const ChunkSeg& w, int j, uint32_t st) {
+    if constexpr (!E4M3) {
+      const int end = w.len - (w.j0 + j) * C::BK;
+      if (end >= C::BK) return;
+      const int from = end < 0 ? 0 : end;
+      constexpr int UR = C::SWB / 16;
+      const uint32_t vt = base + C::OFF_KV + 2 * st * C::KV_TILE;
+      for (int r = 0; r < C::NR; ++r)
+        for (int i = from * UR + lane; i < C::BK * UR; i += 32) st_shared_v4(vt + r * C::V_REGION + i * 16, 0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+  };
+  auto get = [&](int k, ChunkSeg& w) -> bool { return seg_read<D, E4M3>(w, k, gbase, bar, g); };
+
+  ChunkSeg w;
+  ok = get(0, w);
+  if constexpr (C::NQT == 2) {
+    auto tiles_of = [](const ChunkSeg& x, int t) -> int { return t == 0 ? x.n0 : x.n1; };
+    auto first_qk = [&](const ChunkSeg& x, int k, int t, uint32_t kpos) -> bool {
+      if (!wait(bar.q_full(t), k & 1)) return false;
+      tc_fence_after();
+      if (tiles_of(x, t) > 0) M.qk(t, t, kpos, bar.s_full(t));
+      if (tiles_of(x, t) <= 1) M.commit(bar.q_empty(t));
+      return true;
+    };
+    auto tile_pv = [&](const ChunkSeg& x, int j, int t, uint32_t st, uint32_t& go) -> bool {
+      const int n = tiles_of(x, t);
+      if (j < n) {
+        if (!wait(bar.pv_go(t, 0), go & 1)) return false;
+        tc_fence_after();
+        if constexpr (C::PV_SPLIT) {
+          M.pv_half(t, t, 2 * st, 0, j > 0);
+          if (!wait(bar.pv_go(t, 1), go & 1)) return false;
+          tc_fence_after();
+          M.pv_half(t, t, 2 * st, 1, true);
+        } else {
+          M.pv(t, t, 2 * st, j > 0);
+        }
+        ++go;
+        if (j == n - 1) M.commit(bar.o_done(t));
+      }
+      return true;
+    };
+    auto tile_qk = [&](const ChunkSeg& x, int j, int t, uint32_t st, const ChunkSeg& xn, int kn) -> bool {
+      const int n = tiles_of(x, t);
+      if (j + 1 < n) {
+        M.qk(t, t, 2 * st + 1, bar.s_full(t));
+        if (j + 1 == n - 1) M.commit(bar.q_empty(t));
+      } else if (j == x.nmax - 1 && xn.valid) {
+        return first_qk(xn, kn, t, 2 * st + 1);
+      }
+      return true;
+    };
+    if (ok && w.valid) {
+      uint32_t st;
+      ok = stage_acquire(st) && first_qk(w, 0, 0, 2 * st) && first_qk(w, 0, 1, 2 * st);
+      if (ok) M.commit(bar.kv_empty(st));
+      for (int k = 0; ok; ++k) {
+        ChunkSeg wn;
+        if (!(ok = get(k + 1, wn))) break;
+        for (int j = 0; ok && j < w.nmax; ++j) {
+          if (!(ok = stage_acquire(st))) break;
+          clear_tail(w, j, st);
+          if (j == w.nmax - 1)
+            ok = tile_pv(w, j, 0, st, go0) && tile_pv(w, j, 1, st, go1) && tile_qk(w, j, 0, st, wn, k + 1) &&
+                 tile_qk(w, j, 1, st, wn, k + 1);
+          else
+            ok = tile_pv(w, j, 0, st, go0) && tile_qk(w, j, 0, st, wn, k + 1) && tile_pv(w, j, 1, st, go1) &&
+                 tile_qk(w, j, 1, st, wn, k + 1);
+          if (ok) M.commit(bar.kv_empty(st));
+        }
+        if (!ok || !wn.valid) break;
+        w = wn;
+      }
+    }
+  } else {
+    uint32_t qk_total = 0;
+    for (int k = 0; ok && w.valid; ++k) {
+      if (!(ok = wait(bar.q_full(0), k & 1))) break;
+      tc_fence_after();
+      uint32_t st;
+      if (!(ok = stage_acquire(st))) break;
+      const int n = w.n0;
+      const uint32_t qk_base = qk_total;
+      for (int t = 0; t < C::LA && t < n; ++t) {
+        M.qk(0, qk_total & 1, 2 * st + t, bar.s_full(qk_total & 1));
+        ++qk_total;
+      }
+      M.commit(bar.kv_empty(st));
+      if (n <= C::LA) M.commit(bar.q_empty(0));
+      for (int j = 0; j < n; ++j) {
+        if (!(ok = stage_acquire(st))) break;
+        clear_tail(w, j, st);
+        if (!(ok = wait(bar.pv_go(0, go0 & 1), (go0 >> 1) & 1))) break;
+        ++go0;
+        tc_fence_after();
+        M.pv(0, (qk_base + j) & 1, 2 * st, j > 0);
+        M.commit(bar.o_done(0));
+        if (j + C::LA < n) {
+          M.qk(0, qk_total & 1, 2 * st + 1, bar.s_full(qk_total & 1));
+          ++qk_total;
+          if (j + C::LA == n - 1) M.commit(bar.q_empty(0));
+        }
+        M.commit(bar.kv_empty(st));
+      }
+      if (ok) ok = get(k + 1, w);
+    }
+  }
+  (void)go1;
+  M.commit(bar.drain());
+  wait_bar_drain(bar.drain(), 0, g);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ softmax
+// tc_softmax with the rows' limits taken from the segment.
+template <int D, bool E4M3>
+__device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint8_t* gbase,
+                                              uint32_t tmem, int wg, int quarter, int lane, const WaitGuard& g) {
+  using C = ChunkCfg<D, E4M3>;
+  const int r = quarter * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const int ot = (C::NQT == 2) ? wg : 0;
+  float* alpha_s = reinterpret_cast<float*>(gbase + C::OFF_ALPHA) + ot * 256;
+  uint32_t a_pub = 0;
+  float* stat_m = reinterpret_cast<float*>(gbase + C::OFF_STAT_M) + ot * 128;
+  float* stat_l = reinterpret_cast<float*>(gbase + C::OFF_STAT_L) + ot * 128;
+  const float sl2 = p.scale_log2;
+  const uint64_t sl2x2 = f2_pack(sl2, sl2);
+  uint32_t s_waits = 0;
+  bool ok = true;
+  const int tok_r = min(wg * p.tpt + r / p.a.group, (wg + 1) * p.tpt - 1);  // this row's token within the block
+
+  for (int uk = 0; ok; ++uk) {
+    int n, j0, lim0, min_lim, len;
+    {
+      ChunkSeg w;
+      ok = seg_read<D, E4M3>(w, uk, gbase, bar, g);
+      if (!ok || !w.valid) break;
+      n = wg == 0 ? w.n0 : w.n1;
+      j0 = w.j0;
+      len = w.len;
+      // Rows behind the block's last token take that one's limit (they are not written).
+      lim0 = p.a.causal ? w.pos0 + min(tok_r, w.ntok - 1) : w.len - 1;
+      min_lim = p.a.causal ? w.pos0 + wg * p.tpt : w.len - 1;
+    }
+    if (n == 0) continue;
+    lim0 = min(lim0, len - 1);
+    float m = -INFINITY;
+    float l = 0.f;
+    float lres = 0.f;
+    for (int j = 0; j < n; ++j) {
+      const int buf = (C::NQT == 2) ? wg : static_cast<int>(s_waits & 1);
+      const uint32_t par = (C::NQT == 2) ? (s_waits & 1) : ((s_waits >> 1) & 1);
+      ok = warp_wait_bar(bar.s_full(buf), par, g, kStatusTimeoutSoftmax);
+      if (!ok) break;
+      ++s_waits;
+      tc_fence_after();
+      const uint32_t ts = tmem + lane_off + C::TM_S + buf * C::TM_SB;
+      float s[C::BK];
+      float cmax[C::BK / 32];
+      {
+        uint32_t raw_s[C::BK / 32][32];
+#pragma unroll
+        for (int c = 0; c < C::BK / 32; ++c) tmem_ld32_max(ts + c * 32, raw_s[c], cmax[c]);
+#pragma unroll
+        for (int c = 0; c < C::BK / 32; ++c) tmem_wait_ld(raw_s[c], cmax[c]);
+#pragma unroll
+        for (int c = 0; c < C::BK / 32; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(raw_s[c][i]);
+      }
+      const int key0 = (j0 + j) * C::BK;
+      float rmax;
+      if (key0 + C::BK - 1 > min_lim) {
+        const int lim = lim0 - key0;
+        const int lo = __reduce_min_sync(0xffffffffu, lim);
+#pragma unroll
+        for (int cb = 0; cb < C::BK / 32; ++cb) {
+          if (32 * cb + 31 > lo) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * cb + i > lim) s[32 * cb + i] = -INFINITY;
+          }
+        }
+        constexpr int KC = C::BK / 8;
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v = fmax3(s[i], s[i + 8], s[i + 16]);
+#pragma unroll
+          for (int k = 3; k + 1 < KC; k += 2) v = fmax3(v, s[i + 8 * k], s[i + 8 * (k + 1)]);
+          if ((KC - 3) % 2 == 1) v = fmaxf(v, s[i + 8 * (KC - 1)]);
+          mx[i] = v;
+        }
+        rmax = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+      } else {
+        rmax = cmax[0];
+#pragma unroll
+        for (int c = 1; c < C::BK / 32; ++c) rmax = fmaxf(rmax, cmax[c]);
+      }
+      float m_new, alpha;
+      if constexpr (C::LAZY_MAX) {
+        const float rm = rmax * sl2;
+        m_new = (rm > m + C::MAX_SLACK) ? rm : m;
+        alpha = (m_new == m) ? 1.f : ex2(m - m_new);
+      } else {
+        m_new = fmaxf(m, rmax * sl2);
+        alpha = (m_new == m) ? 1.f : ex2(m - m_new);
+      }
+      float nb = (m_new == -INFINITY) ? 0.f : -m_new;
+      if (j > 0) {
+        alpha_s[(a_pub & 1) * 128 + r] = alpha;
+        // As in tc_softmax: the exponentials are scheduled after this arrival.
+        nb = fmaf(0.f, __uint_as_float(warp_arrive_token(bar.a_full(ot, a_pub & 1))), nb);
+        ++a_pub;
+      }
+      const uint64_t nb2 = f2_pack(nb, nb);
+      if constexpr (C::LAZY_MAX) {
+        const float pmax = ex2(fmaf(rmax, sl2, nb));
+        const float pr = __uint_as_float(pack_bf16x2(pmax, 0.f) << 16);
+        lres = lres * alpha + (pr - pmax);
+      }
+      uint64_t acc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = 0ull;
+#pragma unroll
+      for (int h = 0; h < C::BK / 64; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 64 * h; c < 64 * h + 64; c += 2) {
+          const float2 x = f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sl2x2, nb2));
+          const float p0 = ex2(x.x);
+          const float p1 = ex2(x.y);
+          pk[(c >> 1) & 31] = pack_bf16x2(p0, p1);
+          acc[(c >> 1) & 3] = f2_add(acc[(c >> 1) & 3], f2_pack(p0, p1));
+        }
+        tmem_st32(ts + h * C::P_COLS_64, pk);
+        if constexpr (C::PV_SPLIT) {
+          if (h == 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive_elect(bar.pv_go(ot, 0));
+          }
+        }
+      }
+      const float2 a01 = f2_unpack(f2_add(acc[0], acc[1]));
+      const float2 a23 = f2_unpack(f2_add(acc[2], acc[3]));
+      l = l * alpha + ((a01.x + a01.y) + (a23.x + a23.y));
+      m = m_new;
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(C::NQT == 2 ? bar.pv_go(ot, C::PV_SPLIT ? 1 : 0) : bar.pv_go(0, (s_waits - 1) & 1));
+    }
+    if (!ok) break;
+    // The row's log2-sum-exp2 and O's normaliser.
+    stat_m[(uk & 1) * 256 + r] = m + log2f(l);
+    stat_l[(uk & 1) * 256 + r] = l + lres;
+    warp_arrive(bar.l_full(ot));
+  }
+}
+
+// ------------------------------------------------------------------ correction + output
+template <int D, bool E4M3>
+__device__ __forceinline__ void chunk_correction(const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint8_t* gbase,
+                                                 uint32_t tmem, int quarter, int lane, const WaitGuard& g) {
+  using C = ChunkCfg<D, E4M3>;
+  const int r = quarter * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const float* alpha_base = reinterpret_cast<const float*>(gbase + C::OFF_ALPHA);
+  const float* stat_m = reinterpret_cast<const float*>(gbase + C::OFF_STAT_M);
+  const float* stat_l = reinterpret_cast<const float*>(gbase + C::OFF_STAT_L);
+  constexpr bool PER_PV_DONE = (C::NQT == 1);
+  const int tok_r = r / p.a.group, head_r = r - tok_r * p.a.group;
+  uint32_t a_cnt0 = 0, a_cnt1 = 0, od0 = 0, od1 = 0, lf0 = 0, lf1 = 0;
+  uint32_t go_arr = 0;
+  bool ok = true;
+  auto release_o = [&](int t) {
+    if (C::NQT == 2) {
+      warp_arrive(bar.pv_go(t, 0));
+    } else {
+      warp_arrive(bar.pv_go(0, go_arr & 1));
+      ++go_arr;
+    }
+  };
+  auto rescale = [&](int t, uint32_t& a_cnt, uint32_t& od) -> bool {
+    bool k = warp_wait_bar(bar.a_full(t, a_cnt & 1), (a_cnt >> 1) & 1, g, kStatusTimeoutSoftmax);
+    if (!k) return false;
+    const float alpha = alpha_base[t * 256 + (a_cnt & 1) * 128 + r];
+    ++a_cnt;
+    if (PER_PV_DONE) {
+      k = warp_wait_bar(bar.o_done(t), od & 1, g, kStatusTimeoutSoftmax);
+      if (!k) return false;
+      ++od;
+    }
+    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+      tc_fence_after();
+      const uint32_t to = tmem + lane_off + C::TM_O + t * D;
+      const uint64_t a2 = f2_pack(alpha, alpha);
+      constexpr int RG = (C::NQT == 1) ? (D / 32 < 4 ? D / 32 : 4) : 1;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; c += RG) {
+        uint32_t v[RG][32];
+#pragma unroll
+        for (int k2 = 0; k2 < RG; ++k2) tmem_ld32(to + (c + k2) * 32, v[k2]);
+#pragma unroll
+        for (int k2 = 0; k2 < RG; ++k2) tmem_wait_ld(v[k2]);
+#pragma unroll
+        for (int k2 = 0; k2 < RG; ++k2) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 y = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[k2][i]), __uint_as_float(v[k2][i + 1])), a2));
+            v[k2][i] = __float_as_uint(y.x);
+            v[k2][i + 1] = __float_as_uint(y.y);
+          }
+        }
+#pragma unroll
+        for (int k2 = 0; k2 < RG; ++k2) tmem_st32(to + (c + k2) * 32, v[k2]);
+      }
+      tmem_wait_st();
+    }
+    tc_fence_before();
+    release_o(t);
+    return true;
+  };
+  // O of tile t: the rows of a whole unit, or this CTA's part of them.
+  auto epilogue = [&](const ChunkSeg& w, int su, int t, uint32_t& od, uint32_t& lf) -> bool {
+    bool k = warp_wait_bar(bar.o_done(t), od & 1, g, kStatusTimeoutSoftmax);
+    k = k && warp_wait_bar(bar.l_full(t), lf & 1, g, kStatusTimeoutSoftmax);
+    if (!k) return false;
+    ++od;
+    ++lf;
+    tc_fence_after();
+    const float lsum = stat_m[su * 256 + t * 128 + r];
+    const float lrow = stat_l[su * 256 + t * 128 + r];
+    const float inv_l = lrow == 0.f ? 0.f : 1.f / lrow;
+    const uint64_t il2 = f2_pack(inv_l, inv_l);
+    const int tok = t * p.tpt + tok_r;
+    const bool mine = tok_r < p.tpt && tok < w.ntok;
+    const uint32_t to = tmem + lane_off + C::TM_O + t * D;
+    const int hq = w.head * p.a.group + head_r;
+    __nv_bfloat16* dst = p.a.o + static_cast<long long>(w.row0 + tok) * p.a.os[0] + static_cast<long long>(hq) * p.a.os[1];
+    float* part = p.ws.chunk_part + (static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * chunk_floats(C::ROWS, D);
+    float* prow = part + C::ROWS + (static_cast<size_t>(t) * 128 + r) * D;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t v[32];
+      tmem_ld32(to + c * 32, v);
+      tmem_wait_ld(v);
+      if (c == D / 32 - 1) {
+        tc_fence_before();
+        release_o(t);
+      }
+      if (mine && w.out == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t y[4];
+#pragma unroll
+          for (int k2 = 0; k2 < 4; ++k2) {
+            const float2 x = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[8 * i + 2 * k2]), __uint_as_float(v[8 * i + 2 * k2 + 1])), il2));
+            y[k2] = pack_bf16x2(x.x, x.y);
+          }
+          *reinterpret_cast<uint4*>(dst + c * 32 + 8 * i) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      } else if (mine) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 x = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), il2));
+          const float2 y = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), il2));
+          *reinterpret_cast<float4*>(prow + c * 32 + 4 * i) = make_float4(x.x, x.y, y.x, y.y);
+        }
+      }
+      __syncwarp();
+    }
+    if (mine) {
+      if (w.out == 0)
+        p.a.lse[static_cast<long long>(hq) * p.a.pb.rows + w.row0 + tok] = lsum * 0.69314718055994531f;
+      else
+        part[t * 128 + r] = lsum;
+    }
+    return true;
+  };
+
+  release_o(0);
+  if (C::NO == 2) release_o(1);
+  for (int uk = 0; ok; ++uk) {
+    ChunkSeg w;
+    ok = seg_read<D, E4M3>(w, uk, gbase, bar, g);
+    if (!ok || !w.valid) break;
+    // A tile whose keys all lie before this part has nothing to add.
+    if (C::NQT == 2 && w.n0 == 0)
+      p.ws.chunk_part[(static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * chunk_floats(C::ROWS, D) + r] = -INFINITY;
+    for (int j = 0; ok && j < w.nmax; ++j) {
+      if (ok && j >= 1 && j < w.n0) ok = rescale(0, a_cnt0, od0);
+      if (C::NO == 2 && ok && j >= 1 && j < w.n1) ok = rescale(1, a_cnt1, od1);
+      if (ok && j == w.n0 - 1) ok = epilogue(w, uk & 1, 0, od0, lf0);
+      if (C::NO == 2 && ok && j == w.n1 - 1) ok = epilogue(w, uk & 1, 1, od1, lf1);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
+    fa_paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkParams p) {
+  using C = ChunkCfg<D, E4M3>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  ChunkBars<D, E4M3> bar;
+  bar.b0 = base + C::OFF_BAR;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::OFF_TMEM_SLOT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_ABORT);
+
+  pdl_wait();  // the few-row kernel is done with the SM (and what waits for this kernel waits for both)
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar.q_full(t), 1);
+      mbar_init(bar.q_empty(t), 1);
+    }
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(bar.kv_full(i), E4M3 ? C::CONV_WARPS : 1);
+      mbar_init(bar.kv_empty(i), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar.s_full(b), 1);
+      mbar_init(bar.pv_go(b, 0), 8);  // 4 softmax warps + 4 correction warps
+      mbar_init(bar.pv_go(b, 1), C::PV_SPLIT ? 4 : 8);
+      mbar_init(bar.a_full(b, 0), 4);
+      mbar_init(bar.a_full(b, 1), 4);
+      mbar_init(bar.o_done(b), 1);
+      mbar_init(bar.l_full(b), 4);
+    }
+    mbar_init(bar.drain(), 1);
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(bar.seg_full(i), 1);
+      mbar_init(bar.seg_empty(i), C::SEG_READERS);
+    }
+    for (int i = 0; i < C::NSLOT; ++i) {
+      mbar_init(bar.slot_full(i), 1);
+      mbar_init(bar.slot_empty(i), 2);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::LOAD_WARP && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
+    tmem_relinquish();
+  }
+  const PlanShare share = plan_share<C::THREADS>(
+      p.a.pb.B, gridDim.x, blockIdx.x,
+      [&](int b) -> long long {
+        bool bad;
+        const ChunkBlocks c = chunk_blocks<D>(p, paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad));
+        return c.n == 0 ? 0 : p.a.kv.heads * c.before(c.count());
+      },
+      *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitGuard g{abort_flag, p.status, p.limit_ns};
+
+  if (warp < C::SOFTMAX_WARPS) {
+    if constexpr (C::SPLIT_REGS) regs_increase<C::REG_SOFTMAX>();
+    chunk_softmax<D, E4M3>(p, bar, gbase, tmem, warp >> 2, warp & 3, lane, g);
+  } else if (warp < C::SOFTMAX_WARPS + 4) {
+    if constexpr (C::SPLIT_REGS) regs_decrease<C::reg_corr(false)>();
+    chunk_correction<D, E4M3>(p, bar, gbase, tmem, warp & 3, lane, g);
+  } else {
+    if constexpr (C::SPLIT_REGS) regs_decrease<C::REG_CORR_OTHER - C::reg_corr(false)>();
+    if (warp == C::LOAD_WARP) chunk_load<D, E4M3>(&tm_q, &tm_k, &tm_v, p, bar, base, gbase, share, g);
+    if (warp == C::MMA_WARP) chunk_mma<D, E4M3>(p, bar, base, gbase, tmem, g);
+    if constexpr (E4M3)
+      if (warp >= C::CONV_WARP0) chunk_convert<D, E4M3>(p, bar, base, gbase, warp - C::CONV_WARP0, g);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+// Joins the parts of the units that several CTAs held: block (c, y) the rows y, y + gridDim.y, .. (in fours) of the
+// unit that CTA c began.
+template <int D>
+__global__ void __launch_bounds__(128) fa_paged_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+  pdl_wait();
+  constexpr int ROWS = TcCfg<D>::NQT * 128;
+  const PlanRecord rec = p.ws.chunk_rec[blockIdx.x];
+  if (rec.b < 0) return;
+  bool bad;
+  const PagedSeq s = paged_seq(p.a.pb, p.a.kv.ps_log2, rec.b, bad);
+  const ChunkBlocks c = chunk_blocks<D>(p, s);
+  const int ntok = c.tokens(rec.qb);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto part = [&](int i) -> const float* {
+    return p.ws.chunk_part + ((static_cast<size_t>(blockIdx.x) + i) * 2 + (i == 0 ? 1 : 0)) * chunk_floats(ROWS, D);
+  };
+  for (int r = blockIdx.y * 4 + warp; r < ROWS; r += gridDim.y * 4) {
+    const int t = r >> 7, tok_r = (r & 127) / p.a.group, head_r = (r & 127) % p.a.group;
+    const int tok = t * p.tpt + tok_r;
+    if (tok_r >= p.tpt || tok >= ntok) continue;
+    float m = -INFINITY;
+    for (int i = 0; i <= rec.more; ++i) m = fmaxf(m, part(i)[r]);
+    float l = 0.f, o[D / 32] = {};
+    for (int i = 0; i <= rec.more; ++i) {
+      const float* x = part(i);
+      if (x[r] == -INFINITY) continue;  // this part saw none of the row's keys
+      const float f = x[r] == m ? 1.f : ex2(x[r] - m);
+      l += f;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) o[k] += x[ROWS + static_cast<size_t>(r) * D + k * 32 + lane] * f;
+    }
+    const int row = s.row0 + rec.qb * c.tq + tok, hq = rec.head * p.a.group + head_r;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* dst = p.a.o + static_cast<long long>(row) * p.a.os[0] + static_cast<long long>(hq) * p.a.os[1];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) dst[k * 32 + lane] = __float2bfloat16_rn(o[k] * inv);
+    if (lane == 0) p.a.lse[static_cast<long long>(hq) * p.a.pb.rows + row] = (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+// ------------------------------------------------------------------ launch
+inline cudaError_t launch_pdl(void (*kernel)(ChunkParams), dim3 grid, int threads, cudaStream_t stream, const ChunkParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D, bool E4M3>
+int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
+  using C = ChunkCfg<D, E4M3>;
+  auto kernel = fa_paged_chunk_kernel<D, E4M3>;
+  if constexpr (C::SPLIT_REGS) {
+    // The register split is sized for exactly LAUNCH_REGS a thread (see launch_tc_impl).
+    static std::atomic<int> checked_regs{-1};
+    int regs = checked_regs.load(std::memory_order_relaxed);
+    if (regs < 0) {
+      cudaFuncAttributes attr;
+      cudaError_t ea = cudaFuncGetAttributes(&attr, kernel);
+      if (ea != cudaSuccess) return static_cast<int>(ea);
+      regs = attr.numRegs;
+      checked_regs.store(regs, std::memory_order_relaxed);
+    }
+    if (regs != C::LAUNCH_REGS) return -2;
+  }
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  ChunkParams p;
+  p.a = a;
+  p.ws = paged_ws(a.workspace, D);
+  p.status = ctx.status;
+  p.limit_ns = ctx.limit_ns;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.tpt = 128 / a.group;
+  const int most = E4M3 ? C::SLOT_ROWS : C::BK;
+  p.box = (1 << a.kv.ps_log2) < most ? 1 << a.kv.ps_log2 : most;
+  CUtensorMap mq, mk, mv;
+  const long long qdims[3] = {D, a.q_heads, a.pb.rows};
+  const long long qst[2] = {a.qs[1], a.qs[0]};
+  if (encode_paged_map(&mq, a.q, 2, qdims, qst, C::RC, a.group, p.tpt, C::SWB, false) != 0) return -1;
+  const long long dims[4] = {D, 1LL << a.kv.ps_log2, a.kv.heads, a.kv.num_pages};
+  const long long ks[3] = {a.kv.ks[2], a.kv.ks[1], a.kv.ks[0]}, vs[3] = {a.kv.vs[2], a.kv.vs[1], a.kv.vs[0]};
+  // bf16: 64-column regions in the operand layout; e4m3: whole rows of codes, unswizzled.
+  const int cols = E4M3 ? D : C::RC, swizzle = E4M3 ? 0 : C::SWB;
+  if (encode_paged_map(&mk, a.kv.k, E4M3 ? 1 : 2, dims, ks, cols, p.box, 1, swizzle, true) != 0) return -1;
+  if (encode_paged_map(&mv, a.kv.v, E4M3 ? 1 : 2, dims, vs, cols, p.box, 1, swizzle, true) != 0) return -1;
+  const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_ALLOC;
+  cfg.stream = ctx.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, p);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  return static_cast<int>(launch_pdl(fa_paged_chunk_join_kernel<D>, dim3(grid, 8), 128, ctx.stream, p));
+}
+
+template <int D>
+int launch_paged_chunk(const PagedFwdArgs& a, const LaunchCtx& ctx) {
+  return a.e4m3 ? launch_paged_chunk_impl<D, true>(a, ctx) : launch_paged_chunk_impl<D, false>(a, ctx);
+}
+
+}  // namespace fa

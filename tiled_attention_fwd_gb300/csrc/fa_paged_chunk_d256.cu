@@ -1,0 +1,6 @@
+// Paged attention of chunks and prompts, head dimension 256.
+#include "fa_paged_chunk.cuh"
+
+namespace fa {
+template int launch_paged_chunk<256>(const PagedFwdArgs& a, const LaunchCtx& ctx);
+}

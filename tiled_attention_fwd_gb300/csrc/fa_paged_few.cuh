@@ -85,6 +85,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 struct FewParams {
   PagedFwdArgs a;
+  bool scan;  // look for infinities and NaN in the chunks' new V (see fa_paged_mend_kernel)
   PagedWs ws;
   int* status;
   unsigned long long limit_ns;
@@ -619,6 +620,52 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3>::THREADS, 1)
     at.advance(a, j1 - j0);
   }
   if (threadIdx.x == 0 && !recorded) p.ws.few_rec[blockIdx.x].b = -1;
+  if (p.scan) {
+    // Rows of the chunk kernel's sequences, dealt out evenly; a thread takes 16 bytes of a row at a time.
+    __syncthreads();
+    const PlanShare part = plan_share<C::THREADS>(
+        a.pb.B, gridDim.x, blockIdx.x,
+        [&](int b) -> long long {
+          bool bad;
+          const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, b, bad);
+          return s.n > 1 && s.n <= a.max_rows && few_tiles<C::KT>(a, s) == 0 ? s.n : 0;
+        },
+        *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
+    long long rest = part.end - part.start;
+    int b = part.b, row = static_cast<int>(part.offset);
+    bool odd = false;
+    while (rest > 0) {
+      bool bad;
+      const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, b, bad);
+      const bool chunk = s.n > 1 && s.n <= a.max_rows && few_tiles<C::KT>(a, s) == 0;
+      const int take = !chunk ? 0 : rest < s.n - row ? static_cast<int>(rest) : s.n - row;
+      constexpr int UPR = C::ROWB / 16;
+      const long long items = static_cast<long long>(take) * a.kv.heads * UPR;
+#pragma unroll 4
+      for (long long it = threadIdx.x; it < items; it += C::THREADS) {
+        const int unit = static_cast<int>(it % UPR);
+        const int head = static_cast<int>(it / UPR % a.kv.heads);
+        const int pos = s.len - s.n + row + static_cast<int>(it / UPR / a.kv.heads);
+        const int page = pos < 0 ? -1 : paged_page(a.pb, a.kv, b, pos);
+        if (page < 0) continue;
+        const int slot = pos & ((1 << a.kv.ps_log2) - 1);
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv.v) +
+                                                        (page * a.kv.vs[0] + head * a.kv.vs[1] + slot * a.kv.vs[2]) * C::EB +
+                                                        unit * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          odd = odd || (E4M3 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpgeu2(w[k] & 0x7fff7fffu, 0x7f807f80u)) != 0;
+        if (E4M3 && unit == 0)
+          odd = odd || a.kv.v_scale[((static_cast<long long>(page) * a.kv.heads + head) << a.kv.ps_log2) + slot] == 255;
+      }
+      rest -= take;
+      row = 0;
+      ++b;
+    }
+    const int any = __syncthreads_or(odd);
+    if (threadIdx.x == 0) p.ws.odd[blockIdx.x] = any;
+  }
   // After a wait that gave up, what was loaded must land before the CTA leaves.
   for (; done < issued; ++done) {
     const uint32_t bar = bars + 8 * (done % C::S);
@@ -678,7 +725,8 @@ int launch_paged_few_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   if (encode_paged_map(&mv, a.kv.v, C::EB, dims, vs, C::SWB / C::EB, 16, 1, C::SWB, true) != 0) return -1;
   FewParams p;
   p.a = a;
-  p.ws = paged_ws(a.workspace);
+  p.scan = a.causal && static_cast<long long>(a.max_rows) * a.group > kFewRows;
+  p.ws = paged_ws(a.workspace, D);
   p.status = ctx.status;
   p.limit_ns = ctx.limit_ns;
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;

@@ -108,18 +108,35 @@ struct alignas(16) PlanRecord {
 
 // Workspace of fa_paged_fwd.
 struct PagedWs {
-  PlanRecord* few_rec;  // [kPlanCtas]
-  float* few_part;      // [kPlanCtas][2][few_floats(d)]
+  PlanRecord* few_rec;    // [kPlanCtas]
+  PlanRecord* chunk_rec;  // [kPlanCtas]
+  int* odd;               // [kPlanCtas]: a CTA of the few-row kernel met an infinity or a NaN in a chunk's new V
+  float* few_part;        // [kPlanCtas][2][few_floats(d)]: m, l and O of 16 rows
+  float* chunk_part;      // [kPlanCtas][2][chunk_floats(rows, d)]: log-sums and O of a query block
 };
 constexpr int kFewRows = 16;  // rows of a unit of the few-row kernel at most
 constexpr __host__ __device__ size_t few_floats(int d) { return static_cast<size_t>(kFewRows) * (d + 2); }
-inline size_t paged_ws_bytes(int d) {
-  return kPlanCtas * sizeof(PlanRecord) + kPlanCtas * 2 * few_floats(d) * sizeof(float);
+constexpr __host__ __device__ size_t chunk_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 1); }
+inline size_t paged_ws_layout(char* p, int d, PagedWs* w) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* x = p + at;
+    at += (bytes + 255) & ~static_cast<size_t>(255);
+    return x;
+  };
+  PagedWs x;
+  x.few_rec = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
+  x.chunk_rec = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
+  x.odd = reinterpret_cast<int*>(take(kPlanCtas * sizeof(int)));
+  x.few_part = reinterpret_cast<float*>(take(kPlanCtas * 2 * few_floats(d) * sizeof(float)));
+  x.chunk_part = reinterpret_cast<float*>(take(kPlanCtas * 2 * chunk_floats(d <= 128 ? 256 : 128, d) * sizeof(float)));
+  if (w) *w = x;
+  return at;
 }
-inline PagedWs paged_ws(char* p) {
+inline size_t paged_ws_bytes(int d) { return paged_ws_layout(nullptr, d, nullptr); }
+inline PagedWs paged_ws(char* p, int d) {
   PagedWs w;
-  w.few_rec = reinterpret_cast<PlanRecord*>(p);
-  w.few_part = reinterpret_cast<float*>(p + kPlanCtas * sizeof(PlanRecord));
+  paged_ws_layout(p, d, &w);
   return w;
 }
 
@@ -130,5 +147,7 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // Entry points of the attention kernels' translation units; each returns a cudaError_t-like code.
 template <int D>
 int launch_paged_few(const PagedFwdArgs& a, const LaunchCtx& ctx);
+template <int D>
+int launch_paged_chunk(const PagedFwdArgs& a, const LaunchCtx& ctx);
 
 }  // namespace fa
