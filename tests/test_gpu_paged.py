@@ -138,6 +138,19 @@ def test_page_sizes(fmt, page):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("most", [128, 700])
+def test_many_units_on_every_sm(fmt, d, most):
+    """Several units to a CTA one after another: of one key tile, and of a few with borders inside units."""
+    rng = np.random.default_rng(most + d)
+    B, heads = (60, 8) if most == 128 else (16, 8)
+    lens = rng.integers(1, most + 1, B)
+    rows = [int(min(n, r)) for n, r in zip(lens, rng.integers(1, 40 if most == 128 else 90, B))]
+    s = Setup([int(n) for n in lens], rows, heads=heads, group=1, d=d, page=32, fmt=fmt, seed=most, pad=4)
+    check(s, *run(s), d ** -0.5, True)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("rows", [1, 4, 200])
 def test_long_sequences_are_split_and_joined(fmt, rows):
     s = Setup([9001, 4097], [rows, 1], heads=1, group=1, d=128, page=64, fmt=fmt, seed=rows)

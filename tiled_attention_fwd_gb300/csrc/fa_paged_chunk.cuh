@@ -77,6 +77,9 @@ struct ChunkBars : TcBars<D, TcCfg<D>::NQT, kVarBf16> {
   __device__ __forceinline__ uint32_t seg_empty(int i) const { return this->b0 + 288 + 8u * i; }
   __device__ __forceinline__ uint32_t slot_full(int i) const { return this->b0 + 320 + 8u * i; }
   __device__ __forceinline__ uint32_t slot_empty(int i) const { return this->b0 + 352 + 8u * i; }
+  // m and l of this accumulator's k-th unit: the softmax may finish the next unit (one key tile) while the
+  // correction warpgroup has not come to this one yet, so two barriers take turns.
+  __device__ __forceinline__ uint32_t ml_full(int t, int k) const { return this->b0 + 384 + 8u * (2 * t + (k & 1)); }
   static_assert(Base::COUNT * 8 <= 256, "barrier area");
 };
 
@@ -651,6 +654,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
   const float sl2 = p.scale_log2;
   const uint64_t sl2x2 = f2_pack(sl2, sl2);
   uint32_t s_waits = 0;
+  int fin = 0;  // units finished by this warpgroup
   bool ok = true;
   const int tok_r = min(wg * p.tpt + r / p.a.group, (wg + 1) * p.tpt - 1);  // this row's token within the block
 
@@ -777,9 +781,10 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
     }
     if (!ok) break;
     // The row's log2-sum-exp2 and O's normaliser.
-    stat_m[(uk & 1) * 256 + r] = m + log2f(l);
-    stat_l[(uk & 1) * 256 + r] = l + lres;
-    warp_arrive(bar.l_full(ot));
+    stat_m[(fin & 1) * 256 + r] = m + log2f(l);
+    stat_l[(fin & 1) * 256 + r] = l + lres;
+    warp_arrive(bar.ml_full(ot, fin));
+    ++fin;
   }
 }
 
@@ -847,10 +852,11 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
     return true;
   };
   // O of tile t: the rows of a whole unit, or this CTA's part of them.
-  auto epilogue = [&](const ChunkSeg& w, int su, int t, uint32_t& od, uint32_t& lf) -> bool {
+  auto epilogue = [&](const ChunkSeg& w, int t, uint32_t& od, uint32_t& lf) -> bool {
     bool k = warp_wait_bar(bar.o_done(t), od & 1, g, kStatusTimeoutSoftmax);
-    k = k && warp_wait_bar(bar.l_full(t), lf & 1, g, kStatusTimeoutSoftmax);
+    k = k && warp_wait_bar(bar.ml_full(t, lf), (lf >> 1) & 1, g, kStatusTimeoutSoftmax);
     if (!k) return false;
+    const int su = lf & 1;
     ++od;
     ++lf;
     tc_fence_after();
@@ -916,8 +922,8 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
     for (int j = 0; ok && j < w.nmax; ++j) {
       if (ok && j >= 1 && j < w.n0) ok = rescale(0, a_cnt0, od0);
       if (C::NO == 2 && ok && j >= 1 && j < w.n1) ok = rescale(1, a_cnt1, od1);
-      if (ok && j == w.n0 - 1) ok = epilogue(w, uk & 1, 0, od0, lf0);
-      if (C::NO == 2 && ok && j == w.n1 - 1) ok = epilogue(w, uk & 1, 1, od1, lf1);
+      if (ok && j == w.n0 - 1) ok = epilogue(w, 0, od0, lf0);
+      if (C::NO == 2 && ok && j == w.n1 - 1) ok = epilogue(w, 1, od1, lf1);
     }
   }
 }
@@ -957,7 +963,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       mbar_init(bar.a_full(b, 0), 4);
       mbar_init(bar.a_full(b, 1), 4);
       mbar_init(bar.o_done(b), 1);
-      mbar_init(bar.l_full(b), 4);
+      mbar_init(bar.ml_full(b, 0), 4);
+      mbar_init(bar.ml_full(b, 1), 4);
     }
     mbar_init(bar.drain(), 1);
     for (int i = 0; i < kSegRing; ++i) {
