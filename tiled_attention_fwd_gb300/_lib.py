@@ -173,19 +173,22 @@ class CPagedBatch(ctypes.Structure):
                 ("table_stride", ctypes.c_longlong), ("max_pages", _c_int), ("B", _c_int), ("rows", _c_int)]
 
 
+_Strides2 = ctypes.c_longlong * 2
+
+
 def _strides2(st):
-    return (ctypes.c_longlong * 2)(*st)
+    return _Strides2(*st)
 
 
 def fa_paged_write(cache, batch, k, k_stride, v, v_stride, stream) -> int:
     """Rows of k, v into the pages; `cache` and `batch` are CPagedCache / CPagedBatch, strides {row, head} pairs."""
-    return load().fa_paged_write(ctypes.addressof(cache), ctypes.addressof(batch), k, _strides2(k_stride), v,
+    return load().fa_paged_write(ctypes.byref(cache), ctypes.byref(batch), k, _strides2(k_stride), v,
                                  _strides2(v_stride), stream)
 
 
 def fa_paged_read(cache, batch, k, k_stride, v, v_stride, stream) -> int:
     """The tokens that the batch's rows stand for, out of the pages into k, v."""
-    return load().fa_paged_read(ctypes.addressof(cache), ctypes.addressof(batch), k, _strides2(k_stride), v,
+    return load().fa_paged_read(ctypes.byref(cache), ctypes.byref(batch), k, _strides2(k_stride), v,
                                 _strides2(v_stride), stream)
 
 
@@ -196,7 +199,7 @@ def fa_paged_fwd_workspace_bytes(B, heads, d) -> int:
 def fa_paged_fwd(q, q_stride, cache, batch, o, o_stride, lse, q_heads, max_rows, scale, causal, workspace,
                  workspace_bytes, stream) -> int:
     """Attention of the batch's rows over the pages; pointers are integers (device addresses)."""
-    return load().fa_paged_fwd(q, _strides2(q_stride), ctypes.addressof(cache), ctypes.addressof(batch), o,
+    return load().fa_paged_fwd(q, _strides2(q_stride), ctypes.byref(cache), ctypes.byref(batch), o,
                                _strides2(o_stride), lse, q_heads, max_rows, scale, int(bool(causal)), workspace,
                                workspace_bytes, stream)
 
@@ -392,6 +395,7 @@ class PagedCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.heads, self.page_size, self.d = k.shape
         self.device, self.dtype = k.device, k.dtype
+        self._index, self._int32, self._bf16 = k.get_device(), torch.int32, torch.bfloat16
         c = CPagedCache()
         c.k, c.v = k.data_ptr(), v.data_ptr()
         if fp8:
@@ -415,43 +419,50 @@ class PagedCache:
 
 def _paged_batch(cache, page_table, cu_rows, kv_lens, rows):
     """CPagedBatch of int32 tensors on the cache's device."""
-    import torch
-
-    i32 = torch.int32
-    if page_table.dtype != i32 or cu_rows.dtype != i32 or kv_lens.dtype != i32:
+    i32 = cache._int32
+    if page_table.dtype is not i32 or cu_rows.dtype is not i32 or kv_lens.dtype is not i32:
         raise ValueError("page_table, cu_rows and kv_lens must be int32")
-    dev = cache.device
-    if page_table.device != dev or cu_rows.device != dev or kv_lens.device != dev:
+    dev = cache._index
+    if page_table.get_device() != dev or cu_rows.get_device() != dev or kv_lens.get_device() != dev:
         raise ValueError("page_table, cu_rows and kv_lens must be on the cache's device")
-    if page_table.dim() != 2 or kv_lens.dim() != 1 or cu_rows.dim() != 1:
+    shape = page_table.shape
+    if len(shape) != 2 or kv_lens.dim() != 1 or cu_rows.dim() != 1:
         raise ValueError("page_table must be [B, pages], cu_rows [B + 1] and kv_lens [B]")
-    B, width = page_table.shape
+    B, width = shape
     if B == 0 or width == 0 or kv_lens.shape[0] != B or cu_rows.shape[0] != B + 1:
         raise ValueError("page_table must be [B, pages], cu_rows [B + 1] and kv_lens [B], B and pages at least 1")
-    if page_table.stride(1) != 1 or not kv_lens.is_contiguous() or not cu_rows.is_contiguous():
+    stride = page_table.stride()
+    if (stride[1] != 1 and width > 1) or not kv_lens.is_contiguous() or not cu_rows.is_contiguous():
         raise ValueError("cu_rows, kv_lens and the rows of page_table must be contiguous")
-    b = CPagedBatch()
-    b.page_table, b.cu_rows, b.kv_lens = page_table.data_ptr(), cu_rows.data_ptr(), kv_lens.data_ptr()
-    b.table_stride = page_table.stride(0) if B > 1 else width
-    b.max_pages, b.B, b.rows = width, B, rows
-    return b
+    return CPagedBatch(page_table.data_ptr(), cu_rows.data_ptr(), kv_lens.data_ptr(), stride[0] if B > 1 else width,
+                       width, B, rows)
 
 
-def _paged_rows(t, name, cache, heads=None):
+def _paged_rows(t, name, cache, heads):
     """Checks a token-major bf16 tensor [rows, heads, d]; returns its {row, head} strides."""
-    import torch
-
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != cache.device or t.shape[2] != cache.d or \
-            (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be a bf16 tensor [rows, heads, d] with the cache's d"
-                         f"{'' if heads is None else ' and heads'}, on its device")
+    n = t.shape
+    if len(n) != 3 or t.dtype is not cache._bf16 or t.get_device() != cache._index or n[2] != cache.d or n[1] != heads:
+        raise ValueError(f"{name} must be a bf16 tensor [rows, heads, d] of the cache's d (and as many heads as its "
+                         "counterpart), on the cache's device")
     s = t.stride()
     if s[2] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     # Strides of dimensions of one element are never used; torch may report any value for them.
-    n = t.shape
     head = s[1] if n[1] > 1 else cache.d
     return (s[0] if n[0] > 1 else head * n[1]), head
+
+
+def _paged_call(cache, fn, name, *args):
+    """fn(*args, stream) with the cache's device current, on its current stream."""
+    import torch
+
+    if torch.cuda.current_device() == cache._index:
+        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(cache._index):
+            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if rc != FA_OK:
+        raise FAError(rc, name)
 
 
 def paged_write(cache, k, v, page_table, cu_rows, kv_lens):
@@ -462,17 +473,13 @@ def paged_write(cache, k, v, page_table, cu_rows, kv_lens):
     n_b = cu_rows[b + 1] - cu_rows[b].  All on the cache's device (include/fa_gb300.h says what becomes of entries
     that name nothing).  Returns the cache.  Enqueued on the current stream.
     """
-    import torch
-
     ks, vs = _paged_rows(k, "k", cache, cache.heads), _paged_rows(v, "v", cache, cache.heads)
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v must have the same rows")
     batch = _paged_batch(cache, page_table, cu_rows, kv_lens, k.shape[0])
     if k.shape[0] == 0:
         return cache
-    with torch.cuda.device(cache.device):
-        rc = fa_paged_write(cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs, _stream_handle(torch, cache.device))
-    _check(rc, "fa_paged_write")
+    _paged_call(cache, fa_paged_write, "fa_paged_write", cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs)
     return cache
 
 
@@ -494,9 +501,7 @@ def paged_read(cache, page_table, cu_rows, kv_lens, rows=None, out=None):
     batch = _paged_batch(cache, page_table, cu_rows, kv_lens, k.shape[0])
     if k.shape[0] == 0:
         return k, v
-    with torch.cuda.device(cache.device):
-        rc = fa_paged_read(cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs, _stream_handle(torch, cache.device))
-    _check(rc, "fa_paged_read")
+    _paged_call(cache, fa_paged_read, "fa_paged_read", cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs)
     return k, v
 
 
@@ -520,28 +525,28 @@ def paged_forward(q, cache, page_table, cu_rows, kv_lens, max_rows=None, causal:
     """
     import torch
 
-    qs = _paged_rows(q, "q", cache)
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, q_heads, d]")
     rows, heads, d = q.shape
+    qs = _paged_rows(q, "q", cache, heads)
     o = torch.zeros((rows, heads, d), dtype=torch.bfloat16, device=q.device) if out is None else out
     os_ = _paged_rows(o, "out", cache, heads)
     if o.shape[0] != rows:
         raise ValueError("out must have q's shape")
     l = torch.zeros((heads, rows), dtype=torch.float32, device=q.device) if lse is None else lse
-    if l.shape != (heads, rows) or l.dtype != torch.float32 or not l.is_contiguous() or l.device != q.device:
+    if l.shape != (heads, rows) or l.dtype is not torch.float32 or not l.is_contiguous() or \
+            l.get_device() != cache._index:
         raise ValueError("lse must be a contiguous fp32 tensor [q_heads, rows] on q's device")
     batch = _paged_batch(cache, page_table, cu_rows, kv_lens, rows)
     if rows == 0:
         return o, l
     if workspace is None:
         workspace = paged_workspace(cache, batch.B)
-    elif workspace.device != q.device or not workspace.is_contiguous():
+    elif workspace.get_device() != cache._index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
-    with torch.cuda.device(cache.device):
-        rc = fa_paged_fwd(q.data_ptr(), qs, cache._c, batch, o.data_ptr(), os_, l.data_ptr(), heads,
-                          rows if max_rows is None else int(max_rows), float(d ** -0.5 if scale is None else scale),
-                          causal, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                          _stream_handle(torch, cache.device))
-    _check(rc, "fa_paged_fwd")
+    _paged_call(cache, fa_paged_fwd, "fa_paged_fwd", q.data_ptr(), qs, cache._c, batch, o.data_ptr(), os_, l.data_ptr(),
+                heads, rows if max_rows is None else int(max_rows), d ** -0.5 if scale is None else float(scale), causal,
+                workspace.data_ptr(), workspace.nbytes)
     return o, l
 
 

@@ -207,10 +207,10 @@ int launch_move(MoveArgs& a, int d, bool e4m3, const LaunchCtx& ctx) {
 
 // ------------------------------------------------------------------ attention, mending
 // The chunk kernel multiplies whole tiles: P = 0 where a row does not see a key,
-// and 0 times an infinity or a NaN in that key's V is NaN.  The few-row kernel
-// looks through the new tokens' V (a key that some rows of its sequence see and
-// others do not is a new token); where it met such a value, this kernel computes
-// the rows before it again, plainly.  One warp per (row, query head): 32 keys at
+// and 0 times an infinity or a NaN in that key's V is NaN.  It notes whether any
+// O came out infinite or NaN; if so, this kernel looks at every row of a chunk and
+// computes those again, plainly, that have such a V behind them (a key that some
+// rows of its sequence see and others do not is a new token).  One warp per (row, query head): 32 keys at
 // a time, a key per lane for the logits (q from shared memory), then the lanes
 // share out the d columns of V.  It is launched behind every causal chunk call and
 // leaves at once where there is nothing to mend.
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kMendWarps * 32) fa_paged_mend_kernel(const __
     if (b >= a.pb.B) continue;
     bool bad;
     const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, b, bad);
-    if (t < s.row0 || t >= s.row0 + s.n || s.n > a.max_rows || static_cast<long long>(s.n) * a.group <= kFewRows) continue;
+    if (t < s.row0 || t >= s.row0 + s.n || s.n > a.max_rows || (s.n <= kFewMost && s.n * a.group <= a.few_rows)) continue;
     const int see = s.len - s.n + (t - s.row0) + 1;  // keys 0 .. see - 1
     bool odd = false;
     for (int j = max(see, 0) + lane; j < s.len; j += 32) {
@@ -342,27 +342,23 @@ __global__ void __launch_bounds__(kMendWarps * 32) fa_paged_mend_kernel(const __
 template <int D>
 int launch_mend(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   const int ctas = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
-  const MendParams p{a, paged_ws(a.workspace, D).odd, ctas};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas * 4);
-  cfg.blockDim = dim3(kMendWarps * 32);
-  cfg.stream = ctx.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return static_cast<int>(a.e4m3 ? cudaLaunchKernelEx(&cfg, fa_paged_mend_kernel<D, true>, p)
-                                 : cudaLaunchKernelEx(&cfg, fa_paged_mend_kernel<D, false>, p));
+  const MendParams p{a, paged_ws(a.workspace, D).odd, ctas * 4};
+  return a.e4m3 ? launch_dependent(fa_paged_mend_kernel<D, true>, dim3(ctas * 4), kMendWarps * 32, 0, ctx.stream, p)
+                : launch_dependent(fa_paged_mend_kernel<D, false>, dim3(ctas * 4), kMendWarps * 32, 0, ctx.stream, p);
 }
 
-// Sequences of few rows, then the others (unless max_rows says that there are none).
+// Sequences of few rows, then the others (unless max_rows says that there are none), then what CTAs left in parts.
 template <int D>
-int launch_fwd_d(const PagedFwdArgs& a, const LaunchCtx& ctx) {
+int launch_fwd_d(PagedFwdArgs& a, const LaunchCtx& ctx) {
+  const long long most = static_cast<long long>(a.max_rows) * a.group;
+  // 16 rows where that is all there can be, else 32 (d = 256: 16, a thread's registers hold no more outputs).
+  a.few_rows = most <= 16 || D == 256 ? 16 : kFewMost;
+  const bool chunks = most > a.few_rows;
   int e = launch_paged_few<D>(a, ctx);
-  if (e != 0 || static_cast<long long>(a.max_rows) * a.group <= kFewRows) return e;
-  e = launch_paged_chunk<D>(a, ctx);
-  return e != 0 || !a.causal ? e : launch_mend<D>(a, ctx);
+  if (e == 0 && chunks) e = launch_paged_chunk<D>(a, ctx);
+  if (e == 0) e = launch_paged_join<D>(a, chunks, ctx);
+  if (e == 0 && chunks && a.causal) e = launch_mend<D>(a, ctx);
+  return e;
 }
 
 // ------------------------------------------------------------------ checks

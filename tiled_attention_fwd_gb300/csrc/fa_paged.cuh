@@ -111,6 +111,7 @@ struct PagedFwdArgs {
   int q_heads;
   int group;     // query heads per key/value head
   int max_rows;
+  int few_rows;  // rows (tokens x group) of a sequence that the few-row kernel takes at most
   float scale;
   bool causal;
   bool e4m3;

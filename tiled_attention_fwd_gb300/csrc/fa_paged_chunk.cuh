@@ -25,8 +25,6 @@
 //    adds them up: O = sum 2^(L_i - L) O_i, L = log2 sum 2^L_i.
 #pragma once
 
-#include <atomic>
-
 #include "fa_fwd_tc.cuh"
 #include "fa_paged_plan.cuh"
 
@@ -93,18 +91,18 @@ struct ChunkParams {
   int box;      // rows of a K/V box
 };
 
-// sum over i in [0, n) of floor((a i + b) / m), a, b >= 0 (Euclid's way down).
-__host__ __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum over i in [0, n) of floor((a i + b) / m), a, b >= 0, a n + b < 2^32 (Euclid's way down).
+__host__ __device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long sum = 0;
   while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    sum += static_cast<long long>(n) * (n - 1) / 2 * (a / m) + static_cast<long long>(n) * (b / m);
     a %= m;
     b %= m;
-    const long long top = a * n + b;
+    const uint32_t top = a * n + b;
     if (top < m) break;
     n = top / m;
     b = top % m;
-    const long long t = m;
+    const uint32_t t = m;
     m = a;
     a = t;
   }
@@ -135,14 +133,15 @@ struct ChunkBlocks {
     const int past = len - n;
     int one = past < 0 ? -past / tq : 0;
     one = one < k - 1 ? one : k - 1;
-    return one + floor_sum(k - 1 - one, bk, tq, static_cast<long long>(past) + static_cast<long long>(one + 1) * tq + bk - 1) + last;
+    // (Positions are below 2^31, so the sums of a block's end and bk are below 2^32.)
+    return one + floor_sum(k - 1 - one, bk, tq, static_cast<uint32_t>(past + (one + 1) * tq + bk - 1)) + last;
   }
 };
 
 template <int D>
 __device__ __forceinline__ ChunkBlocks chunk_blocks(const ChunkParams& p, const PagedSeq& s) {
   ChunkBlocks c;
-  const bool mine = s.n >= 1 && s.n <= p.a.max_rows && (s.n > kFewRows || s.n * p.a.group > kFewRows);
+  const bool mine = s.n >= 1 && s.n <= p.a.max_rows && (s.n > kFewMost || s.n * p.a.group > p.a.few_rows);
   c.n = mine ? s.n : 0;
   c.len = s.len;
   c.tq = p.tpt * TcCfg<D>::NQT;
@@ -803,6 +802,7 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
   uint32_t a_cnt0 = 0, a_cnt1 = 0, od0 = 0, od1 = 0, lf0 = 0, lf1 = 0;
   uint32_t go_arr = 0;
   bool ok = true;
+  uint64_t odd2 = 0;  // sums of 0 times every O of this thread: NaN if one was infinite or NaN
   auto release_o = [&](int t) {
     if (C::NQT == 2) {
       warp_arrive(bar.pv_go(t, 0));
@@ -869,7 +869,7 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
     const uint32_t to = tmem + lane_off + C::TM_O + t * D;
     const int hq = w.head * p.a.group + head_r;
     __nv_bfloat16* dst = p.a.o + static_cast<long long>(w.row0 + tok) * p.a.os[0] + static_cast<long long>(hq) * p.a.os[1];
-    float* part = p.ws.chunk_part + (static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * chunk_floats(C::ROWS, D);
+    float* part = p.ws.chunk_part + (static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * part_floats(C::ROWS, D);
     float* prow = part + C::ROWS + (static_cast<size_t>(t) * 128 + r) * D;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
@@ -879,6 +879,11 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
       if (c == D / 32 - 1) {
         tc_fence_before();
         release_o(t);
+      }
+      if (mine) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+          odd2 = f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), 0ull, odd2);
       }
       if (mine && w.out == 0) {
 #pragma unroll
@@ -918,7 +923,7 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
     if (!ok || !w.valid) break;
     // A tile whose keys all lie before this part has nothing to add.
     if (C::NQT == 2 && w.n0 == 0)
-      p.ws.chunk_part[(static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * chunk_floats(C::ROWS, D) + r] = -INFINITY;
+      p.ws.chunk_part[(static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * part_floats(C::ROWS, D) + r] = -INFINITY;
     for (int j = 0; ok && j < w.nmax; ++j) {
       if (ok && j >= 1 && j < w.n0) ok = rescale(0, a_cnt0, od0);
       if (C::NO == 2 && ok && j >= 1 && j < w.n1) ok = rescale(1, a_cnt1, od1);
@@ -926,6 +931,9 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
       if (C::NO == 2 && ok && j == w.n1 - 1) ok = epilogue(w, 1, od1, lf1);
     }
   }
+  const float2 odd = f2_unpack(odd2);
+  const int any = __any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f);
+  if (lane == 0) p.ws.odd[blockIdx.x * 4 + quarter] = any;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -1023,60 +1031,107 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   }
 }
 
-// Joins the parts of the units that several CTAs held: block (c, y) the rows y, y + gridDim.y, .. (in fours) of the
-// unit that CTA c began.
+// ------------------------------------------------------------------ joining
+struct JoinParams {
+  PagedFwdArgs a;
+  PagedWs ws;
+  bool chunks;  // the chunk kernel has run
+  int tpt;
+};
+
+// Joins the parts of the units that several CTAs held; blocks (c, .) those of the unit that CTA c began.
 template <int D>
-__global__ void __launch_bounds__(128) fa_paged_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constant__ JoinParams p) {
+  __shared__ float s_o[3][D];
   pdl_wait();
-  constexpr int ROWS = TcCfg<D>::NQT * 128;
-  const PlanRecord rec = p.ws.chunk_rec[blockIdx.x];
-  if (rec.b < 0) return;
-  bool bad;
-  const PagedSeq s = paged_seq(p.a.pb, p.a.kv.ps_log2, rec.b, bad);
-  const ChunkBlocks c = chunk_blocks<D>(p, s);
-  const int ntok = c.tokens(rec.qb);
+  const PagedFwdArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto part = [&](int i) -> const float* {
-    return p.ws.chunk_part + ((static_cast<size_t>(blockIdx.x) + i) * 2 + (i == 0 ? 1 : 0)) * chunk_floats(ROWS, D);
-  };
-  for (int r = blockIdx.y * 4 + warp; r < ROWS; r += gridDim.y * 4) {
-    const int t = r >> 7, tok_r = (r & 127) / p.a.group, head_r = (r & 127) % p.a.group;
-    const int tok = t * p.tpt + tok_r;
-    if (tok_r >= p.tpt || tok >= ntok) continue;
-    float m = -INFINITY;
-    for (int i = 0; i <= rec.more; ++i) m = fmaxf(m, part(i)[r]);
-    float l = 0.f, o[D / 32] = {};
-    for (int i = 0; i <= rec.more; ++i) {
-      const float* x = part(i);
-      if (x[r] == -INFINITY) continue;  // this part saw none of the row's keys
-      const float f = x[r] == m ? 1.f : ex2(x[r] - m);
-      l += f;
+#pragma unroll 1
+  for (int which = 0; which < (p.chunks ? 2 : 1); ++which) {
+    const PlanRecord rec = which == 0 ? p.ws.few_rec[blockIdx.x] : p.ws.chunk_rec[blockIdx.x];
+    if (rec.b < 0) continue;
+    bool bad;
+    const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, rec.b, bad);
+    const int rows = which == 0 ? kFewMost : chunk_rows(D);  // rows of a part
+    const size_t stride = 2 * part_floats(rows, D);          // from one CTA's parts to the next's
+    const float* first = (which == 0 ? p.ws.few_part : p.ws.chunk_part) + blockIdx.x * stride + stride / 2;
+    const float* rest = first + stride / 2;  // part 0 of the next CTA
+    const int n = rec.more + 1;
+    // Few parts: a warp to a row.  Many: the four warps share out a row's parts.
+    const bool split = n > 4;
+    const int step = split ? gridDim.y : gridDim.y * 4;
+    for (int r = split ? blockIdx.y : blockIdx.y * 4 + warp; r < rows; r += step) {
+      int tok, head;
+      if (which == 0) {
+        tok = r / a.group;
+        head = r % a.group;
+        if (tok >= s.n) break;
+      } else {
+        const int tr = (r & 127) / a.group;
+        head = (r & 127) % a.group;
+        const int in = (r >> 7) * p.tpt + tr;
+        tok = rec.qb * p.tpt * (chunk_rows(D) / 128) + in;
+        if (tr >= p.tpt || tok >= s.n) continue;
+      }
+      // m: the largest L; l: sum of 2^(L - m).
+      float m = -INFINITY;
+      for (int i = lane; i < n; i += 32) m = fmaxf(m, i == 0 ? first[r] : rest[(i - 1) * stride + r]);
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) o[k] += x[ROWS + static_cast<size_t>(r) * D + k * 32 + lane] * f;
+      for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+      float l = 0.f, o[D / 32] = {};
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < n) {
+          const float x = i0 + lane == 0 ? first[r] : rest[(i0 + lane - 1) * stride + r];
+          w = x == -INFINITY ? 0.f : ex2(x - m);  // (a part that saw none of the row's keys holds no O)
+        }
+        float sum = w;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        l += sum;
+        const int to = min(32, n - i0);
+#pragma unroll 4
+        for (int i = split ? warp : 0; i < to; i += split ? 4 : 1) {
+          const float f = __shfl_sync(0xffffffffu, w, i);
+          const float* x = (i0 + i == 0 ? first : rest + (i0 + i - 1) * stride) + rows + static_cast<size_t>(r) * D;
+          if (f != 0.f) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) o[c] = fmaf(x[c * 32 + lane], f, o[c]);
+          }
+        }
+      }
+      if (split) {
+        if (warp > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) s_o[warp - 1][c * 32 + lane] = o[c];
+        }
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+            o[c] = (o[c] + s_o[0][c * 32 + lane]) + (s_o[1][c * 32 + lane] + s_o[2][c * 32 + lane]);
+        }
+        __syncthreads();
+        if (warp > 0) continue;
+      }
+      const int row = s.row0 + tok, hq = rec.head * a.group + head;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      __nv_bfloat16* dst = a.o + static_cast<long long>(row) * a.os[0] + static_cast<long long>(hq) * a.os[1];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) dst[c * 32 + lane] = __float2bfloat16_rn(o[c] * inv);
+      if (lane == 0) a.lse[static_cast<long long>(hq) * a.pb.rows + row] = (m + log2f(l)) * 0.69314718055994531f;
     }
-    const int row = s.row0 + rec.qb * c.tq + tok, hq = rec.head * p.a.group + head_r;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16* dst = p.a.o + static_cast<long long>(row) * p.a.os[0] + static_cast<long long>(hq) * p.a.os[1];
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) dst[k * 32 + lane] = __float2bfloat16_rn(o[k] * inv);
-    if (lane == 0) p.a.lse[static_cast<long long>(hq) * p.a.pb.rows + row] = (m + log2f(l)) * 0.69314718055994531f;
   }
 }
 
-// ------------------------------------------------------------------ launch
-inline cudaError_t launch_pdl(void (*kernel)(ChunkParams), dim3 grid, int threads, cudaStream_t stream, const ChunkParams& p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+template <int D>
+int launch_paged_join(const PagedFwdArgs& a, bool chunks, const LaunchCtx& ctx) {
+  const int ctas = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
+  const JoinParams p{a, paged_ws(a.workspace, D), chunks, 128 / a.group};
+  return launch_dependent(fa_paged_join_kernel<D>, dim3(ctas, 16), 128, 0, ctx.stream, p);
 }
 
+// ------------------------------------------------------------------ launch
 template <int D, bool E4M3>
 int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   using C = ChunkCfg<D, E4M3>;
@@ -1094,8 +1149,9 @@ int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
     }
     if (regs != C::LAUNCH_REGS) return -2;
   }
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
-  if (e != cudaSuccess) return static_cast<int>(e);
+  static std::atomic<unsigned long long> allowed{0};
+  const int e = allow_smem(kernel, C::SMEM_ALLOC, allowed);
+  if (e != 0) return e;
   ChunkParams p;
   p.a = a;
   p.ws = paged_ws(a.workspace, D);
@@ -1116,19 +1172,7 @@ int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   if (encode_paged_map(&mk, a.kv.k, E4M3 ? 1 : 2, dims, ks, cols, p.box, 1, swizzle, true) != 0) return -1;
   if (encode_paged_map(&mv, a.kv.v, E4M3 ? 1 : 2, dims, vs, cols, p.box, 1, swizzle, true) != 0) return -1;
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM_ALLOC;
-  cfg.stream = ctx.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, p);
-  if (e != cudaSuccess) return static_cast<int>(e);
-  return static_cast<int>(launch_pdl(fa_paged_chunk_join_kernel<D>, dim3(grid, 8), 128, ctx.stream, p));
+  return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mq, mk, mv, p);
 }
 
 template <int D>

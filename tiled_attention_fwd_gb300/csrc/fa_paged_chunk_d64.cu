@@ -1,6 +1,7 @@
-// Paged attention of chunks and prompts, head dimension 64.
+// Paged attention of chunks and prompts (and the joining of parts), head dimension 64.
 #include "fa_paged_chunk.cuh"
 
 namespace fa {
 template int launch_paged_chunk<64>(const PagedFwdArgs& a, const LaunchCtx& ctx);
+template int launch_paged_join<64>(const PagedFwdArgs& a, bool chunks, const LaunchCtx& ctx);
 }

@@ -7,6 +7,8 @@
 // order of their CTAs (so results do not depend on timing).
 #pragma once
 
+#include <atomic>
+
 #include "fa_paged.cuh"
 
 namespace fa {
@@ -106,17 +108,18 @@ struct alignas(16) PlanRecord {
   int more;
 };
 
-// Workspace of fa_paged_fwd.
+// Workspace of fa_paged_fwd.  A part holds a row's log2-sum-exp2 L (log2 units of the scaled logits) and its
+// normalised O in fp32; parts join as O = sum 2^(L_i - L) O_i, L = log2 sum 2^L_i.
 struct PagedWs {
   PlanRecord* few_rec;    // [kPlanCtas]
   PlanRecord* chunk_rec;  // [kPlanCtas]
-  int* odd;               // [kPlanCtas]: a CTA of the few-row kernel met an infinity or a NaN in a chunk's new V
-  float* few_part;        // [kPlanCtas][2][few_floats(d)]: m, l and O of 16 rows
-  float* chunk_part;      // [kPlanCtas][2][chunk_floats(rows, d)]: log-sums and O of a query block
+  int* odd;               // [kPlanCtas][4]: a correction warp of the chunk kernel met an infinity or a NaN in O
+  float* few_part;        // [kPlanCtas][2][part_floats(kFewMost, d)]
+  float* chunk_part;      // [kPlanCtas][2][part_floats(chunk_rows(d), d)]
 };
-constexpr int kFewRows = 16;  // rows of a unit of the few-row kernel at most
-constexpr __host__ __device__ size_t few_floats(int d) { return static_cast<size_t>(kFewRows) * (d + 2); }
-constexpr __host__ __device__ size_t chunk_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 1); }
+constexpr int kFewMost = 32;  // rows of a unit of the few-row kernel at most
+constexpr __host__ __device__ int chunk_rows(int d) { return d <= 128 ? 256 : 128; }  // of a query block
+constexpr __host__ __device__ size_t part_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 1); }
 inline size_t paged_ws_layout(char* p, int d, PagedWs* w) {
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -127,9 +130,9 @@ inline size_t paged_ws_layout(char* p, int d, PagedWs* w) {
   PagedWs x;
   x.few_rec = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
   x.chunk_rec = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
-  x.odd = reinterpret_cast<int*>(take(kPlanCtas * sizeof(int)));
-  x.few_part = reinterpret_cast<float*>(take(kPlanCtas * 2 * few_floats(d) * sizeof(float)));
-  x.chunk_part = reinterpret_cast<float*>(take(kPlanCtas * 2 * chunk_floats(d <= 128 ? 256 : 128, d) * sizeof(float)));
+  x.odd = reinterpret_cast<int*>(take(kPlanCtas * 4 * sizeof(int)));
+  x.few_part = reinterpret_cast<float*>(take(kPlanCtas * 2 * part_floats(kFewMost, d) * sizeof(float)));
+  x.chunk_part = reinterpret_cast<float*>(take(kPlanCtas * 2 * part_floats(chunk_rows(d), d) * sizeof(float)));
   if (w) *w = x;
   return at;
 }
@@ -149,5 +152,36 @@ template <int D>
 int launch_paged_few(const PagedFwdArgs& a, const LaunchCtx& ctx);
 template <int D>
 int launch_paged_chunk(const PagedFwdArgs& a, const LaunchCtx& ctx);
+template <int D>
+int launch_paged_join(const PagedFwdArgs& a, bool chunks, const LaunchCtx& ctx);
+
+// Launch behind the stream's previous kernel, which may still run: the kernel waits for it itself (pdl_wait).
+template <class... P, class... A>
+int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
+// Allow a kernel its dynamic shared memory, once per device (the attribute is per function and device).
+template <class K>
+int allow_smem(K* kernel, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return 0;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return static_cast<int>(e);
+}
 
 }  // namespace fa
