@@ -351,8 +351,8 @@ int launch_mend(const PagedFwdArgs& a, const LaunchCtx& ctx) {
 template <int D>
 int launch_fwd_d(PagedFwdArgs& a, const LaunchCtx& ctx) {
   const long long most = static_cast<long long>(a.max_rows) * a.group;
-  // 16 rows where that is all there can be, else 32 (d = 256: 16, a thread's registers hold no more outputs).
-  a.few_rows = most <= 16 || D == 256 ? 16 : kFewMost;
+  // 8 or 16 rows where that is all there can be, else 32 (d = 256: 16, a thread's registers hold no more outputs).
+  a.few_rows = most <= 8 ? 8 : most <= 16 || D == 256 ? 16 : kFewMost;
   const bool chunks = most > a.few_rows;
   int e = launch_paged_few<D>(a, ctx);
   if (e == 0 && chunks) e = launch_paged_chunk<D>(a, ctx);
