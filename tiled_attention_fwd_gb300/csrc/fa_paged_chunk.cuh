@@ -359,9 +359,12 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
     if constexpr (!E4M3) {
       const int st = pos % C::NST;
       const uint32_t par = (pos / C::NST) & 1;
-      if (!warp_wait_bar(bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
       const uint32_t full = bar.kv_full(st);
       const int n0 = boxes(t0, t0.key0, C::BK), n1 = t1.kind ? boxes(t1, t1.key0, C::BK) : 0;
+      // The pages are looked up while the stage is still being read.
+      const int page0 = lane < n0 ? page_of(t0, t0.key0 + lane * p.box) : 0;
+      const int page1 = lane < n1 ? page_of(t1, t1.key0 + lane * p.box) : 0;
+      if (!warp_wait_bar(bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
       if (lane == 0) mbar_arrive_expect_tx(full, (n0 + n1) * p.box * D * 2);
       __syncwarp();
 #pragma unroll
@@ -369,7 +372,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
         const ChunkTile& t = i == 0 ? t0 : t1;
         if (lane < (i == 0 ? n0 : n1)) {
           const int key = t.key0 + lane * p.box;
-          const int page = page_of(t, key);
+          const int page = i == 0 ? page0 : page1;
           const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE + lane * p.box * C::SWB;
           for (int r = 0; r < C::NR; ++r)
             tma_load_4d(dst + r * C::K_REGION, t.kind == 1 ? tm_k : tm_v, full, r * C::RC, key & slot_mask, t.head, page,
@@ -386,15 +389,15 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
         for (int h = 0; h < 2; ++h) {
           const int st = pos % C::NSLOT;
           const uint32_t par = (pos / C::NSLOT) & 1;
-          if (!warp_wait_bar(bar.slot_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
           const uint32_t full = bar.slot_full(st);
           const int key0 = t.key0 + h * C::SLOT_ROWS;
           const int n = boxes(t, key0, C::SLOT_ROWS);
+          const int page = lane < n ? page_of(t, key0 + lane * p.box) : 0;
+          if (!warp_wait_bar(bar.slot_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
           if (lane == 0) mbar_arrive_expect_tx(full, n * p.box * (D + 1));
           __syncwarp();
           if (lane < n) {
             const int key = key0 + lane * p.box;
-            const int page = page_of(t, key);
             const uint32_t sc = base + C::OFF_SCALE + st * C::SLOT_ROWS + lane * p.box;
             tma_load_4d(base + C::OFF_OST + st * C::SLOT + lane * p.box * D, t.kind == 1 ? tm_k : tm_v, full, 0,
                         key & slot_mask, t.head, page, pol_kv);
@@ -461,32 +464,49 @@ __device__ __forceinline__ void chunk_convert(const ChunkParams& p, const ChunkB
         const uint8_t* scales = gbase + C::OFF_SCALE + sl * C::SLOT_ROWS;
         const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE;
         const int end = t.len - (t.key0 + h * C::SLOT_ROWS);  // rows of this half that are keys
-        constexpr int UPR = D / 8;                             // 16-byte units of a bf16 row
-        constexpr int UNITS = C::SLOT_ROWS * UPR;
-#pragma unroll 4
-        for (int u0 = 0; u0 < UNITS; u0 += 64) {
-          const int u = u0 + cw * 32 + lane;
-          const int row = u / UPR, unit16 = u % UPR;
-          const uint2 x = *reinterpret_cast<const uint2*>(codes + u * 8);
-          const uint32_t byte = scales[row];
-          uint32_t f = byte > 134u ? 254u << 7 : (byte + 120u) << 7;  // 2^(120 + e), 2^127 at most
-          f = byte == 255u ? 0x7fc0u : f;
-          f |= f << 16;
-          uint32_t w[4];
-          e4m3x4_to_bf16x4(x.x, f, w[0], w[1]);
-          e4m3x4_to_bf16x4(x.y, f, w[2], w[3]);
-          if (byte > 134u) {
-            uint32_t f2 = byte == 255u ? 0x3f80u : (byte - 7u) << 7;  // 2^(e - 7)
-            f2 |= f2 << 16;
+        constexpr int UPR = D / 8;        // 16-byte units of a bf16 row
+        constexpr int RPP = 64 / UPR;     // rows of a pass of the 64 threads
+        constexpr int PASSES = C::SLOT_ROWS / RPP;
+        constexpr int UR = C::SWB / 16;
+        static_assert(PASSES % 4 == 0 && 4 * RPP % 8 == 0, "four passes are whole swizzle periods");
+        const int row0 = (cw * 32 + lane) / UPR, unit16 = lane % UPR;
+        const uint32_t* sw4 = reinterpret_cast<const uint32_t*>(scales);
+        const uint32_t big = lane < C::SLOT_ROWS / 4 ? __vcmpgtu4(sw4[lane], 0x86868686u) : 0u;  // a byte > 134
+        uint32_t to[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = mul_bf16x2(w[k], f2);
+        for (int k = 0; k < 4; ++k) {
+          const int r = k * RPP + row0;
+          const uint32_t sw = C::SWB == 128 ? r & 7 : (r >> 1) & 3;
+          to[k] = dst + (unit16 / UR) * C::K_REGION + (h * C::SLOT_ROWS + r) * C::SWB + (((unit16 % UR) ^ sw) << 4);
+        }
+        const bool fast = end >= C::SLOT_ROWS && !__any_sync(0xffffffffu, big != 0);
+#pragma unroll 1
+        for (int pass = 0; pass < PASSES; pass += 4) {
+          uint2 x[4];
+          uint32_t byte[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = (pass + k) * RPP + row0;
+            x[k] = *reinterpret_cast<const uint2*>(codes + r * D + unit16 * 8);
+            byte[k] = scales[r];
           }
-          if (row >= end) w[0] = w[1] = w[2] = w[3] = 0u;
-          const int trow = h * C::SLOT_ROWS + row;
-          constexpr int UR = C::SWB / 16;
-          const uint32_t sw = C::SWB == 128 ? trow & 7 : (trow >> 1) & 3;
-          st_shared_v4(dst + (unit16 / UR) * C::K_REGION + trow * C::SWB + (((unit16 % UR) ^ sw) << 4), w[0], w[1], w[2],
-                       w[3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+            uint32_t f = byte[k] * 0x00800080u + 120u * 0x00800080u;  // 2^(120 + e), twice
+            if (!fast) {
+              f = byte[k] == 255u ? 0x7fc07fc0u : byte[k] > 134u ? 0x7f007f00u : f;  // NaN, or 2^127 at most
+            }
+            e4m3x4_to_bf16x4(x[k].x, f, w[0], w[1]);
+            e4m3x4_to_bf16x4(x[k].y, f, w[2], w[3]);
+            if (!fast) {
+              const uint32_t f2 = byte[k] > 134u && byte[k] != 255u ? (byte[k] - 7u) * 0x00800080u : 0x3f803f80u;  // 2^(e - 7)
+              const bool past = (pass + k) * RPP + row0 >= end;
+#pragma unroll
+              for (int i2 = 0; i2 < 4; ++i2) w[i2] = past ? 0u : mul_bf16x2(w[i2], f2);
+            }
+            st_shared_v4(to[k] + pass * RPP * C::SWB, w[0], w[1], w[2], w[3]);
+          }
         }
         warp_arrive(bar.slot_empty(sl));
       }
@@ -868,9 +888,11 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
     const bool mine = tok_r < p.tpt && tok < w.ntok;
     const uint32_t to = tmem + lane_off + C::TM_O + t * D;
     const int hq = w.head * p.a.group + head_r;
-    __nv_bfloat16* dst = p.a.o + static_cast<long long>(w.row0 + tok) * p.a.os[0] + static_cast<long long>(hq) * p.a.os[1];
+    // Where this row of O is (-1: it is no row).
+    const long long row_off =
+        mine ? static_cast<long long>(w.row0 + tok) * p.a.os[0] + static_cast<long long>(hq) * p.a.os[1] : -1ll;
     float* part = p.ws.chunk_part + (static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * part_floats(C::ROWS, D);
-    float* prow = part + C::ROWS + (static_cast<size_t>(t) * 128 + r) * D;
+    float4* pblk = reinterpret_cast<float4*>(part + C::ROWS + static_cast<size_t>(t) * 128 * D) + r;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t v[32];
@@ -885,23 +907,49 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
         for (int i = 0; i < 32; i += 2)
           odd2 = f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), 0ull, odd2);
       }
-      if (mine && w.out == 0) {
+      if (w.out == 0) {
+        // 16-byte block k of this row; the four rows of a quad are transposed so that a quad's threads store a row's 64
+        // bytes together (a thread storing its own row's blocks would touch 32 lines an instruction).
+        uint32_t y[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t y[4];
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int k2 = 0; k2 < 4; ++k2) {
             const float2 x = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[8 * i + 2 * k2]), __uint_as_float(v[8 * i + 2 * k2 + 1])), il2));
-            y[k2] = pack_bf16x2(x.x, x.y);
+            y[i][k2] = pack_bf16x2(x.x, x.y);
           }
-          *reinterpret_cast<uint4*>(dst + c * 32 + 8 * i) = make_uint4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+        for (int x = 1; x <= 2; x <<= 1) {
+          const bool up = (lane & x) != 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i & x) continue;
+#pragma unroll
+            for (int k2 = 0; k2 < 4; ++k2) {
+              // Blocks i and i + x: the lower thread of a pair keeps i and takes the partner's i, the upper likewise i + x.
+              const uint32_t give = up ? y[i][k2] : y[i + x][k2];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, give, x);
+              if (up)
+                y[i][k2] = got;
+              else
+                y[i + x][k2] = got;
+            }
+          }
         }
-      } else if (mine) {
+        // Now y[i] is block lane & 3 of the quad's row i.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const long long off = __shfl_sync(0xffffffffu, row_off, (lane & 28) + i);
+          if (off >= 0)
+            *reinterpret_cast<uint4*>(p.a.o + off + c * 32 + 8 * (lane & 3)) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
+        }
+      } else {
+        // 16-byte block i of all 128 rows of the tile together.
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float2 x = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), il2));
           const float2 y = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), il2));
-          *reinterpret_cast<float4*>(prow + c * 32 + 4 * i) = make_float4(x.x, x.y, y.x, y.y);
+          pblk[(c * 8 + i) * 128] = make_float4(x.x, x.y, y.x, y.y);
         }
       }
       __syncwarp();
@@ -1046,81 +1094,116 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
   pdl_wait();
   const PagedFwdArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int which = 0; which < (p.chunks ? 2 : 1); ++which) {
-    const PlanRecord rec = which == 0 ? p.ws.few_rec[blockIdx.x] : p.ws.chunk_rec[blockIdx.x];
-    if (rec.b < 0) continue;
-    bool bad;
-    const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, rec.b, bad);
-    const int rows = which == 0 ? kFewMost : chunk_rows(D);  // rows of a part
-    const size_t stride = 2 * part_floats(rows, D);          // from one CTA's parts to the next's
-    const float* first = (which == 0 ? p.ws.few_part : p.ws.chunk_part) + blockIdx.x * stride + stride / 2;
-    const float* rest = first + stride / 2;  // part 0 of the next CTA
-    const int n = rec.more + 1;
-    // Few parts: a warp to a row.  Many: the four warps share out a row's parts.
-    const bool split = n > 4;
-    const int step = split ? gridDim.y : gridDim.y * 4;
-    for (int r = split ? blockIdx.y : blockIdx.y * 4 + warp; r < rows; r += step) {
-      int tok, head;
-      if (which == 0) {
-        tok = r / a.group;
-        head = r % a.group;
-        if (tok >= s.n) break;
-      } else {
-        const int tr = (r & 127) / a.group;
-        head = (r & 127) % a.group;
-        const int in = (r >> 7) * p.tpt + tr;
-        tok = rec.qb * p.tpt * (chunk_rows(D) / 128) + in;
+  if (p.chunks) {
+    const PlanRecord rec = p.ws.chunk_rec[blockIdx.x];
+    if (rec.b >= 0) {
+      // A warp takes 16 columns of 32 rows, a row a lane (parts hold blocks of 4 columns of all rows of a tile).
+      constexpr int ROWS = chunk_rows(D);
+      bool bad;
+      const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, rec.b, bad);
+      constexpr size_t stride = 2 * part_floats(ROWS, D);  // from one CTA's parts to the next's
+      const float* first = p.ws.chunk_part + blockIdx.x * stride + stride / 2;
+      const float* rest = first + stride / 2 - stride;  // part 0 of CTA + i at rest + i * stride
+      const int n = rec.more + 1;
+      for (int job = blockIdx.y * 4 + warp; job < ROWS / 32 * (D / 16); job += gridDim.y * 4) {
+        const int r = job % (ROWS / 32) * 32 + lane, c16 = job / (ROWS / 32);
+        const int tr = (r & 127) / a.group, head = (r & 127) % a.group;
+        const int tok = (rec.qb * (ROWS / 128) + (r >> 7)) * p.tpt + tr;
         if (tr >= p.tpt || tok >= s.n) continue;
-      }
-      // m: the largest L; l: sum of 2^(L - m).
-      float m = -INFINITY;
-      for (int i = lane; i < n; i += 32) m = fmaxf(m, i == 0 ? first[r] : rest[(i - 1) * stride + r]);
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-      float l = 0.f, o[D / 32] = {};
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        float w = 0.f;
-        if (i0 + lane < n) {
-          const float x = i0 + lane == 0 ? first[r] : rest[(i0 + lane - 1) * stride + r];
-          w = x == -INFINITY ? 0.f : ex2(x - m);  // (a part that saw none of the row's keys holds no O)
-        }
-        float sum = w;
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-        l += sum;
-        const int to = min(32, n - i0);
+        float m = -INFINITY;
 #pragma unroll 4
-        for (int i = split ? warp : 0; i < to; i += split ? 4 : 1) {
-          const float f = __shfl_sync(0xffffffffu, w, i);
-          const float* x = (i0 + i == 0 ? first : rest + (i0 + i - 1) * stride) + rows + static_cast<size_t>(r) * D;
-          if (f != 0.f) {
+        for (int i = 0; i < n; ++i) m = fmaxf(m, (i == 0 ? first : rest + i * stride)[r]);
+        float l = 0.f;
+        float4 o[4] = {};
+        const size_t at = ROWS + static_cast<size_t>(r >> 7) * 128 * D + (static_cast<size_t>(c16) * 4 * 128 + (r & 127)) * 4;
+#pragma unroll 2
+        for (int i = 0; i < n; ++i) {
+          const float* x = i == 0 ? first : rest + i * stride;
+          const float lg = x[r];
+          if (lg == -INFINITY) continue;  // (a part that saw none of the row's keys holds no O)
+          const float f = ex2(lg - m);
+          l += f;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) o[c] = fmaf(x[c * 32 + lane], f, o[c]);
+          for (int k = 0; k < 4; ++k) {
+            const float4 y = *reinterpret_cast<const float4*>(x + at + k * 512);
+            o[k].x = fmaf(y.x, f, o[k].x);
+            o[k].y = fmaf(y.y, f, o[k].y);
+            o[k].z = fmaf(y.z, f, o[k].z);
+            o[k].w = fmaf(y.w, f, o[k].w);
           }
         }
+        const int row = s.row0 + tok, hq = rec.head * a.group + head;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint4* dst = reinterpret_cast<uint4*>(a.o + static_cast<long long>(row) * a.os[0] +
+                                              static_cast<long long>(hq) * a.os[1] + c16 * 16);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          dst[k] = make_uint4(pack_bf16x2(o[2 * k].x * inv, o[2 * k].y * inv), pack_bf16x2(o[2 * k].z * inv, o[2 * k].w * inv),
+                              pack_bf16x2(o[2 * k + 1].x * inv, o[2 * k + 1].y * inv),
+                              pack_bf16x2(o[2 * k + 1].z * inv, o[2 * k + 1].w * inv));
+        if (c16 == 0) a.lse[static_cast<long long>(hq) * a.pb.rows + row] = (m + log2f(l)) * 0.69314718055994531f;
       }
-      if (split) {
-        if (warp > 0) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) s_o[warp - 1][c * 32 + lane] = o[c];
-        }
-        __syncthreads();
-        if (warp == 0) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-            o[c] = (o[c] + s_o[0][c * 32 + lane]) + (s_o[1][c * 32 + lane] + s_o[2][c * 32 + lane]);
-        }
-        __syncthreads();
-        if (warp > 0) continue;
-      }
-      const int row = s.row0 + tok, hq = rec.head * a.group + head;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      __nv_bfloat16* dst = a.o + static_cast<long long>(row) * a.os[0] + static_cast<long long>(hq) * a.os[1];
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) dst[c * 32 + lane] = __float2bfloat16_rn(o[c] * inv);
-      if (lane == 0) a.lse[static_cast<long long>(hq) * a.pb.rows + row] = (m + log2f(l)) * 0.69314718055994531f;
     }
+  }
+  const PlanRecord rec = p.ws.few_rec[blockIdx.x];
+  if (rec.b < 0) return;
+  bool bad;
+  const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, rec.b, bad);
+  constexpr size_t stride = 2 * part_floats(kFewMost, D);
+  const float* first = p.ws.few_part + blockIdx.x * stride + stride / 2;
+  const float* rest = first + stride / 2 - stride;
+  const int n = rec.more + 1;
+  // Few parts: a warp to a row.  Many: the four warps share out a row's parts.
+  const bool split = n > 4;
+  const int step = split ? gridDim.y : gridDim.y * 4;
+  for (int r = split ? blockIdx.y : blockIdx.y * 4 + warp; r < s.n * a.group; r += step) {
+    // m: the largest L; l: sum of 2^(L - m).
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, (i == 0 ? first : rest + i * stride)[r]);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    float l = 0.f, o[D / 32] = {};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float w = 0.f;
+      if (i0 + lane < n) {
+        const float x = (i0 + lane == 0 ? first : rest + (i0 + lane) * stride)[r];
+        w = x == -INFINITY ? 0.f : ex2(x - m);
+      }
+      float sum = w;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+      l += sum;
+      const int to = min(32, n - i0);
+#pragma unroll 4
+      for (int i = split ? warp : 0; i < to; i += split ? 4 : 1) {
+        const float f = __shfl_sync(0xffffffffu, w, i);
+        const float* x = (i0 + i == 0 ? first : rest + (i0 + i) * stride) + kFewMost + static_cast<size_t>(r) * D;
+        if (f != 0.f) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) o[c] = fmaf(x[c * 32 + lane], f, o[c]);
+        }
+      }
+    }
+    if (split) {
+      if (warp > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) s_o[warp - 1][c * 32 + lane] = o[c];
+      }
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          o[c] = (o[c] + s_o[0][c * 32 + lane]) + (s_o[1][c * 32 + lane] + s_o[2][c * 32 + lane]);
+      }
+      __syncthreads();
+      if (warp > 0) continue;
+    }
+    const int row = s.row0 + r / a.group, hq = rec.head * a.group + r % a.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* dst = a.o + static_cast<long long>(row) * a.os[0] + static_cast<long long>(hq) * a.os[1];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) dst[c * 32 + lane] = __float2bfloat16_rn(o[c] * inv);
+    if (lane == 0) a.lse[static_cast<long long>(hq) * a.pb.rows + row] = (m + log2f(l)) * 0.69314718055994531f;
   }
 }
 
