@@ -32,6 +32,23 @@ namespace fa {
 
 constexpr int kSegRing = 4;
 
+// warp_wait_bar in less code: the kernel has to stay within the SM's instruction cache (about 128 KB; at 150 KB a
+// unit's epilogue, fetched anew each time, took 7000 cycles).
+__device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, const WaitGuard& g, int code) {
+  uint64_t t0 = 0;
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *g.abort)) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (__any_sync(0xffffffffu, now - t0 > g.limit_ns)) {
+      *g.abort = 1;
+      if ((threadIdx.x & 31) == 0) atomicOr(g.status, code);
+      return false;
+    }
+  }
+}
+
 // A run of key tiles of one unit.
 struct alignas(16) ChunkSeg {
   int valid;
@@ -52,10 +69,14 @@ static_assert(sizeof(ChunkSeg) == 48, "segment size");
 template <int D, bool E4M3>
 struct ChunkCfg : TcCfg<D> {
   using T = TcCfg<D>;
-  // e4m3: ring of half key tiles (codes) where the contiguous kernel stages its output.
+  // Staged output: buffers of 32 rows x 32 columns per correction warp; e4m3 keeps one and has a ring of half key
+  // tiles (codes) in the place of the others.
+  static constexpr int OUT_BUFS = E4M3 ? 1 : T::OSTB;
+  static constexpr int OFF_OUT = T::OFF_OST;
+  static constexpr int OFF_SLOT = T::OFF_OST + 4 * OUT_BUFS * T::OST_BUF;
   static constexpr int SLOT_ROWS = T::BK / 2;
   static constexpr int SLOT = SLOT_ROWS * D;
-  static constexpr int NSLOT = T::OST / SLOT > 4 ? 4 : T::OST / SLOT;
+  static constexpr int NSLOT = !E4M3 ? 0 : (T::OST - 4 * T::OST_BUF) / SLOT > 4 ? 4 : (T::OST - 4 * T::OST_BUF) / SLOT;
   static constexpr int OFF_SEG = T::OFF_MISC + 6672;
   static constexpr int OFF_SCALE = OFF_SEG + kSegRing * static_cast<int>(sizeof(ChunkSeg));  // [NSLOT][SLOT_ROWS]
   static constexpr int OFF_PLAN = T::OFF_ALPHA;  // before the roles start
@@ -65,7 +86,7 @@ struct ChunkCfg : TcCfg<D> {
   static constexpr int ROWS = T::NQT * 128;
   static_assert(T::OFF_ABORT + 4 <= OFF_SEG && OFF_SEG % 16 == 0, "misc area");
   static_assert(OFF_SCALE + NSLOT * SLOT_ROWS <= T::OFF_MISC + T::MISC, "misc area");
-  static_assert(NSLOT >= 2 && sizeof(PlanScratch) <= 2048, "rings");
+  static_assert((!E4M3 || NSLOT >= 2) && sizeof(PlanScratch) <= 2048, "rings");
 };
 
 template <int D, bool E4M3>
@@ -89,6 +110,7 @@ struct ChunkParams {
   float scale_log2;
   int tpt;      // tokens of a 128-row tile: 128 / group
   int box;      // rows of a K/V box
+  bool tma_o;   // a warp's 32 rows are a box of O (the group is a power of two)
 };
 
 // sum over i in [0, n) of floor((a i + b) / m), a, b >= 0, a n + b < 2^32 (Euclid's way down).
@@ -211,10 +233,13 @@ __device__ __forceinline__ ChunkSeg* seg_slot(uint8_t* gbase, int k) {
 }
 
 // Segment k, read by a whole warp of a role other than the load warp.
-template <int D, bool E4M3>
+// (INLINE: the softmax warps' registers are full, and a call would spill them.)
+template <int D, bool E4M3, bool INLINE = false>
 __device__ __forceinline__ bool seg_read(ChunkSeg& g, int k, uint8_t* gbase, const ChunkBars<D, E4M3>& bar,
                                          const WaitGuard& guard) {
-  if (!warp_wait_bar(bar.seg_full(k % kSegRing), (k / kSegRing) & 1, guard, kStatusTimeoutLoad)) return false;
+  const uint32_t full = bar.seg_full(k % kSegRing), par = (k / kSegRing) & 1;
+  if (!(INLINE ? warp_wait_bar(full, par, guard, kStatusTimeoutLoad) : chunk_wait(full, par, guard, kStatusTimeoutLoad)))
+    return false;
   const int4* src = reinterpret_cast<const int4*>(seg_slot<D, E4M3>(gbase, k));
   int4* dst = reinterpret_cast<int4*>(&g);
 #pragma unroll
@@ -242,30 +267,30 @@ __device__ __forceinline__ bool chunk_stream(const Get& get, const Unit& unit, c
   const ChunkTile none{0, 0, 0, 0, 0};
   ChunkSeg w;
   if (!get(0, w)) return false;
-  if constexpr (C::NQT == 2) {
-    if (!w.valid) return true;
-    if (!unit(w, 0) || !stage(chunk_tile<D>(1, w, 0), none)) return false;
-    for (int k = 0;; ++k) {
-      ChunkSeg wn;
-      if (!get(k + 1, wn)) return false;
-      for (int j = 0; j < w.nmax; ++j) {
-        const ChunkTile kt = j + 1 < w.nmax ? chunk_tile<D>(1, w, j + 1) : wn.valid ? chunk_tile<D>(1, wn, 0) : none;
-        if (!stage(chunk_tile<D>(2, w, j), kt)) return false;
+#pragma unroll 1
+  for (int k = 0; w.valid; ++k) {
+    ChunkSeg wn;
+    if (C::NQT == 2 && !get(k + 1, wn)) return false;
+    if (!unit(w, k)) return false;
+    // Two tiles: the first stage of all holds K_0 alone; one tile: every unit begins with K_0 and K_1.
+#pragma unroll 1
+    for (int j = C::NQT == 1 || k == 0 ? -1 : 0; j < w.nmax; ++j) {
+      ChunkTile t1 = none;
+      if constexpr (C::NQT == 2) {
+        if (j >= 0 && j + 1 < w.nmax)
+          t1 = chunk_tile<D>(1, w, j + 1);
+        else if (j >= 0 && wn.valid)
+          t1 = chunk_tile<D>(1, wn, 0);
+      } else {
+        const int next = j < 0 ? 1 : j + C::LA;
+        if (next < w.nmax) t1 = chunk_tile<D>(1, w, next);
       }
-      if (!wn.valid) return true;
-      if (!unit(wn, k + 1)) return false;
-      w = wn;
+      if (!stage(j < 0 ? chunk_tile<D>(1, w, 0) : chunk_tile<D>(2, w, j), t1)) return false;
     }
-  } else {
-    for (int k = 0; w.valid; ++k) {
-      if (!unit(w, k)) return false;
-      if (!stage(chunk_tile<D>(1, w, 0), 1 < w.nmax ? chunk_tile<D>(1, w, 1) : none)) return false;
-      for (int j = 0; j < w.nmax; ++j)
-        if (!stage(chunk_tile<D>(2, w, j), j + C::LA < w.nmax ? chunk_tile<D>(1, w, j + C::LA) : none)) return false;
-      if (!get(k + 1, w)) return false;
-    }
-    return true;
+    if (C::NQT == 1 && !get(k + 1, wn)) return false;
+    w = wn;
   }
+  return true;
 }
 
 // ------------------------------------------------------------------ load warp
@@ -318,7 +343,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
 
   auto get = [&](int k, ChunkSeg& w) -> bool {
     const int i = k % kSegRing;
-    if (!warp_wait_bar(bar.seg_empty(i), ((k / kSegRing) & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
+    if (!chunk_wait(bar.seg_empty(i), ((k / kSegRing) & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
     w = walk.next(p);
     if (lane == 0) {
       *seg_slot<D, E4M3>(gbase, k) = w;
@@ -333,7 +358,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
   };
   auto unit = [&](const ChunkSeg& w, int k) -> bool {
     for (int t = 0; t < C::NQT; ++t) {
-      if (!warp_wait_bar(bar.q_empty(t), (k & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
+      if (!chunk_wait(bar.q_empty(t), (k & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
       if (lane == 0) {
         mbar_arrive_expect_tx(bar.q_full(t), p.tpt * p.a.group * D * 2);
         for (int r = 0; r < C::NR; ++r)
@@ -364,7 +389,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
       // The pages are looked up while the stage is still being read.
       const int page0 = lane < n0 ? page_of(t0, t0.key0 + lane * p.box) : 0;
       const int page1 = lane < n1 ? page_of(t1, t1.key0 + lane * p.box) : 0;
-      if (!warp_wait_bar(bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
+      if (!chunk_wait(bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
       if (lane == 0) mbar_arrive_expect_tx(full, (n0 + n1) * p.box * D * 2);
       __syncwarp();
 #pragma unroll
@@ -393,13 +418,13 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
           const int key0 = t.key0 + h * C::SLOT_ROWS;
           const int n = boxes(t, key0, C::SLOT_ROWS);
           const int page = lane < n ? page_of(t, key0 + lane * p.box) : 0;
-          if (!warp_wait_bar(bar.slot_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
+          if (!chunk_wait(bar.slot_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
           if (lane == 0) mbar_arrive_expect_tx(full, n * p.box * (D + 1));
           __syncwarp();
           if (lane < n) {
             const int key = key0 + lane * p.box;
             const uint32_t sc = base + C::OFF_SCALE + st * C::SLOT_ROWS + lane * p.box;
-            tma_load_4d(base + C::OFF_OST + st * C::SLOT + lane * p.box * D, t.kind == 1 ? tm_k : tm_v, full, 0,
+            tma_load_4d(base + C::OFF_SLOT + st * C::SLOT + lane * p.box * D, t.kind == 1 ? tm_k : tm_v, full, 0,
                         key & slot_mask, t.head, page, pol_kv);
             // (For a page that is not there any scales do.)
             const long long pg = page == p.a.kv.num_pages ? 0 : page;
@@ -452,15 +477,15 @@ __device__ __forceinline__ void chunk_convert(const ChunkParams& p, const ChunkB
   auto unit = [&](const ChunkSeg&, int) -> bool { return true; };
   auto stage = [&](const ChunkTile& t0, const ChunkTile& t1) -> bool {
     const int st = pos % C::NST;
-    if (!warp_wait_bar(bar.kv_empty(st), ((pos / C::NST) & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
+    if (!chunk_wait(bar.kv_empty(st), ((pos / C::NST) & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
     ++pos;
     for (int i = 0; i < 2; ++i) {
       const ChunkTile& t = i == 0 ? t0 : t1;
       if (t.kind == 0) continue;
       for (int h = 0; h < 2; ++h, ++half) {
         const int sl = half % C::NSLOT;
-        if (!warp_wait_bar(bar.slot_full(sl), (half / C::NSLOT) & 1, g, kStatusTimeoutLoad)) return false;
-        const uint8_t* codes = gbase + C::OFF_OST + sl * C::SLOT;
+        if (!chunk_wait(bar.slot_full(sl), (half / C::NSLOT) & 1, g, kStatusTimeoutLoad)) return false;
+        const uint8_t* codes = gbase + C::OFF_SLOT + sl * C::SLOT;
         const uint8_t* scales = gbase + C::OFF_SCALE + sl * C::SLOT_ROWS;
         const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE;
         const int end = t.len - (t.key0 + h * C::SLOT_ROWS);  // rows of this half that are keys
@@ -528,11 +553,10 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<
   const TcMma<D, C::NQT, kVarBf16> M(tmem, base);
   const int lane = threadIdx.x & 31;
   auto wait = [&](uint32_t b, uint32_t par) -> bool {
-    const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
-    return __all_sync(0xffffffffu, r);
+    return __all_sync(0xffffffffu, mbar_test_wait(b, par)) || chunk_wait(b, par, g, kStatusTimeoutMma);
   };
   uint32_t pos = 0;
-  uint32_t go0 = 0, go1 = 0;
+  uint32_t go0 = 0;
   bool ok = true;
   auto stage_acquire = [&](uint32_t& st) -> bool {
     st = pos % C::NST;
@@ -561,62 +585,61 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<
   ok = get(0, w);
   if constexpr (C::NQT == 2) {
     auto tiles_of = [](const ChunkSeg& x, int t) -> int { return t == 0 ? x.n0 : x.n1; };
-    auto first_qk = [&](const ChunkSeg& x, int k, int t, uint32_t kpos) -> bool {
-      if (!wait(bar.q_full(t), k & 1)) return false;
-      tc_fence_after();
-      if (tiles_of(x, t) > 0) M.qk(t, t, kpos, bar.s_full(t));
-      if (tiles_of(x, t) <= 1) M.commit(bar.q_empty(t));
-      return true;
-    };
-    auto tile_pv = [&](const ChunkSeg& x, int j, int t, uint32_t st, uint32_t& go) -> bool {
-      const int n = tiles_of(x, t);
-      if (j < n) {
-        if (!wait(bar.pv_go(t, 0), go & 1)) return false;
+    // S of key tile 0 of segment k for both tiles, K_0 at position kpos.
+    auto first_qk = [&](const ChunkSeg& x, int k, uint32_t kpos) -> bool {
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        if (!wait(bar.q_full(t), k & 1)) return false;
         tc_fence_after();
-        if constexpr (C::PV_SPLIT) {
-          M.pv_half(t, t, 2 * st, 0, j > 0);
-          if (!wait(bar.pv_go(t, 1), go & 1)) return false;
-          tc_fence_after();
-          M.pv_half(t, t, 2 * st, 1, true);
-        } else {
-          M.pv(t, t, 2 * st, j > 0);
-        }
-        ++go;
-        if (j == n - 1) M.commit(bar.o_done(t));
+        if (tiles_of(x, t) > 0) M.qk(t, t, kpos, bar.s_full(t));
+        if (tiles_of(x, t) <= 1) M.commit(bar.q_empty(t));
       }
       return true;
     };
-    auto tile_qk = [&](const ChunkSeg& x, int j, int t, uint32_t st, const ChunkSeg& xn, int kn) -> bool {
-      const int n = tiles_of(x, t);
-      if (j + 1 < n) {
-        M.qk(t, t, 2 * st + 1, bar.s_full(t));
-        if (j + 1 == n - 1) M.commit(bar.q_empty(t));
-      } else if (j == x.nmax - 1 && xn.valid) {
-        return first_qk(xn, kn, t, 2 * st + 1);
-      }
-      return true;
-    };
-    if (ok && w.valid) {
-      uint32_t st;
-      ok = stage_acquire(st) && first_qk(w, 0, 0, 2 * st) && first_qk(w, 0, 1, 2 * st);
-      if (ok) M.commit(bar.kv_empty(st));
-      for (int k = 0; ok; ++k) {
-        ChunkSeg wn;
-        if (!(ok = get(k + 1, wn))) break;
-        for (int j = 0; ok && j < w.nmax; ++j) {
-          if (!(ok = stage_acquire(st))) break;
+    uint32_t go = 0;  // bit t: parity of tile t's P V products
+    bool begun = false;
+#pragma unroll 1
+    for (int k = 0; ok && w.valid; ++k) {
+      ChunkSeg wn;
+      if (!(ok = get(k + 1, wn))) break;
+#pragma unroll 1
+      for (int j = begun ? 0 : -1; ok && j < w.nmax; ++j) {
+        uint32_t st;
+        if (!(ok = stage_acquire(st))) break;
+        if (j >= 0) {
           clear_tail(w, j, st);
-          if (j == w.nmax - 1)
-            ok = tile_pv(w, j, 0, st, go0) && tile_pv(w, j, 1, st, go1) && tile_qk(w, j, 0, st, wn, k + 1) &&
-                 tile_qk(w, j, 1, st, wn, k + 1);
-          else
-            ok = tile_pv(w, j, 0, st, go0) && tile_qk(w, j, 0, st, wn, k + 1) && tile_pv(w, j, 1, st, go1) &&
-                 tile_qk(w, j, 1, st, wn, k + 1);
-          if (ok) M.commit(bar.kv_empty(st));
+          // P V_t j, then S_t of key tile j + 1, tile by tile (unrolled: this warp's pace is the tensor core's).
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int n = tiles_of(w, t);
+            if (j >= n || !ok) continue;
+            const uint32_t par = (go >> t) & 1;
+            if (!(ok = wait(bar.pv_go(t, 0), par))) break;
+            tc_fence_after();
+            if constexpr (C::PV_SPLIT) {
+              M.pv_half(t, t, 2 * st, 0, j > 0);
+              if (!(ok = wait(bar.pv_go(t, 1), par))) break;
+              tc_fence_after();
+              M.pv_half(t, t, 2 * st, 1, true);
+            } else {
+              M.pv(t, t, 2 * st, j > 0);
+            }
+            go ^= 1u << t;
+            if (j == n - 1) {
+              M.commit(bar.o_done(t));
+            } else {
+              M.qk(t, t, 2 * st + 1, bar.s_full(t));
+              if (j + 1 == n - 1) M.commit(bar.q_empty(t));
+            }
+          }
         }
-        if (!ok || !wn.valid) break;
-        w = wn;
+        // The next segment's first products (in the stage of this one's last V; the very first K_0 stands alone).
+        if (ok && (j < 0 || (j == w.nmax - 1 && wn.valid)))
+          ok = first_qk(j < 0 ? w : wn, j < 0 ? k : k + 1, j < 0 ? 2 * st : 2 * st + 1);
+        if (ok) M.commit(bar.kv_empty(st));
       }
+      begun = true;
+      w = wn;
     }
   } else {
     uint32_t qk_total = 0;
@@ -651,7 +674,7 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<
       if (ok) ok = get(k + 1, w);
     }
   }
-  (void)go1;
+  (void)go0;
   M.commit(bar.drain());
   wait_bar_drain(bar.drain(), 0, g);
   __syncwarp();
@@ -681,7 +704,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
     int n, j0, lim0, min_lim, len;
     {
       ChunkSeg w;
-      ok = seg_read<D, E4M3>(w, uk, gbase, bar, g);
+      ok = seg_read<D, E4M3, true>(w, uk, gbase, bar, g);
       if (!ok || !w.valid) break;
       n = wg == 0 ? w.n0 : w.n1;
       j0 = w.j0;
@@ -809,7 +832,8 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
 
 // ------------------------------------------------------------------ correction + output
 template <int D, bool E4M3>
-__device__ __forceinline__ void chunk_correction(const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint8_t* gbase,
+__device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUtensorMap* tm_o,
+                                                 const ChunkBars<D, E4M3>& bar, uint8_t* gbase,
                                                  uint32_t tmem, int quarter, int lane, const WaitGuard& g) {
   using C = ChunkCfg<D, E4M3>;
   const int r = quarter * 32 + lane;
@@ -819,7 +843,9 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
   const float* stat_l = reinterpret_cast<const float*>(gbase + C::OFF_STAT_L);
   constexpr bool PER_PV_DONE = (C::NQT == 1);
   const int tok_r = r / p.a.group, head_r = r - tok_r * p.a.group;
-  uint32_t a_cnt0 = 0, a_cnt1 = 0, od0 = 0, od1 = 0, lf0 = 0, lf1 = 0;
+  const uint32_t out = smem_u32(gbase + C::OFF_OUT) + static_cast<uint32_t>(quarter * C::OUT_BUFS * C::OST_BUF);
+  uint32_t out_n = 0;  // chunks staged by this warp
+  uint32_t a_cnt = 0, od = 0, lf = 0;  // counts modulo 4 of tile t in bits 2t, 2t + 1
   uint32_t go_arr = 0;
   bool ok = true;
   uint64_t odd2 = 0;  // sums of 0 times every O of this thread: NaN if one was infinite or NaN
@@ -831,15 +857,18 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
       ++go_arr;
     }
   };
-  auto rescale = [&](int t, uint32_t& a_cnt, uint32_t& od) -> bool {
-    bool k = warp_wait_bar(bar.a_full(t, a_cnt & 1), (a_cnt >> 1) & 1, g, kStatusTimeoutSoftmax);
+  auto count = [](uint32_t c, int t) -> uint32_t { return (c >> (2 * t)) & 3; };
+  auto up = [](uint32_t& c, int t) { c = (c & ~(3u << (2 * t))) | ((((c >> (2 * t)) + 1) & 3u) << (2 * t)); };
+  auto rescale = [&](int t) -> bool {
+    const uint32_t ac = count(a_cnt, t);
+    bool k = chunk_wait(bar.a_full(t, ac & 1), ac >> 1, g, kStatusTimeoutSoftmax);
     if (!k) return false;
-    const float alpha = alpha_base[t * 256 + (a_cnt & 1) * 128 + r];
-    ++a_cnt;
+    const float alpha = alpha_base[t * 256 + (ac & 1) * 128 + r];
+    up(a_cnt, t);
     if (PER_PV_DONE) {
-      k = warp_wait_bar(bar.o_done(t), od & 1, g, kStatusTimeoutSoftmax);
+      k = chunk_wait(bar.o_done(t), count(od, t) & 1, g, kStatusTimeoutSoftmax);
       if (!k) return false;
-      ++od;
+      up(od, t);
     }
     if (__any_sync(0xffffffffu, alpha != 1.f)) {
       tc_fence_after();
@@ -872,13 +901,13 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
     return true;
   };
   // O of tile t: the rows of a whole unit, or this CTA's part of them.
-  auto epilogue = [&](const ChunkSeg& w, int t, uint32_t& od, uint32_t& lf) -> bool {
-    bool k = warp_wait_bar(bar.o_done(t), od & 1, g, kStatusTimeoutSoftmax);
-    k = k && warp_wait_bar(bar.ml_full(t, lf), (lf >> 1) & 1, g, kStatusTimeoutSoftmax);
+  auto epilogue = [&](const ChunkSeg& w, int t) -> bool {
+    const int su = count(lf, t) & 1;
+    bool k = chunk_wait(bar.o_done(t), count(od, t) & 1, g, kStatusTimeoutSoftmax);
+    k = k && chunk_wait(bar.ml_full(t, su), count(lf, t) >> 1, g, kStatusTimeoutSoftmax);
     if (!k) return false;
-    const int su = lf & 1;
-    ++od;
-    ++lf;
+    up(od, t);
+    up(lf, t);
     tc_fence_after();
     const float lsum = stat_m[su * 256 + t * 128 + r];
     const float lrow = stat_l[su * 256 + t * 128 + r];
@@ -893,6 +922,10 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
         mine ? static_cast<long long>(w.row0 + tok) * p.a.os[0] + static_cast<long long>(hq) * p.a.os[1] : -1ll;
     float* part = p.ws.chunk_part + (static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * part_floats(C::ROWS, D);
     float4* pblk = reinterpret_cast<float4*>(part + C::ROWS + static_cast<size_t>(t) * 128 * D) + r;
+    // All 32 rows of this warp are rows of O: a box of min(G, 32) heads.
+    const int in = quarter * 32 / p.a.group;
+    const bool boxed = p.tma_o && t * p.tpt + (quarter * 32 + 31) / p.a.group < w.ntok;
+    const int box_head = w.head * p.a.group + (quarter * 32 - in * p.a.group), box_row = w.row0 + t * p.tpt + in;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t v[32];
@@ -908,40 +941,33 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
           odd2 = f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), 0ull, odd2);
       }
       if (w.out == 0) {
-        // 16-byte block k of this row; the four rows of a quad are transposed so that a quad's threads store a row's 64
-        // bytes together (a thread storing its own row's blocks would touch 32 lines an instruction).
-        uint32_t y[4][4];
+        uint32_t y[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int k2 = 0; k2 < 4; ++k2) {
-            const float2 x = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[8 * i + 2 * k2]), __uint_as_float(v[8 * i + 2 * k2 + 1])), il2));
-            y[i][k2] = pack_bf16x2(x.x, x.y);
-          }
-#pragma unroll
-        for (int x = 1; x <= 2; x <<= 1) {
-          const bool up = (lane & x) != 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i & x) continue;
-#pragma unroll
-            for (int k2 = 0; k2 < 4; ++k2) {
-              // Blocks i and i + x: the lower thread of a pair keeps i and takes the partner's i, the upper likewise i + x.
-              const uint32_t give = up ? y[i][k2] : y[i + x][k2];
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, give, x);
-              if (up)
-                y[i][k2] = got;
-              else
-                y[i + x][k2] = got;
-            }
-          }
+        for (int i = 0; i < 16; ++i) {
+          const float2 x = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), il2));
+          y[i] = pack_bf16x2(x.x, x.y);
         }
-        // Now y[i] is block lane & 3 of the quad's row i.
+        if (boxed) {
+          // As in tc_correction: staged in shared memory, stored by TMA.
+          const uint32_t buf = out + (out_n % C::OUT_BUFS) * C::OST_BUF;
+          ++out_n;
+          if (lane == 0) bulk_wait_group_read<C::OUT_BUFS - 1>();
+          __syncwarp();
+          const uint32_t rb = buf + static_cast<uint32_t>(lane) * 64;
+          const uint32_t sw = static_cast<uint32_t>((lane >> 1) & 3);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const long long off = __shfl_sync(0xffffffffu, row_off, (lane & 28) + i);
-          if (off >= 0)
-            *reinterpret_cast<uint4*>(p.a.o + off + c * 32 + 8 * (lane & 3)) = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
+          for (int u = 0; u < 4; ++u)
+            st_shared_v4(rb + ((static_cast<uint32_t>(u) ^ sw) << 4), y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(tm_o, buf, c * 32, box_head, box_row);
+            bulk_commit_group();
+          }
+        } else if (mine) {
+          uint4* dst = reinterpret_cast<uint4*>(p.a.o + row_off + c * 32);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) dst[u] = make_uint4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
         }
       } else {
         // 16-byte block i of all 128 rows of the tile together.
@@ -972,13 +998,19 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
     // A tile whose keys all lie before this part has nothing to add.
     if (C::NQT == 2 && w.n0 == 0)
       p.ws.chunk_part[(static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * part_floats(C::ROWS, D) + r] = -INFINITY;
+    // In the MMA warp's order: the rescales of step j, then what is finished by it.
+#pragma unroll 1
     for (int j = 0; ok && j < w.nmax; ++j) {
-      if (ok && j >= 1 && j < w.n0) ok = rescale(0, a_cnt0, od0);
-      if (C::NO == 2 && ok && j >= 1 && j < w.n1) ok = rescale(1, a_cnt1, od1);
-      if (ok && j == w.n0 - 1) ok = epilogue(w, 0, od0, lf0);
-      if (C::NO == 2 && ok && j == w.n1 - 1) ok = epilogue(w, 1, od1, lf1);
+#pragma unroll 1
+      for (int t = 0; ok && t < C::NO; ++t)
+        if (j >= 1 && j < (t == 0 ? w.n0 : w.n1)) ok = rescale(t);
+#pragma unroll 1
+      for (int t = 0; ok && t < C::NO; ++t)
+        if (j == (t == 0 ? w.n0 : w.n1) - 1) ok = epilogue(w, t);
     }
   }
+  if (lane == 0) bulk_wait_group_all();  // staged chunks are written before the CTA leaves
+  __syncwarp();
   const float2 odd = f2_unpack(odd2);
   const int any = __any_sync(0xffffffffu, odd.x != 0.f || odd.y != 0.f);
   if (lane == 0) p.ws.odd[blockIdx.x * 4 + quarter] = any;
@@ -988,7 +1020,8 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const Chu
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     fa_paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkParams p) {
+                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                          const __grid_constant__ ChunkParams p) {
   using C = ChunkCfg<D, E4M3>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -1038,6 +1071,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
+    prefetch_tmap(&tm_o);
   }
   if (warp == C::MMA_WARP) {
     tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
@@ -1062,7 +1096,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     chunk_softmax<D, E4M3>(p, bar, gbase, tmem, warp >> 2, warp & 3, lane, g);
   } else if (warp < C::SOFTMAX_WARPS + 4) {
     if constexpr (C::SPLIT_REGS) regs_decrease<C::reg_corr(false)>();
-    chunk_correction<D, E4M3>(p, bar, gbase, tmem, warp & 3, lane, g);
+    chunk_correction<D, E4M3>(p, &tm_o, bar, gbase, tmem, warp & 3, lane, g);
   } else {
     if constexpr (C::SPLIT_REGS) regs_decrease<C::REG_CORR_OTHER - C::reg_corr(false)>();
     if (warp == C::LOAD_WARP) chunk_load<D, E4M3>(&tm_q, &tm_k, &tm_v, p, bar, base, gbase, share, g);
@@ -1244,10 +1278,15 @@ int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   p.tpt = 128 / a.group;
   const int most = E4M3 ? C::SLOT_ROWS : C::BK;
   p.box = (1 << a.kv.ps_log2) < most ? 1 << a.kv.ps_log2 : most;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   const long long qdims[3] = {D, a.q_heads, a.pb.rows};
   const long long qst[2] = {a.qs[1], a.qs[0]};
   if (encode_paged_map(&mq, a.q, 2, qdims, qst, C::RC, a.group, p.tpt, C::SWB, false) != 0) return -1;
+  p.tma_o = (a.group & (a.group - 1)) == 0;
+  const int oh = a.group < 32 ? a.group : 32;
+  const long long ost[2] = {a.os[1], a.os[0]};
+  mo = mq;
+  if (p.tma_o && encode_paged_map(&mo, a.o, 2, qdims, ost, 32, oh, 32 / oh, 64, false) != 0) return -1;
   const long long dims[4] = {D, 1LL << a.kv.ps_log2, a.kv.heads, a.kv.num_pages};
   const long long ks[3] = {a.kv.ks[2], a.kv.ks[1], a.kv.ks[0]}, vs[3] = {a.kv.vs[2], a.kv.vs[1], a.kv.vs[0]};
   // bf16: 64-column regions in the operand layout; e4m3: whole rows of codes, unswizzled.
@@ -1255,7 +1294,7 @@ int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   if (encode_paged_map(&mk, a.kv.k, E4M3 ? 1 : 2, dims, ks, cols, p.box, 1, swizzle, true) != 0) return -1;
   if (encode_paged_map(&mv, a.kv.v, E4M3 ? 1 : 2, dims, vs, cols, p.box, 1, swizzle, true) != 0) return -1;
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
-  return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mq, mk, mv, p);
+  return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mq, mk, mv, mo, p);
 }
 
 template <int D>
