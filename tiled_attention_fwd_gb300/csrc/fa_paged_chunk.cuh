@@ -9,7 +9,8 @@
 //    3-D TMA box {columns, G heads, tokens}.  A query block is two tiles
 //    (d = 256: one).
 //  * Work.  The key tiles of all (sequence, query block, head) units form one
-//    line that is cut into equal shares (fa_paged_plan.cuh).  The load warp walks
+//    line, with room for kUnitCost more behind each unit (what its beginning and end
+//    cost), that is cut into equal shares (fa_paged_plan.cuh).  The load warp walks
 //    this CTA's share and hands segments (a run of key tiles of one unit) to
 //    the other warps through a ring in shared memory.
 //  * Pages.  A key tile is loaded page by page (boxes of min(page, tile) rows);
@@ -31,6 +32,7 @@
 namespace fa {
 
 constexpr int kSegRing = 4;
+constexpr int kUnitCost = 2;  // key tiles that a unit costs besides its own (a step takes 3 K cycles, a border 6 to 9 K)
 
 // warp_wait_bar in less code: the kernel has to stay within the SM's instruction cache (about 128 KB; at 150 KB a
 // unit's epilogue, fetched anew each time, took 7000 cycles).
@@ -146,8 +148,10 @@ struct ChunkBlocks {
     return end <= bk ? 1 : (end + bk - 1) / bk;
   }
   __host__ __device__ __forceinline__ int tokens(int q) const { return n - q * tq < tq ? n - q * tq : tq; }
-  // Key tiles of blocks 0 .. k - 1.
-  __host__ __device__ __forceinline__ long long before(int k) const {
+  // Length on the line of blocks 0 .. k - 1 of one head.
+  __host__ __device__ __forceinline__ long long before(int k) const { return tiles_before(k) + static_cast<long long>(kUnitCost) * k; }
+  // Their key tiles.
+  __host__ __device__ __forceinline__ long long tiles_before(int k) const {
     if (k == 0) return 0;
     const long long last = tiles(k - 1, tokens(k - 1));
     if (!causal) return k * last;
@@ -161,7 +165,7 @@ struct ChunkBlocks {
 };
 
 template <int D>
-__device__ __forceinline__ ChunkBlocks chunk_blocks(const ChunkParams& p, const PagedSeq& s) {
+__host__ __device__ __forceinline__ ChunkBlocks chunk_blocks(const ChunkParams& p, const PagedSeq& s) {
   ChunkBlocks c;
   const bool mine = s.n >= 1 && s.n <= p.a.max_rows && (s.n > kFewMost || s.n * p.a.group > p.a.few_rows);
   c.n = mine ? s.n : 0;
@@ -180,17 +184,35 @@ struct ChunkWalk {
   int b, q, head, j, nt;
   PagedSeq s;
   ChunkBlocks c;
-  long long left;
-  __device__ __forceinline__ void load(const ChunkParams& p) {
+  long long pos, end;   // on the line
+  long long last_tile;  // of the latest segment's unit
+  int record_q;         // its query block
+  __host__ __device__ __forceinline__ void load(const ChunkParams& p) {
     bool bad;
     s = paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad);
     c = chunk_blocks<D>(p, s);
   }
-  __device__ __forceinline__ ChunkSeg next(const ChunkParams& p) {
+  // On to the next unit, if the share reaches it.
+  __host__ __device__ __forceinline__ void advance(const ChunkParams& p) {
+    pos += nt - j + kUnitCost;
+    j = 0;
+    if (pos >= end) return;
+    if (++head == p.a.kv.heads) {
+      head = 0;
+      ++q;
+      while (q == c.count()) {
+        ++b;
+        q = 0;
+        load(p);
+      }
+      nt = c.tiles(q, c.tokens(q));
+    }
+  }
+  __host__ __device__ __forceinline__ ChunkSeg next(const ChunkParams& p) {
     ChunkSeg g = {};
-    if (left == 0) return g;
+    if (pos >= end) return g;
     const int ntok = c.tokens(q);
-    const int n = left < nt - j ? static_cast<int>(left) : nt - j;
+    const int n = end - pos < nt - j ? static_cast<int>(end - pos) : nt - j;
     g.valid = 1;
     g.b = b;
     g.head = head;
@@ -208,21 +230,11 @@ struct ChunkWalk {
       g.n1 = n;
     }
     g.out = n == nt ? 0 : j == 0 ? 2 : 1;
-    left -= n;
+    last_tile = pos + (nt - 1 - j);
+    record_q = q;
+    pos += n;
     j += n;
-    if (left > 0 && j == nt) {
-      j = 0;
-      if (++head == p.a.kv.heads) {
-        head = 0;
-        ++q;
-        while (q == c.count()) {
-          ++b;
-          q = 0;
-          load(p);
-        }
-        nt = c.tiles(q, c.tokens(q));
-      }
-    }
+    if (j == nt) advance(p);
     return g;
   }
 };
@@ -309,11 +321,12 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
   bool recorded = false;
 
   ChunkWalk<D, E4M3> walk;
-  walk.left = share.end - share.start;
-  if (walk.left > 0) {
+  walk.pos = share.start;
+  walk.end = share.end;
+  if (walk.pos < walk.end) {
     walk.b = share.b;
     walk.load(p);
-    // The block that holds the share's first tile: 32 candidates at a time.
+    // The block that holds the share's first place: 32 candidates at a time.
     for (int q0 = 0;; q0 += 32) {
       const int q = q0 + lane;
       bool here = false;
@@ -322,7 +335,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
       if (q < walk.c.count()) {
         nt = walk.c.tiles(q, walk.c.tokens(q));
         first = p.a.kv.heads * walk.c.before(q);
-        here = first <= share.offset && share.offset < first + static_cast<long long>(p.a.kv.heads) * nt;
+        here = first <= share.offset && share.offset < first + static_cast<long long>(p.a.kv.heads) * (nt + kUnitCost);
       }
       const uint32_t who = __ballot_sync(0xffffffffu, here);
       if (who != 0) {
@@ -330,12 +343,13 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
         walk.q = q0 + from;
         walk.nt = __shfl_sync(0xffffffffu, nt, from);
         const long long in = share.offset - __shfl_sync(0xffffffffu, first, from);
-        walk.head = static_cast<int>(in / walk.nt);
-        walk.j = static_cast<int>(in - static_cast<long long>(walk.head) * walk.nt);
+        walk.head = static_cast<int>(in / (walk.nt + kUnitCost));
+        walk.j = static_cast<int>(in - static_cast<long long>(walk.head) * (walk.nt + kUnitCost));
+        if (walk.j >= walk.nt) walk.advance(p);  // behind a unit's tiles: its first tile is the next unit's
         break;
       }
-      if (q0 + 32 >= walk.c.count()) {  // cannot be: the share lies within the sequence's tiles
-        walk.left = 0;
+      if (q0 + 32 >= walk.c.count()) {  // cannot be: the share lies within the sequence's places
+        walk.pos = walk.end;
         break;
       }
     }
@@ -348,8 +362,8 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
     if (lane == 0) {
       *seg_slot<D, E4M3>(gbase, k) = w;
       if (w.out == 2) {  // this unit's first part: who holds the rest
-        const long long last = share.end - 1 + (walk.nt - w.nmax);
-        p.ws.chunk_rec[blockIdx.x] = PlanRecord{w.b, w.head, walk.q, plan_cta_of(last, share.total, share.ctas) - static_cast<int>(blockIdx.x)};
+        p.ws.chunk_rec[blockIdx.x] = PlanRecord{w.b, w.head, walk.record_q,
+                                                plan_cta_of(walk.last_tile, share.total, share.ctas) - static_cast<int>(blockIdx.x)};
       }
     }
     recorded = recorded || w.out == 2;
@@ -998,16 +1012,16 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUt
     // A tile whose keys all lie before this part has nothing to add.
     if (C::NQT == 2 && w.n0 == 0)
       p.ws.chunk_part[(static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * part_floats(C::ROWS, D) + r] = -INFINITY;
-    // In the MMA warp's order: the rescales of step j, then what is finished by it.
+    // The rescales in the MMA warp's order, then the output (tile 0's too, where it is finished a step earlier: the other
+    // tile's last product waits for its rescale).
 #pragma unroll 1
-    for (int j = 0; ok && j < w.nmax; ++j) {
-#pragma unroll 1
-      for (int t = 0; ok && t < C::NO; ++t)
-        if (j >= 1 && j < (t == 0 ? w.n0 : w.n1)) ok = rescale(t);
+    for (int j = 1; ok && j < w.nmax; ++j)
 #pragma unroll 1
       for (int t = 0; ok && t < C::NO; ++t)
-        if (j == (t == 0 ? w.n0 : w.n1) - 1) ok = epilogue(w, t);
-    }
+        if (j < (t == 0 ? w.n0 : w.n1)) ok = rescale(t);
+#pragma unroll 1
+    for (int t = 0; ok && t < C::NO; ++t)
+      if ((t == 0 ? w.n0 : w.n1) > 0) ok = epilogue(w, t);
   }
   if (lane == 0) bulk_wait_group_all();  // staged chunks are written before the CTA leaves
   __syncwarp();
@@ -1084,6 +1098,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
         const ChunkBlocks c = chunk_blocks<D>(p, paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad));
         return c.n == 0 ? 0 : p.a.kv.heads * c.before(c.count());
       },
+      1 + kUnitCost,
       *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
   tc_fence_before();
   __syncthreads();

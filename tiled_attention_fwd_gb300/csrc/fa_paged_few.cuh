@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
         bool bad;
         return static_cast<long long>(a.kv.heads) * few_tiles<C::KT>(a, paged_seq(a.pb, a.kv.ps_log2, b, bad));
       },
+      1,
       *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
 
   // ---- the warp's loads

@@ -32,14 +32,14 @@ struct PlanScratch {
 };
 
 // CTA that holds tile x of W dealt to n CTAs.
-__device__ __forceinline__ int plan_cta_of(long long x, long long total, int n) {
+__host__ __device__ __forceinline__ int plan_cta_of(long long x, long long total, int n) {
   return static_cast<int>(((x + 1) * n - 1) / total);
 }
 
-// All THREADS threads of the CTA take part.  tiles(b): sequence b's tiles (the
-// same value whenever it is asked).
+// All THREADS threads of the CTA take part.  tiles(b): the length of sequence b's
+// tiles on the line (the same value whenever it is asked); a CTA has `least` of it at least.
 template <int THREADS, class F>
-__device__ __forceinline__ PlanShare plan_share(int B, int ctas, int cta, const F& tiles, PlanScratch& s) {
+__device__ __forceinline__ PlanShare plan_share(int B, int ctas, int cta, const F& tiles, int least, PlanScratch& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Sum of one chunk of THREADS sequences up to and including this thread's, and of the whole chunk.
   auto scan = [&](long long w, long long& sum) -> long long {
@@ -71,7 +71,7 @@ __device__ __forceinline__ PlanShare plan_share(int B, int ctas, int cta, const 
   }
   PlanShare p;
   p.total = total;
-  p.ctas = total < ctas ? static_cast<int>(total) : ctas;
+  p.ctas = total / least < ctas ? static_cast<int>(total / least) : ctas;
   p.start = p.end = 0;
   p.b = 0;
   p.offset = 0;
