@@ -26,6 +26,8 @@
 //    adds them up: O = sum 2^(L_i - L) O_i, L = log2 sum 2^L_i.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_fwd_tc.cuh"
 #include "fa_paged_plan.cuh"
 
@@ -518,35 +520,38 @@ __device__ __forceinline__ void chunk_convert(const ChunkParams& p, const ChunkB
           const uint32_t sw = C::SWB == 128 ? r & 7 : (r >> 1) & 3;
           to[k] = dst + (unit16 / UR) * C::K_REGION + (h * C::SLOT_ROWS + r) * C::SWB + (((unit16 % UR) ^ sw) << 4);
         }
-        const bool fast = end >= C::SLOT_ROWS && !__any_sync(0xffffffffu, big != 0);
+        auto convert = [&](auto checked) {
 #pragma unroll 1
-        for (int pass = 0; pass < PASSES; pass += 4) {
-          uint2 x[4];
-          uint32_t byte[4];
+          for (int pass = 0; pass < PASSES; pass += 4) {
+            uint2 x[4];
+            uint32_t byte[4], w[4][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = (pass + k) * RPP + row0;
-            x[k] = *reinterpret_cast<const uint2*>(codes + r * D + unit16 * 8);
-            byte[k] = scales[r];
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-            uint32_t f = byte[k] * 0x00800080u + 120u * 0x00800080u;  // 2^(120 + e), twice
-            if (!fast) {
-              f = byte[k] == 255u ? 0x7fc07fc0u : byte[k] > 134u ? 0x7f007f00u : f;  // NaN, or 2^127 at most
+            for (int k = 0; k < 4; ++k) {
+              const int r = (pass + k) * RPP + row0;
+              x[k] = *reinterpret_cast<const uint2*>(codes + r * D + unit16 * 8);
+              byte[k] = scales[r];
             }
-            e4m3x4_to_bf16x4(x[k].x, f, w[0], w[1]);
-            e4m3x4_to_bf16x4(x[k].y, f, w[2], w[3]);
-            if (!fast) {
-              const uint32_t f2 = byte[k] > 134u && byte[k] != 255u ? (byte[k] - 7u) * 0x00800080u : 0x3f803f80u;  // 2^(e - 7)
-              const bool past = (pass + k) * RPP + row0 >= end;
 #pragma unroll
-              for (int i2 = 0; i2 < 4; ++i2) w[i2] = past ? 0u : mul_bf16x2(w[i2], f2);
+            for (int k = 0; k < 4; ++k) {
+              uint32_t f = byte[k] * 0x00800080u + 120u * 0x00800080u;  // 2^(120 + e), twice
+              if constexpr (decltype(checked)::value) f = byte[k] == 255u ? 0x7fc07fc0u : byte[k] > 134u ? 0x7f007f00u : f;  // NaN, or 2^127 at most
+              e4m3x4_to_bf16x4(x[k].x, f, w[k][0], w[k][1]);
+              e4m3x4_to_bf16x4(x[k].y, f, w[k][2], w[k][3]);
+              if constexpr (decltype(checked)::value) {
+                const uint32_t f2 = byte[k] > 134u && byte[k] != 255u ? (byte[k] - 7u) * 0x00800080u : 0x3f803f80u;  // 2^(e - 7)
+                const bool past = (pass + k) * RPP + row0 >= end;
+#pragma unroll
+                for (int i2 = 0; i2 < 4; ++i2) w[k][i2] = past ? 0u : mul_bf16x2(w[k][i2], f2);
+              }
             }
-            st_shared_v4(to[k] + pass * RPP * C::SWB, w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st_shared_v4(to[k] + pass * RPP * C::SWB, w[k][0], w[k][1], w[k][2], w[k][3]);
           }
-        }
+        };
+        if (end >= C::SLOT_ROWS && !__any_sync(0xffffffffu, big != 0))
+          convert(std::false_type{});
+        else
+          convert(std::true_type{});
         warp_arrive(bar.slot_empty(sl));
       }
     }
