@@ -17,10 +17,10 @@
 //    only boxes that hold keys of the sequence are.  V rows behind the last token
 //    are set to zero before the tensor core reads them: such slots hold anything,
 //    and 0 times NaN is NaN.
-//  * e4m3 pages.  The load warp brings codes and scales into a small ring, two
-//    warps turn them into the bf16 tiles that the tensor core reads (exact: a
-//    code has 4 significant bits and a scale is a power of two), so the rest of
-//    the pipeline is the same.
+//  * e4m3 pages.  The load warp brings codes and scales into a small ring, the
+//    correction warps and two more turn them into the bf16 tiles that the tensor
+//    core reads (exact: a code has 4 significant bits and a scale is a power of
+//    two), so the rest of the pipeline is the same.
 //  * Output.  A unit held whole is written as it is finished; of others O and
 //    the log-sum (base 2) go to the workspace in fp32 and the joining kernel
 //    adds them up: O = sum 2^(L_i - L) O_i, L = log2 sum 2^L_i.
@@ -53,6 +53,19 @@ __device__ __forceinline__ bool chunk_wait(uint32_t bar, uint32_t parity, const 
   }
 }
 
+// mbar_try_wait that comes back after about `ns` at the latest.
+__device__ __forceinline__ uint32_t mbar_try_wait_ns(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n\t"
+      "selp.b32 %0, 1, 0, P1;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok;
+}
+
 // A run of key tiles of one unit.
 struct alignas(16) ChunkSeg {
   int valid;
@@ -73,20 +86,23 @@ static_assert(sizeof(ChunkSeg) == 48, "segment size");
 template <int D, bool E4M3>
 struct ChunkCfg : TcCfg<D> {
   using T = TcCfg<D>;
-  // Staged output: buffers of 32 rows x 32 columns per correction warp; e4m3 keeps one and has a ring of half key
+  // Staged output: buffers of 32 rows x 32 columns per correction warp; e4m3 keeps one and has a ring of quarter key
   // tiles (codes) in the place of the others.
   static constexpr int OUT_BUFS = E4M3 ? 1 : T::OSTB;
   static constexpr int OFF_OUT = T::OFF_OST;
   static constexpr int OFF_SLOT = T::OFF_OST + 4 * OUT_BUFS * T::OST_BUF;
-  static constexpr int SLOT_ROWS = T::BK / 2;
+  static constexpr int SLOT_ROWS = T::BK / 4;
   static constexpr int SLOT = SLOT_ROWS * D;
-  static constexpr int NSLOT = !E4M3 ? 0 : (T::OST - 4 * T::OST_BUF) / SLOT > 4 ? 4 : (T::OST - 4 * T::OST_BUF) / SLOT;
+  static constexpr int NSLOT = !E4M3 ? 0 : (T::OST - 4 * T::OST_BUF) / SLOT > 8 ? 8 : (T::OST - 4 * T::OST_BUF) / SLOT;
+  // Two tiles: the softmax warps rescale O themselves where a row's maximum moved far (rare, see LAZY_MAX), so the
+  // correction warps are free for the output and, with e4m3 pages, for most of the conversion.
+  static constexpr bool SELF_RESCALE = T::NQT == 2;
   static constexpr int OFF_SEG = T::OFF_MISC + 6672;
   static constexpr int OFF_SCALE = OFF_SEG + kSegRing * static_cast<int>(sizeof(ChunkSeg));  // [NSLOT][SLOT_ROWS]
   static constexpr int OFF_PLAN = T::OFF_ALPHA;  // before the roles start
-  static constexpr int CONV_WARPS = E4M3 ? 2 : 0;
-  static constexpr int CONV_WARP0 = T::LOAD_WARP + 1;
-  static constexpr int SEG_READERS = T::SOFTMAX_WARPS + 4 + 1 + CONV_WARPS;
+  static constexpr int CONV_WARPS = !E4M3 ? 0 : SELF_RESCALE ? 6 : 2;  // warps that convert e4m3 tiles
+  static constexpr int CONV_WARP0 = T::LOAD_WARP + 1;                  // the last two; the others are the correction warps
+  static constexpr int SEG_READERS = T::SOFTMAX_WARPS + 4 + 1 + (E4M3 ? 2 : 0);
   static constexpr int ROWS = T::NQT * 128;
   static_assert(T::OFF_ABORT + 4 <= OFF_SEG && OFF_SEG % 16 == 0, "misc area");
   static_assert(OFF_SCALE + NSLOT * SLOT_ROWS <= T::OFF_MISC + T::MISC, "misc area");
@@ -99,10 +115,12 @@ struct ChunkBars : TcBars<D, TcCfg<D>::NQT, kVarBf16> {
   __device__ __forceinline__ uint32_t seg_full(int i) const { return this->b0 + 256 + 8u * i; }
   __device__ __forceinline__ uint32_t seg_empty(int i) const { return this->b0 + 288 + 8u * i; }
   __device__ __forceinline__ uint32_t slot_full(int i) const { return this->b0 + 320 + 8u * i; }
-  __device__ __forceinline__ uint32_t slot_empty(int i) const { return this->b0 + 352 + 8u * i; }
+  __device__ __forceinline__ uint32_t slot_empty(int i) const { return this->b0 + 384 + 8u * i; }
   // m and l of this accumulator's k-th unit: the softmax may finish the next unit (one key tile) while the
   // correction warpgroup has not come to this one yet, so two barriers take turns.
-  __device__ __forceinline__ uint32_t ml_full(int t, int k) const { return this->b0 + 384 + 8u * (2 * t + (k & 1)); }
+  __device__ __forceinline__ uint32_t ml_full(int t, int k) const { return this->b0 + 448 + 8u * (2 * t + (k & 1)); }
+  // Two tiles: O of tile t has been read out (there are no alphas to publish, so the barrier is free).
+  __device__ __forceinline__ uint32_t o_free(int t) const { return this->a_full(t, 0); }
   static_assert(Base::COUNT * 8 <= 256, "barrier area");
 };
 
@@ -424,28 +442,31 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
       last_par = (last_par & ~(1u << st)) | (par << st);
       ++pos;
     } else {
+#pragma unroll 1
       for (int i = 0; i < 2; ++i) {
         const ChunkTile& t = i == 0 ? t0 : t1;
         if (t.kind == 0) continue;
-        for (int h = 0; h < 2; ++h) {
+        // Lane l looks after box l of the tile.
+        const int n = boxes(t, t.key0, C::BK), key = t.key0 + lane * p.box;
+        const int page = lane < n ? page_of(t, key) : 0;
+        // (For a page that is not there any scales do.)
+        const long long pg = page == p.a.kv.num_pages ? 0 : page;
+        const uint8_t* sc = (t.kind == 1 ? p.a.kv.k_scale : p.a.kv.v_scale) +
+                            (((pg * p.a.kv.heads + t.head) << p.a.kv.ps_log2) + (key & slot_mask));
+        const int in_slot = lane * p.box % C::SLOT_ROWS;
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
           const int st = pos % C::NSLOT;
           const uint32_t par = (pos / C::NSLOT) & 1;
           const uint32_t full = bar.slot_full(st);
-          const int key0 = t.key0 + h * C::SLOT_ROWS;
-          const int n = boxes(t, key0, C::SLOT_ROWS);
-          const int page = lane < n ? page_of(t, key0 + lane * p.box) : 0;
+          const int here = boxes(t, t.key0 + h * C::SLOT_ROWS, C::SLOT_ROWS);
           if (!chunk_wait(bar.slot_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(full, n * p.box * (D + 1));
+          if (lane == 0) mbar_arrive_expect_tx(full, here * p.box * (D + 1));
           __syncwarp();
-          if (lane < n) {
-            const int key = key0 + lane * p.box;
-            const uint32_t sc = base + C::OFF_SCALE + st * C::SLOT_ROWS + lane * p.box;
-            tma_load_4d(base + C::OFF_SLOT + st * C::SLOT + lane * p.box * D, t.kind == 1 ? tm_k : tm_v, full, 0,
-                        key & slot_mask, t.head, page, pol_kv);
-            // (For a page that is not there any scales do.)
-            const long long pg = page == p.a.kv.num_pages ? 0 : page;
-            bulk_load(sc, (t.kind == 1 ? p.a.kv.k_scale : p.a.kv.v_scale) +
-                              (((pg * p.a.kv.heads + t.head) << p.a.kv.ps_log2) + (key & slot_mask)), p.box, full);
+          if (lane < n && lane * p.box / C::SLOT_ROWS == h) {
+            tma_load_4d(base + C::OFF_SLOT + st * C::SLOT + in_slot * D, t.kind == 1 ? tm_k : tm_v, full, 0, key & slot_mask,
+                        t.head, page, pol_kv);
+            bulk_load(base + C::OFF_SCALE + st * C::SLOT_ROWS + in_slot, sc, p.box, full);
           }
           issued |= 1u << st;
           last_par = (last_par & ~(1u << st)) | (par << st);
@@ -482,57 +503,62 @@ __device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t x, uint32_t f, uint32_
   hi = mul_bf16x2(__byte_perm(l, h, 0x7362), f);
 }
 
-// Two warps: every half tile that the load warp brought, into the stages.
-template <int D, bool E4M3>
-__device__ __forceinline__ void chunk_convert(const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint32_t base,
-                                              uint8_t* gbase, int cw, const WaitGuard& g) {
+// Quarter tiles that the load warp brought, into the stages.  Two tiles: of three quarters the four correction warps
+// take two and the last two warps one; one tile: the last two take all.  wait(bar, parity) waits, get fetches segments.
+template <int D, bool E4M3, int WARPS, class Get, class Wait>
+__device__ __forceinline__ bool chunk_convert(const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint32_t base,
+                                              uint8_t* gbase, int cw, const Get& get, const Wait& wait) {
   using C = ChunkCfg<D, E4M3>;
   const int lane = threadIdx.x & 31;
-  uint32_t pos = 0, half = 0;
-  auto get = [&](int k, ChunkSeg& w) -> bool { return seg_read<D, E4M3>(w, k, gbase, bar, g); };
+  uint32_t pos = 0, quarter = 0;
   auto unit = [&](const ChunkSeg&, int) -> bool { return true; };
   auto stage = [&](const ChunkTile& t0, const ChunkTile& t1) -> bool {
     const int st = pos % C::NST;
-    if (!chunk_wait(bar.kv_empty(st), ((pos / C::NST) & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
+    if (!wait(bar.kv_empty(st), ((pos / C::NST) & 1) ^ 1)) return false;
     ++pos;
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       const ChunkTile& t = i == 0 ? t0 : t1;
       if (t.kind == 0) continue;
-      for (int h = 0; h < 2; ++h, ++half) {
-        const int sl = half % C::NSLOT;
-        if (!chunk_wait(bar.slot_full(sl), (half / C::NSLOT) & 1, g, kStatusTimeoutLoad)) return false;
+#pragma unroll 1
+      for (int h = 0; h < 4; ++h, ++quarter) {
+        if (C::SELF_RESCALE && (quarter % 3 == 2) != (WARPS == 2)) continue;
+        const int sl = quarter % C::NSLOT;
+        if (!wait(bar.slot_full(sl), (quarter / C::NSLOT) & 1)) return false;
         const uint8_t* codes = gbase + C::OFF_SLOT + sl * C::SLOT;
         const uint8_t* scales = gbase + C::OFF_SCALE + sl * C::SLOT_ROWS;
         const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE;
-        const int end = t.len - (t.key0 + h * C::SLOT_ROWS);  // rows of this half that are keys
-        constexpr int UPR = D / 8;        // 16-byte units of a bf16 row
-        constexpr int RPP = 64 / UPR;     // rows of a pass of the 64 threads
+        const int end = t.len - (t.key0 + h * C::SLOT_ROWS);  // rows of this quarter that are keys
+        constexpr int UPR = D / 8;                 // 16-byte units of a bf16 row
+        constexpr int RPP = 32 * WARPS / UPR;      // rows of a pass of the group's threads
         constexpr int PASSES = C::SLOT_ROWS / RPP;
+        constexpr int BATCH = PASSES < 4 ? PASSES : 4;
         constexpr int UR = C::SWB / 16;
-        static_assert(PASSES % 4 == 0 && 4 * RPP % 8 == 0, "four passes are whole swizzle periods");
+        static_assert(PASSES >= 1 && PASSES % BATCH == 0 && (PASSES == BATCH || BATCH * RPP % 8 == 0),
+                      "a batch of passes is a whole number of swizzle periods");
         const int row0 = (cw * 32 + lane) / UPR, unit16 = lane % UPR;
         const uint32_t* sw4 = reinterpret_cast<const uint32_t*>(scales);
         const uint32_t big = lane < C::SLOT_ROWS / 4 ? __vcmpgtu4(sw4[lane], 0x86868686u) : 0u;  // a byte > 134
-        uint32_t to[4];
+        uint32_t to[BATCH];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < BATCH; ++k) {
           const int r = k * RPP + row0;
           const uint32_t sw = C::SWB == 128 ? r & 7 : (r >> 1) & 3;
           to[k] = dst + (unit16 / UR) * C::K_REGION + (h * C::SLOT_ROWS + r) * C::SWB + (((unit16 % UR) ^ sw) << 4);
         }
         auto convert = [&](auto checked) {
 #pragma unroll 1
-          for (int pass = 0; pass < PASSES; pass += 4) {
-            uint2 x[4];
-            uint32_t byte[4], w[4][4];
+          for (int pass = 0; pass < PASSES; pass += BATCH) {
+            uint2 x[BATCH];
+            uint32_t byte[BATCH], w[BATCH][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < BATCH; ++k) {
               const int r = (pass + k) * RPP + row0;
               x[k] = *reinterpret_cast<const uint2*>(codes + r * D + unit16 * 8);
               byte[k] = scales[r];
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < BATCH; ++k) {
               uint32_t f = byte[k] * 0x00800080u + 120u * 0x00800080u;  // 2^(120 + e), twice
               if constexpr (decltype(checked)::value) f = byte[k] == 255u ? 0x7fc07fc0u : byte[k] > 134u ? 0x7f007f00u : f;  // NaN, or 2^127 at most
               e4m3x4_to_bf16x4(x[k].x, f, w[k][0], w[k][1]);
@@ -545,7 +571,7 @@ __device__ __forceinline__ void chunk_convert(const ChunkParams& p, const ChunkB
               }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) st_shared_v4(to[k] + pass * RPP * C::SWB, w[k][0], w[k][1], w[k][2], w[k][3]);
+            for (int k = 0; k < BATCH; ++k) st_shared_v4(to[k] + pass * RPP * C::SWB, w[k][0], w[k][1], w[k][2], w[k][3]);
           }
         };
         if (end >= C::SLOT_ROWS && !__any_sync(0xffffffffu, big != 0))
@@ -553,14 +579,14 @@ __device__ __forceinline__ void chunk_convert(const ChunkParams& p, const ChunkB
         else
           convert(std::true_type{});
         warp_arrive(bar.slot_empty(sl));
+        if constexpr (WARPS == 2) warp_arrive(bar.slot_empty(sl));  // (four arrivals free a slot)
       }
     }
     fence_proxy_async_smem();  // before the tensor core reads them
     warp_arrive(bar.kv_full(st));
     return true;
   };
-  chunk_stream<D>(get, unit, stage);
-  __syncwarp();
+  return chunk_stream<D>(get, unit, stage);
 }
 
 // ------------------------------------------------------------------ MMA issuer
@@ -615,7 +641,8 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<
       }
       return true;
     };
-    uint32_t go = 0;  // bit t: parity of tile t's P V products
+    uint32_t go = 0;    // bit t: parity of tile t's P V products
+    uint32_t free_par = 0;  // bit t: parity of its units' first ones
     bool begun = false;
 #pragma unroll 1
     for (int k = 0; ok && w.valid; ++k) {
@@ -633,6 +660,10 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<
             const int n = tiles_of(w, t);
             if (j >= n || !ok) continue;
             const uint32_t par = (go >> t) & 1;
+            if (j == 0) {  // O has been read out (or is free from the start)
+              if (!(ok = wait(bar.o_free(t), (free_par >> t) & 1))) break;
+              free_par ^= 1u << t;
+            }
             if (!(ok = wait(bar.pv_go(t, 0), par))) break;
             tc_fence_after();
             if constexpr (C::PV_SPLIT) {
@@ -745,59 +776,82 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
       ++s_waits;
       tc_fence_after();
       const uint32_t ts = tmem + lane_off + C::TM_S + buf * C::TM_SB;
-      float s[C::BK];
-      float cmax[C::BK / 32];
-      {
-        uint32_t raw_s[C::BK / 32][32];
-#pragma unroll
-        for (int c = 0; c < C::BK / 32; ++c) tmem_ld32_max(ts + c * 32, raw_s[c], cmax[c]);
-#pragma unroll
-        for (int c = 0; c < C::BK / 32; ++c) tmem_wait_ld(raw_s[c], cmax[c]);
-#pragma unroll
-        for (int c = 0; c < C::BK / 32; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(raw_s[c][i]);
-      }
       const int key0 = (j0 + j) * C::BK;
-      float rmax;
-      if (key0 + C::BK - 1 > min_lim) {
-        const int lim = lim0 - key0;
-        const int lo = __reduce_min_sync(0xffffffffu, lim);
+      float s[C::BK];
+      float rmax, m_new, alpha;
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        float cmax[C::BK / 32];
+        {
+          uint32_t raw_s[C::BK / 32][32];
 #pragma unroll
-        for (int cb = 0; cb < C::BK / 32; ++cb) {
-          if (32 * cb + 31 > lo) {
+          for (int c = 0; c < C::BK / 32; ++c) tmem_ld32_max(ts + c * 32, raw_s[c], cmax[c]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * cb + i > lim) s[32 * cb + i] = -INFINITY;
+          for (int c = 0; c < C::BK / 32; ++c) tmem_wait_ld(raw_s[c], cmax[c]);
+#pragma unroll
+          for (int c = 0; c < C::BK / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(raw_s[c][i]);
+        }
+        if (key0 + C::BK - 1 > min_lim) {
+          const int lim = lim0 - key0;
+          const int lo = __reduce_min_sync(0xffffffffu, lim);
+#pragma unroll
+          for (int cb = 0; cb < C::BK / 32; ++cb) {
+            if (32 * cb + 31 > lo) {
+              // Bit i: column 32 cb + i is behind the limit.
+              const int v = lim - 32 * cb;
+              const uint32_t hide = v < 0 ? 0xffffffffu : v >= 31 ? 0u : 0xfffffffeu << v;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if ((hide >> i) & 1) s[32 * cb + i] = -INFINITY;
+            }
           }
+          constexpr int KC = C::BK / 8;
+          float mx[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float v = fmax3(s[i], s[i + 8], s[i + 16]);
+#pragma unroll
+            for (int k = 3; k + 1 < KC; k += 2) v = fmax3(v, s[i + 8 * k], s[i + 8 * (k + 1)]);
+            if ((KC - 3) % 2 == 1) v = fmaxf(v, s[i + 8 * (KC - 1)]);
+            mx[i] = v;
+          }
+          rmax = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+        } else {
+          rmax = cmax[0];
+#pragma unroll
+          for (int c = 1; c < C::BK / 32; ++c) rmax = fmaxf(rmax, cmax[c]);
         }
-        constexpr int KC = C::BK / 8;
-        float mx[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float v = fmax3(s[i], s[i + 8], s[i + 16]);
-#pragma unroll
-          for (int k = 3; k + 1 < KC; k += 2) v = fmax3(v, s[i + 8 * k], s[i + 8 * (k + 1)]);
-          if ((KC - 3) % 2 == 1) v = fmaxf(v, s[i + 8 * (KC - 1)]);
-          mx[i] = v;
+        if (again) break;
+        if constexpr (C::LAZY_MAX) {
+          const float rm = rmax * sl2;
+          m_new = (rm > m + C::MAX_SLACK) ? rm : m;
+        } else {
+          m_new = fmaxf(m, rmax * sl2);
         }
-        rmax = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
-      } else {
-        rmax = cmax[0];
+        alpha = (m_new == m) ? 1.f : ex2(m - m_new);
+        if (!C::SELF_RESCALE || j == 0 || __all_sync(0xffffffffu, alpha == 1.f)) break;
+        // Rescale O (P V j - 1 is done: S j was issued behind it), then fetch S again: the registers hold one of them.
+        const uint32_t to = tmem + lane_off + C::TM_O + ot * D;
+        const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(to + c * 32, v);
+          tmem_wait_ld(v);
 #pragma unroll
-        for (int c = 1; c < C::BK / 32; ++c) rmax = fmaxf(rmax, cmax[c]);
-      }
-      float m_new, alpha;
-      if constexpr (C::LAZY_MAX) {
-        const float rm = rmax * sl2;
-        m_new = (rm > m + C::MAX_SLACK) ? rm : m;
-        alpha = (m_new == m) ? 1.f : ex2(m - m_new);
-      } else {
-        m_new = fmaxf(m, rmax * sl2);
-        alpha = (m_new == m) ? 1.f : ex2(m - m_new);
+          for (int i = 0; i < 32; i += 2) {
+            const float2 y = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), a2));
+            v[i] = __float_as_uint(y.x);
+            v[i + 1] = __float_as_uint(y.y);
+          }
+          tmem_st32(to + c * 32, v);
+        }
+        tmem_wait_st();
       }
       float nb = (m_new == -INFINITY) ? 0.f : -m_new;
-      if (j > 0) {
+      if (!C::SELF_RESCALE && j > 0) {
         alpha_s[(a_pub & 1) * 128 + r] = alpha;
         // As in tc_softmax: the exponentials are scheduled after this arrival.
         nb = fmaf(0.f, __uint_as_float(warp_arrive_token(bar.a_full(ot, a_pub & 1))), nb);
@@ -852,7 +906,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
 // ------------------------------------------------------------------ correction + output
 template <int D, bool E4M3>
 __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUtensorMap* tm_o,
-                                                 const ChunkBars<D, E4M3>& bar, uint8_t* gbase,
+                                                 const ChunkBars<D, E4M3>& bar, uint32_t base, uint8_t* gbase,
                                                  uint32_t tmem, int quarter, int lane, const WaitGuard& g) {
   using C = ChunkCfg<D, E4M3>;
   const int r = quarter * 32 + lane;
@@ -869,8 +923,8 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUt
   bool ok = true;
   uint64_t odd2 = 0;  // sums of 0 times every O of this thread: NaN if one was infinite or NaN
   auto release_o = [&](int t) {
-    if (C::NQT == 2) {
-      warp_arrive(bar.pv_go(t, 0));
+    if (C::SELF_RESCALE) {
+      warp_arrive(bar.o_free(t));
     } else {
       warp_arrive(bar.pv_go(0, go_arr & 1));
       ++go_arr;
@@ -1010,23 +1064,73 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUt
 
   release_o(0);
   if (C::NO == 2) release_o(1);
-  for (int uk = 0; ok; ++uk) {
-    ChunkSeg w;
-    ok = seg_read<D, E4M3>(w, uk, gbase, bar, g);
-    if (!ok || !w.valid) break;
-    // A tile whose keys all lie before this part has nothing to add.
+  // A tile whose keys all lie before this part has nothing to add.
+  auto nothing = [&](const ChunkSeg& w) {
     if (C::NQT == 2 && w.n0 == 0)
       p.ws.chunk_part[(static_cast<size_t>(blockIdx.x) * 2 + (w.out - 1)) * part_floats(C::ROWS, D) + r] = -INFINITY;
-    // The rescales in the MMA warp's order, then the output (tile 0's too, where it is finished a step earlier: the other
-    // tile's last product waits for its rescale).
+  };
+  if constexpr (!(E4M3 && C::SELF_RESCALE)) {
+    for (int uk = 0; ok; ++uk) {
+      ChunkSeg w;
+      ok = seg_read<D, E4M3>(w, uk, gbase, bar, g);
+      if (!ok || !w.valid) break;
+      nothing(w);
+      if constexpr (!C::SELF_RESCALE) {
 #pragma unroll 1
-    for (int j = 1; ok && j < w.nmax; ++j)
+        for (int j = 1; ok && j < w.nmax; ++j) ok = rescale(0);
+      }
 #pragma unroll 1
       for (int t = 0; ok && t < C::NO; ++t)
-        if (j < (t == 0 ? w.n0 : w.n1)) ok = rescale(t);
-#pragma unroll 1
-    for (int t = 0; ok && t < C::NO; ++t)
-      if ((t == 0 ? w.n0 : w.n1) > 0) ok = epilogue(w, t);
+        if ((t == 0 ? w.n0 : w.n1) > 0) ok = epilogue(w, t);
+    }
+  } else {
+    // Converting, and in between the outputs as they are finished.  A segment is held in the ring until its output is
+    // out, so the waits below have to go on with the outputs (the load warp may wait for the ring, the MMA warp for O).
+    int seen = 0, out_k = 0, out_t = 0;  // segments fetched; the next output
+    auto output = [&](bool block) -> bool {
+      if (out_k >= seen) return true;
+      const ChunkSeg& w = *seg_slot<D, E4M3>(gbase, out_k);
+      if (out_t < 2) {
+        if ((out_t == 0 ? w.n0 : w.n1) == 0) {
+          if (out_t == 0) nothing(w);
+          ++out_t;
+        } else if (block || __all_sync(0xffffffffu, mbar_test_wait(bar.o_done(out_t), count(od, out_t) & 1))) {
+          const ChunkSeg copy = w;
+          if (!epilogue(copy, out_t)) return false;
+          ++out_t;
+        }
+      }
+      if (out_t == 2) {
+        warp_arrive(bar.seg_empty(out_k % kSegRing));
+        ++out_k;
+        out_t = 0;
+      }
+      return true;
+    };
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+      uint64_t t0 = 0;
+      while (true) {
+        if (__all_sync(0xffffffffu, mbar_test_wait(b, parity))) return true;
+        if (!output(false)) return false;
+        if (__all_sync(0xffffffffu, mbar_try_wait_ns(b, parity, 300))) return true;
+        if (__any_sync(0xffffffffu, *g.abort)) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, now - t0 > g.limit_ns)) {
+          *g.abort = 1;
+          if (lane == 0) atomicOr(g.status, kStatusTimeoutLoad);
+          return false;
+        }
+      }
+    };
+    auto get = [&](int k, ChunkSeg& w) -> bool {
+      if (!wait(bar.seg_full(k % kSegRing), (k / kSegRing) & 1)) return false;
+      w = *seg_slot<D, E4M3>(gbase, k);
+      if (w.valid) seen = k + 1;
+      return true;
+    };
+    ok = chunk_convert<D, E4M3, 4>(p, bar, base, gbase, quarter, get, wait);
+    while (ok && out_k < seen) ok = output(true);
   }
   if (lane == 0) bulk_wait_group_all();  // staged chunks are written before the CTA leaves
   __syncwarp();
@@ -1066,8 +1170,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar.s_full(b), 1);
-      mbar_init(bar.pv_go(b, 0), 8);  // 4 softmax warps + 4 correction warps
-      mbar_init(bar.pv_go(b, 1), C::PV_SPLIT ? 4 : 8);
+      mbar_init(bar.pv_go(b, 0), C::SELF_RESCALE ? 4 : 8);  // 4 softmax warps (+ 4 correction warps)
+      mbar_init(bar.pv_go(b, 1), C::SELF_RESCALE ? 4 : 8);
       mbar_init(bar.a_full(b, 0), 4);
       mbar_init(bar.a_full(b, 1), 4);
       mbar_init(bar.o_done(b), 1);
@@ -1081,7 +1185,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     }
     for (int i = 0; i < C::NSLOT; ++i) {
       mbar_init(bar.slot_full(i), 1);
-      mbar_init(bar.slot_empty(i), 2);
+      mbar_init(bar.slot_empty(i), 4);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -1116,13 +1220,17 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     chunk_softmax<D, E4M3>(p, bar, gbase, tmem, warp >> 2, warp & 3, lane, g);
   } else if (warp < C::SOFTMAX_WARPS + 4) {
     if constexpr (C::SPLIT_REGS) regs_decrease<C::reg_corr(false)>();
-    chunk_correction<D, E4M3>(p, &tm_o, bar, gbase, tmem, warp & 3, lane, g);
+    chunk_correction<D, E4M3>(p, &tm_o, bar, base, gbase, tmem, warp & 3, lane, g);
   } else {
     if constexpr (C::SPLIT_REGS) regs_decrease<C::REG_CORR_OTHER - C::reg_corr(false)>();
     if (warp == C::LOAD_WARP) chunk_load<D, E4M3>(&tm_q, &tm_k, &tm_v, p, bar, base, gbase, share, g);
     if (warp == C::MMA_WARP) chunk_mma<D, E4M3>(p, bar, base, gbase, tmem, g);
     if constexpr (E4M3)
-      if (warp >= C::CONV_WARP0) chunk_convert<D, E4M3>(p, bar, base, gbase, warp - C::CONV_WARP0, g);
+      if (warp >= C::CONV_WARP0)
+        chunk_convert<D, E4M3, 2>(
+            p, bar, base, gbase, warp - C::CONV_WARP0,
+            [&](int k, ChunkSeg& w) -> bool { return seg_read<D, E4M3>(w, k, gbase, bar, g); },
+            [&](uint32_t b, uint32_t parity) -> bool { return chunk_wait(b, parity, g, kStatusTimeoutLoad); });
   }
   __syncwarp();
   tc_fence_before();
