@@ -131,7 +131,8 @@ struct ChunkParams {
   unsigned long long limit_ns;
   float scale_log2;
   int tpt;      // tokens of a 128-row tile: 128 / group
-  int box;      // rows of a K/V box
+  int box;      // rows of a K/V box, a power of two
+  int box_log2;
   bool tma_o;   // a warp's 32 rows are a box of O (the group is a power of two)
 };
 
@@ -406,7 +407,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
   // Boxes of up to `rows` keys from key0 on, one lane each: those that begin before the sequence's end.
   auto boxes = [&](const ChunkTile& t, int key0, int rows) -> int {
     const int n = min(rows, t.len - key0);
-    return n <= 0 ? 0 : (n + p.box - 1) / p.box;
+    return n <= 0 ? 0 : (n + p.box - 1) >> p.box_log2;
   };
   auto page_of = [&](const ChunkTile& t, int key) -> int {
     const int page = paged_page(p.a.pb, p.a.kv, t.b, key);
@@ -442,36 +443,54 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
       last_par = (last_par & ~(1u << st)) | (par << st);
       ++pos;
     } else {
+      // Lane l looks after box l of a tile.  (For a page that is not there any scales do.)
+      const int row = lane << p.box_log2, h = row / C::SLOT_ROWS, in_slot = row % C::SLOT_ROWS;
+      const int page0 = t0.key0 + row < t0.len && row < C::BK ? page_of(t0, t0.key0 + row) : 0;
+      const int page1 = t1.kind && t1.key0 + row < t1.len && row < C::BK ? page_of(t1, t1.key0 + row) : 0;
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
         const ChunkTile& t = i == 0 ? t0 : t1;
         if (t.kind == 0) continue;
-        // Lane l looks after box l of the tile.
-        const int n = boxes(t, t.key0, C::BK), key = t.key0 + lane * p.box;
-        const int page = lane < n ? page_of(t, key) : 0;
-        // (For a page that is not there any scales do.)
-        const long long pg = page == p.a.kv.num_pages ? 0 : page;
-        const uint8_t* sc = (t.kind == 1 ? p.a.kv.k_scale : p.a.kv.v_scale) +
-                            (((pg * p.a.kv.heads + t.head) << p.a.kv.ps_log2) + (key & slot_mask));
-        const int in_slot = lane * p.box % C::SLOT_ROWS;
-#pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          const int st = pos % C::NSLOT;
-          const uint32_t par = (pos / C::NSLOT) & 1;
-          const uint32_t full = bar.slot_full(st);
-          const int here = boxes(t, t.key0 + h * C::SLOT_ROWS, C::SLOT_ROWS);
-          if (!chunk_wait(bar.slot_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(full, here * p.box * (D + 1));
-          __syncwarp();
-          if (lane < n && lane * p.box / C::SLOT_ROWS == h) {
-            tma_load_4d(base + C::OFF_SLOT + st * C::SLOT + in_slot * D, t.kind == 1 ? tm_k : tm_v, full, 0, key & slot_mask,
-                        t.head, page, pol_kv);
-            bulk_load(base + C::OFF_SCALE + st * C::SLOT_ROWS + in_slot, sc, p.box, full);
+        const int key = t.key0 + row, page = i == 0 ? page0 : page1;
+        const bool here = key < t.len && row < C::BK;
+        const uint8_t* sc = (t.kind == 1 ? p.a.kv.k_scale : p.a.kv.v_scale) + (key & slot_mask) +
+                            ((static_cast<long long>(page == p.a.kv.num_pages ? 0 : page) * p.a.kv.heads + t.head) << p.a.kv.ps_log2);
+        // Each lane issues its box as soon as its slot is free (a lane at a slot's beginning also says how much comes;
+        // slots behind the sequence's end get nothing).
+        const uint32_t sl = (pos + h) % C::NSLOT, par = ((pos + h) / C::NSLOT) & 1;
+        const uint32_t bytes = (boxes(t, key, C::SLOT_ROWS) << p.box_log2) * (D + 1);  // (of the lane's slot, at its beginning)
+        bool todo = row < C::BK;
+        uint64_t t_start = 0;
+        while (__any_sync(0xffffffffu, todo)) {
+          if (todo && mbar_try_wait_ns(bar.slot_empty(sl), par ^ 1, 200)) {
+            todo = false;
+            const uint32_t full = bar.slot_full(sl);
+            if (in_slot == 0) mbar_arrive_expect_tx(full, bytes);
+            if (here) {
+              tma_load_4d(base + C::OFF_SLOT + sl * C::SLOT + in_slot * D, t.kind == 1 ? tm_k : tm_v, full, 0,
+                          key & slot_mask, t.head, page, pol_kv);
+              bulk_load(base + C::OFF_SCALE + sl * C::SLOT_ROWS + in_slot, sc, p.box, full);
+            }
+          } else if (todo) {
+            const uint64_t now = globaltimer_ns();
+            if (t_start == 0) t_start = now;
+            if (now - t_start > g.limit_ns) {
+              *g.abort = 1;
+              atomicOr(g.status, kStatusTimeoutLoad);
+            }
           }
-          issued |= 1u << st;
-          last_par = (last_par & ~(1u << st)) | (par << st);
-          ++pos;
+          if (__any_sync(0xffffffffu, *g.abort)) break;
         }
+        const uint32_t filled = __ballot_sync(0xffffffffu, !todo && row < C::BK);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (!((filled >> ((k * C::SLOT_ROWS) >> p.box_log2)) & 1)) continue;
+          const uint32_t st = (pos + k) % C::NSLOT;
+          issued |= 1u << st;
+          last_par = (last_par & ~(1u << st)) | ((((pos + k) / C::NSLOT) & 1) << st);
+        }
+        pos += 4;
+        if (__any_sync(0xffffffffu, todo)) return false;
       }
     }
     return true;
@@ -522,9 +541,14 @@ __device__ __forceinline__ bool chunk_convert(const ChunkParams& p, const ChunkB
       if (t.kind == 0) continue;
 #pragma unroll 1
       for (int h = 0; h < 4; ++h, ++quarter) {
-        if (C::SELF_RESCALE && (quarter % 3 == 2) != (WARPS == 2)) continue;
+        // Every warp waits for and frees every slot, its own quarter or not: a slot's phases have to pass it one by one
+        // (a wait for the phase after next would take the last one for it).
         const int sl = quarter % C::NSLOT;
         if (!wait(bar.slot_full(sl), (quarter / C::NSLOT) & 1)) return false;
+        if (C::SELF_RESCALE && (quarter % 3 == 2) != (WARPS == 2)) {
+          warp_arrive(bar.slot_empty(sl));
+          continue;
+        }
         const uint8_t* codes = gbase + C::OFF_SLOT + sl * C::SLOT;
         const uint8_t* scales = gbase + C::OFF_SCALE + sl * C::SLOT_ROWS;
         const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE;
@@ -579,7 +603,6 @@ __device__ __forceinline__ bool chunk_convert(const ChunkParams& p, const ChunkB
         else
           convert(std::true_type{});
         warp_arrive(bar.slot_empty(sl));
-        if constexpr (WARPS == 2) warp_arrive(bar.slot_empty(sl));  // (four arrivals free a slot)
       }
     }
     fence_proxy_async_smem();  // before the tensor core reads them
@@ -778,7 +801,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
       const uint32_t ts = tmem + lane_off + C::TM_S + buf * C::TM_SB;
       const int key0 = (j0 + j) * C::BK;
       float s[C::BK];
-      float rmax, m_new, alpha;
+      float rmax;
 #pragma unroll 1
       for (bool again = false;; again = true) {
         float cmax[C::BK / 32];
@@ -824,14 +847,16 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
           for (int c = 1; c < C::BK / 32; ++c) rmax = fmaxf(rmax, cmax[c]);
         }
         if (again) break;
-        if constexpr (C::LAZY_MAX) {
-          const float rm = rmax * sl2;
-          m_new = (rm > m + C::MAX_SLACK) ? rm : m;
-        } else {
-          m_new = fmaxf(m, rmax * sl2);
-        }
-        alpha = (m_new == m) ? 1.f : ex2(m - m_new);
-        if (!C::SELF_RESCALE || j == 0 || __all_sync(0xffffffffu, alpha == 1.f)) break;
+        if (!C::SELF_RESCALE) break;
+        // The reference maximum moves (rarely) where the row's exceeds it by more than MAX_SLACK.
+        const float rm = rmax * sl2;
+        const bool moves = rm > m + C::MAX_SLACK;
+        if (!__any_sync(0xffffffffu, moves)) break;
+        const float alpha = moves ? ex2(m - rm) : 1.f;
+        m = moves ? rm : m;
+        l *= alpha;
+        lres *= alpha;
+        if (j == 0) break;
         // Rescale O (P V j - 1 is done: S j was issued behind it), then fetch S again: the registers hold one of them.
         const uint32_t to = tmem + lane_off + C::TM_O + ot * D;
         const uint64_t a2 = f2_pack(alpha, alpha);
@@ -850,18 +875,25 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
         }
         tmem_wait_st();
       }
-      float nb = (m_new == -INFINITY) ? 0.f : -m_new;
-      if (!C::SELF_RESCALE && j > 0) {
-        alpha_s[(a_pub & 1) * 128 + r] = alpha;
-        // As in tc_softmax: the exponentials are scheduled after this arrival.
-        nb = fmaf(0.f, __uint_as_float(warp_arrive_token(bar.a_full(ot, a_pub & 1))), nb);
-        ++a_pub;
+      uint32_t after = 0;  // (0; the exponentials below are scheduled behind the arrival, as in tc_softmax)
+      if constexpr (!C::SELF_RESCALE) {
+        const float m_new = fmaxf(m, rmax * sl2);
+        const float alpha = (m_new == m) ? 1.f : ex2(m - m_new);
+        l *= alpha;
+        m = m_new;
+        if (j > 0) {
+          alpha_s[(a_pub & 1) * 128 + r] = alpha;
+          after = warp_arrive_token(bar.a_full(ot, a_pub & 1));
+          ++a_pub;
+        }
       }
+      float nb = (m == -INFINITY) ? 0.f : -m;
+      if constexpr (!C::SELF_RESCALE) nb = fmaf(0.f, __uint_as_float(after), nb);
       const uint64_t nb2 = f2_pack(nb, nb);
       if constexpr (C::LAZY_MAX) {
         const float pmax = ex2(fmaf(rmax, sl2, nb));
         const float pr = __uint_as_float(pack_bf16x2(pmax, 0.f) << 16);
-        lres = lres * alpha + (pr - pmax);
+        lres += pr - pmax;
       }
       uint64_t acc[4];
 #pragma unroll
@@ -888,8 +920,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
       }
       const float2 a01 = f2_unpack(f2_add(acc[0], acc[1]));
       const float2 a23 = f2_unpack(f2_add(acc[2], acc[3]));
-      l = l * alpha + ((a01.x + a01.y) + (a23.x + a23.y));
-      m = m_new;
+      l += (a01.x + a01.y) + (a23.x + a23.y);
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(C::NQT == 2 ? bar.pv_go(ot, C::PV_SPLIT ? 1 : 0) : bar.pv_go(0, (s_waits - 1) & 1));
@@ -1185,7 +1216,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     }
     for (int i = 0; i < C::NSLOT; ++i) {
       mbar_init(bar.slot_full(i), 1);
-      mbar_init(bar.slot_empty(i), 4);
+      mbar_init(bar.slot_empty(i), C::CONV_WARPS);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -1406,6 +1437,8 @@ int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   p.tpt = 128 / a.group;
   const int most = E4M3 ? C::SLOT_ROWS : C::BK;
   p.box = (1 << a.kv.ps_log2) < most ? 1 << a.kv.ps_log2 : most;
+  for (p.box_log2 = 4; (1 << p.box_log2) < p.box; ++p.box_log2) {
+  }
   CUtensorMap mq, mk, mv, mo;
   const long long qdims[3] = {D, a.q_heads, a.pb.rows};
   const long long qst[2] = {a.qs[1], a.qs[0]};
