@@ -17,8 +17,8 @@
 //    only boxes that hold keys of the sequence are.  V rows behind the last token
 //    are set to zero before the tensor core reads them: such slots hold anything,
 //    and 0 times NaN is NaN.
-//  * e4m3 pages.  The load warp brings codes and scales into a small ring, the
-//    correction warps and two more turn them into the bf16 tiles that the tensor
+//  * e4m3 pages.  The load warp brings codes and scales, the correction warps and
+//    two more turn them (d >= 128: in place) into the bf16 tiles that the tensor
 //    core reads (exact: a code has 4 significant bits and a scale is a power of
 //    two), so the rest of the pipeline is the same.
 //  * Output.  A unit held whole is written as it is finished; of others O and
@@ -86,27 +86,33 @@ static_assert(sizeof(ChunkSeg) == 48, "segment size");
 template <int D, bool E4M3>
 struct ChunkCfg : TcCfg<D> {
   using T = TcCfg<D>;
-  // Staged output: buffers of 32 rows x 32 columns per correction warp; e4m3 keeps one and has a ring of quarter key
-  // tiles (codes) in the place of the others.
-  static constexpr int OUT_BUFS = E4M3 ? 1 : T::OSTB;
+  // Staged output: buffers of 32 rows x 32 columns per correction warp; e4m3 has one less, and scale bytes there.
+  static constexpr int OUT_BUFS = E4M3 ? T::OSTB - 1 : T::OSTB;
   static constexpr int OFF_OUT = T::OFF_OST;
-  static constexpr int OFF_SLOT = T::OFF_OST + 4 * OUT_BUFS * T::OST_BUF;
-  static constexpr int SLOT_ROWS = T::BK / 4;
-  static constexpr int SLOT = SLOT_ROWS * D;
-  static constexpr int NSLOT = !E4M3 ? 0 : (T::OST - 4 * T::OST_BUF) / SLOT > 8 ? 8 : (T::OST - 4 * T::OST_BUF) / SLOT;
+  static constexpr int OFF_SCALE = T::OFF_OST + 4 * OUT_BUFS * T::OST_BUF;  // [2][2][BK]
+  // e4m3: where the codes of a stage's tiles are loaded to.  d >= 128: into the tile itself, its upper half: the codes
+  // of a row (d bytes, in columns of 128) lie where the row's last bf16 columns go, so a warp that has read a row may
+  // write it.  d <= 64: into two buffers of their own.
+  static constexpr bool IN_PLACE = D >= 128;
+  static constexpr int CODE_COLS = D < 128 ? D : 128;
+  static constexpr int CODES = T::BK * D;  // bytes of a tile's codes
+  static constexpr int OFF_CODES = T::OFF_OST + T::OST;  // [2][2][CODES]
+  static constexpr int SMEM_E4M3 = OFF_CODES + (IN_PLACE ? 0 : 4 * CODES) + 1024;
+  static constexpr int SMEM_CHUNK = E4M3 && SMEM_E4M3 > T::SMEM_ALLOC ? SMEM_E4M3 : T::SMEM_ALLOC;
+  static_assert(SMEM_CHUNK <= T::SMEM_LIMIT && 4 * T::BK <= 4 * T::OST_BUF, "shared memory budget");
+  static_assert(!IN_PLACE || T::NST == 2, "a stage and its codes have the same index");
   // Two tiles: the softmax warps rescale O themselves where a row's maximum moved far (rare, see LAZY_MAX), so the
   // correction warps are free for the output and, with e4m3 pages, for most of the conversion.
   static constexpr bool SELF_RESCALE = T::NQT == 2;
   static constexpr int OFF_SEG = T::OFF_MISC + 6672;
-  static constexpr int OFF_SCALE = OFF_SEG + kSegRing * static_cast<int>(sizeof(ChunkSeg));  // [NSLOT][SLOT_ROWS]
   static constexpr int OFF_PLAN = T::OFF_ALPHA;  // before the roles start
   static constexpr int CONV_WARPS = !E4M3 ? 0 : SELF_RESCALE ? 6 : 2;  // warps that convert e4m3 tiles
   static constexpr int CONV_WARP0 = T::LOAD_WARP + 1;                  // the last two; the others are the correction warps
   static constexpr int SEG_READERS = T::SOFTMAX_WARPS + 4 + 1 + (E4M3 ? 2 : 0);
   static constexpr int ROWS = T::NQT * 128;
   static_assert(T::OFF_ABORT + 4 <= OFF_SEG && OFF_SEG % 16 == 0, "misc area");
-  static_assert(OFF_SCALE + NSLOT * SLOT_ROWS <= T::OFF_MISC + T::MISC, "misc area");
-  static_assert((!E4M3 || NSLOT >= 2) && sizeof(PlanScratch) <= 2048, "rings");
+  static_assert(OFF_SEG + kSegRing * static_cast<int>(sizeof(ChunkSeg)) <= T::OFF_MISC + T::MISC, "misc area");
+  static_assert(sizeof(PlanScratch) <= 2048, "plan scratch");
 };
 
 template <int D, bool E4M3>
@@ -114,8 +120,9 @@ struct ChunkBars : TcBars<D, TcCfg<D>::NQT, kVarBf16> {
   using Base = TcBars<D, TcCfg<D>::NQT, kVarBf16>;
   __device__ __forceinline__ uint32_t seg_full(int i) const { return this->b0 + 256 + 8u * i; }
   __device__ __forceinline__ uint32_t seg_empty(int i) const { return this->b0 + 288 + 8u * i; }
-  __device__ __forceinline__ uint32_t slot_full(int i) const { return this->b0 + 320 + 8u * i; }
-  __device__ __forceinline__ uint32_t slot_empty(int i) const { return this->b0 + 384 + 8u * i; }
+  // e4m3: the codes of a stage have landed / (d <= 64) have been read.
+  __device__ __forceinline__ uint32_t code_full(int i) const { return this->b0 + 320 + 8u * i; }
+  __device__ __forceinline__ uint32_t code_empty(int i) const { return this->b0 + 336 + 8u * i; }
   // m and l of this accumulator's k-th unit: the softmax may finish the next unit (one key tile) while the
   // correction warpgroup has not come to this one yet, so two barriers take turns.
   __device__ __forceinline__ uint32_t ml_full(int t, int k) const { return this->b0 + 448 + 8u * (2 * t + (k & 1)); }
@@ -326,6 +333,13 @@ __device__ __forceinline__ bool chunk_stream(const Get& get, const Unit& unit, c
   return true;
 }
 
+// Offset of the codes of the tile at position i of stage st (buffer cb).
+template <int D>
+__device__ __forceinline__ uint32_t chunk_codes(int st, int cb, int i) {
+  using C = ChunkCfg<D, true>;
+  return C::IN_PLACE ? C::OFF_KV + st * C::STAGE + i * C::KV_TILE + C::KV_TILE / 2 : C::OFF_CODES + (cb * 2 + i) * C::CODES;
+}
+
 // ------------------------------------------------------------------ load warp
 template <int D, bool E4M3>
 __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
@@ -335,8 +349,8 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
   const int lane = threadIdx.x & 31;
   const uint64_t pol_q = policy_evict_first();
   const uint64_t pol_kv = policy_evict_last();
-  uint32_t pos = 0;          // stages (e4m3: half tiles) filled so far
-  uint32_t issued = 0;       // bit i: stage or slot i has been loaded
+  uint32_t pos = 0;          // stages filled so far
+  uint32_t issued = 0;       // bit i: stage (e4m3: codes) i has been loaded
   uint32_t last_par = 0;     // bit i: parity of its latest load
   int last_q = -1;           // latest segment whose Q tiles were loaded
   bool recorded = false;
@@ -416,90 +430,53 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
   };
   const int slot_mask = (1 << p.a.kv.ps_log2) - 1;
   auto stage = [&](const ChunkTile& t0, const ChunkTile& t1) -> bool {
-    if constexpr (!E4M3) {
-      const int st = pos % C::NST;
-      const uint32_t par = (pos / C::NST) & 1;
-      const uint32_t full = bar.kv_full(st);
-      const int n0 = boxes(t0, t0.key0, C::BK), n1 = t1.kind ? boxes(t1, t1.key0, C::BK) : 0;
-      // The pages are looked up while the stage is still being read.
-      const int page0 = lane < n0 ? page_of(t0, t0.key0 + lane * p.box) : 0;
-      const int page1 = lane < n1 ? page_of(t1, t1.key0 + lane * p.box) : 0;
-      if (!chunk_wait(bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
-      if (lane == 0) mbar_arrive_expect_tx(full, (n0 + n1) * p.box * D * 2);
-      __syncwarp();
+    const int st = pos % C::NST, cb = pos & 1;
+    const bool own = E4M3 && !C::IN_PLACE;  // codes have buffers of their own
+    const uint32_t full = E4M3 ? bar.code_full(cb) : bar.kv_full(st);
+    const int n0 = boxes(t0, t0.key0, C::BK), n1 = t1.kind ? boxes(t1, t1.key0, C::BK) : 0;
+    // The pages are looked up while the stage is still being read.
+    const int row = lane << p.box_log2;
+    const int page0 = lane < n0 ? page_of(t0, t0.key0 + row) : 0;
+    const int page1 = lane < n1 ? page_of(t1, t1.key0 + row) : 0;
+    const uint32_t par = own ? (pos >> 1) & 1 : (pos / C::NST) & 1;
+    if (!chunk_wait(own ? bar.code_empty(cb) : bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
+    if (lane == 0) mbar_arrive_expect_tx(full, ((n0 + n1) << p.box_log2) * (E4M3 ? D + 1 : D * 2));
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const ChunkTile& t = i == 0 ? t0 : t1;
-        if (lane < (i == 0 ? n0 : n1)) {
-          const int key = t.key0 + lane * p.box;
-          const int page = i == 0 ? page0 : page1;
-          const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE + lane * p.box * C::SWB;
-          for (int r = 0; r < C::NR; ++r)
-            tma_load_4d(dst + r * C::K_REGION, t.kind == 1 ? tm_k : tm_v, full, r * C::RC, key & slot_mask, t.head, page,
-                        pol_kv);
-        }
-      }
-      issued |= 1u << st;
-      last_par = (last_par & ~(1u << st)) | (par << st);
-      ++pos;
-    } else {
-      // Lane l looks after box l of a tile.  (For a page that is not there any scales do.)
-      const int row = lane << p.box_log2, h = row / C::SLOT_ROWS, in_slot = row % C::SLOT_ROWS;
-      const int page0 = t0.key0 + row < t0.len && row < C::BK ? page_of(t0, t0.key0 + row) : 0;
-      const int page1 = t1.kind && t1.key0 + row < t1.len && row < C::BK ? page_of(t1, t1.key0 + row) : 0;
-#pragma unroll 1
-      for (int i = 0; i < 2; ++i) {
-        const ChunkTile& t = i == 0 ? t0 : t1;
-        if (t.kind == 0) continue;
+    for (int i = 0; i < 2; ++i) {
+      const ChunkTile& t = i == 0 ? t0 : t1;
+      if (lane < (i == 0 ? n0 : n1)) {
         const int key = t.key0 + row, page = i == 0 ? page0 : page1;
-        const bool here = key < t.len && row < C::BK;
-        const uint8_t* sc = (t.kind == 1 ? p.a.kv.k_scale : p.a.kv.v_scale) + (key & slot_mask) +
-                            ((static_cast<long long>(page == p.a.kv.num_pages ? 0 : page) * p.a.kv.heads + t.head) << p.a.kv.ps_log2);
-        // Each lane issues its box as soon as its slot is free (a lane at a slot's beginning also says how much comes;
-        // slots behind the sequence's end get nothing).
-        const uint32_t sl = (pos + h) % C::NSLOT, par = ((pos + h) / C::NSLOT) & 1;
-        const uint32_t bytes = (boxes(t, key, C::SLOT_ROWS) << p.box_log2) * (D + 1);  // (of the lane's slot, at its beginning)
-        bool todo = row < C::BK;
-        uint64_t t_start = 0;
-        while (__any_sync(0xffffffffu, todo)) {
-          if (todo && mbar_try_wait_ns(bar.slot_empty(sl), par ^ 1, 200)) {
-            todo = false;
-            const uint32_t full = bar.slot_full(sl);
-            if (in_slot == 0) mbar_arrive_expect_tx(full, bytes);
-            if (here) {
-              tma_load_4d(base + C::OFF_SLOT + sl * C::SLOT + in_slot * D, t.kind == 1 ? tm_k : tm_v, full, 0,
-                          key & slot_mask, t.head, page, pol_kv);
-              bulk_load(base + C::OFF_SCALE + sl * C::SLOT_ROWS + in_slot, sc, p.box, full);
-            }
-          } else if (todo) {
-            const uint64_t now = globaltimer_ns();
-            if (t_start == 0) t_start = now;
-            if (now - t_start > g.limit_ns) {
-              *g.abort = 1;
-              atomicOr(g.status, kStatusTimeoutLoad);
-            }
-          }
-          if (__any_sync(0xffffffffu, *g.abort)) break;
+        const CUtensorMap* tm = t.kind == 1 ? tm_k : tm_v;
+        if constexpr (!E4M3) {
+          const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE + row * C::SWB;
+          for (int r = 0; r < C::NR; ++r)
+            tma_load_4d(dst + r * C::K_REGION, tm, full, r * C::RC, key & slot_mask, t.head, page, pol_kv);
+        } else {
+          const uint32_t dst = base + chunk_codes<D>(st, cb, i) + row * C::CODE_COLS;
+          for (int r = 0; r < D / C::CODE_COLS; ++r)
+            tma_load_4d(dst + r * C::BK * C::CODE_COLS, tm, full, r * C::CODE_COLS, key & slot_mask, t.head, page, pol_kv);
+          // (For a page that is not there any scales do.)
+          const long long pg = page == p.a.kv.num_pages ? 0 : page;
+          bulk_load(base + C::OFF_SCALE + (cb * 2 + i) * C::BK + row,
+                    (t.kind == 1 ? p.a.kv.k_scale : p.a.kv.v_scale) +
+                        (((pg * p.a.kv.heads + t.head) << p.a.kv.ps_log2) + (key & slot_mask)),
+                    p.box, full);
         }
-        const uint32_t filled = __ballot_sync(0xffffffffu, !todo && row < C::BK);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (!((filled >> ((k * C::SLOT_ROWS) >> p.box_log2)) & 1)) continue;
-          const uint32_t st = (pos + k) % C::NSLOT;
-          issued |= 1u << st;
-          last_par = (last_par & ~(1u << st)) | ((((pos + k) / C::NSLOT) & 1) << st);
-        }
-        pos += 4;
-        if (__any_sync(0xffffffffu, todo)) return false;
       }
     }
+    const int slot = E4M3 ? cb : st;
+    const uint32_t load_par = E4M3 ? (pos >> 1) & 1 : par;
+    issued |= 1u << slot;
+    last_par = (last_par & ~(1u << slot)) | (load_par << slot);
+    ++pos;
     return true;
   };
   chunk_stream<D>(get, unit, stage);
   if (lane == 0 && !recorded) p.ws.chunk_rec[blockIdx.x].b = -1;
   // Every issued copy must land before the CTA may exit.
-  for (int i = 0; i < (E4M3 ? C::NSLOT : C::NST); ++i)
-    if (issued & (1u << i)) wait_bar_drain(E4M3 ? bar.slot_full(i) : bar.kv_full(i), (last_par >> i) & 1, g);
+  for (int i = 0; i < (E4M3 ? 2 : C::NST); ++i)
+    if (issued & (1u << i)) wait_bar_drain(E4M3 ? bar.code_full(i) : bar.kv_full(i), (last_par >> i) & 1, g);
   for (int t = 0; t < C::NQT; ++t)
     if (last_q >= 0) wait_bar_drain(bar.q_full(t), last_q & 1, g);
   __syncwarp();
@@ -522,90 +499,83 @@ __device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t x, uint32_t f, uint32_
   hi = mul_bf16x2(__byte_perm(l, h, 0x7362), f);
 }
 
-// Quarter tiles that the load warp brought, into the stages.  Two tiles: of three quarters the four correction warps
-// take two and the last two warps one; one tile: the last two take all.  wait(bar, parity) waits, get fetches segments.
-template <int D, bool E4M3, int WARPS, class Get, class Wait>
+// Stage after stage, groups of 16 rows dealt out to WARPS warps, this one the cw-th.  wait(bar, parity) waits, get
+// fetches segments.
+template <int D, bool E4M3, class Get, class Wait>
 __device__ __forceinline__ bool chunk_convert(const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint32_t base,
                                               uint8_t* gbase, int cw, const Get& get, const Wait& wait) {
   using C = ChunkCfg<D, E4M3>;
+  constexpr int WARPS = C::CONV_WARPS;
+  constexpr int UPR = D / 8;              // 16-byte units of a bf16 row
+  constexpr int RPP = 32 / UPR;           // rows of a pass of the warp
+  constexpr int PASSES = 16 / RPP;
+  constexpr int BATCH = RPP * 4 >= 8 ? (PASSES < 4 ? PASSES : 4) : 8 / RPP;
+  constexpr int UR = C::SWB / 16;
+  static_assert(PASSES % BATCH == 0 && BATCH * RPP % 8 == 0, "a batch of passes is a whole number of swizzle periods");
   const int lane = threadIdx.x & 31;
-  uint32_t pos = 0, quarter = 0;
+  const int row0 = lane / UPR, unit16 = lane % UPR;
+  // This thread's places within 8 / RPP passes of rows.
+  uint32_t to[BATCH];
+#pragma unroll
+  for (int k = 0; k < BATCH; ++k) {
+    const int r = k * RPP + row0;
+    const uint32_t sw = C::SWB == 128 ? r & 7 : (r >> 1) & 3;
+    to[k] = (unit16 / UR) * C::K_REGION + r * C::SWB + (((unit16 % UR) ^ sw) << 4);
+  }
+  const uint32_t from = unit16 / (C::CODE_COLS / 8) * (C::BK * C::CODE_COLS) + row0 * C::CODE_COLS +
+                        unit16 % (C::CODE_COLS / 8) * 8;
+  uint32_t pos = 0;
   auto unit = [&](const ChunkSeg&, int) -> bool { return true; };
   auto stage = [&](const ChunkTile& t0, const ChunkTile& t1) -> bool {
-    const int st = pos % C::NST;
-    if (!wait(bar.kv_empty(st), ((pos / C::NST) & 1) ^ 1)) return false;
+    const int st = pos % C::NST, cb = pos & 1;
+    if (!C::IN_PLACE && !wait(bar.kv_empty(st), ((pos / C::NST) & 1) ^ 1)) return false;
+    if (!wait(bar.code_full(cb), (pos >> 1) & 1)) return false;
     ++pos;
+    const int groups = t1.kind ? C::BK / 8 : C::BK / 16;
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      const ChunkTile& t = i == 0 ? t0 : t1;
-      if (t.kind == 0) continue;
+    for (int gr = cw; gr < groups; gr += WARPS) {
+      const int i = gr / (C::BK / 16), r16 = gr % (C::BK / 16) * 16;
+      const int end = (i == 0 ? t0.len - t0.key0 : t1.len - t1.key0) - r16;  // rows of these 16 that are keys
+      const uint8_t* codes = gbase + chunk_codes<D>(st, cb, i) + r16 * C::CODE_COLS + from;
+      const uint8_t* scales = gbase + C::OFF_SCALE + (cb * 2 + i) * C::BK + r16;
+      const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE + r16 * C::SWB;
+      const uint32_t big = lane < 4 ? __vcmpgtu4(reinterpret_cast<const uint32_t*>(scales)[lane], 0x86868686u) : 0u;  // a byte > 134
+      auto convert = [&](auto checked) {
 #pragma unroll 1
-      for (int h = 0; h < 4; ++h, ++quarter) {
-        // Every warp waits for and frees every slot, its own quarter or not: a slot's phases have to pass it one by one
-        // (a wait for the phase after next would take the last one for it).
-        const int sl = quarter % C::NSLOT;
-        if (!wait(bar.slot_full(sl), (quarter / C::NSLOT) & 1)) return false;
-        if (C::SELF_RESCALE && (quarter % 3 == 2) != (WARPS == 2)) {
-          warp_arrive(bar.slot_empty(sl));
-          continue;
-        }
-        const uint8_t* codes = gbase + C::OFF_SLOT + sl * C::SLOT;
-        const uint8_t* scales = gbase + C::OFF_SCALE + sl * C::SLOT_ROWS;
-        const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE;
-        const int end = t.len - (t.key0 + h * C::SLOT_ROWS);  // rows of this quarter that are keys
-        constexpr int UPR = D / 8;                 // 16-byte units of a bf16 row
-        constexpr int RPP = 32 * WARPS / UPR;      // rows of a pass of the group's threads
-        constexpr int PASSES = C::SLOT_ROWS / RPP;
-        constexpr int BATCH = PASSES < 4 ? PASSES : 4;
-        constexpr int UR = C::SWB / 16;
-        static_assert(PASSES >= 1 && PASSES % BATCH == 0 && (PASSES == BATCH || BATCH * RPP % 8 == 0),
-                      "a batch of passes is a whole number of swizzle periods");
-        const int row0 = (cw * 32 + lane) / UPR, unit16 = lane % UPR;
-        const uint32_t* sw4 = reinterpret_cast<const uint32_t*>(scales);
-        const uint32_t big = lane < C::SLOT_ROWS / 4 ? __vcmpgtu4(sw4[lane], 0x86868686u) : 0u;  // a byte > 134
-        uint32_t to[BATCH];
+        for (int pass = 0; pass < PASSES; pass += BATCH) {
+          uint2 x[BATCH];
+          uint32_t byte[BATCH], w[BATCH][4];
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-          const int r = k * RPP + row0;
-          const uint32_t sw = C::SWB == 128 ? r & 7 : (r >> 1) & 3;
-          to[k] = dst + (unit16 / UR) * C::K_REGION + (h * C::SLOT_ROWS + r) * C::SWB + (((unit16 % UR) ^ sw) << 4);
-        }
-        auto convert = [&](auto checked) {
-#pragma unroll 1
-          for (int pass = 0; pass < PASSES; pass += BATCH) {
-            uint2 x[BATCH];
-            uint32_t byte[BATCH], w[BATCH][4];
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-              const int r = (pass + k) * RPP + row0;
-              x[k] = *reinterpret_cast<const uint2*>(codes + r * D + unit16 * 8);
-              byte[k] = scales[r];
-            }
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-              uint32_t f = byte[k] * 0x00800080u + 120u * 0x00800080u;  // 2^(120 + e), twice
-              if constexpr (decltype(checked)::value) f = byte[k] == 255u ? 0x7fc07fc0u : byte[k] > 134u ? 0x7f007f00u : f;  // NaN, or 2^127 at most
-              e4m3x4_to_bf16x4(x[k].x, f, w[k][0], w[k][1]);
-              e4m3x4_to_bf16x4(x[k].y, f, w[k][2], w[k][3]);
-              if constexpr (decltype(checked)::value) {
-                const uint32_t f2 = byte[k] > 134u && byte[k] != 255u ? (byte[k] - 7u) * 0x00800080u : 0x3f803f80u;  // 2^(e - 7)
-                const bool past = (pass + k) * RPP + row0 >= end;
-#pragma unroll
-                for (int i2 = 0; i2 < 4; ++i2) w[k][i2] = past ? 0u : mul_bf16x2(w[k][i2], f2);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) st_shared_v4(to[k] + pass * RPP * C::SWB, w[k][0], w[k][1], w[k][2], w[k][3]);
+          for (int k = 0; k < BATCH; ++k) {
+            x[k] = *reinterpret_cast<const uint2*>(codes + (pass + k) * RPP * C::CODE_COLS);
+            byte[k] = scales[(pass + k) * RPP + row0];
           }
-        };
-        if (end >= C::SLOT_ROWS && !__any_sync(0xffffffffu, big != 0))
-          convert(std::false_type{});
-        else
-          convert(std::true_type{});
-        warp_arrive(bar.slot_empty(sl));
-      }
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            uint32_t f = byte[k] * 0x00800080u + 120u * 0x00800080u;  // 2^(120 + e), twice
+            if constexpr (decltype(checked)::value)
+              f = byte[k] == 255u ? 0x7fc07fc0u : byte[k] > 134u ? 0x7f007f00u : f;  // NaN, or 2^127 at most
+            e4m3x4_to_bf16x4(x[k].x, f, w[k][0], w[k][1]);
+            e4m3x4_to_bf16x4(x[k].y, f, w[k][2], w[k][3]);
+            if constexpr (decltype(checked)::value) {
+              const uint32_t f2 = byte[k] > 134u && byte[k] != 255u ? (byte[k] - 7u) * 0x00800080u : 0x3f803f80u;  // 2^(e - 7)
+              const bool past = (pass + k) * RPP + row0 >= end;
+#pragma unroll
+              for (int i2 = 0; i2 < 4; ++i2) w[k][i2] = past ? 0u : mul_bf16x2(w[k][i2], f2);
+            }
+          }
+          if constexpr (C::IN_PLACE) __syncwarp();  // the rows have been read by all of the warp
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) st_shared_v4(dst + to[k] + pass * RPP * C::SWB, w[k][0], w[k][1], w[k][2], w[k][3]);
+        }
+      };
+      if (end >= 16 && !__any_sync(0xffffffffu, big != 0))
+        convert(std::false_type{});
+      else
+        convert(std::true_type{});
     }
     fence_proxy_async_smem();  // before the tensor core reads them
+    if constexpr (!C::IN_PLACE) warp_arrive(bar.code_empty(cb));
     warp_arrive(bar.kv_full(st));
     return true;
   };
@@ -1160,7 +1130,7 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUt
       if (w.valid) seen = k + 1;
       return true;
     };
-    ok = chunk_convert<D, E4M3, 4>(p, bar, base, gbase, quarter, get, wait);
+    ok = chunk_convert<D, E4M3>(p, bar, base, gbase, quarter, get, wait);
     while (ok && out_k < seen) ok = output(true);
   }
   if (lane == 0) bulk_wait_group_all();  // staged chunks are written before the CTA leaves
@@ -1214,9 +1184,9 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       mbar_init(bar.seg_full(i), 1);
       mbar_init(bar.seg_empty(i), C::SEG_READERS);
     }
-    for (int i = 0; i < C::NSLOT; ++i) {
-      mbar_init(bar.slot_full(i), 1);
-      mbar_init(bar.slot_empty(i), C::CONV_WARPS);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar.code_full(i), 1);
+      mbar_init(bar.code_empty(i), E4M3 ? C::CONV_WARPS : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -1258,8 +1228,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     if (warp == C::MMA_WARP) chunk_mma<D, E4M3>(p, bar, base, gbase, tmem, g);
     if constexpr (E4M3)
       if (warp >= C::CONV_WARP0)
-        chunk_convert<D, E4M3, 2>(
-            p, bar, base, gbase, warp - C::CONV_WARP0,
+        chunk_convert<D, E4M3>(
+            p, bar, base, gbase, warp - C::CONV_WARP0 + C::CONV_WARPS - 2,
             [&](int k, ChunkSeg& w) -> bool { return seg_read<D, E4M3>(w, k, gbase, bar, g); },
             [&](uint32_t b, uint32_t parity) -> bool { return chunk_wait(b, parity, g, kStatusTimeoutLoad); });
   }
@@ -1426,7 +1396,7 @@ int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
     if (regs != C::LAUNCH_REGS) return -2;
   }
   static std::atomic<unsigned long long> allowed{0};
-  const int e = allow_smem(kernel, C::SMEM_ALLOC, allowed);
+  const int e = allow_smem(kernel, C::SMEM_CHUNK, allowed);
   if (e != 0) return e;
   ChunkParams p;
   p.a = a;
@@ -1435,8 +1405,7 @@ int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   p.limit_ns = ctx.limit_ns;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.tpt = 128 / a.group;
-  const int most = E4M3 ? C::SLOT_ROWS : C::BK;
-  p.box = (1 << a.kv.ps_log2) < most ? 1 << a.kv.ps_log2 : most;
+  p.box = (1 << a.kv.ps_log2) < C::BK ? 1 << a.kv.ps_log2 : C::BK;
   for (p.box_log2 = 4; (1 << p.box_log2) < p.box; ++p.box_log2) {
   }
   CUtensorMap mq, mk, mv, mo;
@@ -1450,12 +1419,12 @@ int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   if (p.tma_o && encode_paged_map(&mo, a.o, 2, qdims, ost, 32, oh, 32 / oh, 64, false) != 0) return -1;
   const long long dims[4] = {D, 1LL << a.kv.ps_log2, a.kv.heads, a.kv.num_pages};
   const long long ks[3] = {a.kv.ks[2], a.kv.ks[1], a.kv.ks[0]}, vs[3] = {a.kv.vs[2], a.kv.vs[1], a.kv.vs[0]};
-  // bf16: 64-column regions in the operand layout; e4m3: whole rows of codes, unswizzled.
-  const int cols = E4M3 ? D : C::RC, swizzle = E4M3 ? 0 : C::SWB;
+  // bf16: 64-column regions in the operand layout; e4m3: rows of codes, 128 columns at a time, unswizzled.
+  const int cols = E4M3 ? C::CODE_COLS : C::RC, swizzle = E4M3 ? 0 : C::SWB;
   if (encode_paged_map(&mk, a.kv.k, E4M3 ? 1 : 2, dims, ks, cols, p.box, 1, swizzle, true) != 0) return -1;
   if (encode_paged_map(&mv, a.kv.v, E4M3 ? 1 : 2, dims, vs, cols, p.box, 1, swizzle, true) != 0) return -1;
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
-  return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mq, mk, mv, mo, p);
+  return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_CHUNK, ctx.stream, mq, mk, mv, mo, p);
 }
 
 template <int D>
