@@ -772,8 +772,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
       const int key0 = (j0 + j) * C::BK;
       float s[C::BK];
       float rmax;
-#pragma unroll 1
-      for (bool again = false;; again = true) {
+      auto fetch = [&]() {
         float cmax[C::BK / 32];
         {
           uint32_t raw_s[C::BK / 32][32];
@@ -816,34 +815,39 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
 #pragma unroll
           for (int c = 1; c < C::BK / 32; ++c) rmax = fmaxf(rmax, cmax[c]);
         }
-        if (again) break;
-        if (!C::SELF_RESCALE) break;
+      };
+      fetch();
+      if constexpr (C::SELF_RESCALE) {
         // The reference maximum moves (rarely) where the row's exceeds it by more than MAX_SLACK.
         const float rm = rmax * sl2;
         const bool moves = rm > m + C::MAX_SLACK;
-        if (!__any_sync(0xffffffffu, moves)) break;
-        const float alpha = moves ? ex2(m - rm) : 1.f;
-        m = moves ? rm : m;
-        l *= alpha;
-        lres *= alpha;
-        if (j == 0) break;
-        // Rescale O (P V j - 1 is done: S j was issued behind it), then fetch S again: the registers hold one of them.
-        const uint32_t to = tmem + lane_off + C::TM_O + ot * D;
-        const uint64_t a2 = f2_pack(alpha, alpha);
+        if (__any_sync(0xffffffffu, moves)) {
+          const float alpha = moves ? ex2(m - rm) : 1.f;
+          m = moves ? rm : m;
+          l *= alpha;
+          lres *= alpha;
+          if (j > 0) {
+            // Rescale O (P V j - 1 is done: S j was issued behind it), then fetch S again: the registers hold one of them.
+            // (A second copy of the fetch: as a loop the common path took 5 % longer.)
+            const uint32_t to = tmem + lane_off + C::TM_O + ot * D;
+            const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(to + c * 32, v);
-          tmem_wait_ld(v);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(to + c * 32, v);
+              tmem_wait_ld(v);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 y = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), a2));
-            v[i] = __float_as_uint(y.x);
-            v[i + 1] = __float_as_uint(y.y);
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), a2));
+                v[i] = __float_as_uint(y.x);
+                v[i + 1] = __float_as_uint(y.y);
+              }
+              tmem_st32(to + c * 32, v);
+            }
+            tmem_wait_st();
+            fetch();
           }
-          tmem_st32(to + c * 32, v);
         }
-        tmem_wait_st();
       }
       uint32_t after = 0;  // (0; the exponentials below are scheduled behind the arrival, as in tc_softmax)
       if constexpr (!C::SELF_RESCALE) {
