@@ -42,7 +42,7 @@ struct FewCfg {
   static constexpr int THREADS = 32 * NW;
   // Keys of a group: 4 KB of K, so that what a group costs besides its products is spread over as many keys as
   // registers hold logits of.
-  static constexpr int KG = E4M3 ? (D >= 128 ? 32 : 64) : (D >= 128 ? 16 : D == 64 ? 32 : 64);
+  static constexpr int KG = E4M3 ? (D >= 128 || NT == 4 ? 32 : 64) : (D >= 128 ? 16 : D == 64 ? 32 : 64);
   static constexpr int NG = KG / 16;
   static constexpr int KT = KG * NW;                      // keys of a tile (one group per warp)
   static constexpr int SWB = ROWB < 128 ? ROWB : 128;     // swizzle span
@@ -108,6 +108,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+constexpr int kFewUnitCost = 2;   // tiles that a unit costs besides its own (beginning it, joining the warps)
 constexpr float kFewSlack = 8.f;  // log2 units by which a logit may exceed the reference maximum
 
 struct FewParams {
@@ -125,7 +126,14 @@ __device__ __forceinline__ int few_tiles(const PagedFwdArgs& a, const PagedSeq& 
   return s.len <= KT ? 1 : (s.len + KT - 1) / KT;  // without keys too: the rows get their zeros
 }
 
-// Walks the tiles of a CTA's share.
+// Length of sequence b's units on the line of work.
+template <int KT>
+__device__ __forceinline__ long long few_length(const PagedFwdArgs& a, const PagedSeq& s) {
+  const int nt = few_tiles<KT>(a, s);
+  return nt == 0 ? 0 : static_cast<long long>(a.kv.heads) * (nt + kFewUnitCost);
+}
+
+// Walks the tiles of a CTA's share; `left`: what is left of it on the line (0: no more tiles).
 template <int KT>
 struct FewCursor {
   int b, head, j, nt, left;
@@ -140,14 +148,21 @@ struct FewCursor {
     b = p.b;
     if (left == 0) return;
     load(a);
-    head = static_cast<int>(p.offset / nt);
-    j = static_cast<int>(p.offset - static_cast<long long>(head) * nt);
+    head = static_cast<int>(p.offset / (nt + kFewUnitCost));
+    j = static_cast<int>(p.offset - static_cast<long long>(head) * (nt + kFewUnitCost));
+    if (j >= nt) {  // behind a unit's tiles (a share is longer than that)
+      left += j - nt;
+      j = nt;
+      advance(a, 0);
+    }
   }
   // Move on by k tiles of the present unit.
   __device__ __forceinline__ void advance(const PagedFwdArgs& a, int k) {
     left -= k;
     j += k;
-    if (left == 0 || j < nt) return;
+    if (j < nt) return;
+    left = max(left - kFewUnitCost, 0);
+    if (left == 0) return;
     j = 0;
     if (++head < a.kv.heads) return;
     head = 0;
@@ -197,9 +212,9 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
       a.pb.B, gridDim.x, blockIdx.x,
       [&](int b) -> long long {
         bool bad;
-        return static_cast<long long>(a.kv.heads) * few_tiles<C::KT>(a, paged_seq(a.pb, a.kv.ps_log2, b, bad));
+        return few_length<C::KT>(a, paged_seq(a.pb, a.kv.ps_log2, b, bad));
       },
-      1,
+      1 + kFewUnitCost,
       *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
 
   // ---- the warp's loads
@@ -249,6 +264,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
   bool ok = true;
   bool recorded = false;
   const float scale_log2 = a.scale * 1.4426950408889634f;
+  const uint32_t group_magic = 65536u / a.group + 1;
   // Swizzled place of 16-byte unit `unit` of row `row` in a K or V tile of a stage.
   auto place = [](uint32_t row, uint32_t unit) -> uint32_t {
     constexpr uint32_t U = C::SWB / 16;
@@ -274,24 +290,21 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
     const int j0 = at.j;
     const int j1 = at.left < at.nt - j0 ? j0 + at.left : at.nt;
     const int na = (rows + 7) >> 3;  // row tiles that hold rows
-    // The last key that this thread's rows 8t + 2jq, + 1 see (rows behind the last: any).
-    int lim[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 8 * t + 2 * jq + i;
-        lim[t][i] = a.causal && r < rows ? s.len - s.n + r / a.group : s.len - 1;
-      }
+    // r / group of a row (exact: r (magic - 65536 / group) < 32 and a group is 32 at most).
+    auto token_of = [&](int r) -> int { return static_cast<int>(static_cast<uint32_t>(r) * group_magic >> 16); };
+    // The last key that row r sees (rows behind the last: any).
+    auto sees = [&](int r) -> int { return a.causal && r < rows ? s.len - s.n + token_of(r) : s.len - 1; };
     auto q_row = [&](int r) -> const __nv_bfloat16* {
-      return r >= rows ? nullptr : a.q + static_cast<long long>(s.row0 + r / a.group) * a.qs[0] +
-                                       static_cast<long long>(at.head * a.group + r % a.group) * a.qs[1];
+      const int tok = token_of(r);
+      return r >= rows ? nullptr : a.q + static_cast<long long>(s.row0 + tok) * a.qs[0] +
+                                       static_cast<long long>(at.head * a.group + r - tok * a.group) * a.qs[1];
     };
     // Rows that exist see the keys up to here (row 0 sees the fewest).
     const int lim_all = a.causal ? s.len - s.n : s.len - 1;
     // q as the B operand: row 8t + g, elements 16k + 2jq, + 1 and 16k + 8 + 2jq, + 1.
     uint32_t qf[C::QS ? 1 : NT][C::QS ? 1 : C::KS][2];
-    float rowf[NT][2];  // factors of rows 8t + 2jq, + 1
+    float rowf[NT][2];  // factors of rows 8t + 2jq, + 1 (q in shared memory: read again for every group)
+    const float2* rf = reinterpret_cast<const float2*>(gbase + C::OFF_ROWF);
     if constexpr (C::QS == 0) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -328,26 +341,31 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
       }
     } else {
       // q into shared memory: a warp per row, four elements a lane.
-      float* rf = reinterpret_cast<float*>(gbase + C::OFF_ROWF);
-      for (int r = warp; r < 8 * NT; r += C::NW) {
-        const __nv_bfloat16* q = q_row(r);
-        constexpr int CH = (D / 4 + 31) / 32;
-        uint8_t* dst = gbase + C::OFF_Q;
-        uint2 w[CH];
-        uint32_t top = 0;
+      constexpr int CH = (D / 4 + 31) / 32, RW = 8 * NT / C::NW;
+      uint2 w[RW][CH];
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        const __nv_bfloat16* q = q_row(warp + i * C::NW);
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch) {
           const int at4 = ch * 32 + lane;  // elements 4 at4 ..
-          w[ch] = q && at4 < D / 4 ? *reinterpret_cast<const uint2*>(q + 4 * at4) : make_uint2(0u, 0u);
-          top = __vmaxu2(top, __vmaxu2(w[ch].x & 0x7fff7fffu, w[ch].y & 0x7fff7fffu));
+          w[i][ch] = q && at4 < D / 4 ? *reinterpret_cast<const uint2*>(q + 4 * at4) : make_uint2(0u, 0u);
         }
+      }
+      uint8_t* dst = gbase + C::OFF_Q;
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        const int r = warp + i * C::NW;
         if constexpr (!E4M3) {
 #pragma unroll
           for (int ch = 0; ch < CH; ++ch) {
             const int at4 = ch * 32 + lane;
-            if (at4 < D / 4) *reinterpret_cast<uint2*>(dst + q_place(r, at4 >> 1) + (at4 & 1) * 8) = w[ch];
+            if (at4 < D / 4) *reinterpret_cast<uint2*>(dst + q_place(r, at4 >> 1) + (at4 & 1) * 8) = w[i][ch];
           }
         } else {
+          uint32_t top = 0;
+#pragma unroll
+          for (int ch = 0; ch < CH; ++ch) top = __vmaxu2(top, __vmaxu2(w[i][ch].x & 0x7fff7fffu, w[i][ch].y & 0x7fff7fffu));
           top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
           float factor;
           const float f = row_scale(top, factor);
@@ -357,18 +375,14 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
             const int at4 = ch * 32 + lane, blk = at4 >> 2, x = at4 & 3;
             if (at4 >= D / 4) continue;
             *reinterpret_cast<uint32_t*>(dst + q_place(r, 2 * blk) + 4 * x) =
-                pack_f16x2(__uint_as_float(w[ch].x << 16) * f, __uint_as_float(w[ch].x & 0xffff0000u) * f);
+                pack_f16x2(__uint_as_float(w[i][ch].x << 16) * f, __uint_as_float(w[i][ch].x & 0xffff0000u) * f);
             *reinterpret_cast<uint32_t*>(dst + q_place(r, 2 * blk + 1) + 4 * x) =
-                pack_f16x2(__uint_as_float(w[ch].y << 16) * f, __uint_as_float(w[ch].y & 0xffff0000u) * f);
+                pack_f16x2(__uint_as_float(w[i][ch].y << 16) * f, __uint_as_float(w[i][ch].y & 0xffff0000u) * f);
           }
-          if (lane == 0) rf[r] = factor;
+          if (lane == 0) reinterpret_cast<float*>(gbase + C::OFF_ROWF)[r] = factor;
         }
       }
       __syncthreads();
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) rowf[t][i] = E4M3 ? rf[8 * t + 2 * jq + i] : scale_log2;
     }
     // O^T: columns 16c + g and 16c + g + 8 (e4m3: 16c + 2g and 16c + 2g + 1) of rows 8t + 2jq, + 1.
     float o[NT][C::KS][4];
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-              if (t < na) mma_16816<E4M3>(x[t][sg], ka[h], qb[t][h][0], qb[t][h][1]);
+              mma_16816<E4M3>(x[t][sg], ka[h], qb[t][h][0], qb[t][h][1]);
         }
       }
       const bool edge = key0 + C::KG - 1 > lim_all;  // some row does not see some key
@@ -453,21 +467,24 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
       if constexpr (E4M3) {
         const uint8_t* sc = gbase + C::OFF_SCALE + (warp * C::S + st) * 2 * C::KG;
         int vb[NG][2], top = 0;
+        float kf[NG][2];
 #pragma unroll
         for (int sg = 0; sg < NG; ++sg)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int at_key = 16 * sg + 8 * i + g;
-            const float kf = scale_of_byte(sc[at_key]);
+            kf[sg][i] = scale_of_byte(sc[at_key]);
             vb[sg][i] = sc[C::KG + at_key];
             if (edge && key0 + at_key >= s.len) vb[sg][i] = 0;
             top = max(top, vb[sg][i] == 255 ? 0 : vb[sg][i]);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              x[t][sg][2 * i] *= kf;
-              x[t][sg][2 * i + 1] *= kf;
-            }
           }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int sg = 0; sg < NG; ++sg)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[t][sg][i] *= kf[sg][i >> 1];
+        }
         top = max(vexp, __reduce_max_sync(0xffffffffu, top));
         const int fall = top - vexp;  // 0 .. 254
         vdown = fall > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - fall) << 23);
@@ -479,17 +496,26 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
             pf[sg][i] = vb[sg][i] == 255 ? __uint_as_float(0x7fc00000u)
                                          : __uint_as_float(static_cast<uint32_t>(max(127 + 6 + vb[sg][i] - top, 0)) << 23);
       }
+      if constexpr (C::QS != 0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float2 f = E4M3 ? rf[4 * t + jq] : make_float2(scale_log2, scale_log2);
+          rowf[t][0] = f.x;
+          rowf[t][1] = f.y;
+        }
+      }
       uint32_t pb[NT][NG][2];  // P^T as the B operand
       float top[NT][2];        // this thread's largest logits of its rows (in units of the scaled ones)
       bool moves = vdown != 1.f;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         if (edge) {
+          const int lim[2] = {sees(8 * t + 2 * jq), sees(8 * t + 2 * jq + 1)};
 #pragma unroll
           for (int sg = 0; sg < NG; ++sg)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (key0 + 16 * sg + 8 * (i >> 1) + g > lim[t][i & 1]) x[t][sg][i] = -INFINITY;
+              if (key0 + 16 * sg + 8 * (i >> 1) + g > lim[i & 1]) x[t][sg][i] = -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -497,7 +523,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
 #pragma unroll
           for (int sg = 1; sg < NG; ++sg) y = fmax3(y, x[t][sg][i], x[t][sg][2 + i]);
           top[t][i] = y * rowf[t][i];
-          moves = moves || (t < na && top[t][i] > m[t][i] + kFewSlack);
+          moves = moves || top[t][i] > m[t][i] + kFewSlack;
         }
       }
       if (__any_sync(0xffffffffu, moves)) {
@@ -527,7 +553,6 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if (t >= na) continue;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float ref = m[t][i] == -INFINITY ? 0.f : -m[t][i];
@@ -548,11 +573,12 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
           for (int h = 0; h < 2; ++h) {
             float* y = &x[t][sg][2 * h];
             if constexpr (E4M3) {
+              y[0] *= pf[sg][h];
+              y[1] *= pf[sg][h];
+              if (edge) {  // a scale of NaN reaches only the rows that see its token
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                y[i] *= pf[sg][h];
-                // A scale of NaN reaches only the rows that see its token.
-                if (edge && key0 + 16 * sg + 8 * h + g > lim[t][i]) y[i] = 0.f;
+                for (int i = 0; i < 2; ++i)
+                  if (key0 + 16 * sg + 8 * h + g > sees(8 * t + 2 * jq + i)) y[i] = 0.f;
               }
               pb[t][sg][h] = transpose_8x8(pack_f16x2(y[0], y[1]));
             } else {
@@ -596,7 +622,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
               ldsm_x4_t(vt + place(16 * sg + (lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1)), b);
 #pragma unroll
               for (int t = 0; t < NT; ++t)
-                if (t < na) mma_16816<false>(o[t][c], b, pb[t][sg][0], pb[t][sg][1]);
+                mma_16816<false>(o[t][c], b, pb[t][sg][0], pb[t][sg][1]);
             } else {
               // A transposed fragment holds two columns of two keys: 16c + 2g becomes row g of the operand, 16c + 2g + 1 row g + 8.
               ldsm_x4_t(vt + place(16 * sg + (lane & 15), c + (lane >> 4)), b);
@@ -608,46 +634,52 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
                     e4m3x2_to_f16x2(static_cast<uint16_t>(hi)), e4m3x2_to_f16x2(static_cast<uint16_t>(hi >> 16))};
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                  if (t < na) mma_16816<true>(o[t][c + h], va, pb[t][sg][0], pb[t][sg][1]);
+                  mma_16816<true>(o[t][c + h], va, pb[t][sg][0], pb[t][sg][1]);
               }
             }
           }
         }
       } else {
         // Key by key, and only for the rows that see the key.
-#pragma unroll
-        for (int sg = 0; sg < NG; ++sg)
 #pragma unroll 1
-          for (int i = 0; i < 16; ++i) {
-            const int key = 16 * sg + i;
+        for (int key = 0; key < C::KG; ++key) {
+          // (One copy of this code for all of a group's keys: unrolled it would crowd out what runs often.)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              float pv[2];
+          for (int t = 0; t < NT; ++t) {
+            if (t >= na) continue;
+            uint32_t mine = 0;  // of row 8t + g: keys 2jq, + 1 of the key's eight
 #pragma unroll
-              for (int r = 0; r < 2; ++r)
-                pv[r] = __shfl_sync(0xffffffffu, i >= 8 ? x[t][sg][2 + r] : x[t][sg][r], (i & 7) * 4 + jq);
-              const bool see[2] = {t < na && key0 + key <= lim[t][0], t < na && key0 + key <= lim[t][1]};
+            for (int i = 0; i < 2 * NG; ++i) mine = key >> 3 == i ? pb[t][i >> 1][i & 1] : mine;
+            float pv[2];
+            bool see[2];
 #pragma unroll
-              for (int c = 0; c < C::KS; ++c) {
-                float v[2];  // the columns of o[t][c][0..1] and o[t][c][2..3]
-                if constexpr (!E4M3) {
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t pair = __shfl_sync(0xffffffffu, mine, (2 * jq + r) * 4 + ((key & 7) >> 1));
+              const uint32_t one = key & 1 ? pair >> 16 : pair & 0xffffu;
+              pv[r] = E4M3 ? __half2float(__ushort_as_half(static_cast<uint16_t>(one))) : __uint_as_float(one << 16);
+              see[r] = key0 + key <= sees(8 * t + 2 * jq + r);
+            }
 #pragma unroll
-                  for (int h = 0; h < 2; ++h)
-                    v[h] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vt_g + place(key, 2 * c + h) + 2 * g));
-                } else {
-                  const uint32_t h2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(vt_g + place(key, c) + 2 * g));
-                  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                  v[0] = y.x;
-                  v[1] = y.y;
-                }
+            for (int c = 0; c < C::KS; ++c) {
+              float v[2];  // the columns of o[t][c][0..1] and o[t][c][2..3]
+              if constexpr (!E4M3) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-#pragma unroll
-                  for (int r = 0; r < 2; ++r)
-                    if (see[r]) o[t][c][2 * h + r] = fmaf(pv[r], v[h], o[t][c][2 * h + r]);
+                  v[h] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vt_g + place(key, 2 * c + h) + 2 * g));
+              } else {
+                const uint32_t h2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(vt_g + place(key, c) + 2 * g));
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                v[0] = y.x;
+                v[1] = y.y;
               }
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                  if (see[r]) o[t][c][2 * h + r] = fmaf(pv[r], v[h], o[t][c][2 * h + r]);
             }
           }
+        }
       }
       __syncwarp();  // the stage has been read
       ++done;
@@ -658,34 +690,37 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
     float* join_o = reinterpret_cast<float*>(gbase + C::OFF_JOIN);
     float* join_ml = reinterpret_cast<float*>(gbase + C::OFF_ML);
     const float vf = E4M3 ? scale_of_byte(static_cast<uint32_t>(vexp)) : 1.f;
+#pragma unroll 1
+    for (int t8 = 0; t8 < na; ++t8) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (t >= na) continue;
+      for (int t = 0; t < NT; ++t) {
+        if (t != t8) continue;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 4);
-        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
-        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
-        float* dst = join_o + (warp * 8 + 2 * jq + i) * C::JROW;
+        for (int i = 0; i < 2; ++i) {
+          l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 4);
+          l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
+          l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
+          float* dst = join_o + (warp * 8 + 2 * jq + i) * C::JROW;
 #pragma unroll
-        for (int c = 0; c < C::KS; ++c) {
-          if constexpr (E4M3) {
-            *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) =
-                make_float2(o[t][c][i] * 0x1p-6f * vf, o[t][c][2 + i] * 0x1p-6f * vf);
-          } else {
-            dst[16 * c + g] = o[t][c][i];
-            dst[16 * c + 8 + g] = o[t][c][2 + i];
+          for (int c = 0; c < C::KS; ++c) {
+            if constexpr (E4M3) {
+              *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) =
+                  make_float2(o[t][c][i] * 0x1p-6f * vf, o[t][c][2 + i] * 0x1p-6f * vf);
+            } else {
+              dst[16 * c + g] = o[t][c][i];
+              dst[16 * c + 8 + g] = o[t][c][2 + i];
+            }
           }
-        }
-        if (g == 0) {
-          join_ml[warp * 16 + 2 * jq + i] = m[t][i];
-          join_ml[warp * 16 + 8 + 2 * jq + i] = l[t][i];
+          if (g == 0) {
+            join_ml[warp * 16 + 2 * jq + i] = m[t][i];
+            join_ml[warp * 16 + 8 + 2 * jq + i] = l[t][i];
+          }
         }
       }
       __syncthreads();
 #pragma unroll 1
       for (int r8 = warp; r8 < 8; r8 += C::NW) {
-        const int r = 8 * t + r8;
+        const int r = 8 * t8 + r8;
         if (r >= rows || *abort_flag != 0) break;
         float top = -INFINITY;
 #pragma unroll
@@ -700,7 +735,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(src[32 * c], f, acc[c]);
         }
-        const int row = s.row0 + r / a.group, hq = at.head * a.group + r % a.group;
+        const int tok = token_of(r), row = s.row0 + tok, hq = at.head * a.group + r - tok * a.group;
         const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
         const float lg = top + log2f(lsum);
         if (whole) {
