@@ -505,7 +505,13 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
         }
       }
       uint32_t pb[NT][NG][2];  // P^T as the B operand
-      float top[NT][2];        // this thread's largest logits of its rows (in units of the scaled ones)
+      // This thread's largest logit of row 8t + 2jq + i, scaled.
+      auto largest = [&](int t, int i) -> float {
+        float y = fmaxf(x[t][0][i], x[t][0][2 + i]);
+#pragma unroll
+        for (int sg = 1; sg < NG; ++sg) y = fmax3(y, x[t][sg][i], x[t][sg][2 + i]);
+        return y * rowf[t][i];
+      };
       bool moves = vdown != 1.f;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -518,13 +524,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
               if (key0 + 16 * sg + 8 * (i >> 1) + g > lim[i & 1]) x[t][sg][i] = -INFINITY;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float y = fmaxf(x[t][0][i], x[t][0][2 + i]);
-#pragma unroll
-          for (int sg = 1; sg < NG; ++sg) y = fmax3(y, x[t][sg][i], x[t][sg][2 + i]);
-          top[t][i] = y * rowf[t][i];
-          moves = moves || top[t][i] > m[t][i] + kFewSlack;
-        }
+        for (int i = 0; i < 2; ++i) moves = moves || largest(t, i) > m[t][i] + kFewSlack;
       }
       if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
           float alpha[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float y = top[t][i];
+            float y = largest(t, i);
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
