@@ -9,7 +9,7 @@
 //    3-D TMA box {columns, G heads, tokens}.  A query block is two tiles
 //    (d = 256: one).
 //  * Work.  The key tiles of all (sequence, query block, head) units form one
-//    line, with room for kUnitCost more behind each unit (what its beginning and end
+//    line, with room for UNIT_COST more behind each unit (what its beginning and end
 //    cost), that is cut into equal shares (fa_paged_plan.cuh).  The load warp walks
 //    this CTA's share and hands segments (a run of key tiles of one unit) to
 //    the other warps through a ring in shared memory.
@@ -34,7 +34,6 @@
 namespace fa {
 
 constexpr int kSegRing = 4;
-constexpr int kUnitCost = 2;  // key tiles that a unit costs besides its own (a step takes 3 K cycles, a border 6 to 9 K)
 
 // warp_wait_bar in less code: the kernel has to stay within the SM's instruction cache (about 128 KB; at 150 KB a
 // unit's epilogue, fetched anew each time, took 7000 cycles).
@@ -110,6 +109,7 @@ struct ChunkCfg : TcCfg<D> {
   static constexpr int CONV_WARP0 = T::LOAD_WARP + 1;                  // the last two; the others are the correction warps
   static constexpr int SEG_READERS = T::SOFTMAX_WARPS + 4 + 1 + (E4M3 ? 2 : 0);
   static constexpr int ROWS = T::NQT * 128;
+  static constexpr int UNIT_COST = E4M3 ? (D == 256 ? 2 : 5) : (D == 256 ? 2 : 1);
   static_assert(T::OFF_ABORT + 4 <= OFF_SEG && OFF_SEG % 16 == 0, "misc area");
   static_assert(OFF_SEG + kSegRing * static_cast<int>(sizeof(ChunkSeg)) <= T::OFF_MISC + T::MISC, "misc area");
   static_assert(sizeof(PlanScratch) <= 2048, "plan scratch");
@@ -164,6 +164,7 @@ __host__ __device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t 
 // The query blocks of a sequence (TQ tokens each) and the key tiles they visit.
 struct ChunkBlocks {
   int n, len, tq, bk;
+  int unit;  // key tiles that a unit costs besides its own
   bool causal;
   __host__ __device__ __forceinline__ int count() const { return (n + tq - 1) / tq; }
   // Key tiles of the first `ntok` tokens of block q: those up to the last token's position (one at least).
@@ -177,7 +178,7 @@ struct ChunkBlocks {
   }
   __host__ __device__ __forceinline__ int tokens(int q) const { return n - q * tq < tq ? n - q * tq : tq; }
   // Length on the line of blocks 0 .. k - 1 of one head.
-  __host__ __device__ __forceinline__ long long before(int k) const { return tiles_before(k) + static_cast<long long>(kUnitCost) * k; }
+  __host__ __device__ __forceinline__ long long before(int k) const { return tiles_before(k) + static_cast<long long>(unit) * k; }
   // Their key tiles.
   __host__ __device__ __forceinline__ long long tiles_before(int k) const {
     if (k == 0) return 0;
@@ -192,7 +193,7 @@ struct ChunkBlocks {
   }
 };
 
-template <int D>
+template <int D, bool E4M3>
 __host__ __device__ __forceinline__ ChunkBlocks chunk_blocks(const ChunkParams& p, const PagedSeq& s) {
   ChunkBlocks c;
   const bool mine = s.n >= 1 && s.n <= p.a.max_rows && (s.n > kFewMost || s.n * p.a.group > p.a.few_rows);
@@ -200,6 +201,7 @@ __host__ __device__ __forceinline__ ChunkBlocks chunk_blocks(const ChunkParams& 
   c.len = s.len;
   c.tq = p.tpt * TcCfg<D>::NQT;
   c.bk = TcCfg<D>::BK;
+  c.unit = ChunkCfg<D, E4M3>::UNIT_COST;
   c.causal = p.a.causal;
   return c;
 }
@@ -218,11 +220,11 @@ struct ChunkWalk {
   __host__ __device__ __forceinline__ void load(const ChunkParams& p) {
     bool bad;
     s = paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad);
-    c = chunk_blocks<D>(p, s);
+    c = chunk_blocks<D, E4M3>(p, s);
   }
   // On to the next unit, if the share reaches it.
   __host__ __device__ __forceinline__ void advance(const ChunkParams& p) {
-    pos += nt - j + kUnitCost;
+    pos += nt - j + C::UNIT_COST;
     j = 0;
     if (pos >= end) return;
     if (++head == p.a.kv.heads) {
@@ -370,7 +372,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
       if (q < walk.c.count()) {
         nt = walk.c.tiles(q, walk.c.tokens(q));
         first = p.a.kv.heads * walk.c.before(q);
-        here = first <= share.offset && share.offset < first + static_cast<long long>(p.a.kv.heads) * (nt + kUnitCost);
+        here = first <= share.offset && share.offset < first + static_cast<long long>(p.a.kv.heads) * (nt + C::UNIT_COST);
       }
       const uint32_t who = __ballot_sync(0xffffffffu, here);
       if (who != 0) {
@@ -378,8 +380,8 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
         walk.q = q0 + from;
         walk.nt = __shfl_sync(0xffffffffu, nt, from);
         const long long in = share.offset - __shfl_sync(0xffffffffu, first, from);
-        walk.head = static_cast<int>(in / (walk.nt + kUnitCost));
-        walk.j = static_cast<int>(in - static_cast<long long>(walk.head) * (walk.nt + kUnitCost));
+        walk.head = static_cast<int>(in / (walk.nt + C::UNIT_COST));
+        walk.j = static_cast<int>(in - static_cast<long long>(walk.head) * (walk.nt + C::UNIT_COST));
         if (walk.j >= walk.nt) walk.advance(p);  // behind a unit's tiles: its first tile is the next unit's
         break;
       }
@@ -1209,10 +1211,10 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       p.a.pb.B, gridDim.x, blockIdx.x,
       [&](int b) -> long long {
         bool bad;
-        const ChunkBlocks c = chunk_blocks<D>(p, paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad));
+        const ChunkBlocks c = chunk_blocks<D, E4M3>(p, paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad));
         return c.n == 0 ? 0 : p.a.kv.heads * c.before(c.count());
       },
-      1 + kUnitCost,
+      1 + C::UNIT_COST,
       *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
   tc_fence_before();
   __syncthreads();
