@@ -49,11 +49,25 @@ __device__ __forceinline__ int find_seq(const int* cu_rows, int B, int t, int la
   return lo;
 }
 
+// Two threads hold 64 bytes in a row, the even one the first 32: afterwards the even one has the 16-byte units 0 and 2,
+// the odd one 1 and 3 (and the other way round), so that a warp's accesses are whole 32-byte sectors.
+__device__ __forceinline__ void swap_in_pair(uint4& a, uint4& b, int lane) {
+  const bool odd = lane & 1;
+  uint4 x = odd ? a : b;
+  x.x = __shfl_xor_sync(0xffffffffu, x.x, 1);
+  x.y = __shfl_xor_sync(0xffffffffu, x.y, 1);
+  x.z = __shfl_xor_sync(0xffffffffu, x.z, 1);
+  x.w = __shfl_xor_sync(0xffffffffu, x.w, 1);
+  (odd ? a : b) = x;
+}
+
 template <int D, bool E4M3, bool WRITE>
 __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const MoveArgs a) {
   __shared__ int s_page[kMoveTokens];  // -1: nothing to move
   __shared__ int s_slot[kMoveTokens];
-  constexpr int LPR = D / 16;  // threads a row
+  constexpr int EPT = E4M3 ? 16 : 8;  // elements of a thread's item
+  constexpr int LPR = D / EPT;        // threads a row
+  constexpr int U = E4M3 ? 2 : 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = blockIdx.x * a.tokens_per_block;
   const int nt = min(a.tokens_per_block, a.pb.rows - t0);
@@ -84,41 +98,67 @@ __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const MoveA
     }
   }
   __syncthreads();
+  // Thread x takes items x, x + 256, ... of the block's; item = (token, K or V, head, part of the row).  U items at a
+  // time, their loads before any store.
   const int per_token = 2 * a.kv.heads * LPR;
   const int items = nt * per_token;
-  for (int i0 = 0; i0 < items; i0 += kMoveThreads) {
-    // The threads of a row stay together (LPR divides 32 and `items`).
-    const int item = i0 + static_cast<int>(threadIdx.x);
-    const int i = min(item, items - 1) / per_token;
-    const int r = min(item, items - 1) - i * per_token;
-    const int part = r % LPR;
-    const int h = (r / LPR) % a.kv.heads;
-    const bool is_v = r / LPR >= a.kv.heads;
-    const int page = s_page[i], slot = s_slot[i];
-    const bool active = item < items && page >= 0;
-    const long long* cs = is_v ? a.kv.vs : a.kv.ks;
-    const long long* ts = is_v ? a.vs : a.ks;
-    const long long c_off = active ? page * cs[0] + h * cs[1] + slot * cs[2] + part * 16 : 0;
-    const long long t_off = active ? (t0 + i) * ts[0] + h * ts[1] + part * 16 : 0;
-    const long long s_off = active ? ((static_cast<long long>(page) * a.kv.heads + h) << a.kv.ps_log2) + slot : 0;
-    char* cache = static_cast<char*>(is_v ? a.kv.v : a.kv.k);
-    uint8_t* scales = is_v ? a.kv.v_scale : a.kv.k_scale;
-    if constexpr (WRITE) {
-      uint4 x[2] = {};
-      if (active) {
-        const uint4* src = reinterpret_cast<const uint4*>((is_v ? a.v_in : a.k_in) + t_off);
-        x[0] = src[0];
-        x[1] = src[1];
+  const int step_i = kMoveThreads / per_token, step_r = kMoveThreads % per_token;
+  int i = static_cast<int>(threadIdx.x) / per_token, r = static_cast<int>(threadIdx.x) % per_token;
+  for (int i0 = 0; i0 < items; i0 += U * kMoveThreads) {
+    bool active[U];
+    uint4 x[U][E4M3 ? 2 : 1];
+    char* c_at[U];          // in the cache
+    __nv_bfloat16* t_at[U];  // in the token-major tensor (e4m3: the first of this thread's two places)
+    uint8_t* s_at[U];       // e4m3: the row's scale
+    uint8_t byte[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // (The threads of a row stay together: LPR divides 32 and `items`.)
+      const int page = i < nt ? s_page[i] : -1, slot = i < nt ? s_slot[i] : 0;
+      active[u] = page >= 0;
+      const int part = r % LPR;
+      const bool is_v = r / LPR >= a.kv.heads;
+      const int h = r / LPR - (is_v ? a.kv.heads : 0);
+      const long long* cs = is_v ? a.kv.vs : a.kv.ks;
+      const long long* ts = is_v ? a.vs : a.ks;
+      c_at[u] = static_cast<char*>(is_v ? a.kv.v : a.kv.k) +
+                (page * cs[0] + h * cs[1] + slot * cs[2] + part * EPT) * (E4M3 ? 1 : 2);
+      const __nv_bfloat16* t = WRITE ? (is_v ? a.v_in : a.k_in) : (is_v ? a.v_out : a.k_out);
+      t_at[u] = const_cast<__nv_bfloat16*>(t) + (t0 + i) * ts[0] + h * ts[1] +
+                (E4M3 ? (part & ~1) * EPT + (part & 1) * 8 : part * EPT);
+      if constexpr (E4M3)
+        s_at[u] = (is_v ? a.kv.v_scale : a.kv.k_scale) +
+                  ((static_cast<long long>(page) * a.kv.heads + h) << a.kv.ps_log2) + slot;
+      i += step_i;
+      r += step_r;
+      if (r >= per_token) {
+        r -= per_token;
+        ++i;
       }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      x[u][0] = make_uint4(0, 0, 0, 0);
+      if constexpr (E4M3 && WRITE) x[u][1] = make_uint4(0, 0, 0, 0);
+      if (!active[u]) continue;
       if constexpr (!E4M3) {
-        if (active) {
-          uint4* dst = reinterpret_cast<uint4*>(cache + c_off * 2);
-          dst[0] = x[0];
-          dst[1] = x[1];
-        }
+        x[u][0] = *reinterpret_cast<const uint4*>(WRITE ? reinterpret_cast<const char*>(t_at[u]) : c_at[u]);
+      } else if constexpr (WRITE) {
+        x[u][0] = *reinterpret_cast<const uint4*>(t_at[u]);
+        x[u][1] = *reinterpret_cast<const uint4*>(t_at[u] + 16);
       } else {
+        x[u][0] = *reinterpret_cast<const uint4*>(c_at[u]);
+        byte[u] = *s_at[u];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if constexpr (!E4M3) {
+        if (active[u]) *reinterpret_cast<uint4*>(WRITE ? c_at[u] : reinterpret_cast<char*>(t_at[u])) = x[u][0];
+      } else if constexpr (WRITE) {
+        swap_in_pair(x[u][0], x[u][1], lane);
         // The row's largest magnitude as bits: bf16 magnitudes order as integers (infinities and NaN on top).
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(x[u]);
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
@@ -127,11 +167,11 @@ __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const MoveA
         top = max(top & 0xffffu, top >> 16) << 16;  // as fp32 bits
         const bool fine = top < 0x7f800000u;
         // amax = (1 + f) 2^x: the least e with amax 2^-e <= 448 = 1.75 * 2^8 is x - 8, or x - 7 where 1 + f > 1.75.
-        int byte = static_cast<int>(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-        byte = byte < 0 ? 0 : byte;  // (top < 2^128, so byte <= 247)
-        const float inv = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+        int e = static_cast<int>(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+        e = e < 0 ? 0 : e;  // (top < 2^128, so e <= 247)
+        const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
         // At the largest scale 256 would dequantise to 2^128: codes stop at 240 there.
-        const float most = byte == 247 ? 240.f : 448.f;
+        const float most = e == 247 ? 240.f : 448.f;
         uint32_t c[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -145,22 +185,13 @@ __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const MoveA
           for (int n = 0; n < 4; ++n) y[n] = fminf(fmaxf(y[n], -most), most);
           c[k] = fine ? pack_e4m3x4(y[0], y[1], y[2], y[3]) : 0u;
         }
-        if (active) {
-          *reinterpret_cast<uint4*>(cache + c_off) = make_uint4(c[0], c[1], c[2], c[3]);
-          if (part == 0) scales[s_off] = static_cast<uint8_t>(fine ? byte : 255);
+        if (active[u]) {
+          *reinterpret_cast<uint4*>(c_at[u]) = make_uint4(c[0], c[1], c[2], c[3]);
+          if (lane % LPR == 0) *s_at[u] = static_cast<uint8_t>(fine ? e : 255);
         }
-      }
-    } else if (active) {
-      uint4* dst = reinterpret_cast<uint4*>((is_v ? a.v_out : a.k_out) + t_off);
-      if constexpr (!E4M3) {
-        const uint4* src = reinterpret_cast<const uint4*>(cache + c_off * 2);
-        const uint4 x0 = src[0], x1 = src[1];
-        dst[0] = x0;
-        dst[1] = x1;
       } else {
-        const uint4 x = *reinterpret_cast<const uint4*>(cache + c_off);
-        const float f = scale_of_byte(scales[s_off]);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const float f = active[u] ? scale_of_byte(byte[u]) : 0.f;
+        const uint32_t w[4] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w};
         uint32_t out[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -168,8 +199,12 @@ __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const MoveA
           const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h2));
           out[k] = pack_bf16x2(y.x * f, y.y * f);
         }
-        dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-        dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+        uint4 y0 = make_uint4(out[0], out[1], out[2], out[3]), y1 = make_uint4(out[4], out[5], out[6], out[7]);
+        swap_in_pair(y0, y1, lane);
+        if (active[u]) {
+          *reinterpret_cast<uint4*>(t_at[u]) = y0;
+          *reinterpret_cast<uint4*>(t_at[u] + 16) = y1;
+        }
       }
     }
   }
@@ -189,7 +224,7 @@ template <bool WRITE>
 int launch_move(MoveArgs& a, int d, bool e4m3, const LaunchCtx& ctx) {
   // Tokens a block: enough rows for every thread, more once the blocks
   // outnumber what the SMs hold at once (8 blocks each).
-  const int per_token = 2 * a.kv.heads * (d / 16);
+  const int per_token = 2 * a.kv.heads * (d / (e4m3 ? 16 : 8));
   int tb = (kMoveThreads + per_token - 1) / per_token;
   const int even = a.pb.rows / (ctx.num_sms * 8);
   tb = tb < even ? even : tb;
@@ -241,7 +276,11 @@ __global__ void __launch_bounds__(kMendWarps * 32) fa_paged_mend_kernel(const __
   const PagedFwdArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool any = false;
-  for (int i = lane; i < p.n_odd; i += 32) any = any || p.odd[i] != 0;
+#pragma unroll
+  for (int i = 0; i < kPlanCtas * 4; i += 128) {  // all loads at once: the flags are all that most calls look at
+    const int4 x = i + 4 * lane < p.n_odd ? reinterpret_cast<const int4*>(p.odd)[i / 4 + lane] : make_int4(0, 0, 0, 0);
+    any = any || (x.x | x.y | x.z | x.w) != 0;
+  }
   if (!__any_sync(0xffffffffu, any)) return;
   const long long units = static_cast<long long>(a.pb.rows) * a.q_heads;
   for (long long unit = static_cast<long long>(blockIdx.x) * kMendWarps + warp; unit < units;
