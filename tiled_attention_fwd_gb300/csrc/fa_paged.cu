@@ -389,15 +389,16 @@ int launch_mend(const PagedFwdArgs& a, const LaunchCtx& ctx) {
                 : launch_dependent(fa_paged_mend_kernel<D, false>, dim3(ctas * 4), kMendWarps * 32, 0, ctx.stream, p);
 }
 
-// Sequences of few rows, then the others (unless max_rows says that there are none), then what CTAs left in parts.
+// The chunks (unless max_rows says that there are none), then the sequences of few rows, whose blocks begin on SMs
+// that have done their share of the chunks, then what CTAs left in parts.
 template <int D>
 int launch_fwd_d(PagedFwdArgs& a, const LaunchCtx& ctx) {
   const long long most = static_cast<long long>(a.max_rows) * a.group;
   // 8 or 16 rows where that is all there can be, else 32 (d = 256: 16, a thread's registers hold no more outputs).
   a.few_rows = most <= 8 ? 8 : most <= 16 || D == 256 ? 16 : kFewMost;
   const bool chunks = most > a.few_rows;
-  int e = launch_paged_few<D>(a, ctx);
-  if (e == 0 && chunks) e = launch_paged_chunk<D>(a, ctx);
+  int e = chunks ? launch_paged_chunk<D>(a, ctx) : 0;
+  if (e == 0) e = launch_paged_few<D>(a, chunks, ctx);
   if (e == 0) e = launch_paged_join<D>(a, chunks, ctx);
   if (e == 0 && chunks && a.causal) e = launch_mend<D>(a, ctx);
   return e;

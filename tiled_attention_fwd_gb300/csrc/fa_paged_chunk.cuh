@@ -107,7 +107,11 @@ struct ChunkCfg : TcCfg<D> {
   static constexpr int OFF_PLAN = T::OFF_ALPHA;  // before the roles start
   static constexpr int CONV_WARPS = !E4M3 ? 0 : SELF_RESCALE ? 6 : 2;  // warps that convert e4m3 tiles
   static constexpr int CONV_WARP0 = T::LOAD_WARP + 1;                  // the last two; the others are the correction warps
-  static constexpr int SEG_READERS = T::SOFTMAX_WARPS + 4 + 1 + (E4M3 ? 2 : 0);
+  // d = 256, bf16: a second load warp issues the boxes of the tiles at position 1.  A warp needs about 130 cycles a box,
+  // and tiles of 16-token pages have 32 of them (prompts on pages of 16: 368 us, with one load warp 496; of 64: 346 and
+  // 351).  d = 128 has half as many boxes and loses more at the borders of units (180 and 180 us; pages of 64: 182 and 172).
+  static constexpr int LOADERS = !E4M3 && D == 256 ? 2 : 1;
+  static constexpr int SEG_READERS = T::SOFTMAX_WARPS + 4 + 1 + (E4M3 ? 2 : LOADERS - 1);
   static constexpr int ROWS = T::NQT * 128;
   static constexpr int UNIT_COST = E4M3 ? (D == 256 ? 2 : 5) : (D == 256 ? 2 : 1);
   static_assert(T::OFF_ABORT + 4 <= OFF_SEG && OFF_SEG % 16 == 0, "misc area");
@@ -343,24 +347,99 @@ __device__ __forceinline__ uint32_t chunk_codes(int st, int cb, int i) {
 }
 
 // ------------------------------------------------------------------ load warp
+// What a load warp has issued.
+struct ChunkLoaded {
+  uint32_t issued;    // bit i: stage (e4m3: codes) i has been loaded
+  uint32_t last_par;  // bit i: parity of its latest load
+};
+
+// Every issued copy must land before the CTA may exit.
+template <int D, bool E4M3>
+__device__ __forceinline__ void chunk_drain(const ChunkBars<D, E4M3>& bar, const ChunkLoaded& done, const WaitGuard& g) {
+  for (int i = 0; i < (E4M3 ? 2 : TcCfg<D>::NST); ++i)
+    if (done.issued & (1u << i)) wait_bar_drain(E4M3 ? bar.code_full(i) : bar.kv_full(i), (done.last_par >> i) & 1, g);
+}
+
+// Loads the tiles of the pos-th stage: t0 where bit 0 of `which` is set, t1 where bit 1 is.
+template <int D, bool E4M3>
+__device__ __forceinline__ bool chunk_load_stage(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const ChunkParams& p,
+                                                 const ChunkBars<D, E4M3>& bar, uint32_t base, uint32_t pos, int which,
+                                                 const ChunkTile& t0, const ChunkTile& t1, ChunkLoaded& done,
+                                                 const WaitGuard& g) {
+  using C = ChunkCfg<D, E4M3>;
+  const int lane = threadIdx.x & 31;
+  const uint64_t pol_kv = policy_evict_last();
+  // Boxes of up to `rows` keys from key0 on, one lane each: those that begin before the sequence's end.
+  auto boxes = [&](const ChunkTile& t, int key0, int rows) -> int {
+    const int n = min(rows, t.len - key0);
+    return n <= 0 ? 0 : (n + p.box - 1) >> p.box_log2;
+  };
+  auto page_of = [&](const ChunkTile& t, int key) -> int {
+    const int page = paged_page(p.a.pb, p.a.kv, t.b, key);
+    if (page < 0) atomicOr(p.status, kStatusBadBatch);
+    return page < 0 ? p.a.kv.num_pages : page;  // a coordinate outside the tensor reads as zeros
+  };
+  const int slot_mask = (1 << p.a.kv.ps_log2) - 1;
+  const int st = pos % C::NST, cb = pos & 1;
+  const bool own = E4M3 && !C::IN_PLACE;  // codes have buffers of their own
+  const uint32_t full = E4M3 ? bar.code_full(cb) : bar.kv_full(st);
+  const int n0 = which & 1 ? boxes(t0, t0.key0, C::BK) : 0, n1 = (which & 2) && t1.kind ? boxes(t1, t1.key0, C::BK) : 0;
+  // The pages are looked up while the stage is still being read.
+  const int row = lane << p.box_log2;
+  const int page0 = lane < n0 ? page_of(t0, t0.key0 + row) : 0;
+  const int page1 = lane < n1 ? page_of(t1, t1.key0 + row) : 0;
+  const uint32_t par = own ? (pos >> 1) & 1 : (pos / C::NST) & 1;
+  if (!chunk_wait(own ? bar.code_empty(cb) : bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
+  if (lane == 0) mbar_arrive_expect_tx(full, ((n0 + n1) << p.box_log2) * (E4M3 ? D + 1 : D * 2));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const ChunkTile& t = i == 0 ? t0 : t1;
+    if (lane < (i == 0 ? n0 : n1)) {
+      const int key = t.key0 + row, page = i == 0 ? page0 : page1;
+      const CUtensorMap* tm = t.kind == 1 ? tm_k : tm_v;
+      if constexpr (!E4M3) {
+        const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE + row * C::SWB;
+        for (int r = 0; r < C::NR; ++r)
+          tma_load_4d(dst + r * C::K_REGION, tm, full, r * C::RC, key & slot_mask, t.head, page, pol_kv);
+      } else {
+        const uint32_t dst = base + chunk_codes<D>(st, cb, i) + row * C::CODE_COLS;
+        for (int r = 0; r < D / C::CODE_COLS; ++r)
+          tma_load_4d(dst + r * C::BK * C::CODE_COLS, tm, full, r * C::CODE_COLS, key & slot_mask, t.head, page, pol_kv);
+        // (For a page that is not there any scales do.)
+        const long long pg = page == p.a.kv.num_pages ? 0 : page;
+        bulk_load(base + C::OFF_SCALE + (cb * 2 + i) * C::BK + row,
+                  (t.kind == 1 ? p.a.kv.k_scale : p.a.kv.v_scale) +
+                      (((pg * p.a.kv.heads + t.head) << p.a.kv.ps_log2) + (key & slot_mask)),
+                  p.box, full);
+      }
+    }
+  }
+  const int slot = E4M3 ? cb : st;
+  const uint32_t load_par = E4M3 ? (pos >> 1) & 1 : par;
+  done.issued |= 1u << slot;
+  done.last_par = (done.last_par & ~(1u << slot)) | (load_par << slot);
+  return true;
+}
+
+// The load warp, or the second one (bf16), which reads the segments that the first finds and loads the tiles at
+// position 1.
 template <int D, bool E4M3>
 __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                            const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint32_t base,
-                                           uint8_t* gbase, const PlanShare& share, const WaitGuard& g) {
+                                           uint8_t* gbase, const PlanShare& share, bool second, const WaitGuard& g) {
   using C = ChunkCfg<D, E4M3>;
   const int lane = threadIdx.x & 31;
   const uint64_t pol_q = policy_evict_first();
-  const uint64_t pol_kv = policy_evict_last();
   uint32_t pos = 0;          // stages filled so far
-  uint32_t issued = 0;       // bit i: stage (e4m3: codes) i has been loaded
-  uint32_t last_par = 0;     // bit i: parity of its latest load
+  ChunkLoaded done{0, 0};
   int last_q = -1;           // latest segment whose Q tiles were loaded
   bool recorded = false;
 
   ChunkWalk<D, E4M3> walk;
   walk.pos = share.start;
   walk.end = share.end;
-  if (walk.pos < walk.end) {
+  if (walk.pos < walk.end && !second) {
     walk.b = share.b;
     walk.load(p);
     // The block that holds the share's first place: 32 candidates at a time.
@@ -394,6 +473,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
 
   auto get = [&](int k, ChunkSeg& w) -> bool {
     const int i = k % kSegRing;
+    if (C::LOADERS == 2 && second) return seg_read<D, E4M3>(w, k, gbase, bar, g);
     if (!chunk_wait(bar.seg_empty(i), ((k / kSegRing) & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
     w = walk.next(p);
     if (lane == 0) {
@@ -408,6 +488,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
     return true;
   };
   auto unit = [&](const ChunkSeg& w, int k) -> bool {
+    if (C::LOADERS == 2 && second) return true;
     for (int t = 0; t < C::NQT; ++t) {
       if (!chunk_wait(bar.q_empty(t), (k & 1) ^ 1, g, kStatusTimeoutLoad)) return false;
       if (lane == 0) {
@@ -420,65 +501,14 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
     last_q = k;
     return true;
   };
-  // Boxes of up to `rows` keys from key0 on, one lane each: those that begin before the sequence's end.
-  auto boxes = [&](const ChunkTile& t, int key0, int rows) -> int {
-    const int n = min(rows, t.len - key0);
-    return n <= 0 ? 0 : (n + p.box - 1) >> p.box_log2;
-  };
-  auto page_of = [&](const ChunkTile& t, int key) -> int {
-    const int page = paged_page(p.a.pb, p.a.kv, t.b, key);
-    if (page < 0) atomicOr(p.status, kStatusBadBatch);
-    return page < 0 ? p.a.kv.num_pages : page;  // a coordinate outside the tensor reads as zeros
-  };
-  const int slot_mask = (1 << p.a.kv.ps_log2) - 1;
   auto stage = [&](const ChunkTile& t0, const ChunkTile& t1) -> bool {
-    const int st = pos % C::NST, cb = pos & 1;
-    const bool own = E4M3 && !C::IN_PLACE;  // codes have buffers of their own
-    const uint32_t full = E4M3 ? bar.code_full(cb) : bar.kv_full(st);
-    const int n0 = boxes(t0, t0.key0, C::BK), n1 = t1.kind ? boxes(t1, t1.key0, C::BK) : 0;
-    // The pages are looked up while the stage is still being read.
-    const int row = lane << p.box_log2;
-    const int page0 = lane < n0 ? page_of(t0, t0.key0 + row) : 0;
-    const int page1 = lane < n1 ? page_of(t1, t1.key0 + row) : 0;
-    const uint32_t par = own ? (pos >> 1) & 1 : (pos / C::NST) & 1;
-    if (!chunk_wait(own ? bar.code_empty(cb) : bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
-    if (lane == 0) mbar_arrive_expect_tx(full, ((n0 + n1) << p.box_log2) * (E4M3 ? D + 1 : D * 2));
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const ChunkTile& t = i == 0 ? t0 : t1;
-      if (lane < (i == 0 ? n0 : n1)) {
-        const int key = t.key0 + row, page = i == 0 ? page0 : page1;
-        const CUtensorMap* tm = t.kind == 1 ? tm_k : tm_v;
-        if constexpr (!E4M3) {
-          const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE + row * C::SWB;
-          for (int r = 0; r < C::NR; ++r)
-            tma_load_4d(dst + r * C::K_REGION, tm, full, r * C::RC, key & slot_mask, t.head, page, pol_kv);
-        } else {
-          const uint32_t dst = base + chunk_codes<D>(st, cb, i) + row * C::CODE_COLS;
-          for (int r = 0; r < D / C::CODE_COLS; ++r)
-            tma_load_4d(dst + r * C::BK * C::CODE_COLS, tm, full, r * C::CODE_COLS, key & slot_mask, t.head, page, pol_kv);
-          // (For a page that is not there any scales do.)
-          const long long pg = page == p.a.kv.num_pages ? 0 : page;
-          bulk_load(base + C::OFF_SCALE + (cb * 2 + i) * C::BK + row,
-                    (t.kind == 1 ? p.a.kv.k_scale : p.a.kv.v_scale) +
-                        (((pg * p.a.kv.heads + t.head) << p.a.kv.ps_log2) + (key & slot_mask)),
-                    p.box, full);
-        }
-      }
-    }
-    const int slot = E4M3 ? cb : st;
-    const uint32_t load_par = E4M3 ? (pos >> 1) & 1 : par;
-    issued |= 1u << slot;
-    last_par = (last_par & ~(1u << slot)) | (load_par << slot);
+    if (!chunk_load_stage<D, E4M3>(tm_k, tm_v, p, bar, base, pos, C::LOADERS == 1 ? 3 : second ? 2 : 1, t0, t1, done, g)) return false;
     ++pos;
     return true;
   };
   chunk_stream<D>(get, unit, stage);
-  if (lane == 0 && !recorded) p.ws.chunk_rec[blockIdx.x].b = -1;
-  // Every issued copy must land before the CTA may exit.
-  for (int i = 0; i < (E4M3 ? 2 : C::NST); ++i)
-    if (issued & (1u << i)) wait_bar_drain(E4M3 ? bar.code_full(i) : bar.kv_full(i), (last_par >> i) & 1, g);
+  if (lane == 0 && !recorded && !second) p.ws.chunk_rec[blockIdx.x].b = -1;
+  chunk_drain<D, E4M3>(bar, done, g);
   for (int t = 0; t < C::NQT; ++t)
     if (last_q >= 0) wait_bar_drain(bar.q_full(t), last_q & 1, g);
   __syncwarp();
@@ -1164,15 +1194,14 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::OFF_TMEM_SLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_ABORT);
 
-  pdl_wait();  // the few-row kernel is done with the SM (and what waits for this kernel waits for both)
-  pdl_launch_dependents();
+  pdl_launch_dependents();  // the few-row kernel's blocks take the SMs as this kernel's leave them
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar.q_full(t), 1);
       mbar_init(bar.q_empty(t), 1);
     }
     for (int i = 0; i < C::NST; ++i) {
-      mbar_init(bar.kv_full(i), E4M3 ? C::CONV_WARPS : 1);
+      mbar_init(bar.kv_full(i), E4M3 ? C::CONV_WARPS : C::LOADERS);
       mbar_init(bar.kv_empty(i), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -1230,7 +1259,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     chunk_correction<D, E4M3>(p, &tm_o, bar, base, gbase, tmem, warp & 3, lane, g);
   } else {
     if constexpr (C::SPLIT_REGS) regs_decrease<C::REG_CORR_OTHER - C::reg_corr(false)>();
-    if (warp == C::LOAD_WARP) chunk_load<D, E4M3>(&tm_q, &tm_k, &tm_v, p, bar, base, gbase, share, g);
+    if (warp >= C::LOAD_WARP && warp < C::LOAD_WARP + C::LOADERS)
+      chunk_load<D, E4M3>(&tm_q, &tm_k, &tm_v, p, bar, base, gbase, share, warp > C::LOAD_WARP, g);
     if (warp == C::MMA_WARP) chunk_mma<D, E4M3>(p, bar, base, gbase, tmem, g);
     if constexpr (E4M3)
       if (warp >= C::CONV_WARP0)
@@ -1430,7 +1460,8 @@ int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   if (encode_paged_map(&mk, a.kv.k, E4M3 ? 1 : 2, dims, ks, cols, p.box, 1, swizzle, true) != 0) return -1;
   if (encode_paged_map(&mv, a.kv.v, E4M3 ? 1 : 2, dims, vs, cols, p.box, 1, swizzle, true) != 0) return -1;
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
-  return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_CHUNK, ctx.stream, mq, mk, mv, mo, p);
+  kernel<<<grid, C::THREADS, C::SMEM_CHUNK, ctx.stream>>>(mq, mk, mv, mo, p);
+  return static_cast<int>(cudaGetLastError());
 }
 
 template <int D>

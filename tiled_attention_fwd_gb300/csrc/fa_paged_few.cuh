@@ -773,10 +773,11 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
         break;
       }
   }
+  pdl_wait();  // what waits for this kernel waits for the chunks' kernel before it, too
 }
 
 template <int D, bool E4M3, int NT>
-int launch_paged_few_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
+int launch_paged_few_impl(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx) {
   using C = FewCfg<D, E4M3, NT>;
   auto kernel = fa_paged_few_kernel<D, E4M3, NT>;
   static std::atomic<unsigned long long> allowed{0};
@@ -796,21 +797,22 @@ int launch_paged_few_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   if (encode_paged_map(&mk, a.kv.k, C::EB, dims, ks, C::SWB / C::EB, box, 1, C::SWB, true) != 0) return -1;
   if (encode_paged_map(&mv, a.kv.v, C::EB, dims, vs, C::SWB / C::EB, box, 1, C::SWB, true) != 0) return -1;
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
+  if (behind_chunks) return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM, ctx.stream, mk, mv, p);
   kernel<<<grid, C::THREADS, C::SMEM, ctx.stream>>>(mk, mv, p);
   return static_cast<int>(cudaGetLastError());
 }
 
 template <int D, int NT>
-int launch_paged_few_fmt(const PagedFwdArgs& a, const LaunchCtx& ctx) {
-  return a.e4m3 ? launch_paged_few_impl<D, true, NT>(a, ctx) : launch_paged_few_impl<D, false, NT>(a, ctx);
+int launch_paged_few_fmt(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx) {
+  return a.e4m3 ? launch_paged_few_impl<D, true, NT>(a, behind_chunks, ctx) : launch_paged_few_impl<D, false, NT>(a, behind_chunks, ctx);
 }
 
 template <int D>
-int launch_paged_few(const PagedFwdArgs& a, const LaunchCtx& ctx) {
-  if (a.few_rows <= 8) return launch_paged_few_fmt<D, 1>(a, ctx);
+int launch_paged_few(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx) {
+  if (a.few_rows <= 8) return launch_paged_few_fmt<D, 1>(a, behind_chunks, ctx);
   if constexpr (D <= 128)
-    if (a.few_rows > 16) return launch_paged_few_fmt<D, 4>(a, ctx);
-  return launch_paged_few_fmt<D, 2>(a, ctx);
+    if (a.few_rows > 16) return launch_paged_few_fmt<D, 4>(a, behind_chunks, ctx);
+  return launch_paged_few_fmt<D, 2>(a, behind_chunks, ctx);
 }
 
 }  // namespace fa

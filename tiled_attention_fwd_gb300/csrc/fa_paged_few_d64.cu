@@ -2,5 +2,5 @@
 #include "fa_paged_few.cuh"
 
 namespace fa {
-template int launch_paged_few<64>(const PagedFwdArgs& a, const LaunchCtx& ctx);
+template int launch_paged_few<64>(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx);
 }

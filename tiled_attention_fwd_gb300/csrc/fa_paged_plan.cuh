@@ -149,7 +149,7 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 // Entry points of the attention kernels' translation units; each returns a cudaError_t-like code.
 template <int D>
-int launch_paged_few(const PagedFwdArgs& a, const LaunchCtx& ctx);
+int launch_paged_few(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx);
 template <int D>
 int launch_paged_chunk(const PagedFwdArgs& a, const LaunchCtx& ctx);
 template <int D>
