@@ -456,8 +456,9 @@ def _paged_call(cache, fn, name, *args):
     """fn(*args, stream) with the cache's device current, on its current stream."""
     import torch
 
-    if torch.cuda.current_device() == cache._index:
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    # (torch.cuda.current_device and current_stream look the same up in 3 us, a fifth of a small step.)
+    if torch._C._cuda_getDevice() == cache._index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(cache._index))
     else:
         with torch.cuda.device(cache._index):
             rc = fn(*args, torch.cuda.current_stream().cuda_stream)
