@@ -397,6 +397,7 @@ int launch_fwd_d(PagedFwdArgs& a, const LaunchCtx& ctx) {
   // 8 or 16 rows where that is all there can be, else 32 (d = 256: 16, a thread's registers hold no more outputs).
   a.few_rows = most <= 8 ? 8 : most <= 16 || D == 256 ? 16 : kFewMost;
   const bool chunks = most > a.few_rows;
+  a.few_sets = a.e4m3 && a.few_rows > 16 && static_cast<long long>(a.pb.B) * a.kv.heads >= 2 * ctx.num_sms ? 2 : 1;
   int e = chunks ? launch_paged_chunk<D>(a, ctx) : 0;
   if (e == 0) e = launch_paged_few<D>(a, chunks, ctx);
   if (e == 0) e = launch_paged_join<D>(a, chunks, ctx);

@@ -112,6 +112,7 @@ struct PagedFwdArgs {
   int group;     // query heads per key/value head
   int max_rows;
   int few_rows;  // rows (tokens x group) of a sequence that the few-row kernel takes at most
+  int few_sets;  // its launches (1 or 2)
   float scale;
   bool causal;
   bool e4m3;

@@ -1286,7 +1286,8 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 struct JoinParams {
   PagedFwdArgs a;
   PagedWs ws;
-  bool chunks;  // the chunk kernel has run
+  bool chunks;   // the chunk kernel has run
+  int few_sets;  // launches of the few-row kernel
   int tpt;
 };
 
@@ -1348,72 +1349,75 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
       }
     }
   }
-  const PlanRecord rec = p.ws.few_rec[blockIdx.x];
-  if (rec.b < 0) return;
-  bool bad;
-  const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, rec.b, bad);
-  constexpr size_t stride = 2 * part_floats(kFewMost, D);
-  const float* first = p.ws.few_part + blockIdx.x * stride + stride / 2;
-  const float* rest = first + stride / 2 - stride;
-  const int n = rec.more + 1;
-  // Few parts: a warp to a row.  Many: the four warps share out a row's parts.
-  const bool split = n > 4;
-  const int step = split ? gridDim.y : gridDim.y * 4;
-  for (int r = split ? blockIdx.y : blockIdx.y * 4 + warp; r < s.n * a.group; r += step) {
-    // m: the largest L; l: sum of 2^(L - m).
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, (i == 0 ? first : rest + i * stride)[r]);
+#pragma unroll 1
+  for (int set = 0; set < p.few_sets; ++set) {
+    const PlanRecord rec = p.ws.few_rec[set][blockIdx.x];
+    if (rec.b < 0) continue;
+    bool bad;
+    const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, rec.b, bad);
+    constexpr size_t stride = 2 * part_floats(kFewMost, D);
+    const float* first = p.ws.few_part[set] + blockIdx.x * stride + stride / 2;
+    const float* rest = first + stride / 2 - stride;
+    const int n = rec.more + 1;
+    // Few parts: a warp to a row.  Many: the four warps share out a row's parts.
+    const bool split = n > 4;
+    const int step = split ? gridDim.y : gridDim.y * 4;
+    for (int r = split ? blockIdx.y : blockIdx.y * 4 + warp; r < s.n * a.group; r += step) {
+      // m: the largest L; l: sum of 2^(L - m).
+      float m = -INFINITY;
+      for (int i = lane; i < n; i += 32) m = fmaxf(m, (i == 0 ? first : rest + i * stride)[r]);
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-    float l = 0.f, o[D / 32] = {};
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float w = 0.f;
-      if (i0 + lane < n) {
-        const float x = (i0 + lane == 0 ? first : rest + (i0 + lane) * stride)[r];
-        w = x == -INFINITY ? 0.f : ex2(x - m);
-      }
-      float sum = w;
+      for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+      float l = 0.f, o[D / 32] = {};
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < n) {
+          const float x = (i0 + lane == 0 ? first : rest + (i0 + lane) * stride)[r];
+          w = x == -INFINITY ? 0.f : ex2(x - m);
+        }
+        float sum = w;
 #pragma unroll
-      for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-      l += sum;
-      const int to = min(32, n - i0);
+        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        l += sum;
+        const int to = min(32, n - i0);
 #pragma unroll 4
-      for (int i = split ? warp : 0; i < to; i += split ? 4 : 1) {
-        const float f = __shfl_sync(0xffffffffu, w, i);
-        const float* x = (i0 + i == 0 ? first : rest + (i0 + i) * stride) + kFewMost + static_cast<size_t>(r) * D;
-        if (f != 0.f) {
+        for (int i = split ? warp : 0; i < to; i += split ? 4 : 1) {
+          const float f = __shfl_sync(0xffffffffu, w, i);
+          const float* x = (i0 + i == 0 ? first : rest + (i0 + i) * stride) + kFewMost + static_cast<size_t>(r) * D;
+          if (f != 0.f) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) o[c] = fmaf(x[c * 32 + lane], f, o[c]);
+            for (int c = 0; c < D / 32; ++c) o[c] = fmaf(x[c * 32 + lane], f, o[c]);
+          }
         }
       }
-    }
-    if (split) {
-      if (warp > 0) {
+      if (split) {
+        if (warp > 0) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) s_o[warp - 1][c * 32 + lane] = o[c];
+          for (int c = 0; c < D / 32; ++c) s_o[warp - 1][c * 32 + lane] = o[c];
+        }
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+            o[c] = (o[c] + s_o[0][c * 32 + lane]) + (s_o[1][c * 32 + lane] + s_o[2][c * 32 + lane]);
+        }
+        __syncthreads();
+        if (warp > 0) continue;
       }
-      __syncthreads();
-      if (warp == 0) {
+      const int row = s.row0 + r / a.group, hq = rec.head * a.group + r % a.group;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      __nv_bfloat16* dst = a.o + static_cast<long long>(row) * a.os[0] + static_cast<long long>(hq) * a.os[1];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-          o[c] = (o[c] + s_o[0][c * 32 + lane]) + (s_o[1][c * 32 + lane] + s_o[2][c * 32 + lane]);
-      }
-      __syncthreads();
-      if (warp > 0) continue;
+      for (int c = 0; c < D / 32; ++c) dst[c * 32 + lane] = __float2bfloat16_rn(o[c] * inv);
+      if (lane == 0) a.lse[static_cast<long long>(hq) * a.pb.rows + row] = (m + log2f(l)) * 0.69314718055994531f;
     }
-    const int row = s.row0 + r / a.group, hq = rec.head * a.group + r % a.group;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16* dst = a.o + static_cast<long long>(row) * a.os[0] + static_cast<long long>(hq) * a.os[1];
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) dst[c * 32 + lane] = __float2bfloat16_rn(o[c] * inv);
-    if (lane == 0) a.lse[static_cast<long long>(hq) * a.pb.rows + row] = (m + log2f(l)) * 0.69314718055994531f;
   }
 }
 
 template <int D>
 int launch_paged_join(const PagedFwdArgs& a, bool chunks, const LaunchCtx& ctx) {
   const int ctas = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
-  const JoinParams p{a, paged_ws(a.workspace, D), chunks, 128 / a.group};
+  const JoinParams p{a, paged_ws(a.workspace, D), chunks, a.few_sets, 128 / a.group};
   return launch_dependent(fa_paged_join_kernel<D>, dim3(ctas, 16), 128, 0, ctx.stream, p);
 }
 

@@ -29,6 +29,8 @@
 // one vote of the warp says so.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_paged_plan.cuh"
 
 namespace fa {
@@ -113,24 +115,26 @@ constexpr float kFewSlack = 8.f;  // log2 units by which a logit may exceed the 
 
 struct FewParams {
   PagedFwdArgs a;
-  PagedWs ws;
+  PlanRecord* rec;  // of this launch's units
+  float* part;
   int* status;
   unsigned long long limit_ns;
+  int from, most;  // the launch takes sequences of more than `from` rows and of `most` at most
   int box_log2;  // log2 of the tokens of a K/V box: a page or a group, whichever is smaller
 };
 
 // Tiles of KT keys of one head of sequence b in this kernel (0: not one of its sequences).
 template <int KT>
-__device__ __forceinline__ int few_tiles(const PagedFwdArgs& a, const PagedSeq& s) {
-  if (s.n < 1 || s.n > a.max_rows || s.n > kFewMost || s.n * a.group > a.few_rows) return 0;
+__device__ __forceinline__ int few_tiles(const FewParams& p, const PagedSeq& s) {
+  if (s.n < 1 || s.n > p.a.max_rows || s.n > kFewMost || s.n * p.a.group > p.most || s.n * p.a.group <= p.from) return 0;
   return s.len <= KT ? 1 : (s.len + KT - 1) / KT;  // without keys too: the rows get their zeros
 }
 
 // Length of sequence b's units on the line of work.
 template <int KT>
-__device__ __forceinline__ long long few_length(const PagedFwdArgs& a, const PagedSeq& s) {
-  const int nt = few_tiles<KT>(a, s);
-  return nt == 0 ? 0 : static_cast<long long>(a.kv.heads) * (nt + kFewUnitCost);
+__device__ __forceinline__ long long few_length(const FewParams& p, const PagedSeq& s) {
+  const int nt = few_tiles<KT>(p, s);
+  return nt == 0 ? 0 : static_cast<long long>(p.a.kv.heads) * (nt + kFewUnitCost);
 }
 
 // Walks the tiles of a CTA's share; `left`: what is left of it on the line (0: no more tiles).
@@ -138,37 +142,37 @@ template <int KT>
 struct FewCursor {
   int b, head, j, nt, left;
   PagedSeq s;
-  __device__ __forceinline__ void load(const PagedFwdArgs& a) {
+  __device__ __forceinline__ void load(const FewParams& p) {
     bool bad;
-    s = paged_seq(a.pb, a.kv.ps_log2, b, bad);
-    nt = few_tiles<KT>(a, s);
+    s = paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad);
+    nt = few_tiles<KT>(p, s);
   }
-  __device__ __forceinline__ void start(const PagedFwdArgs& a, const PlanShare& p) {
-    left = static_cast<int>(p.end - p.start);  // (W / 152 tiles: W < 2^38)
-    b = p.b;
+  __device__ __forceinline__ void start(const FewParams& p, const PlanShare& w) {
+    left = static_cast<int>(w.end - w.start);  // (W / 152 tiles: W < 2^38)
+    b = w.b;
     if (left == 0) return;
-    load(a);
-    head = static_cast<int>(p.offset / (nt + kFewUnitCost));
-    j = static_cast<int>(p.offset - static_cast<long long>(head) * (nt + kFewUnitCost));
+    load(p);
+    head = static_cast<int>(w.offset / (nt + kFewUnitCost));
+    j = static_cast<int>(w.offset - static_cast<long long>(head) * (nt + kFewUnitCost));
     if (j >= nt) {  // behind a unit's tiles (a share is longer than that)
       left += j - nt;
       j = nt;
-      advance(a, 0);
+      advance(p, 0);
     }
   }
   // Move on by k tiles of the present unit.
-  __device__ __forceinline__ void advance(const PagedFwdArgs& a, int k) {
+  __device__ __forceinline__ void advance(const FewParams& p, int k) {
     left -= k;
     j += k;
     if (j < nt) return;
     left = max(left - kFewUnitCost, 0);
     if (left == 0) return;
     j = 0;
-    if (++head < a.kv.heads) return;
+    if (++head < p.a.kv.heads) return;
     head = 0;
     do {
       ++b;
-      load(a);
+      load(p);
     } while (nt == 0);
   }
 };
@@ -212,20 +216,20 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
       a.pb.B, gridDim.x, blockIdx.x,
       [&](int b) -> long long {
         bool bad;
-        return few_length<C::KT>(a, paged_seq(a.pb, a.kv.ps_log2, b, bad));
+        return few_length<C::KT>(p, paged_seq(a.pb, a.kv.ps_log2, b, bad));
       },
       1 + kFewUnitCost,
       *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
 
   // ---- the warp's loads
   FewCursor<C::KT> ahead;  // next group to load
-  ahead.start(a, share);
+  ahead.start(p, share);
   uint32_t issued = 0, done = 0;
   const uint64_t policy = policy_evict_first();  // a unit's K and V are read once
   const int box_log2 = p.box_log2;
   const int slot_mask = (1 << a.kv.ps_log2) - 1;
   auto issue = [&]() {
-    while (ahead.left > 0 && ahead.j * C::KT + warp * C::KG >= ahead.s.len) ahead.advance(a, 1);
+    while (ahead.left > 0 && ahead.j * C::KT + warp * C::KG >= ahead.s.len) ahead.advance(p, 1);
     if (ahead.left == 0) return;
     const int key0 = ahead.j * C::KT + warp * C::KG;
     const uint32_t st = issued % C::S;
@@ -253,14 +257,14 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
       }
     }
     ++issued;
-    ahead.advance(a, 1);
+    ahead.advance(p, 1);
   };
 #pragma unroll 1
   for (int i = 0; i < C::S; ++i) issue();
 
   // ---- units
   FewCursor<C::KT> at;
-  at.start(a, share);
+  at.start(p, share);
   bool ok = true;
   bool recorded = false;
   const float scale_log2 = a.scale * 1.4426950408889634f;
@@ -744,7 +748,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
           for (int c = 0; c < D / 32; ++c) dst[32 * c] = __float2bfloat16_rn(acc[c] * inv);
           if (lane == 0) a.lse[static_cast<long long>(hq) * a.pb.rows + row] = lg * 0.69314718055994531f;
         } else {
-          float* part = p.ws.few_part + (blockIdx.x * 2 + (j0 == 0 ? 1 : 0)) * part_floats(kFewMost, D);
+          float* part = p.part + (blockIdx.x * 2 + (j0 == 0 ? 1 : 0)) * part_floats(kFewMost, D);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) part[kFewMost + r * D + 32 * c + lane] = acc[c] * inv;
           if (lane == 0) part[r] = lg;
@@ -755,14 +759,14 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
     if (!whole && j0 == 0) {
       if (threadIdx.x == 0) {
         const long long last = share.end - at.left + at.nt - 1;  // the unit's last tile
-        p.ws.few_rec[blockIdx.x] =
+        p.rec[blockIdx.x] =
             PlanRecord{at.b, at.head, 0, plan_cta_of(last, share.total, share.ctas) - static_cast<int>(blockIdx.x)};
       }
       recorded = true;
     }
-    at.advance(a, j1 - j0);
+    at.advance(p, j1 - j0);
   }
-  if (threadIdx.x == 0 && !recorded) p.ws.few_rec[blockIdx.x].b = -1;
+  if (threadIdx.x == 0 && !recorded) p.rec[blockIdx.x].b = -1;
   // After a wait that gave up, what was loaded must land before the CTA leaves.
   for (; done < issued; ++done) {
     const uint32_t bar = bars + 8 * (done % C::S);
@@ -777,7 +781,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
 }
 
 template <int D, bool E4M3, int NT>
-int launch_paged_few_impl(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx) {
+int launch_paged_few_impl(const PagedFwdArgs& a, int set, int from, int most, bool behind, const LaunchCtx& ctx) {
   using C = FewCfg<D, E4M3, NT>;
   auto kernel = fa_paged_few_kernel<D, E4M3, NT>;
   static std::atomic<unsigned long long> allowed{0};
@@ -785,7 +789,11 @@ int launch_paged_few_impl(const PagedFwdArgs& a, bool behind_chunks, const Launc
   if (e != 0) return e;
   FewParams p;
   p.a = a;
-  p.ws = paged_ws(a.workspace, D);
+  const PagedWs ws = paged_ws(a.workspace, D);
+  p.rec = ws.few_rec[set];
+  p.part = ws.few_part[set];
+  p.from = from;
+  p.most = most;
   p.status = ctx.status;
   p.limit_ns = ctx.limit_ns;
   const int box = (1 << a.kv.ps_log2) < C::KG ? 1 << a.kv.ps_log2 : C::KG;
@@ -797,22 +805,32 @@ int launch_paged_few_impl(const PagedFwdArgs& a, bool behind_chunks, const Launc
   if (encode_paged_map(&mk, a.kv.k, C::EB, dims, ks, C::SWB / C::EB, box, 1, C::SWB, true) != 0) return -1;
   if (encode_paged_map(&mv, a.kv.v, C::EB, dims, vs, C::SWB / C::EB, box, 1, C::SWB, true) != 0) return -1;
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
-  if (behind_chunks) return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM, ctx.stream, mk, mv, p);
+  if (behind) return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM, ctx.stream, mk, mv, p);
   kernel<<<grid, C::THREADS, C::SMEM, ctx.stream>>>(mk, mv, p);
   return static_cast<int>(cudaGetLastError());
 }
 
-template <int D, int NT>
-int launch_paged_few_fmt(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx) {
-  return a.e4m3 ? launch_paged_few_impl<D, true, NT>(a, behind_chunks, ctx) : launch_paged_few_impl<D, false, NT>(a, behind_chunks, ctx);
-}
-
+// Row tiles cost nothing while reading K and V bounds the kernel (bf16: 1.4 us a tile of 128 keys with 1, 2 or 4), but
+// with e4m3 pages they do (256 keys, d = 128: 1.4, 1.65 and 2.7 us), so sequences of more than 16 rows are a launch of
+// their own there, if there is work enough for two (2 to 8 tokens of 4 heads over 4.5 K: 40 sequences of 8 key/value
+// heads 127 us and in one launch 139; 4 sequences 43 and 34).
 template <int D>
 int launch_paged_few(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx) {
-  if (a.few_rows <= 8) return launch_paged_few_fmt<D, 1>(a, behind_chunks, ctx);
-  if constexpr (D <= 128)
-    if (a.few_rows > 16) return launch_paged_few_fmt<D, 4>(a, behind_chunks, ctx);
-  return launch_paged_few_fmt<D, 2>(a, behind_chunks, ctx);
+  auto launch = [&](auto nt, int set, int from, int most, bool behind) -> int {
+    constexpr int NT = decltype(nt)::value;
+    return a.e4m3 ? launch_paged_few_impl<D, true, NT>(a, set, from, most, behind, ctx)
+                  : launch_paged_few_impl<D, false, NT>(a, set, from, most, behind, ctx);
+  };
+  using std::integral_constant;
+  if (a.few_rows <= 8) return launch(integral_constant<int, 1>{}, 0, 0, 8, behind_chunks);
+  if constexpr (D <= 128) {
+    if (a.few_rows > 16) {
+      const int e = launch(integral_constant<int, 4>{}, 0, a.few_sets == 2 ? 16 : 0, kFewMost, behind_chunks);
+      if (e != 0 || a.few_sets == 1) return e;
+      return launch(integral_constant<int, 2>{}, 1, 0, 16, true);
+    }
+  }
+  return launch(integral_constant<int, 2>{}, 0, 0, 16, behind_chunks);
 }
 
 }  // namespace fa

@@ -111,11 +111,11 @@ struct alignas(16) PlanRecord {
 // Workspace of fa_paged_fwd.  A part holds a row's log2-sum-exp2 L (log2 units of the scaled logits) and its
 // normalised O in fp32; parts join as O = sum 2^(L_i - L) O_i, L = log2 sum 2^L_i.
 struct PagedWs {
-  PlanRecord* few_rec;    // [kPlanCtas]
-  PlanRecord* chunk_rec;  // [kPlanCtas]
-  int* odd;               // [kPlanCtas][4]: a correction warp of the chunk kernel met an infinity or a NaN in O
-  float* few_part;        // [kPlanCtas][2][part_floats(kFewMost, d)]
-  float* chunk_part;      // [kPlanCtas][2][part_floats(chunk_rows(d), d)]
+  PlanRecord* few_rec[2];  // of the one or two launches of the few-row kernel: [kPlanCtas]
+  PlanRecord* chunk_rec;   // [kPlanCtas]
+  int* odd;                // [kPlanCtas][4]: a correction warp of the chunk kernel met an infinity or a NaN in O
+  float* few_part[2];      // [kPlanCtas][2][part_floats(kFewMost, d)]
+  float* chunk_part;       // [kPlanCtas][2][part_floats(chunk_rows(d), d)]
 };
 constexpr int kFewMost = 32;  // rows of a unit of the few-row kernel at most
 constexpr __host__ __device__ int chunk_rows(int d) { return d <= 128 ? 256 : 128; }  // of a query block
@@ -128,10 +128,11 @@ inline size_t paged_ws_layout(char* p, int d, PagedWs* w) {
     return x;
   };
   PagedWs x;
-  x.few_rec = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
+  for (int i = 0; i < 2; ++i) x.few_rec[i] = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
   x.chunk_rec = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
   x.odd = reinterpret_cast<int*>(take(kPlanCtas * 4 * sizeof(int)));
-  x.few_part = reinterpret_cast<float*>(take(kPlanCtas * 2 * part_floats(kFewMost, d) * sizeof(float)));
+  for (int i = 0; i < 2; ++i)
+    x.few_part[i] = reinterpret_cast<float*>(take(kPlanCtas * 2 * part_floats(kFewMost, d) * sizeof(float)));
   x.chunk_part = reinterpret_cast<float*>(take(kPlanCtas * 2 * part_floats(chunk_rows(d), d) * sizeof(float)));
   if (w) *w = x;
   return at;
