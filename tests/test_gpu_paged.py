@@ -151,6 +151,21 @@ def test_many_units_on_every_sm(fmt, d, most):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("most", [8, 40])
+def test_drafts_of_many_sequences(fmt, d, most):
+    """Sequences of 0 to 32 rows (e4m3: those of more than 16 are a launch of their own), alone and beside chunks."""
+    rng = np.random.default_rng(d + most)
+    B = 160
+    lens = [int(n) for n in rng.integers(0, 90, B)]
+    rows = [int(min(n, r)) for n, r in zip(lens, rng.integers(0, 9, B))]
+    if most > 8:
+        rows[::20] = [min(n, most) for n in lens[::20]]
+    s = Setup(lens, rows, heads=2, group=4, d=d, page=16, fmt=fmt, seed=most, pad=2)
+    check(s, *run(s), d ** -0.5, True)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("rows", [1, 4, 200])
 def test_long_sequences_are_split_and_joined(fmt, rows):
     s = Setup([9001, 4097], [rows, 1], heads=1, group=1, d=128, page=64, fmt=fmt, seed=rows)
@@ -327,6 +342,40 @@ def test_captured_step_replays_with_new_contents(fmt):
                                                lens.tolist(), d ** -0.5, True)
         assert (np.abs(o.cpu().double().numpy() - o_ref) <= 2.0 ** -7 * (absum + np.abs(o_ref))).all()
         assert np.abs(lse.cpu().double().numpy() - l_ref).max() <= 1e-5
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_captured_mixed_batch_replays_with_new_lengths(fmt):
+    """A graph of one call over a chunk, drafts and single tokens (every kernel of the attention), replayed with other
+    rows to a sequence: what is a chunk in one replay is a single token in another."""
+    heads, group, d, page, T, B = 2, 4, 64, 16, 120, 6
+    s = Setup([400, 333, 290, 129, 257, 64], [20] * B, heads=heads, group=group, d=d, page=page, fmt=fmt, seed=12)
+    cache = s.cache()
+    table, cu, lens = s.batch()
+    q = s.tokens()[0]
+    o, lse = torch.full_like(q, 7.0), torch.full((heads * group, T), 7.0, device="cuda")
+    ws = fa.paged_workspace(cache, B)
+
+    def call():
+        fa.paged_forward(q, cache, table, cu, lens, max_rows=110, out=o, lse=lse, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for rows in ([1, 8, 2, 100, 0, 6], [70, 1, 1, 1, 1, 1], [1, 5, 8, 4, 3, 1], [9, 9, 9, 9, 9, 64]):
+        s.rows, s.cu = rows, np.concatenate([[0], np.cumsum(rows)])
+        cu.copy_(torch.tensor(s.cu, dtype=torch.int32))
+        o.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        graph.replay()
+        fa.check_status()
+        check(s, o, lse, d ** -0.5, True)
 
 
 def test_two_streams_with_workspaces_of_their_own():

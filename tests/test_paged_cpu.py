@@ -134,3 +134,24 @@ def test_paged_attention_takes_pages_heads_and_positions_apart():
             e = [math.exp(0.3 * float(x @ q[row, h])) for x in k]
             assert abs(lse[h, row] - math.log(sum(e))) < 1e-12
             assert np.abs(o[row, h] - sum(a * x for a, x in zip(e, v)) / sum(e)).max() < 1e-12
+
+
+def test_paged_kernels_fit_their_registers():
+    """The chunk kernels' register split (d <= 128) is sized for exactly 128 a thread at launch; the few-row and the
+    moving kernels keep their state in registers."""
+    from tiled_attention_fwd_gb300 import build
+
+    rep = build.ptxas_report({"fa_paged.cu"} | {f"fa_paged_{k}_d{d}.cu" for k in ("few", "chunk") for d in (32, 64, 128, 256)})
+    chunk = {k: r for k, r in rep.items() if "fa_paged_chunk_kernel" in k}
+    few = {k: r for k, r in rep.items() if "fa_paged_few_kernel" in k}
+    move = {k: r for k, r in rep.items() if "fa_paged_move_kernel" in k}
+    # 4 head dimensions x bf16 / e4m3 (x 1, 2 or 4 row tiles, 4 at d <= 128; x write / read)
+    assert (len(chunk), len(few), len(move)) == (8, 22, 16)
+    for name, r in chunk.items():
+        if "ILi256E" in name:
+            assert r["registers"] <= 168, (name, r)  # 384 threads, not re-split
+        else:
+            assert r["registers"] == 128, (name, r)
+    for name, r in {**few, **move}.items():
+        # Four row tiles of e4m3 at d = 128 need a few registers more than there are (outside the products).
+        assert r["spill_stores"] <= (64 if "ILi128ELb1ELi4E" in name else 0), (name, r)
