@@ -10,13 +10,15 @@ namespace fa {
 namespace {
 
 // ------------------------------------------------------------------ moving rows
-// One block moves TB tokens: first a warp per token finds its sequence, page
-// and slot, then every thread takes 16 elements of a row (one token, one head,
-// K or V) at a time, d / 16 threads a row, so a warp's accesses are whole
+// One block moves a few tokens: first a warp per token finds its sequence, page
+// and slot, then every thread takes 8 elements (e4m3: 16) of a row (one token, one head,
+// K or V) at a time, several rows in flight, so a warp's accesses are whole
 // 128-byte lines on both sides.
 //
 // Bound by memory: a row is read once and written once (2d bytes on the
-// token side, 2d or d + 1 on the cache's).
+// token side, 2d or d + 1 on the cache's).  Measured, 8 heads, d = 128: whole
+// prefixes read at 6.0 TB/s (bf16) and 5.9 TB/s (e4m3), 0.88 and 0.87 of a copy's
+// rate; prompts written at 6.0 TB/s (bf16) and 4.5 TB/s (e4m3, 0.67).
 struct MoveArgs {
   PagedKv kv;
   PagedBatch pb;

@@ -10,11 +10,14 @@
 //    load S groups ahead, across the borders of units; no barrier between
 //    warps but where a unit ends;
 //  * products by mma.sync m16n8k16 with the rows as N, 8 to a tile: S^T = K Q^T and
-//    O^T = V^T P^T, so that 8 rows cost half of what 16 do (mma.sync measured 8
-//    cycles a 16x8x16 product and SM on this GPU, which would bound e4m3 pages with the
-//    rows as a padded M of 16; a tcgen05 tile of 128 rows would multiply mostly
+//    O^T = V^T P^T, so that 8 rows cost half of what 16 do (mma.sync measured 2
+//    cycles a 16x8x16 product and SM on this GPU; with two warps a scheduler what
+//    bounds e4m3 pages is the instructions of a warp and their latencies, and a
+//    padded M of 16 has twice the logits; a tcgen05 tile of 128 rows would multiply mostly
 //    padding, and its softmax would cost 128 rows); the row tiles share every K and
-//    V fragment;
+//    V fragment, and every row tile is computed whether it holds rows or not (with a
+//    branch each the compiler cannot interleave them: e4m3, 4 tiles, 3.2 us a tile of
+//    256 keys instead of 2.7);
 //  * softmax state m, l and the output stay in registers; at a unit's end the
 //    warps' results are joined in shared memory, in the warps' order.
 // e4m3 pages: codes are exact in fp16, so S = Q K^T runs in fp16 with the codes
@@ -27,6 +30,10 @@
 // The reference maximum m moves only when a logit exceeds it by more than 8 (log2
 // units), so p <= 2^8 and most groups need neither the rows' maxima nor a rescale:
 // one vote of the warp says so.
+//
+// Measured: single tokens of 64 sequences, 1.24 GB of bf16 pages, d = 128: 188 us, 6.6 TB/s (0.97 of a copy's rate);
+// 1.12 GB of e4m3 pages 181 us, 6.2 TB/s; 2 to 8 drafted tokens of 4 heads over 376 MB of e4m3 pages 128 us, 2.9 TB/s
+// (issue slots 37 % used with two warps a scheduler, tensor pipe 30 %: latencies).
 #pragma once
 
 #include <type_traits>
