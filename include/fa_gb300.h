@@ -327,7 +327,7 @@ typedef struct fa_paged_batch {
   const int* cu_rows;       /* device, [B + 1], cu_rows[0] >= 0, not decreasing                      */
   const int* kv_lens;       /* device, [B], >= 0                                                     */
   long long table_stride;
-  int max_pages;            /* entries of a row of page_table, >= 1                                  */
+  int max_pages;            /* entries of a row of page_table, >= 1, times page_size <= 2^31 - 4096  */
   int B;                    /* sequences, >= 1                                                       */
   int rows;                 /* rows of the token-major tensors, >= 0 (0: nothing is done)            */
 } fa_paged_batch;
@@ -337,7 +337,7 @@ typedef struct fa_paged_batch {
  * finds them (quantised for e4m3 pages).  A row of e4m3 pages that holds an
  * infinity or a NaN is stored as scale 255 and reads back as NaN throughout; a
  * row of zeros has scale 0.  Two rows of one call must not name the same slot
- * (else which of them is left, for each 32 bytes, is unspecified).
+ * (else which of them is left, for each 16 bytes, is unspecified).
  *
  *   k, v      : bf16, element (row, h, c) at row*s[0] + h*s[1] + c, s = k_stride /
  *               v_stride: {row, head} element strides, multiples of 8; 16-byte aligned.

@@ -155,3 +155,11 @@ def test_paged_kernels_fit_their_registers():
     for name, r in {**few, **move}.items():
         # Four row tiles of e4m3 at d = 128 need a few registers more than there are (outside the products).
         assert r["spill_stores"] <= (64 if "ILi128ELb1ELi4E" in name else 0), (name, r)
+
+
+@pytest.mark.parametrize("page_size", [16, 1024])
+def test_positions_that_would_pass_32_bits_are_refused(page_size):
+    n = 0x7ffff000 // page_size + 1
+    c, b = cache(page_size=page_size), batch(max_pages=n, table_stride=n)
+    assert fa.fa_paged_write(c, b, FAKE, (256, 64), FAKE, (256, 64), None) == -2
+    assert fa.fa_paged_fwd(FAKE, (512, 64), c, b, FAKE, (512, 64), FAKE, 8, 1, 0.1, 1, FAKE, 1 << 40, None) == -2

@@ -430,8 +430,8 @@ int take(const fa_paged_cache* c, const fa_paged_batch* b, PagedKv* kv, PagedBat
   if ((1 << log2) != c->page_size) return FA_ERR_BAD_SHAPE;
   if (b->B < 1 || b->rows < 0 || b->max_pages < 1 || b->table_stride < b->max_pages) return FA_ERR_BAD_SHAPE;
   if (c->d != 32 && c->d != 64 && c->d != 128 && c->d != 256) return FA_ERR_UNSUPPORTED_D;
-  // Positions are 32-bit.
-  if ((static_cast<long long>(b->max_pages) << log2) > 0x7fffff00LL) return FA_ERR_BAD_SHAPE;
+  // Positions are 32-bit, those at the end of a tile (512 keys at most) and of the batch of tiles behind it, too.
+  if ((static_cast<long long>(b->max_pages) << log2) > 0x7ffff000LL) return FA_ERR_BAD_SHAPE;
   const int eb = *e4m3 ? 1 : 2;
   int rc = check_strides(c->k_stride, 3, eb);
   if (rc == FA_OK) rc = check_strides(c->v_stride, 3, eb);
