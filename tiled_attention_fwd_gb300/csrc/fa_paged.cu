@@ -16,9 +16,9 @@ namespace {
 // 128-byte lines on both sides.
 //
 // Bound by memory: a row is read once and written once (2d bytes on the
-// token side, 2d or d + 1 on the cache's).  Measured, 8 heads, d = 128: whole
-// prefixes read at 6.0 TB/s (bf16) and 5.9 TB/s (e4m3), 0.88 and 0.87 of a copy's
-// rate; prompts written at 6.0 TB/s (bf16) and 4.5 TB/s (e4m3, 0.67).
+// token side, 2d or d + 1 on the cache's).  Measured: prefixes of
+// 350 MB read at 6.1 TB/s (bf16, 8 heads, d = 128) and 6.0 TB/s (e4m3, 16 heads, d = 64),
+// 0.9 of a copy's rate; prompts written at 6.0 TB/s (bf16) and 4.6 TB/s (e4m3, 0.68).
 struct MoveArgs {
   PagedKv kv;
   PagedBatch pb;

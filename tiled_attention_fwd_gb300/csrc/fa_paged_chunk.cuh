@@ -28,7 +28,7 @@
 // Bound by the tensor cores and the softmax as the contiguous forward is (1.55 us a step of 256 rows and 128 keys at
 // d = 128), at short lengths by the units' borders (about 2.5 us each), with e4m3 pages by a stage's way through loading,
 // converting and multiplying (2.5 us a step, 5 us or more a border).  Measured at d = 128: chunks of 541 to 2048 tokens
-// over 7 to 16 K, bf16, 474 GFLOP: 332 us, 1.43 PFLOP/s; 65 to 1024 tokens over 1.7 to 8 K, e4m3, 210 GFLOP: 288 us;
+// over 7 to 16 K, bf16, 474 GFLOP: 332 us, 1.43 PFLOP/s (353 in a long run at full power); 65 to 1024 tokens over 1.7 to 8 K, e4m3, 210 GFLOP: 288 us;
 // prompts of 1.7 to 4 K tokens, 161 GFLOP: 180 us.  Of a call's time about 12 us are the joining kernel (40 MB of parts
 // through L2) and 2 us the mending kernel's look at its flags.
 #pragma once
