@@ -378,8 +378,9 @@ size_t fa_paged_fwd_workspace_bytes(int B, int heads, int d);
  *   reach it, whatever they hold (NaN and infinities too), nor do slots behind kv_lens[b].
  *   o and lse must not overlap each other, q or the cache.
  *
- * Arithmetic: fp32 softmax state and sums; bf16 products with fp32 accumulation (e4m3 pages: see
- * the kernels); o rounded to bf16 once at the end.  Results do not depend on what else runs:
+ * Arithmetic: fp32 softmax state and sums; bf16 products with fp32 accumulation (e4m3 pages with
+ * few rows: fp16 products, in which a value's weight times its scale counts as 0 below 2^-31 of
+ * the row's largest); o rounded to bf16 once at the end.  Results do not depend on what else runs:
  * no atomics, and partial results are joined in a fixed order.
  */
 int fa_paged_fwd(const void* q, const long long* q_stride, const fa_paged_cache* cache, const fa_paged_batch* batch,

@@ -78,6 +78,10 @@ struct FewCfg {
   static_assert(OFF_ABORT + 16 - OFF_ML <= MISC && SMEM <= 227 * 1024, "shared memory budget");
   static_assert(S >= 2 && OFF_SCALE % 16 == 0 && OFF_BAR % 8 == 0 && OFF_PLAN % 8 == 0, "layout");
   static_assert(NT == 1 || NT == 2 || (NT == 4 && D <= 128), "row tiles");
+  // Pages looked up a group ahead: where a warp's instructions are the bound, not memory (e4m3, single tokens of 128
+  // sequences, d = 128: 178 us instead of 183, d = 64: 123 and 137; bf16 the same within 1 %; four row tiles have no
+  // registers left).
+  static constexpr bool EARLY = E4M3 && NT <= 2 && D <= 128;
   static constexpr int KS = D / 16;                       // K steps of S^T = 16-column tiles of O^T
 };
 
@@ -235,8 +239,18 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
   const uint64_t policy = policy_evict_first();  // a unit's K and V are read once
   const int box_log2 = p.box_log2;
   const int slot_mask = (1 << a.kv.ps_log2) - 1;
-  auto issue = [&]() {
+  // The next group with keys; where EARLY, its page's number is on its way until the group is issued.
+  int next_page = -1;
+  auto find = [&]() {
     while (ahead.left > 0 && ahead.j * C::KT + warp * C::KG >= ahead.s.len) ahead.advance(p, 1);
+    if constexpr (C::EARLY) {
+      const int key = ahead.j * C::KT + warp * C::KG + ((lane >> 1) << box_log2);  // lanes 2i and 2i + 1: box i
+      if (ahead.left > 0 && lane < 2 * NG && key < ahead.s.len)
+        next_page = a.pb.page_table[ahead.b * a.pb.table_stride + (key >> a.kv.ps_log2)];
+    }
+  };
+  auto issue = [&]() {
+    if constexpr (!C::EARLY) find();
     if (ahead.left == 0) return;
     const int key0 = ahead.j * C::KT + warp * C::KG;
     const uint32_t st = issued % C::S;
@@ -247,7 +261,8 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
     __syncwarp();
     if (lane < 2 * nbox) {
       const int is_v = lane & 1, row = (lane >> 1) << box_log2;
-      const int page = paged_page(a.pb, a.kv, ahead.b, key0 + row);
+      int page = next_page >= 0 && next_page < a.kv.num_pages ? next_page : -1;
+      if constexpr (!C::EARLY) page = paged_page(a.pb, a.kv, ahead.b, key0 + row);
       const int slot = (key0 + row) & slot_mask;
       if (page < 0) atomicOr(p.status, kStatusBadBatch);
       // A page that is not there reads as zeros (a coordinate outside the tensor).
@@ -265,7 +280,9 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
     }
     ++issued;
     ahead.advance(p, 1);
+    if constexpr (C::EARLY) find();
   };
+  if constexpr (C::EARLY) find();
 #pragma unroll 1
   for (int i = 0; i < C::S; ++i) issue();
 
