@@ -32,7 +32,7 @@
 // one vote of the warp says so.
 //
 // Measured: single tokens of 64 sequences, 1.24 GB of bf16 pages, d = 128: 188 us, 6.6 TB/s (0.97 of a copy's rate);
-// 1.12 GB of e4m3 pages 181 us, 6.2 TB/s; 2 to 8 drafted tokens of 4 heads over 376 MB of e4m3 pages 128 us, 2.9 TB/s
+// 1.12 GB of e4m3 pages 174 us, 6.4 TB/s; 2 to 8 drafted tokens of 4 heads over 376 MB of e4m3 pages 122 us, 3.1 TB/s
 // (issue slots 37 % used with two warps a scheduler, tensor pipe 30 %: latencies).
 #pragma once
 
@@ -79,7 +79,7 @@ struct FewCfg {
   static_assert(S >= 2 && OFF_SCALE % 16 == 0 && OFF_BAR % 8 == 0 && OFF_PLAN % 8 == 0, "layout");
   static_assert(NT == 1 || NT == 2 || (NT == 4 && D <= 128), "row tiles");
   // Pages looked up a group ahead: where a warp's instructions are the bound, not memory (e4m3, single tokens of 128
-  // sequences, d = 128: 178 us instead of 183, d = 64: 123 and 137; bf16 the same within 1 %; four row tiles have no
+  // sequences, d = 128: 178 us instead of 183, d = 64: 122 and 138; bf16 and d = 256 the same; four row tiles have no
   // registers left).
   static constexpr bool EARLY = E4M3 && NT <= 2 && D <= 128;
   static constexpr int KS = D / 16;                       // K steps of S^T = 16-column tiles of O^T
@@ -493,19 +493,24 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
       float pf[NG][2];  // e4m3: 2^6 times V's scales of keys 16 sg + g, + 8, in units of 2^(vexp - 127)
       float vdown = 1.f;
       if constexpr (E4M3) {
-        const uint8_t* sc = gbase + C::OFF_SCALE + (warp * C::S + st) * 2 * C::KG;
-        int vb[NG][2], top = 0;
+        // A lane turns the scales of keys 32 r + lane into factors; a fragment's come by shuffle.
+        constexpr int KPL = C::KG / 32;
+        const uint8_t* sc = gbase + C::OFF_SCALE + (warp * C::S + st) * 2 * C::KG + lane;
+        uint32_t vb[KPL];
+        float mine[KPL];
+        uint32_t top = 0;
+#pragma unroll
+        for (int r = 0; r < KPL; ++r) {
+          mine[r] = scale_of_byte(sc[32 * r]);
+          vb[r] = sc[C::KG + 32 * r];
+          if (edge && key0 + 32 * r + lane >= s.len) vb[r] = 0;
+          top = max(top, vb[r] == 255 ? 0 : vb[r]);
+        }
         float kf[NG][2];
 #pragma unroll
         for (int sg = 0; sg < NG; ++sg)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int at_key = 16 * sg + 8 * i + g;
-            kf[sg][i] = scale_of_byte(sc[at_key]);
-            vb[sg][i] = sc[C::KG + at_key];
-            if (edge && key0 + at_key >= s.len) vb[sg][i] = 0;
-            top = max(top, vb[sg][i] == 255 ? 0 : vb[sg][i]);
-          }
+          for (int i = 0; i < 2; ++i) kf[sg][i] = __shfl_sync(0xffffffffu, mine[sg >> 1], (16 * sg + 8 * i + g) & 31);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -513,16 +518,18 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[t][sg][i] *= kf[sg][i >> 1];
         }
-        top = max(vexp, __reduce_max_sync(0xffffffffu, top));
-        const int fall = top - vexp;  // 0 .. 254
+        const int most = max(vexp, static_cast<int>(__reduce_max_sync(0xffffffffu, top)));
+        const int fall = most - vexp;  // 0 .. 254
         vdown = fall > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - fall) << 23);
-        vexp = top;
+        vexp = most;
+#pragma unroll
+        for (int r = 0; r < KPL; ++r)
+          mine[r] = vb[r] == 255 ? __uint_as_float(0x7fc00000u)
+                                 : __uint_as_float(static_cast<uint32_t>(max(127 + 6 + static_cast<int>(vb[r]) - most, 0)) << 23);
 #pragma unroll
         for (int sg = 0; sg < NG; ++sg)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            pf[sg][i] = vb[sg][i] == 255 ? __uint_as_float(0x7fc00000u)
-                                         : __uint_as_float(static_cast<uint32_t>(max(127 + 6 + vb[sg][i] - top, 0)) << 23);
+          for (int i = 0; i < 2; ++i) pf[sg][i] = __shfl_sync(0xffffffffu, mine[sg >> 1], (16 * sg + 8 * i + g) & 31);
       }
       if constexpr (C::QS != 0) {
 #pragma unroll
