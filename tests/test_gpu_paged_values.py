@@ -1,0 +1,79 @@
+"""The paged cache on the GPU with values that a cache may hold and random tokens do not show: scales far apart, NaN codes,
+scales near the end of the range, very small queries over very large keys.  Bounds are those of paged_util."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.paged as ref
+from paged_util import Setup, check, run
+
+pytestmark = pytest.mark.gpu
+
+D = (32, 64, 128, 256)
+
+
+def place(s, b, pos):
+    return s.table[b, pos // s.page], pos % s.page
+
+
+def refresh(s):
+    """The oracle's values after codes or scale bytes of s (e4m3) were changed."""
+    s.values = [ref.dequantise(c.float().double().numpy(), b.numpy()) for c, b in zip(s.kv, s.scale_bytes)]
+
+
+# ------------------------------------------------------------------ V's scales
+@pytest.mark.parametrize("d", D)
+@pytest.mark.parametrize("n,group", [(4, 1), (4, 4), (4, 8), (100, 2)])
+@pytest.mark.parametrize("up", [12, 16, 24, 40, 80, 125])
+def test_an_unseen_token_of_any_size_leaves_earlier_rows(d, n, group, up):
+    """A new token's V is 2^up times the others'; rows before it do not see it."""
+    s = Setup([150, 70], [n, 3], heads=2, group=group, d=d, fmt="e4m3", seed=d + up)
+    page, slot = place(s, 0, 150 - n // 2)
+    byte = s.scale_bytes[1][page, :, slot]
+    byte.copy_((byte.int() + up).clamp(max=247).to(torch.uint8))
+    refresh(s)
+    check(s, *run(s), d ** -0.5, True)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("light,up", [(20, 24), (45, 32), (60, 40), (64, 64), (90, 95), (120, 110)])
+def test_a_visible_token_of_small_weight_and_large_value(d, light, up):
+    """One of 300 tokens has a weight of about 2^-light of the others' and a V 2^up times theirs."""
+    s = Setup([300], [1], heads=1, group=1, d=d, fmt="e4m3", seed=light)
+    q = s.q[0, 0].double().numpy()
+    page, slot = place(s, 0, 37)
+    codes, byte = ref.quantise_rows(-q / (q @ q) * d ** 0.5 * light * np.log(2.0))
+    s.kv[0][page, 0, slot] = torch.from_numpy(codes).float().to(torch.float8_e4m3fn)
+    s.scale_bytes[0][page, 0, slot] = int(byte)
+    s.scale_bytes[1][page, 0, slot] += up
+    refresh(s)
+    check(s, *run(s), d ** -0.5, True)
+
+
+@pytest.mark.parametrize("d", D)
+@pytest.mark.parametrize("n,group", [(1, 1), (1, 8), (4, 4), (4, 8)])
+@pytest.mark.parametrize("spread", [6, 20, 60, 90])
+def test_scales_of_values_that_are_far_apart(d, n, group, spread):
+    s = Setup([333, 40], [n, n], heads=2, group=group, d=d, page=32, fmt="e4m3", seed=spread)
+    g = torch.Generator().manual_seed(spread + d)
+    s.scale_bytes[1] = (127 + torch.randint(-spread, spread + 1, s.scale_bytes[1].shape, generator=g)).to(torch.uint8)
+    s.scale_bytes[1][~s.held[:, None, :].expand_as(s.scale_bytes[1])] = 255
+    refresh(s)
+    check(s, *run(s), d ** -0.5, True)
+
+
+@pytest.mark.parametrize("n,group", [(1, 4), (4, 2), (4, 8)])
+@pytest.mark.parametrize("byte", [0, 20, 70, 200, 240])
+@pytest.mark.parametrize("tokens", ["all", "first 200", "last 200"])
+def test_values_all_small_or_all_large(n, group, byte, tokens):
+    """Whole runs of tokens with tiny (byte 20: 2^-107), zero (0: codes are zeros, too) or huge values."""
+    s = Setup([333], [n], heads=2, group=group, d=64, page=16, fmt="e4m3", seed=byte + n)
+    for pos in range(333):
+        if (tokens == "first 200" and pos >= 200) or (tokens == "last 200" and pos < 133):
+            continue
+        page, slot = place(s, 0, pos)
+        s.scale_bytes[1][page, :, slot] = byte
+        if byte == 0:
+            s.kv[1][page, :, slot] = 0.0
+    refresh(s)
+    check(s, *run(s), 0.125, True)

@@ -24,12 +24,18 @@
 // as they are and every q row multiplied by a power of two that brings its
 // largest element to [2^13, 2^14) (exact down to 2^-37 of that element); the
 // rows' and the keys' powers of two multiply the fp32 result.  V's scales go
-// into P: P' = p 2^(e_j - E) 2^6 in fp16, E the largest exponent so far (kept
-// like the maximum: a larger one rescales the output, exactly).  P' is rounded
-// to 11 bits down to p 2^(e_j - E) = 2^-20, finer than bf16's 8, and to 2^-31 below.
-// The reference maximum m moves only when a logit exceeds it by more than 8 (log2
-// units), so p <= 2^8 and most groups need neither the rows' maxima nor a rescale:
-// one vote of the warp says so.
+// into P: P' = p 2^(e_j - E) 2^6 in fp16, e_j the scale's exponent and E a warp's
+// fixed one (of tokens that all rows see).  So that no token of small weight, and
+// none that a row does not see, takes bits from that row, what counts for the
+// reference m is the row's largest product p_j 2^(e_j - E), not its largest p_j:
+//   m = max_j (x_j + e_j - E),  p_j = 2^(x_j - m),  x_j the logit in log2 units.
+// P' is then rounded to 11 bits down to 2^-20 of the row's largest product, finer
+// than bf16's 8, and to 2^-31 of it below; l and o stand for 2^m whatever m is.
+// m moves only when x_j + e_j - E exceeds it by more than 8, so P' <= 2^14 and most
+// groups need neither the rows' maxima nor a rescale: one vote of the warp says so
+// (with the group's largest e_j for every key's).  (With E the largest exponent so far and m the largest logit, as plain as
+// can be, a hidden token 2^24 times larger than the others cost the earlier rows their bits; it was 0.7 % faster with
+// single tokens and 3.5 % with drafts.)
 //
 // Measured: single tokens of 64 sequences, 1.24 GB of bf16 pages, d = 128: 188 us, 6.6 TB/s (0.97 of a copy's rate);
 // 1.12 GB of e4m3 pages 174 us, 6.4 TB/s; 2 to 8 drafted tokens of 4 heads over 376 MB of e4m3 pages 122 us, 3.1 TB/s
@@ -68,8 +74,9 @@ struct FewCfg {
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = NW * S * 2 * KV;
   static constexpr int OFF_JOIN = OFF_Q + QS;
-  static constexpr int OFF_ML = OFF_JOIN + JOIN;          // the warps' m and l [NW][2][8]
-  static constexpr int OFF_ROWF = OFF_ML + NW * 16 * 4;   // e4m3, q in shared memory: the rows' factors [NT * 8]
+  static constexpr int OFF_ML = OFF_JOIN + JOIN;          // the warps' m and l (e4m3: and m + E) [NW][ML / 8][8]
+  static constexpr int ML = E4M3 ? 24 : 16;
+  static constexpr int OFF_ROWF = OFF_ML + NW * ML * 4;   // e4m3, q in shared memory: the rows' factors [NT * 8]
   static constexpr int OFF_SCALE = OFF_ROWF + 128;        // e4m3: K and V scale bytes [NW][S][2][KG]
   static constexpr int OFF_BAR = OFF_SCALE + (E4M3 ? NW * S * 2 * KG : 0);
   static constexpr int OFF_PLAN = OFF_BAR + NW * S * 8;
@@ -125,6 +132,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // tile and 6 to 8 with four, against 1.4 to 2.9 us a tile (drafts of ragged lengths 177 us without it, 157 with it).
 constexpr int kFewUnitCost = 2;
 constexpr float kFewSlack = 8.f;  // log2 units by which a logit may exceed the reference maximum
+// e4m3: how far e_j may count above and below E in m.  Where one lies farther above, E grows; one farther below (its P' is what
+// it is) counts as E - kFewBelow, and a scale byte of 0 (zeros, or values below 2^-118) as E - kFewZero.  So a row's largest
+// p_j lies within 2^-kFewAbove .. 2^(kFewBelow + 8): l holds every weight that counts, and stays finite whatever E grows
+// by, where the scales of V in a sequence (zeros aside) lie within 2^190 of each other.
+constexpr int kFewAbove = 96, kFewBelow = 96, kFewZero = 64;
+constexpr int kNoBase = -256;  // E before the first group
 
 struct FewParams {
   PagedFwdArgs a;
@@ -238,7 +251,6 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
   FewCursor<C::KT> ahead;  // next group to load
   ahead.start(p, share);
   uint32_t issued = 0, done = 0;
-  const uint64_t policy = policy_evict_first();  // a unit's K and V are read once
   const int box_log2 = p.box_log2;
   const int slot_mask = (1 << a.kv.ps_log2) - 1;
   // The next group with keys; where EARLY, its page's number is on its way until the group is issued.
@@ -254,6 +266,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
   auto issue = [&]() {
     if constexpr (!C::EARLY) find();
     if (ahead.left == 0) return;
+    const uint64_t policy = policy_evict_first();  // a unit's K and V are read once (made here: registers are full)
     const int key0 = ahead.j * C::KT + warp * C::KG;
     const uint32_t st = issued % C::S;
     const uint32_t bar = bars + 8 * st;
@@ -429,7 +442,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
         l[t][i] = 0.f;
       }
     }
-    int vexp = 0;  // e4m3: the largest V scale byte so far; o is in units of 2^(vexp - 127 - 6)
+    int vbase = kNoBase;  // e4m3: E as a scale byte; o is in units of 2^(vbase - 127 - 6)
 
 #pragma unroll 1
     for (int j = j0; j < j1; ++j) {
@@ -492,8 +505,8 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
         }
       }
       const bool edge = key0 + C::KG - 1 > lim_all;  // some row does not see some key
-      float pf[NG][2];  // e4m3: 2^6 times V's scales of keys 16 sg + g, + 8, in units of 2^(vexp - 127)
-      float vdown = 1.f;
+      float pf[NG][2];  // e4m3: 2^6 times V's scales of keys 16 sg + g, + 8, in units of 2^(vbase - 127)
+      float slack = kFewSlack;  // e4m3: less by the log2 of the largest of these scales (without the 2^6)
       if constexpr (E4M3) {
         // A lane turns the scales of keys 32 r + lane into factors; a fragment's come by shuffle.
         constexpr int KPL = C::KG / 32;
@@ -520,14 +533,33 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[t][sg][i] *= kf[sg][i >> 1];
         }
-        const int most = max(vexp, static_cast<int>(__reduce_max_sync(0xffffffffu, top)));
-        const int fall = most - vexp;  // 0 .. 254
-        vdown = fall > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - fall) << 23);
-        vexp = most;
+        const int most = static_cast<int>(__reduce_max_sync(0xffffffffu, top));
+        if (most - vbase > kFewAbove) {
+          if (vbase == kNoBase) {
+            // The largest scale of keys that every row sees, or the first key's: the rows that see anything here see that.
+            uint32_t all = 0;
+#pragma unroll
+            for (int r = 0; r < KPL; ++r)
+              if (vb[r] != 255 && key0 + 32 * r + lane <= max(lim_all, key0)) all = max(all, vb[r]);
+            all = __reduce_max_sync(0xffffffffu, all);
+            vbase = all == 0 ? 127 : max(static_cast<int>(all), 80);
+          }
+          // (o is in units of 2^(E + m): both change, it does not.)
+          const int up = max(most - kFewAbove - vbase, 0);  // <= 78
+          vbase += up;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              m[t][i] -= static_cast<float>(up);
+              l[t][i] *= __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+            }
+        }
+        slack = kFewSlack - static_cast<float>(max(most - vbase, -kFewZero));
 #pragma unroll
         for (int r = 0; r < KPL; ++r)
           mine[r] = vb[r] == 255 ? __uint_as_float(0x7fc00000u)
-                                 : __uint_as_float(static_cast<uint32_t>(max(127 + 6 + static_cast<int>(vb[r]) - most, 0)) << 23);
+                                 : __uint_as_float(static_cast<uint32_t>(max(127 + 6 + static_cast<int>(vb[r]) - vbase, 0)) << 23);
 #pragma unroll
         for (int sg = 0; sg < NG; ++sg)
 #pragma unroll
@@ -549,7 +581,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
         for (int sg = 1; sg < NG; ++sg) y = fmax3(y, x[t][sg][i], x[t][sg][2 + i]);
         return y * rowf[t][i];
       };
-      bool moves = vdown != 1.f;
+      bool moves = false;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         if (edge) {
@@ -561,15 +593,33 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
               if (key0 + 16 * sg + 8 * (i >> 1) + g > lim[i & 1]) x[t][sg][i] = -INFINITY;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) moves = moves || largest(t, i) > m[t][i] + kFewSlack;
+        for (int i = 0; i < 2; ++i) moves = moves || largest(t, i) > m[t][i] + slack;
       }
       if (__any_sync(0xffffffffu, moves)) {
+        float ve[NG][2];  // e4m3: e_j - E of this thread's keys (a scale of NaN: 0)
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int sg = 0; sg < NG; ++sg)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int e = static_cast<int>(__float_as_uint(pf[sg][h]) >> 23) - (127 + 6);
+              const int low = e <= -min(vbase, 127 + 6) ? -kFewZero : max(e, -kFewBelow);
+              ve[sg][h] = e > kFewAbove ? 0.f : static_cast<float>(low);
+            }
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float alpha[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float y = largest(t, i);
+            float y = -INFINITY;
+            if constexpr (E4M3) {
+#pragma unroll
+              for (int sg = 0; sg < NG; ++sg)
+                y = fmax3(y, fmaf(x[t][sg][i], rowf[t][i], ve[sg][0]), fmaf(x[t][sg][2 + i], rowf[t][i], ve[sg][1]));
+            } else {
+              y = largest(t, i);
+            }
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
@@ -577,7 +627,6 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
             alpha[i] = m_new == m[t][i] ? 1.f : ex2(m[t][i] - m_new);
             m[t][i] = m_new;
             l[t][i] *= alpha[i];
-            alpha[i] *= vdown;
           }
 #pragma unroll
           for (int c = 0; c < C::KS; ++c) {
@@ -726,7 +775,6 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
     const bool whole = j0 == 0 && j1 == at.nt;
     float* join_o = reinterpret_cast<float*>(gbase + C::OFF_JOIN);
     float* join_ml = reinterpret_cast<float*>(gbase + C::OFF_ML);
-    const float vf = E4M3 ? scale_of_byte(static_cast<uint32_t>(vexp)) : 1.f;
 #pragma unroll 1
     for (int t8 = 0; t8 < na; ++t8) {
 #pragma unroll
@@ -741,16 +789,16 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < C::KS; ++c) {
             if constexpr (E4M3) {
-              *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) =
-                  make_float2(o[t][c][i] * 0x1p-6f * vf, o[t][c][2 + i] * 0x1p-6f * vf);
+              *reinterpret_cast<float2*>(dst + 16 * c + 2 * g) = make_float2(o[t][c][i], o[t][c][2 + i]);
             } else {
               dst[16 * c + g] = o[t][c][i];
               dst[16 * c + 8 + g] = o[t][c][2 + i];
             }
           }
           if (g == 0) {
-            join_ml[warp * 16 + 2 * jq + i] = m[t][i];
-            join_ml[warp * 16 + 8 + 2 * jq + i] = l[t][i];
+            join_ml[warp * C::ML + 2 * jq + i] = m[t][i];
+            join_ml[warp * C::ML + 8 + 2 * jq + i] = l[t][i];
+            if constexpr (E4M3) join_ml[warp * C::ML + 16 + 2 * jq + i] = m[t][i] + static_cast<float>(vbase);
           }
         }
       }
@@ -761,19 +809,38 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
         if (r >= rows || *abort_flag != 0) break;
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < C::NW; ++w) top = fmaxf(top, join_ml[w * 16 + r8]);
+        for (int w = 0; w < C::NW; ++w) top = fmaxf(top, join_ml[w * C::ML + r8]);
         float lsum = 0.f, acc[D / 32] = {};
+        float otop = -INFINITY;  // e4m3: the largest E + m, O's reference
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int w = 0; w < C::NW; ++w) otop = fmaxf(otop, join_ml[w * C::ML + 16 + r8]);
+        }
 #pragma unroll
         for (int w = 0; w < C::NW; ++w) {
-          const float mw = join_ml[w * 16 + r8];
-          const float f = mw == top ? 1.f : ex2(mw - top);
-          lsum = fmaf(join_ml[w * 16 + 8 + r8], f, lsum);
+          const float mw = join_ml[w * C::ML + r8];
+          float f = mw == top ? 1.f : ex2((E4M3 ? 0.5f : 1.f) * (mw - top));
+          if constexpr (!E4M3) {
+            lsum = fmaf(join_ml[w * C::ML + 8 + r8], f, lsum);
+          } else {
+            // (The m of warps may lie 2^200 apart, where one has a large l and the other a small one: by halves.)
+            lsum = fmaf(join_ml[w * C::ML + 8 + r8] * f, f, lsum);
+            const float ow = join_ml[w * C::ML + 16 + r8];
+            f = ow == otop ? 1.f : ex2(ow - otop);
+          }
           const float* src = join_o + (w * 8 + r8) * C::JROW + lane;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(src[32 * c], f, acc[c]);
         }
         const int tok = token_of(r), row = s.row0 + tok, hq = at.head * a.group + r - tok * a.group;
-        const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+        float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+        if constexpr (E4M3) {
+          // From 2^otop to 2^top in V's units, by halves, too (no keys seen: m = -inf, O = 0).
+          const float f = top == -INFINITY ? 0.f : ex2(0.5f * (otop - top - (127.f + 6.f)));
+          inv *= f;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) acc[c] *= f;
+        }
         const float lg = top + log2f(lsum);
         if (whole) {
           __nv_bfloat16* dst = a.o + static_cast<long long>(row) * a.os[0] + static_cast<long long>(hq) * a.os[1] + lane;
