@@ -381,7 +381,7 @@ size_t fa_paged_fwd_workspace_bytes(int B, int heads, int d);
  * Arithmetic: fp32 softmax state and sums; bf16 products with fp32 accumulation (e4m3 pages with
  * few rows: fp16 products, in which a key's weight times its V's scale counts as 0 below 2^-31 of
  * the largest such product of the row's own keys; the scales of V in a sequence, those of zeros aside,
- * within 2^190 of each other, and values of scale 0, below 2^-118, may count as zeros);
+ * within 2^190 of each other, and values of K and V below 2^-117, scales 0 and 1, may count as zeros);
  * o rounded to bf16 once at the end.  Results do not depend on what else runs:
  * no atomics, and partial results are joined in a fixed order.
  */

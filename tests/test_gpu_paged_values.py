@@ -77,3 +77,20 @@ def test_values_all_small_or_all_large(n, group, byte, tokens):
             s.kv[1][page, :, slot] = 0.0
     refresh(s)
     check(s, *run(s), 0.125, True)
+
+
+# ------------------------------------------------------------------ logits from the ends of the range
+@pytest.mark.parametrize("d", D)
+@pytest.mark.parametrize("n,group", [(1, 2), (4, 2), (4, 8), (100, 2)])
+@pytest.mark.parametrize("small,large,shrink", [(60, 60, 0), (100, 100, 0), (112, 112, 0), (121, 121, 0), (-60, -60, 0),
+                                                (-100, -100, 0), (100, 112, 12), (100, 118, 18)])
+def test_small_queries_over_large_keys(d, n, group, small, large, shrink):
+    """q is 2^-small, K 2^large and the scale 2^-shrink of the usual: the logits are ordinary, a code's product with the key's
+    scale is not."""
+    s = Setup([150, 70], [n, 3], heads=2, group=group, d=d, fmt="e4m3", seed=d + n)
+    s.wide *= 2.0 ** -small  # (q, k and v rows are views of it)
+    b = s.scale_bytes[0]
+    s.scale_bytes[0] = torch.where(b == 255, b, (b.int() + large).to(torch.uint8))
+    refresh(s)
+    scale = d ** -0.5 * 2.0 ** -shrink
+    check(s, *run(s, scale=scale), scale, True)

@@ -322,7 +322,10 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
   auto row_scale = [&](uint32_t top, float& rowf) -> float {
     int e = static_cast<int>(top >> 7);  // biased exponent
     e = e == 255 ? 140 : e < 27 ? 27 : e;
-    rowf = fmaxf(scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 13) << 23), 0x1p-126f);  // never 0 (times -inf)
+    // Times 2^24: a key's factor is 2^-24 of its scale, for |x| < 2^31 (d 2^14 448) times a scale (2^120 at most, from
+    // paged_write) may pass fp32's range where a tiny q keeps the logit in it.  Never 0 (times -inf) nor infinite (times 0).
+    rowf = scale_log2 * 0x1p24f * __uint_as_float(static_cast<uint32_t>(e - 13) << 23);
+    rowf = fminf(fmaxf(rowf, 0x1p-126f), 0x1.fffffep127f);
     return __uint_as_float(static_cast<uint32_t>(267 - e) << 23);  // 2^(13 - (e - 127))
   };
 
@@ -516,7 +519,8 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
         uint32_t top = 0;
 #pragma unroll
         for (int r = 0; r < KPL; ++r) {
-          mine[r] = scale_of_byte(sc[32 * r]);
+          const uint32_t kb = sc[32 * r];
+          mine[r] = __uint_as_float(kb == 255 ? 0x7fc00000u : kb << 23) * 0x1p-24f;  // (0 and 1: 0)
           vb[r] = sc[C::KG + 32 * r];
           if (edge && key0 + 32 * r + lane >= s.len) vb[r] = 0;
           top = max(top, vb[r] == 255 ? 0 : vb[r]);
