@@ -94,3 +94,30 @@ def test_small_queries_over_large_keys(d, n, group, small, large, shrink):
     refresh(s)
     scale = d ** -0.5 * 2.0 ** -shrink
     check(s, *run(s, scale=scale), scale, True)
+
+
+# ------------------------------------------------------------------ parts that count for nothing
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 4, 100])
+def test_a_nan_of_negligible_weight_is_a_nan_however_the_keys_are_split(fmt, n):
+    """Every row sees a token whose V is NaN and whose weight, like that of its 1600 neighbours, is below 2^-150."""
+    s = Setup([9001], [n], heads=1, group=1, d=64, page=64, fmt=fmt, seed=n)
+    far = np.zeros(64)
+    far[0] = -1000.0
+    codes, byte = ref.quantise_rows(far)
+    s.q[:, 0, 0] = 4.0  # so these tokens' logits are near -500
+    for pos in range(1600):
+        page, slot = place(s, 0, pos)
+        if fmt == "bf16":
+            s.kv[0][page, 0, slot] = torch.from_numpy(far).bfloat16()
+        else:
+            s.kv[0][page, 0, slot] = torch.from_numpy(codes).float().to(torch.float8_e4m3fn)
+            s.scale_bytes[0][page, 0, slot] = int(byte)
+    page, slot = place(s, 0, 5)
+    if fmt == "bf16":
+        s.kv[1][page, 0, slot, 3] = float("nan")
+        s.values = [t.double().numpy() for t in s.kv]
+    else:
+        s.scale_bytes[1][page, 0, slot] = 255
+        refresh(s)
+    check(s, *run(s), 0.125, True)

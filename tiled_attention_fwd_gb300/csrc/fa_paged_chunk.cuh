@@ -1394,10 +1394,9 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
         for (int i = split ? warp : 0; i < to; i += split ? 4 : 1) {
           const float f = __shfl_sync(0xffffffffu, w, i);
           const float* x = (i0 + i == 0 ? first : rest + (i0 + i) * stride) + kFewMost + static_cast<size_t>(r) * D;
-          if (f != 0.f) {
+          // (Where f = 0, too: a NaN that the row sees counts at any weight, and a part without keys for it holds zeros.)
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) o[c] = fmaf(x[c * 32 + lane], f, o[c]);
-          }
+          for (int c = 0; c < D / 32; ++c) o[c] = fmaf(x[c * 32 + lane], f, o[c]);
         }
       }
       if (split) {
