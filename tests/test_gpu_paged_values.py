@@ -121,3 +121,18 @@ def test_a_nan_of_negligible_weight_is_a_nan_however_the_keys_are_split(fmt, n):
         s.scale_bytes[1][page, 0, slot] = 255
         refresh(s)
     check(s, *run(s), 0.125, True)
+
+
+# ------------------------------------------------------------------ NaN codes
+@pytest.mark.parametrize("d", D)
+@pytest.mark.parametrize("n,group", [(1, 2), (4, 2), (4, 8), (100, 2)])
+@pytest.mark.parametrize("code", [0x7f, 0xff])
+@pytest.mark.parametrize("new", [True, False])
+def test_nan_codes_under_a_finite_scale(d, n, group, code, new):
+    """A code that is e4m3's NaN, in one column of K or V: NaN for the rows that see it, nothing for the others."""
+    s = Setup([150, 70], [n, 3], heads=3, group=group, d=d, fmt="e4m3", seed=d + n)
+    page, slot = place(s, 0, 150 - n + n // 2 if new else 21)
+    s.kv[0].view(torch.uint8)[page, 1, slot, 3] = code
+    s.kv[1].view(torch.uint8)[page, 2, slot, d - 5] = code
+    refresh(s)
+    check(s, *run(s), d ** -0.5, True)

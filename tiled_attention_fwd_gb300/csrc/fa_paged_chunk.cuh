@@ -528,7 +528,8 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
 // Eight codes (two words) to eight bf16, times the scale: the bits of a code are
 // put where bf16 has them (sign; 4 exponent bits below bf16's 8; 3 mantissa
 // bits), which is the value times 2^-120, also for denormals; one multiplication
-// by 2^(120 + e) makes it right (two where that power is beyond bf16).
+// by 2^(120 + e) makes it right (two where that power is beyond bf16).  Only the
+// NaN codes 0x7f and 0xff come out as +-480 and are set apart.
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -539,6 +540,19 @@ __device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t x, uint32_t f, uint32_
   const uint32_t l = (x << 4) & 0xf0f0f0f0u;                        // low bytes: lowest exponent bit, mantissa
   lo = mul_bf16x2(__byte_perm(l, h, 0x5140), f);
   hi = mul_bf16x2(__byte_perm(l, h, 0x7362), f);
+}
+
+// A top bit is set where a byte of x holds a NaN code: one more carries out of its seven ones (2 operations a word; they
+// and the vote cost chunks of e4m3 pages 287 to 297 us, for conversion is short of integer operations).
+__device__ __forceinline__ uint32_t e4m3x4_any_nan(uint32_t x) { return (x + 0x01010101u) ^ x; }
+// The top bit of each byte that holds a NaN code (the others: anything).
+__device__ __forceinline__ uint32_t e4m3x4_nan(uint32_t x) { return (x & 0x7f7f7f7fu) + 0x01010101u; }
+// Bits of a bf16 NaN where bytes 0 and 1 (HIGH: 2 and 3) of `nan` have their top bit set.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t nan_bf16x2(uint32_t nan) {
+  uint32_t r;  // (a selector's bit 3: the byte's sign, eight times)
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(nan), "n"(HIGH ? 0xbbaa : 0x9988));
+  return r & 0x7fff7fffu;
 }
 
 // Stage after stage, groups of 16 rows dealt out to WARPS warps, this one the cw-th.  wait(bar, parity) waits, get
@@ -582,15 +596,22 @@ __device__ __forceinline__ bool chunk_convert(const ChunkParams& p, const ChunkB
       const uint8_t* scales = gbase + C::OFF_SCALE + (cb * 2 + i) * C::BK + r16;
       const uint32_t dst = base + C::OFF_KV + st * C::STAGE + i * C::KV_TILE + r16 * C::SWB;
       const uint32_t big = lane < 4 ? __vcmpgtu4(reinterpret_cast<const uint32_t*>(scales)[lane], 0x86868686u) : 0u;  // a byte > 134
-      auto convert = [&](auto checked) {
+      // From `pass` on; where not `checked`, up to the first batch that holds a NaN code.
+      auto convert = [&](auto checked, int pass) -> int {
 #pragma unroll 1
-        for (int pass = 0; pass < PASSES; pass += BATCH) {
+        for (; pass < PASSES; pass += BATCH) {
           uint2 x[BATCH];
           uint32_t byte[BATCH], w[BATCH][4];
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
             x[k] = *reinterpret_cast<const uint2*>(codes + (pass + k) * RPP * C::CODE_COLS);
             byte[k] = scales[(pass + k) * RPP + row0];
+          }
+          if constexpr (!decltype(checked)::value) {
+            uint32_t nan = 0;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) nan |= e4m3x4_any_nan(x[k].x) | e4m3x4_any_nan(x[k].y);
+            if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0)) return pass;
           }
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
@@ -603,18 +624,20 @@ __device__ __forceinline__ bool chunk_convert(const ChunkParams& p, const ChunkB
               const uint32_t f2 = byte[k] > 134u && byte[k] != 255u ? (byte[k] - 7u) * 0x00800080u : 0x3f803f80u;  // 2^(e - 7)
               const bool past = (pass + k) * RPP + row0 >= end;
 #pragma unroll
-              for (int i2 = 0; i2 < 4; ++i2) w[k][i2] = past ? 0u : mul_bf16x2(w[k][i2], f2);
+              for (int i2 = 0; i2 < 4; ++i2) {
+                const uint32_t nan = e4m3x4_nan(i2 < 2 ? x[k].x : x[k].y);
+                w[k][i2] = past ? 0u : mul_bf16x2(w[k][i2], f2) | (i2 & 1 ? nan_bf16x2<true>(nan) : nan_bf16x2<false>(nan));
+              }
             }
           }
           if constexpr (C::IN_PLACE) __syncwarp();  // the rows have been read by all of the warp
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) st_shared_v4(dst + to[k] + pass * RPP * C::SWB, w[k][0], w[k][1], w[k][2], w[k][3]);
         }
+        return PASSES;
       };
-      if (end >= 16 && !__any_sync(0xffffffffu, big != 0))
-        convert(std::false_type{});
-      else
-        convert(std::true_type{});
+      const int done = end >= 16 && !__any_sync(0xffffffffu, big != 0) ? convert(std::false_type{}, 0) : 0;
+      if (done < PASSES) convert(std::true_type{}, done);
     }
     fence_proxy_async_smem();  // before the tensor core reads them
     if constexpr (!C::IN_PLACE) warp_arrive(bar.code_empty(cb));
