@@ -290,7 +290,9 @@ int fa_fwd_noalloc(const void* q, const void* k, const void* v, void* o, float* 
  * exponent: real value = e4m3 value * 2^(scale - 127), scale 255 = NaN.  The
  * scale is the smallest power of two that brings the row's largest magnitude
  * to 448 (e4m3's largest value) or less, so dividing by it is exact, a written
- * value is rounded once, and what is read back is exact in bf16.
+ * value is rounded once, and what is read back is exact in bf16.  Pages that were filled by other means may
+ * hold any codes and scales: e4m3's NaN is NaN at every scale, and a value beyond bf16's range (scales from 248 on)
+ * may count as an infinity for the rows that see it.
  */
 typedef struct fa_paged_cache {
   void* k;                  /* pages of keys, bf16 or e4m3, 16-byte aligned                          */

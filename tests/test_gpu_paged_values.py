@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle.paged as ref
-from paged_util import Setup, check, run
+from paged_util import Setup, U, check, run
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +136,24 @@ def test_nan_codes_under_a_finite_scale(d, n, group, code, new):
     s.kv[1].view(torch.uint8)[page, 2, slot, d - 5] = code
     refresh(s)
     check(s, *run(s), d ** -0.5, True)
+
+
+# ------------------------------------------------------------------ scales beyond bf16's range
+@pytest.mark.parametrize("d", D)
+@pytest.mark.parametrize("n,group", [(4, 2), (4, 8), (100, 2)])
+@pytest.mark.parametrize("byte", [248, 250, 254])
+def test_unseen_values_beyond_bf16_leave_earlier_rows(d, n, group, byte):
+    """448 times 2^121 and more is no bf16: a token that holds it (not from paged_write) reaches the rows that see it."""
+    s = Setup([150, 70], [n, 3], heads=2, group=group, d=d, fmt="e4m3", seed=d + n)
+    o_ref, l_ref, absum, size = ref.attention(s.q.double().numpy(), *s.values, s.table, s.cu, s.lens, d ** -0.5, True)
+    page, slot = place(s, 0, 149)
+    for j in range(2):
+        s.kv[j].view(torch.uint8)[page, 1, slot] = 0x7e
+        s.scale_bytes[j][page, 1, slot] = byte
+    o, lse = (t.cpu().double().numpy() for t in run(s))
+    keep = np.r_[0:n - 1, n:n + 3]
+    e_s = (d + 8) * 2.0 ** -24 * size
+    tol_o = U * (absum + 2 * np.abs(o_ref)) + (2.0 ** -16 + 2 * e_s.T[:, :, None]) * absum
+    assert (np.abs(o - o_ref) <= tol_o)[keep].all()
+    tol_l = 2 * e_s + 150 / 16 * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -22 * np.abs(l_ref)
+    assert (np.abs(lse - l_ref) <= tol_l)[:, keep].all()

@@ -262,11 +262,12 @@ struct MendParams {
   int n_odd;
 };
 
+// (A scale byte of 248 and more, which paged_write never stores, may take a code beyond bf16's range: an infinity in the tile.)
 template <int D, bool E4M3>
 __device__ __forceinline__ bool row_is_odd(const PagedKv& kv, int page, int head, int slot) {
   const uint8_t* v = static_cast<const uint8_t*>(kv.v) +
                      (page * kv.vs[0] + head * kv.vs[1] + slot * kv.vs[2]) * (E4M3 ? 1 : 2);
-  bool odd = E4M3 && kv.v_scale[((static_cast<long long>(page) * kv.heads + head) << kv.ps_log2) + slot] == 255;
+  bool odd = E4M3 && kv.v_scale[((static_cast<long long>(page) * kv.heads + head) << kv.ps_log2) + slot] >= 248;
   for (int i = 0; i < D * (E4M3 ? 1 : 2) / 4; ++i) {
     const uint32_t w = reinterpret_cast<const uint32_t*>(v)[i];
     odd = odd || (E4M3 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u)) != 0;
