@@ -139,9 +139,9 @@ struct TcCfg {
   static constexpr int OFF_MISC = OFF_KV + NST * STAGE;
   static constexpr int OFF_BAR = OFF_MISC;                    // 64 barriers at most
   static constexpr int OFF_ALPHA = OFF_MISC + 512;            // float [NO][2][128] (by step parity)
-  // m and l of a finished unit, double-buffered by the parity of the unit's
-  // index within the CTA: the softmax may finish the next unit (one key tile)
-  // while the correction warpgroup still reads this one's.
+  // m and l of a finished unit, double-buffered by the parity of the number of
+  // units that its tile has finished: the softmax may finish the next unit (one
+  // key tile) while the correction warpgroup still reads this one's.
   static constexpr int OFF_STAT_M = OFF_ALPHA + 4 * 128 * 4;  // float [2][NO][128]
   static constexpr int OFF_STAT_L = OFF_STAT_M + 4 * 128 * 4; // float [2][NO][128]
   static constexpr int OFF_TMEM_SLOT = OFF_STAT_L + 4 * 128 * 4;
@@ -282,9 +282,14 @@ struct TcBars {
   // steps ahead of the correction warpgroup).
   __device__ __forceinline__ uint32_t a_full(int t, int k) const { return b0 + 32 + 8u * (2 * C::NST + 6 + 2 * t + k); }
   __device__ __forceinline__ uint32_t o_done(int t) const { return b0 + 32 + 8u * (2 * C::NST + 10 + t); }
-  __device__ __forceinline__ uint32_t l_full(int t) const { return b0 + 32 + 8u * (2 * C::NST + 12 + t); }
-  __device__ __forceinline__ uint32_t drain() const { return b0 + 32 + 8u * (2 * C::NST + 14); }
-  static constexpr int COUNT = 4 + 2 * C::NST + 15;
+  // m and l of tile t's k-th unit: two barriers take turns, for the softmax may finish unit k + 1 (one key tile) before
+  // the correction warpgroup waits for unit k, and a barrier two phases ahead looks as if nothing had arrived.  (It cannot
+  // finish unit k + 2 by then: its S comes behind P V of unit k + 1, which waits for O to be read out.)
+  __device__ __forceinline__ uint32_t l_full(int t, uint32_t k) const {
+    return b0 + 32 + 8u * (2 * C::NST + 12 + 2 * t + (k & 1));
+  }
+  __device__ __forceinline__ uint32_t drain() const { return b0 + 32 + 8u * (2 * C::NST + 16); }
+  static constexpr int COUNT = 4 + 2 * C::NST + 17;
   static_assert(COUNT * 8 <= 512, "barrier area");
 };
 
@@ -743,7 +748,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams& p, const TcBars<D, NQ
   float* stat_l = reinterpret_cast<float*>(gbase + C::OFF_STAT_L) + ot * 128;
   const float sl2 = p.scale_log2;
   const uint64_t sl2x2 = f2_pack(sl2, sl2);
-  uint32_t s_waits = 0;  // S buffers consumed by this warpgroup
+  uint32_t s_waits = 0;  // S buffers consumed by this warpgroup; bit 31: parity of the units that it has finished
   bool ok = true;
 
   for (int uk = 0, u; ok && (u = tc_unit<C::PAIR>(uk)) < p.total_units; ++uk) {
@@ -895,9 +900,11 @@ __device__ __forceinline__ void tc_softmax(const TcParams& p, const TcBars<D, NQ
     if (!ok) break;
     // Lazy max: the row's log2-sum-exp2 (from the fp32 sum) and O's
     // normaliser; otherwise m and l.
-    stat_m[(uk & 1) * 256 + r] = C::LAZY_MAX ? m + log2f(l) : m;
-    stat_l[(uk & 1) * 256 + r] = C::LAZY_MAX ? l + lres : l;
-    warp_arrive(bar.l_full(ot));
+    const uint32_t fin = s_waits >> 31;
+    stat_m[fin * 256 + r] = C::LAZY_MAX ? m + log2f(l) : m;
+    stat_l[fin * 256 + r] = C::LAZY_MAX ? l + lres : l;
+    warp_arrive(bar.l_full(ot, fin));
+    s_waits ^= 0x80000000u;
   }
 }
 
@@ -983,9 +990,10 @@ __device__ __forceinline__ void tc_correction(const TcParams& p, const CUtensorM
   // chunks earlier has finished reading.
   const uint32_t ost = smem_u32(gbase + C::OFF_OST) + static_cast<uint32_t>(quarter * C::OSTB * C::OST_BUF);
   uint32_t ost_n = 0;  // chunks staged by this warp so far
-  auto epilogue = [&](const TcUnit& w, int su, int t, uint32_t& od, uint32_t& lf) -> bool {
+  auto epilogue = [&](const TcUnit& w, int t, uint32_t& od, uint32_t& lf) -> bool {
+    const uint32_t su = lf & 1;
     bool k = warp_wait_bar(bar.o_done(t), od & 1, g, kStatusTimeoutSoftmax);
-    k = k && warp_wait_bar(bar.l_full(t), lf & 1, g, kStatusTimeoutSoftmax);
+    k = k && warp_wait_bar(bar.l_full(t, lf), (lf >> 1) & 1, g, kStatusTimeoutSoftmax);
     if (!k) return false;
     ++od;
     ++lf;
@@ -1049,8 +1057,8 @@ __device__ __forceinline__ void tc_correction(const TcParams& p, const CUtensorM
     for (int j = 0; ok && j < w.nmax; ++j) {
       if (ok && j >= 1 && j < n0) ok = rescale(0, a_cnt0, od0);
       if (C::NO == 2 && ok && j >= 1 && j < w.n[1]) ok = rescale(1, a_cnt1, od1);
-      if (ok && j == n0 - 1) ok = epilogue(w, uk & 1, 0, od0, lf0);
-      if (C::NO == 2 && ok && j == w.n[1] - 1) ok = epilogue(w, uk & 1, 1, od1, lf1);
+      if (ok && j == n0 - 1) ok = epilogue(w, 0, od0, lf0);
+      if (C::NO == 2 && ok && j == w.n[1] - 1) ok = epilogue(w, 1, od1, lf1);
     }
   }
   // The staged O tiles must be written (and their shared memory read) before the CTA exits.
@@ -1098,7 +1106,8 @@ __global__ void __launch_bounds__(TcCfg<D, NQ, VAR>::THREADS, 1)
       mbar_init(bar.a_full(b, 0), 4);
       mbar_init(bar.a_full(b, 1), 4);
       mbar_init(bar.o_done(b), 1);
-      mbar_init(bar.l_full(b), 4);
+      mbar_init(bar.l_full(b, 0), 4);
+      mbar_init(bar.l_full(b, 1), 4);
     }
     mbar_init(bar.drain(), 1);
     *abort_flag = 0;
