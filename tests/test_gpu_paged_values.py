@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import oracle.paged as ref
+import tiled_attention_fwd_gb300 as fa
 from paged_util import Setup, U, check, run
 
 pytestmark = pytest.mark.gpu
@@ -157,3 +158,16 @@ def test_unseen_values_beyond_bf16_leave_earlier_rows(d, n, group, byte):
     assert (np.abs(o - o_ref) <= tol_o)[keep].all()
     tol_l = 2 * e_s + 150 / 16 * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -22 * np.abs(l_ref)
     assert (np.abs(lse - l_ref) <= tol_l)[:, keep].all()
+
+
+# ------------------------------------------------------------------ pools of one page or one head
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("pages,heads", [(1, 1), (1, 2), (5, 1)])
+def test_strides_of_one_element_dimensions_are_not_looked_at(fmt, pages, heads):
+    """torch may report any stride for a dimension of one element: 7 here, which no row of 16 bytes could have."""
+    lens = [64 * pages - 9]
+    s = Setup(lens, [3], heads=heads, group=2, d=64, page=64, fmt=fmt, seed=heads, spare=0)
+    cache = s.cache()
+    odd = [torch.as_strided(t, t.shape, (7 if pages == 1 else t.stride(0), 7 if heads == 1 else t.stride(1), 64, 1))
+           for t in (cache.k, cache.v)]
+    check(s, *run(s, cache=fa.PagedCache(*odd, cache.k_scale, cache.v_scale)), 0.125, True)

@@ -400,7 +400,11 @@ class PagedCache:
         c.k, c.v = k.data_ptr(), v.data_ptr()
         if fp8:
             c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
-        c.k_stride[:], c.v_stride[:] = k.stride()[:3], v.stride()[:3]
+        for dst, t in ((c.k_stride, k), (c.v_stride, v)):
+            page, head, slot, _ = t.stride()
+            # Strides of dimensions of one element are never used; torch may report any value for them.
+            head = head if self.heads > 1 else slot * self.page_size
+            dst[:] = page if self.num_pages > 1 else head * self.heads, head, slot
         c.num_pages, c.page_size, c.heads, c.d = self.num_pages, self.page_size, self.heads, self.d
         self._c = c
 
