@@ -248,9 +248,9 @@ int launch_move(MoveArgs& a, int d, bool e4m3, const LaunchCtx& ctx) {
 // ------------------------------------------------------------------ attention, mending
 // The chunk kernel multiplies whole tiles: P = 0 where a row does not see a key,
 // and 0 times an infinity or a NaN in that key's V is NaN.  It notes whether any
-// O came out infinite or NaN; if so, this kernel looks at every row of a chunk and
-// computes those again, plainly, that have such a V behind them (a key that some
-// rows of its sequence see and others do not is a new token).  One warp per (row, query head): 32 keys at
+// O came out infinite or NaN; if so, this kernel looks at the O of every row of a chunk
+// and computes those NaN rows again, plainly, that have such a V behind them (a key that
+// some rows of its sequence see and others do not is a new token).  One warp per (row, query head): 32 keys at
 // a time, a key per lane for the logits (q from shared memory), then the lanes
 // share out the d columns of V.  It is launched behind every causal chunk call and
 // leaves at once where there is nothing to mend.
@@ -268,9 +268,13 @@ __device__ __forceinline__ bool row_is_odd(const PagedKv& kv, int page, int head
   const uint8_t* v = static_cast<const uint8_t*>(kv.v) +
                      (page * kv.vs[0] + head * kv.vs[1] + slot * kv.vs[2]) * (E4M3 ? 1 : 2);
   bool odd = E4M3 && kv.v_scale[((static_cast<long long>(page) * kv.heads + head) << kv.ps_log2) + slot] >= 248;
-  for (int i = 0; i < D * (E4M3 ? 1 : 2) / 4; ++i) {
-    const uint32_t w = reinterpret_cast<const uint32_t*>(v)[i];
-    odd = odd || (E4M3 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u)) != 0;
+#pragma unroll
+  for (int i = 0; i < D * (E4M3 ? 1 : 2) / 16; ++i) {
+    const uint4 x = reinterpret_cast<const uint4*>(v)[i];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      odd = odd || (E4M3 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpgeu2(w[k] & 0x7fff7fffu, 0x7f807f80u)) != 0;
   }
   return odd;
 }
@@ -298,6 +302,11 @@ __global__ void __launch_bounds__(kMendWarps * 32) fa_paged_mend_kernel(const __
     bool bad;
     const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, b, bad);
     if (t < s.row0 || t >= s.row0 + s.n || s.n > a.max_rows || (s.n <= kFewMost && s.n * a.group <= a.few_rows)) continue;
+    // Such a V has made the row's O a NaN (0 times it); all other rows are done with here.
+    bool spoiled = false;
+#pragma unroll
+    for (int c = 0; c < D; c += 32) spoiled = spoiled || __hisnan(a.o[t * a.os[0] + hq * a.os[1] + c + lane]);
+    if (!__any_sync(0xffffffffu, spoiled)) continue;
     const int see = s.len - s.n + (t - s.row0) + 1;  // keys 0 .. see - 1
     bool odd = false;
     for (int j = max(see, 0) + lane; j < s.len; j += 32) {
