@@ -1403,12 +1403,12 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
       for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
       float l = 0.f, o[D / 32] = {};
       for (int i0 = 0; i0 < n; i0 += 32) {
-        float w = 0.f;
+        float w = -1.f;  // (no part, or one that saw none of the row's keys)
         if (i0 + lane < n) {
           const float x = (i0 + lane == 0 ? first : rest + (i0 + lane) * stride)[r];
-          w = x == -INFINITY ? 0.f : ex2(x - m);
+          if (x != -INFINITY) w = ex2(x - m);
         }
-        float sum = w;
+        float sum = w < 0.f ? 0.f : w;
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
         l += sum;
@@ -1417,9 +1417,10 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
         for (int i = split ? warp : 0; i < to; i += split ? 4 : 1) {
           const float f = __shfl_sync(0xffffffffu, w, i);
           const float* x = (i0 + i == 0 ? first : rest + (i0 + i) * stride) + kFewMost + static_cast<size_t>(r) * D;
-          // (Where f = 0, too: a NaN that the row sees counts at any weight, and a part without keys for it holds zeros.)
+          if (f >= 0.f) {  // (where f = 0, too: a NaN that the row sees counts at any weight; f = NaN is in l already)
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) o[c] = fmaf(x[c * 32 + lane], f, o[c]);
+            for (int c = 0; c < D / 32; ++c) o[c] = fmaf(x[c * 32 + lane], f, o[c]);
+          }
         }
       }
       if (split) {
