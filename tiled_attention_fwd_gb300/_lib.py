@@ -511,7 +511,7 @@ def paged_read(cache, page_table, cu_rows, kv_lens, rows=None, out=None):
 
 
 def paged_workspace(cache, B):
-    """A workspace for paged_forward calls of B sequences (or fewer) on this cache, one call at a time."""
+    """A workspace for paged_forward calls of B sequences (its size is the same for any B) on this cache, one call at a time."""
     import torch
 
     return torch.empty(fa_paged_fwd_workspace_bytes(B, cache.heads, cache.d), dtype=torch.uint8, device=cache.device)
@@ -556,7 +556,7 @@ def paged_forward(q, cache, page_table, cu_rows, kv_lens, max_rows=None, causal:
 
 
 def check_status(device=None):
-    """Synchronise the current stream and raise FAError if a device wait timed out."""
+    """Synchronise the current stream and raise FAError if a device wait timed out or a batch named what is not there."""
     import torch
 
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)

@@ -27,8 +27,8 @@
 //
 // Bound by the tensor cores and the softmax as the contiguous forward is (1.55 us a step of 256 rows and 128 keys at
 // d = 128), at short lengths by the units' borders (about 2.5 us each), with e4m3 pages by a stage's way through loading,
-// converting and multiplying (2.5 us a step, 5 us or more a border).  Measured at d = 128: chunks of 541 to 2048 tokens
-// over 7 to 16 K, bf16, 474 GFLOP: 332 us, 1.43 PFLOP/s (353 in a long run at full power); 65 to 1024 tokens over 1.7 to 8 K, e4m3, 210 GFLOP: 288 us;
+// converting and multiplying (2.7 us a step, 5 us or more a border).  Measured at d = 128: chunks of 541 to 2048 tokens
+// over 7 to 16 K, bf16, 474 GFLOP: 349 us, 1.36 PFLOP/s (340 to 360 with the card's power); 65 to 1024 tokens over 1.7 to 8 K, e4m3, 210 GFLOP: 297 us;
 // prompts of 1.7 to 4 K tokens, 161 GFLOP: 180 us.  Of a call's time about 12 us are the joining kernel (40 MB of parts
 // through L2) and 2 us the mending kernel's look at its flags.
 #pragma once
@@ -157,7 +157,9 @@ struct ChunkParams {
   bool tma_o;   // a warp's 32 rows are a box of O (the group is a power of two)
 };
 
-// sum over i in [0, n) of floor((a i + b) / m), a, b >= 0, a n + b < 2^32 (Euclid's way down).
+// sum over i in [0, n) of floor((a i + b) / m), a, b >= 0, a n + b < 2^32: the lattice points under a line, counted by Euclid's
+// algorithm (Graham, Knuth and Patashnik, Concrete Mathematics, 3.5, reduce such sums this way): whole parts of a / m and
+// b / m are summed directly, then the axes change places.
 __host__ __device__ inline long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long sum = 0;
   while (n > 0) {

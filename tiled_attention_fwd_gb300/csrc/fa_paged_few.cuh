@@ -34,12 +34,12 @@
 // m moves only when x_j + e_j - E exceeds it by more than 8, so P' <= 2^14 and most
 // groups need neither the rows' maxima nor a rescale: one vote of the warp says so
 // (with the group's largest e_j for every key's).  (With E the largest exponent so far and m the largest logit, as plain as
-// can be, a hidden token 2^24 times larger than the others cost the earlier rows their bits; it was 0.7 % faster with
-// single tokens and 3.5 % with drafts.)
+// can be, a hidden token 2^24 times larger than the others cost the earlier rows their bits; it was as fast with
+// single tokens and 3 % faster with drafts.)
 //
 // Measured: single tokens of 64 sequences, 1.24 GB of bf16 pages, d = 128: 188 us, 6.6 TB/s (0.97 of a copy's rate);
-// 1.12 GB of e4m3 pages 174 us, 6.4 TB/s; 2 to 8 drafted tokens of 4 heads over 376 MB of e4m3 pages 122 us, 3.1 TB/s
-// (issue slots 37 % used with two warps a scheduler, tensor pipe 30 %: latencies).
+// 1.12 GB of e4m3 pages 171 us, 6.5 TB/s; 2 to 8 drafted tokens of 4 heads over 376 MB of e4m3 pages 124 us, 3.0 TB/s
+// (issue slots 36 % used with two warps a scheduler, tensor pipe 30 %: latencies), over 743 MB of bf16 pages 135 us, 5.5 TB/s.
 #pragma once
 
 #include <type_traits>
@@ -916,8 +916,12 @@ int launch_paged_few_impl(const PagedFwdArgs& a, int set, int from, int most, bo
 
 // Row tiles cost nothing while reading K and V bounds the kernel (bf16: 1.4 us a tile of 128 keys with 1, 2 or 4), but
 // with e4m3 pages they do (256 keys, d = 128: 1.4, 1.65 and 2.7 us), so sequences of more than 16 rows are a launch of
-// their own there, if there is work enough for two (2 to 8 tokens of 4 heads over 4.5 K: 40 sequences of 8 key/value
-// heads 127 us and in one launch 139; 4 sequences 43 and 34).
+// their own there, if there is work enough for two.  Which sequences have how many rows only the device knows; B times the
+// heads decides.  4 query heads to a key/value head, 0.8 to 8 K tokens, us in one launch / two:
+//   B heads                        32       64       128      192      320       640       1280
+//   2 to 8 new tokens a sequence   33 / 43  46 / 61  72 / 75  89 / 92  149 / 139 259 / 233 500 / 456
+//   1, rarely 8                    29 / 34  44 / 43  70 / 60  86 / 79  149 / 119 260 / 183 492 / 330
+//   5 to 8 (all in the first)      34 / 38  47 / 51  75 / 79  92 / 96  150 / 155 263 / 264 502 / 508
 template <int D>
 int launch_paged_few(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx) {
   auto launch = [&](auto nt, int set, int from, int most, bool behind) -> int {
