@@ -384,7 +384,8 @@ size_t fa_paged_fwd_workspace_bytes(int B, int heads, int d);
  * few rows: fp16 products, in which a key's weight times its V's scale counts as 0 below 2^-31 of
  * the largest such product of the row's own keys; the scales of V in a sequence, those of zeros aside,
  * within 2^190 of each other, and values of K and V below 2^-117, scales 0 and 1, may count as zeros);
- * o rounded to bf16 once at the end.  Results do not depend on what else runs:
+ * o rounded to bf16 once at the end.  Weights are up to 2^8 before they are normalised, so |v| < 2^100 keeps the
+ * sums in fp32's range at any length.  Results do not depend on what else runs:
  * no atomics, and partial results are joined in a fixed order.
  */
 int fa_paged_fwd(const void* q, const long long* q_stride, const fa_paged_cache* cache, const fa_paged_batch* batch,
