@@ -5,9 +5,9 @@ if nothing had arrived."""
 import pytest
 
 
-def explore(units, barriers, slot_by_unit):
+def explore(units, barriers, slot_by_unit, order=("l_full", "o_done")):
     """(deadlocks, wrong reads) reachable; units: the tiles each unit has, [(1, 1), ..]; `barriers` per tile (1 or 2);
-    statistics in slot (unit's index & 1) or (number of the tile's finished units & 1)."""
+    statistics in slot (unit's index & 1) or (number of the tile's finished units & 1); order: of the correction's waits."""
     mine = [[k for k, has in enumerate(units) if has[t]] for t in range(2)]  # units of tile t
 
     def mma():  # (kind, tile): S of the first unit, then every unit's P V, then the next unit's S
@@ -27,7 +27,7 @@ def explore(units, barriers, slot_by_unit):
     for k, has in enumerate(units):
         for t in range(2):
             if has[t]:
-                correction += [("o_done", t, k), ("l_full", t, k), ("read", t, k), ("free", t, k)]
+                correction += [(order[0], t, k), (order[1], t, k), ("read", t, k), ("free", t, k)]
 
     # State: program counters (MMA, softmax 0, softmax 1, correction); per tile the phases of s_full, o_done, the softmax's and
     # the correction's arrivals on pv_go, l_full; the units whose statistics the slots hold.
@@ -99,14 +99,16 @@ def explore(units, barriers, slot_by_unit):
 BOTH, FIRST = (1, 1), (1, 0)  # a unit at the end of an odd number of query tiles has the first alone
 
 
+@pytest.mark.parametrize("order", [("l_full", "o_done"), ("o_done", "l_full")])  # fa_fwd_tc.cuh, fa_paged_chunk.cuh
 @pytest.mark.parametrize("units", [[BOTH] * 5, [BOTH, FIRST] * 3, [FIRST, BOTH, BOTH, FIRST, BOTH], [FIRST] * 4])
-def test_two_barriers_hand_over_every_unit(units):
-    assert explore(units, 2, False) == (0, set())
+def test_two_barriers_hand_over_every_unit(units, order):
+    assert explore(units, 2, False, order) == (0, set())
 
 
-def test_one_barrier_can_be_overrun():
+@pytest.mark.parametrize("order", [("l_full", "o_done"), ("o_done", "l_full")])
+def test_one_barrier_can_be_overrun(order):
     """What the two barriers are for: with one, a correction that comes late waits for a phase that is long over."""
-    stuck, _ = explore([BOTH] * 4, 1, False)
+    stuck, _ = explore([BOTH] * 4, 1, False, order)
     assert stuck > 0
 
 

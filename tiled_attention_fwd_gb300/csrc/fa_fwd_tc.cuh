@@ -286,9 +286,9 @@ struct TcBars {
   // the correction warpgroup waits for unit k, and a barrier two phases ahead looks as if nothing had arrived.  (It cannot
   // finish unit k + 2 by then: its S comes behind P V of unit k + 1, which waits for O to be read out.)
   __device__ __forceinline__ uint32_t l_full(int t, uint32_t k) const {
-    return b0 + 32 + 8u * (2 * C::NST + 12 + 2 * t + (k & 1));
+    return b0 + 32 + 8u * (2 * C::NST + 12 + t) + 24u * (k & 1);
   }
-  __device__ __forceinline__ uint32_t drain() const { return b0 + 32 + 8u * (2 * C::NST + 16); }
+  __device__ __forceinline__ uint32_t drain() const { return b0 + 32 + 8u * (2 * C::NST + 14); }
   static constexpr int COUNT = 4 + 2 * C::NST + 17;
   static_assert(COUNT * 8 <= 512, "barrier area");
 };
@@ -992,8 +992,8 @@ __device__ __forceinline__ void tc_correction(const TcParams& p, const CUtensorM
   uint32_t ost_n = 0;  // chunks staged by this warp so far
   auto epilogue = [&](const TcUnit& w, int t, uint32_t& od, uint32_t& lf) -> bool {
     const uint32_t su = lf & 1;
-    bool k = warp_wait_bar(bar.o_done(t), od & 1, g, kStatusTimeoutSoftmax);
-    k = k && warp_wait_bar(bar.l_full(t, lf), (lf >> 1) & 1, g, kStatusTimeoutSoftmax);
+    bool k = warp_wait_bar(bar.l_full(t, lf), (lf >> 1) & 1, g, kStatusTimeoutSoftmax);
+    k = k && warp_wait_bar(bar.o_done(t), od & 1, g, kStatusTimeoutSoftmax);
     if (!k) return false;
     ++od;
     ++lf;
