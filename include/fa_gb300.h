@@ -55,7 +55,8 @@ enum {
   FA_ERR_BAD_SCALE = -8,      /* scale is not a finite number > 0                            */
   FA_ERR_WORKSPACE = -9,      /* the workspace passed to fa_fwd_host or fa_bwd is too small  */
   FA_ERR_SCRATCH = -10,       /* the kernel needs more scratch than fa_fwd_noalloc provides  */
-  FA_ERR_BAD_BATCH = -11      /* page_table, cu_rows or kv_lens named what is not there (reported by fa_status) */
+  FA_ERR_BAD_BATCH = -11,     /* a batch's offsets, lengths or pages named what is not there (reported by fa_status) */
+  FA_ERR_NO_PAGES = -12       /* fa_paged_extend had too few free pages (reported by fa_status) */
 };
 
 /*
@@ -393,12 +394,143 @@ int fa_paged_fwd(const void* q, const long long* q_stride, const fa_paged_cache*
                  void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Tables of the paged cache, built on the device.  (No counterpart in the
+ * pages.)  A pool holds the pages that no sequence has, as a stack: the first
+ * *free_count entries of free_pages are page numbers, the last of them is taken
+ * first.  (free_pages = num_pages - 1 .. 0 and *free_count = num_pages: all
+ * free.)  A sequence of len tokens has the first ceil(len / page_size) entries
+ * of its row of page_table.  The arrays are the caller's; calls on the same
+ * ones are ordered by a stream.
+ */
+typedef struct fa_page_pool {
+  int* free_pages;          /* device, [num_pages]                                                   */
+  int* free_count;          /* device, one int, 0 .. num_pages                                       */
+  int num_pages;            /* >= 1                                                                  */
+  int page_size;            /* tokens a page: 16, 32, 64, 128, 256, 512 or 1024                      */
+} fa_page_pool;
+
+/*
+ * fa_paged_extend - lengthens sequence b by new_rows[b] tokens: takes the pages
+ * that it needs beyond its own (in the order of the sequences, then of their
+ * positions), enters them in its row of page_table, advances kv_lens[b], and
+ * writes what the calls above read: cu_rows (the sums of the new rows), and for
+ * each new row its slot, page * page_size + position % page_size, and its
+ * position.  Rows of slots and positions behind cu_rows[B] are left as they are.
+ *
+ * A sequence is extended whole or not at all: not, if a count or length is
+ * negative or the length would pass max_pages * page_size (fa_status reports
+ * FA_ERR_BAD_BATCH); if the new rows of all sequences up to it that pass these checks exceed
+ * `rows` (likewise); or if it needs pages and those that they need together
+ * exceed *free_count (FA_ERR_NO_PAGES).  Then its length stays, and it has no rows in cu_rows.
+ *
+ *   page_table : device, [B] rows of max_pages entries, table_stride ints apart.
+ *   kv_lens, new_rows : device, [B].    cu_rows : device, [B + 1].
+ *   slots      : device, long long [rows], positions : device, int [rows]; 16-byte aligned.  Either may be NULL (not written).
+ *   rows       : most new rows that the arrays hold, >= 0.
+ *   An entry of free_pages that is no page (outside [0, num_pages)) is entered as -1 and reported as
+ *   FA_ERR_BAD_BATCH, and so is an entry of page_table that a new row needs and that is none: its slot is -1.
+ */
+int fa_paged_extend(const fa_page_pool* pool, int* page_table, long long table_stride, int max_pages, int* kv_lens,
+                    const int* new_rows, int* cu_rows, long long* slots, int* positions, int B, int rows, void* stream);
+
+/*
+ * fa_paged_release - the sequences b with done[b] != 0 end: their pages go back
+ * onto the stack (in the order of the sequences, then of their positions), their
+ * entries of page_table become -1 and their lengths 0.  Entries that are no page
+ * are left out, and so is what the stack cannot hold (pages given back twice);
+ * fa_status reports FA_ERR_BAD_BATCH for either, and for negative or too large lengths.
+ *
+ *   done : device, one byte a sequence.   Other arguments as fa_paged_extend's.
+ */
+int fa_paged_release(const fa_page_pool* pool, int* page_table, long long table_stride, int max_pages, int* kv_lens,
+                     const unsigned char* done, int B, void* stream);
+
+/*
+ * Cross attention: the rows of a ragged batch attend to the states of an
+ * encoder, of another length for each sequence, contiguous and without a causal
+ * mask; the formula at the top of this file with N_q and N_k of each sequence's
+ * own, and grouped heads.  (The pages' kernels have one length for all.)
+ *
+ * Sequence b has the rows cu_rows[b] .. cu_rows[b+1]-1 of the token-major
+ * tensors q, o, dout, dq and the places cu_keys[b] .. cu_keys[b+1]-1 of k, v,
+ * dk, dv; the first key_lens[b] of them are its keys (key_lens = NULL: all).  The
+ * arrays are read on the device only, so a captured graph replays with new
+ * contents.  A packed batch has key_lens = NULL; a padded one ([B][S][heads][d])
+ * has cu_keys[b] = b * S, and what lies in its padding is never seen, NaN included.
+ *
+ * What is not there is never touched: a row range outside [0, rows) or that
+ * decreases counts as no rows, places outside [0, keys) as no keys, a length below 0
+ * or beyond the places is cut; fa_status reports FA_ERR_BAD_BATCH and the results
+ * of that sequence are unspecified.  Sequences must not share rows, nor, in the backward pass, places.
+ */
+typedef struct fa_cross_batch {
+  const int* cu_rows;       /* device, [B + 1], cu_rows[0] >= 0, not decreasing                      */
+  const int* cu_keys;       /* device, [B + 1], cu_keys[0] >= 0, not decreasing                      */
+  const int* key_lens;      /* device, [B], or NULL                                                  */
+  int B;                    /* sequences, >= 1                                                       */
+  int rows;                 /* rows of q, 0 <= rows <= 2^31 - 4096 (0: nothing to attend)            */
+  int keys;                 /* rows of k and v, likewise (0: k and v may be NULL)                    */
+} fa_cross_batch;
+
+/* fa_cross_fwd_workspace_bytes - size of the device workspace of fa_cross_fwd
+ * for head dimension d.  It does not depend on any length.  0 for an unsupported d. */
+size_t fa_cross_fwd_workspace_bytes(int d);
+
+/*
+ * fa_cross_fwd - O and L of the rows.
+ *
+ *   q, o      : bf16, [rows] x q_heads x d, element (row, h, c) at row*s[0] + h*s[1] + c, s = q_stride /
+ *               o_stride: {row, head} element strides, multiples of 8; 16-byte aligned.
+ *   k, v      : bf16, [keys] x heads x d, likewise.  q_heads is a multiple of heads, at most 32
+ *               times as many: head h reads key/value head h / (q_heads / heads).
+ *   lse       : fp32 [q_heads][rows], contiguous (natural log).
+ *   d         : 32, 64, 128 or 256.
+ *   max_rows  : an upper bound of a sequence's rows, known to the host (it chooses the kernels).  Rows of a
+ *               sequence that has more are left as they are and fa_status reports FA_ERR_BAD_BATCH.
+ *   workspace : 256-byte aligned, at least fa_cross_fwd_workspace_bytes bytes; contents on entry
+ *               ignored.  Calls that may run at the same time need workspaces of their own.
+ *   Rows of a sequence without keys have o = 0 and L = -infinity; rows of no sequence are left as they are.
+ *   o and lse must not overlap each other or the inputs.
+ *
+ * Arithmetic: as fa_paged_fwd's on bf16 pages.  Results do not depend on what else runs.
+ */
+int fa_cross_fwd(const void* q, const long long* q_stride, const void* k, const long long* k_stride, const void* v,
+                 const long long* v_stride, const fa_cross_batch* batch, void* o, const long long* o_stride, float* lse,
+                 int q_heads, int heads, int d, int max_rows, float scale, void* workspace, size_t workspace_bytes,
+                 void* stream);
+
+/* fa_cross_bwd_workspace_bytes - size of the device workspace of fa_cross_bwd
+ * for B sequences and `rows` rows of all.  Returns 0 for invalid shapes. */
+size_t fa_cross_bwd_workspace_bytes(int B, int rows, int q_heads, int heads, int d);
+
+/*
+ * fa_cross_bwd - gradients of fa_cross_fwd's O with respect to q, k and v, given dout = dL/dO:
+ *   P = exp(scale q k^T - L),  D = sum_c dO O,  dS = P (dO v^T - D),
+ *   dq = scale dS k,  dk = scale sum over the group's heads of dS^T q,  dv = sum over them of P^T dO.
+ *
+ *   o, lse     : the outputs of fa_cross_fwd for q, k, v, scale and this batch.
+ *   dq, dk, dv : bf16, shaped like q, k, v.  Rows of no sequence and places of none are left as they are;
+ *                a sequence's places behind its keys get zeros, and so do its keys if it has no rows
+ *                and its rows if it has no keys.
+ *   strides    : host pointer to 16 element strides, {row, head} of q, k, v, o, dout, dq, dk, dv in this
+ *                order, each as in fa_cross_fwd.
+ *   workspace  : 256-byte aligned, at least fa_cross_bwd_workspace_bytes bytes, as in fa_cross_fwd.
+ *   Other arguments as fa_cross_fwd's.  The outputs must not overlap each other or the inputs.
+ *
+ * Arithmetic: as fa_bwd's (P and dS rounded to bf16 before their products, fp32 sums); deterministic.
+ */
+int fa_cross_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                 void* dq, void* dk, void* dv, const long long* strides, const fa_cross_batch* batch, int q_heads,
+                 int heads, int d, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * fa_status - synchronises `stream`, then reads and clears the device status
  * word of the current device, and the status word of fa_fwd_noalloc's static
  * scratch on that device.  Returns FA_OK, FA_ERR_TIMEOUT if a kernel
  * launched since the last call gave up on a bounded wait, FA_ERR_BAD_BATCH if
- * none did but one was given a batch that names what is not there, or
- * FA_ERR_CUDA if the synchronisation itself failed.
+ * none did but one was given a batch that names what is not there,
+ * FA_ERR_NO_PAGES if neither was so but fa_paged_extend had too few free pages,
+ * or FA_ERR_CUDA if the synchronisation itself failed.
  */
 int fa_status(void* stream);
 

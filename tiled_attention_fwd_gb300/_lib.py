@@ -35,6 +35,12 @@ _SIGNATURES = {
     "fa_paged_read": (_c_int, [_c_void_p] * 7),
     "fa_paged_fwd_workspace_bytes": (_c_size_t, [_c_int] * 3),
     "fa_paged_fwd": (_c_int, [_c_void_p] * 7 + [_c_int] * 2 + [_c_float, _c_int, _c_void_p, _c_size_t, _c_void_p]),
+    "fa_paged_extend": (_c_int, [_c_void_p] * 2 + [ctypes.c_longlong, _c_int] + [_c_void_p] * 5 + [_c_int] * 2 + [_c_void_p]),
+    "fa_paged_release": (_c_int, [_c_void_p] * 2 + [ctypes.c_longlong, _c_int] + [_c_void_p] * 2 + [_c_int, _c_void_p]),
+    "fa_cross_fwd_workspace_bytes": (_c_size_t, [_c_int]),
+    "fa_cross_fwd": (_c_int, [_c_void_p] * 10 + [_c_int] * 4 + [_c_float, _c_void_p, _c_size_t, _c_void_p]),
+    "fa_cross_bwd_workspace_bytes": (_c_size_t, [_c_int] * 5),
+    "fa_cross_bwd": (_c_int, [_c_void_p] * 11 + [_c_int] * 3 + [_c_float, _c_void_p, _c_size_t, _c_void_p]),
     "fa_status": (_c_int, [_c_void_p]),
     "fa_selftest_wait": (_c_int, [_c_void_p]),
     "fa_set_wait_limit_ms": (_c_int, [_c_int]),
@@ -202,6 +208,60 @@ def fa_paged_fwd(q, q_stride, cache, batch, o, o_stride, lse, q_heads, max_rows,
     return load().fa_paged_fwd(q, _strides2(q_stride), ctypes.byref(cache), ctypes.byref(batch), o,
                                _strides2(o_stride), lse, q_heads, max_rows, scale, int(bool(causal)), workspace,
                                workspace_bytes, stream)
+
+
+class CPagePool(ctypes.Structure):
+    """fa_page_pool: the stack of free pages."""
+
+    _fields_ = [("free_pages", _c_void_p), ("free_count", _c_void_p), ("num_pages", _c_int), ("page_size", _c_int)]
+
+
+class CCrossBatch(ctypes.Structure):
+    """fa_cross_batch: the sequences of a cross-attention call."""
+
+    _fields_ = [("cu_rows", _c_void_p), ("cu_keys", _c_void_p), ("key_lens", _c_void_p), ("B", _c_int), ("rows", _c_int),
+                ("keys", _c_int)]
+
+
+def fa_paged_extend(pool, page_table, table_stride, max_pages, kv_lens, new_rows, cu_rows, slots, positions, B, rows,
+                    stream) -> int:
+    """Pages, offsets, slots and positions of new rows; `pool` is a CPagePool, pointers are integers."""
+    return load().fa_paged_extend(ctypes.byref(pool), page_table, table_stride, max_pages, kv_lens, new_rows, cu_rows,
+                                  slots, positions, B, rows, stream)
+
+
+def fa_paged_release(pool, page_table, table_stride, max_pages, kv_lens, done, B, stream) -> int:
+    """The pages of sequences that are done, back onto the stack."""
+    return load().fa_paged_release(ctypes.byref(pool), page_table, table_stride, max_pages, kv_lens, done, B, stream)
+
+
+def fa_cross_fwd_workspace_bytes(d) -> int:
+    return load().fa_cross_fwd_workspace_bytes(d)
+
+
+def fa_cross_fwd(q, q_stride, k, k_stride, v, v_stride, batch, o, o_stride, lse, q_heads, heads, d, max_rows, scale,
+                 workspace, workspace_bytes, stream) -> int:
+    """Cross attention of a ragged batch; `batch` is a CCrossBatch, strides {row, head} pairs, pointers integers."""
+    return load().fa_cross_fwd(q, _strides2(q_stride), k, _strides2(k_stride), v, _strides2(v_stride),
+                               ctypes.byref(batch), o, _strides2(o_stride), lse, q_heads, heads, d, max_rows, scale,
+                               workspace, workspace_bytes, stream)
+
+
+def fa_cross_bwd_workspace_bytes(B, rows, q_heads, heads, d) -> int:
+    return load().fa_cross_bwd_workspace_bytes(B, rows, q_heads, heads, d)
+
+
+_Strides16 = ctypes.c_longlong * 16
+
+
+def fa_cross_bwd(q, k, v, o, lse, dout, dq, dk, dv, strides, batch, q_heads, heads, d, scale, workspace,
+                 workspace_bytes, stream) -> int:
+    """Its gradients; `strides` holds 8 {row, head} pairs (q, k, v, o, dout, dq, dk, dv)."""
+    flat = [x for st in strides for x in st]
+    if len(flat) != 16:
+        raise ValueError("strides must hold 8 pairs")
+    return load().fa_cross_bwd(q, k, v, o, lse, dout, dq, dk, dv, _Strides16(*flat), ctypes.byref(batch), q_heads, heads,
+                               d, scale, workspace, workspace_bytes, stream)
 
 
 def fa_status(stream) -> int:
@@ -456,18 +516,23 @@ def _paged_rows(t, name, cache, heads):
     return (s[0] if n[0] > 1 else head * n[1]), head
 
 
-def _paged_call(cache, fn, name, *args):
-    """fn(*args, stream) with the cache's device current, on its current stream."""
+def _call_on(index, fn, name, *args):
+    """fn(*args, stream) with device `index` current, on its current stream."""
     import torch
 
     # (torch.cuda.current_device and current_stream look the same up in 3 us, a fifth of a small step.)
-    if torch._C._cuda_getDevice() == cache._index:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(cache._index))
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(cache._index):
+        with torch.cuda.device(index):
             rc = fn(*args, torch.cuda.current_stream().cuda_stream)
     if rc != FA_OK:
         raise FAError(rc, name)
+
+
+def _paged_call(cache, fn, name, *args):
+    """fn(*args, stream) on the cache's device."""
+    _call_on(cache._index, fn, name, *args)
 
 
 def paged_write(cache, k, v, page_table, cu_rows, kv_lens):
@@ -555,8 +620,207 @@ def paged_forward(q, cache, page_table, cu_rows, kv_lens, max_rows=None, causal:
     return o, l
 
 
+class PagePool:
+    """The pages of a cache that no sequence has, as a stack on the GPU: the first free_count[0] entries of free_pages
+    (int32 [num_pages]) are free, the last of them is taken first.  ``PagePool.full`` makes one of all pages."""
+
+    def __init__(self, free_pages, free_count, page_size):
+        import torch
+
+        if free_pages.dtype is not torch.int32 or free_count.dtype is not torch.int32 or free_pages.dim() != 1 or \
+                free_count.numel() != 1 or not free_pages.is_contiguous() or free_pages.shape[0] == 0:
+            raise ValueError("free_pages must be a contiguous int32 tensor [num_pages] and free_count one int32")
+        if not free_pages.is_cuda or free_count.device != free_pages.device:
+            raise ValueError("free_pages and free_count must be CUDA tensors of one device")
+        self.free_pages, self.free_count, self.page_size = free_pages, free_count, int(page_size)
+        self.num_pages, self.device = free_pages.shape[0], free_pages.device
+        self._index, self._int32, self._int64 = free_pages.get_device(), torch.int32, torch.int64
+        self._c = CPagePool(free_pages.data_ptr(), free_count.data_ptr(), self.num_pages, self.page_size)
+
+    @classmethod
+    def full(cls, num_pages, page_size, device="cuda"):
+        """A pool in which every page is free; page 0 is taken first."""
+        import torch
+
+        return cls(torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   torch.full((1,), num_pages, dtype=torch.int32, device=device), page_size)
+
+
+def _pool_tables(pool, page_table, **vectors):
+    """Checks a call's int32 tables; returns (B, width, stride)."""
+    B, width = page_table.shape if page_table.dim() == 2 else (0, 0)
+    if B == 0 or width == 0 or page_table.dtype is not pool._int32 or page_table.get_device() != pool._index:
+        raise ValueError("page_table must be int32 [B, pages], B and pages at least 1, on the pool's device")
+    stride = page_table.stride()
+    if stride[1] != 1 and width > 1:
+        raise ValueError("the rows of page_table must be contiguous")
+    for name, (t, n) in vectors.items():
+        if t.dtype is not pool._int32 or tuple(t.shape) != (B + n,) or t.get_device() != pool._index or \
+                not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor [{'B + 1' if n else 'B'}] on the pool's device")
+    return B, width, stride[0] if B > 1 else width
+
+
+def paged_extend(pool, page_table, kv_lens, new_rows, rows=None, out=None):
+    """Lengthen sequence b by new_rows[b] tokens: pages from the pool into page_table (int32 [B, pages]), kv_lens (int32 [B])
+    advanced, both in place.  Returns (cu_rows int32 [B + 1], slots int64 [rows], positions int32 [rows]): what paged_write and
+    paged_forward read, and each new row's slot (page * page_size + position % page_size) and position.  ``rows``: how many
+    rows the caller's tensors have (a bound of the new ones, known to the host); or ``out`` = (cu_rows, slots, positions).
+    Rows behind cu_rows[B] are left as they are (-1 in new tensors).  A sequence is extended whole or, where pages, rows or its
+    row of page_table do not suffice, not at all; check_status then says why (include/fa_gb300.h).  Enqueued on the
+    current stream."""
+    import torch
+
+    if out is None:
+        if rows is None:
+            raise ValueError("paged_extend needs rows or out")
+        i32 = dict(dtype=torch.int32, device=pool.device)
+        out = (torch.empty(page_table.shape[0] + 1, **i32), torch.full((rows,), -1, dtype=torch.int64, device=pool.device),
+               torch.full((rows,), -1, **i32))
+    cu_rows, slots, positions = out
+    B, width, stride = _pool_tables(pool, page_table, kv_lens=(kv_lens, 0), new_rows=(new_rows, 0), cu_rows=(cu_rows, 1))
+    n = slots.shape
+    if len(n) != 1 or positions.shape != n or slots.dtype is not pool._int64 or positions.dtype is not pool._int32 or \
+            slots.get_device() != pool._index or positions.get_device() != pool._index or not slots.is_contiguous() or \
+            not positions.is_contiguous() or (rows is not None and rows != n[0]):
+        raise ValueError("slots and positions must be contiguous int64 and int32 tensors [rows] on the pool's device")
+    _call_on(pool._index, fa_paged_extend, "fa_paged_extend", pool._c, page_table.data_ptr(), stride, width,
+             kv_lens.data_ptr(), new_rows.data_ptr(), cu_rows.data_ptr(), slots.data_ptr(), positions.data_ptr(), B, n[0])
+    return cu_rows, slots, positions
+
+
+def paged_release(pool, page_table, kv_lens, done):
+    """End the sequences b with done[b] (bool or uint8 [B]): their pages go back to the pool, their entries of page_table become
+    -1 and their lengths 0, in place.  Returns the pool.  Enqueued on the current stream."""
+    B, width, stride = _pool_tables(pool, page_table, kv_lens=(kv_lens, 0))
+    if done.element_size() != 1 or done.is_floating_point() or tuple(done.shape) != (B,) or \
+            done.get_device() != pool._index or not done.is_contiguous():
+        raise ValueError("done must be a contiguous bool or uint8 tensor [B] on the pool's device")
+    _call_on(pool._index, fa_paged_release, "fa_paged_release", pool._c, page_table.data_ptr(), stride, width,
+             kv_lens.data_ptr(), done.data_ptr(), B)
+    return pool
+
+
+def _cross_rows(t, name, ref, heads=None, rows=None):
+    """Checks a token-major bf16 tensor [rows, heads, d] beside `ref`; returns its {row, head} strides."""
+    n = t.shape
+    if len(n) != 3 or t.dtype is not ref.dtype or t.get_device() != ref.get_device() or n[2] != ref.shape[2] or \
+            (heads is not None and n[1] != heads) or (rows is not None and n[0] != rows):
+        raise ValueError(f"{name} must be a bf16 tensor [rows, heads, d] on q's device, with its counterpart's shape")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    # Strides of dimensions of one element are never used; torch may report any value for them.
+    head = s[1] if n[1] > 1 else n[2]
+    return (s[0] if n[0] > 1 else head * n[1]), head
+
+
+def _cross_batch(q, k, cu_rows, cu_keys, key_lens):
+    """CCrossBatch of int32 tensors on q's device."""
+    import torch
+
+    if q.dim() != 3 or k.dim() != 3 or q.dtype is not torch.bfloat16 or not q.is_cuda or 0 in q.shape[1:] or 0 in k.shape[1:]:
+        raise ValueError("q must be a bf16 CUDA tensor [rows, q_heads, d] and k, v [keys, heads, d]")
+    n = cu_rows.shape
+    ts = (cu_rows, cu_keys) if key_lens is None else (cu_rows, cu_keys, key_lens)
+    if len(n) != 1 or n[0] < 2 or cu_keys.shape != n or (key_lens is not None and tuple(key_lens.shape) != (n[0] - 1,)):
+        raise ValueError("cu_rows and cu_keys must be [B + 1] and key_lens [B], B at least 1")
+    for t in ts:
+        if t.dtype is not torch.int32 or t.get_device() != q.get_device() or not t.is_contiguous():
+            raise ValueError("cu_rows, cu_keys and key_lens must be contiguous int32 tensors on q's device")
+    return CCrossBatch(cu_rows.data_ptr(), cu_keys.data_ptr(), None if key_lens is None else key_lens.data_ptr(), n[0] - 1,
+                       q.shape[0], k.shape[0])
+
+
+def _cross_ws(workspace, q):
+    if workspace.get_device() != q.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def cross_workspace(k):
+    """A workspace for cross_forward calls with keys like k ([keys, heads, d]; its size depends on d alone), one call at a time."""
+    import torch
+
+    return torch.empty(fa_cross_fwd_workspace_bytes(k.shape[2]), dtype=torch.uint8, device=k.device)
+
+
+def cross_forward(q, k, v, cu_rows, cu_keys, key_lens=None, max_rows=None, scale: float | None = None, out=None, lse=None,
+                  workspace=None):
+    """O, L = cross attention of a ragged batch: the rows of q (bf16 [rows, q_heads, d]) to k and v (bf16 [keys, heads, d]).
+
+    Sequence b has the rows cu_rows[b] .. cu_rows[b + 1] and the places cu_keys[b] .. cu_keys[b + 1] (int32 [B + 1]), of which
+    the first key_lens[b] (int32 [B]; default: all) are keys; all three are read on the device.  q_heads is a multiple of
+    heads, 32 times as many at most.  Any strides with a contiguous last dimension.  ``max_rows``: an upper bound of a sequence's rows (default: all rows of q; a
+    serving step passes 1).  Returns O (like q, contiguous unless ``out`` is given) and L fp32 [q_heads, rows]; rows of no
+    sequence are left as they are (zero in new tensors), rows without keys get O = 0 and L = -inf.  ``workspace``
+    (cross_workspace) is allocated here if not given.  Enqueued on the current stream.
+    """
+    import torch
+
+    batch = _cross_batch(q, k, cu_rows, cu_keys, key_lens)
+    rows, heads, d = q.shape
+    qs = _cross_rows(q, "q", q)
+    ks = _cross_rows(k, "k", q)
+    vs = _cross_rows(v, "v", q, k.shape[1], k.shape[0])
+    o = torch.zeros((rows, heads, d), dtype=torch.bfloat16, device=q.device) if out is None else out
+    os_ = _cross_rows(o, "out", q, heads, rows)
+    l = torch.zeros((heads, rows), dtype=torch.float32, device=q.device) if lse is None else lse
+    if l.shape != (heads, rows) or l.dtype is not torch.float32 or not l.is_contiguous() or l.get_device() != q.get_device():
+        raise ValueError("lse must be a contiguous fp32 tensor [q_heads, rows] on q's device")
+    if rows == 0:
+        return o, l
+    ws = _cross_ws(cross_workspace(q) if workspace is None else workspace, q)
+    _call_on(q.get_device(), fa_cross_fwd, "fa_cross_fwd", q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, batch,
+             o.data_ptr(), os_, l.data_ptr(), heads, k.shape[1], d, rows if max_rows is None else int(max_rows),
+             d ** -0.5 if scale is None else float(scale), *ws)
+    return o, l
+
+
+def cross_backward_workspace(q, k, B):
+    """A workspace for cross_backward calls of B sequences with tensors shaped like q and k, one call at a time."""
+    import torch
+
+    return torch.empty(fa_cross_bwd_workspace_bytes(B, q.shape[0], q.shape[1], k.shape[1], q.shape[2]), dtype=torch.uint8,
+                       device=q.device)
+
+
+def cross_backward(q, k, v, o, lse, dout, cu_rows, cu_keys, key_lens=None, scale: float | None = None, out=None,
+                   workspace=None):
+    """dQ, dK, dV of cross_forward, given its inputs and outputs (o, lse) and the upstream gradient dout (like q).
+
+    dK and dV sum over the query heads that share a key/value head; places behind a sequence's keys get zeros.  Returns bf16
+    tensors like q, k and v (``out`` = (dq, dk, dv) if given, else new ones); rows and places of no sequence are left as they
+    are (zero in new tensors).  ``workspace`` (cross_backward_workspace) is allocated here if not given.  Deterministic.
+    Enqueued on the current stream.
+    """
+    import torch
+
+    batch = _cross_batch(q, k, cu_rows, cu_keys, key_lens)
+    rows, heads, d = q.shape
+    keys, kv_heads = k.shape[:2]
+    if out is None:
+        out = tuple(torch.zeros(t.shape, dtype=torch.bfloat16, device=q.device) for t in (q, k, v))
+    dq, dk, dv = out
+    st = [_cross_rows(t, name, q, h, n) for t, name, h, n in
+          ((q, "q", heads, rows), (k, "k", kv_heads, keys), (v, "v", kv_heads, keys), (o, "o", heads, rows),
+           (dout, "dout", heads, rows), (dq, "out[0]", heads, rows), (dk, "out[1]", kv_heads, keys),
+           (dv, "out[2]", kv_heads, keys))]
+    if lse.shape != (heads, rows) or lse.dtype is not torch.float32 or not lse.is_contiguous() or \
+            lse.get_device() != q.get_device():
+        raise ValueError("lse must be a contiguous fp32 tensor [q_heads, rows] on q's device")
+    if rows == 0 and keys == 0:
+        return dq, dk, dv
+    ws = _cross_ws(cross_backward_workspace(q, k, batch.B) if workspace is None else workspace, q)
+    _call_on(q.get_device(), fa_cross_bwd, "fa_cross_bwd", q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+             lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), st, batch, heads, kv_heads, d,
+             d ** -0.5 if scale is None else float(scale), *ws)
+    return dq, dk, dv
+
+
 def check_status(device=None):
-    """Synchronise the current stream and raise FAError if a device wait timed out or a batch named what is not there."""
+    """Synchronise the current stream and raise FAError if a device wait timed out, a batch named what is not there or
+    paged_extend ran out of pages."""
     import torch
 
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)

@@ -583,8 +583,9 @@ int fa_status(void* stream) {
   if (word != 0 && cudaMemset(s->status, 0, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
   const int na = fa::noalloc_take_status();
   if (na == FA_ERR_CUDA) return FA_ERR_CUDA;
-  if ((word & ~fa::kBadBatchBit) != 0 || na == FA_ERR_TIMEOUT) return FA_ERR_TIMEOUT;
-  return word != 0 ? FA_ERR_BAD_BATCH : FA_OK;
+  if ((word & ~(fa::kBadBatchBit | fa::kNoPagesBit)) != 0 || na == FA_ERR_TIMEOUT) return FA_ERR_TIMEOUT;
+  if ((word & fa::kBadBatchBit) != 0) return FA_ERR_BAD_BATCH;
+  return word != 0 ? FA_ERR_NO_PAGES : FA_OK;
 }
 
 int fa_selftest_wait(void* stream) {
@@ -612,7 +613,8 @@ const char* fa_strerror(int code) {
     case FA_ERR_BAD_SCALE: return "FA_ERR_BAD_SCALE: scale (and every dequantisation factor) must be finite and > 0";
     case FA_ERR_WORKSPACE: return "FA_ERR_WORKSPACE: workspace too small";
     case FA_ERR_SCRATCH: return "FA_ERR_SCRATCH: the kernel needs more scratch than fa_fwd_noalloc's static array holds";
-    case FA_ERR_BAD_BATCH: return "FA_ERR_BAD_BATCH: page_table, cu_rows or kv_lens named what is not there";
+    case FA_ERR_BAD_BATCH: return "FA_ERR_BAD_BATCH: page_table, cu_rows or kv_lens (cu_keys, key_lens, new_rows) named what is not there";
+    case FA_ERR_NO_PAGES: return "FA_ERR_NO_PAGES: fa_paged_extend had too few free pages";
     default: return "unknown fa_gb300 error code";
   }
 }

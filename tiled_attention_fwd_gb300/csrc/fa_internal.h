@@ -86,6 +86,8 @@ int current_ctx(LaunchCtx* ctx, void* stream);
 
 // Bit of the device status word that stands for FA_ERR_BAD_BATCH (the others: expired waits).
 constexpr int kBadBatchBit = 1 << 4;
+// The same for FA_ERR_NO_PAGES.
+constexpr int kNoPagesBit = 1 << 5;
 
 // Resolve the driver's tensor-map encoder (no device state, no allocation).  Returns 0 on success.
 int load_tensor_map_encoder();
