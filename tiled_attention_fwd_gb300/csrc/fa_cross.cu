@@ -4,6 +4,7 @@
 
 #include "../../include/fa_gb300.h"
 #include "fa_cross.cuh"
+#include "fa_paged_plan.cuh"
 
 namespace fa {
 namespace {
@@ -27,47 +28,6 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // Simple kernels: one warp to a row of outputs, a block to a sequence (grid.y) at a time.
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) fa_cross_fwd_plain(const CrossArgs a, __nv_bfloat16* o, float* lse) {
-  __shared__ float s_q[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int b = blockIdx.y; b < a.cb.B; b += gridDim.y) {
-    bool bad;
-    const CrossSeq s = cross_seq(a.cb, b, bad);
-    if (bad || s.n > a.max_rows) atomicOr(a.status, kBadBatchBit);
-    if (s.n > a.max_rows) continue;
-    for (long long unit = blockIdx.x * kWarps + warp; unit < static_cast<long long>(s.n) * a.q_heads; unit += gridDim.x * kWarps) {
-      const long long t = s.row0 + unit / a.q_heads;
-      const int h = static_cast<int>(unit % a.q_heads), hk = h / a.group;
-      __syncwarp();
-      for (int c = lane; c < D; c += 32) s_q[warp][c] = __bfloat162float(a.q[t * a.st[0][0] + h * a.st[0][1] + c]);
-      __syncwarp();
-      float m = -INFINITY, l = 0.f, acc[D / 32] = {};
-      for (int j0 = 0; j0 < s.len; j0 += 32) {
-        const int j = j0 + lane;
-        float x = -INFINITY;
-        if (j < s.len) x = dot_row<D>(s_q[warp], a.k + (static_cast<long long>(s.key0) + j) * a.st[1][0] + hk * a.st[1][1]) * a.scale;
-        float top = x;
-        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-        const float m_new = fmaxf(m, top);
-        const float alpha = m_new == m ? 1.f : expf(m - m_new);
-        const float p = j < s.len ? expf(x - (m_new == -INFINITY ? 0.f : m_new)) : 0.f;
-        l = l * alpha + warp_sum(p);
-        m = m_new;
-        for (int c = 0; c < D / 32; ++c) acc[c] *= alpha;
-        for (int i = 0; i < min(32, s.len - j0); ++i) {
-          const float pi = __shfl_sync(0xffffffffu, p, i);
-          const __nv_bfloat16* v = a.v + (static_cast<long long>(s.key0) + j0 + i) * a.st[2][0] + hk * a.st[2][1];
-          for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(pi, __bfloat162float(v[c * 32 + lane]), acc[c]);
-        }
-      }
-      const float inv = s.len == 0 ? 0.f : 1.f / l;
-      for (int c = 0; c < D / 32; ++c) o[t * a.st[3][0] + h * a.st[3][1] + c * 32 + lane] = __float2bfloat16_rn(acc[c] * inv);
-      if (lane == 0) lse[static_cast<long long>(h) * a.cb.rows + t] = m + logf(l);
-    }
-  }
-}
-
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) fa_cross_dq_plain(const CrossArgs a) {
   __shared__ float s_q[kWarps][D], s_do[kWarps][D];
@@ -159,12 +119,21 @@ __global__ void __launch_bounds__(kWarps * 32) fa_cross_dkv_plain(const CrossArg
   }
 }
 
+// The forward pass is the paged attention's kernels on keys that lie packed: longer sequences (unless max_rows says that there are
+// none), then those of few rows, then what CTAs left in parts.
 template <int D>
-int launch_fwd_plain(const CrossArgs& a, void* o, float* lse, const LaunchCtx& ctx) {
-  const dim3 grid(16, a.cb.B < 1024 ? a.cb.B : 1024);
-  fa_cross_fwd_plain<D><<<grid, kWarps * 32, 0, ctx.stream>>>(a, static_cast<__nv_bfloat16*>(o), lse);
-  return static_cast<int>(cudaGetLastError());
+int launch_fwd_d(PagedFwdArgs& a, const LaunchCtx& ctx) {
+  const long long most = static_cast<long long>(a.max_rows) * a.group;
+  // 8 or 16 rows where that is all there can be, else 32 (d = 256: 16), as fa_paged_fwd.
+  a.few_rows = most <= 8 ? 8 : most <= 16 || D == 256 ? 16 : kFewMost;
+  a.few_sets = 1;
+  const bool chunks = most > a.few_rows;
+  int e = chunks ? launch_paged_chunk<D, true>(a, ctx) : 0;
+  if (e == 0) e = launch_paged_few<D, true>(a, chunks, ctx);
+  if (e == 0) e = launch_paged_join<D, true>(a, chunks, ctx);
+  return e;
 }
+
 template <int D>
 int launch_bwd_plain(const CrossArgs& a, const LaunchCtx& ctx) {
   const dim3 grid(16, a.cb.B < 1024 ? a.cb.B : 1024);
@@ -206,7 +175,7 @@ int take(const fa_cross_batch* b, int q_heads, int heads, int d, float scale, Cr
 
 extern "C" {
 
-size_t fa_cross_fwd_workspace_bytes(int d) { return d == 32 || d == 64 || d == 128 || d == 256 ? 256 : 0; }
+size_t fa_cross_fwd_workspace_bytes(int d) { return d == 32 || d == 64 || d == 128 || d == 256 ? fa::paged_ws_bytes(d) : 0; }
 
 int fa_cross_fwd(const void* q, const long long* q_stride, const void* k, const long long* k_stride, const void* v,
                  const long long* v_stride, const fa_cross_batch* batch, void* o, const long long* o_stride, float* lse,
@@ -222,8 +191,6 @@ int fa_cross_fwd(const void* q, const long long* q_stride, const void* k, const 
   for (int i = 0; i < 4; ++i) {
     rc = fa::check_strides(st[i], 2);
     if (rc != FA_OK) return rc;
-    a.st[i][0] = st[i][0];
-    a.st[i][1] = st[i][1];
   }
   if (fa::misaligned(q, 16) || fa::misaligned(k, 16) || fa::misaligned(v, 16) || fa::misaligned(o, 16) ||
       fa::misaligned(lse, 4) || fa::misaligned(workspace, 256))
@@ -232,17 +199,35 @@ int fa_cross_fwd(const void* q, const long long* q_stride, const void* k, const 
   fa::LaunchCtx ctx;
   rc = fa::current_ctx(&ctx, stream);
   if (rc != FA_OK || batch->rows == 0) return rc;
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.k = static_cast<const __nv_bfloat16*>(k);
-  a.v = static_cast<const __nv_bfloat16*>(v);
-  a.max_rows = max_rows;
-  a.status = ctx.status;
+  fa::PagedFwdArgs p = {};
+  // (Without keys the tensor maps are made of something that is there; nothing is read through them.)
+  p.kv.k = const_cast<void*>(batch->keys > 0 ? k : workspace);
+  p.kv.v = const_cast<void*>(batch->keys > 0 ? v : workspace);
+  for (int i = 0; i < 2; ++i) {
+    p.qs[i] = q_stride[i];
+    p.kv.ks[i] = k_stride[i];
+    p.kv.vs[i] = v_stride[i];
+    p.os[i] = o_stride[i];
+  }
+  p.kv.heads = heads;
+  p.pb.B = batch->B;
+  p.pb.rows = batch->rows;
+  p.cb = a.cb;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.q_heads = q_heads;
+  p.group = a.group;
+  p.max_rows = max_rows;
+  p.scale = scale;
+  p.d = d;
+  p.workspace = static_cast<char*>(workspace);
   int e;
   switch (d) {
-    case 32: e = fa::launch_fwd_plain<32>(a, o, lse, ctx); break;
-    case 64: e = fa::launch_fwd_plain<64>(a, o, lse, ctx); break;
-    case 128: e = fa::launch_fwd_plain<128>(a, o, lse, ctx); break;
-    default: e = fa::launch_fwd_plain<256>(a, o, lse, ctx); break;
+    case 32: e = fa::launch_fwd_d<32>(p, ctx); break;
+    case 64: e = fa::launch_fwd_d<64>(p, ctx); break;
+    case 128: e = fa::launch_fwd_d<128>(p, ctx); break;
+    default: e = fa::launch_fwd_d<256>(p, ctx); break;
   }
   return e == 0 ? FA_OK : FA_ERR_CUDA;
 }

@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fa_cross.cuh"
 #include "fa_internal.h"
 #include "ptx.cuh"
 
@@ -45,11 +46,12 @@ struct PagedSeq {
   int row0;  // first row
   int n;     // rows
   int len;   // tokens, cut to what the page table can hold
+  int key0;  // packed keys: the first one's row of k and v
 };
 
 // Sequence b, cut to what is there; `bad` is set if anything had to be.
 __host__ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& pb, int ps_log2, int b, bool& bad) {
-  PagedSeq s;
+  PagedSeq s = {};
   const int lo = pb.cu_rows[b], hi = pb.cu_rows[b + 1];
   int len = pb.kv_lens[b];
   const long long most = static_cast<long long>(pb.max_pages) << ps_log2;
@@ -80,6 +82,17 @@ __device__ __forceinline__ void paged_report(const PagedBatch& pb, int ps_log2, 
   if (any) atomicOr(status, kStatusBadBatch);
 }
 
+// Sequence b of a paged batch, or of packed keys.
+template <bool PACKED>
+__host__ __device__ __forceinline__ PagedSeq attn_seq(const PagedBatch& pb, const CrossBatch& cb, int ps_log2, int b, bool& bad) {
+  if constexpr (PACKED) {
+    const CrossSeq c = cross_seq(cb, b, bad);
+    return PagedSeq{c.row0, c.n, c.len, c.key0};
+  } else {
+    return paged_seq(pb, ps_log2, b, bad);
+  }
+}
+
 // Page of position pos of sequence b, or -1 if the table names none that exists.
 __host__ __device__ __forceinline__ int paged_page(const PagedBatch& pb, const PagedKv& kv, int b, int pos) {
   const int page = pb.page_table[b * pb.table_stride + (pos >> kv.ps_log2)];
@@ -99,10 +112,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
   return r;
 }
 
-// Arguments of the attention kernels.
+// Arguments of the attention kernels.  They read K and V from pages, or (PACKED) from rows that lie one after another: then
+// the sequences are cb's, kv.k, kv.v, kv.ks, kv.vs ({row, head} strides) and kv.heads say where the rows are, and of pb only B and rows count.
 struct PagedFwdArgs {
   PagedKv kv;
   PagedBatch pb;
+  CrossBatch cb;
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;  // [q_heads][rows]

@@ -79,7 +79,7 @@ struct alignas(16) ChunkSeg {
   int head;   // key/value head
   int row0;   // row of the block's first token
   int ntok;   // tokens of the block
-  int pos0;   // position of its first token
+  int pos0;   // position of its first token; packed keys: row of the sequence's first key
   int len;    // tokens of the sequence
   int j0;     // first key tile
   int n0;     // key tiles of query tile 0 in this segment (they start at j0)
@@ -224,7 +224,7 @@ __host__ __device__ __forceinline__ ChunkBlocks chunk_blocks(const ChunkParams& 
 
 // ------------------------------------------------------------------ segments
 // The load warp's walk over its CTA's share.
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool PACKED>
 struct ChunkWalk {
   using C = ChunkCfg<D, E4M3>;
   int b, q, head, j, nt;
@@ -235,7 +235,7 @@ struct ChunkWalk {
   int record_q;         // its query block
   __host__ __device__ __forceinline__ void load(const ChunkParams& p) {
     bool bad;
-    s = paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad);
+    s = attn_seq<PACKED>(p.a.pb, p.a.cb, p.a.kv.ps_log2, b, bad);
     c = chunk_blocks<D, E4M3>(p, s);
   }
   // On to the next unit, if the share reaches it.
@@ -264,7 +264,7 @@ struct ChunkWalk {
     g.head = head;
     g.row0 = s.row0 + q * c.tq;
     g.ntok = ntok;
-    g.pos0 = s.len - s.n + q * c.tq;
+    g.pos0 = PACKED ? s.key0 : s.len - s.n + q * c.tq;
     g.len = s.len;
     g.j0 = j;
     g.nmax = n;
@@ -310,10 +310,11 @@ __device__ __forceinline__ bool seg_read(ChunkSeg& g, int k, uint8_t* gbase, con
 struct ChunkTile {
   int kind;  // 0: none, 1: K, 2: V
   int b, head, key0, len;
+  int base;  // packed keys: row of the sequence's first key
 };
 template <int D>
 __device__ __forceinline__ ChunkTile chunk_tile(int kind, const ChunkSeg& g, int j) {
-  return ChunkTile{kind, g.b, g.head, (g.j0 + j) * TcCfg<D>::BK, g.len};
+  return ChunkTile{kind, g.b, g.head, (g.j0 + j) * TcCfg<D>::BK, g.len, g.pos0};
 }
 
 // The order in which stages are filled and read (see tc_producer): get(k, seg)
@@ -322,7 +323,7 @@ __device__ __forceinline__ ChunkTile chunk_tile(int kind, const ChunkSeg& g, int
 template <int D, class Get, class Unit, class Stage>
 __device__ __forceinline__ bool chunk_stream(const Get& get, const Unit& unit, const Stage& stage) {
   using C = TcCfg<D>;
-  const ChunkTile none{0, 0, 0, 0, 0};
+  const ChunkTile none{0, 0, 0, 0, 0, 0};
   ChunkSeg w;
   if (!get(0, w)) return false;
 #pragma unroll 1
@@ -434,9 +435,36 @@ __device__ __forceinline__ bool chunk_load_stage(const CUtensorMap* tm_k, const 
   return true;
 }
 
+// The same of packed keys: whole tiles (behind the last key: the next sequence's, or zeros behind the tensor); lane i loads
+// position i.
+template <int D>
+__device__ __forceinline__ bool chunk_load_packed(const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                                  const ChunkBars<D, false>& bar, uint32_t base, uint32_t pos, int which,
+                                                  const ChunkTile& t0, const ChunkTile& t1, ChunkLoaded& done,
+                                                  const WaitGuard& g) {
+  using C = ChunkCfg<D, false>;
+  const int lane = threadIdx.x & 31;
+  const uint64_t pol_kv = policy_evict_last();
+  const int st = pos % C::NST;
+  const uint32_t full = bar.kv_full(st), par = (pos / C::NST) & 1;
+  const bool has0 = which & 1, has1 = (which & 2) && t1.kind;
+  if (!chunk_wait(bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
+  if (lane == 0) mbar_arrive_expect_tx(full, (has0 + has1) * C::KV_TILE);
+  __syncwarp();
+  if (lane == 0 ? has0 : lane == 1 && has1) {
+    const ChunkTile& t = lane == 0 ? t0 : t1;
+    const uint32_t dst = base + C::OFF_KV + st * C::STAGE + lane * C::KV_TILE;
+    for (int r = 0; r < C::NR; ++r)
+      tma_load_3d(dst + r * C::K_REGION, t.kind == 1 ? tm_k : tm_v, full, r * C::RC, t.head, t.base + t.key0, pol_kv);
+  }
+  done.issued |= 1u << st;
+  done.last_par = (done.last_par & ~(1u << st)) | (par << st);
+  return true;
+}
+
 // The load warp, or the second one (bf16), which reads the segments that the first finds and loads the tiles at
 // position 1.
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool PACKED>
 __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                            const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint32_t base,
                                            uint8_t* gbase, const PlanShare& share, bool second, const WaitGuard& g) {
@@ -448,7 +476,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
   int last_q = -1;           // latest segment whose Q tiles were loaded
   bool recorded = false;
 
-  ChunkWalk<D, E4M3> walk;
+  ChunkWalk<D, E4M3, PACKED> walk;
   walk.pos = share.start;
   walk.end = share.end;
   if (walk.pos < walk.end && !second) {
@@ -514,9 +542,14 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
     return true;
   };
   auto stage = [&](const ChunkTile& t0, const ChunkTile& t1) -> bool {
-    if (!chunk_load_stage<D, E4M3>(tm_k, tm_v, p, bar, base, pos, C::LOADERS == 1 ? 3 : second ? 2 : 1, t0, t1, done, g)) return false;
+    const int which = C::LOADERS == 1 ? 3 : second ? 2 : 1;
+    bool ok;
+    if constexpr (PACKED)
+      ok = chunk_load_packed<D>(tm_k, tm_v, bar, base, pos, which, t0, t1, done, g);
+    else
+      ok = chunk_load_stage<D, E4M3>(tm_k, tm_v, p, bar, base, pos, which, t0, t1, done, g);
     ++pos;
-    return true;
+    return ok;
   };
   chunk_stream<D>(get, unit, stage);
   if (lane == 0 && !recorded && !second) p.ws.chunk_rec[blockIdx.x].b = -1;
@@ -1216,7 +1249,7 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUt
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool PACKED = false>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     fa_paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -1279,7 +1312,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
       p.a.pb.B, gridDim.x, blockIdx.x,
       [&](int b) -> long long {
         bool bad;
-        const ChunkBlocks c = chunk_blocks<D, E4M3>(p, paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad));
+        const ChunkBlocks c = chunk_blocks<D, E4M3>(p, attn_seq<PACKED>(p.a.pb, p.a.cb, p.a.kv.ps_log2, b, bad));
         return c.n == 0 ? 0 : p.a.kv.heads * c.before(c.count());
       },
       1 + C::UNIT_COST,
@@ -1299,7 +1332,7 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
   } else {
     if constexpr (C::SPLIT_REGS) regs_decrease<C::REG_CORR_OTHER - C::reg_corr(false)>();
     if (warp >= C::LOAD_WARP && warp < C::LOAD_WARP + C::LOADERS)
-      chunk_load<D, E4M3>(&tm_q, &tm_k, &tm_v, p, bar, base, gbase, share, warp > C::LOAD_WARP, g);
+      chunk_load<D, E4M3, PACKED>(&tm_q, &tm_k, &tm_v, p, bar, base, gbase, share, warp > C::LOAD_WARP, g);
     if (warp == C::MMA_WARP) chunk_mma<D, E4M3>(p, bar, base, gbase, tmem, g);
     if constexpr (E4M3)
       if (warp >= C::CONV_WARP0)
@@ -1327,7 +1360,7 @@ struct JoinParams {
 };
 
 // Joins the parts of the units that several CTAs held; blocks (c, .) those of the unit that CTA c began.
-template <int D>
+template <int D, bool PACKED = false>
 __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constant__ JoinParams p) {
   __shared__ float s_o[3][D];
   pdl_wait();
@@ -1339,7 +1372,7 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
       // A warp takes 16 columns of 32 rows, a row a lane (parts hold blocks of 4 columns of all rows of a tile).
       constexpr int ROWS = chunk_rows(D);
       bool bad;
-      const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, rec.b, bad);
+      const PagedSeq s = attn_seq<PACKED>(a.pb, a.cb, a.kv.ps_log2, rec.b, bad);
       constexpr size_t stride = 2 * part_floats(ROWS, D);  // from one CTA's parts to the next's
       const float* first = p.ws.chunk_part + blockIdx.x * stride + stride / 2;
       const float* rest = first + stride / 2 - stride;  // part 0 of CTA + i at rest + i * stride
@@ -1389,7 +1422,7 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
     const PlanRecord rec = p.ws.few_rec[set][blockIdx.x];
     if (rec.b < 0) continue;
     bool bad;
-    const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, rec.b, bad);
+    const PagedSeq s = attn_seq<PACKED>(a.pb, a.cb, a.kv.ps_log2, rec.b, bad);
     constexpr size_t stride = 2 * part_floats(kFewMost, D);
     const float* first = p.ws.few_part[set] + blockIdx.x * stride + stride / 2;
     const float* rest = first + stride / 2 - stride;
@@ -1449,18 +1482,18 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
   }
 }
 
-template <int D>
+template <int D, bool PACKED>
 int launch_paged_join(const PagedFwdArgs& a, bool chunks, const LaunchCtx& ctx) {
   const int ctas = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
   const JoinParams p{a, paged_ws(a.workspace, D), chunks, a.few_sets, 128 / a.group};
-  return launch_dependent(fa_paged_join_kernel<D>, dim3(ctas, 16), 128, 0, ctx.stream, p);
+  return launch_dependent(fa_paged_join_kernel<D, PACKED>, dim3(ctas, 16), 128, 0, ctx.stream, p);
 }
 
 // ------------------------------------------------------------------ launch
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool PACKED>
 int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   using C = ChunkCfg<D, E4M3>;
-  auto kernel = fa_paged_chunk_kernel<D, E4M3>;
+  auto kernel = fa_paged_chunk_kernel<D, E4M3, PACKED>;
   if constexpr (C::SPLIT_REGS) {
     // The register split is sized for exactly LAUNCH_REGS a thread (see launch_tc_impl).
     static std::atomic<int> checked_regs{-1};
@@ -1496,20 +1529,29 @@ int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   const long long ost[2] = {a.os[1], a.os[0]};
   mo = mq;
   if (p.tma_o && encode_paged_map(&mo, a.o, 2, qdims, ost, 32, oh, 32 / oh, 64, false) != 0) return -1;
-  const long long dims[4] = {D, 1LL << a.kv.ps_log2, a.kv.heads, a.kv.num_pages};
-  const long long ks[3] = {a.kv.ks[2], a.kv.ks[1], a.kv.ks[0]}, vs[3] = {a.kv.vs[2], a.kv.vs[1], a.kv.vs[0]};
-  // bf16: 64-column regions in the operand layout; e4m3: rows of codes, 128 columns at a time, unswizzled.
-  const int cols = E4M3 ? C::CODE_COLS : C::RC, swizzle = E4M3 ? 0 : C::SWB;
-  if (encode_paged_map(&mk, a.kv.k, E4M3 ? 1 : 2, dims, ks, cols, p.box, 1, swizzle, true) != 0) return -1;
-  if (encode_paged_map(&mv, a.kv.v, E4M3 ? 1 : 2, dims, vs, cols, p.box, 1, swizzle, true) != 0) return -1;
+  if constexpr (PACKED) {
+    const long long dims[3] = {D, a.kv.heads, a.cb.keys > 0 ? a.cb.keys : 1};
+    const long long ks[2] = {a.kv.ks[1], a.kv.ks[0]}, vs[2] = {a.kv.vs[1], a.kv.vs[0]};
+    if (encode_paged_map(&mk, a.kv.k, 2, dims, ks, C::RC, 1, C::BK, C::SWB, false) != 0) return -1;
+    if (encode_paged_map(&mv, a.kv.v, 2, dims, vs, C::RC, 1, C::BK, C::SWB, false) != 0) return -1;
+  } else {
+    const long long dims[4] = {D, 1LL << a.kv.ps_log2, a.kv.heads, a.kv.num_pages};
+    const long long ks[3] = {a.kv.ks[2], a.kv.ks[1], a.kv.ks[0]}, vs[3] = {a.kv.vs[2], a.kv.vs[1], a.kv.vs[0]};
+    // bf16: 64-column regions in the operand layout; e4m3: rows of codes, 128 columns at a time, unswizzled.
+    const int cols = E4M3 ? C::CODE_COLS : C::RC, swizzle = E4M3 ? 0 : C::SWB;
+    if (encode_paged_map(&mk, a.kv.k, E4M3 ? 1 : 2, dims, ks, cols, p.box, 1, swizzle, true) != 0) return -1;
+    if (encode_paged_map(&mv, a.kv.v, E4M3 ? 1 : 2, dims, vs, cols, p.box, 1, swizzle, true) != 0) return -1;
+  }
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
   kernel<<<grid, C::THREADS, C::SMEM_CHUNK, ctx.stream>>>(mq, mk, mv, mo, p);
   return static_cast<int>(cudaGetLastError());
 }
 
-template <int D>
+template <int D, bool PACKED>
 int launch_paged_chunk(const PagedFwdArgs& a, const LaunchCtx& ctx) {
-  return a.e4m3 ? launch_paged_chunk_impl<D, true>(a, ctx) : launch_paged_chunk_impl<D, false>(a, ctx);
+  if constexpr (!PACKED)
+    if (a.e4m3) return launch_paged_chunk_impl<D, true, false>(a, ctx);
+  return launch_paged_chunk_impl<D, false, PACKED>(a, ctx);
 }
 
 }  // namespace fa

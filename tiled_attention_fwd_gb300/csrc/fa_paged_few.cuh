@@ -164,13 +164,13 @@ __device__ __forceinline__ long long few_length(const FewParams& p, const PagedS
 }
 
 // Walks the tiles of a CTA's share; `left`: what is left of it on the line (0: no more tiles).
-template <int KT>
+template <int KT, bool PACKED>
 struct FewCursor {
   int b, head, j, nt, left;
   PagedSeq s;
   __device__ __forceinline__ void load(const FewParams& p) {
     bool bad;
-    s = paged_seq(p.a.pb, p.a.kv.ps_log2, b, bad);
+    s = attn_seq<PACKED>(p.a.pb, p.a.cb, p.a.kv.ps_log2, b, bad);
     nt = few_tiles<KT>(p, s);
   }
   __device__ __forceinline__ void start(const FewParams& p, const PlanShare& w) {
@@ -203,7 +203,7 @@ struct FewCursor {
   }
 };
 
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, bool PACKED = false>
 __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
     fa_paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ FewParams p) {
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
     bool any = false;
     for (int b = threadIdx.x; b < a.pb.B; b += C::THREADS) {
       bool bad;
-      const PagedSeq s = paged_seq(a.pb, a.kv.ps_log2, b, bad);
+      const PagedSeq s = attn_seq<PACKED>(a.pb, a.cb, a.kv.ps_log2, b, bad);
       any = any || bad || s.n > a.max_rows;
     }
     if (any) atomicOr(p.status, kStatusBadBatch);
@@ -242,13 +242,13 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
       a.pb.B, gridDim.x, blockIdx.x,
       [&](int b) -> long long {
         bool bad;
-        return few_length<C::KT>(p, paged_seq(a.pb, a.kv.ps_log2, b, bad));
+        return few_length<C::KT>(p, attn_seq<PACKED>(a.pb, a.cb, a.kv.ps_log2, b, bad));
       },
       1 + kFewUnitCost,
       *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
 
   // ---- the warp's loads
-  FewCursor<C::KT> ahead;  // next group to load
+  FewCursor<C::KT, PACKED> ahead;  // next group to load
   ahead.start(p, share);
   uint32_t issued = 0, done = 0;
   const int box_log2 = p.box_log2;
@@ -270,6 +270,20 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
     const int key0 = ahead.j * C::KT + warp * C::KG;
     const uint32_t st = issued % C::S;
     const uint32_t bar = bars + 8 * st;
+    if constexpr (PACKED) {
+      // One box of the group's keys (behind the last one: the next sequence's, or zeros behind the tensor); lanes 0 and 1 load K and V.
+      if (lane == 0) mbar_arrive_expect_tx(bar, 2 * C::KV);
+      __syncwarp();
+      if (lane < 2) {
+#pragma unroll
+        for (int r = 0; r < C::REGIONS; ++r)
+          tma_load_3d(ring + (st * 2 + lane) * C::KV + r * C::REGION, lane ? &tm_v : &tm_k, bar, r * (C::SWB / C::EB), ahead.head,
+                      ahead.s.key0 + key0, policy);
+      }
+      ++issued;
+      ahead.advance(p, 1);
+      return;
+    }
     // Boxes that hold keys of the sequence; lanes 2i and 2i + 1 load K and V of box i.
     const int nbox = NG == 1 ? 1 : (min(C::KG, ahead.s.len - key0) + (1 << box_log2) - 1) >> box_log2;
     if (lane == 0) mbar_arrive_expect_tx(bar, 2 * (nbox << box_log2) * (C::ROWB + (E4M3 ? 1 : 0)));
@@ -302,7 +316,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
   for (int i = 0; i < C::S; ++i) issue();
 
   // ---- units
-  FewCursor<C::KT> at;
+  FewCursor<C::KT, PACKED> at;
   at.start(p, share);
   bool ok = true;
   bool recorded = false;
@@ -884,10 +898,10 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
   pdl_wait();  // what waits for this kernel waits for the chunks' kernel before it, too
 }
 
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, bool PACKED>
 int launch_paged_few_impl(const PagedFwdArgs& a, int set, int from, int most, bool behind, const LaunchCtx& ctx) {
   using C = FewCfg<D, E4M3, NT>;
-  auto kernel = fa_paged_few_kernel<D, E4M3, NT>;
+  auto kernel = fa_paged_few_kernel<D, E4M3, NT, PACKED>;
   static std::atomic<unsigned long long> allowed{0};
   const int e = allow_smem(kernel, C::SMEM, allowed);
   if (e != 0) return e;
@@ -904,10 +918,17 @@ int launch_paged_few_impl(const PagedFwdArgs& a, int set, int from, int most, bo
   for (p.box_log2 = 4; (1 << p.box_log2) < box; ++p.box_log2) {
   }
   CUtensorMap mk, mv;
-  const long long dims[4] = {D, 1LL << a.kv.ps_log2, a.kv.heads, a.kv.num_pages};
-  const long long ks[3] = {a.kv.ks[2], a.kv.ks[1], a.kv.ks[0]}, vs[3] = {a.kv.vs[2], a.kv.vs[1], a.kv.vs[0]};
-  if (encode_paged_map(&mk, a.kv.k, C::EB, dims, ks, C::SWB / C::EB, box, 1, C::SWB, true) != 0) return -1;
-  if (encode_paged_map(&mv, a.kv.v, C::EB, dims, vs, C::SWB / C::EB, box, 1, C::SWB, true) != 0) return -1;
+  if constexpr (PACKED) {
+    const long long dims[3] = {D, a.kv.heads, a.cb.keys > 0 ? a.cb.keys : 1};
+    const long long ks[2] = {a.kv.ks[1], a.kv.ks[0]}, vs[2] = {a.kv.vs[1], a.kv.vs[0]};
+    if (encode_paged_map(&mk, a.kv.k, 2, dims, ks, C::SWB / 2, 1, C::KG, C::SWB, false) != 0) return -1;
+    if (encode_paged_map(&mv, a.kv.v, 2, dims, vs, C::SWB / 2, 1, C::KG, C::SWB, false) != 0) return -1;
+  } else {
+    const long long dims[4] = {D, 1LL << a.kv.ps_log2, a.kv.heads, a.kv.num_pages};
+    const long long ks[3] = {a.kv.ks[2], a.kv.ks[1], a.kv.ks[0]}, vs[3] = {a.kv.vs[2], a.kv.vs[1], a.kv.vs[0]};
+    if (encode_paged_map(&mk, a.kv.k, C::EB, dims, ks, C::SWB / C::EB, box, 1, C::SWB, true) != 0) return -1;
+    if (encode_paged_map(&mv, a.kv.v, C::EB, dims, vs, C::SWB / C::EB, box, 1, C::SWB, true) != 0) return -1;
+  }
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
   if (behind) return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM, ctx.stream, mk, mv, p);
   kernel<<<grid, C::THREADS, C::SMEM, ctx.stream>>>(mk, mv, p);
@@ -922,12 +943,13 @@ int launch_paged_few_impl(const PagedFwdArgs& a, int set, int from, int most, bo
 //   2 to 8 new tokens a sequence   33 / 43  46 / 61  72 / 75  89 / 92  149 / 139 259 / 233 500 / 456
 //   1, rarely 8                    29 / 34  44 / 43  70 / 60  86 / 79  149 / 119 260 / 183 492 / 330
 //   5 to 8 (all in the first)      34 / 38  47 / 51  75 / 79  92 / 96  150 / 155 263 / 264 502 / 508
-template <int D>
+template <int D, bool PACKED>
 int launch_paged_few(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx) {
   auto launch = [&](auto nt, int set, int from, int most, bool behind) -> int {
     constexpr int NT = decltype(nt)::value;
-    return a.e4m3 ? launch_paged_few_impl<D, true, NT>(a, set, from, most, behind, ctx)
-                  : launch_paged_few_impl<D, false, NT>(a, set, from, most, behind, ctx);
+    if constexpr (!PACKED)
+      if (a.e4m3) return launch_paged_few_impl<D, true, NT, false>(a, set, from, most, behind, ctx);
+    return launch_paged_few_impl<D, false, NT, PACKED>(a, set, from, most, behind, ctx);
   };
   using std::integral_constant;
   if (a.few_rows <= 8) return launch(integral_constant<int, 1>{}, 0, 0, 8, behind_chunks);

@@ -149,11 +149,11 @@ __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepc
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Entry points of the attention kernels' translation units; each returns a cudaError_t-like code.
-template <int D>
+template <int D, bool PACKED = false>
 int launch_paged_few(const PagedFwdArgs& a, bool behind_chunks, const LaunchCtx& ctx);
-template <int D>
+template <int D, bool PACKED = false>
 int launch_paged_chunk(const PagedFwdArgs& a, const LaunchCtx& ctx);
-template <int D>
+template <int D, bool PACKED = false>
 int launch_paged_join(const PagedFwdArgs& a, bool chunks, const LaunchCtx& ctx);
 
 // Launch behind the stream's previous kernel, which may still run: the kernel waits for it itself (pdl_wait).
