@@ -468,8 +468,8 @@ typedef struct fa_cross_batch {
   const int* cu_keys;       /* device, [B + 1], cu_keys[0] >= 0, not decreasing                      */
   const int* key_lens;      /* device, [B], or NULL                                                  */
   int B;                    /* sequences, >= 1                                                       */
-  int rows;                 /* rows of q, 0 <= rows <= 2^31 - 4096 (0: nothing to attend)            */
-  int keys;                 /* rows of k and v, likewise (0: k and v may be NULL)                    */
+  int rows;                 /* rows of q, 0 <= rows, rows + B <= 2^31 - 4096                          */
+  int keys;                 /* rows of k and v, 0 .. 2^31 - 4096 (0: k and v may be NULL)             */
 } fa_cross_batch;
 
 /* fa_cross_fwd_workspace_bytes - size of the device workspace of fa_cross_fwd

@@ -9,116 +9,6 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
-
-template <int D>
-__device__ __forceinline__ float dot_row(const float* x, const __nv_bfloat16* y) {
-  float sum = 0.f;
-  for (int c = 0; c < D; c += 2) {
-    const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(y + c));
-    sum = fmaf(x[c], v.x, fmaf(x[c + 1], v.y, sum));
-  }
-  return sum;
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-  return x;
-}
-
-// Simple kernels: one warp to a row of outputs, a block to a sequence (grid.y) at a time.
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) fa_cross_dq_plain(const CrossArgs a) {
-  __shared__ float s_q[kWarps][D], s_do[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int b = blockIdx.y; b < a.cb.B; b += gridDim.y) {
-    bool bad;
-    const CrossSeq s = cross_seq(a.cb, b, bad);
-    if (bad) atomicOr(a.status, kBadBatchBit);
-    for (long long unit = blockIdx.x * kWarps + warp; unit < static_cast<long long>(s.n) * a.q_heads; unit += gridDim.x * kWarps) {
-      const long long t = s.row0 + unit / a.q_heads;
-      const int h = static_cast<int>(unit % a.q_heads), hk = h / a.group;
-      __syncwarp();
-      float dsum = 0.f;
-      for (int c = lane; c < D; c += 32) {
-        s_q[warp][c] = __bfloat162float(a.q[t * a.st[0][0] + h * a.st[0][1] + c]);
-        s_do[warp][c] = __bfloat162float(a.dout[t * a.st[4][0] + h * a.st[4][1] + c]);
-        dsum = fmaf(s_do[warp][c], __bfloat162float(a.o[t * a.st[3][0] + h * a.st[3][1] + c]), dsum);
-      }
-      dsum = warp_sum(dsum);
-      __syncwarp();
-      const float L = a.lse[static_cast<long long>(h) * a.cb.rows + t];
-      float acc[D / 32] = {};
-      for (int j0 = 0; j0 < s.len; j0 += 32) {
-        const int j = j0 + lane;
-        float ds = 0.f;
-        if (j < s.len) {
-          const long long at = static_cast<long long>(s.key0) + j;
-          const float p = expf(dot_row<D>(s_q[warp], a.k + at * a.st[1][0] + hk * a.st[1][1]) * a.scale - L);
-          ds = p * (dot_row<D>(s_do[warp], a.v + at * a.st[2][0] + hk * a.st[2][1]) - dsum);
-        }
-        for (int i = 0; i < min(32, s.len - j0); ++i) {
-          const float di = __shfl_sync(0xffffffffu, ds, i);
-          const __nv_bfloat16* k = a.k + (static_cast<long long>(s.key0) + j0 + i) * a.st[1][0] + hk * a.st[1][1];
-          for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(di, __bfloat162float(k[c * 32 + lane]), acc[c]);
-        }
-      }
-      for (int c = 0; c < D / 32; ++c)
-        a.dq[t * a.st[5][0] + h * a.st[5][1] + c * 32 + lane] = __float2bfloat16_rn(acc[c] * a.scale);
-    }
-  }
-}
-
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) fa_cross_dkv_plain(const CrossArgs a) {
-  __shared__ float s_k[kWarps][D], s_v[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int b = blockIdx.y; b < a.cb.B; b += gridDim.y) {
-    bool bad;
-    const CrossSeq s = cross_seq(a.cb, b, bad);
-    for (long long unit = blockIdx.x * kWarps + warp; unit < static_cast<long long>(s.places) * a.heads; unit += gridDim.x * kWarps) {
-      const int j = static_cast<int>(unit / a.heads), hk = static_cast<int>(unit % a.heads);
-      const long long at = static_cast<long long>(s.key0) + j;
-      __syncwarp();
-      for (int c = lane; c < D; c += 32) {
-        s_k[warp][c] = __bfloat162float(a.k[at * a.st[1][0] + hk * a.st[1][1] + c]);
-        s_v[warp][c] = __bfloat162float(a.v[at * a.st[2][0] + hk * a.st[2][1] + c]);
-      }
-      __syncwarp();
-      float dk[D / 32] = {}, dv[D / 32] = {};
-      const long long rows = j < s.len ? static_cast<long long>(s.n) * a.group : 0;
-      for (long long r0 = 0; r0 < rows; r0 += 32) {
-        const long long r = r0 + lane;
-        float p = 0.f, ds = 0.f;
-        if (r < rows) {
-          const long long t = s.row0 + r / a.group;
-          const int h = hk * a.group + static_cast<int>(r % a.group);
-          const __nv_bfloat16* dout = a.dout + t * a.st[4][0] + h * a.st[4][1];
-          const __nv_bfloat16* o = a.o + t * a.st[3][0] + h * a.st[3][1];
-          float dsum = 0.f;
-          for (int c = 0; c < D; ++c) dsum = fmaf(__bfloat162float(dout[c]), __bfloat162float(o[c]), dsum);
-          p = expf(dot_row<D>(s_k[warp], a.q + t * a.st[0][0] + h * a.st[0][1]) * a.scale - a.lse[static_cast<long long>(h) * a.cb.rows + t]);
-          ds = p * (dot_row<D>(s_v[warp], dout) - dsum);
-        }
-        for (int i = 0; i < static_cast<int>(min(32ll, rows - r0)); ++i) {
-          const float pi = __shfl_sync(0xffffffffu, p, i), di = __shfl_sync(0xffffffffu, ds, i);
-          const long long t = s.row0 + (r0 + i) / a.group;
-          const int h = hk * a.group + static_cast<int>((r0 + i) % a.group);
-          for (int c = 0; c < D / 32; ++c) {
-            dk[c] = fmaf(di, __bfloat162float(a.q[t * a.st[0][0] + h * a.st[0][1] + c * 32 + lane]), dk[c]);
-            dv[c] = fmaf(pi, __bfloat162float(a.dout[t * a.st[4][0] + h * a.st[4][1] + c * 32 + lane]), dv[c]);
-          }
-        }
-      }
-      for (int c = 0; c < D / 32; ++c) {
-        a.dk[at * a.st[6][0] + hk * a.st[6][1] + c * 32 + lane] = __float2bfloat16_rn(dk[c] * a.scale);
-        a.dv[at * a.st[7][0] + hk * a.st[7][1] + c * 32 + lane] = __float2bfloat16_rn(dv[c]);
-      }
-    }
-  }
-}
-
 // The forward pass is the paged attention's kernels on keys that lie packed: longer sequences (unless max_rows says that there are
 // none), then those of few rows, then what CTAs left in parts.
 template <int D>
@@ -132,14 +22,6 @@ int launch_fwd_d(PagedFwdArgs& a, const LaunchCtx& ctx) {
   if (e == 0) e = launch_paged_few<D, true>(a, chunks, ctx);
   if (e == 0) e = launch_paged_join<D, true>(a, chunks, ctx);
   return e;
-}
-
-template <int D>
-int launch_bwd_plain(const CrossArgs& a, const LaunchCtx& ctx) {
-  const dim3 grid(16, a.cb.B < 1024 ? a.cb.B : 1024);
-  fa_cross_dq_plain<D><<<grid, kWarps * 32, 0, ctx.stream>>>(a);
-  fa_cross_dkv_plain<D><<<grid, kWarps * 32, 0, ctx.stream>>>(a);
-  return static_cast<int>(cudaGetLastError());
 }
 
 // ------------------------------------------------------------------ checks
@@ -157,7 +39,8 @@ int check_strides(const long long* s, int n) {
 // Checks that both passes share; fills the batch and the shape.
 int take(const fa_cross_batch* b, int q_heads, int heads, int d, float scale, CrossArgs* a) {
   if (!b || !b->cu_rows || !b->cu_keys) return FA_ERR_NULL_POINTER;
-  if (b->B < 1 || b->rows < 0 || b->keys < 0 || b->rows > 0x7ffff000 || b->keys > 0x7ffff000) return FA_ERR_BAD_SHAPE;
+  // Positions at the end of a tile are 32-bit, too, and so are the tiles of all sequences.
+  if (b->B < 1 || b->rows < 0 || b->keys < 0 || b->rows > 0x7ffff000 - b->B || b->keys > 0x7ffff000) return FA_ERR_BAD_SHAPE;
   if (heads < 1 || heads > 65535 || q_heads < 1 || q_heads % heads != 0 || q_heads / heads > kCrossGroup) return FA_ERR_BAD_SHAPE;
   if (d != 32 && d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED_D;
   if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_BAD_SCALE;
@@ -233,10 +116,15 @@ int fa_cross_fwd(const void* q, const long long* q_stride, const void* k, const 
 }
 
 size_t fa_cross_bwd_workspace_bytes(int B, int rows, int q_heads, int heads, int d) {
-  if (B < 1 || rows < 0 || rows > 0x7ffff000 || heads < 1 || heads > 65535 || q_heads < 1 || q_heads % heads != 0 ||
+  if (B < 1 || rows < 0 || rows > 0x7ffff000 - B || heads < 1 || heads > 65535 || q_heads < 1 || q_heads % heads != 0 ||
       q_heads / heads > fa::kCrossGroup || (d != 32 && d != 64 && d != 128 && d != 256))
     return 0;
-  return 256 + static_cast<size_t>(rows) * q_heads * 8;
+  switch (d) {
+    case 32: return fa::cross_bwd_ws_bytes_d32(B, rows, heads, q_heads / heads);
+    case 64: return fa::cross_bwd_ws_bytes_d64(B, rows, heads, q_heads / heads);
+    case 128: return fa::cross_bwd_ws_bytes_d128(B, rows, heads, q_heads / heads);
+    default: return fa::cross_bwd_ws_bytes_d256(B, rows, heads, q_heads / heads);
+  }
 }
 
 int fa_cross_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
@@ -272,10 +160,10 @@ int fa_cross_bwd(const void* q, const void* k, const void* v, const void* o, con
   a.workspace = static_cast<char*>(workspace);
   int e;
   switch (d) {
-    case 32: e = fa::launch_bwd_plain<32>(a, ctx); break;
-    case 64: e = fa::launch_bwd_plain<64>(a, ctx); break;
-    case 128: e = fa::launch_bwd_plain<128>(a, ctx); break;
-    default: e = fa::launch_bwd_plain<256>(a, ctx); break;
+    case 32: e = fa::launch_cross_bwd_d32(a, ctx); break;
+    case 64: e = fa::launch_cross_bwd_d64(a, ctx); break;
+    case 128: e = fa::launch_cross_bwd_d128(a, ctx); break;
+    default: e = fa::launch_cross_bwd_d256(a, ctx); break;
   }
   return e == 0 ? FA_OK : FA_ERR_CUDA;
 }

@@ -70,4 +70,14 @@ struct CrossArgs {
   char* workspace;
 };
 
+// The backward pass for one head dimension (fa_cross_bwd_d<D>.cu); a cudaError_t-like code.  And the bytes of its workspace.
+int launch_cross_bwd_d32(const CrossArgs& a, const LaunchCtx& ctx);
+int launch_cross_bwd_d64(const CrossArgs& a, const LaunchCtx& ctx);
+int launch_cross_bwd_d128(const CrossArgs& a, const LaunchCtx& ctx);
+int launch_cross_bwd_d256(const CrossArgs& a, const LaunchCtx& ctx);
+size_t cross_bwd_ws_bytes_d32(int B, int rows, int heads, int group);
+size_t cross_bwd_ws_bytes_d64(int B, int rows, int heads, int group);
+size_t cross_bwd_ws_bytes_d128(int B, int rows, int heads, int group);
+size_t cross_bwd_ws_bytes_d256(int B, int rows, int heads, int group);
+
 }  // namespace fa

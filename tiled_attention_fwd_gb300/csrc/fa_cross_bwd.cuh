@@ -1,0 +1,831 @@
+// Gradients of cross attention over ragged batches: the backward pass's two
+// kernels (fa_bwd_tc.cuh: a key-parallel one for dK and dV, a query-parallel
+// one for dQ, no atomics on results) on work that is found on the device.
+//
+//   P = 2^(scale log2e q k^T - L log2e),  D = sum_c dO O,  dS = P (dO v^T - D),
+//   dV = P^T dO,  dK = scale dS^T Q (both summed over the heads of a group),  dQ = scale dS K.
+//
+//  * Rows.  The G query heads of a key/value head share tiles, token by token
+//    (a 3-D TMA box {columns, G heads, tokens}), so a group's heads add up in one
+//    accumulator, short sequences fill tiles, and K and V are read once for all of them.
+//      MODE 0 (dK, dV): a unit is 128 keys of one head; tiles of BS / G tokens of Q and dO stream past.
+//      MODE 1 (dQ): a unit is 128 / G tokens of one key/value head; tiles of BS keys of K and V stream past.
+//    Rows of a streamed box that no token fills are zeros from the kernel's start on, and what
+//    lies behind a sequence's last token or key (anything, NaN too) is set to zero in its last tile
+//    before the tensor core reads it: 0 times NaN is NaN.
+//  * Work.  The streamed tiles of all (sequence, head, unit) form one line that
+//    is cut into equal shares (fa_paged_plan.cuh), with room for UNIT_COST more behind
+//    each unit.  The load warp walks this CTA's share and hands segments (a run of one unit's
+//    streamed tiles) to the other warps through a ring in shared memory.
+//  * Output.  A unit held whole is written as it is finished; parts of others go to
+//    the workspace in fp32 and the joining kernel adds them up in the order of their CTAs.
+#pragma once
+
+#include "fa_bwd_tc.cuh"
+#include "fa_cross.cuh"
+#include "fa_paged_plan.cuh"
+
+namespace fa {
+
+constexpr int kBwdSegRing = 4;
+
+// Tokens of a streamed tile of MODE 0 and of a fixed tile of MODE 1.
+template <int D>
+constexpr __host__ __device__ int bwd_tokens0(int group) { return BwdCfg<D, 0>::BS / group; }
+constexpr __host__ __device__ int bwd_tokens1(int group) { return 128 / group; }
+
+// -L log2e and -D of the rows, as MODE 0 streams them: BS values a tile of tokens, [heads][tiles][BS]; sequence b's tiles
+// begin at tile row0 / tokens + b (its n rows need no more than what is left up to the next sequence's).
+template <int D>
+__host__ __device__ __forceinline__ long long bwd_tile0(const CrossSeq& s, int b, int group) {
+  return s.row0 / bwd_tokens0<D>(group) + static_cast<long long>(b);
+}
+template <int D>
+__host__ __device__ __forceinline__ long long bwd_tiles(int rows, int B, int group) {
+  return rows / bwd_tokens0<D>(group) + static_cast<long long>(B);
+}
+
+// Workspace of fa_cross_bwd.
+struct CrossBwdWs {
+  PlanRecord* rec[2];  // of the two kernels: [kPlanCtas]
+  float* l2;           // [heads][tiles][BS]
+  float* dsum;
+  float* part[2];      // [kPlanCtas][2][part floats]
+};
+// Floats of a part: 128 rows of MODE 0's dK and dV halves, or of dQ.
+template <int D, int MODE>
+constexpr __host__ __device__ size_t bwd_part_floats() {
+  return static_cast<size_t>(128) * BwdCfg<D, MODE>::NOUT * BwdCfg<D, MODE>::OUTW;
+}
+template <int D>
+size_t cross_bwd_ws(char* p, int B, int rows, int heads, int group, CrossBwdWs* w) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* x = p + at;
+    at += (bytes + 255) & ~static_cast<size_t>(255);
+    return x;
+  };
+  CrossBwdWs x;
+  const size_t vec = static_cast<size_t>(heads) * bwd_tiles<D>(rows, B, group) * BwdCfg<D, 0>::BS * sizeof(float);
+  for (int i = 0; i < 2; ++i) x.rec[i] = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
+  x.l2 = reinterpret_cast<float*>(take(vec));
+  x.dsum = reinterpret_cast<float*>(take(vec));
+  x.part[0] = reinterpret_cast<float*>(take(kPlanCtas * 2 * bwd_part_floats<D, 0>() * sizeof(float)));
+  x.part[1] = reinterpret_cast<float*>(take(kPlanCtas * 2 * bwd_part_floats<D, 1>() * sizeof(float)));
+  if (w) *w = x;
+  return at;
+}
+
+struct CrossBwdParams {
+  CrossArgs a;
+  CrossBwdWs ws;
+  unsigned long long limit_ns;
+  float scale_log2;
+  long long tiles;  // of the vectors, a head
+};
+
+// A run of streamed tiles of one unit.
+struct alignas(16) BwdSeg {
+  int valid;
+  int head;   // key/value head
+  int fix0;   // first row of the fixed tile in its tensor
+  int fix_n;  // its keys (MODE 0) or tokens (MODE 1)
+  int tok0;   // MODE 1: its first token within the sequence
+  int str0;   // the sequence's first row in the streamed tensor
+  int str_n;  // its tokens (MODE 0) or keys (MODE 1)
+  int vec0;   // its first tile of the vectors
+  int s0;     // first streamed tile
+  int n;      // streamed tiles
+  int half;
+  int out;    // 0: the unit is whole; 1, 2: part 0, part 1 of this CTA
+};
+static_assert(sizeof(BwdSeg) == 48, "segment size");
+
+template <int D, int MODE>
+struct CrossBwdCfg : BwdCfg<D, MODE> {
+  using C = BwdCfg<D, MODE>;
+  static constexpr int OFF_SEG = C::OFF_MISC + 576;
+  static constexpr int OFF_PLAN = OFF_SEG + kBwdSegRing * static_cast<int>(sizeof(BwdSeg));
+  static constexpr int READERS = 9;
+  // Streamed tiles that a unit costs besides its own (loading the fixed tiles, the output).
+  static constexpr int UNIT_COST = 2;
+  static_assert(C::OFF_ABORT + 4 <= OFF_SEG && OFF_PLAN + sizeof(PlanScratch) <= C::OFF_MISC + C::MISC, "misc area");
+};
+
+template <int D, int MODE>
+struct CrossBwdBars : BwdBars<D, MODE> {
+  using Base = BwdBars<D, MODE>;
+  __device__ __forceinline__ uint32_t seg_full(int i) const { return this->b0 + 256 + 8u * i; }
+  __device__ __forceinline__ uint32_t seg_empty(int i) const { return this->b0 + 288 + 8u * i; }
+  static_assert(Base::COUNT * 8 <= 256, "barrier area");
+};
+
+// The units of a sequence.
+struct BwdUnits {
+  int fix;    // fixed tiles a head
+  int str;    // streamed tiles
+  int units;  // fixed tiles x heads x halves
+};
+template <int D, int MODE>
+__host__ __device__ __forceinline__ BwdUnits bwd_units(const CrossArgs& a, const CrossSeq& s) {
+  using C = BwdCfg<D, MODE>;
+  BwdUnits u = {0, 0, 0};
+  if (s.n == 0 || s.len == 0) return u;  // the gradients are zeros: the preparing kernel writes them
+  if (MODE == 0) {
+    const int t = bwd_tokens0<D>(a.group);
+    u.fix = (s.len + 127) / 128;
+    u.str = (s.n + t - 1) / t;
+  } else {
+    const int t = bwd_tokens1(a.group);
+    u.fix = (s.n + t - 1) / t;
+    u.str = (s.len + C::BS - 1) / C::BS;
+  }
+  u.units = u.fix * a.heads * C::HALVES;
+  return u;
+}
+
+// ------------------------------------------------------------------ segments
+template <int D, int MODE>
+struct CrossBwdWalk {
+  using C = CrossBwdCfg<D, MODE>;
+  int b, u, j;
+  CrossSeq s;
+  BwdUnits c;
+  long long pos, end;   // on the line
+  long long last_tile;  // of the latest segment's unit
+  int record_u;         // the latest segment's unit
+  int record_b;
+  __device__ __forceinline__ void load(const CrossBwdParams& p) {
+    bool bad;
+    s = cross_seq(p.a.cb, b, bad);
+    c = bwd_units<D, MODE>(p.a, s);
+  }
+  __device__ __forceinline__ void start(const CrossBwdParams& p, const PlanShare& w) {
+    pos = w.start;
+    end = w.end;
+    b = w.b;
+    if (pos >= end) return;
+    load(p);
+    const int unit = c.str + C::UNIT_COST;
+    u = static_cast<int>(w.offset / unit);
+    j = static_cast<int>(w.offset - static_cast<long long>(u) * unit);
+    if (j >= c.str) advance(p);  // behind a unit's tiles: the share's first tile is the next unit's
+  }
+  __device__ __forceinline__ void advance(const CrossBwdParams& p) {
+    pos += c.str - j + C::UNIT_COST;
+    j = 0;
+    if (pos >= end) return;
+    if (++u < c.units) return;
+    u = 0;
+    do {
+      ++b;
+      load(p);
+    } while (c.units == 0);
+  }
+  __device__ __forceinline__ BwdSeg next(const CrossBwdParams& p) {
+    BwdSeg g = {};
+    if (pos >= end) return g;
+    const int n = end - pos < c.str - j ? static_cast<int>(end - pos) : c.str - j;
+    g.valid = 1;
+    g.half = u % C::HALVES;
+    const int tile = u / C::HALVES % c.fix;
+    g.head = u / C::HALVES / c.fix;
+    if (MODE == 0) {
+      g.fix0 = s.key0 + tile * 128;
+      g.fix_n = min(128, s.len - tile * 128);
+      g.str0 = s.row0;
+      g.str_n = s.n;
+    } else {
+      g.tok0 = tile * bwd_tokens1(p.a.group);
+      g.fix0 = s.row0 + g.tok0;
+      g.fix_n = min(bwd_tokens1(p.a.group), s.n - g.tok0);
+      g.str0 = s.key0;
+      g.str_n = s.len;
+    }
+    g.vec0 = static_cast<int>(bwd_tile0<D>(s, b, p.a.group));
+    g.s0 = j;
+    g.n = n;
+    g.out = n == c.str ? 0 : j == 0 ? 2 : 1;
+    last_tile = pos + (c.str - 1 - j);
+    record_u = u;
+    record_b = b;
+    pos += n;
+    j += n;
+    if (j == c.str) advance(p);
+    return g;
+  }
+};
+
+template <int D, int MODE>
+__device__ __forceinline__ BwdSeg* bwd_seg_slot(uint8_t* gbase, int k) {
+  return reinterpret_cast<BwdSeg*>(gbase + CrossBwdCfg<D, MODE>::OFF_SEG) + (k % kBwdSegRing);
+}
+
+// Segment k, read by a whole warp of a role other than the load warp.
+template <int D, int MODE>
+__device__ __forceinline__ bool bwd_seg_read(BwdSeg& g, int k, uint8_t* gbase, const CrossBwdBars<D, MODE>& bar,
+                                             const WaitGuard& guard) {
+  if (!warp_wait_bar(bar.seg_full(k % kBwdSegRing), (k / kBwdSegRing) & 1, guard, kStatusTimeoutLoad)) return false;
+  const int4* src = reinterpret_cast<const int4*>(bwd_seg_slot<D, MODE>(gbase, k));
+  int4* dst = reinterpret_cast<int4*>(&g);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) dst[i] = src[i];
+  warp_arrive(bar.seg_empty(k % kBwdSegRing));
+  return true;
+}
+
+// ------------------------------------------------------------------ load warp
+template <int D, int MODE>
+__device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const CUtensorMap* tm_a2, const CUtensorMap* tm_b1,
+                                               const CUtensorMap* tm_b2, const CrossBwdParams& p,
+                                               const CrossBwdBars<D, MODE>& bar, uint32_t base, uint8_t* gbase,
+                                               const PlanShare& share, const WaitGuard& g) {
+  using C = CrossBwdCfg<D, MODE>;
+  const int lane = threadIdx.x & 31;
+  const uint64_t pol_fix = policy_evict_first();  // read by one unit
+  const uint64_t pol_str = policy_evict_last();   // read by every unit of the head
+  const int group = p.a.group;
+  const int t0 = bwd_tokens0<D>(group), t1 = bwd_tokens1(group);
+  uint32_t pos = 0;       // stages issued so far
+  uint32_t issued = 0;    // bit i: stage i has been loaded at least once
+  uint32_t last_par = 0;  // bit i: parity of stage i's latest load
+  int last_fix = -1;      // latest segment whose fixed tiles were loaded
+  bool recorded = false, ok = true;
+  CrossBwdWalk<D, MODE> walk;
+  walk.start(p, share);
+  for (int k = 0;; ++k) {
+    const int i = k % kBwdSegRing;
+    if (!(ok = warp_wait_bar(bar.seg_empty(i), ((k / kBwdSegRing) & 1) ^ 1, g, kStatusTimeoutLoad))) break;
+    const BwdSeg w = walk.next(p);
+    if (lane == 0) {
+      *bwd_seg_slot<D, MODE>(gbase, k) = w;
+      if (w.out == 2)  // this unit's first part: who holds the rest
+        p.ws.rec[MODE][blockIdx.x] =
+            PlanRecord{walk.record_b, w.head, walk.record_u,
+                       plan_cta_of(walk.last_tile, share.total, share.ctas) - static_cast<int>(blockIdx.x)};
+    }
+    recorded = recorded || w.out == 2;
+    warp_arrive(bar.seg_full(i));
+    if (!w.valid) break;
+    // The fixed tiles: K, V (128 keys of a head), or Q, dO (a group's heads of 128 / G tokens).
+    if (!(ok = warp_wait_bar(bar.fix_empty(), (k & 1) ^ 1, g, kStatusTimeoutLoad))) break;
+    if (lane == 0) {
+      const int rows = MODE == 0 ? 128 : t1 * group;
+      mbar_arrive_expect_tx(bar.fix_full(), 2 * C::NR * rows * C::SWB);
+      for (int r = 0; r < C::NR; ++r) {
+        const uint32_t dst = base + C::OFF_FIX + r * C::FIX_REGION;
+        const int h = MODE == 0 ? w.head : w.head * group;
+        tma_load_3d(dst, tm_a1, bar.fix_full(), r * C::RC, h, w.fix0, pol_fix);
+        tma_load_3d(dst + C::FIX_TILE, tm_a2, bar.fix_full(), r * C::RC, h, w.fix0, pol_fix);
+      }
+    }
+    last_fix = k;
+    for (int t = 0; t < w.n; ++t) {
+      const int st = pos % C::NST;
+      const uint32_t par = (pos / C::NST) & 1;
+      if (!(ok = warp_wait_bar(bar.st_empty(st), par ^ 1, g, kStatusTimeoutLoad))) break;
+      if (lane == 0) {
+        const uint32_t s0 = base + C::OFF_ST + st * C::STAGE;
+        const uint32_t full = bar.st_full(st);
+        const int rows = MODE == 0 ? t0 * group : C::BS;
+        mbar_arrive_expect_tx(full, 2 * C::NR * rows * C::SWB + (C::KV ? 2 * C::VEC_BYTES : 0));
+        const int s = w.s0 + t, h = MODE == 0 ? w.head * group : w.head;
+        const int row = w.str0 + s * (MODE == 0 ? t0 : C::BS);
+        for (int r = 0; r < C::NR; ++r) {
+          tma_load_3d(s0 + r * C::S_REGION, tm_b1, full, r * C::RC, h, row, pol_str);
+          tma_load_3d(s0 + C::S_TILE + r * C::S_REGION, tm_b2, full, r * C::RC, h, row, pol_str);
+        }
+        if constexpr (C::KV) {
+          // (BS * 4 is a multiple of 16.)
+          const long long off = (w.head * p.tiles + w.vec0 + s) * C::BS;
+          bulk_load(s0 + 2 * C::S_TILE, p.ws.l2 + off, C::VEC_BYTES, full);
+          bulk_load(s0 + 2 * C::S_TILE + C::VEC_BYTES, p.ws.dsum + off, C::VEC_BYTES, full);
+        }
+      }
+      issued |= 1u << st;
+      last_par = (last_par & ~(1u << st)) | (par << st);
+      ++pos;
+    }
+    if (!ok) break;
+  }
+  if (lane == 0 && !recorded) p.ws.rec[MODE][blockIdx.x].b = -1;
+  // Every issued copy must land before the CTA may exit.
+  for (int i = 0; i < C::NST; ++i)
+    if (issued & (1u << i)) bwd_wait_drain(bar.st_full(i), (last_par >> i) & 1, g);
+  if (last_fix >= 0) bwd_wait_drain(bar.fix_full(), last_fix & 1, g);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ MMA issuer
+// bwd_mma's order of products, segment by segment.
+template <int D, int MODE>
+__device__ __forceinline__ void cross_bwd_mma(const CrossBwdParams& p, const CrossBwdBars<D, MODE>& bar, uint32_t base,
+                                              uint8_t* gbase, uint32_t tmem, const WaitGuard& g) {
+  using C = CrossBwdCfg<D, MODE>;
+  const BwdMma<D, MODE> M(tmem, base);
+  const int lane = threadIdx.x & 31;
+  const int per = MODE == 0 ? bwd_tokens0<D>(p.a.group) : C::BS;  // tokens or keys of a streamed tile
+  auto wait = [&](uint32_t b, uint32_t par) -> bool {
+    const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
+    return __all_sync(0xffffffffu, r);
+  };
+  // Rows of the streamed tile at stage st behind the last token or key: zeros.  (MODE 1: of K only; V's take part in
+  // dP alone, whose columns there are not looked at.)
+  auto clear_tail = [&](const BwdSeg& w, int t, uint32_t st) {
+    const int left = w.str_n - (w.s0 + t) * per;
+    if (left >= per) return;
+    const int from = MODE == 0 ? left * p.a.group : left;
+    const int to = MODE == 0 ? per * p.a.group : C::BS;
+    constexpr int UR = C::SWB / 16;
+    const uint32_t s0 = base + C::OFF_ST + st * C::STAGE;
+    for (int r = 0; r < C::NR; ++r)
+      for (int i = from * UR + lane; i < to * UR; i += 32) {
+        st_shared_v4(s0 + r * C::S_REGION + i * 16, 0, 0, 0, 0);
+        if constexpr (C::KV) st_shared_v4(s0 + C::S_TILE + r * C::S_REGION + i * 16, 0, 0, 0, 0);
+      }
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+  uint32_t pos = 0;            // streamed stages consumed before the current segment
+  uint32_t pr0 = 0, pr1 = 0;   // p_ready phases consumed, per buffer
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    BwdSeg w;
+    if (!(ok = bwd_seg_read<D, MODE>(w, k, gbase, bar, g)) || !w.valid) break;
+    const int n = w.n;
+    if (!(ok = wait(bar.fix_full(), k & 1))) break;
+    tc_fence_after();
+    auto stage_of = [&](int t) -> uint32_t { return (pos + t) % C::NST; };
+    auto acquire = [&](int t) -> bool {
+      const uint32_t q = pos + t;
+      if (!wait(bar.st_full(q % C::NST), (q / C::NST) & 1)) return false;
+      clear_tail(w, t, q % C::NST);
+      tc_fence_after();
+      return true;
+    };
+    for (int t = 0; ok && t < n && t < 2; ++t) {
+      if (!(ok = acquire(t))) break;
+      M.sdp(stage_of(t), t & 1);
+      mma_commit_elect(bar.s_full(t & 1));
+      if (t == n - 1) mma_commit_elect(bar.fix_empty());
+    }
+    for (int t = 0; ok && t < n; ++t) {
+      const int b = t & 1;
+      uint32_t& pr = b ? pr1 : pr0;
+      if (!(ok = wait(bar.p_ready(b), pr & 1))) break;
+      ++pr;
+      tc_fence_after();
+      if (t == 0 && k > 0) {
+        if (!(ok = wait(bar.out_free(), (k - 1) & 1))) break;
+        tc_fence_after();
+      }
+      M.accumulate(stage_of(t), b, t > 0, w.half);
+      mma_commit_elect(bar.st_empty(stage_of(t)));
+      if (t + 2 < n) {
+        if (!(ok = acquire(t + 2))) break;
+        M.sdp(stage_of(t + 2), b);
+        mma_commit_elect(bar.s_full(b));
+        if (t + 2 == n - 1) mma_commit_elect(bar.fix_empty());
+      }
+    }
+    if (!ok) break;
+    pos += n;
+    mma_commit_elect(bar.out_done());
+  }
+  // All issued MMAs must complete before TMEM is released.
+  mma_commit_elect(bar.drain());
+  bwd_wait_drain(bar.drain(), 0, g);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ elementwise warpgroups
+// bwd_elementwise without a causal mask; outputs as bf16, or a part's in fp32.
+template <int D, int MODE>
+__device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, const CrossBwdBars<D, MODE>& bar,
+                                                      uint8_t* gbase, uint32_t tmem, int b, int quarter, int lane,
+                                                      const WaitGuard& g) {
+  using C = CrossBwdCfg<D, MODE>;
+  const int r = quarter * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const float sl2 = p.scale_log2;
+  const uint64_t sl2x2 = f2_pack(sl2, sl2);
+  // MODE 1: this thread's token within the fixed tile, and its head of the group.
+  const int per = MODE == 0 ? bwd_tokens0<D>(p.a.group) : C::BS;  // tokens or keys of a streamed tile
+  const int tok_r = MODE == 0 ? 0 : r / p.a.group, head_r = MODE == 0 ? 0 : r - tok_r * p.a.group;
+  uint32_t sf = 0;    // s_full(b) phases consumed
+  uint32_t pos = 0;   // streamed stages before the current segment
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    BwdSeg w;
+    if (!(ok = bwd_seg_read<D, MODE>(w, k, gbase, bar, g)) || !w.valid) break;
+    const int n = w.n;
+    const bool mine = MODE == 0 ? r < w.fix_n : tok_r < w.fix_n;  // (tokens: fix_n <= 128 / G)
+    uint64_t l2_row = 0, d_row = 0;  // MODE 1: this row's -L * log2(e) and -D, twice
+    if constexpr (MODE == 1) {
+      float l2 = -INFINITY, dsum = 0.f;
+      if (mine) {
+        const int t0 = bwd_tokens0<D>(p.a.group), tok = w.tok0 + tok_r;
+        const long long at = (w.head * p.tiles + w.vec0 + tok / t0) * BwdCfg<D, 0>::BS + tok % t0 * p.a.group + head_r;
+        // (Written by the kernel before the one before: past L1.)
+        l2 = __ldcg(p.ws.l2 + at);
+        dsum = __ldcg(p.ws.dsum + at);
+      }
+      l2_row = f2_pack(l2, l2);
+      d_row = f2_pack(dsum, dsum);
+    }
+    for (int t = b; ok && t < n; t += 2) {
+      ok = warp_wait_bar(bar.s_full(b), sf & 1, g, kStatusTimeoutSoftmax);
+      if (!ok) break;
+      ++sf;
+      const uint32_t q = pos + t;
+      const int st = q % C::NST;
+      if constexpr (C::KV) {
+        // The stage's vectors were written by TMA; observe that completion here too.
+        ok = warp_wait_bar(bar.st_full(st), (q / C::NST) & 1, g, kStatusTimeoutSoftmax);
+        if (!ok) break;
+      }
+      tc_fence_after();
+      // Rows of the tile that are a token's or a key's.  (The others are zeros in Q, dO and K, but zero times an infinity is NaN,
+      // and V's are whatever its neighbours are.)
+      const int there = MODE == 0 ? min(w.str_n - (w.s0 + t) * per, per) * p.a.group : w.str_n - (w.s0 + t) * per;
+      const bool need_mask = there < C::BS;
+      const float4* vl2 = reinterpret_cast<const float4*>(gbase + C::OFF_ST + st * C::STAGE + 2 * C::S_TILE);
+      const float4* vd = vl2 + C::BS / 4;
+#pragma unroll 1
+      for (int h = 0; h < C::BS / 32; ++h) {
+        uint32_t rs[32], rd[32];
+        tmem_ld32(tmem + lane_off + C::TM_S + b * C::BS + h * 32, rs);
+        tmem_ld32(tmem + lane_off + C::TM_DP + b * C::BS + h * 32, rd);
+        tmem_wait_ld(rs);
+        tmem_wait_ld(rd);
+        uint32_t pk[16], dk[16];
+#pragma unroll
+        for (int c4 = 0; c4 < 8; ++c4) {
+          // -L * log2(e) and -D of the four streamed rows (MODE 0) or of this row (MODE 1).
+          uint64_t nl[2], nd[2];
+          if constexpr (C::KV) {
+            const float4 a = vl2[h * 8 + c4], d4 = vd[h * 8 + c4];
+            nl[0] = f2_pack(a.x, a.y);
+            nl[1] = f2_pack(a.z, a.w);
+            nd[0] = f2_pack(d4.x, d4.y);
+            nd[1] = f2_pack(d4.z, d4.w);
+          } else {
+            nl[0] = nl[1] = l2_row;
+            nd[0] = nd[1] = d_row;
+          }
+#pragma unroll
+          for (int e2 = 0; e2 < 2; ++e2) {
+            const int c = c4 * 4 + e2 * 2;
+            const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2x2, nl[e2]));
+            float p0 = ex2(x.x), p1 = ex2(x.y);
+            float2 ds = f2_unpack(
+                f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(rd[c]), __uint_as_float(rd[c + 1])), nd[e2])));
+            if (need_mask) {
+              if (h * 32 + c >= there) p0 = ds.x = 0.f;
+              if (h * 32 + c + 1 >= there) p1 = ds.y = 0.f;
+            }
+            pk[c4 * 2 + e2] = pack_bf16x2(p0, p1);
+            dk[c4 * 2 + e2] = pack_bf16x2(ds.x, ds.y);
+          }
+        }
+        // As in bwd_elementwise: chunk h's bf16 pairs land behind what has been read.
+        if constexpr (C::KV) tmem_st16(tmem + lane_off + C::TM_S + b * C::BS + h * 16, pk);
+        tmem_st16(tmem + lane_off + C::TM_DP + b * C::BS + h * 16, dk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(bar.p_ready(b));
+    }
+    if (!ok) break;
+    pos += n;
+    // Read the unit's accumulators out.
+    ok = warp_wait_bar(bar.out_done(), k & 1, g, kStatusTimeoutSoftmax);
+    if (!ok) break;
+    tc_fence_after();
+    const bool second = C::KV && b == 1;
+    const uint32_t acc = tmem + lane_off + C::TM_OUT + (second ? C::OUTW : 0);
+    const float f = second ? 1.f : p.a.scale;  // dK and dQ carry the softmax scale
+    const uint64_t f2 = f2_pack(f, f);
+    __nv_bfloat16* out = MODE == 1 ? p.a.dq : second ? p.a.dv : p.a.dk;
+    const long long* os = p.a.st[MODE == 1 ? 5 : second ? 7 : 6];
+    const int head = MODE == 0 ? w.head : w.head * p.a.group + head_r;
+    const long long row = w.fix0 + (MODE == 0 ? r : tok_r);
+    __nv_bfloat16* orow = out + row * os[0] + head * os[1] + w.half * C::OUTW;
+    float4* part = reinterpret_cast<float4*>(p.ws.part[MODE] + (blockIdx.x * 2 + (w.out - 1)) * bwd_part_floats<D, MODE>() +
+                                             (second ? 128 * C::OUTW : 0)) + r;
+#pragma unroll 1
+    for (int c = 0; c < C::OUTW / 32; ++c) {
+      if (!C::KV && (c & 1) != b) continue;
+      uint32_t v[32];
+      tmem_ld32(acc + c * 32, v);
+      tmem_wait_ld(v);
+      if (w.out == 0) {
+        uint32_t packed[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 y = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2));
+          packed[i] = pack_bf16x2(y.x, y.y);
+        }
+        if (mine) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(packed[4 * i], packed[4 * i + 1], packed[4 * i + 2], packed[4 * i + 3]);
+        }
+      } else {
+        // 16-byte block i of all 128 rows together.
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          part[(c * 8 + i) * 128] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+      }
+    }
+    tc_fence_before();
+    warp_arrive(bar.out_free());
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <int D, int MODE>
+__global__ void __launch_bounds__(BwdCfg<D, MODE>::THREADS, 1)
+    fa_cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_a2,
+                        const __grid_constant__ CUtensorMap tm_b1, const __grid_constant__ CUtensorMap tm_b2,
+                        const __grid_constant__ CrossBwdParams p) {
+  using C = CrossBwdCfg<D, MODE>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  CrossBwdBars<D, MODE> bar;
+  bar.b0 = base + C::OFF_MISC;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::OFF_TMEM_SLOT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_ABORT);
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar.fix_full(), 1);
+    mbar_init(bar.fix_empty(), 1);
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(bar.st_full(i), 1);
+      mbar_init(bar.st_empty(i), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar.s_full(b), 1);
+      mbar_init(bar.p_ready(b), 4);
+    }
+    mbar_init(bar.out_done(), 1);
+    mbar_init(bar.out_free(), 8);
+    mbar_init(bar.drain(), 1);
+    for (int i = 0; i < kBwdSegRing; ++i) {
+      mbar_init(bar.seg_full(i), 1);
+      mbar_init(bar.seg_empty(i), C::READERS);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::LOAD_WARP && lane == 0) {
+    prefetch_tmap(&tm_a1);
+    prefetch_tmap(&tm_a2);
+    prefetch_tmap(&tm_b1);
+    prefetch_tmap(&tm_b2);
+  }
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
+    tmem_relinquish();
+  }
+  if (MODE == 0 && bwd_tokens0<D>(p.a.group) * p.a.group < C::BS) {
+    // Rows of a streamed tile that no token fills stay zeros.
+    for (int i = threadIdx.x; i < C::NST * C::STAGE / 16; i += C::THREADS) st_shared_v4(base + C::OFF_ST + i * 16, 0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  const PlanShare share = plan_share<C::THREADS>(
+      p.a.cb.B, gridDim.x, blockIdx.x,
+      [&](int b) -> long long {
+        bool bad;
+        const BwdUnits u = bwd_units<D, MODE>(p.a, cross_seq(p.a.cb, b, bad));
+        return static_cast<long long>(u.units) * (u.str + C::UNIT_COST);
+      },
+      1 + C::UNIT_COST, *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
+  // The preparing kernel is done (MODE 1's CTAs begin when all of MODE 0's have come past here, so it is for them, too).
+  if (MODE == 0) pdl_wait();
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitGuard g{abort_flag, p.a.status, p.limit_ns};
+
+  if (warp < 8) {
+    cross_bwd_elementwise<D, MODE>(p, bar, gbase, tmem, warp >> 2, warp & 3, lane, g);
+  } else if (warp == C::MMA_WARP) {
+    cross_bwd_mma<D, MODE>(p, bar, base, gbase, tmem, g);
+  } else if (warp == C::LOAD_WARP) {
+    cross_bwd_load<D, MODE>(&tm_a1, &tm_a2, &tm_b1, &tm_b2, p, bar, base, gbase, share, g);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+  if (MODE == 1) pdl_wait();  // what waits for this kernel waits for MODE 0's, too
+}
+
+// ------------------------------------------------------------------ preparing
+// -L log2e and -D of every row into the vectors (-inf and 0 behind a sequence's last), and
+// zeros where no product is made: places behind a sequence's keys, keys of sequences without rows, rows without keys.
+constexpr int kPrepThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __grid_constant__ CrossBwdParams p) {
+  constexpr int BS = BwdCfg<D, 0>::BS;
+  constexpr int CPR = D / 8;     // 16-byte chunks per row
+  constexpr int RPW = 32 / CPR;  // rows per warp step
+  constexpr int WARPS = kPrepThreads / 32;
+  const CrossArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  if (blockIdx.x == 0) {
+    bool any = false;
+    for (int b = threadIdx.x; b < a.cb.B; b += kPrepThreads) {
+      bool bad;
+      cross_seq(a.cb, b, bad);
+      any = any || bad;
+    }
+    if (any) atomicOr(a.status, kBadBatchBit);
+  }
+  const int t0 = bwd_tokens0<D>(a.group);
+  for (long long tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    // The last sequence whose tiles begin at `tile` or before, found in steps of 32 sub-ranges (every warp for itself).
+    int lo = 0, count = a.cb.B;
+    while (count > 1) {
+      const int step = (count + 31) / 32;
+      const int at = lo + lane * step;
+      const bool here = at < lo + count && a.cb.cu_rows[at] / t0 + static_cast<long long>(at) <= tile;
+      const int k = __popc(__ballot_sync(0xffffffffu, here));  // (lane 0 always, where the offsets do not decrease)
+      const int from = lo + (k > 0 ? k - 1 : 0) * step;
+      count = min(step, lo + count - from);
+      lo = from;
+    }
+    bool bad;
+    const CrossSeq s = cross_seq(a.cb, lo, bad);
+    const long long first = (tile - bwd_tile0<D>(s, lo, a.group)) * t0;  // token of the tile's first row
+    if (first < 0 || first >= s.n || s.len == 0) continue;               // nobody reads it
+    const int sub = lane / CPR, chunk = lane % CPR;
+    for (int i = warp * RPW + sub; i < a.heads * BS; i += WARPS * RPW) {
+      const int head = i / BS, r = i % BS;
+      const int tok = r / a.group, hq = head * a.group + r % a.group;
+      const bool valid = tok < t0 && first + tok < s.n;
+      float acc = 0.f;
+      if (valid) {
+        const long long row = s.row0 + first + tok;
+        const uint4 x = *reinterpret_cast<const uint4*>(a.o + row * a.st[3][0] + hq * a.st[3][1] + chunk * 8);
+        const uint4 y = *reinterpret_cast<const uint4*>(a.dout + row * a.st[4][0] + hq * a.st[4][1] + chunk * 8);
+        const uint32_t xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&xv[e]));
+          const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&yv[e]));
+          acc = fmaf(u.x, v.x, acc);
+          acc = fmaf(u.y, v.y, acc);
+        }
+      }
+#pragma unroll
+      for (int m = CPR / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+      if (chunk == 0) {
+        const long long at = (head * p.tiles + tile) * BS + r;
+        p.ws.dsum[at] = valid ? -acc : 0.f;
+        p.ws.l2[at] = valid ? -a.lse[static_cast<long long>(hq) * a.cb.rows + s.row0 + first + tok] * 1.4426950408889634f : -INFINITY;
+      }
+    }
+  }
+  // Zeros: several blocks to a sequence.
+  const int per = gridDim.x / a.cb.B > 0 ? gridDim.x / a.cb.B : 1;
+  for (int x = blockIdx.x; x / per < a.cb.B; x += gridDim.x) {
+    const int b = x / per, part = x % per;
+    bool bad;
+    const CrossSeq s = cross_seq(a.cb, b, bad);
+    auto fill = [&](__nv_bfloat16* out, const long long* st, int row0, int from, int to, int heads) {
+      const long long items = static_cast<long long>(to - from) * heads * CPR;
+      for (long long i = static_cast<long long>(part) * kPrepThreads + threadIdx.x; i < items; i += static_cast<long long>(per) * kPrepThreads) {
+        const long long row = row0 + from + i / (heads * CPR);
+        const int rest = static_cast<int>(i % (heads * CPR));
+        *reinterpret_cast<uint4*>(out + row * st[0] + rest / CPR * st[1] + rest % CPR * 8) = make_uint4(0, 0, 0, 0);
+      }
+    };
+    const int from = s.n > 0 ? s.len : 0;
+    fill(a.dk, a.st[6], s.key0, from, s.places, a.heads);
+    fill(a.dv, a.st[7], s.key0, from, s.places, a.heads);
+    if (s.len == 0) fill(a.dq, a.st[5], s.row0, 0, s.n, a.q_heads);
+  }
+}
+
+// ------------------------------------------------------------------ joining
+// Joins the parts of the units that several CTAs held; blocks (c, .) those of the units that CTA c began (z = 0: dK and dV,
+// z = 1: dQ).  A warp takes 16 columns of 32 rows, a row a lane.
+template <int D, int MODE>
+__device__ __forceinline__ void cross_bwd_join(const CrossBwdParams& p) {
+  using C = BwdCfg<D, MODE>;
+  const CrossArgs& a = p.a;
+  const PlanRecord rec = p.ws.rec[MODE][blockIdx.x];
+  if (rec.b < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool bad;
+  const CrossSeq s = cross_seq(a.cb, rec.b, bad);
+  const BwdUnits u = bwd_units<D, MODE>(a, s);
+  const int half = rec.qb % C::HALVES, tile = rec.qb / C::HALVES % u.fix;
+  constexpr size_t stride = 2 * bwd_part_floats<D, MODE>();  // from one CTA's parts to the next's
+  const float* first = p.ws.part[MODE] + blockIdx.x * stride + stride / 2;
+  const float* rest = first + stride / 2 - stride;  // part 0 of CTA + i at rest + i * stride
+  const int n = rec.more + 1;
+  constexpr int COLS = C::NOUT * C::OUTW / 16;
+  for (int job = blockIdx.y * 4 + warp; job < 4 * COLS; job += gridDim.y * 4) {
+    const int r = job % 4 * 32 + lane, c16 = job / 4;
+    const int tok = MODE == 0 ? r : r / a.group;
+    const int left = MODE == 0 ? s.len - tile * 128 : s.n - tile * bwd_tokens1(a.group);
+    if (tok >= left || (MODE == 1 && tok >= bwd_tokens1(a.group))) continue;
+    float4 acc[4] = {};
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+      const float4* x = reinterpret_cast<const float4*>(i == 0 ? first : rest + i * stride) + r;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 y = x[(c16 * 4 + k) * 128];
+        acc[k].x += y.x;
+        acc[k].y += y.y;
+        acc[k].z += y.z;
+        acc[k].w += y.w;
+      }
+    }
+    const bool second = MODE == 0 && c16 * 16 >= C::OUTW;
+    const int c = c16 * 16 - (second ? C::OUTW : 0);
+    const float f = second ? 1.f : a.scale;
+    const int head = MODE == 0 ? rec.head : rec.head * a.group + r % a.group;
+    const long long row = MODE == 0 ? static_cast<long long>(s.key0) + tile * 128 + r
+                                    : static_cast<long long>(s.row0) + tile * bwd_tokens1(a.group) + tok;
+    const long long* os = a.st[MODE == 1 ? 5 : second ? 7 : 6];
+    uint4* dst = reinterpret_cast<uint4*>((MODE == 1 ? a.dq : second ? a.dv : a.dk) + row * os[0] + head * os[1] +
+                                          half * C::OUTW + c);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      dst[k] = make_uint4(pack_bf16x2(acc[2 * k].x * f, acc[2 * k].y * f), pack_bf16x2(acc[2 * k].z * f, acc[2 * k].w * f),
+                          pack_bf16x2(acc[2 * k + 1].x * f, acc[2 * k + 1].y * f),
+                          pack_bf16x2(acc[2 * k + 1].z * f, acc[2 * k + 1].w * f));
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(128) fa_cross_bwd_join_kernel(const __grid_constant__ CrossBwdParams p) {
+  pdl_wait();
+  if (blockIdx.z == 0)
+    cross_bwd_join<D, 0>(p);
+  else
+    cross_bwd_join<D, 1>(p);
+}
+
+// ------------------------------------------------------------------ launch
+template <int D, int MODE>
+int launch_cross_bwd_mode(const CrossBwdParams& p, int grid, const LaunchCtx& ctx) {
+  using C = CrossBwdCfg<D, MODE>;
+  auto kernel = fa_cross_bwd_kernel<D, MODE>;
+  static std::atomic<unsigned long long> allowed{0};
+  const int e = allow_smem(kernel, C::SMEM_ALLOC, allowed);
+  if (e != 0) return e;
+  const CrossArgs& a = p.a;
+  CUtensorMap mq, mo, mk, mv;
+  // Boxes of a group's heads of some tokens, and of one head of some keys.
+  const int tokens = MODE == 0 ? bwd_tokens0<D>(a.group) : bwd_tokens1(a.group), keys = MODE == 0 ? 128 : C::BS;
+  const long long qd[3] = {D, a.q_heads, a.cb.rows}, kd[3] = {D, a.heads, a.cb.keys};
+  auto encode = [&](CUtensorMap* m, const void* t, int i, const long long* dims, int box1, int box2) {
+    const long long st[2] = {a.st[i][1], a.st[i][0]};
+    return encode_paged_map(m, t, 2, dims, st, C::RC, box1, box2, C::SWB, false);
+  };
+  if (encode(&mq, a.q, 0, qd, a.group, tokens) != 0 || encode(&mo, a.dout, 4, qd, a.group, tokens) != 0 ||
+      encode(&mk, a.k, 1, kd, 1, keys) != 0 || encode(&mv, a.v, 2, kd, 1, keys) != 0)
+    return -1;
+  return MODE == 0 ? launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mk, mv, mq, mo, p)
+                   : launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mq, mo, mk, mv, p);
+}
+
+template <int D>
+int launch_cross_bwd(const CrossArgs& a, const LaunchCtx& ctx) {
+  CrossBwdParams p;
+  p.a = a;
+  cross_bwd_ws<D>(a.workspace, a.cb.B, a.cb.rows, a.heads, a.group, &p.ws);
+  p.limit_ns = ctx.limit_ns;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.tiles = bwd_tiles<D>(a.cb.rows, a.cb.B, a.group);
+  fa_cross_prep_kernel<D><<<ctx.num_sms * 8, kPrepThreads, 0, ctx.stream>>>(p);
+  int e = static_cast<int>(cudaGetLastError());
+  if (e != 0 || a.cb.rows == 0 || a.cb.keys == 0) return e;  // (zeros are all there is)
+  const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
+  e = launch_cross_bwd_mode<D, 0>(p, grid, ctx);
+  if (e == 0) e = launch_cross_bwd_mode<D, 1>(p, grid, ctx);
+  if (e == 0) e = launch_dependent(fa_cross_bwd_join_kernel<D>, dim3(grid, 16, 2), 128, 0, ctx.stream, p);
+  return e;
+}
+
+}  // namespace fa
