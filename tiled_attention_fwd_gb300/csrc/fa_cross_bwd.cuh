@@ -10,9 +10,10 @@
 //    accumulator, short sequences fill tiles, and K and V are read once for all of them.
 //      MODE 0 (dK, dV): a unit is 128 keys of one head; tiles of BS / G tokens of Q and dO stream past.
 //      MODE 1 (dQ): a unit is 128 / G tokens of one key/value head; tiles of BS keys of K and V stream past.
-//    Rows of a streamed box that no token fills are zeros from the kernel's start on, and what
-//    lies behind a sequence's last token or key (anything, NaN too) is set to zero in its last tile
-//    before the tensor core reads it: 0 times NaN is NaN.
+//    Rows of a streamed tile that are no token's or key's (anything, NaN too) meet zeros of P and dS in the accumulations, and 0
+//    times NaN is NaN: the warpgroup that forms these sets such rows to zero first, behind S and dP of the tile.
+//  * Sequences of few rows have a kernel of their own (fa_cross_bwd_short.cuh, MODE 2 here) that makes all three gradients
+//    in one pass; these two take the others.
 //  * Work.  The streamed tiles of all (sequence, head, unit) form one line that
 //    is cut into equal shares (fa_paged_plan.cuh), with room for UNIT_COST more behind
 //    each unit.  The load warp walks this CTA's share and hands segments (a run of one unit's
@@ -45,18 +46,37 @@ __host__ __device__ __forceinline__ long long bwd_tiles(int rows, int B, int gro
   return rows / bwd_tokens0<D>(group) + static_cast<long long>(B);
 }
 
+// 128-row tiles of a sequence's rows (all heads of a group) that MODE 2 takes at most (d = 256: none).
+constexpr __host__ __device__ int bwd_short_tiles(int d) { return d == 32 ? 4 : d == 64 ? 2 : d == 128 ? 1 : 0; }
+template <int D>
+__host__ __device__ __forceinline__ bool bwd_short(const CrossSeq& s, int group) {
+  return s.n <= bwd_short_tiles(D) * bwd_tokens1(group);
+}
+
+// Units, fixed and streamed tiles of a kernel.
+template <int D, int MODE>
+struct BwdWork {
+  static constexpr int HALVES = BwdCfg<D, MODE>::HALVES;
+  static constexpr int STR = BwdCfg<D, MODE>::BS;
+  static constexpr size_t PART = static_cast<size_t>(128) * BwdCfg<D, MODE>::NOUT * BwdCfg<D, MODE>::OUTW;  // floats of a part
+  // Streamed tiles that a unit costs besides its own (loading the fixed tiles, the output).
+  static constexpr int UNIT_COST = 2;
+};
+template <int D>
+struct BwdWork<D, 2> {
+  static constexpr int HALVES = 1;
+  static constexpr int STR = 128;
+  static constexpr size_t PART = static_cast<size_t>(128) * bwd_short_tiles(D) * D;
+  static constexpr int UNIT_COST = 1;
+};
+
 // Workspace of fa_cross_bwd.
 struct CrossBwdWs {
-  PlanRecord* rec[2];  // of the two kernels: [kPlanCtas]
+  PlanRecord* rec[3];  // of the kernels: [kPlanCtas]
   float* l2;           // [heads][tiles][BS]
   float* dsum;
-  float* part[2];      // [kPlanCtas][2][part floats]
+  float* part[3];      // [kPlanCtas][2][part floats]
 };
-// Floats of a part: 128 rows of MODE 0's dK and dV halves, or of dQ.
-template <int D, int MODE>
-constexpr __host__ __device__ size_t bwd_part_floats() {
-  return static_cast<size_t>(128) * BwdCfg<D, MODE>::NOUT * BwdCfg<D, MODE>::OUTW;
-}
 template <int D>
 size_t cross_bwd_ws(char* p, int B, int rows, int heads, int group, CrossBwdWs* w) {
   size_t at = 0;
@@ -67,11 +87,12 @@ size_t cross_bwd_ws(char* p, int B, int rows, int heads, int group, CrossBwdWs* 
   };
   CrossBwdWs x;
   const size_t vec = static_cast<size_t>(heads) * bwd_tiles<D>(rows, B, group) * BwdCfg<D, 0>::BS * sizeof(float);
-  for (int i = 0; i < 2; ++i) x.rec[i] = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
+  for (int i = 0; i < 3; ++i) x.rec[i] = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
   x.l2 = reinterpret_cast<float*>(take(vec));
   x.dsum = reinterpret_cast<float*>(take(vec));
-  x.part[0] = reinterpret_cast<float*>(take(kPlanCtas * 2 * bwd_part_floats<D, 0>() * sizeof(float)));
-  x.part[1] = reinterpret_cast<float*>(take(kPlanCtas * 2 * bwd_part_floats<D, 1>() * sizeof(float)));
+  x.part[0] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, 0>::PART * sizeof(float)));
+  x.part[1] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, 1>::PART * sizeof(float)));
+  x.part[2] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, 2>::PART * sizeof(float)));
   if (w) *w = x;
   return at;
 }
@@ -89,10 +110,10 @@ struct alignas(16) BwdSeg {
   int valid;
   int head;   // key/value head
   int fix0;   // first row of the fixed tile in its tensor
-  int fix_n;  // its keys (MODE 0) or tokens (MODE 1)
+  int fix_n;  // its keys (MODE 0) or tokens (MODE 1, 2)
   int tok0;   // MODE 1: its first token within the sequence
   int str0;   // the sequence's first row in the streamed tensor
-  int str_n;  // its tokens (MODE 0) or keys (MODE 1)
+  int str_n;  // its tokens (MODE 0) or keys (MODE 1, 2)
   int vec0;   // its first tile of the vectors
   int s0;     // first streamed tile
   int n;      // streamed tiles
@@ -107,8 +128,6 @@ struct CrossBwdCfg : BwdCfg<D, MODE> {
   static constexpr int OFF_SEG = C::OFF_MISC + 576;
   static constexpr int OFF_PLAN = OFF_SEG + kBwdSegRing * static_cast<int>(sizeof(BwdSeg));
   static constexpr int READERS = 9;
-  // Streamed tiles that a unit costs besides its own (loading the fixed tiles, the output).
-  static constexpr int UNIT_COST = 2;
   static_assert(C::OFF_ABORT + 4 <= OFF_SEG && OFF_PLAN + sizeof(PlanScratch) <= C::OFF_MISC + C::MISC, "misc area");
 };
 
@@ -128,17 +147,21 @@ struct BwdUnits {
 };
 template <int D, int MODE>
 __host__ __device__ __forceinline__ BwdUnits bwd_units(const CrossArgs& a, const CrossSeq& s) {
-  using C = BwdCfg<D, MODE>;
+  using C = BwdWork<D, MODE>;
   BwdUnits u = {0, 0, 0};
   if (s.n == 0 || s.len == 0) return u;  // the gradients are zeros: the preparing kernel writes them
-  if (MODE == 0) {
+  if (bwd_short<D>(s, a.group) != (MODE == 2)) return u;
+  if (MODE == 2) {
+    u.fix = 1;
+    u.str = (s.len + C::STR - 1) / C::STR;
+  } else if (MODE == 0) {
     const int t = bwd_tokens0<D>(a.group);
     u.fix = (s.len + 127) / 128;
     u.str = (s.n + t - 1) / t;
   } else {
     const int t = bwd_tokens1(a.group);
     u.fix = (s.n + t - 1) / t;
-    u.str = (s.len + C::BS - 1) / C::BS;
+    u.str = (s.len + C::STR - 1) / C::STR;
   }
   u.units = u.fix * a.heads * C::HALVES;
   return u;
@@ -147,7 +170,7 @@ __host__ __device__ __forceinline__ BwdUnits bwd_units(const CrossArgs& a, const
 // ------------------------------------------------------------------ segments
 template <int D, int MODE>
 struct CrossBwdWalk {
-  using C = CrossBwdCfg<D, MODE>;
+  using C = BwdWork<D, MODE>;
   int b, u, j;
   CrossSeq s;
   BwdUnits c;
@@ -198,7 +221,7 @@ struct CrossBwdWalk {
     } else {
       g.tok0 = tile * bwd_tokens1(p.a.group);
       g.fix0 = s.row0 + g.tok0;
-      g.fix_n = min(bwd_tokens1(p.a.group), s.n - g.tok0);
+      g.fix_n = MODE == 2 ? s.n : min(bwd_tokens1(p.a.group), s.n - g.tok0);
       g.str0 = s.key0;
       g.str_n = s.len;
     }
@@ -216,17 +239,11 @@ struct CrossBwdWalk {
   }
 };
 
-template <int D, int MODE>
-__device__ __forceinline__ BwdSeg* bwd_seg_slot(uint8_t* gbase, int k) {
-  return reinterpret_cast<BwdSeg*>(gbase + CrossBwdCfg<D, MODE>::OFF_SEG) + (k % kBwdSegRing);
-}
-
-// Segment k, read by a whole warp of a role other than the load warp.
-template <int D, int MODE>
-__device__ __forceinline__ bool bwd_seg_read(BwdSeg& g, int k, uint8_t* gbase, const CrossBwdBars<D, MODE>& bar,
-                                             const WaitGuard& guard) {
+// Segment k of the ring at `ring`, read by a whole warp of a role other than the load warp.
+template <class Bars>
+__device__ __forceinline__ bool bwd_seg_read(BwdSeg& g, int k, const uint8_t* ring, const Bars& bar, const WaitGuard& guard) {
   if (!warp_wait_bar(bar.seg_full(k % kBwdSegRing), (k / kBwdSegRing) & 1, guard, kStatusTimeoutLoad)) return false;
-  const int4* src = reinterpret_cast<const int4*>(bwd_seg_slot<D, MODE>(gbase, k));
+  const int4* src = reinterpret_cast<const int4*>(reinterpret_cast<const BwdSeg*>(ring) + (k % kBwdSegRing));
   int4* dst = reinterpret_cast<int4*>(&g);
 #pragma unroll
   for (int i = 0; i < 3; ++i) dst[i] = src[i];
@@ -258,7 +275,7 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
     if (!(ok = warp_wait_bar(bar.seg_empty(i), ((k / kBwdSegRing) & 1) ^ 1, g, kStatusTimeoutLoad))) break;
     const BwdSeg w = walk.next(p);
     if (lane == 0) {
-      *bwd_seg_slot<D, MODE>(gbase, k) = w;
+      reinterpret_cast<BwdSeg*>(gbase + C::OFF_SEG)[i] = w;
       if (w.out == 2)  // this unit's first part: who holds the rest
         p.ws.rec[MODE][blockIdx.x] =
             PlanRecord{walk.record_b, w.head, walk.record_u,
@@ -323,35 +340,16 @@ __device__ __forceinline__ void cross_bwd_mma(const CrossBwdParams& p, const Cro
                                               uint8_t* gbase, uint32_t tmem, const WaitGuard& g) {
   using C = CrossBwdCfg<D, MODE>;
   const BwdMma<D, MODE> M(tmem, base);
-  const int lane = threadIdx.x & 31;
-  const int per = MODE == 0 ? bwd_tokens0<D>(p.a.group) : C::BS;  // tokens or keys of a streamed tile
   auto wait = [&](uint32_t b, uint32_t par) -> bool {
     const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
     return __all_sync(0xffffffffu, r);
-  };
-  // Rows of the streamed tile at stage st behind the last token or key: zeros.  (MODE 1: of K only; V's take part in
-  // dP alone, whose columns there are not looked at.)
-  auto clear_tail = [&](const BwdSeg& w, int t, uint32_t st) {
-    const int left = w.str_n - (w.s0 + t) * per;
-    if (left >= per) return;
-    const int from = MODE == 0 ? left * p.a.group : left;
-    const int to = MODE == 0 ? per * p.a.group : C::BS;
-    constexpr int UR = C::SWB / 16;
-    const uint32_t s0 = base + C::OFF_ST + st * C::STAGE;
-    for (int r = 0; r < C::NR; ++r)
-      for (int i = from * UR + lane; i < to * UR; i += 32) {
-        st_shared_v4(s0 + r * C::S_REGION + i * 16, 0, 0, 0, 0);
-        if constexpr (C::KV) st_shared_v4(s0 + C::S_TILE + r * C::S_REGION + i * 16, 0, 0, 0, 0);
-      }
-    fence_proxy_async_smem();
-    __syncwarp();
   };
   uint32_t pos = 0;            // streamed stages consumed before the current segment
   uint32_t pr0 = 0, pr1 = 0;   // p_ready phases consumed, per buffer
   bool ok = true;
   for (int k = 0; ok; ++k) {
     BwdSeg w;
-    if (!(ok = bwd_seg_read<D, MODE>(w, k, gbase, bar, g)) || !w.valid) break;
+    if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
     const int n = w.n;
     if (!(ok = wait(bar.fix_full(), k & 1))) break;
     tc_fence_after();
@@ -359,7 +357,6 @@ __device__ __forceinline__ void cross_bwd_mma(const CrossBwdParams& p, const Cro
     auto acquire = [&](int t) -> bool {
       const uint32_t q = pos + t;
       if (!wait(bar.st_full(q % C::NST), (q / C::NST) & 1)) return false;
-      clear_tail(w, t, q % C::NST);
       tc_fence_after();
       return true;
     };
@@ -417,7 +414,7 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
   bool ok = true;
   for (int k = 0; ok; ++k) {
     BwdSeg w;
-    if (!(ok = bwd_seg_read<D, MODE>(w, k, gbase, bar, g)) || !w.valid) break;
+    if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
     const int n = w.n;
     const bool mine = MODE == 0 ? r < w.fix_n : tok_r < w.fix_n;  // (tokens: fix_n <= 128 / G)
     uint64_t l2_row = 0, d_row = 0;  // MODE 1: this row's -L * log2(e) and -D, twice
@@ -426,7 +423,7 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
       if (mine) {
         const int t0 = bwd_tokens0<D>(p.a.group), tok = w.tok0 + tok_r;
         const long long at = (w.head * p.tiles + w.vec0 + tok / t0) * BwdCfg<D, 0>::BS + tok % t0 * p.a.group + head_r;
-        // (Written by the kernel before the one before: past L1.)
+        // (Written by a kernel that is not the one before: past L1.)
         l2 = __ldcg(p.ws.l2 + at);
         dsum = __ldcg(p.ws.dsum + at);
       }
@@ -445,10 +442,22 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
         if (!ok) break;
       }
       tc_fence_after();
-      // Rows of the tile that are a token's or a key's.  (The others are zeros in Q, dO and K, but zero times an infinity is NaN,
-      // and V's are whatever its neighbours are.)
+      // Rows of the tile that are a token's or a key's; the others are not looked at in S and dP, but meet zeros of P and dS in
+      // the accumulations.
       const int there = MODE == 0 ? min(w.str_n - (w.s0 + t) * per, per) * p.a.group : w.str_n - (w.s0 + t) * per;
       const bool need_mask = there < C::BS;
+      if (need_mask) {
+        const uint32_t tile = smem_u32(gbase + C::OFF_ST + st * C::STAGE);
+        for (int x = r; x < (C::KV ? 2 : 1) * C::BS; x += 128) {
+          const int row = x % C::BS;
+          if (row < there) continue;
+#pragma unroll
+          for (int u = 0; u < D / 8; ++u)
+            st_shared_v4(tile + x / C::BS * C::S_TILE + u / (C::SWB / 16) * C::S_REGION + row * C::SWB + u % (C::SWB / 16) * 16, 0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
       const float4* vl2 = reinterpret_cast<const float4*>(gbase + C::OFF_ST + st * C::STAGE + 2 * C::S_TILE);
       const float4* vd = vl2 + C::BS / 4;
 #pragma unroll 1
@@ -511,7 +520,7 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
     const int head = MODE == 0 ? w.head : w.head * p.a.group + head_r;
     const long long row = w.fix0 + (MODE == 0 ? r : tok_r);
     __nv_bfloat16* orow = out + row * os[0] + head * os[1] + w.half * C::OUTW;
-    float4* part = reinterpret_cast<float4*>(p.ws.part[MODE] + (blockIdx.x * 2 + (w.out - 1)) * bwd_part_floats<D, MODE>() +
+    float4* part = reinterpret_cast<float4*>(p.ws.part[MODE] + (blockIdx.x * 2 + (w.out - 1)) * BwdWork<D, MODE>::PART +
                                              (second ? 128 * C::OUTW : 0)) + r;
 #pragma unroll 1
     for (int c = 0; c < C::OUTW / 32; ++c) {
@@ -594,21 +603,17 @@ __global__ void __launch_bounds__(BwdCfg<D, MODE>::THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
     tmem_relinquish();
   }
-  if (MODE == 0 && bwd_tokens0<D>(p.a.group) * p.a.group < C::BS) {
-    // Rows of a streamed tile that no token fills stay zeros.
-    for (int i = threadIdx.x; i < C::NST * C::STAGE / 16; i += C::THREADS) st_shared_v4(base + C::OFF_ST + i * 16, 0, 0, 0, 0);
-    fence_proxy_async_smem();
-  }
   const PlanShare share = plan_share<C::THREADS>(
       p.a.cb.B, gridDim.x, blockIdx.x,
       [&](int b) -> long long {
         bool bad;
         const BwdUnits u = bwd_units<D, MODE>(p.a, cross_seq(p.a.cb, b, bad));
-        return static_cast<long long>(u.units) * (u.str + C::UNIT_COST);
+        return static_cast<long long>(u.units) * (u.str + BwdWork<D, MODE>::UNIT_COST);
       },
-      1 + C::UNIT_COST, *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
-  // The preparing kernel is done (MODE 1's CTAs begin when all of MODE 0's have come past here, so it is for them, too).
-  if (MODE == 0) pdl_wait();
+      1 + BwdWork<D, MODE>::UNIT_COST, *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
+  // The kernel that comes first waits for the preparing one; those behind it begin when all of its CTAs have done so.
+  constexpr bool FIRST = MODE == 0 && bwd_short_tiles(D) == 0;
+  if (FIRST) pdl_wait();
   pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
@@ -631,7 +636,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MODE>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
-  if (MODE == 1) pdl_wait();  // what waits for this kernel waits for MODE 0's, too
+  if (!FIRST) pdl_wait();  // what waits for this kernel waits for those before it, too
 }
 
 // ------------------------------------------------------------------ preparing
@@ -658,7 +663,11 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
     if (any) atomicOr(a.status, kBadBatchBit);
   }
   const int t0 = bwd_tokens0<D>(a.group);
-  for (long long tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+  const int sub = lane / CPR, chunk = lane % CPR;
+  // A tile of one key/value head's rows at a time.
+  for (long long x = blockIdx.x; x < p.tiles * a.heads; x += gridDim.x) {
+    const long long tile = x / a.heads;
+    const int head = static_cast<int>(x % a.heads);
     // The last sequence whose tiles begin at `tile` or before, found in steps of 32 sub-ranges (every warp for itself).
     int lo = 0, count = a.cb.B;
     while (count > 1) {
@@ -674,21 +683,21 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
     const CrossSeq s = cross_seq(a.cb, lo, bad);
     const long long first = (tile - bwd_tile0<D>(s, lo, a.group)) * t0;  // token of the tile's first row
     if (first < 0 || first >= s.n || s.len == 0) continue;               // nobody reads it
-    const int sub = lane / CPR, chunk = lane % CPR;
-    for (int i = warp * RPW + sub; i < a.heads * BS; i += WARPS * RPW) {
-      const int head = i / BS, r = i % BS;
+#pragma unroll 1
+    for (int r = warp * RPW + sub; r < BS; r += WARPS * RPW) {
       const int tok = r / a.group, hq = head * a.group + r % a.group;
       const bool valid = tok < t0 && first + tok < s.n;
-      float acc = 0.f;
+      float acc = 0.f, lse = 0.f;
       if (valid) {
         const long long row = s.row0 + first + tok;
-        const uint4 x = *reinterpret_cast<const uint4*>(a.o + row * a.st[3][0] + hq * a.st[3][1] + chunk * 8);
-        const uint4 y = *reinterpret_cast<const uint4*>(a.dout + row * a.st[4][0] + hq * a.st[4][1] + chunk * 8);
-        const uint32_t xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+        if (chunk == 0) lse = a.lse[static_cast<long long>(hq) * a.cb.rows + row];
+        const uint4 u4 = *reinterpret_cast<const uint4*>(a.o + row * a.st[3][0] + hq * a.st[3][1] + chunk * 8);
+        const uint4 v4 = *reinterpret_cast<const uint4*>(a.dout + row * a.st[4][0] + hq * a.st[4][1] + chunk * 8);
+        const uint32_t uv[4] = {u4.x, u4.y, u4.z, u4.w}, vv[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&xv[e]));
-          const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&yv[e]));
+          const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&uv[e]));
+          const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&vv[e]));
           acc = fmaf(u.x, v.x, acc);
           acc = fmaf(u.y, v.y, acc);
         }
@@ -698,23 +707,20 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
       if (chunk == 0) {
         const long long at = (head * p.tiles + tile) * BS + r;
         p.ws.dsum[at] = valid ? -acc : 0.f;
-        p.ws.l2[at] = valid ? -a.lse[static_cast<long long>(hq) * a.cb.rows + s.row0 + first + tok] * 1.4426950408889634f : -INFINITY;
+        p.ws.l2[at] = valid ? -lse * 1.4426950408889634f : -INFINITY;
       }
     }
   }
-  // Zeros: several blocks to a sequence.
+  // Zeros: several blocks to a sequence, a warp to a row.
   const int per = gridDim.x / a.cb.B > 0 ? gridDim.x / a.cb.B : 1;
   for (int x = blockIdx.x; x / per < a.cb.B; x += gridDim.x) {
     const int b = x / per, part = x % per;
     bool bad;
     const CrossSeq s = cross_seq(a.cb, b, bad);
     auto fill = [&](__nv_bfloat16* out, const long long* st, int row0, int from, int to, int heads) {
-      const long long items = static_cast<long long>(to - from) * heads * CPR;
-      for (long long i = static_cast<long long>(part) * kPrepThreads + threadIdx.x; i < items; i += static_cast<long long>(per) * kPrepThreads) {
-        const long long row = row0 + from + i / (heads * CPR);
-        const int rest = static_cast<int>(i % (heads * CPR));
-        *reinterpret_cast<uint4*>(out + row * st[0] + rest / CPR * st[1] + rest % CPR * 8) = make_uint4(0, 0, 0, 0);
-      }
+      for (int row = from + part * WARPS + warp; row < to; row += per * WARPS)
+        for (int c = lane; c < heads * CPR; c += 32)
+          *reinterpret_cast<uint4*>(out + (static_cast<long long>(row0) + row) * st[0] + c / CPR * st[1] + c % CPR * 8) = make_uint4(0, 0, 0, 0);
     };
     const int from = s.n > 0 ? s.len : 0;
     fill(a.dk, a.st[6], s.key0, from, s.places, a.heads);
@@ -724,11 +730,11 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
 }
 
 // ------------------------------------------------------------------ joining
-// Joins the parts of the units that several CTAs held; blocks (c, .) those of the units that CTA c began (z = 0: dK and dV,
-// z = 1: dQ).  A warp takes 16 columns of 32 rows, a row a lane.
+// Joins the parts of the units that several CTAs held; blocks (c, .) those of the unit that CTA c began.  A warp takes 16
+// columns of 32 rows, a row a lane (a part holds blocks of 4 columns of 128 rows: MODE 0: dK's half, then dV's; MODE 2: tile by tile).
 template <int D, int MODE>
 __device__ __forceinline__ void cross_bwd_join(const CrossBwdParams& p) {
-  using C = BwdCfg<D, MODE>;
+  using C = BwdWork<D, MODE>;
   const CrossArgs& a = p.a;
   const PlanRecord rec = p.ws.rec[MODE][blockIdx.x];
   if (rec.b < 0) return;
@@ -736,17 +742,21 @@ __device__ __forceinline__ void cross_bwd_join(const CrossBwdParams& p) {
   bool bad;
   const CrossSeq s = cross_seq(a.cb, rec.b, bad);
   const BwdUnits u = bwd_units<D, MODE>(a, s);
-  const int half = rec.qb % C::HALVES, tile = rec.qb / C::HALVES % u.fix;
-  constexpr size_t stride = 2 * bwd_part_floats<D, MODE>();  // from one CTA's parts to the next's
+  const int half = rec.qb % C::HALVES, tile0 = rec.qb / C::HALVES % u.fix;
+  constexpr size_t stride = 2 * C::PART;  // from one CTA's parts to the next's
   const float* first = p.ws.part[MODE] + blockIdx.x * stride + stride / 2;
   const float* rest = first + stride / 2 - stride;  // part 0 of CTA + i at rest + i * stride
   const int n = rec.more + 1;
-  constexpr int COLS = C::NOUT * C::OUTW / 16;
+  constexpr int WIDTH = MODE == 0 ? D / C::HALVES : D;          // columns of a block of 128 rows
+  constexpr int BLOCKS = static_cast<int>(C::PART / (128 * WIDTH));  // dK and dV, dQ, or dQ's tiles
+  constexpr int COLS = BLOCKS * WIDTH / 16;
   for (int job = blockIdx.y * 4 + warp; job < 4 * COLS; job += gridDim.y * 4) {
     const int r = job % 4 * 32 + lane, c16 = job / 4;
+    const int block = c16 * 16 / WIDTH, c = c16 * 16 % WIDTH;
+    const int tile = MODE == 2 ? block : tile0;
     const int tok = MODE == 0 ? r : r / a.group;
     const int left = MODE == 0 ? s.len - tile * 128 : s.n - tile * bwd_tokens1(a.group);
-    if (tok >= left || (MODE == 1 && tok >= bwd_tokens1(a.group))) continue;
+    if (tok >= left || (MODE != 0 && tok >= bwd_tokens1(a.group))) continue;
     float4 acc[4] = {};
 #pragma unroll 2
     for (int i = 0; i < n; ++i) {
@@ -760,15 +770,14 @@ __device__ __forceinline__ void cross_bwd_join(const CrossBwdParams& p) {
         acc[k].w += y.w;
       }
     }
-    const bool second = MODE == 0 && c16 * 16 >= C::OUTW;
-    const int c = c16 * 16 - (second ? C::OUTW : 0);
-    const float f = second ? 1.f : a.scale;
+    const bool is_dv = MODE == 0 && block == 1;
+    const float f = is_dv ? 1.f : a.scale;
     const int head = MODE == 0 ? rec.head : rec.head * a.group + r % a.group;
     const long long row = MODE == 0 ? static_cast<long long>(s.key0) + tile * 128 + r
                                     : static_cast<long long>(s.row0) + tile * bwd_tokens1(a.group) + tok;
-    const long long* os = a.st[MODE == 1 ? 5 : second ? 7 : 6];
-    uint4* dst = reinterpret_cast<uint4*>((MODE == 1 ? a.dq : second ? a.dv : a.dk) + row * os[0] + head * os[1] +
-                                          half * C::OUTW + c);
+    const long long* os = a.st[MODE != 0 ? 5 : is_dv ? 7 : 6];
+    uint4* dst = reinterpret_cast<uint4*>((MODE != 0 ? a.dq : is_dv ? a.dv : a.dk) + row * os[0] + head * os[1] +
+                                          half * WIDTH + c);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       dst[k] = make_uint4(pack_bf16x2(acc[2 * k].x * f, acc[2 * k].y * f), pack_bf16x2(acc[2 * k].z * f, acc[2 * k].w * f),
@@ -777,13 +786,15 @@ __device__ __forceinline__ void cross_bwd_join(const CrossBwdParams& p) {
   }
 }
 
+// The parts of all kernels, or (`longer` false) of MODE 2 alone.
 template <int D>
-__global__ void __launch_bounds__(128) fa_cross_bwd_join_kernel(const __grid_constant__ CrossBwdParams p) {
+__global__ void __launch_bounds__(128) fa_cross_bwd_join_kernel(const __grid_constant__ CrossBwdParams p, bool longer) {
   pdl_wait();
-  if (blockIdx.z == 0)
+  if constexpr (bwd_short_tiles(D) > 0) cross_bwd_join<D, 2>(p);
+  if (longer) {
     cross_bwd_join<D, 0>(p);
-  else
     cross_bwd_join<D, 1>(p);
+  }
 }
 
 // ------------------------------------------------------------------ launch
@@ -808,24 +819,6 @@ int launch_cross_bwd_mode(const CrossBwdParams& p, int grid, const LaunchCtx& ct
     return -1;
   return MODE == 0 ? launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mk, mv, mq, mo, p)
                    : launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mq, mo, mk, mv, p);
-}
-
-template <int D>
-int launch_cross_bwd(const CrossArgs& a, const LaunchCtx& ctx) {
-  CrossBwdParams p;
-  p.a = a;
-  cross_bwd_ws<D>(a.workspace, a.cb.B, a.cb.rows, a.heads, a.group, &p.ws);
-  p.limit_ns = ctx.limit_ns;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.tiles = bwd_tiles<D>(a.cb.rows, a.cb.B, a.group);
-  fa_cross_prep_kernel<D><<<ctx.num_sms * 8, kPrepThreads, 0, ctx.stream>>>(p);
-  int e = static_cast<int>(cudaGetLastError());
-  if (e != 0 || a.cb.rows == 0 || a.cb.keys == 0) return e;  // (zeros are all there is)
-  const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
-  e = launch_cross_bwd_mode<D, 0>(p, grid, ctx);
-  if (e == 0) e = launch_cross_bwd_mode<D, 1>(p, grid, ctx);
-  if (e == 0) e = launch_dependent(fa_cross_bwd_join_kernel<D>, dim3(grid, 16, 2), 128, 0, ctx.stream, p);
-  return e;
 }
 
 }  // namespace fa

@@ -1,5 +1,5 @@
 // Gradients of cross attention, head dimension 256.
-#include "fa_cross_bwd.cuh"
+#include "fa_cross_bwd_short.cuh"
 
 namespace fa {
 int launch_cross_bwd_d256(const CrossArgs& a, const LaunchCtx& ctx) { return launch_cross_bwd<256>(a, ctx); }

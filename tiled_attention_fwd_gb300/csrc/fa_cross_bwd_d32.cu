@@ -1,5 +1,5 @@
 // Gradients of cross attention, head dimension 32.
-#include "fa_cross_bwd.cuh"
+#include "fa_cross_bwd_short.cuh"
 
 namespace fa {
 int launch_cross_bwd_d32(const CrossArgs& a, const LaunchCtx& ctx) { return launch_cross_bwd<32>(a, ctx); }

@@ -1,0 +1,672 @@
+// Gradients of cross attention for sequences of few rows (all heads of a group
+// within 512, 256 or 128 rows at d = 32, 64, 128): dQ, dK and dV in one pass
+// over the keys, and the launch of the whole backward pass.
+//
+// A unit is one key/value head of a sequence: its Q and dO stay in shared memory,
+// tiles of 128 keys of K and V stream past, and each tile's dK and dV are finished
+// with it, for all rows that add to them are there.  Five products a tile, where
+// the two kernels for longer sequences (fa_cross_bwd.cuh) need seven, and every
+// tensor is read or written once.  An item is QT rows against 128 keys:
+//   S^T = K Q^T, dP^T = V dO^T          128 lanes = keys, QT columns = rows, double-buffered in tensor memory
+//   P^T, dS^T in bf16 over them         two warpgroups take turns
+//   dV += P^T dO, dK += dS^T Q          A from tensor memory; read out and stored by a third warpgroup, key tile by key tile
+//   dQ += dS K                          A = dS^T, which the warpgroups also write to shared memory (M-major), over all key tiles
+// Items run on across key tiles and units, two of them in flight; Q and dO come in 128-row
+// tiles through a ring of their own, so that the next unit's are there when this one ends.
+#pragma once
+
+#include "fa_cross_bwd.cuh"
+
+namespace fa {
+
+template <int D>
+struct ShortCfg {
+  static constexpr int QT = D <= 64 ? 64 : 32;          // rows of an item
+  static constexpr int TILES = bwd_short_tiles(D);      // 128-row tiles of a unit at most
+  static constexpr int SLOTS = D == 32 ? 6 : D == 64 ? 3 : 1;  // of the ring of Q and dO tiles
+  static constexpr int SWB = (D * 2 >= 128) ? 128 : D * 2;  // swizzle span in bytes
+  static constexpr uint32_t SWZ = (SWB == 128) ? 2u : 4u;   // descriptor swizzle code
+  static constexpr int RC = SWB / 2;                    // bf16 columns per swizzle region
+  static constexpr int NR = D / RC;
+  static constexpr int REGION = 128 * SWB;
+  static constexpr int TILE = 128 * D * 2;              // bytes of 128 rows or keys
+  static constexpr int STAGE = 2 * TILE;                // K, V
+  // Shared memory: [Q, dO tiles][K/V stages][dS^T: 2 regions of 64 rows, 128 keys][misc].
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_ST = SLOTS * 2 * TILE;
+  static constexpr int DS_REGION = 128 * 128;
+  static constexpr int DS = 2 * DS_REGION;
+  static constexpr int VEC = 2 * 128 * 4;               // bytes of -L log2e and -D of a tile's rows
+  static constexpr int MISC = 1024 + SLOTS * VEC;
+  static constexpr int SMEM_LIMIT = 227 * 1024;
+  static constexpr int NST_FIT = (SMEM_LIMIT - 1024 - MISC - DS - OFF_ST) / STAGE;
+  static constexpr int NST = NST_FIT > 4 ? 4 : NST_FIT;
+  static constexpr int OFF_DS = OFF_ST + NST * STAGE;
+  static constexpr int OFF_MISC = OFF_DS + DS;
+  static constexpr int OFF_TMEM_SLOT = OFF_MISC + 384;
+  static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
+  static constexpr int OFF_SEG = OFF_MISC + 400;
+  static constexpr int OFF_PLAN = OFF_SEG + kBwdSegRing * static_cast<int>(sizeof(BwdSeg));
+  static constexpr int OFF_VEC = OFF_MISC + 1024;
+  static constexpr int SMEM_USED = OFF_MISC + MISC + 1024;  // + slack for 1024-byte alignment
+  static constexpr int SMEM_ALLOC = SMEM_USED < 120 * 1024 ? 120 * 1024 : SMEM_USED;
+  // TMEM columns: S^T buffers, dP^T buffers, dK, dV, dQ's tiles.
+  static constexpr int TM_S = 0;
+  static constexpr int TM_DP = 2 * QT;
+  static constexpr int TM_DK = 4 * QT;
+  static constexpr int TM_DV = 4 * QT + D;
+  static constexpr int TM_DQ = 4 * QT + 2 * D;
+  static constexpr int TM_COLS = 512;
+  // Warps: 0-3 and 4-7 elementwise (buffer 0, 1), 8-11 output, 12 MMA, 13 load.
+  static constexpr int OUT_WARP0 = 8;
+  static constexpr int MMA_WARP = 12;
+  static constexpr int LOAD_WARP = 13;
+  static constexpr int THREADS = 448;
+  static constexpr int READERS = 13;
+  static_assert(TM_DQ + TILES * D <= TM_COLS, "TMEM budget");
+  static_assert(SLOTS >= TILES && NST >= 2 && SMEM_USED <= SMEM_LIMIT, "shared memory budget");
+  static_assert(OFF_PLAN % 8 == 0 && OFF_PLAN + sizeof(PlanScratch) <= OFF_VEC, "misc area");
+};
+
+template <int D>
+struct ShortBars {
+  using C = ShortCfg<D>;
+  uint32_t b0;
+  __device__ __forceinline__ uint32_t s_full(int b) const { return b0 + 8u * b; }         // S^T and dP^T of buffer b
+  __device__ __forceinline__ uint32_t p_ready(int b) const { return b0 + 16 + 8u * b; }   // P^T and dS^T (4 warps)
+  // dS^T in shared memory (its m-th row tile) has been read.  Two barriers take turns: where a row tile is one item, a warpgroup
+  // may come to tile m + 2 before tile m has been read, and a barrier two phases behind looks as if it had.
+  __device__ __forceinline__ uint32_t ds_empty(uint32_t m) const { return b0 + 32 + 8u * (m & 1); }
+  __device__ __forceinline__ uint32_t kv_done() const { return b0 + 48; }   // dK and dV of a key tile
+  __device__ __forceinline__ uint32_t kv_free() const { return b0 + 56; }   // read out (4 warps)
+  __device__ __forceinline__ uint32_t dq_done() const { return b0 + 64; }
+  __device__ __forceinline__ uint32_t dq_free() const { return b0 + 72; }
+  __device__ __forceinline__ uint32_t drain() const { return b0 + 80; }
+  __device__ __forceinline__ uint32_t seg_full(int i) const { return b0 + 88 + 8u * i; }
+  __device__ __forceinline__ uint32_t seg_empty(int i) const { return b0 + 120 + 8u * i; }
+  __device__ __forceinline__ uint32_t st_full(int i) const { return b0 + 152 + 8u * i; }
+  __device__ __forceinline__ uint32_t st_empty(int i) const { return b0 + 152 + 8u * (C::NST + i); }
+  // A tile of Q and dO and its vectors (the copies, and the load warp's own stores) / used for the last time.
+  __device__ __forceinline__ uint32_t q_full(int i) const { return b0 + 152 + 16u * C::NST + 8u * i; }
+  __device__ __forceinline__ uint32_t q_empty(int i) const { return b0 + 152 + 16u * C::NST + 8u * (C::SLOTS + i); }
+  static_assert(152 + 16 * (C::NST + C::SLOTS) <= 384 && kBwdSegRing == 4, "barrier area");
+};
+
+// Rows of tile i of a unit of n tokens.
+__device__ __forceinline__ int short_rows(int n, int i, int t1, int group) { return min(n - i * t1, t1) * group; }
+
+// Walks the items of this CTA's segments: key tiles, within them the unit's 128-row tiles, within those QT rows at a time.
+template <int D>
+struct ShortItem {
+  using C = ShortCfg<D>;
+  BwdSeg w;
+  int k;             // segment
+  int j, i, s;       // key tile, row tile, QT rows of it
+  int nt, ns;        // row tiles of the unit; items of row tile i
+  uint32_t tile;     // key tiles before this one's
+  uint32_t slot0;    // row tiles of the segments before this one's
+  __device__ __forceinline__ void rows(int t1, int group) { ns = (short_rows(w.fix_n, i, t1, group) + C::QT - 1) / C::QT; }
+  // A segment has been read into w.
+  __device__ __forceinline__ void enter(int t1, int group) {
+    j = i = s = 0;
+    nt = (w.fix_n + t1 - 1) / t1;
+    rows(t1, group);
+  }
+  // On to the next item; false where that is the next segment's first.
+  __device__ __forceinline__ bool next(int t1, int group) {
+    if (++s < ns) return true;
+    s = 0;
+    if (++i == nt) {
+      i = 0;
+      ++tile;
+      if (++j == w.n) {
+        slot0 += nt;
+        ++k;
+        return false;
+      }
+    }
+    rows(t1, group);
+    return true;
+  }
+  __device__ __forceinline__ uint32_t slot() const { return slot0 + i; }
+};
+
+// ------------------------------------------------------------------ load warp
+template <int D>
+__device__ __forceinline__ void short_load(const CUtensorMap* tm_q, const CUtensorMap* tm_do, const CUtensorMap* tm_k,
+                                           const CUtensorMap* tm_v, const CrossBwdParams& p, const ShortBars<D>& bar,
+                                           uint32_t base, uint8_t* gbase, const PlanShare& share, const WaitGuard& g) {
+  using C = ShortCfg<D>;
+  const int lane = threadIdx.x & 31;
+  const uint64_t policy = policy_evict_first();  // everything is read once
+  const int group = p.a.group, t1 = bwd_tokens1(group), t0 = bwd_tokens0<D>(group);
+  uint32_t pos = 0;       // stages issued so far
+  uint32_t issued = 0;    // bit i: stage i has been loaded at least once
+  uint32_t last_par = 0;  // bit i: parity of stage i's latest load
+  uint32_t slots = 0;     // row tiles issued so far; and as for the stages:
+  uint32_t q_issued = 0, q_par = 0;
+  bool recorded = false, ok = true;
+  CrossBwdWalk<D, 2> walk;
+  walk.start(p, share);
+  for (int k = 0;; ++k) {
+    const int i = k % kBwdSegRing;
+    if (!(ok = warp_wait_bar(bar.seg_empty(i), ((k / kBwdSegRing) & 1) ^ 1, g, kStatusTimeoutLoad))) break;
+    const BwdSeg w = walk.next(p);
+    if (lane == 0) {
+      reinterpret_cast<BwdSeg*>(gbase + C::OFF_SEG)[i] = w;
+      if (w.out == 2)  // this unit's first part: who holds the rest
+        p.ws.rec[2][blockIdx.x] =
+            PlanRecord{walk.record_b, w.head, walk.record_u,
+                       plan_cta_of(walk.last_tile, share.total, share.ctas) - static_cast<int>(blockIdx.x)};
+    }
+    recorded = recorded || w.out == 2;
+    warp_arrive(bar.seg_full(i));
+    if (!w.valid) break;
+    auto load_kv = [&](int t) -> bool {
+      const int st = pos % C::NST;
+      const uint32_t par = (pos / C::NST) & 1;
+      if (!warp_wait_bar(bar.st_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
+      if (lane == 0) {
+        const uint32_t s0 = base + C::OFF_ST + st * C::STAGE;
+        const int row = w.str0 + (w.s0 + t) * 128;
+        mbar_arrive_expect_tx(bar.st_full(st), C::STAGE);
+        for (int r = 0; r < C::NR; ++r) {
+          tma_load_3d(s0 + r * C::REGION, tm_k, bar.st_full(st), r * C::RC, w.head, row, policy);
+          tma_load_3d(s0 + C::TILE + r * C::REGION, tm_v, bar.st_full(st), r * C::RC, w.head, row, policy);
+        }
+      }
+      issued |= 1u << st;
+      last_par = (last_par & ~(1u << st)) | (par << st);
+      ++pos;
+      return true;
+    };
+    auto load_q = [&](int x) -> bool {
+      const int slot = slots % C::SLOTS;
+      const uint32_t par = (slots / C::SLOTS) & 1;
+      // The vectors are on their way while the slot may still be read.
+      float l2[4], dsum[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = e * 32 + lane, tok = x * t1 + r / group, h = r % group;
+        l2[e] = -INFINITY;
+        dsum[e] = 0.f;
+        if (r < t1 * group && tok < w.fix_n) {
+          const long long at = (w.head * p.tiles + w.vec0 + tok / t0) * BwdCfg<D, 0>::BS + tok % t0 * group + h;
+          l2[e] = __ldcg(p.ws.l2 + at);
+          dsum[e] = __ldcg(p.ws.dsum + at);
+        }
+      }
+      if (!warp_wait_bar(bar.q_empty(slot), par ^ 1, g, kStatusTimeoutLoad)) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar.q_full(slot), 2 * C::NR * t1 * group * C::SWB);
+        for (int r = 0; r < C::NR; ++r) {
+          const uint32_t dst = base + C::OFF_Q + slot * 2 * C::TILE + r * C::REGION;
+          tma_load_3d(dst, tm_q, bar.q_full(slot), r * C::RC, w.head * group, w.fix0 + x * t1, policy);
+          tma_load_3d(dst + C::TILE, tm_do, bar.q_full(slot), r * C::RC, w.head * group, w.fix0 + x * t1, policy);
+        }
+      }
+      float* vec = reinterpret_cast<float*>(gbase + C::OFF_VEC + slot * C::VEC);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        vec[e * 32 + lane] = l2[e];
+        vec[128 + e * 32 + lane] = dsum[e];
+      }
+      warp_arrive(bar.q_full(slot));
+      q_issued |= 1u << slot;
+      q_par = (q_par & ~(1u << slot)) | (par << slot);
+      ++slots;
+      return true;
+    };
+    // The first K and V come before Q and dO, whose place is free later.
+    const int nt = (w.fix_n + t1 - 1) / t1;
+    ok = load_kv(0);
+    for (int x = 0; ok && x < nt; ++x) ok = load_q(x);
+    for (int t = 1; ok && t < w.n; ++t) ok = load_kv(t);
+    if (!ok) break;
+  }
+  if (lane == 0 && !recorded) p.ws.rec[2][blockIdx.x].b = -1;
+  // Every issued copy must land before the CTA may exit.
+  for (int i = 0; i < C::NST; ++i)
+    if (issued & (1u << i)) bwd_wait_drain(bar.st_full(i), (last_par >> i) & 1, g);
+  for (int i = 0; i < C::SLOTS; ++i)
+    if (q_issued & (1u << i)) bwd_wait_drain(bar.q_full(i), (q_par >> i) & 1, g);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ MMA issuer
+template <int D>
+struct ShortMma {
+  using C = ShortCfg<D>;
+  static constexpr uint32_t IDESC_S = make_idesc_bf16(128, C::QT, 0);  // S^T, dP^T: B K-major
+  static constexpr uint32_t IDESC_O = make_idesc_bf16(128, D, 1);      // dV, dK: A in TMEM, B MN-major
+  static constexpr uint32_t IDESC_Q = IDESC_O | (1u << 15);            // dQ: A M-major
+  static constexpr uint32_t HI = sdesc_hi(8 * C::SWB, C::SWZ);
+  static constexpr uint32_t HI_DS = sdesc_hi(8 * 128, 2);
+  static constexpr __host__ __device__ uint32_t k_step(int kk) {
+    return ((kk * 16 / C::RC) * C::REGION + (kk * 16 % C::RC) * 2) >> 4;
+  }
+  struct SSteps {
+    static constexpr __host__ __device__ uint32_t da(int k) { return k_step(k) - k_step(k - 1); }
+    static constexpr __host__ __device__ uint32_t db(int k) { return k_step(k) - k_step(k - 1); }
+  };
+  struct AccSteps {
+    static constexpr __host__ __device__ uint32_t ta(int) { return 8; }  // 16 bf16 = 8 TMEM columns
+    static constexpr __host__ __device__ uint32_t db(int) { return 16 * C::SWB >> 4; }
+  };
+  struct QSteps {
+    static constexpr __host__ __device__ uint32_t da(int) { return 16 * 128 >> 4; }  // 16 keys of dS^T
+    static constexpr __host__ __device__ uint32_t db(int) { return 16 * C::SWB >> 4; }
+  };
+  uint32_t tmem, base;
+  // S^T and dP^T of rows s QT .. of the tile in `slot` and the keys at stage st, into buffer b.
+  __device__ __forceinline__ void sdp(uint32_t st, uint32_t slot, int s, int b) const {
+    const uint32_t k = sdesc_lo(base + C::OFF_ST + st * C::STAGE, 16), v = k + (C::TILE >> 4);
+    const uint32_t q = sdesc_lo(base + C::OFF_Q + slot * 2 * C::TILE + s * C::QT * C::SWB, 16), o = q + (C::TILE >> 4);
+    mma_ss_run<D / 16, SSteps>(tmem + C::TM_S + b * C::QT, k, HI, q, HI, IDESC_S, 0u);
+    mma_ss_run<D / 16, SSteps>(tmem + C::TM_DP + b * C::QT, v, HI, o, HI, IDESC_S, 0u);
+  }
+  // dV (+)= P^T dO, dK (+)= dS^T Q.
+  __device__ __forceinline__ void dkv(uint32_t slot, int s, int b, bool acc) const {
+    const uint32_t q = sdesc_lo(base + C::OFF_Q + slot * 2 * C::TILE + s * C::QT * C::SWB, C::REGION), o = q + (C::TILE >> 4);
+    mma_ts_run<C::QT / 16, AccSteps>(tmem + C::TM_DV, tmem + C::TM_S + b * C::QT, o, HI, IDESC_O, acc ? 1u : 0u);
+    mma_ts_run<C::QT / 16, AccSteps>(tmem + C::TM_DK, tmem + C::TM_DP + b * C::QT, q, HI, IDESC_O, acc ? 1u : 0u);
+  }
+  // dQ of row tile i (+)= dS K.
+  __device__ __forceinline__ void dq(uint32_t st, int i, bool acc) const {
+    mma_ss_run<8, QSteps>(tmem + C::TM_DQ + i * D, sdesc_lo(base + C::OFF_DS, C::DS_REGION), HI_DS,
+                          sdesc_lo(base + C::OFF_ST + st * C::STAGE, C::REGION), HI, IDESC_Q, acc ? 1u : 0u);
+  }
+};
+
+// Per item: dV, dK; S^T and dP^T of the item after the next into the buffer that they leave; dQ where a row tile is complete.
+template <int D>
+__device__ __forceinline__ void short_mma(const CrossBwdParams& p, const ShortBars<D>& bar, uint32_t base, uint8_t* gbase,
+                                          uint32_t tmem, const WaitGuard& g) {
+  using C = ShortCfg<D>;
+  const ShortMma<D> M{tmem, base};
+  const int group = p.a.group, t1 = bwd_tokens1(group);
+  auto wait = [&](uint32_t b, uint32_t par) -> bool {
+    const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
+    return __all_sync(0xffffffffu, r);
+  };
+  ShortItem<D> at = {}, ahead = {};  // the item whose P^T comes next; the one whose S^T does
+  bool more = true;                  // `ahead` is one
+  // `ahead` reads a segment without handing it back; `at` does that.
+  auto enter_ahead = [&]() -> bool {
+    if (!wait(bar.seg_full(ahead.k % kBwdSegRing), (ahead.k / kBwdSegRing) & 1)) return false;
+    ahead.w = reinterpret_cast<const BwdSeg*>(gbase + C::OFF_SEG)[ahead.k % kBwdSegRing];
+    more = ahead.w.valid != 0;
+    if (more) ahead.enter(t1, group);
+    return true;
+  };
+  uint32_t issued = 0;      // items whose S^T and dP^T are on their way
+  uint32_t st_free = 0, q_free = 0;  // stages and row tiles handed back
+  uint32_t dqs = 0;                  // row tiles of dS^T multiplied
+  // S^T and dP^T of items up to `to`, as far as their K, V, Q and dO can be there: what they wait for must not wait for `at`.
+  auto issue = [&](uint32_t to) -> bool {
+    while (more && issued <= to && ahead.tile < st_free + C::NST && ahead.slot() < q_free + C::SLOTS) {
+      const uint32_t slot = ahead.slot();
+      if (ahead.i == 0 && ahead.s == 0 && !wait(bar.st_full(ahead.tile % C::NST), (ahead.tile / C::NST) & 1)) return false;
+      if (ahead.j == 0 && ahead.s == 0 && !wait(bar.q_full(slot % C::SLOTS), (slot / C::SLOTS) & 1)) return false;
+      tc_fence_after();
+      M.sdp(ahead.tile % C::NST, slot % C::SLOTS, ahead.s, issued & 1);
+      mma_commit_elect(bar.s_full(issued & 1));
+      ++issued;
+      if (!ahead.next(t1, group) && !enter_ahead()) return false;
+    }
+    return true;
+  };
+  bool ok = enter_ahead();
+  bool begun = false;  // `at` is within a segment
+  for (uint32_t n = 0; ok; ++n) {
+    if (!begun) {
+      if (!(ok = bwd_seg_read(at.w, at.k, gbase + C::OFF_SEG, bar, g)) || !at.w.valid) break;
+      at.enter(t1, group);
+      begun = true;
+    }
+    if (!(ok = issue(n + 1))) break;
+    const uint32_t slot = at.slot() % C::SLOTS, st = at.tile % C::NST;
+    const int i = at.i, j = at.j, b = n & 1;
+    const bool last_s = at.s == at.ns - 1, last = last_s && i == at.nt - 1, first = i == 0 && at.s == 0;
+    if (!(ok = wait(bar.p_ready(b), (n >> 1) & 1))) break;
+    if (first && at.tile > 0 && !(ok = wait(bar.kv_free(), (at.tile - 1) & 1))) break;
+    tc_fence_after();
+    M.dkv(slot, at.s, b, !first);
+    if (last) mma_commit_elect(bar.kv_done());
+    if (last_s && j == at.w.n - 1) {
+      mma_commit_elect(bar.q_empty(slot));
+      ++q_free;
+    }
+    if (!(ok = issue(n + 2))) break;
+    if (last_s) {
+      if (j == 0 && i == 0 && at.k > 0) {
+        if (!(ok = wait(bar.dq_free(), (at.k - 1) & 1))) break;
+        tc_fence_after();
+      }
+      M.dq(st, i, j > 0);
+      mma_commit_elect(bar.ds_empty(dqs++));
+      if (last) {
+        mma_commit_elect(bar.st_empty(st));
+        ++st_free;
+        if (j == at.w.n - 1) mma_commit_elect(bar.dq_done());
+      }
+    }
+    begun = at.next(t1, group);
+  }
+  // All issued MMAs must complete before TMEM is released.
+  mma_commit_elect(bar.drain());
+  bwd_wait_drain(bar.drain(), 0, g);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ elementwise warpgroups
+// Warpgroup b takes every other item; thread = key.  What would meet a zero of P^T or dS^T in a product (Q and dO behind a tile's
+// last row, K behind the last key: anything, and 0 times NaN is NaN) is set to zero by the warpgroup of the first item that reads
+// it, behind that item's S^T and dP^T, whose rows and columns there are not looked at.
+template <int D>
+__device__ __forceinline__ void short_elementwise(const CrossBwdParams& p, const ShortBars<D>& bar, uint32_t base, uint8_t* gbase,
+                                                  uint32_t tmem, int b, int quarter, int lane, const WaitGuard& g) {
+  using C = ShortCfg<D>;
+  constexpr int UNITS = D / 8;  // 16-byte units of a row
+  const int r = quarter * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint64_t sl2x2 = f2_pack(p.scale_log2, p.scale_log2);
+  const int group = p.a.group, t1 = bwd_tokens1(group);
+  uint32_t dqs = 0;  // row tiles of dS^T before this item's
+  auto zero_row = [&](uint32_t tile, int row) {
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) st_shared_v4(tile + u / (C::SWB / 16) * C::REGION + row * C::SWB + u % (C::SWB / 16) * 16, 0, 0, 0, 0);
+  };
+  ShortItem<D> it = {};
+  bool begun = false, ok = true;
+  for (uint32_t n = 0; ok; ++n) {
+    if (!begun) {
+      if (!(ok = bwd_seg_read(it.w, it.k, gbase + C::OFF_SEG, bar, g)) || !it.w.valid) break;
+      it.enter(t1, group);
+      begun = true;
+    }
+    const uint32_t slot = it.slot() % C::SLOTS;
+    if ((n & 1) == static_cast<uint32_t>(b)) {
+      const int rows = short_rows(it.w.fix_n, it.i, t1, group) - it.s * C::QT;  // of this item's QT on
+      const int left = it.w.str_n - (it.w.s0 + it.j) * 128;
+      const bool key = r < left;  // this thread's key is one
+      if (!(ok = warp_wait_bar(bar.s_full(b), (n >> 1) & 1, g, kStatusTimeoutSoftmax))) break;
+      // (Complete, for the MMA warp has waited for it: this makes the vectors visible here.)
+      if (!(ok = warp_wait_bar(bar.q_full(slot), (it.slot() / C::SLOTS) & 1, g, kStatusTimeoutSoftmax))) break;
+      tc_fence_after();
+      if (it.j == 0 && rows < C::QT) {
+        const uint32_t tile = base + C::OFF_Q + slot * 2 * C::TILE;
+        for (int x = r; x < 2 * C::QT; x += 128) {
+          const int row = x % C::QT;
+          if (row >= rows) zero_row(tile + x / C::QT * C::TILE, it.s * C::QT + row);
+        }
+      }
+      if (it.i == 0 && it.s == 0 && !key) zero_row(base + C::OFF_ST + it.tile % C::NST * C::STAGE, r);
+      __syncwarp();
+      const bool need_mask = left < 128 || rows < C::QT;
+      const float4* vl2 = reinterpret_cast<const float4*>(gbase + C::OFF_VEC + slot * C::VEC) + it.s * (C::QT / 4);
+      const float4* vd = vl2 + 32;
+#pragma unroll 1
+      for (int h = 0; h < C::QT / 32; ++h) {
+        uint32_t rs[32], rd[32];
+        tmem_ld32(tmem + lane_off + C::TM_S + b * C::QT + h * 32, rs);
+        tmem_ld32(tmem + lane_off + C::TM_DP + b * C::QT + h * 32, rd);
+        tmem_wait_ld(rs);
+        tmem_wait_ld(rd);
+        uint32_t pk[16], dk[16];
+#pragma unroll
+        for (int c4 = 0; c4 < 8; ++c4) {
+          const float4 a = vl2[h * 8 + c4], d4 = vd[h * 8 + c4];
+          const uint64_t nl[2] = {f2_pack(a.x, a.y), f2_pack(a.z, a.w)}, nd[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
+#pragma unroll
+          for (int e2 = 0; e2 < 2; ++e2) {
+            const int c = c4 * 4 + e2 * 2;
+            const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2x2, nl[e2]));
+            float p0 = ex2(x.x), p1 = ex2(x.y);
+            float2 ds = f2_unpack(
+                f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(rd[c]), __uint_as_float(rd[c + 1])), nd[e2])));
+            if (need_mask) {
+              if (!key || h * 32 + c >= rows) p0 = ds.x = 0.f;
+              if (!key || h * 32 + c + 1 >= rows) p1 = ds.y = 0.f;
+            }
+            pk[c4 * 2 + e2] = pack_bf16x2(p0, p1);
+            dk[c4 * 2 + e2] = pack_bf16x2(ds.x, ds.y);
+          }
+        }
+        // Chunk h's bf16 pairs land behind what has been read.
+        tmem_st16(tmem + lane_off + C::TM_S + b * C::QT + h * 16, pk);
+        tmem_st16(tmem + lane_off + C::TM_DP + b * C::QT + h * 16, dk);
+        // The row tile's dS^T before this one has been read.
+        if (h == 0 && dqs > 0 && !(ok = warp_wait_bar(bar.ds_empty(dqs - 1), ((dqs - 1) >> 1) & 1, g, kStatusTimeoutSoftmax))) break;
+        // dS^T into shared memory: key r's row of 64 rows of Q a region, 128-byte swizzled.
+        const int q0 = it.s * C::QT + h * 32;
+        const uint32_t row = base + C::OFF_DS + (q0 >> 6) * C::DS_REGION + r * 128;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          st_shared_v4(row + (((((q0 & 63) >> 3) + u) ^ (r & 7)) << 4), dk[4 * u], dk[4 * u + 1], dk[4 * u + 2], dk[4 * u + 3]);
+      }
+      if (!ok) break;
+      tmem_wait_st();
+      tc_fence_before();
+      fence_proxy_async_smem();
+      warp_arrive(bar.p_ready(b));
+    }
+    if (it.s == it.ns - 1) ++dqs;
+    begun = it.next(t1, group);
+  }
+}
+
+// ------------------------------------------------------------------ output
+template <int D>
+__device__ __forceinline__ void short_output(const CrossBwdParams& p, const ShortBars<D>& bar, uint8_t* gbase, uint32_t tmem,
+                                             int quarter, int lane, const WaitGuard& g) {
+  using C = ShortCfg<D>;
+  const int r = quarter * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const int group = p.a.group, t1 = bwd_tokens1(group);
+  const int tok_r = r / group, head_r = r - tok_r * group;
+  uint32_t tiles = 0;  // key tiles read out
+  bool ok = true;
+  // 32 columns of TMEM times f, as bf16.
+  auto chunk = [&](uint32_t at, uint32_t (&v)[32]) {
+    tmem_ld32(tmem + lane_off + at, v);
+    tmem_wait_ld(v);
+  };
+  auto store = [&](const uint32_t (&v)[32], float f, __nv_bfloat16* to) {
+    const uint64_t f2 = f2_pack(f, f);
+    uint4* dst = reinterpret_cast<uint4*>(to);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[8 * u + 2 * e]), __uint_as_float(v[8 * u + 2 * e + 1])), f2));
+        y[e] = pack_bf16x2(x.x, x.y);
+      }
+      dst[u] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  };
+  for (int k = 0; ok; ++k) {
+    BwdSeg w;
+    if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
+    for (int j = 0; j < w.n; ++j) {
+      if (!(ok = warp_wait_bar(bar.kv_done(), tiles & 1, g, kStatusTimeoutSoftmax))) break;
+      ++tiles;
+      tc_fence_after();
+      const int at = (w.s0 + j) * 128 + r;
+      const bool mine = at < w.str_n;
+      const long long row = static_cast<long long>(w.str0) + at;
+      __nv_bfloat16* dk = p.a.dk + row * p.a.st[6][0] + w.head * p.a.st[6][1];
+      __nv_bfloat16* dv = p.a.dv + row * p.a.st[7][0] + w.head * p.a.st[7][1];
+#pragma unroll 1
+      for (int c = 0; c < 2 * D / 32; ++c) {
+        uint32_t v[32];
+        const bool is_dv = c >= D / 32;
+        const int cc = is_dv ? c - D / 32 : c;
+        chunk(C::TM_DK + c * 32, v);  // (dV lies behind dK)
+        if (c == 2 * D / 32 - 1) {
+          tc_fence_before();
+          warp_arrive(bar.kv_free());
+        }
+        if (mine) store(v, is_dv ? 1.f : p.a.scale, (is_dv ? dv : dk) + cc * 32);
+      }
+    }
+    if (!ok || !(ok = warp_wait_bar(bar.dq_done(), k & 1, g, kStatusTimeoutSoftmax))) break;
+    tc_fence_after();
+    const int nt = (w.fix_n + t1 - 1) / t1;
+#pragma unroll 1
+    for (int c = 0; c < nt * (D / 32); ++c) {
+      uint32_t v[32];
+      const int i = c / (D / 32), cc = c % (D / 32), tok = i * t1 + tok_r;
+      chunk(C::TM_DQ + c * 32, v);
+      if (w.out == 0) {
+        if (tok_r < t1 && tok < w.fix_n)
+          store(v, p.a.scale, p.a.dq + (static_cast<long long>(w.fix0) + tok) * p.a.st[5][0] +
+                                  static_cast<long long>(w.head * group + head_r) * p.a.st[5][1] + cc * 32);
+      } else {
+        // 16-byte block b of all 128 rows of the tile together.
+        float4* part = reinterpret_cast<float4*>(p.ws.part[2] + (blockIdx.x * 2 + (w.out - 1)) * BwdWork<D, 2>::PART) + r;
+#pragma unroll
+        for (int b = 0; b < 8; ++b)
+          part[(c * 8 + b) * 128] = make_float4(__uint_as_float(v[4 * b]), __uint_as_float(v[4 * b + 1]),
+                                                __uint_as_float(v[4 * b + 2]), __uint_as_float(v[4 * b + 3]));
+      }
+    }
+    tc_fence_before();
+    warp_arrive(bar.dq_free());
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <int D>
+__global__ void __launch_bounds__(ShortCfg<D>::THREADS, 1)
+    fa_cross_bwd_short_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                              const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                              const __grid_constant__ CrossBwdParams p) {
+  using C = ShortCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const ShortBars<D> bar{base + C::OFF_MISC};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::OFF_TMEM_SLOT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_ABORT);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar.s_full(i), 1);
+      mbar_init(bar.p_ready(i), 4);
+    }
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(bar.q_full(i), 2);
+      mbar_init(bar.q_empty(i), 1);
+    }
+    mbar_init(bar.ds_empty(0), 1);
+    mbar_init(bar.ds_empty(1), 1);
+    mbar_init(bar.kv_done(), 1);
+    mbar_init(bar.kv_free(), 4);
+    mbar_init(bar.dq_done(), 1);
+    mbar_init(bar.dq_free(), 4);
+    mbar_init(bar.drain(), 1);
+    for (int i = 0; i < kBwdSegRing; ++i) {
+      mbar_init(bar.seg_full(i), 1);
+      mbar_init(bar.seg_empty(i), C::READERS);
+    }
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(bar.st_full(i), 1);
+      mbar_init(bar.st_empty(i), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::LOAD_WARP && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_do);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
+    tmem_relinquish();
+  }
+  const PlanShare share = plan_share<C::THREADS>(
+      p.a.cb.B, gridDim.x, blockIdx.x,
+      [&](int b) -> long long {
+        bool bad;
+        const BwdUnits u = bwd_units<D, 2>(p.a, cross_seq(p.a.cb, b, bad));
+        return static_cast<long long>(u.units) * (u.str + BwdWork<D, 2>::UNIT_COST);
+      },
+      1 + BwdWork<D, 2>::UNIT_COST, *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
+  pdl_wait();  // for the preparing kernel; and so have all CTAs when the next kernel's begin
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitGuard g{abort_flag, p.a.status, p.limit_ns};
+
+  if (warp < C::OUT_WARP0) {
+    short_elementwise<D>(p, bar, base, gbase, tmem, warp >> 2, warp & 3, lane, g);
+  } else if (warp < C::MMA_WARP) {
+    short_output<D>(p, bar, gbase, tmem, warp & 3, lane, g);
+  } else if (warp == C::MMA_WARP) {
+    short_mma<D>(p, bar, base, gbase, tmem, g);
+  } else {
+    short_load<D>(&tm_q, &tm_do, &tm_k, &tm_v, p, bar, base, gbase, share, g);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------ launch
+template <int D>
+int launch_cross_bwd_short(const CrossBwdParams& p, int grid, const LaunchCtx& ctx) {
+  using C = ShortCfg<D>;
+  auto kernel = fa_cross_bwd_short_kernel<D>;
+  static std::atomic<unsigned long long> allowed{0};
+  const int e = allow_smem(kernel, C::SMEM_ALLOC, allowed);
+  if (e != 0) return e;
+  const CrossArgs& a = p.a;
+  CUtensorMap mq, mo, mk, mv;
+  const long long qd[3] = {D, a.q_heads, a.cb.rows}, kd[3] = {D, a.heads, a.cb.keys};
+  auto encode = [&](CUtensorMap* m, const void* t, int i, const long long* dims, int box1, int box2) {
+    const long long st[2] = {a.st[i][1], a.st[i][0]};
+    return encode_paged_map(m, t, 2, dims, st, C::RC, box1, box2, C::SWB, false);
+  };
+  if (encode(&mq, a.q, 0, qd, a.group, bwd_tokens1(a.group)) != 0 || encode(&mo, a.dout, 4, qd, a.group, bwd_tokens1(a.group)) != 0 ||
+      encode(&mk, a.k, 1, kd, 1, 128) != 0 || encode(&mv, a.v, 2, kd, 1, 128) != 0)
+    return -1;
+  return launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mq, mo, mk, mv, p);
+}
+
+// The preparing kernel, the kernel for few rows, the two for more (where there may be such sequences), and the joining of parts.
+template <int D>
+int launch_cross_bwd(const CrossArgs& a, const LaunchCtx& ctx) {
+  CrossBwdParams p;
+  p.a = a;
+  cross_bwd_ws<D>(a.workspace, a.cb.B, a.cb.rows, a.heads, a.group, &p.ws);
+  p.limit_ns = ctx.limit_ns;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.tiles = bwd_tiles<D>(a.cb.rows, a.cb.B, a.group);
+  fa_cross_prep_kernel<D><<<ctx.num_sms * 8, kPrepThreads, 0, ctx.stream>>>(p);
+  int e = static_cast<int>(cudaGetLastError());
+  if (e != 0 || a.cb.rows == 0 || a.cb.keys == 0) return e;  // (zeros are all there is)
+  const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
+  constexpr bool SHORT = bwd_short_tiles(D) > 0;
+  const bool longer = !SHORT || a.cb.rows > bwd_short_tiles(D) * bwd_tokens1(a.group);
+  if constexpr (SHORT) e = launch_cross_bwd_short<D>(p, grid, ctx);
+  if (e == 0 && longer) e = launch_cross_bwd_mode<D, 0>(p, grid, ctx);
+  if (e == 0 && longer) e = launch_cross_bwd_mode<D, 1>(p, grid, ctx);
+  if (e == 0) e = launch_dependent(fa_cross_bwd_join_kernel<D>, dim3(grid, 8), 128, 0, ctx.stream, p, longer);
+  return e;
+}
+
+}  // namespace fa
