@@ -60,19 +60,21 @@ struct BwdWork {
   static constexpr int STR = BwdCfg<D, MODE>::BS;
   static constexpr size_t PART = static_cast<size_t>(128) * BwdCfg<D, MODE>::NOUT * BwdCfg<D, MODE>::OUTW;  // floats of a part
   // Streamed tiles that a unit costs besides its own (loading the fixed tiles, the output).
-  static constexpr int UNIT_COST = 2;
+  static constexpr int UNIT_COST = 2;  // (of places on the line, as a streamed tile is one)
 };
 template <int D>
 struct BwdWork<D, 2> {
   static constexpr int HALVES = 1;
   static constexpr int STR = 128;
   static constexpr size_t PART = static_cast<size_t>(128) * bwd_short_tiles(D) * D;
-  static constexpr int UNIT_COST = 1;
+  static constexpr int QT = D <= 64 ? 64 : 32;  // rows of an item (fa_cross_bwd_short.cuh); a streamed tile has as many places as items
+  static constexpr int UNIT_COST = 2;
 };
 
 // Workspace of fa_cross_bwd.
 struct CrossBwdWs {
   PlanRecord* rec[3];  // of the kernels: [kPlanCtas]
+  int* part0;          // [kPlanCtas]: MODE 2's CTA has written its part 0
   float* l2;           // [heads][tiles][BS]
   float* dsum;
   float* part[3];      // [kPlanCtas][2][part floats]
@@ -88,6 +90,7 @@ size_t cross_bwd_ws(char* p, int B, int rows, int heads, int group, CrossBwdWs* 
   CrossBwdWs x;
   const size_t vec = static_cast<size_t>(heads) * bwd_tiles<D>(rows, B, group) * BwdCfg<D, 0>::BS * sizeof(float);
   for (int i = 0; i < 3; ++i) x.rec[i] = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
+  x.part0 = reinterpret_cast<int*>(take(kPlanCtas * sizeof(int)));
   x.l2 = reinterpret_cast<float*>(take(vec));
   x.dsum = reinterpret_cast<float*>(take(vec));
   x.part[0] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, 0>::PART * sizeof(float)));
@@ -144,16 +147,24 @@ struct BwdUnits {
   int fix;    // fixed tiles a head
   int str;    // streamed tiles
   int units;  // fixed tiles x heads x halves
+  int w;      // places of a streamed tile on the line
+  // Places of a unit.
+  template <int COST>
+  __host__ __device__ __forceinline__ int length() const { return str * w + COST; }
 };
 template <int D, int MODE>
 __host__ __device__ __forceinline__ BwdUnits bwd_units(const CrossArgs& a, const CrossSeq& s) {
   using C = BwdWork<D, MODE>;
-  BwdUnits u = {0, 0, 0};
+  BwdUnits u = {0, 0, 0, 1};
   if (s.n == 0 || s.len == 0) return u;  // the gradients are zeros: the preparing kernel writes them
   if (bwd_short<D>(s, a.group) != (MODE == 2)) return u;
   if (MODE == 2) {
     u.fix = 1;
     u.str = (s.len + C::STR - 1) / C::STR;
+    if constexpr (MODE == 2) {
+      const int t = bwd_tokens1(a.group), full = s.n / t, rest = s.n % t;  // whole row tiles, and tokens of the last one
+      u.w = full * ((t * a.group + C::QT - 1) / C::QT) + (rest * a.group + C::QT - 1) / C::QT;
+    }
   } else if (MODE == 0) {
     const int t = bwd_tokens0<D>(a.group);
     u.fix = (s.len + 127) / 128;
@@ -189,13 +200,20 @@ struct CrossBwdWalk {
     b = w.b;
     if (pos >= end) return;
     load(p);
-    const int unit = c.str + C::UNIT_COST;
+    const int unit = c.template length<C::UNIT_COST>();
     u = static_cast<int>(w.offset / unit);
-    j = static_cast<int>(w.offset - static_cast<long long>(u) * unit);
-    if (j >= c.str) advance(p);  // behind a unit's tiles: the share's first tile is the next unit's
+    const int in = static_cast<int>(w.offset - static_cast<long long>(u) * unit);
+    // The first tile that begins at the share's first place or behind it.
+    j = (in + c.w - 1) / c.w;
+    if (j >= c.str) {
+      pos += unit - in;
+      enter(p);
+    } else {
+      pos += j * c.w - in;
+    }
   }
-  __device__ __forceinline__ void advance(const CrossBwdParams& p) {
-    pos += c.str - j + C::UNIT_COST;
+  // On to the next unit, if the share reaches it.
+  __device__ __forceinline__ void enter(const CrossBwdParams& p) {
     j = 0;
     if (pos >= end) return;
     if (++u < c.units) return;
@@ -208,7 +226,8 @@ struct CrossBwdWalk {
   __device__ __forceinline__ BwdSeg next(const CrossBwdParams& p) {
     BwdSeg g = {};
     if (pos >= end) return g;
-    const int n = end - pos < c.str - j ? static_cast<int>(end - pos) : c.str - j;
+    const long long begin = (end - pos + c.w - 1) / c.w;  // tiles that begin before the share's end
+    const int n = begin < c.str - j ? static_cast<int>(begin) : c.str - j;
     g.valid = 1;
     g.half = u % C::HALVES;
     const int tile = u / C::HALVES % c.fix;
@@ -229,12 +248,15 @@ struct CrossBwdWalk {
     g.s0 = j;
     g.n = n;
     g.out = n == c.str ? 0 : j == 0 ? 2 : 1;
-    last_tile = pos + (c.str - 1 - j);
+    last_tile = pos + static_cast<long long>(c.str - 1 - j) * c.w;
     record_u = u;
     record_b = b;
-    pos += n;
+    pos += static_cast<long long>(n) * c.w;
     j += n;
-    if (j == c.str) advance(p);
+    if (j == c.str) {
+      pos += C::UNIT_COST;
+      enter(p);
+    }
     return g;
   }
 };
@@ -608,7 +630,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MODE>::THREADS, 1)
       [&](int b) -> long long {
         bool bad;
         const BwdUnits u = bwd_units<D, MODE>(p.a, cross_seq(p.a.cb, b, bad));
-        return static_cast<long long>(u.units) * (u.str + BwdWork<D, MODE>::UNIT_COST);
+        return u.units == 0 ? 0ll : static_cast<long long>(u.units) * u.template length<BwdWork<D, MODE>::UNIT_COST>();
       },
       1 + BwdWork<D, MODE>::UNIT_COST, *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
   // The kernel that comes first waits for the preparing one; those behind it begin when all of its CTAs have done so.
@@ -760,6 +782,7 @@ __device__ __forceinline__ void cross_bwd_join(const CrossBwdParams& p) {
     float4 acc[4] = {};
 #pragma unroll 2
     for (int i = 0; i < n; ++i) {
+      if (MODE == 2 && i > 0 && p.ws.part0[blockIdx.x + i] == 0) continue;  // no tile began in that CTA's share
       const float4* x = reinterpret_cast<const float4*>(i == 0 ? first : rest + i * stride) + r;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {

@@ -8,9 +8,10 @@
 // the two kernels for longer sequences (fa_cross_bwd.cuh) need seven, and every
 // tensor is read or written once.  An item is QT rows against 128 keys:
 //   S^T = K Q^T, dP^T = V dO^T          128 lanes = keys, QT columns = rows, double-buffered in tensor memory
-//   P^T, dS^T in bf16 over them         two warpgroups take turns
+//   P^T, dS^T in bf16 over them         two warpgroups, half the columns each (d = 128: they take turns)
 //   dV += P^T dO, dK += dS^T Q          A from tensor memory; read out and stored by a third warpgroup, key tile by key tile
-//   dQ += dS K                          A = dS^T, which the warpgroups also write to shared memory (M-major), over all key tiles
+//   dQ += dS K                          A = dS^T, which the warpgroups also write to shared memory (M-major), over all key tiles;
+//                                       issued by a warp of its own (d <= 64)
 // Items run on across key tiles and units, two of them in flight; Q and dO come in 128-row
 // tiles through a ring of their own, so that the next unit's are there when this one ends.
 #pragma once
@@ -21,7 +22,12 @@ namespace fa {
 
 template <int D>
 struct ShortCfg {
-  static constexpr int QT = D <= 64 ? 64 : 32;          // rows of an item
+  static constexpr int QT = BwdWork<D, 2>::QT;          // rows of an item
+  // Both warpgroups take part in every item, half its columns each (QT = 64), or they take turns (QT = 32).
+  static constexpr bool SPLIT = QT == 64;
+  static constexpr int EW_WARPS = SPLIT ? 8 : 4;        // of an item
+  static constexpr int EW_COLS = SPLIT ? QT / 2 : QT;   // columns of a thread
+  static constexpr int SUBS = 128 / QT;                 // items of a full row tile
   static constexpr int TILES = bwd_short_tiles(D);      // 128-row tiles of a unit at most
   static constexpr int SLOTS = D == 32 ? 6 : D == 64 ? 3 : 1;  // of the ring of Q and dO tiles
   static constexpr int SWB = (D * 2 >= 128) ? 128 : D * 2;  // swizzle span in bytes
@@ -57,12 +63,15 @@ struct ShortCfg {
   static constexpr int TM_DV = 4 * QT + D;
   static constexpr int TM_DQ = 4 * QT + 2 * D;
   static constexpr int TM_COLS = 512;
-  // Warps: 0-3 and 4-7 elementwise (buffer 0, 1), 8-11 output, 12 MMA, 13 load.
+  // Warps: 0-7 elementwise, 8-11 output, 12 MMA, 13 load, 14 MMA of dQ.
   static constexpr int OUT_WARP0 = 8;
   static constexpr int MMA_WARP = 12;
   static constexpr int LOAD_WARP = 13;
-  static constexpr int THREADS = 448;
-  static constexpr int READERS = 13;
+  // (Only where a row tile has two items: the warp waits for each buffer once a row tile, and with four it could miss a phase.)
+  static constexpr bool DQ_APART = SUBS == 2;
+  static constexpr int DQ_WARP = 14;
+  static constexpr int THREADS = DQ_APART ? 480 : 448;
+  static constexpr int READERS = DQ_APART ? 14 : 13;
   static_assert(TM_DQ + TILES * D <= TM_COLS, "TMEM budget");
   static_assert(SLOTS >= TILES && NST >= 2 && SMEM_USED <= SMEM_LIMIT, "shared memory budget");
   static_assert(OFF_PLAN % 8 == 0 && OFF_PLAN + sizeof(PlanScratch) <= OFF_VEC, "misc area");
@@ -73,7 +82,7 @@ struct ShortBars {
   using C = ShortCfg<D>;
   uint32_t b0;
   __device__ __forceinline__ uint32_t s_full(int b) const { return b0 + 8u * b; }         // S^T and dP^T of buffer b
-  __device__ __forceinline__ uint32_t p_ready(int b) const { return b0 + 16 + 8u * b; }   // P^T and dS^T (4 warps)
+  __device__ __forceinline__ uint32_t p_ready(int b) const { return b0 + 16 + 8u * b; }   // P^T and dS^T (EW_WARPS)
   // dS^T in shared memory (its m-th row tile) has been read.  Two barriers take turns: where a row tile is one item, a warpgroup
   // may come to tile m + 2 before tile m has been read, and a barrier two phases behind looks as if it had.
   __device__ __forceinline__ uint32_t ds_empty(uint32_t m) const { return b0 + 32 + 8u * (m & 1); }
@@ -82,6 +91,7 @@ struct ShortBars {
   __device__ __forceinline__ uint32_t dq_done() const { return b0 + 64; }
   __device__ __forceinline__ uint32_t dq_free() const { return b0 + 72; }
   __device__ __forceinline__ uint32_t drain() const { return b0 + 80; }
+  __device__ __forceinline__ uint32_t drain_dq() const { return b0 + 376; }
   __device__ __forceinline__ uint32_t seg_full(int i) const { return b0 + 88 + 8u * i; }
   __device__ __forceinline__ uint32_t seg_empty(int i) const { return b0 + 120 + 8u * i; }
   __device__ __forceinline__ uint32_t st_full(int i) const { return b0 + 152 + 8u * i; }
@@ -89,46 +99,66 @@ struct ShortBars {
   // A tile of Q and dO and its vectors (the copies, and the load warp's own stores) / used for the last time.
   __device__ __forceinline__ uint32_t q_full(int i) const { return b0 + 152 + 16u * C::NST + 8u * i; }
   __device__ __forceinline__ uint32_t q_empty(int i) const { return b0 + 152 + 16u * C::NST + 8u * (C::SLOTS + i); }
-  static_assert(152 + 16 * (C::NST + C::SLOTS) <= 384 && kBwdSegRing == 4, "barrier area");
+  static_assert(152 + 16 * (C::NST + C::SLOTS) <= 376 && kBwdSegRing == 4, "barrier area");
 };
 
 // Rows of tile i of a unit of n tokens.
 __device__ __forceinline__ int short_rows(int n, int i, int t1, int group) { return min(n - i * t1, t1) * group; }
 
-// Walks the items of this CTA's segments: key tiles, within them the unit's 128-row tiles, within those QT rows at a time.
+// A place in a ring of N: its index and the parity of its phase.
+template <int N>
+struct RingPos {
+  uint32_t at = 0, par = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      par ^= 1;
+    }
+  }
+};
+
+// Walks the items of this CTA's segments: key tiles, within them the unit's items, SUBS to a row tile.
 template <int D>
 struct ShortItem {
   using C = ShortCfg<D>;
-  BwdSeg w;
-  int k;             // segment
-  int j, i, s;       // key tile, row tile, QT rows of it
-  int nt, ns;        // row tiles of the unit; items of row tile i
-  uint32_t tile;     // key tiles before this one's
-  uint32_t slot0;    // row tiles of the segments before this one's
-  __device__ __forceinline__ void rows(int t1, int group) { ns = (short_rows(w.fix_n, i, t1, group) + C::QT - 1) / C::QT; }
-  // A segment has been read into w.
-  __device__ __forceinline__ void enter(int t1, int group) {
-    j = i = s = 0;
-    nt = (w.fix_n + t1 - 1) / t1;
-    rows(t1, group);
+  int n;             // key tiles of the segment
+  int items;         // items of a key tile
+  int j, m;          // key tile, item of it
+  RingPos<C::NST> st;        // the key tile's stage
+  uint32_t slot0 = 0;        // row tiles of the segments before this one's, modulo SLOTS, and the parity of their phase
+  uint32_t slot0_par = 0;
+  // A segment has been read.
+  __device__ __forceinline__ void enter(const BwdSeg& w, int t1, int group) {
+    const int nt = (w.fix_n + t1 - 1) / t1;
+    n = w.n;
+    items = (nt - 1) * C::SUBS + (short_rows(w.fix_n, nt - 1, t1, group) + C::QT - 1) / C::QT;
+    j = m = 0;
+  }
+  __device__ __forceinline__ int tile() const { return m / C::SUBS; }  // row tile of the unit
+  __device__ __forceinline__ int sub() const { return m % C::SUBS; }
+  __device__ __forceinline__ bool last_sub() const { return sub() == C::SUBS - 1 || m == items - 1; }
+  __device__ __forceinline__ bool last() const { return m == items - 1; }
+  __device__ __forceinline__ void slot(uint32_t& at, uint32_t& par) const {
+    at = slot0 + tile();
+    par = slot0_par;
+    if (at >= C::SLOTS) {  // (a unit has SLOTS row tiles at most)
+      at -= C::SLOTS;
+      par ^= 1;
+    }
   }
   // On to the next item; false where that is the next segment's first.
-  __device__ __forceinline__ bool next(int t1, int group) {
-    if (++s < ns) return true;
-    s = 0;
-    if (++i == nt) {
-      i = 0;
-      ++tile;
-      if (++j == w.n) {
-        slot0 += nt;
-        ++k;
-        return false;
-      }
+  __device__ __forceinline__ bool next() {
+    if (++m < items) return true;
+    m = 0;
+    st.next();
+    if (++j < n) return true;
+    slot0 += (items + C::SUBS - 1) / C::SUBS;
+    if (slot0 >= C::SLOTS) {
+      slot0 -= C::SLOTS;
+      slot0_par ^= 1;
     }
-    rows(t1, group);
-    return true;
+    return false;
   }
-  __device__ __forceinline__ uint32_t slot() const { return slot0 + i; }
 };
 
 // ------------------------------------------------------------------ load warp
@@ -145,7 +175,7 @@ __device__ __forceinline__ void short_load(const CUtensorMap* tm_q, const CUtens
   uint32_t last_par = 0;  // bit i: parity of stage i's latest load
   uint32_t slots = 0;     // row tiles issued so far; and as for the stages:
   uint32_t q_issued = 0, q_par = 0;
-  bool recorded = false, ok = true;
+  bool recorded = false, part0 = false, ok = true;
   CrossBwdWalk<D, 2> walk;
   walk.start(p, share);
   for (int k = 0;; ++k) {
@@ -160,6 +190,7 @@ __device__ __forceinline__ void short_load(const CUtensorMap* tm_q, const CUtens
                        plan_cta_of(walk.last_tile, share.total, share.ctas) - static_cast<int>(blockIdx.x)};
     }
     recorded = recorded || w.out == 2;
+    part0 = part0 || w.out == 1;
     warp_arrive(bar.seg_full(i));
     if (!w.valid) break;
     auto load_kv = [&](int t) -> bool {
@@ -225,6 +256,7 @@ __device__ __forceinline__ void short_load(const CUtensorMap* tm_q, const CUtens
     if (!ok) break;
   }
   if (lane == 0 && !recorded) p.ws.rec[2][blockIdx.x].b = -1;
+  if (lane == 0) p.ws.part0[blockIdx.x] = part0 ? 1 : 0;
   // Every issued copy must land before the CTA may exit.
   for (int i = 0; i < C::NST; ++i)
     if (issued & (1u << i)) bwd_wait_drain(bar.st_full(i), (last_par >> i) & 1, g);
@@ -257,101 +289,139 @@ struct ShortMma {
     static constexpr __host__ __device__ uint32_t da(int) { return 16 * 128 >> 4; }  // 16 keys of dS^T
     static constexpr __host__ __device__ uint32_t db(int) { return 16 * C::SWB >> 4; }
   };
-  uint32_t tmem, base;
-  // S^T and dP^T of rows s QT .. of the tile in `slot` and the keys at stage st, into buffer b.
-  __device__ __forceinline__ void sdp(uint32_t st, uint32_t slot, int s, int b) const {
-    const uint32_t k = sdesc_lo(base + C::OFF_ST + st * C::STAGE, 16), v = k + (C::TILE >> 4);
-    const uint32_t q = sdesc_lo(base + C::OFF_Q + slot * 2 * C::TILE + s * C::QT * C::SWB, 16), o = q + (C::TILE >> 4);
-    mma_ss_run<D / 16, SSteps>(tmem + C::TM_S + b * C::QT, k, HI, q, HI, IDESC_S, 0u);
-    mma_ss_run<D / 16, SSteps>(tmem + C::TM_DP + b * C::QT, v, HI, o, HI, IDESC_S, 0u);
+  uint32_t tmem;
+  uint32_t q_lo, q_mn;    // Q of slot 0 (dO lies a tile behind), K-major and MN-major
+  uint32_t kv_lo, k_mn;   // K of stage 0 (V lies a tile behind)
+  uint32_t ds_lo;
+  __device__ __forceinline__ ShortMma(uint32_t tmem_, uint32_t base) : tmem(tmem_) {
+    q_lo = sdesc_lo(base + C::OFF_Q, 16);
+    q_mn = sdesc_lo(base + C::OFF_Q, C::REGION);
+    kv_lo = sdesc_lo(base + C::OFF_ST, 16);
+    k_mn = sdesc_lo(base + C::OFF_ST, C::REGION);
+    ds_lo = sdesc_lo(base + C::OFF_DS, C::DS_REGION);
   }
-  // dV (+)= P^T dO, dK (+)= dS^T Q.
-  __device__ __forceinline__ void dkv(uint32_t slot, int s, int b, bool acc) const {
-    const uint32_t q = sdesc_lo(base + C::OFF_Q + slot * 2 * C::TILE + s * C::QT * C::SWB, C::REGION), o = q + (C::TILE >> 4);
-    mma_ts_run<C::QT / 16, AccSteps>(tmem + C::TM_DV, tmem + C::TM_S + b * C::QT, o, HI, IDESC_O, acc ? 1u : 0u);
-    mma_ts_run<C::QT / 16, AccSteps>(tmem + C::TM_DK, tmem + C::TM_DP + b * C::QT, q, HI, IDESC_O, acc ? 1u : 0u);
+  static constexpr uint32_t V = C::TILE >> 4;
+  static __device__ __forceinline__ uint32_t q_off(uint32_t slot, int s) {
+    return slot * (2 * C::TILE >> 4) + static_cast<uint32_t>(s) * (C::QT * C::SWB >> 4);
+  }
+  // S^T and dP^T of rows s QT .. of the tile in `slot` and the keys at stage st, into buffer b.
+  __device__ __forceinline__ void sdp(uint32_t st, uint32_t slot, int s, uint32_t b) const {
+    const uint32_t k = kv_lo + st * (C::STAGE >> 4), q = q_lo + q_off(slot, s);
+    mma_ss_run<D / 16, SSteps>(tmem + C::TM_S + b * C::QT, k, HI, q, HI, IDESC_S, 0u);
+    mma_ss_run<D / 16, SSteps>(tmem + C::TM_DP + b * C::QT, k + V, HI, q + V, HI, IDESC_S, 0u);
+  }
+  // dV (+)= P^T dO, dK (+)= dS^T Q (SPLIT: the two warpgroups' halves of the rows one after the other).
+  __device__ __forceinline__ void dkv(uint32_t slot, int s, uint32_t b, bool acc) const {
+    const uint32_t q = q_mn + q_off(slot, s);
+    const uint32_t f = acc ? 1u : 0u;
+    constexpr int N = C::EW_COLS / 16;
+    constexpr uint32_t HALF = C::EW_COLS * C::SWB >> 4;
+    mma_ts_run<N, AccSteps>(tmem + C::TM_DV, tmem + C::TM_S + b * C::QT, q + V, HI, IDESC_O, f);
+    if constexpr (C::SPLIT)
+      mma_ts_run<N, AccSteps>(tmem + C::TM_DV, tmem + C::TM_S + b * C::QT + C::EW_COLS, q + V + HALF, HI, IDESC_O, 1u);
+    mma_ts_run<N, AccSteps>(tmem + C::TM_DK, tmem + C::TM_DP + b * C::QT, q, HI, IDESC_O, f);
+    if constexpr (C::SPLIT)
+      mma_ts_run<N, AccSteps>(tmem + C::TM_DK, tmem + C::TM_DP + b * C::QT + C::EW_COLS, q + HALF, HI, IDESC_O, 1u);
   }
   // dQ of row tile i (+)= dS K.
   __device__ __forceinline__ void dq(uint32_t st, int i, bool acc) const {
-    mma_ss_run<8, QSteps>(tmem + C::TM_DQ + i * D, sdesc_lo(base + C::OFF_DS, C::DS_REGION), HI_DS,
-                          sdesc_lo(base + C::OFF_ST + st * C::STAGE, C::REGION), HI, IDESC_Q, acc ? 1u : 0u);
+    mma_ss_run<8, QSteps>(tmem + C::TM_DQ + i * D, ds_lo, HI_DS, k_mn + st * (C::STAGE >> 4), HI, IDESC_Q, acc ? 1u : 0u);
   }
 };
 
-// Per item: dV, dK; S^T and dP^T of the item after the next into the buffer that they leave; dQ where a row tile is complete.
+// Per item: dV, dK; S^T and dP^T of the item after the next into the buffer that they leave; dQ where a row tile is complete.  (DQ_APART:
+// dQ is a warp's of its own: what bounds a tile here is how fast its 40 small products are issued.)
 template <int D>
 __device__ __forceinline__ void short_mma(const CrossBwdParams& p, const ShortBars<D>& bar, uint32_t base, uint8_t* gbase,
                                           uint32_t tmem, const WaitGuard& g) {
   using C = ShortCfg<D>;
-  const ShortMma<D> M{tmem, base};
+  const ShortMma<D> M(tmem, base);
   const int group = p.a.group, t1 = bwd_tokens1(group);
   auto wait = [&](uint32_t b, uint32_t par) -> bool {
     const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
     return __all_sync(0xffffffffu, r);
   };
-  ShortItem<D> at = {}, ahead = {};  // the item whose P^T comes next; the one whose S^T does
-  bool more = true;                  // `ahead` is one
+  ShortItem<D> at, ahead;  // the item whose P^T comes next; the one whose S^T does
+  int at_k = 0, ahead_k = 0;
+  bool more = true;        // `ahead` is one
+  uint32_t ahead_tile = 0, ahead_slot = 0;  // key and row tiles (of units begun) that `ahead` has come past
+  uint32_t st_free = 0, q_free = 0;         // stages and row tiles that are, or will be without this warp, handed back
   // `ahead` reads a segment without handing it back; `at` does that.
   auto enter_ahead = [&]() -> bool {
-    if (!wait(bar.seg_full(ahead.k % kBwdSegRing), (ahead.k / kBwdSegRing) & 1)) return false;
-    ahead.w = reinterpret_cast<const BwdSeg*>(gbase + C::OFF_SEG)[ahead.k % kBwdSegRing];
-    more = ahead.w.valid != 0;
-    if (more) ahead.enter(t1, group);
+    if (!wait(bar.seg_full(ahead_k % kBwdSegRing), (ahead_k / kBwdSegRing) & 1)) return false;
+    const BwdSeg& w = reinterpret_cast<const BwdSeg*>(gbase + C::OFF_SEG)[ahead_k % kBwdSegRing];
+    more = w.valid != 0;
+    if (more) ahead.enter(w, t1, group);
     return true;
   };
-  uint32_t issued = 0;      // items whose S^T and dP^T are on their way
-  uint32_t st_free = 0, q_free = 0;  // stages and row tiles handed back
-  uint32_t dqs = 0;                  // row tiles of dS^T multiplied
+  uint32_t issued = 0;  // items whose S^T and dP^T are on their way
   // S^T and dP^T of items up to `to`, as far as their K, V, Q and dO can be there: what they wait for must not wait for `at`.
   auto issue = [&](uint32_t to) -> bool {
-    while (more && issued <= to && ahead.tile < st_free + C::NST && ahead.slot() < q_free + C::SLOTS) {
-      const uint32_t slot = ahead.slot();
-      if (ahead.i == 0 && ahead.s == 0 && !wait(bar.st_full(ahead.tile % C::NST), (ahead.tile / C::NST) & 1)) return false;
-      if (ahead.j == 0 && ahead.s == 0 && !wait(bar.q_full(slot % C::SLOTS), (slot / C::SLOTS) & 1)) return false;
+    while (more && issued <= to && ahead_tile < st_free + C::NST && ahead_slot + ahead.tile() < q_free + C::SLOTS) {
+      uint32_t slot, par;
+      ahead.slot(slot, par);
+      if (ahead.m == 0 && !wait(bar.st_full(ahead.st.at), ahead.st.par)) return false;
+      if (ahead.j == 0 && ahead.sub() == 0 && !wait(bar.q_full(slot), par)) return false;
       tc_fence_after();
-      M.sdp(ahead.tile % C::NST, slot % C::SLOTS, ahead.s, issued & 1);
+      M.sdp(ahead.st.at, slot, ahead.sub(), issued & 1);
       mma_commit_elect(bar.s_full(issued & 1));
       ++issued;
-      if (!ahead.next(t1, group) && !enter_ahead()) return false;
+      const int tiles = (ahead.items + C::SUBS - 1) / C::SUBS;
+      if (ahead.last()) ++ahead_tile;
+      if (!ahead.next()) {
+        ahead_slot += tiles;
+        ++ahead_k;
+        if (!enter_ahead()) return false;
+      }
     }
     return true;
   };
+  uint32_t tiles = 0;  // key tiles whose dK and dV were begun
+  uint32_t dqs = 0;    // row tiles of dS^T multiplied here
   bool ok = enter_ahead();
   bool begun = false;  // `at` is within a segment
   for (uint32_t n = 0; ok; ++n) {
     if (!begun) {
-      if (!(ok = bwd_seg_read(at.w, at.k, gbase + C::OFF_SEG, bar, g)) || !at.w.valid) break;
-      at.enter(t1, group);
+      BwdSeg w;
+      if (!(ok = bwd_seg_read(w, at_k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
+      at.enter(w, t1, group);
       begun = true;
     }
-    if (!(ok = issue(n + 1))) break;
-    const uint32_t slot = at.slot() % C::SLOTS, st = at.tile % C::NST;
-    const int i = at.i, j = at.j, b = n & 1;
-    const bool last_s = at.s == at.ns - 1, last = last_s && i == at.nt - 1, first = i == 0 && at.s == 0;
+    if (issued < n + 2 && !(ok = issue(n + 1))) break;
+    uint32_t slot, par;
+    at.slot(slot, par);
+    const uint32_t b = n & 1;
     if (!(ok = wait(bar.p_ready(b), (n >> 1) & 1))) break;
-    if (first && at.tile > 0 && !(ok = wait(bar.kv_free(), (at.tile - 1) & 1))) break;
+    if (at.m == 0) {
+      if (tiles > 0 && !(ok = wait(bar.kv_free(), (tiles - 1) & 1))) break;
+      ++tiles;
+    }
     tc_fence_after();
-    M.dkv(slot, at.s, b, !first);
-    if (last) mma_commit_elect(bar.kv_done());
-    if (last_s && j == at.w.n - 1) {
+    M.dkv(slot, at.sub(), b, at.m > 0);
+    const bool end = at.last_sub() && at.j == at.n - 1;  // Q and dO of this row tile are used for the last time
+    if (at.last()) {
+      mma_commit_elect(bar.kv_done());
+      if (C::DQ_APART) ++st_free;  // (once the other warp has multiplied this row tile, and nothing here keeps it from that)
+    }
+    if (end) {
       mma_commit_elect(bar.q_empty(slot));
       ++q_free;
     }
     if (!(ok = issue(n + 2))) break;
-    if (last_s) {
-      if (j == 0 && i == 0 && at.k > 0) {
-        if (!(ok = wait(bar.dq_free(), (at.k - 1) & 1))) break;
+    if (!C::DQ_APART && at.last_sub()) {
+      if (at.j == 0 && at.tile() == 0 && at_k > 0) {
+        if (!(ok = wait(bar.dq_free(), (at_k - 1) & 1))) break;
         tc_fence_after();
       }
-      M.dq(st, i, j > 0);
+      M.dq(at.st.at, at.tile(), at.j > 0);
       mma_commit_elect(bar.ds_empty(dqs++));
-      if (last) {
-        mma_commit_elect(bar.st_empty(st));
+      if (at.last()) {
+        mma_commit_elect(bar.st_empty(at.st.at));
         ++st_free;
-        if (j == at.w.n - 1) mma_commit_elect(bar.dq_done());
+        if (end) mma_commit_elect(bar.dq_done());
       }
     }
-    begun = at.next(t1, group);
+    if (!(begun = at.next())) ++at_k;
   }
   // All issued MMAs must complete before TMEM is released.
   mma_commit_elect(bar.drain());
@@ -359,14 +429,60 @@ __device__ __forceinline__ void short_mma(const CrossBwdParams& p, const ShortBa
   __syncwarp();
 }
 
+// dQ, row tile by row tile.
+template <int D>
+__device__ __forceinline__ void short_mma_dq(const CrossBwdParams& p, const ShortBars<D>& bar, uint32_t base, uint8_t* gbase,
+                                             uint32_t tmem, const WaitGuard& g) {
+  using C = ShortCfg<D>;
+  const ShortMma<D> M(tmem, base);
+  const int group = p.a.group, t1 = bwd_tokens1(group);
+  auto wait = [&](uint32_t b, uint32_t par) -> bool {
+    const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
+    return __all_sync(0xffffffffu, r);
+  };
+  ShortItem<D> it;
+  int k = 0;
+  uint32_t n = 0, dqs = 0;
+  bool begun = false, ok = true;
+  while (ok) {
+    if (!begun) {
+      BwdSeg w;
+      if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
+      it.enter(w, t1, group);
+      begun = true;
+    }
+    if (it.last_sub()) {
+      // The row tile's last items are ready, one in each buffer (and so are those before them; none behind them is before this
+      // tile has been multiplied, so the phases are these).
+      if (it.sub() > 0 && !(ok = wait(bar.p_ready((n - 1) & 1), ((n - 1) >> 1) & 1))) break;
+      if (!(ok = wait(bar.p_ready(n & 1), (n >> 1) & 1))) break;
+      if (it.j == 0 && it.tile() == 0 && k > 0 && !(ok = wait(bar.dq_free(), (k - 1) & 1))) break;
+      tc_fence_after();
+      M.dq(it.st.at, it.tile(), it.j > 0);
+      mma_commit_elect(bar.ds_empty(dqs++));
+      if (it.last()) {
+        mma_commit_elect(bar.st_empty(it.st.at));
+        if (it.j == it.n - 1) mma_commit_elect(bar.dq_done());
+      }
+    }
+    ++n;
+    if (!(begun = it.next())) ++k;
+  }
+  // All issued MMAs must complete before TMEM is released.
+  mma_commit_elect(bar.drain_dq());
+  bwd_wait_drain(bar.drain_dq(), 0, g);
+  __syncwarp();
+}
+
 // ------------------------------------------------------------------ elementwise warpgroups
-// Warpgroup b takes every other item; thread = key.  What would meet a zero of P^T or dS^T in a product (Q and dO behind a tile's
-// last row, K behind the last key: anything, and 0 times NaN is NaN) is set to zero by the warpgroup of the first item that reads
+// Thread = key.  What would meet a zero of P^T or dS^T in a product (Q and dO behind a tile's
+// last row, K behind the last key: anything, and 0 times NaN is NaN) is set to zero in the first item that reads
 // it, behind that item's S^T and dP^T, whose rows and columns there are not looked at.
 template <int D>
 __device__ __forceinline__ void short_elementwise(const CrossBwdParams& p, const ShortBars<D>& bar, uint32_t base, uint8_t* gbase,
-                                                  uint32_t tmem, int b, int quarter, int lane, const WaitGuard& g) {
+                                                  uint32_t tmem, int wg, int quarter, int lane, const WaitGuard& g) {
   using C = ShortCfg<D>;
+  static_assert(C::EW_COLS == 32, "a thread's columns");
   constexpr int UNITS = D / 8;  // 16-byte units of a row
   const int r = quarter * 32 + lane;
   const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
@@ -377,82 +493,85 @@ __device__ __forceinline__ void short_elementwise(const CrossBwdParams& p, const
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) st_shared_v4(tile + u / (C::SWB / 16) * C::REGION + row * C::SWB + u % (C::SWB / 16) * 16, 0, 0, 0, 0);
   };
-  ShortItem<D> it = {};
+  ShortItem<D> it;
+  BwdSeg w;
+  int k = 0;
   bool begun = false, ok = true;
   for (uint32_t n = 0; ok; ++n) {
     if (!begun) {
-      if (!(ok = bwd_seg_read(it.w, it.k, gbase + C::OFF_SEG, bar, g)) || !it.w.valid) break;
-      it.enter(t1, group);
+      if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
+      it.enter(w, t1, group);
       begun = true;
     }
-    const uint32_t slot = it.slot() % C::SLOTS;
-    if ((n & 1) == static_cast<uint32_t>(b)) {
-      const int rows = short_rows(it.w.fix_n, it.i, t1, group) - it.s * C::QT;  // of this item's QT on
-      const int left = it.w.str_n - (it.w.s0 + it.j) * 128;
+    const uint32_t b = n & 1;
+    if (C::SPLIT || b == static_cast<uint32_t>(wg)) {
+      uint32_t slot, par;
+      it.slot(slot, par);
+      const int c0 = C::SPLIT ? wg * C::EW_COLS : 0;  // this warpgroup's first column of the item
+      const int rows = short_rows(w.fix_n, it.tile(), t1, group) - it.sub() * C::QT;  // of this item's QT on
+      const int left = w.str_n - (w.s0 + it.j) * 128;
       const bool key = r < left;  // this thread's key is one
       if (!(ok = warp_wait_bar(bar.s_full(b), (n >> 1) & 1, g, kStatusTimeoutSoftmax))) break;
       // (Complete, for the MMA warp has waited for it: this makes the vectors visible here.)
-      if (!(ok = warp_wait_bar(bar.q_full(slot), (it.slot() / C::SLOTS) & 1, g, kStatusTimeoutSoftmax))) break;
+      if (!(ok = warp_wait_bar(bar.q_full(slot), par, g, kStatusTimeoutSoftmax))) break;
       tc_fence_after();
-      if (it.j == 0 && rows < C::QT) {
-        const uint32_t tile = base + C::OFF_Q + slot * 2 * C::TILE;
-        for (int x = r; x < 2 * C::QT; x += 128) {
-          const int row = x % C::QT;
-          if (row >= rows) zero_row(tile + x / C::QT * C::TILE, it.s * C::QT + row);
-        }
-      }
-      if (it.i == 0 && it.s == 0 && !key) zero_row(base + C::OFF_ST + it.tile % C::NST * C::STAGE, r);
-      __syncwarp();
       const bool need_mask = left < 128 || rows < C::QT;
-      const float4* vl2 = reinterpret_cast<const float4*>(gbase + C::OFF_VEC + slot * C::VEC) + it.s * (C::QT / 4);
-      const float4* vd = vl2 + 32;
-#pragma unroll 1
-      for (int h = 0; h < C::QT / 32; ++h) {
-        uint32_t rs[32], rd[32];
-        tmem_ld32(tmem + lane_off + C::TM_S + b * C::QT + h * 32, rs);
-        tmem_ld32(tmem + lane_off + C::TM_DP + b * C::QT + h * 32, rd);
-        tmem_wait_ld(rs);
-        tmem_wait_ld(rd);
-        uint32_t pk[16], dk[16];
-#pragma unroll
-        for (int c4 = 0; c4 < 8; ++c4) {
-          const float4 a = vl2[h * 8 + c4], d4 = vd[h * 8 + c4];
-          const uint64_t nl[2] = {f2_pack(a.x, a.y), f2_pack(a.z, a.w)}, nd[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
-#pragma unroll
-          for (int e2 = 0; e2 < 2; ++e2) {
-            const int c = c4 * 4 + e2 * 2;
-            const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2x2, nl[e2]));
-            float p0 = ex2(x.x), p1 = ex2(x.y);
-            float2 ds = f2_unpack(
-                f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(rd[c]), __uint_as_float(rd[c + 1])), nd[e2])));
-            if (need_mask) {
-              if (!key || h * 32 + c >= rows) p0 = ds.x = 0.f;
-              if (!key || h * 32 + c + 1 >= rows) p1 = ds.y = 0.f;
-            }
-            pk[c4 * 2 + e2] = pack_bf16x2(p0, p1);
-            dk[c4 * 2 + e2] = pack_bf16x2(ds.x, ds.y);
+      if (need_mask) {
+        if (it.j == 0 && rows < C::QT) {  // SPLIT: warpgroup 0 Q, 1 dO
+          const uint32_t tile = base + C::OFF_Q + slot * 2 * C::TILE;
+          for (int x = C::SPLIT ? wg * C::QT + r : r; x < (C::SPLIT ? (wg + 1) : 2) * C::QT; x += 128) {
+            const int row = x % C::QT;
+            if (row >= rows) zero_row(tile + x / C::QT * C::TILE, it.sub() * C::QT + row);
           }
         }
-        // Chunk h's bf16 pairs land behind what has been read.
-        tmem_st16(tmem + lane_off + C::TM_S + b * C::QT + h * 16, pk);
-        tmem_st16(tmem + lane_off + C::TM_DP + b * C::QT + h * 16, dk);
-        // The row tile's dS^T before this one has been read.
-        if (h == 0 && dqs > 0 && !(ok = warp_wait_bar(bar.ds_empty(dqs - 1), ((dqs - 1) >> 1) & 1, g, kStatusTimeoutSoftmax))) break;
-        // dS^T into shared memory: key r's row of 64 rows of Q a region, 128-byte swizzled.
-        const int q0 = it.s * C::QT + h * 32;
-        const uint32_t row = base + C::OFF_DS + (q0 >> 6) * C::DS_REGION + r * 128;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          st_shared_v4(row + (((((q0 & 63) >> 3) + u) ^ (r & 7)) << 4), dk[4 * u], dk[4 * u + 1], dk[4 * u + 2], dk[4 * u + 3]);
+        if (it.m == 0 && !key && (!C::SPLIT || wg == 0)) zero_row(base + C::OFF_ST + it.st.at * C::STAGE, r);
+        __syncwarp();
       }
-      if (!ok) break;
+      const float4* vl2 = reinterpret_cast<const float4*>(gbase + C::OFF_VEC + slot * C::VEC) + (it.sub() * C::QT + c0) / 4;
+      const float4* vd = vl2 + 32;
+      uint32_t rs[32], rd[32];
+      tmem_ld32(tmem + lane_off + C::TM_S + b * C::QT + c0, rs);
+      tmem_ld32(tmem + lane_off + C::TM_DP + b * C::QT + c0, rd);
+      tmem_wait_ld(rs);
+      tmem_wait_ld(rd);
+      uint32_t pk[16], dk[16];
+#pragma unroll
+      for (int c4 = 0; c4 < 8; ++c4) {
+        const float4 a = vl2[c4], d4 = vd[c4];
+        const uint64_t nl[2] = {f2_pack(a.x, a.y), f2_pack(a.z, a.w)}, nd[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const int c = c4 * 4 + e2 * 2;
+          const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2x2, nl[e2]));
+          float p0 = ex2(x.x), p1 = ex2(x.y);
+          float2 ds = f2_unpack(
+              f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(rd[c]), __uint_as_float(rd[c + 1])), nd[e2])));
+          if (need_mask) {
+            if (!key || c0 + c >= rows) p0 = ds.x = 0.f;
+            if (!key || c0 + c + 1 >= rows) p1 = ds.y = 0.f;
+          }
+          pk[c4 * 2 + e2] = pack_bf16x2(p0, p1);
+          dk[c4 * 2 + e2] = pack_bf16x2(ds.x, ds.y);
+        }
+      }
+      // The bf16 pairs land over what this warpgroup has read.
+      tmem_st16(tmem + lane_off + C::TM_S + b * C::QT + c0, pk);
+      tmem_st16(tmem + lane_off + C::TM_DP + b * C::QT + c0, dk);
+      // The row tile's dS^T before this one has been read.
+      if (dqs > 0 && !(ok = warp_wait_bar(bar.ds_empty(dqs - 1), ((dqs - 1) >> 1) & 1, g, kStatusTimeoutSoftmax))) break;
+      // dS^T into shared memory: key r's row of 64 rows of Q a region, 128-byte swizzled.
+      const int q0 = it.sub() * C::QT + c0;
+      const uint32_t row = base + C::OFF_DS + (q0 >> 6) * C::DS_REGION + r * 128;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        st_shared_v4(row + (((((q0 & 63) >> 3) + u) ^ (r & 7)) << 4), dk[4 * u], dk[4 * u + 1], dk[4 * u + 2], dk[4 * u + 3]);
       tmem_wait_st();
       tc_fence_before();
       fence_proxy_async_smem();
       warp_arrive(bar.p_ready(b));
     }
-    if (it.s == it.ns - 1) ++dqs;
-    begun = it.next(t1, group);
+    if (it.last_sub()) ++dqs;
+    if (!(begun = it.next())) ++k;
   }
 }
 
@@ -557,7 +676,7 @@ __global__ void __launch_bounds__(ShortCfg<D>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar.s_full(i), 1);
-      mbar_init(bar.p_ready(i), 4);
+      mbar_init(bar.p_ready(i), C::EW_WARPS);
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(bar.q_full(i), 2);
@@ -570,6 +689,7 @@ __global__ void __launch_bounds__(ShortCfg<D>::THREADS, 1)
     mbar_init(bar.dq_done(), 1);
     mbar_init(bar.dq_free(), 4);
     mbar_init(bar.drain(), 1);
+    mbar_init(bar.drain_dq(), 1);
     for (int i = 0; i < kBwdSegRing; ++i) {
       mbar_init(bar.seg_full(i), 1);
       mbar_init(bar.seg_empty(i), C::READERS);
@@ -596,7 +716,7 @@ __global__ void __launch_bounds__(ShortCfg<D>::THREADS, 1)
       [&](int b) -> long long {
         bool bad;
         const BwdUnits u = bwd_units<D, 2>(p.a, cross_seq(p.a.cb, b, bad));
-        return static_cast<long long>(u.units) * (u.str + BwdWork<D, 2>::UNIT_COST);
+        return u.units == 0 ? 0ll : static_cast<long long>(u.units) * u.template length<BwdWork<D, 2>::UNIT_COST>();
       },
       1 + BwdWork<D, 2>::UNIT_COST, *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
   pdl_wait();  // for the preparing kernel; and so have all CTAs when the next kernel's begin
@@ -613,6 +733,8 @@ __global__ void __launch_bounds__(ShortCfg<D>::THREADS, 1)
     short_output<D>(p, bar, gbase, tmem, warp & 3, lane, g);
   } else if (warp == C::MMA_WARP) {
     short_mma<D>(p, bar, base, gbase, tmem, g);
+  } else if (warp == C::DQ_WARP) {
+    if constexpr (C::DQ_APART) short_mma_dq<D>(p, bar, base, gbase, tmem, g);
   } else {
     short_load<D>(&tm_q, &tm_do, &tm_k, &tm_v, p, bar, base, gbase, share, g);
   }
