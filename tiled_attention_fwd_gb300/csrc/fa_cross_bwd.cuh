@@ -67,8 +67,9 @@ struct BwdWork<D, 2> {
   static constexpr int HALVES = 1;
   static constexpr int STR = 128;
   static constexpr size_t PART = static_cast<size_t>(128) * bwd_short_tiles(D) * D;
-  static constexpr int QT = D <= 64 ? 64 : 32;  // rows of an item (fa_cross_bwd_short.cuh); a streamed tile has as many places as items
-  static constexpr int UNIT_COST = 2;
+  static constexpr int QT = D <= 64 ? 64 : 32;  // rows of an item (fa_cross_bwd_short.cuh), which is a place on the line
+  static constexpr int TILE_COST = 2;  // items that a streamed tile costs besides its own (its loads, its dK and dV)
+  static constexpr int UNIT_COST = 3;
 };
 
 // Workspace of fa_cross_bwd.
@@ -163,7 +164,7 @@ __host__ __device__ __forceinline__ BwdUnits bwd_units(const CrossArgs& a, const
     u.str = (s.len + C::STR - 1) / C::STR;
     if constexpr (MODE == 2) {
       const int t = bwd_tokens1(a.group), full = s.n / t, rest = s.n % t;  // whole row tiles, and tokens of the last one
-      u.w = full * ((t * a.group + C::QT - 1) / C::QT) + (rest * a.group + C::QT - 1) / C::QT;
+      u.w = full * ((t * a.group + C::QT - 1) / C::QT) + (rest * a.group + C::QT - 1) / C::QT + C::TILE_COST;
     }
   } else if (MODE == 0) {
     const int t = bwd_tokens0<D>(a.group);

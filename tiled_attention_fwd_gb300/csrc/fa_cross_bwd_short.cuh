@@ -24,12 +24,12 @@ template <int D>
 struct ShortCfg {
   static constexpr int QT = BwdWork<D, 2>::QT;          // rows of an item
   // Both warpgroups take part in every item, half its columns each (QT = 64), or they take turns (QT = 32).
-  static constexpr bool SPLIT = QT == 64;
+  static constexpr bool SPLIT = false;
   static constexpr int EW_WARPS = SPLIT ? 8 : 4;        // of an item
   static constexpr int EW_COLS = SPLIT ? QT / 2 : QT;   // columns of a thread
   static constexpr int SUBS = 128 / QT;                 // items of a full row tile
   static constexpr int TILES = bwd_short_tiles(D);      // 128-row tiles of a unit at most
-  static constexpr int SLOTS = D == 32 ? 6 : D == 64 ? 3 : 1;  // of the ring of Q and dO tiles
+  static constexpr int SLOTS = D == 32 ? 6 : D == 64 ? 2 : 1;  // of the ring of Q and dO tiles
   static constexpr int SWB = (D * 2 >= 128) ? 128 : D * 2;  // swizzle span in bytes
   static constexpr uint32_t SWZ = (SWB == 128) ? 2u : 4u;   // descriptor swizzle code
   static constexpr int RC = SWB / 2;                    // bf16 columns per swizzle region
@@ -43,12 +43,18 @@ struct ShortCfg {
   static constexpr int DS_REGION = 128 * 128;
   static constexpr int DS = 2 * DS_REGION;
   static constexpr int VEC = 2 * 128 * 4;               // bytes of -L log2e and -D of a tile's rows
+  // Output goes through shared memory, 32 rows of up to 64 columns a warp, so that a store is of whole rows (direct stores of a
+  // thread's own row touch 32 lines each: 3700 cycles a key tile at d = 64); d = 128 has no room left.
+  static constexpr bool STAGED = D <= 64;
+  static constexpr int OUT_BUF = 32 * D * 2;
+  static constexpr int OUT = STAGED ? 4 * OUT_BUF : 0;
   static constexpr int MISC = 1024 + SLOTS * VEC;
   static constexpr int SMEM_LIMIT = 227 * 1024;
-  static constexpr int NST_FIT = (SMEM_LIMIT - 1024 - MISC - DS - OFF_ST) / STAGE;
+  static constexpr int NST_FIT = (SMEM_LIMIT - 1024 - MISC - DS - OUT - OFF_ST) / STAGE;
   static constexpr int NST = NST_FIT > 4 ? 4 : NST_FIT;
   static constexpr int OFF_DS = OFF_ST + NST * STAGE;
-  static constexpr int OFF_MISC = OFF_DS + DS;
+  static constexpr int OFF_OUT = OFF_DS + DS;
+  static constexpr int OFF_MISC = OFF_OUT + OUT;
   static constexpr int OFF_TMEM_SLOT = OFF_MISC + 384;
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
   static constexpr int OFF_SEG = OFF_MISC + 400;
@@ -63,15 +69,16 @@ struct ShortCfg {
   static constexpr int TM_DV = 4 * QT + D;
   static constexpr int TM_DQ = 4 * QT + 2 * D;
   static constexpr int TM_COLS = 512;
-  // Warps: 0-7 elementwise, 8-11 output, 12 MMA, 13 load, 14 MMA of dQ.
+  // Warps: 0-7 elementwise, 8-11 output, 12 MMA of S and dP, 13 load, 14 MMA of dK and dV, 15 MMA of dQ.
   static constexpr int OUT_WARP0 = 8;
-  static constexpr int MMA_WARP = 12;
+  static constexpr int S_WARP = 12;
   static constexpr int LOAD_WARP = 13;
+  static constexpr int KV_WARP = 14;
   // (Only where a row tile has two items: the warp waits for each buffer once a row tile, and with four it could miss a phase.)
   static constexpr bool DQ_APART = SUBS == 2;
-  static constexpr int DQ_WARP = 14;
-  static constexpr int THREADS = DQ_APART ? 480 : 448;
-  static constexpr int READERS = DQ_APART ? 14 : 13;
+  static constexpr int DQ_WARP = 15;
+  static constexpr int THREADS = DQ_APART ? 512 : 480;
+  static constexpr int READERS = DQ_APART ? 15 : 14;
   static_assert(TM_DQ + TILES * D <= TM_COLS, "TMEM budget");
   static_assert(SLOTS >= TILES && NST >= 2 && SMEM_USED <= SMEM_LIMIT, "shared memory budget");
   static_assert(OFF_PLAN % 8 == 0 && OFF_PLAN + sizeof(PlanScratch) <= OFF_VEC, "misc area");
@@ -83,23 +90,23 @@ struct ShortBars {
   uint32_t b0;
   __device__ __forceinline__ uint32_t s_full(int b) const { return b0 + 8u * b; }         // S^T and dP^T of buffer b
   __device__ __forceinline__ uint32_t p_ready(int b) const { return b0 + 16 + 8u * b; }   // P^T and dS^T (EW_WARPS)
+  __device__ __forceinline__ uint32_t buf_free(int b) const { return b0 + 32 + 8u * b; }  // multiplied into dV and dK
   // dS^T in shared memory (its m-th row tile) has been read.  Two barriers take turns: where a row tile is one item, a warpgroup
   // may come to tile m + 2 before tile m has been read, and a barrier two phases behind looks as if it had.
-  __device__ __forceinline__ uint32_t ds_empty(uint32_t m) const { return b0 + 32 + 8u * (m & 1); }
-  __device__ __forceinline__ uint32_t kv_done() const { return b0 + 48; }   // dK and dV of a key tile
-  __device__ __forceinline__ uint32_t kv_free() const { return b0 + 56; }   // read out (4 warps)
-  __device__ __forceinline__ uint32_t dq_done() const { return b0 + 64; }
-  __device__ __forceinline__ uint32_t dq_free() const { return b0 + 72; }
-  __device__ __forceinline__ uint32_t drain() const { return b0 + 80; }
-  __device__ __forceinline__ uint32_t drain_dq() const { return b0 + 376; }
-  __device__ __forceinline__ uint32_t seg_full(int i) const { return b0 + 88 + 8u * i; }
-  __device__ __forceinline__ uint32_t seg_empty(int i) const { return b0 + 120 + 8u * i; }
-  __device__ __forceinline__ uint32_t st_full(int i) const { return b0 + 152 + 8u * i; }
-  __device__ __forceinline__ uint32_t st_empty(int i) const { return b0 + 152 + 8u * (C::NST + i); }
+  __device__ __forceinline__ uint32_t ds_empty(uint32_t m) const { return b0 + 48 + 8u * (m & 1); }
+  __device__ __forceinline__ uint32_t kv_done() const { return b0 + 64; }   // dK and dV of a key tile
+  __device__ __forceinline__ uint32_t kv_free() const { return b0 + 72; }   // read out (4 warps)
+  __device__ __forceinline__ uint32_t dq_done() const { return b0 + 80; }
+  __device__ __forceinline__ uint32_t dq_free() const { return b0 + 88; }
+  __device__ __forceinline__ uint32_t drain(int i) const { return b0 + 96 + 8u * i; }  // of the issuing warps
+  __device__ __forceinline__ uint32_t seg_full(int i) const { return b0 + 120 + 8u * i; }
+  __device__ __forceinline__ uint32_t seg_empty(int i) const { return b0 + 152 + 8u * i; }
+  __device__ __forceinline__ uint32_t st_full(int i) const { return b0 + 184 + 8u * i; }
+  __device__ __forceinline__ uint32_t st_empty(int i) const { return b0 + 184 + 8u * (C::NST + i); }
   // A tile of Q and dO and its vectors (the copies, and the load warp's own stores) / used for the last time.
-  __device__ __forceinline__ uint32_t q_full(int i) const { return b0 + 152 + 16u * C::NST + 8u * i; }
-  __device__ __forceinline__ uint32_t q_empty(int i) const { return b0 + 152 + 16u * C::NST + 8u * (C::SLOTS + i); }
-  static_assert(152 + 16 * (C::NST + C::SLOTS) <= 376 && kBwdSegRing == 4, "barrier area");
+  __device__ __forceinline__ uint32_t q_full(int i) const { return b0 + 184 + 16u * C::NST + 8u * i; }
+  __device__ __forceinline__ uint32_t q_empty(int i) const { return b0 + 184 + 16u * C::NST + 8u * (C::SLOTS + i); }
+  static_assert(184 + 16 * (C::NST + C::SLOTS) <= 384 && kBwdSegRing == 4, "barrier area");
 };
 
 // Rows of tile i of a unit of n tokens.
@@ -329,104 +336,99 @@ struct ShortMma {
   }
 };
 
-// Per item: dV, dK; S^T and dP^T of the item after the next into the buffer that they leave; dQ where a row tile is complete.  (DQ_APART:
-// dQ is a warp's of its own: what bounds a tile here is how fast its 40 small products are issued.)
-template <int D>
-__device__ __forceinline__ void short_mma(const CrossBwdParams& p, const ShortBars<D>& bar, uint32_t base, uint8_t* gbase,
-                                          uint32_t tmem, const WaitGuard& g) {
-  using C = ShortCfg<D>;
-  const ShortMma<D> M(tmem, base);
-  const int group = p.a.group, t1 = bwd_tokens1(group);
-  auto wait = [&](uint32_t b, uint32_t par) -> bool {
+// Three warps issue the products (their instructions, about 10 for each small product, bound a single one: 32 sequences of 17 to 200 rows
+// 138 us with one, 116 with dQ apart): S^T and dP^T; dV and dK (DQ_APART false: and dQ); dQ.  What one warp's products read and
+// another's overwrite is handed over by a barrier (buf_free), for only those of one warp complete in order.
+struct ShortIssuer {
+  const WaitGuard& g;
+  __device__ __forceinline__ bool wait(uint32_t b, uint32_t par) const {
     const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
     return __all_sync(0xffffffffu, r);
-  };
-  ShortItem<D> at, ahead;  // the item whose P^T comes next; the one whose S^T does
-  int at_k = 0, ahead_k = 0;
-  bool more = true;        // `ahead` is one
-  uint32_t ahead_tile = 0, ahead_slot = 0;  // key and row tiles (of units begun) that `ahead` has come past
-  uint32_t st_free = 0, q_free = 0;         // stages and row tiles that are, or will be without this warp, handed back
-  // `ahead` reads a segment without handing it back; `at` does that.
-  auto enter_ahead = [&]() -> bool {
-    if (!wait(bar.seg_full(ahead_k % kBwdSegRing), (ahead_k / kBwdSegRing) & 1)) return false;
-    const BwdSeg& w = reinterpret_cast<const BwdSeg*>(gbase + C::OFF_SEG)[ahead_k % kBwdSegRing];
-    more = w.valid != 0;
-    if (more) ahead.enter(w, t1, group);
-    return true;
-  };
-  uint32_t issued = 0;  // items whose S^T and dP^T are on their way
-  // S^T and dP^T of items up to `to`, as far as their K, V, Q and dO can be there: what they wait for must not wait for `at`.
-  auto issue = [&](uint32_t to) -> bool {
-    while (more && issued <= to && ahead_tile < st_free + C::NST && ahead_slot + ahead.tile() < q_free + C::SLOTS) {
-      uint32_t slot, par;
-      ahead.slot(slot, par);
-      if (ahead.m == 0 && !wait(bar.st_full(ahead.st.at), ahead.st.par)) return false;
-      if (ahead.j == 0 && ahead.sub() == 0 && !wait(bar.q_full(slot), par)) return false;
-      tc_fence_after();
-      M.sdp(ahead.st.at, slot, ahead.sub(), issued & 1);
-      mma_commit_elect(bar.s_full(issued & 1));
-      ++issued;
-      const int tiles = (ahead.items + C::SUBS - 1) / C::SUBS;
-      if (ahead.last()) ++ahead_tile;
-      if (!ahead.next()) {
-        ahead_slot += tiles;
-        ++ahead_k;
-        if (!enter_ahead()) return false;
-      }
-    }
-    return true;
-  };
-  uint32_t tiles = 0;  // key tiles whose dK and dV were begun
-  uint32_t dqs = 0;    // row tiles of dS^T multiplied here
-  bool ok = enter_ahead();
-  bool begun = false;  // `at` is within a segment
+  }
+  // All products issued must complete before TMEM is released.
+  __device__ __forceinline__ void finish(uint32_t drain) const {
+    mma_commit_elect(drain);
+    bwd_wait_drain(drain, 0, g);
+    __syncwarp();
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void short_mma_s(const CrossBwdParams& p, const ShortBars<D>& bar, uint32_t base, uint8_t* gbase,
+                                            uint32_t tmem, const WaitGuard& g) {
+  using C = ShortCfg<D>;
+  const ShortMma<D> M(tmem, base);
+  const ShortIssuer is{g};
+  const int group = p.a.group, t1 = bwd_tokens1(group);
+  ShortItem<D> it;
+  int k = 0;
+  bool begun = false, ok = true;
   for (uint32_t n = 0; ok; ++n) {
     if (!begun) {
       BwdSeg w;
-      if (!(ok = bwd_seg_read(w, at_k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
-      at.enter(w, t1, group);
-      begun = true;
+      if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
+      it.enter(w, t1, group);
     }
-    if (issued < n + 2 && !(ok = issue(n + 1))) break;
     uint32_t slot, par;
-    at.slot(slot, par);
+    it.slot(slot, par);
+    if (it.m == 0 && !(ok = is.wait(bar.st_full(it.st.at), it.st.par))) break;
+    if (it.j == 0 && it.sub() == 0 && !(ok = is.wait(bar.q_full(slot), par))) break;
+    if (n >= 2 && !(ok = is.wait(bar.buf_free(n & 1), ((n >> 1) - 1) & 1))) break;
+    tc_fence_after();
+    M.sdp(it.st.at, slot, it.sub(), n & 1);
+    mma_commit_elect(bar.s_full(n & 1));
+    if (!(begun = it.next())) ++k;
+  }
+  is.finish(bar.drain(0));
+}
+
+template <int D>
+__device__ __forceinline__ void short_mma_kv(const CrossBwdParams& p, const ShortBars<D>& bar, uint32_t base, uint8_t* gbase,
+                                             uint32_t tmem, const WaitGuard& g) {
+  using C = ShortCfg<D>;
+  const ShortMma<D> M(tmem, base);
+  const ShortIssuer is{g};
+  const int group = p.a.group, t1 = bwd_tokens1(group);
+  ShortItem<D> it;
+  int k = 0;
+  uint32_t tiles = 0;  // key tiles whose dK and dV were begun
+  uint32_t dqs = 0;    // row tiles of dS^T multiplied here
+  bool begun = false, ok = true;
+  for (uint32_t n = 0; ok; ++n) {
+    if (!begun) {
+      BwdSeg w;
+      if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
+      it.enter(w, t1, group);
+    }
+    uint32_t slot, par;
+    it.slot(slot, par);
     const uint32_t b = n & 1;
-    if (!(ok = wait(bar.p_ready(b), (n >> 1) & 1))) break;
-    if (at.m == 0) {
-      if (tiles > 0 && !(ok = wait(bar.kv_free(), (tiles - 1) & 1))) break;
+    if (!(ok = is.wait(bar.p_ready(b), (n >> 1) & 1))) break;
+    if (it.m == 0) {
+      if (tiles > 0 && !(ok = is.wait(bar.kv_free(), (tiles - 1) & 1))) break;
       ++tiles;
     }
     tc_fence_after();
-    M.dkv(slot, at.sub(), b, at.m > 0);
-    const bool end = at.last_sub() && at.j == at.n - 1;  // Q and dO of this row tile are used for the last time
-    if (at.last()) {
-      mma_commit_elect(bar.kv_done());
-      if (C::DQ_APART) ++st_free;  // (once the other warp has multiplied this row tile, and nothing here keeps it from that)
-    }
-    if (end) {
-      mma_commit_elect(bar.q_empty(slot));
-      ++q_free;
-    }
-    if (!(ok = issue(n + 2))) break;
-    if (!C::DQ_APART && at.last_sub()) {
-      if (at.j == 0 && at.tile() == 0 && at_k > 0) {
-        if (!(ok = wait(bar.dq_free(), (at_k - 1) & 1))) break;
+    M.dkv(slot, it.sub(), b, it.m > 0);
+    mma_commit_elect(bar.buf_free(b));
+    if (it.last()) mma_commit_elect(bar.kv_done());
+    const bool end = it.last_sub() && it.j == it.n - 1;
+    if (end) mma_commit_elect(bar.q_empty(slot));  // Q and dO of this row tile have been used for the last time
+    if (!C::DQ_APART && it.last_sub()) {
+      if (it.j == 0 && it.tile() == 0 && k > 0) {
+        if (!(ok = is.wait(bar.dq_free(), (k - 1) & 1))) break;
         tc_fence_after();
       }
-      M.dq(at.st.at, at.tile(), at.j > 0);
+      M.dq(it.st.at, it.tile(), it.j > 0);
       mma_commit_elect(bar.ds_empty(dqs++));
-      if (at.last()) {
-        mma_commit_elect(bar.st_empty(at.st.at));
-        ++st_free;
+      if (it.last()) {
+        mma_commit_elect(bar.st_empty(it.st.at));
         if (end) mma_commit_elect(bar.dq_done());
       }
     }
-    if (!(begun = at.next())) ++at_k;
+    if (!(begun = it.next())) ++k;
   }
-  // All issued MMAs must complete before TMEM is released.
-  mma_commit_elect(bar.drain());
-  bwd_wait_drain(bar.drain(), 0, g);
-  __syncwarp();
+  is.finish(bar.drain(1));
 }
 
 // dQ, row tile by row tile.
@@ -435,11 +437,8 @@ __device__ __forceinline__ void short_mma_dq(const CrossBwdParams& p, const Shor
                                              uint32_t tmem, const WaitGuard& g) {
   using C = ShortCfg<D>;
   const ShortMma<D> M(tmem, base);
+  const ShortIssuer is{g};
   const int group = p.a.group, t1 = bwd_tokens1(group);
-  auto wait = [&](uint32_t b, uint32_t par) -> bool {
-    const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
-    return __all_sync(0xffffffffu, r);
-  };
   ShortItem<D> it;
   int k = 0;
   uint32_t n = 0, dqs = 0;
@@ -449,14 +448,13 @@ __device__ __forceinline__ void short_mma_dq(const CrossBwdParams& p, const Shor
       BwdSeg w;
       if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
       it.enter(w, t1, group);
-      begun = true;
     }
     if (it.last_sub()) {
       // The row tile's last items are ready, one in each buffer (and so are those before them; none behind them is before this
       // tile has been multiplied, so the phases are these).
-      if (it.sub() > 0 && !(ok = wait(bar.p_ready((n - 1) & 1), ((n - 1) >> 1) & 1))) break;
-      if (!(ok = wait(bar.p_ready(n & 1), (n >> 1) & 1))) break;
-      if (it.j == 0 && it.tile() == 0 && k > 0 && !(ok = wait(bar.dq_free(), (k - 1) & 1))) break;
+      if (it.sub() > 0 && !(ok = is.wait(bar.p_ready((n - 1) & 1), ((n - 1) >> 1) & 1))) break;
+      if (!(ok = is.wait(bar.p_ready(n & 1), (n >> 1) & 1))) break;
+      if (it.j == 0 && it.tile() == 0 && k > 0 && !(ok = is.wait(bar.dq_free(), (k - 1) & 1))) break;
       tc_fence_after();
       M.dq(it.st.at, it.tile(), it.j > 0);
       mma_commit_elect(bar.ds_empty(dqs++));
@@ -468,10 +466,7 @@ __device__ __forceinline__ void short_mma_dq(const CrossBwdParams& p, const Shor
     ++n;
     if (!(begun = it.next())) ++k;
   }
-  // All issued MMAs must complete before TMEM is released.
-  mma_commit_elect(bar.drain_dq());
-  bwd_wait_drain(bar.drain_dq(), 0, g);
-  __syncwarp();
+  is.finish(bar.drain(2));
 }
 
 // ------------------------------------------------------------------ elementwise warpgroups
@@ -482,7 +477,6 @@ template <int D>
 __device__ __forceinline__ void short_elementwise(const CrossBwdParams& p, const ShortBars<D>& bar, uint32_t base, uint8_t* gbase,
                                                   uint32_t tmem, int wg, int quarter, int lane, const WaitGuard& g) {
   using C = ShortCfg<D>;
-  static_assert(C::EW_COLS == 32, "a thread's columns");
   constexpr int UNITS = D / 8;  // 16-byte units of a row
   const int r = quarter * 32 + lane;
   const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
@@ -501,7 +495,6 @@ __device__ __forceinline__ void short_elementwise(const CrossBwdParams& p, const
     if (!begun) {
       if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
       it.enter(w, t1, group);
-      begun = true;
     }
     const uint32_t b = n & 1;
     if (C::SPLIT || b == static_cast<uint32_t>(wg)) {
@@ -529,42 +522,53 @@ __device__ __forceinline__ void short_elementwise(const CrossBwdParams& p, const
       }
       const float4* vl2 = reinterpret_cast<const float4*>(gbase + C::OFF_VEC + slot * C::VEC) + (it.sub() * C::QT + c0) / 4;
       const float4* vd = vl2 + 32;
-      uint32_t rs[32], rd[32];
-      tmem_ld32(tmem + lane_off + C::TM_S + b * C::QT + c0, rs);
-      tmem_ld32(tmem + lane_off + C::TM_DP + b * C::QT + c0, rd);
-      tmem_wait_ld(rs);
-      tmem_wait_ld(rd);
-      uint32_t pk[16], dk[16];
+#pragma unroll 1
+      for (int h = 0; h < C::EW_COLS / 32; ++h) {
+        uint32_t rs[32], rd[32];
+        tmem_ld32(tmem + lane_off + C::TM_S + b * C::QT + c0 + 32 * h, rs);
+        tmem_ld32(tmem + lane_off + C::TM_DP + b * C::QT + c0 + 32 * h, rd);
+        tmem_wait_ld(rs);
+        tmem_wait_ld(rd);
+        uint32_t pk[16], dk[16];
 #pragma unroll
-      for (int c4 = 0; c4 < 8; ++c4) {
-        const float4 a = vl2[c4], d4 = vd[c4];
-        const uint64_t nl[2] = {f2_pack(a.x, a.y), f2_pack(a.z, a.w)}, nd[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
+        for (int c4 = 0; c4 < 8; ++c4) {
+          const float4 a = vl2[h * 8 + c4], d4 = vd[h * 8 + c4];
+          const uint64_t nl[2] = {f2_pack(a.x, a.y), f2_pack(a.z, a.w)}, nd[2] = {f2_pack(d4.x, d4.y), f2_pack(d4.z, d4.w)};
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) {
-          const int c = c4 * 4 + e2 * 2;
-          const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2x2, nl[e2]));
-          float p0 = ex2(x.x), p1 = ex2(x.y);
-          float2 ds = f2_unpack(
-              f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(rd[c]), __uint_as_float(rd[c + 1])), nd[e2])));
-          if (need_mask) {
-            if (!key || c0 + c >= rows) p0 = ds.x = 0.f;
-            if (!key || c0 + c + 1 >= rows) p1 = ds.y = 0.f;
+          for (int e2 = 0; e2 < 2; ++e2) {
+            const int c = c4 * 4 + e2 * 2;
+            const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2x2, nl[e2]));
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            const float2 ds = f2_unpack(
+                f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(rd[c]), __uint_as_float(rd[c + 1])), nd[e2])));
+            pk[c4 * 2 + e2] = pack_bf16x2(p0, p1);
+            dk[c4 * 2 + e2] = pack_bf16x2(ds.x, ds.y);
           }
-          pk[c4 * 2 + e2] = pack_bf16x2(p0, p1);
-          dk[c4 * 2 + e2] = pack_bf16x2(ds.x, ds.y);
         }
-      }
-      // The bf16 pairs land over what this warpgroup has read.
-      tmem_st16(tmem + lane_off + C::TM_S + b * C::QT + c0, pk);
-      tmem_st16(tmem + lane_off + C::TM_DP + b * C::QT + c0, dk);
-      // The row tile's dS^T before this one has been read.
-      if (dqs > 0 && !(ok = warp_wait_bar(bar.ds_empty(dqs - 1), ((dqs - 1) >> 1) & 1, g, kStatusTimeoutSoftmax))) break;
-      // dS^T into shared memory: key r's row of 64 rows of Q a region, 128-byte swizzled.
-      const int q0 = it.sub() * C::QT + c0;
-      const uint32_t row = base + C::OFF_DS + (q0 >> 6) * C::DS_REGION + r * 128;
+        if (need_mask) {
+          // (Bits, so that a NaN goes, too; outside the loop above, whose instructions are what an item costs.)
+          const int v = rows - c0 - 32 * h;  // columns of this thread's that are rows
+          const uint32_t keep = key ? 0xffffffffu : 0u;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        st_shared_v4(row + (((((q0 & 63) >> 3) + u) ^ (r & 7)) << 4), dk[4 * u], dk[4 * u + 1], dk[4 * u + 2], dk[4 * u + 3]);
+          for (int c = 0; c < 16; ++c) {
+            const uint32_t m = v >= 2 * c + 2 ? keep : v == 2 * c + 1 ? keep & 0xffffu : 0u;
+            pk[c] &= m;
+            dk[c] &= m;
+          }
+        }
+        // The bf16 pairs land over what this warpgroup has read.
+        tmem_st16(tmem + lane_off + C::TM_S + b * C::QT + c0 + 16 * h, pk);
+        tmem_st16(tmem + lane_off + C::TM_DP + b * C::QT + c0 + 16 * h, dk);
+        // The row tile's dS^T before this one has been read.
+        if (h == 0 && dqs > 0 && !(ok = warp_wait_bar(bar.ds_empty(dqs - 1), ((dqs - 1) >> 1) & 1, g, kStatusTimeoutSoftmax))) break;
+        // dS^T into shared memory: key r's row of 64 rows of Q a region, 128-byte swizzled.
+        const int q0 = it.sub() * C::QT + c0 + 32 * h;
+        const uint32_t row = base + C::OFF_DS + (q0 >> 6) * C::DS_REGION + r * 128;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          st_shared_v4(row + (((((q0 & 63) >> 3) + u) ^ (r & 7)) << 4), dk[4 * u], dk[4 * u + 1], dk[4 * u + 2], dk[4 * u + 3]);
+      }
+      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       fence_proxy_async_smem();
@@ -586,23 +590,52 @@ __device__ __forceinline__ void short_output(const CrossBwdParams& p, const Shor
   const int tok_r = r / group, head_r = r - tok_r * group;
   uint32_t tiles = 0;  // key tiles read out
   bool ok = true;
-  // 32 columns of TMEM times f, as bf16.
+  // 32 columns of TMEM.
   auto chunk = [&](uint32_t at, uint32_t (&v)[32]) {
     tmem_ld32(tmem + lane_off + at, v);
     tmem_wait_ld(v);
   };
-  auto store = [&](const uint32_t (&v)[32], float f, __nv_bfloat16* to) {
+  // D columns of TMEM from `at` on, times f, as bf16.
+  auto take = [&](uint32_t at, float f, uint32_t (&y)[D / 2]) {
     const uint64_t f2 = f2_pack(f, f);
-    uint4* dst = reinterpret_cast<uint4*>(to);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      uint32_t y[4];
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t v[32];
+      chunk(at + c * 32, v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 x = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[8 * u + 2 * e]), __uint_as_float(v[8 * u + 2 * e + 1])), f2));
-        y[e] = pack_bf16x2(x.x, x.y);
+      for (int i = 0; i < 16; ++i) {
+        const float2 x = f2_unpack(f2_mul(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2));
+        y[c * 16 + i] = pack_bf16x2(x.x, x.y);
       }
-      dst[u] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  };
+  // The warp's 32 rows of D columns to where `to` says (each thread's own row's place; null: nowhere).
+  const uint32_t buf = smem_u32(gbase + C::OFF_OUT) + static_cast<uint32_t>(quarter) * C::OUT_BUF;
+  constexpr int UR = D / 8;                   // 16-byte units of a row
+  constexpr int RPL = UR < 8 ? 8 / UR : 1;    // rows of a 128-byte line
+  auto place = [&](int row, int u) -> uint32_t { return buf + row * (D * 2) + ((u ^ ((row / RPL) & (UR - 1))) << 4); };
+  auto put = [&](const uint32_t (&y)[D / 2], __nv_bfloat16* to) {
+    if constexpr (C::STAGED) {
+      __syncwarp();  // the rows before these have been read
+#pragma unroll
+      for (int u = 0; u < UR; ++u) st_shared_v4(place(lane, u), y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+      __syncwarp();
+      const unsigned long long mine = reinterpret_cast<unsigned long long>(to);
+#pragma unroll 2
+      for (int i = 0; i < UR; ++i) {  // 32 / UR rows at a time
+        const int row = i * (32 / UR) + lane / UR, u = lane % UR;
+        const unsigned long long there = __shfl_sync(0xffffffffu, mine, row);
+        uint32_t x0, x1, x2, x3;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                     : "r"(place(row, u)));
+        if (there) reinterpret_cast<uint4*>(there)[u] = make_uint4(x0, x1, x2, x3);
+      }
+    } else {
+      if (to) {
+#pragma unroll
+        for (int u = 0; u < UR; ++u) reinterpret_cast<uint4*>(to)[u] = make_uint4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+      }
     }
   };
   for (int k = 0; ok; ++k) {
@@ -617,34 +650,38 @@ __device__ __forceinline__ void short_output(const CrossBwdParams& p, const Shor
       const long long row = static_cast<long long>(w.str0) + at;
       __nv_bfloat16* dk = p.a.dk + row * p.a.st[6][0] + w.head * p.a.st[6][1];
       __nv_bfloat16* dv = p.a.dv + row * p.a.st[7][0] + w.head * p.a.st[7][1];
-#pragma unroll 1
-      for (int c = 0; c < 2 * D / 32; ++c) {
-        uint32_t v[32];
-        const bool is_dv = c >= D / 32;
-        const int cc = is_dv ? c - D / 32 : c;
-        chunk(C::TM_DK + c * 32, v);  // (dV lies behind dK)
-        if (c == 2 * D / 32 - 1) {
-          tc_fence_before();
-          warp_arrive(bar.kv_free());
-        }
-        if (mine) store(v, is_dv ? 1.f : p.a.scale, (is_dv ? dv : dk) + cc * 32);
-      }
+      // (d = 32: both are read out before they are stored, for the next tile's products wait for that.)
+      constexpr bool BOTH = D <= 32;
+      uint32_t yk[D / 2], yv[D / 2];
+      take(C::TM_DK, p.a.scale, yk);
+      if constexpr (!BOTH) put(yk, mine ? dk : nullptr);
+      take(C::TM_DV, 1.f, yv);
+      tc_fence_before();
+      warp_arrive(bar.kv_free());
+      if constexpr (BOTH) put(yk, mine ? dk : nullptr);
+      put(yv, mine ? dv : nullptr);
     }
     if (!ok || !(ok = warp_wait_bar(bar.dq_done(), k & 1, g, kStatusTimeoutSoftmax))) break;
     tc_fence_after();
     const int nt = (w.fix_n + t1 - 1) / t1;
 #pragma unroll 1
-    for (int c = 0; c < nt * (D / 32); ++c) {
-      uint32_t v[32];
-      const int i = c / (D / 32), cc = c % (D / 32), tok = i * t1 + tok_r;
-      chunk(C::TM_DQ + c * 32, v);
+    for (int i = 0; i < nt; ++i) {
+      const int tok = i * t1 + tok_r;
       if (w.out == 0) {
-        if (tok_r < t1 && tok < w.fix_n)
-          store(v, p.a.scale, p.a.dq + (static_cast<long long>(w.fix0) + tok) * p.a.st[5][0] +
-                                  static_cast<long long>(w.head * group + head_r) * p.a.st[5][1] + cc * 32);
-      } else {
-        // 16-byte block b of all 128 rows of the tile together.
-        float4* part = reinterpret_cast<float4*>(p.ws.part[2] + (blockIdx.x * 2 + (w.out - 1)) * BwdWork<D, 2>::PART) + r;
+        const bool mine = tok_r < t1 && tok < w.fix_n;
+        __nv_bfloat16* dq = p.a.dq + (static_cast<long long>(w.fix0) + tok) * p.a.st[5][0] +
+                            static_cast<long long>(w.head * group + head_r) * p.a.st[5][1];
+        uint32_t y[D / 2];
+        take(C::TM_DQ + i * D, p.a.scale, y);
+        put(y, mine ? dq : nullptr);
+        continue;
+      }
+      // 16-byte block b of all 128 rows of the tile together.
+      float4* part = reinterpret_cast<float4*>(p.ws.part[2] + (blockIdx.x * 2 + (w.out - 1)) * BwdWork<D, 2>::PART) + r;
+#pragma unroll 1
+      for (int c = i * (D / 32); c < (i + 1) * (D / 32); ++c) {
+        uint32_t v[32];
+        chunk(C::TM_DQ + c * 32, v);
 #pragma unroll
         for (int b = 0; b < 8; ++b)
           part[(c * 8 + b) * 128] = make_float4(__uint_as_float(v[4 * b]), __uint_as_float(v[4 * b + 1]),
@@ -677,6 +714,7 @@ __global__ void __launch_bounds__(ShortCfg<D>::THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar.s_full(i), 1);
       mbar_init(bar.p_ready(i), C::EW_WARPS);
+      mbar_init(bar.buf_free(i), 1);
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(bar.q_full(i), 2);
@@ -688,8 +726,7 @@ __global__ void __launch_bounds__(ShortCfg<D>::THREADS, 1)
     mbar_init(bar.kv_free(), 4);
     mbar_init(bar.dq_done(), 1);
     mbar_init(bar.dq_free(), 4);
-    mbar_init(bar.drain(), 1);
-    mbar_init(bar.drain_dq(), 1);
+    for (int i = 0; i < 3; ++i) mbar_init(bar.drain(i), 1);
     for (int i = 0; i < kBwdSegRing; ++i) {
       mbar_init(bar.seg_full(i), 1);
       mbar_init(bar.seg_empty(i), C::READERS);
@@ -707,7 +744,7 @@ __global__ void __launch_bounds__(ShortCfg<D>::THREADS, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  if (warp == C::MMA_WARP) {
+  if (warp == C::S_WARP) {
     tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
     tmem_relinquish();
   }
@@ -729,10 +766,12 @@ __global__ void __launch_bounds__(ShortCfg<D>::THREADS, 1)
 
   if (warp < C::OUT_WARP0) {
     short_elementwise<D>(p, bar, base, gbase, tmem, warp >> 2, warp & 3, lane, g);
-  } else if (warp < C::MMA_WARP) {
+  } else if (warp < C::S_WARP) {
     short_output<D>(p, bar, gbase, tmem, warp & 3, lane, g);
-  } else if (warp == C::MMA_WARP) {
-    short_mma<D>(p, bar, base, gbase, tmem, g);
+  } else if (warp == C::S_WARP) {
+    short_mma_s<D>(p, bar, base, gbase, tmem, g);
+  } else if (warp == C::KV_WARP) {
+    short_mma_kv<D>(p, bar, base, gbase, tmem, g);
   } else if (warp == C::DQ_WARP) {
     if constexpr (C::DQ_APART) short_mma_dq<D>(p, bar, base, gbase, tmem, g);
   } else {
@@ -742,7 +781,7 @@ __global__ void __launch_bounds__(ShortCfg<D>::THREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == C::MMA_WARP) {
+  if (warp == C::S_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
