@@ -8,7 +8,7 @@
 // the two kernels for longer sequences (fa_cross_bwd.cuh) need seven, and every
 // tensor is read or written once.  An item is QT rows against 128 keys:
 //   S^T = K Q^T, dP^T = V dO^T          128 lanes = keys, QT columns = rows, double-buffered in tensor memory
-//   P^T, dS^T in bf16 over them         two warpgroups, half the columns each (d = 128: they take turns)
+//   P^T, dS^T in bf16 over them         two warpgroups take turns
 //   dV += P^T dO, dK += dS^T Q          A from tensor memory; read out and stored by a third warpgroup, key tile by key tile
 //   dQ += dS K                          A = dS^T, which the warpgroups also write to shared memory (M-major), over all key tiles;
 //                                       issued by a warp of its own (d <= 64)
@@ -23,10 +23,7 @@ namespace fa {
 template <int D>
 struct ShortCfg {
   static constexpr int QT = BwdWork<D, 2>::QT;          // rows of an item
-  // Both warpgroups take part in every item, half its columns each (QT = 64), or they take turns (QT = 32).
-  static constexpr bool SPLIT = false;
-  static constexpr int EW_WARPS = SPLIT ? 8 : 4;        // of an item
-  static constexpr int EW_COLS = SPLIT ? QT / 2 : QT;   // columns of a thread
+  static constexpr int EW_WARPS = 4;                    // of an item
   static constexpr int SUBS = 128 / QT;                 // items of a full row tile
   static constexpr int TILES = bwd_short_tiles(D);      // 128-row tiles of a unit at most
   static constexpr int SLOTS = D == 32 ? 6 : D == 64 ? 2 : 1;  // of the ring of Q and dO tiles
@@ -317,18 +314,13 @@ struct ShortMma {
     mma_ss_run<D / 16, SSteps>(tmem + C::TM_S + b * C::QT, k, HI, q, HI, IDESC_S, 0u);
     mma_ss_run<D / 16, SSteps>(tmem + C::TM_DP + b * C::QT, k + V, HI, q + V, HI, IDESC_S, 0u);
   }
-  // dV (+)= P^T dO, dK (+)= dS^T Q (SPLIT: the two warpgroups' halves of the rows one after the other).
+  // dV (+)= P^T dO, dK (+)= dS^T Q.
   __device__ __forceinline__ void dkv(uint32_t slot, int s, uint32_t b, bool acc) const {
     const uint32_t q = q_mn + q_off(slot, s);
     const uint32_t f = acc ? 1u : 0u;
-    constexpr int N = C::EW_COLS / 16;
-    constexpr uint32_t HALF = C::EW_COLS * C::SWB >> 4;
+    constexpr int N = C::QT / 16;
     mma_ts_run<N, AccSteps>(tmem + C::TM_DV, tmem + C::TM_S + b * C::QT, q + V, HI, IDESC_O, f);
-    if constexpr (C::SPLIT)
-      mma_ts_run<N, AccSteps>(tmem + C::TM_DV, tmem + C::TM_S + b * C::QT + C::EW_COLS, q + V + HALF, HI, IDESC_O, 1u);
     mma_ts_run<N, AccSteps>(tmem + C::TM_DK, tmem + C::TM_DP + b * C::QT, q, HI, IDESC_O, f);
-    if constexpr (C::SPLIT)
-      mma_ts_run<N, AccSteps>(tmem + C::TM_DK, tmem + C::TM_DP + b * C::QT + C::EW_COLS, q + HALF, HI, IDESC_O, 1u);
   }
   // dQ of row tile i (+)= dS K.
   __device__ __forceinline__ void dq(uint32_t st, int i, bool acc) const {
@@ -497,10 +489,9 @@ __device__ __forceinline__ void short_elementwise(const CrossBwdParams& p, const
       it.enter(w, t1, group);
     }
     const uint32_t b = n & 1;
-    if (C::SPLIT || b == static_cast<uint32_t>(wg)) {
+    if (b == static_cast<uint32_t>(wg)) {
       uint32_t slot, par;
       it.slot(slot, par);
-      const int c0 = C::SPLIT ? wg * C::EW_COLS : 0;  // this warpgroup's first column of the item
       const int rows = short_rows(w.fix_n, it.tile(), t1, group) - it.sub() * C::QT;  // of this item's QT on
       const int left = w.str_n - (w.s0 + it.j) * 128;
       const bool key = r < left;  // this thread's key is one
@@ -510,23 +501,23 @@ __device__ __forceinline__ void short_elementwise(const CrossBwdParams& p, const
       tc_fence_after();
       const bool need_mask = left < 128 || rows < C::QT;
       if (need_mask) {
-        if (it.j == 0 && rows < C::QT) {  // SPLIT: warpgroup 0 Q, 1 dO
+        if (it.j == 0 && rows < C::QT) {  // first Q's, then dO's
           const uint32_t tile = base + C::OFF_Q + slot * 2 * C::TILE;
-          for (int x = C::SPLIT ? wg * C::QT + r : r; x < (C::SPLIT ? (wg + 1) : 2) * C::QT; x += 128) {
+          for (int x = r; x < 2 * C::QT; x += 128) {
             const int row = x % C::QT;
             if (row >= rows) zero_row(tile + x / C::QT * C::TILE, it.sub() * C::QT + row);
           }
         }
-        if (it.m == 0 && !key && (!C::SPLIT || wg == 0)) zero_row(base + C::OFF_ST + it.st.at * C::STAGE, r);
+        if (it.m == 0 && !key) zero_row(base + C::OFF_ST + it.st.at * C::STAGE, r);
         __syncwarp();
       }
-      const float4* vl2 = reinterpret_cast<const float4*>(gbase + C::OFF_VEC + slot * C::VEC) + (it.sub() * C::QT + c0) / 4;
+      const float4* vl2 = reinterpret_cast<const float4*>(gbase + C::OFF_VEC + slot * C::VEC) + it.sub() * C::QT / 4;
       const float4* vd = vl2 + 32;
 #pragma unroll 1
-      for (int h = 0; h < C::EW_COLS / 32; ++h) {
+      for (int h = 0; h < C::QT / 32; ++h) {
         uint32_t rs[32], rd[32];
-        tmem_ld32(tmem + lane_off + C::TM_S + b * C::QT + c0 + 32 * h, rs);
-        tmem_ld32(tmem + lane_off + C::TM_DP + b * C::QT + c0 + 32 * h, rd);
+        tmem_ld32(tmem + lane_off + C::TM_S + b * C::QT + 32 * h, rs);
+        tmem_ld32(tmem + lane_off + C::TM_DP + b * C::QT + 32 * h, rd);
         tmem_wait_ld(rs);
         tmem_wait_ld(rd);
         uint32_t pk[16], dk[16];
@@ -547,7 +538,7 @@ __device__ __forceinline__ void short_elementwise(const CrossBwdParams& p, const
         }
         if (need_mask) {
           // (Bits, so that a NaN goes, too; outside the loop above, whose instructions are what an item costs.)
-          const int v = rows - c0 - 32 * h;  // columns of this thread's that are rows
+          const int v = rows - 32 * h;  // columns of this thread's that are rows
           const uint32_t keep = key ? 0xffffffffu : 0u;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
@@ -557,12 +548,12 @@ __device__ __forceinline__ void short_elementwise(const CrossBwdParams& p, const
           }
         }
         // The bf16 pairs land over what this warpgroup has read.
-        tmem_st16(tmem + lane_off + C::TM_S + b * C::QT + c0 + 16 * h, pk);
-        tmem_st16(tmem + lane_off + C::TM_DP + b * C::QT + c0 + 16 * h, dk);
+        tmem_st16(tmem + lane_off + C::TM_S + b * C::QT + 16 * h, pk);
+        tmem_st16(tmem + lane_off + C::TM_DP + b * C::QT + 16 * h, dk);
         // The row tile's dS^T before this one has been read.
         if (h == 0 && dqs > 0 && !(ok = warp_wait_bar(bar.ds_empty(dqs - 1), ((dqs - 1) >> 1) & 1, g, kStatusTimeoutSoftmax))) break;
         // dS^T into shared memory: key r's row of 64 rows of Q a region, 128-byte swizzled.
-        const int q0 = it.sub() * C::QT + c0 + 32 * h;
+        const int q0 = it.sub() * C::QT + 32 * h;
         const uint32_t row = base + C::OFF_DS + (q0 >> 6) * C::DS_REGION + r * 128;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
