@@ -10,6 +10,8 @@
 //    accumulator, short sequences fill tiles, and K and V are read once for all of them.
 //      MODE 0 (dK, dV): a unit is 128 keys of one head; tiles of BS / G tokens of Q and dO stream past.
 //      MODE 1 (dQ): a unit is 128 / G tokens of one key/value head; tiles of BS keys of K and V stream past.
+//    d = 256: two accumulators of 128 x 256 leave no tensor memory for S and dP, so dV (MODE 3: S, dV) and dK (MODE 4: S, dP, dK)
+//    are passes of their own: five products a tile, and six where two units with half of the columns each make both.
 //    Rows of a streamed tile that are no token's or key's (anything, NaN too) meet zeros of P and dS in the accumulations, and 0
 //    times NaN is NaN: the warpgroup that forms these sets such rows to zero first, behind S and dP of the tile.
 //  * Sequences of few rows have a kernel of their own (fa_cross_bwd_short.cuh, MODE 2 here) that makes all three gradients
@@ -29,6 +31,44 @@
 namespace fa {
 
 constexpr int kBwdSegRing = 4;
+
+// dV or dK of d = 256: TMEM columns S' buffers, (dK) dP's buffers, the accumulator; the vectors of the streamed rows lie
+// behind everything else, where they leave room for one more stage.
+template <int MODE>
+struct BwdWideCfg {
+  static constexpr bool KV = false;
+  static constexpr int BM = 128;
+  static constexpr int BS = 32;
+  static constexpr int OUTW = 256, NOUT = 1;
+  static constexpr int SWB = 128;
+  static constexpr uint32_t SWZ = 2u;
+  static constexpr int RC = 64, NR = 4;
+  static constexpr int FIX_REGION = BM * SWB, S_REGION = BS * SWB;
+  static constexpr int FIX_TILE = BM * 512, S_TILE = BS * 512;
+  static constexpr int VEC_BYTES = BS * 4;
+  static constexpr int STAGE = 2 * S_TILE;
+  static constexpr int OFF_FIX = 0;
+  static constexpr int OFF_ST = (MODE == 3 ? 1 : 2) * FIX_TILE;  // dV: K alone
+  static constexpr int NST = MODE == 3 ? 4 : 3;
+  static constexpr int OFF_MISC = OFF_ST + NST * STAGE;
+  static constexpr int MISC = 1024 + NST * 2 * VEC_BYTES;
+  static constexpr int OFF_TMEM_SLOT = OFF_MISC + 512;
+  static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
+  static constexpr int SMEM_ALLOC = OFF_MISC + MISC + 1024;  // + slack for 1024-byte alignment
+  static constexpr int TM_S = 0, TM_DP = 2 * BS, TM_OUT = 4 * BS, TM_COLS = 512;
+  static constexpr bool RUNS = true;
+  static constexpr int MMA_WARP = 8, LOAD_WARP = 9;
+  static constexpr int THREADS = 320;
+  static_assert(TM_OUT + OUTW <= TM_COLS && SMEM_ALLOC <= 227 * 1024, "TMEM and shared memory budgets");
+};
+template <>
+struct BwdCfg<256, 3> : BwdWideCfg<3> {};
+template <>
+struct BwdCfg<256, 4> : BwdWideCfg<4> {};
+
+// Whether a unit is 128 keys (else 128 rows), and which of the workspace's three records and parts are a mode's.
+constexpr __host__ __device__ bool bwd_by_key(int mode) { return mode == 0 || mode >= 3; }
+constexpr __host__ __device__ int bwd_place(int mode) { return mode == 3 ? 0 : mode == 4 ? 2 : mode; }
 
 // Tokens of a streamed tile of MODE 0 and of a fixed tile of MODE 1.
 template <int D>
@@ -56,7 +96,6 @@ __host__ __device__ __forceinline__ bool bwd_short(const CrossSeq& s, int group)
 // Units, fixed and streamed tiles of a kernel.
 template <int D, int MODE>
 struct BwdWork {
-  static constexpr int HALVES = BwdCfg<D, MODE>::HALVES;
   static constexpr int STR = BwdCfg<D, MODE>::BS;
   static constexpr size_t PART = static_cast<size_t>(128) * BwdCfg<D, MODE>::NOUT * BwdCfg<D, MODE>::OUTW;  // floats of a part
   // Streamed tiles that a unit costs besides its own (loading the fixed tiles, the output).
@@ -64,7 +103,6 @@ struct BwdWork {
 };
 template <int D>
 struct BwdWork<D, 2> {
-  static constexpr int HALVES = 1;
   static constexpr int STR = 128;
   static constexpr size_t PART = static_cast<size_t>(128) * bwd_short_tiles(D) * D;
   static constexpr int QT = D <= 64 ? 64 : 32;  // rows of an item (fa_cross_bwd_short.cuh), which is a place on the line
@@ -74,7 +112,7 @@ struct BwdWork<D, 2> {
 
 // Workspace of fa_cross_bwd.
 struct CrossBwdWs {
-  PlanRecord* rec[3];  // of the kernels: [kPlanCtas]
+  PlanRecord* rec[3];  // of the kernels (bwd_place): [kPlanCtas]
   int* part0;          // [kPlanCtas]: MODE 2's CTA has written its part 0
   float* l2;           // [heads][tiles][BS]
   float* dsum;
@@ -94,9 +132,9 @@ size_t cross_bwd_ws(char* p, int B, int rows, int heads, int group, CrossBwdWs* 
   x.part0 = reinterpret_cast<int*>(take(kPlanCtas * sizeof(int)));
   x.l2 = reinterpret_cast<float*>(take(vec));
   x.dsum = reinterpret_cast<float*>(take(vec));
-  x.part[0] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, 0>::PART * sizeof(float)));
+  x.part[0] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, D == 256 ? 3 : 0>::PART * sizeof(float)));
   x.part[1] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, 1>::PART * sizeof(float)));
-  x.part[2] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, 2>::PART * sizeof(float)));
+  x.part[2] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, D == 256 ? 4 : 2>::PART * sizeof(float)));
   if (w) *w = x;
   return at;
 }
@@ -114,14 +152,14 @@ struct alignas(16) BwdSeg {
   int valid;
   int head;   // key/value head
   int fix0;   // first row of the fixed tile in its tensor
-  int fix_n;  // its keys (MODE 0) or tokens (MODE 1, 2)
+  int fix_n;  // its keys (bwd_by_key) or tokens
   int tok0;   // MODE 1: its first token within the sequence
   int str0;   // the sequence's first row in the streamed tensor
-  int str_n;  // its tokens (MODE 0) or keys (MODE 1, 2)
+  int str_n;  // its tokens (bwd_by_key) or keys
   int vec0;   // its first tile of the vectors
   int s0;     // first streamed tile
   int n;      // streamed tiles
-  int half;
+  int unused;
   int out;    // 0: the unit is whole; 1, 2: part 0, part 1 of this CTA
 };
 static_assert(sizeof(BwdSeg) == 48, "segment size");
@@ -131,8 +169,44 @@ struct CrossBwdCfg : BwdCfg<D, MODE> {
   using C = BwdCfg<D, MODE>;
   static constexpr int OFF_SEG = C::OFF_MISC + 576;
   static constexpr int OFF_PLAN = OFF_SEG + kBwdSegRing * static_cast<int>(sizeof(BwdSeg));
-  static constexpr int READERS = 9;
-  static_assert(C::OFF_ABORT + 4 <= OFF_SEG && OFF_PLAN + sizeof(PlanScratch) <= C::OFF_MISC + C::MISC, "misc area");
+  static constexpr bool BY_KEY = bwd_by_key(MODE);      // K and V stay, Q and dO stream past, with the vectors
+  static constexpr bool DV = MODE == 0 || MODE == 3;
+  static constexpr bool DP = MODE != 3;                 // dP is formed, and dK or dQ
+  // Warps: 0-7 elementwise, 8 MMA, 9 load; d = 256: 10 MMA of the accumulators.  One warp takes some 65 cycles for each
+  // product, which of 32 streamed rows is more than the tensor core takes (6 sequences of 100 to 700 rows, d = 256: 242 us with one, 203 with
+  // two); with more rows it is not, and the warps' signals to each other cost more (d = 128, 1 to 4 K rows: 1.27 ms with one, 1.41 with two).
+  static constexpr bool ACC_APART = D == 256;
+  static constexpr int ACC_WARP = C::LOAD_WARP + 1;
+  static constexpr int THREADS = ACC_APART ? 352 : 320;
+  static constexpr int READERS = ACC_APART ? 10 : 9;
+  // A stage's vectors.
+  static __device__ __forceinline__ int off_vec(int st) {
+    return MODE == 0 ? C::OFF_ST + st * C::STAGE + 2 * C::S_TILE : C::OFF_MISC + 1024 + st * 2 * C::VEC_BYTES;
+  }
+  static_assert(C::OFF_ABORT + 4 <= OFF_SEG && OFF_PLAN + sizeof(PlanScratch) <= C::OFF_MISC + 1024, "misc area");
+};
+
+template <int D, int MODE>
+struct CrossBwdMma : BwdMma<D, MODE> {
+  using BwdMma<D, MODE>::BwdMma;
+};
+// S = K Q^T, dV (+)= P^T dO.
+template <int D>
+struct CrossBwdMma<D, 3> : BwdMma<D, 3> {
+  using Base = BwdMma<D, 3>;
+  using C = BwdCfg<D, 3>;
+  using Base::BwdMma;
+  __device__ __forceinline__ void sdp(uint32_t st, int b) const {
+    using S0 = typename Base::template SdpSteps<0>;
+    using S8 = typename Base::template SdpSteps<8>;
+    const uint32_t d = this->tmem + C::TM_S + b * C::BS, q = this->b1 + st * Base::STAGE_STEP;
+    mma_ss_run<8, S0>(d, this->a1, Base::DESC_HI, q, Base::DESC_HI, Base::IDESC_S, 0u);
+    mma_ss_run<8, S8>(d, this->a1 + Base::a_step(8), Base::DESC_HI, q + Base::b_step(8), Base::DESC_HI, Base::IDESC_S, 1u);
+  }
+  __device__ __forceinline__ void accumulate(uint32_t st, int b, bool acc, int) const {
+    mma_ts_run<C::BS / 16, typename Base::AccSteps>(this->tmem + C::TM_OUT, this->tmem + C::TM_S + b * C::BS,
+                                                    this->b2_mn + st * Base::STAGE_STEP, Base::DESC_HI, Base::IDESC_O, acc ? 1u : 0u);
+  }
 };
 
 template <int D, int MODE>
@@ -140,14 +214,17 @@ struct CrossBwdBars : BwdBars<D, MODE> {
   using Base = BwdBars<D, MODE>;
   __device__ __forceinline__ uint32_t seg_full(int i) const { return this->b0 + 256 + 8u * i; }
   __device__ __forceinline__ uint32_t seg_empty(int i) const { return this->b0 + 288 + 8u * i; }
-  static_assert(Base::COUNT * 8 <= 256, "barrier area");
+  // The accumulations that read P and dS in buffer b are complete.
+  __device__ __forceinline__ uint32_t buf_free(int b) const { return this->b0 + 240 + 8u * b; }
+  __device__ __forceinline__ uint32_t drain_acc() const { return this->b0 + 232; }
+  static_assert(Base::COUNT * 8 <= 232, "barrier area");
 };
 
 // The units of a sequence.
 struct BwdUnits {
   int fix;    // fixed tiles a head
   int str;    // streamed tiles
-  int units;  // fixed tiles x heads x halves
+  int units;  // fixed tiles x heads
   int w;      // places of a streamed tile on the line
   // Places of a unit.
   template <int COST>
@@ -166,7 +243,7 @@ __host__ __device__ __forceinline__ BwdUnits bwd_units(const CrossArgs& a, const
       const int t = bwd_tokens1(a.group), full = s.n / t, rest = s.n % t;  // whole row tiles, and tokens of the last one
       u.w = full * ((t * a.group + C::QT - 1) / C::QT) + (rest * a.group + C::QT - 1) / C::QT + C::TILE_COST;
     }
-  } else if (MODE == 0) {
+  } else if (bwd_by_key(MODE)) {
     const int t = bwd_tokens0<D>(a.group);
     u.fix = (s.len + 127) / 128;
     u.str = (s.n + t - 1) / t;
@@ -175,7 +252,7 @@ __host__ __device__ __forceinline__ BwdUnits bwd_units(const CrossArgs& a, const
     u.fix = (s.n + t - 1) / t;
     u.str = (s.len + C::STR - 1) / C::STR;
   }
-  u.units = u.fix * a.heads * C::HALVES;
+  u.units = u.fix * a.heads;
   return u;
 }
 
@@ -230,10 +307,9 @@ struct CrossBwdWalk {
     const long long begin = (end - pos + c.w - 1) / c.w;  // tiles that begin before the share's end
     const int n = begin < c.str - j ? static_cast<int>(begin) : c.str - j;
     g.valid = 1;
-    g.half = u % C::HALVES;
-    const int tile = u / C::HALVES % c.fix;
-    g.head = u / C::HALVES / c.fix;
-    if (MODE == 0) {
+    const int tile = u % c.fix;
+    g.head = u / c.fix;
+    if (bwd_by_key(MODE)) {
       g.fix0 = s.key0 + tile * 128;
       g.fix_n = min(128, s.len - tile * 128);
       g.str0 = s.row0;
@@ -300,7 +376,7 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
     if (lane == 0) {
       reinterpret_cast<BwdSeg*>(gbase + C::OFF_SEG)[i] = w;
       if (w.out == 2)  // this unit's first part: who holds the rest
-        p.ws.rec[MODE][blockIdx.x] =
+        p.ws.rec[bwd_place(MODE)][blockIdx.x] =
             PlanRecord{walk.record_b, w.head, walk.record_u,
                        plan_cta_of(walk.last_tile, share.total, share.ctas) - static_cast<int>(blockIdx.x)};
     }
@@ -310,13 +386,13 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
     // The fixed tiles: K, V (128 keys of a head), or Q, dO (a group's heads of 128 / G tokens).
     if (!(ok = warp_wait_bar(bar.fix_empty(), (k & 1) ^ 1, g, kStatusTimeoutLoad))) break;
     if (lane == 0) {
-      const int rows = MODE == 0 ? 128 : t1 * group;
-      mbar_arrive_expect_tx(bar.fix_full(), 2 * C::NR * rows * C::SWB);
+      const int rows = C::BY_KEY ? 128 : t1 * group;
+      mbar_arrive_expect_tx(bar.fix_full(), (C::DP ? 2 : 1) * C::NR * rows * C::SWB);
       for (int r = 0; r < C::NR; ++r) {
         const uint32_t dst = base + C::OFF_FIX + r * C::FIX_REGION;
-        const int h = MODE == 0 ? w.head : w.head * group;
+        const int h = C::BY_KEY ? w.head : w.head * group;
         tma_load_3d(dst, tm_a1, bar.fix_full(), r * C::RC, h, w.fix0, pol_fix);
-        tma_load_3d(dst + C::FIX_TILE, tm_a2, bar.fix_full(), r * C::RC, h, w.fix0, pol_fix);
+        if (C::DP) tma_load_3d(dst + C::FIX_TILE, tm_a2, bar.fix_full(), r * C::RC, h, w.fix0, pol_fix);
       }
     }
     last_fix = k;
@@ -327,19 +403,20 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
       if (lane == 0) {
         const uint32_t s0 = base + C::OFF_ST + st * C::STAGE;
         const uint32_t full = bar.st_full(st);
-        const int rows = MODE == 0 ? t0 * group : C::BS;
-        mbar_arrive_expect_tx(full, 2 * C::NR * rows * C::SWB + (C::KV ? 2 * C::VEC_BYTES : 0));
-        const int s = w.s0 + t, h = MODE == 0 ? w.head * group : w.head;
-        const int row = w.str0 + s * (MODE == 0 ? t0 : C::BS);
+        const int rows = C::BY_KEY ? t0 * group : C::BS;
+        mbar_arrive_expect_tx(full, 2 * C::NR * rows * C::SWB + (C::BY_KEY ? (C::DP ? 2 : 1) * C::VEC_BYTES : 0));
+        const int s = w.s0 + t, h = C::BY_KEY ? w.head * group : w.head;
+        const int row = w.str0 + s * (C::BY_KEY ? t0 : C::BS);
         for (int r = 0; r < C::NR; ++r) {
           tma_load_3d(s0 + r * C::S_REGION, tm_b1, full, r * C::RC, h, row, pol_str);
           tma_load_3d(s0 + C::S_TILE + r * C::S_REGION, tm_b2, full, r * C::RC, h, row, pol_str);
         }
-        if constexpr (C::KV) {
+        if constexpr (C::BY_KEY) {
           // (BS * 4 is a multiple of 16.)
           const long long off = (w.head * p.tiles + w.vec0 + s) * C::BS;
-          bulk_load(s0 + 2 * C::S_TILE, p.ws.l2 + off, C::VEC_BYTES, full);
-          bulk_load(s0 + 2 * C::S_TILE + C::VEC_BYTES, p.ws.dsum + off, C::VEC_BYTES, full);
+          const uint32_t vec = base + C::off_vec(st);
+          bulk_load(vec, p.ws.l2 + off, C::VEC_BYTES, full);
+          if (C::DP) bulk_load(vec + C::VEC_BYTES, p.ws.dsum + off, C::VEC_BYTES, full);
         }
       }
       issued |= 1u << st;
@@ -348,7 +425,7 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
     }
     if (!ok) break;
   }
-  if (lane == 0 && !recorded) p.ws.rec[MODE][blockIdx.x].b = -1;
+  if (lane == 0 && !recorded) p.ws.rec[bwd_place(MODE)][blockIdx.x].b = -1;
   // Every issued copy must land before the CTA may exit.
   for (int i = 0; i < C::NST; ++i)
     if (issued & (1u << i)) bwd_wait_drain(bar.st_full(i), (last_par >> i) & 1, g);
@@ -357,16 +434,27 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
 }
 
 // ------------------------------------------------------------------ MMA issuer
-// bwd_mma's order of products, segment by segment.
-template <int D, int MODE>
-__device__ __forceinline__ void cross_bwd_mma(const CrossBwdParams& p, const CrossBwdBars<D, MODE>& bar, uint32_t base,
-                                              uint8_t* gbase, uint32_t tmem, const WaitGuard& g) {
-  using C = CrossBwdCfg<D, MODE>;
-  const BwdMma<D, MODE> M(tmem, base);
-  auto wait = [&](uint32_t b, uint32_t par) -> bool {
+struct CrossIssuer {
+  const WaitGuard& g;
+  __device__ __forceinline__ bool wait(uint32_t b, uint32_t par) const {
     const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
     return __all_sync(0xffffffffu, r);
-  };
+  }
+  // All products issued must complete before TMEM is released.
+  __device__ __forceinline__ void finish(uint32_t drain) const {
+    mma_commit_elect(drain);
+    bwd_wait_drain(drain, 0, g);
+    __syncwarp();
+  }
+};
+
+// bwd_mma's order of products, segment by segment.
+template <int D, int MODE>
+__device__ __forceinline__ void cross_bwd_mma(const CrossBwdBars<D, MODE>& bar, uint32_t base,
+                                              uint8_t* gbase, uint32_t tmem, const WaitGuard& g) {
+  using C = CrossBwdCfg<D, MODE>;
+  const CrossBwdMma<D, MODE> M(tmem, base);
+  const CrossIssuer is{g};
   uint32_t pos = 0;            // streamed stages consumed before the current segment
   uint32_t pr0 = 0, pr1 = 0;   // p_ready phases consumed, per buffer
   bool ok = true;
@@ -374,12 +462,12 @@ __device__ __forceinline__ void cross_bwd_mma(const CrossBwdParams& p, const Cro
     BwdSeg w;
     if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
     const int n = w.n;
-    if (!(ok = wait(bar.fix_full(), k & 1))) break;
+    if (!(ok = is.wait(bar.fix_full(), k & 1))) break;
     tc_fence_after();
     auto stage_of = [&](int t) -> uint32_t { return (pos + t) % C::NST; };
     auto acquire = [&](int t) -> bool {
       const uint32_t q = pos + t;
-      if (!wait(bar.st_full(q % C::NST), (q / C::NST) & 1)) return false;
+      if (!is.wait(bar.st_full(q % C::NST), (q / C::NST) & 1)) return false;
       tc_fence_after();
       return true;
     };
@@ -392,14 +480,14 @@ __device__ __forceinline__ void cross_bwd_mma(const CrossBwdParams& p, const Cro
     for (int t = 0; ok && t < n; ++t) {
       const int b = t & 1;
       uint32_t& pr = b ? pr1 : pr0;
-      if (!(ok = wait(bar.p_ready(b), pr & 1))) break;
+      if (!(ok = is.wait(bar.p_ready(b), pr & 1))) break;
       ++pr;
       tc_fence_after();
       if (t == 0 && k > 0) {
-        if (!(ok = wait(bar.out_free(), (k - 1) & 1))) break;
+        if (!(ok = is.wait(bar.out_free(), (k - 1) & 1))) break;
         tc_fence_after();
       }
-      M.accumulate(stage_of(t), b, t > 0, w.half);
+      M.accumulate(stage_of(t), b, t > 0, 0);
       mma_commit_elect(bar.st_empty(stage_of(t)));
       if (t + 2 < n) {
         if (!(ok = acquire(t + 2))) break;
@@ -412,10 +500,66 @@ __device__ __forceinline__ void cross_bwd_mma(const CrossBwdParams& p, const Cro
     pos += n;
     mma_commit_elect(bar.out_done());
   }
-  // All issued MMAs must complete before TMEM is released.
-  mma_commit_elect(bar.drain());
-  bwd_wait_drain(bar.drain(), 0, g);
-  __syncwarp();
+  is.finish(bar.drain());
+}
+
+// ACC_APART: S and dP, segment by segment.
+template <int D, int MODE>
+__device__ __forceinline__ void cross_bwd_sdp(const CrossBwdBars<D, MODE>& bar, uint32_t base, uint8_t* gbase, uint32_t tmem,
+                                              const WaitGuard& g) {
+  using C = CrossBwdCfg<D, MODE>;
+  const CrossBwdMma<D, MODE> M(tmem, base);
+  const CrossIssuer is{g};
+  uint32_t pos = 0;                // streamed stages issued
+  uint32_t used[2] = {0, 0};       // tiles issued into the buffers
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    BwdSeg w;
+    if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
+    if (!(ok = is.wait(bar.fix_full(), k & 1))) break;
+    for (int t = 0; t < w.n; ++t, ++pos) {
+      const int b = t & 1;
+      uint32_t& u = b ? used[1] : used[0];
+      if (!(ok = is.wait(bar.st_full(pos % C::NST), (pos / C::NST) & 1))) break;
+      if (u > 0 && !(ok = is.wait(bar.buf_free(b), (u - 1) & 1))) break;
+      ++u;
+      tc_fence_after();
+      M.sdp(pos % C::NST, b);
+      mma_commit_elect(bar.s_full(b));
+      if (t == w.n - 1) mma_commit_elect(bar.fix_empty());
+    }
+  }
+  is.finish(bar.drain());
+}
+
+// The accumulations.
+template <int D, int MODE>
+__device__ __forceinline__ void cross_bwd_acc(const CrossBwdBars<D, MODE>& bar, uint32_t base, uint8_t* gbase, uint32_t tmem,
+                                              const WaitGuard& g) {
+  using C = CrossBwdCfg<D, MODE>;
+  const CrossBwdMma<D, MODE> M(tmem, base);
+  const CrossIssuer is{g};
+  uint32_t pos = 0;            // streamed stages consumed
+  uint32_t pr0 = 0, pr1 = 0;   // p_ready phases consumed, per buffer
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    BwdSeg w;
+    if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
+    for (int t = 0; t < w.n; ++t, ++pos) {
+      const int b = t & 1;
+      uint32_t& pr = b ? pr1 : pr0;
+      if (!(ok = is.wait(bar.p_ready(b), pr & 1))) break;
+      ++pr;
+      if (t == 0 && k > 0 && !(ok = is.wait(bar.out_free(), (k - 1) & 1))) break;
+      tc_fence_after();
+      M.accumulate(pos % C::NST, b, t > 0, 0);
+      mma_commit_elect(bar.buf_free(b));
+      mma_commit_elect(bar.st_empty(pos % C::NST));
+    }
+    if (!ok) break;
+    mma_commit_elect(bar.out_done());
+  }
+  is.finish(bar.drain_acc());
 }
 
 // ------------------------------------------------------------------ elementwise warpgroups
@@ -430,8 +574,8 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
   const float sl2 = p.scale_log2;
   const uint64_t sl2x2 = f2_pack(sl2, sl2);
   // MODE 1: this thread's token within the fixed tile, and its head of the group.
-  const int per = MODE == 0 ? bwd_tokens0<D>(p.a.group) : C::BS;  // tokens or keys of a streamed tile
-  const int tok_r = MODE == 0 ? 0 : r / p.a.group, head_r = MODE == 0 ? 0 : r - tok_r * p.a.group;
+  const int per = C::BY_KEY ? bwd_tokens0<D>(p.a.group) : C::BS;  // tokens or keys of a streamed tile
+  const int tok_r = C::BY_KEY ? 0 : r / p.a.group, head_r = C::BY_KEY ? 0 : r - tok_r * p.a.group;
   uint32_t sf = 0;    // s_full(b) phases consumed
   uint32_t pos = 0;   // streamed stages before the current segment
   bool ok = true;
@@ -439,7 +583,7 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
     BwdSeg w;
     if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
     const int n = w.n;
-    const bool mine = MODE == 0 ? r < w.fix_n : tok_r < w.fix_n;  // (tokens: fix_n <= 128 / G)
+    const bool mine = C::BY_KEY ? r < w.fix_n : tok_r < w.fix_n;  // (tokens: fix_n <= 128 / G)
     uint64_t l2_row = 0, d_row = 0;  // MODE 1: this row's -L * log2(e) and -D, twice
     if constexpr (MODE == 1) {
       float l2 = -INFINITY, dsum = 0.f;
@@ -459,7 +603,7 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
       ++sf;
       const uint32_t q = pos + t;
       const int st = q % C::NST;
-      if constexpr (C::KV) {
+      if constexpr (C::BY_KEY) {
         // The stage's vectors were written by TMA; observe that completion here too.
         ok = warp_wait_bar(bar.st_full(st), (q / C::NST) & 1, g, kStatusTimeoutSoftmax);
         if (!ok) break;
@@ -467,11 +611,12 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
       tc_fence_after();
       // Rows of the tile that are a token's or a key's; the others are not looked at in S and dP, but meet zeros of P and dS in
       // the accumulations.
-      const int there = MODE == 0 ? min(w.str_n - (w.s0 + t) * per, per) * p.a.group : w.str_n - (w.s0 + t) * per;
+      const int there = C::BY_KEY ? min(w.str_n - (w.s0 + t) * per, per) * p.a.group : w.str_n - (w.s0 + t) * per;
       const bool need_mask = there < C::BS;
       if (need_mask) {
-        const uint32_t tile = smem_u32(gbase + C::OFF_ST + st * C::STAGE);
-        for (int x = r; x < (C::KV ? 2 : 1) * C::BS; x += 128) {
+        // (MODE 0: both tiles; dV alone: dO's; else the first one's.)
+        const uint32_t tile = smem_u32(gbase + C::OFF_ST + st * C::STAGE) + (MODE == 3 ? C::S_TILE : 0);
+        for (int x = r; x < (MODE == 0 ? 2 : 1) * C::BS; x += 128) {
           const int row = x % C::BS;
           if (row < there) continue;
 #pragma unroll
@@ -481,26 +626,29 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
         fence_proxy_async_smem();
         __syncwarp();
       }
-      const float4* vl2 = reinterpret_cast<const float4*>(gbase + C::OFF_ST + st * C::STAGE + 2 * C::S_TILE);
+      const float4* vl2 = reinterpret_cast<const float4*>(gbase + (C::BY_KEY ? C::off_vec(st) : 0));
       const float4* vd = vl2 + C::BS / 4;
 #pragma unroll 1
       for (int h = 0; h < C::BS / 32; ++h) {
         uint32_t rs[32], rd[32];
         tmem_ld32(tmem + lane_off + C::TM_S + b * C::BS + h * 32, rs);
-        tmem_ld32(tmem + lane_off + C::TM_DP + b * C::BS + h * 32, rd);
+        if constexpr (C::DP) tmem_ld32(tmem + lane_off + C::TM_DP + b * C::BS + h * 32, rd);
         tmem_wait_ld(rs);
-        tmem_wait_ld(rd);
+        if constexpr (C::DP) tmem_wait_ld(rd);
         uint32_t pk[16], dk[16];
 #pragma unroll
         for (int c4 = 0; c4 < 8; ++c4) {
           // -L * log2(e) and -D of the four streamed rows (MODE 0) or of this row (MODE 1).
           uint64_t nl[2], nd[2];
-          if constexpr (C::KV) {
-            const float4 a = vl2[h * 8 + c4], d4 = vd[h * 8 + c4];
+          if constexpr (C::BY_KEY) {
+            const float4 a = vl2[h * 8 + c4];
             nl[0] = f2_pack(a.x, a.y);
             nl[1] = f2_pack(a.z, a.w);
-            nd[0] = f2_pack(d4.x, d4.y);
-            nd[1] = f2_pack(d4.z, d4.w);
+            if constexpr (C::DP) {
+              const float4 d4 = vd[h * 8 + c4];
+              nd[0] = f2_pack(d4.x, d4.y);
+              nd[1] = f2_pack(d4.z, d4.w);
+            }
           } else {
             nl[0] = nl[1] = l2_row;
             nd[0] = nd[1] = d_row;
@@ -510,8 +658,9 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
             const int c = c4 * 4 + e2 * 2;
             const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(rs[c]), __uint_as_float(rs[c + 1])), sl2x2, nl[e2]));
             float p0 = ex2(x.x), p1 = ex2(x.y);
-            float2 ds = f2_unpack(
-                f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(rd[c]), __uint_as_float(rd[c + 1])), nd[e2])));
+            float2 ds = {0.f, 0.f};
+            if constexpr (C::DP)
+              ds = f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(rd[c]), __uint_as_float(rd[c + 1])), nd[e2])));
             if (need_mask) {
               if (h * 32 + c >= there) p0 = ds.x = 0.f;
               if (h * 32 + c + 1 >= there) p1 = ds.y = 0.f;
@@ -521,8 +670,8 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
           }
         }
         // As in bwd_elementwise: chunk h's bf16 pairs land behind what has been read.
-        if constexpr (C::KV) tmem_st16(tmem + lane_off + C::TM_S + b * C::BS + h * 16, pk);
-        tmem_st16(tmem + lane_off + C::TM_DP + b * C::BS + h * 16, dk);
+        if constexpr (C::DV) tmem_st16(tmem + lane_off + C::TM_S + b * C::BS + h * 16, pk);
+        if constexpr (C::DP) tmem_st16(tmem + lane_off + C::TM_DP + b * C::BS + h * 16, dk);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -534,20 +683,21 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
     ok = warp_wait_bar(bar.out_done(), k & 1, g, kStatusTimeoutSoftmax);
     if (!ok) break;
     tc_fence_after();
-    const bool second = C::KV && b == 1;
+    const bool second = MODE == 0 && b == 1;
+    const bool dv = second || MODE == 3;
     const uint32_t acc = tmem + lane_off + C::TM_OUT + (second ? C::OUTW : 0);
-    const float f = second ? 1.f : p.a.scale;  // dK and dQ carry the softmax scale
+    const float f = dv ? 1.f : p.a.scale;  // dK and dQ carry the softmax scale
     const uint64_t f2 = f2_pack(f, f);
-    __nv_bfloat16* out = MODE == 1 ? p.a.dq : second ? p.a.dv : p.a.dk;
-    const long long* os = p.a.st[MODE == 1 ? 5 : second ? 7 : 6];
-    const int head = MODE == 0 ? w.head : w.head * p.a.group + head_r;
-    const long long row = w.fix0 + (MODE == 0 ? r : tok_r);
-    __nv_bfloat16* orow = out + row * os[0] + head * os[1] + w.half * C::OUTW;
-    float4* part = reinterpret_cast<float4*>(p.ws.part[MODE] + (blockIdx.x * 2 + (w.out - 1)) * BwdWork<D, MODE>::PART +
+    __nv_bfloat16* out = MODE == 1 ? p.a.dq : dv ? p.a.dv : p.a.dk;
+    const long long* os = p.a.st[MODE == 1 ? 5 : dv ? 7 : 6];
+    const int head = C::BY_KEY ? w.head : w.head * p.a.group + head_r;
+    const long long row = w.fix0 + (C::BY_KEY ? r : tok_r);
+    __nv_bfloat16* orow = out + row * os[0] + head * os[1];
+    float4* part = reinterpret_cast<float4*>(p.ws.part[bwd_place(MODE)] + (blockIdx.x * 2 + (w.out - 1)) * BwdWork<D, MODE>::PART +
                                              (second ? 128 * C::OUTW : 0)) + r;
 #pragma unroll 1
     for (int c = 0; c < C::OUTW / 32; ++c) {
-      if (!C::KV && (c & 1) != b) continue;
+      if (MODE != 0 && (c & 1) != b) continue;
       uint32_t v[32];
       tmem_ld32(acc + c * 32, v);
       tmem_wait_ld(v);
@@ -579,7 +729,7 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
 
 // ------------------------------------------------------------------ kernel
 template <int D, int MODE>
-__global__ void __launch_bounds__(BwdCfg<D, MODE>::THREADS, 1)
+__global__ void __launch_bounds__(CrossBwdCfg<D, MODE>::THREADS, 1)
     fa_cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_a2,
                         const __grid_constant__ CUtensorMap tm_b1, const __grid_constant__ CUtensorMap tm_b2,
                         const __grid_constant__ CrossBwdParams p) {
@@ -605,10 +755,12 @@ __global__ void __launch_bounds__(BwdCfg<D, MODE>::THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar.s_full(b), 1);
       mbar_init(bar.p_ready(b), 4);
+      if (C::ACC_APART) mbar_init(bar.buf_free(b), 1);
     }
     mbar_init(bar.out_done(), 1);
     mbar_init(bar.out_free(), 8);
     mbar_init(bar.drain(), 1);
+    if (C::ACC_APART) mbar_init(bar.drain_acc(), 1);
     for (int i = 0; i < kBwdSegRing; ++i) {
       mbar_init(bar.seg_full(i), 1);
       mbar_init(bar.seg_empty(i), C::READERS);
@@ -635,7 +787,7 @@ __global__ void __launch_bounds__(BwdCfg<D, MODE>::THREADS, 1)
       },
       1 + BwdWork<D, MODE>::UNIT_COST, *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
   // The kernel that comes first waits for the preparing one; those behind it begin when all of its CTAs have done so.
-  constexpr bool FIRST = MODE == 0 && bwd_short_tiles(D) == 0;
+  constexpr bool FIRST = MODE == 3;
   if (FIRST) pdl_wait();
   pdl_launch_dependents();
   tc_fence_before();
@@ -647,9 +799,14 @@ __global__ void __launch_bounds__(BwdCfg<D, MODE>::THREADS, 1)
   if (warp < 8) {
     cross_bwd_elementwise<D, MODE>(p, bar, gbase, tmem, warp >> 2, warp & 3, lane, g);
   } else if (warp == C::MMA_WARP) {
-    cross_bwd_mma<D, MODE>(p, bar, base, gbase, tmem, g);
+    if constexpr (C::ACC_APART)
+      cross_bwd_sdp<D, MODE>(bar, base, gbase, tmem, g);
+    else
+      cross_bwd_mma<D, MODE>(bar, base, gbase, tmem, g);
   } else if (warp == C::LOAD_WARP) {
     cross_bwd_load<D, MODE>(&tm_a1, &tm_a2, &tm_b1, &tm_b2, p, bar, base, gbase, share, g);
+  } else if constexpr (C::ACC_APART) {
+    cross_bwd_acc<D, MODE>(bar, base, gbase, tmem, g);
   }
 
   __syncwarp();
@@ -754,32 +911,32 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
 
 // ------------------------------------------------------------------ joining
 // Joins the parts of the units that several CTAs held; blocks (c, .) those of the unit that CTA c began.  A warp takes 16
-// columns of 32 rows, a row a lane (a part holds blocks of 4 columns of 128 rows: MODE 0: dK's half, then dV's; MODE 2: tile by tile).
+// columns of 32 rows, a row a lane (a part holds blocks of 4 columns of 128 rows: MODE 0: dK, then dV; MODE 2: tile by tile).
 template <int D, int MODE>
 __device__ __forceinline__ void cross_bwd_join(const CrossBwdParams& p) {
   using C = BwdWork<D, MODE>;
   const CrossArgs& a = p.a;
-  const PlanRecord rec = p.ws.rec[MODE][blockIdx.x];
+  const PlanRecord rec = p.ws.rec[bwd_place(MODE)][blockIdx.x];
   if (rec.b < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool bad;
   const CrossSeq s = cross_seq(a.cb, rec.b, bad);
   const BwdUnits u = bwd_units<D, MODE>(a, s);
-  const int half = rec.qb % C::HALVES, tile0 = rec.qb / C::HALVES % u.fix;
+  const int tile0 = rec.qb % u.fix;
   constexpr size_t stride = 2 * C::PART;  // from one CTA's parts to the next's
-  const float* first = p.ws.part[MODE] + blockIdx.x * stride + stride / 2;
+  const float* first = p.ws.part[bwd_place(MODE)] + blockIdx.x * stride + stride / 2;
   const float* rest = first + stride / 2 - stride;  // part 0 of CTA + i at rest + i * stride
   const int n = rec.more + 1;
-  constexpr int WIDTH = MODE == 0 ? D / C::HALVES : D;          // columns of a block of 128 rows
-  constexpr int BLOCKS = static_cast<int>(C::PART / (128 * WIDTH));  // dK and dV, dQ, or dQ's tiles
-  constexpr int COLS = BLOCKS * WIDTH / 16;
+  constexpr bool BY_KEY = bwd_by_key(MODE);
+  constexpr int BLOCKS = static_cast<int>(C::PART / (128 * D));  // dK and dV, one of them, dQ, or dQ's tiles
+  constexpr int COLS = BLOCKS * D / 16;
   for (int job = blockIdx.y * 4 + warp; job < 4 * COLS; job += gridDim.y * 4) {
     const int r = job % 4 * 32 + lane, c16 = job / 4;
-    const int block = c16 * 16 / WIDTH, c = c16 * 16 % WIDTH;
+    const int block = c16 * 16 / D, c = c16 * 16 % D;
     const int tile = MODE == 2 ? block : tile0;
-    const int tok = MODE == 0 ? r : r / a.group;
-    const int left = MODE == 0 ? s.len - tile * 128 : s.n - tile * bwd_tokens1(a.group);
-    if (tok >= left || (MODE != 0 && tok >= bwd_tokens1(a.group))) continue;
+    const int tok = BY_KEY ? r : r / a.group;
+    const int left = BY_KEY ? s.len - tile * 128 : s.n - tile * bwd_tokens1(a.group);
+    if (tok >= left || (!BY_KEY && tok >= bwd_tokens1(a.group))) continue;
     float4 acc[4] = {};
 #pragma unroll 2
     for (int i = 0; i < n; ++i) {
@@ -794,14 +951,13 @@ __device__ __forceinline__ void cross_bwd_join(const CrossBwdParams& p) {
         acc[k].w += y.w;
       }
     }
-    const bool is_dv = MODE == 0 && block == 1;
+    const bool is_dv = MODE == 3 || (MODE == 0 && block == 1);
     const float f = is_dv ? 1.f : a.scale;
-    const int head = MODE == 0 ? rec.head : rec.head * a.group + r % a.group;
-    const long long row = MODE == 0 ? static_cast<long long>(s.key0) + tile * 128 + r
+    const int head = BY_KEY ? rec.head : rec.head * a.group + r % a.group;
+    const long long row = BY_KEY ? static_cast<long long>(s.key0) + tile * 128 + r
                                     : static_cast<long long>(s.row0) + tile * bwd_tokens1(a.group) + tok;
-    const long long* os = a.st[MODE != 0 ? 5 : is_dv ? 7 : 6];
-    uint4* dst = reinterpret_cast<uint4*>((MODE != 0 ? a.dq : is_dv ? a.dv : a.dk) + row * os[0] + head * os[1] +
-                                          half * WIDTH + c);
+    const long long* os = a.st[!BY_KEY ? 5 : is_dv ? 7 : 6];
+    uint4* dst = reinterpret_cast<uint4*>((!BY_KEY ? a.dq : is_dv ? a.dv : a.dk) + row * os[0] + head * os[1] + c);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       dst[k] = make_uint4(pack_bf16x2(acc[2 * k].x * f, acc[2 * k].y * f), pack_bf16x2(acc[2 * k].z * f, acc[2 * k].w * f),
@@ -814,8 +970,13 @@ __device__ __forceinline__ void cross_bwd_join(const CrossBwdParams& p) {
 template <int D>
 __global__ void __launch_bounds__(128) fa_cross_bwd_join_kernel(const __grid_constant__ CrossBwdParams p, bool longer) {
   pdl_wait();
-  if constexpr (bwd_short_tiles(D) > 0) cross_bwd_join<D, 2>(p);
-  if (longer) {
+  if constexpr (D == 256) {
+    cross_bwd_join<D, 3>(p);
+    cross_bwd_join<D, 4>(p);
+    cross_bwd_join<D, 1>(p);
+  } else {
+    cross_bwd_join<D, 2>(p);
+    if (!longer) return;
     cross_bwd_join<D, 0>(p);
     cross_bwd_join<D, 1>(p);
   }
@@ -832,7 +993,7 @@ int launch_cross_bwd_mode(const CrossBwdParams& p, int grid, const LaunchCtx& ct
   const CrossArgs& a = p.a;
   CUtensorMap mq, mo, mk, mv;
   // Boxes of a group's heads of some tokens, and of one head of some keys.
-  const int tokens = MODE == 0 ? bwd_tokens0<D>(a.group) : bwd_tokens1(a.group), keys = MODE == 0 ? 128 : C::BS;
+  const int tokens = C::BY_KEY ? bwd_tokens0<D>(a.group) : bwd_tokens1(a.group), keys = C::BY_KEY ? 128 : C::BS;
   const long long qd[3] = {D, a.q_heads, a.cb.rows}, kd[3] = {D, a.heads, a.cb.keys};
   auto encode = [&](CUtensorMap* m, const void* t, int i, const long long* dims, int box1, int box2) {
     const long long st[2] = {a.st[i][1], a.st[i][0]};
@@ -841,7 +1002,7 @@ int launch_cross_bwd_mode(const CrossBwdParams& p, int grid, const LaunchCtx& ct
   if (encode(&mq, a.q, 0, qd, a.group, tokens) != 0 || encode(&mo, a.dout, 4, qd, a.group, tokens) != 0 ||
       encode(&mk, a.k, 1, kd, 1, keys) != 0 || encode(&mv, a.v, 2, kd, 1, keys) != 0)
     return -1;
-  return MODE == 0 ? launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mk, mv, mq, mo, p)
+  return C::BY_KEY ? launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mk, mv, mq, mo, p)
                    : launch_dependent(kernel, dim3(grid), C::THREADS, C::SMEM_ALLOC, ctx.stream, mq, mo, mk, mv, p);
 }
 

@@ -331,26 +331,12 @@ struct ShortMma {
 // Three warps issue the products (their instructions, about 10 for each small product, bound a single one: 32 sequences of 17 to 200 rows
 // 138 us with one, 116 with dQ apart): S^T and dP^T; dV and dK (DQ_APART false: and dQ); dQ.  What one warp's products read and
 // another's overwrite is handed over by a barrier (buf_free), for only those of one warp complete in order.
-struct ShortIssuer {
-  const WaitGuard& g;
-  __device__ __forceinline__ bool wait(uint32_t b, uint32_t par) const {
-    const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
-    return __all_sync(0xffffffffu, r);
-  }
-  // All products issued must complete before TMEM is released.
-  __device__ __forceinline__ void finish(uint32_t drain) const {
-    mma_commit_elect(drain);
-    bwd_wait_drain(drain, 0, g);
-    __syncwarp();
-  }
-};
-
 template <int D>
 __device__ __forceinline__ void short_mma_s(const CrossBwdParams& p, const ShortBars<D>& bar, uint32_t base, uint8_t* gbase,
                                             uint32_t tmem, const WaitGuard& g) {
   using C = ShortCfg<D>;
   const ShortMma<D> M(tmem, base);
-  const ShortIssuer is{g};
+  const CrossIssuer is{g};
   const int group = p.a.group, t1 = bwd_tokens1(group);
   ShortItem<D> it;
   int k = 0;
@@ -379,7 +365,7 @@ __device__ __forceinline__ void short_mma_kv(const CrossBwdParams& p, const Shor
                                              uint32_t tmem, const WaitGuard& g) {
   using C = ShortCfg<D>;
   const ShortMma<D> M(tmem, base);
-  const ShortIssuer is{g};
+  const CrossIssuer is{g};
   const int group = p.a.group, t1 = bwd_tokens1(group);
   ShortItem<D> it;
   int k = 0;
@@ -429,7 +415,7 @@ __device__ __forceinline__ void short_mma_dq(const CrossBwdParams& p, const Shor
                                              uint32_t tmem, const WaitGuard& g) {
   using C = ShortCfg<D>;
   const ShortMma<D> M(tmem, base);
-  const ShortIssuer is{g};
+  const CrossIssuer is{g};
   const int group = p.a.group, t1 = bwd_tokens1(group);
   ShortItem<D> it;
   int k = 0;
@@ -812,10 +798,14 @@ int launch_cross_bwd(const CrossArgs& a, const LaunchCtx& ctx) {
   int e = static_cast<int>(cudaGetLastError());
   if (e != 0 || a.cb.rows == 0 || a.cb.keys == 0) return e;  // (zeros are all there is)
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
-  constexpr bool SHORT = bwd_short_tiles(D) > 0;
-  const bool longer = !SHORT || a.cb.rows > bwd_short_tiles(D) * bwd_tokens1(a.group);
-  if constexpr (SHORT) e = launch_cross_bwd_short<D>(p, grid, ctx);
-  if (e == 0 && longer) e = launch_cross_bwd_mode<D, 0>(p, grid, ctx);
+  const bool longer = D == 256 || a.cb.rows > bwd_short_tiles(D) * bwd_tokens1(a.group);
+  if constexpr (D == 256) {
+    e = launch_cross_bwd_mode<D, 3>(p, grid, ctx);
+    if (e == 0) e = launch_cross_bwd_mode<D, 4>(p, grid, ctx);
+  } else {
+    e = launch_cross_bwd_short<D>(p, grid, ctx);
+    if (e == 0 && longer) e = launch_cross_bwd_mode<D, 0>(p, grid, ctx);
+  }
   if (e == 0 && longer) e = launch_cross_bwd_mode<D, 1>(p, grid, ctx);
   if (e == 0) e = launch_dependent(fa_cross_bwd_join_kernel<D>, dim3(grid, 8), 128, 0, ctx.stream, p, longer);
   return e;
