@@ -177,8 +177,10 @@ struct CrossBwdCfg : BwdCfg<D, MODE> {
   // two); with more rows it is not, and the warps' signals to each other cost more (d = 128, 1 to 4 K rows: 1.27 ms with one, 1.41 with two).
   static constexpr bool ACC_APART = D == 256;
   static constexpr int ACC_WARP = C::LOAD_WARP + 1;
-  static constexpr int THREADS = ACC_APART ? 352 : 320;
-  static constexpr int READERS = ACC_APART ? 10 : 9;
+  static constexpr bool DP_APART = ACC_APART && DP;
+  static constexpr int DP_WARP = ACC_WARP + 1;
+  static constexpr int THREADS = DP_APART ? 384 : ACC_APART ? 352 : 320;
+  static constexpr int READERS = THREADS / 32 - 1;
   // A stage's vectors.
   static __device__ __forceinline__ int off_vec(int st) {
     return MODE == 0 ? C::OFF_ST + st * C::STAGE + 2 * C::S_TILE : C::OFF_MISC + 1024 + st * 2 * C::VEC_BYTES;
@@ -188,24 +190,26 @@ struct CrossBwdCfg : BwdCfg<D, MODE> {
 
 template <int D, int MODE>
 struct CrossBwdMma : BwdMma<D, MODE> {
-  using BwdMma<D, MODE>::BwdMma;
-};
-// S = K Q^T, dV (+)= P^T dO.
-template <int D>
-struct CrossBwdMma<D, 3> : BwdMma<D, 3> {
-  using Base = BwdMma<D, 3>;
-  using C = BwdCfg<D, 3>;
+  using Base = BwdMma<D, MODE>;
+  using C = BwdCfg<D, MODE>;
   using Base::BwdMma;
-  __device__ __forceinline__ void sdp(uint32_t st, int b) const {
+  // d = 256, X = 0: S, 1: dP of the tile in stage st, into buffer b.
+  template <int X>
+  __device__ __forceinline__ void first(uint32_t st, int b) const {
     using S0 = typename Base::template SdpSteps<0>;
     using S8 = typename Base::template SdpSteps<8>;
-    const uint32_t d = this->tmem + C::TM_S + b * C::BS, q = this->b1 + st * Base::STAGE_STEP;
-    mma_ss_run<8, S0>(d, this->a1, Base::DESC_HI, q, Base::DESC_HI, Base::IDESC_S, 0u);
-    mma_ss_run<8, S8>(d, this->a1 + Base::a_step(8), Base::DESC_HI, q + Base::b_step(8), Base::DESC_HI, Base::IDESC_S, 1u);
+    const uint32_t d = this->tmem + (X ? C::TM_DP : C::TM_S) + b * C::BS;
+    const uint32_t x = X ? this->a2 : this->a1, y = (X ? this->b2 : this->b1) + st * Base::STAGE_STEP;
+    mma_ss_run<8, S0>(d, x, Base::DESC_HI, y, Base::DESC_HI, Base::IDESC_S, 0u);
+    mma_ss_run<8, S8>(d, x + Base::a_step(8), Base::DESC_HI, y + Base::b_step(8), Base::DESC_HI, Base::IDESC_S, 1u);
   }
-  __device__ __forceinline__ void accumulate(uint32_t st, int b, bool acc, int) const {
-    mma_ts_run<C::BS / 16, typename Base::AccSteps>(this->tmem + C::TM_OUT, this->tmem + C::TM_S + b * C::BS,
-                                                    this->b2_mn + st * Base::STAGE_STEP, Base::DESC_HI, Base::IDESC_O, acc ? 1u : 0u);
+  // MODE 0: dK (+)= dS^T Q, dV (+)= P^T dO; 1: dQ (+)= dS K; 3: dV; 4: dK.
+  __device__ __forceinline__ void add(uint32_t st, int b, bool acc) const {
+    if constexpr (MODE == 3)
+      mma_ts_run<C::BS / 16, typename Base::AccSteps>(this->tmem + C::TM_OUT, this->tmem + C::TM_S + b * C::BS,
+                                                      this->b2_mn + st * Base::STAGE_STEP, Base::DESC_HI, Base::IDESC_O, acc ? 1u : 0u);
+    else
+      this->accumulate(st, b, acc, 0);
   }
 };
 
@@ -217,7 +221,8 @@ struct CrossBwdBars : BwdBars<D, MODE> {
   // The accumulations that read P and dS in buffer b are complete.
   __device__ __forceinline__ uint32_t buf_free(int b) const { return this->b0 + 240 + 8u * b; }
   __device__ __forceinline__ uint32_t drain_acc() const { return this->b0 + 232; }
-  static_assert(Base::COUNT * 8 <= 232, "barrier area");
+  __device__ __forceinline__ uint32_t drain_dp() const { return this->b0 + 224; }
+  static_assert(Base::COUNT * 8 <= 224, "barrier area");
 };
 
 // The units of a sequence.
@@ -487,7 +492,7 @@ __device__ __forceinline__ void cross_bwd_mma(const CrossBwdBars<D, MODE>& bar, 
         if (!(ok = is.wait(bar.out_free(), (k - 1) & 1))) break;
         tc_fence_after();
       }
-      M.accumulate(stage_of(t), b, t > 0, 0);
+      M.add(stage_of(t), b, t > 0);
       mma_commit_elect(bar.st_empty(stage_of(t)));
       if (t + 2 < n) {
         if (!(ok = acquire(t + 2))) break;
@@ -503,8 +508,8 @@ __device__ __forceinline__ void cross_bwd_mma(const CrossBwdBars<D, MODE>& bar, 
   is.finish(bar.drain());
 }
 
-// ACC_APART: S and dP, segment by segment.
-template <int D, int MODE>
+// ACC_APART: S (X = 0) or dP, segment by segment.
+template <int D, int MODE, int X>
 __device__ __forceinline__ void cross_bwd_sdp(const CrossBwdBars<D, MODE>& bar, uint32_t base, uint8_t* gbase, uint32_t tmem,
                                               const WaitGuard& g) {
   using C = CrossBwdCfg<D, MODE>;
@@ -524,12 +529,12 @@ __device__ __forceinline__ void cross_bwd_sdp(const CrossBwdBars<D, MODE>& bar, 
       if (u > 0 && !(ok = is.wait(bar.buf_free(b), (u - 1) & 1))) break;
       ++u;
       tc_fence_after();
-      M.sdp(pos % C::NST, b);
+      M.template first<X>(pos % C::NST, b);
       mma_commit_elect(bar.s_full(b));
       if (t == w.n - 1) mma_commit_elect(bar.fix_empty());
     }
   }
-  is.finish(bar.drain());
+  is.finish(X ? bar.drain_dp() : bar.drain());
 }
 
 // The accumulations.
@@ -552,7 +557,7 @@ __device__ __forceinline__ void cross_bwd_acc(const CrossBwdBars<D, MODE>& bar, 
       ++pr;
       if (t == 0 && k > 0 && !(ok = is.wait(bar.out_free(), (k - 1) & 1))) break;
       tc_fence_after();
-      M.accumulate(pos % C::NST, b, t > 0, 0);
+      M.add(pos % C::NST, b, t > 0);
       mma_commit_elect(bar.buf_free(b));
       mma_commit_elect(bar.st_empty(pos % C::NST));
     }
@@ -747,13 +752,13 @@ __global__ void __launch_bounds__(CrossBwdCfg<D, MODE>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(bar.fix_full(), 1);
-    mbar_init(bar.fix_empty(), 1);
+    mbar_init(bar.fix_empty(), C::DP_APART ? 2 : 1);
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(bar.st_full(i), 1);
       mbar_init(bar.st_empty(i), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(bar.s_full(b), 1);
+      mbar_init(bar.s_full(b), C::DP_APART ? 2 : 1);
       mbar_init(bar.p_ready(b), 4);
       if (C::ACC_APART) mbar_init(bar.buf_free(b), 1);
     }
@@ -761,6 +766,7 @@ __global__ void __launch_bounds__(CrossBwdCfg<D, MODE>::THREADS, 1)
     mbar_init(bar.out_free(), 8);
     mbar_init(bar.drain(), 1);
     if (C::ACC_APART) mbar_init(bar.drain_acc(), 1);
+    if (C::DP_APART) mbar_init(bar.drain_dp(), 1);
     for (int i = 0; i < kBwdSegRing; ++i) {
       mbar_init(bar.seg_full(i), 1);
       mbar_init(bar.seg_empty(i), C::READERS);
@@ -800,13 +806,15 @@ __global__ void __launch_bounds__(CrossBwdCfg<D, MODE>::THREADS, 1)
     cross_bwd_elementwise<D, MODE>(p, bar, gbase, tmem, warp >> 2, warp & 3, lane, g);
   } else if (warp == C::MMA_WARP) {
     if constexpr (C::ACC_APART)
-      cross_bwd_sdp<D, MODE>(bar, base, gbase, tmem, g);
+      cross_bwd_sdp<D, MODE, 0>(bar, base, gbase, tmem, g);
     else
       cross_bwd_mma<D, MODE>(bar, base, gbase, tmem, g);
   } else if (warp == C::LOAD_WARP) {
     cross_bwd_load<D, MODE>(&tm_a1, &tm_a2, &tm_b1, &tm_b2, p, bar, base, gbase, share, g);
-  } else if constexpr (C::ACC_APART) {
-    cross_bwd_acc<D, MODE>(bar, base, gbase, tmem, g);
+  } else if (C::ACC_APART && warp == C::ACC_WARP) {
+    if constexpr (C::ACC_APART) cross_bwd_acc<D, MODE>(bar, base, gbase, tmem, g);
+  } else {
+    if constexpr (C::DP_APART) cross_bwd_sdp<D, MODE, 1>(bar, base, gbase, tmem, g);
   }
 
   __syncwarp();
@@ -966,20 +974,16 @@ __device__ __forceinline__ void cross_bwd_join(const CrossBwdParams& p) {
   }
 }
 
-// The parts of all kernels, or (`longer` false) of MODE 2 alone.
+// The parts of the kernels, one to blockIdx.z (the first may be the only one).
 template <int D>
-__global__ void __launch_bounds__(128) fa_cross_bwd_join_kernel(const __grid_constant__ CrossBwdParams p, bool longer) {
+__global__ void __launch_bounds__(128) fa_cross_bwd_join_kernel(const __grid_constant__ CrossBwdParams p) {
   pdl_wait();
-  if constexpr (D == 256) {
-    cross_bwd_join<D, 3>(p);
-    cross_bwd_join<D, 4>(p);
+  if (blockIdx.z == 0)
+    cross_bwd_join<D, D == 256 ? 3 : 2>(p);
+  else if (blockIdx.z == 1)
+    cross_bwd_join<D, D == 256 ? 4 : 0>(p);
+  else
     cross_bwd_join<D, 1>(p);
-  } else {
-    cross_bwd_join<D, 2>(p);
-    if (!longer) return;
-    cross_bwd_join<D, 0>(p);
-    cross_bwd_join<D, 1>(p);
-  }
 }
 
 // ------------------------------------------------------------------ launch

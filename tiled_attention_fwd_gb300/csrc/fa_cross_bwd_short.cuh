@@ -807,7 +807,7 @@ int launch_cross_bwd(const CrossArgs& a, const LaunchCtx& ctx) {
     if (e == 0 && longer) e = launch_cross_bwd_mode<D, 0>(p, grid, ctx);
   }
   if (e == 0 && longer) e = launch_cross_bwd_mode<D, 1>(p, grid, ctx);
-  if (e == 0) e = launch_dependent(fa_cross_bwd_join_kernel<D>, dim3(grid, 8), 128, 0, ctx.stream, p, longer);
+  if (e == 0) e = launch_dependent(fa_cross_bwd_join_kernel<D>, dim3(grid, 8, longer ? 3 : 1), 128, 0, ctx.stream, p);
   return e;
 }
 
