@@ -750,6 +750,22 @@ __global__ void __launch_bounds__(CrossBwdCfg<D, MODE>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::OFF_TMEM_SLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::OFF_ABORT);
 
+  // The kernel that comes first waits for the preparing one; those behind it begin when all of its CTAs have done so.
+  constexpr bool FIRST = MODE == 3;
+  const PlanShare share = plan_share<C::THREADS>(
+      p.a.cb.B, gridDim.x, blockIdx.x,
+      [&](int b) -> long long {
+        bool bad;
+        const BwdUnits u = bwd_units<D, MODE>(p.a, cross_seq(p.a.cb, b, bad));
+        return u.units == 0 ? 0ll : static_cast<long long>(u.units) * u.template length<BwdWork<D, MODE>::UNIT_COST>();
+      },
+      1 + BwdWork<D, MODE>::UNIT_COST, *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
+  if (D < 256 && share.start >= share.end) {  // (where all sequences are short: out of the way at once)
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) p.ws.rec[bwd_place(MODE)][blockIdx.x].b = -1;
+    pdl_wait();
+    return;
+  }
   if (threadIdx.x == 0) {
     mbar_init(bar.fix_full(), 1);
     mbar_init(bar.fix_empty(), C::DP_APART ? 2 : 1);
@@ -784,16 +800,6 @@ __global__ void __launch_bounds__(CrossBwdCfg<D, MODE>::THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
     tmem_relinquish();
   }
-  const PlanShare share = plan_share<C::THREADS>(
-      p.a.cb.B, gridDim.x, blockIdx.x,
-      [&](int b) -> long long {
-        bool bad;
-        const BwdUnits u = bwd_units<D, MODE>(p.a, cross_seq(p.a.cb, b, bad));
-        return u.units == 0 ? 0ll : static_cast<long long>(u.units) * u.template length<BwdWork<D, MODE>::UNIT_COST>();
-      },
-      1 + BwdWork<D, MODE>::UNIT_COST, *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
-  // The kernel that comes first waits for the preparing one; those behind it begin when all of its CTAs have done so.
-  constexpr bool FIRST = MODE == 3;
   if (FIRST) pdl_wait();
   pdl_launch_dependents();
   tc_fence_before();
@@ -828,12 +834,50 @@ __global__ void __launch_bounds__(CrossBwdCfg<D, MODE>::THREADS, 1)
 }
 
 // ------------------------------------------------------------------ preparing
-// -L log2e and -D of every row into the vectors (-inf and 0 behind a sequence's last), and
-// zeros where no product is made: places behind a sequence's keys, keys of sequences without rows, rows without keys.
+// -L log2e and -D of every row into the vectors (-inf and 0 behind a sequence's last), and zeros.
 constexpr int kPrepThreads = 256;
 
+// Zeros where no product is made: dK and dV of places behind a sequence's keys and of sequences without rows, dQ of rows without
+// keys.  Several blocks to a sequence, a warp to a row.
 template <int D>
-__global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __grid_constant__ CrossBwdParams p) {
+struct BwdZeros {
+  static constexpr int CPR = D / 8;
+  int per, x, grid, warp, warps;  // blocks of a sequence; this block's next (sequence, share); ..
+  int at = 0, to = 0, q_to = 0;   // the sequence's next row of this warp's; behind its places; behind its rows without keys
+  CrossSeq s;
+  __device__ __forceinline__ BwdZeros(const CrossArgs& a, int block, int grid_, int warp_, int warps_)
+      : per(max(grid_ / a.cb.B, 1)), x(block), grid(grid_), warp(warp_), warps(warps_) {}
+  // One row of dK and dV, or of dQ; false behind the last.
+  __device__ __forceinline__ bool row(const CrossBwdParams& p) {
+    const CrossArgs& a = p.a;
+    const int lane = threadIdx.x & 31;
+    if (at >= max(to, q_to)) {
+      if (x / per >= a.cb.B) return false;
+      bool bad;
+      s = cross_seq(a.cb, x / per, bad);
+      at = x % per * warps + warp + (s.n > 0 ? s.len : 0);
+      to = s.places;
+      q_to = s.len == 0 ? s.n : 0;
+      x += grid;
+      return true;
+    }
+    auto clear = [&](__nv_bfloat16* out, const long long* st, int row0, int heads) {
+      for (int c = lane; c < heads * CPR; c += 32)
+        *reinterpret_cast<uint4*>(out + (static_cast<long long>(row0) + at) * st[0] + c / CPR * st[1] + c % CPR * 8) = make_uint4(0, 0, 0, 0);
+    };
+    if (at < to) {
+      clear(a.dk, a.st[6], s.key0, a.heads);
+      clear(a.dv, a.st[7], s.key0, a.heads);
+    }
+    if (at < q_to) clear(a.dq, a.st[5], s.row0, a.q_heads);
+    at += per * warps;
+    return true;
+  }
+};
+
+// (`zeros`: the kernel for short sequences, which writes them else, is not launched behind this one.)
+template <int D>
+__global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __grid_constant__ CrossBwdParams p, bool zeros) {
   constexpr int BS = BwdCfg<D, 0>::BS;
   constexpr int CPR = D / 8;     // 16-byte chunks per row
   constexpr int RPW = 32 / CPR;  // rows per warp step
@@ -899,21 +943,10 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
       }
     }
   }
-  // Zeros: several blocks to a sequence, a warp to a row.
-  const int per = gridDim.x / a.cb.B > 0 ? gridDim.x / a.cb.B : 1;
-  for (int x = blockIdx.x; x / per < a.cb.B; x += gridDim.x) {
-    const int b = x / per, part = x % per;
-    bool bad;
-    const CrossSeq s = cross_seq(a.cb, b, bad);
-    auto fill = [&](__nv_bfloat16* out, const long long* st, int row0, int from, int to, int heads) {
-      for (int row = from + part * WARPS + warp; row < to; row += per * WARPS)
-        for (int c = lane; c < heads * CPR; c += 32)
-          *reinterpret_cast<uint4*>(out + (static_cast<long long>(row0) + row) * st[0] + c / CPR * st[1] + c % CPR * 8) = make_uint4(0, 0, 0, 0);
-    };
-    const int from = s.n > 0 ? s.len : 0;
-    fill(a.dk, a.st[6], s.key0, from, s.places, a.heads);
-    fill(a.dv, a.st[7], s.key0, from, s.places, a.heads);
-    if (s.len == 0) fill(a.dq, a.st[5], s.row0, 0, s.n, a.q_heads);
+  if (zeros) {
+    BwdZeros<D> z(a, blockIdx.x, gridDim.x, warp, WARPS);
+    while (z.row(p)) {
+    }
   }
 }
 

@@ -567,6 +567,10 @@ __device__ __forceinline__ void short_output(const CrossBwdParams& p, const Shor
   const int tok_r = r / group, head_r = r - tok_r * group;
   uint32_t tiles = 0;  // key tiles read out
   bool ok = true;
+  // The zeros of dK and dV, a few rows behind each key tile: they cost nothing here (written before, 32 padded sequences of 100 to
+  // 1024 places: 9 us).
+  BwdZeros<D> zeros(p.a, blockIdx.x, gridDim.x, quarter, 4);
+  bool more = true;
   // 32 columns of TMEM.
   auto chunk = [&](uint32_t at, uint32_t (&v)[32]) {
     tmem_ld32(tmem + lane_off + at, v);
@@ -637,6 +641,7 @@ __device__ __forceinline__ void short_output(const CrossBwdParams& p, const Shor
       warp_arrive(bar.kv_free());
       if constexpr (BOTH) put(yk, mine ? dk : nullptr);
       put(yv, mine ? dv : nullptr);
+      for (int i = 0; i < 8 && more; ++i) more = zeros.row(p);
     }
     if (!ok || !(ok = warp_wait_bar(bar.dq_done(), k & 1, g, kStatusTimeoutSoftmax))) break;
     tc_fence_after();
@@ -668,6 +673,7 @@ __device__ __forceinline__ void short_output(const CrossBwdParams& p, const Shor
     tc_fence_before();
     warp_arrive(bar.dq_free());
   }
+  while (more) more = zeros.row(p);
 }
 
 // ------------------------------------------------------------------ kernel
@@ -794,9 +800,10 @@ int launch_cross_bwd(const CrossArgs& a, const LaunchCtx& ctx) {
   p.limit_ns = ctx.limit_ns;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.tiles = bwd_tiles<D>(a.cb.rows, a.cb.B, a.group);
-  fa_cross_prep_kernel<D><<<ctx.num_sms * 8, kPrepThreads, 0, ctx.stream>>>(p);
+  const bool products = a.cb.rows > 0 && a.cb.keys > 0;
+  fa_cross_prep_kernel<D><<<ctx.num_sms * 8, kPrepThreads, 0, ctx.stream>>>(p, D == 256 || !products);
   int e = static_cast<int>(cudaGetLastError());
-  if (e != 0 || a.cb.rows == 0 || a.cb.keys == 0) return e;  // (zeros are all there is)
+  if (e != 0 || !products) return e;  // (zeros are all there is)
   const int grid = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
   const bool longer = D == 256 || a.cb.rows > bwd_short_tiles(D) * bwd_tokens1(a.group);
   if constexpr (D == 256) {
