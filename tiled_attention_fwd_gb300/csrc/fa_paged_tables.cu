@@ -7,6 +7,7 @@
 // every CTA makes the sums for itself (they are short), the cluster's barrier
 // stands between reading the old lengths and writing the new ones, and the
 // CTAs share out pages and rows.  No atomics on results: the order is fixed.
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/fa_gb300.h"
@@ -18,6 +19,7 @@ namespace {
 
 constexpr int kTableThreads = 1024;
 constexpr int kTableWarps = kTableThreads / 32;
+constexpr int kTableCtas = 16;  // of the cluster where the device takes one of that many, else half of them
 
 __device__ __forceinline__ uint32_t cluster_ctas() {
   uint32_t r;
@@ -127,8 +129,9 @@ __global__ void __launch_bounds__(kTableThreads, 1) fa_paged_extend_kernel(const
     const int row = static_cast<int>(cu0 + r[0] - (served ? n : 0));
     s_row[threadIdx.x] = row;
     s_old[threadIdx.x] = old;
-    s_top[threadIdx.x] = static_cast<int>(need0 + x[0]) - need;
+    s_top[threadIdx.x] = static_cast<int>(min(need0 + x[0] - need, static_cast<long long>(a.num_pages)));  // (those not served: behind all)
     if (threadIdx.x == kTableThreads - 1) s_row[kTableThreads] = static_cast<int>(cu0 + rsum[0]);
+    const long long need_first = need0;
     need0 += sum[0];
     rows0 += sum[1];
     cu0 += rsum[0];
@@ -137,19 +140,16 @@ __global__ void __launch_bounds__(kTableThreads, 1) fa_paged_extend_kernel(const
       a.cu_rows[b] = row;
       if (served && n > 0) a.lens[b] = static_cast<int>(want);
     }
-    // New pages into the table: a warp to a sequence.
-    const int here = min(kTableThreads, a.B - b0);
-    for (int i = rank * kTableWarps + warp; i < here; i += ctas * kTableWarps) {
-      const int rows = s_row[i + 1] - s_row[i];
-      if (rows == 0) continue;
-      const int held = pages_of(s_old[i], a.ps_log2);
-      const int more = pages_of(static_cast<long long>(s_old[i]) + rows, a.ps_log2) - held;
-      int* to = a.table + static_cast<long long>(b0 + i) * a.stride + held;
-      for (int k = lane; k < more; k += 32) {
-        const int page = page_at(s_top[i] + k);
-        bad = bad || page < 0;
-        to[k] = page;
-      }
+    // New pages into the table, one a thread: the served sequences' needs lie one behind another from the top of the stack on.
+    const long long pages_end = min(need0, static_cast<long long>(s_taken));
+    for (long long t = need_first + rank * kTableThreads + threadIdx.x; t < pages_end; t += ctas * kTableThreads) {
+      int i = 0;  // the sequence that takes it: the last one whose pages begin there or before
+#pragma unroll
+      for (int step = kTableThreads / 2; step > 0; step >>= 1)
+        if (s_top[i + step] <= t) i += step;
+      const int page = page_at(static_cast<int>(t));
+      bad = bad || page < 0;
+      a.table[static_cast<long long>(b0 + i) * a.stride + pages_of(s_old[i], a.ps_log2) + (static_cast<int>(t) - s_top[i])] = page;
     }
     // Slots and positions, four rows a thread (both arrays are 16-byte aligned, so a group of four is stored whole).
     const int first = s_row[0], last = s_row[kTableThreads];
@@ -163,6 +163,15 @@ __global__ void __launch_bounds__(kTableThreads, 1) fa_paged_extend_kernel(const
         if (s_row[i + step] <= from) i += step;
       long long slot[4];
       int pos[4];
+      const int mask = (1 << a.ps_log2) - 1;
+      // The page of position x of sequence i, -1 where it is none of the cache's.
+      auto page_of = [&](int x) -> int {
+        const int k = x >> a.ps_log2, held = pages_of(s_old[i], a.ps_log2);
+        int page = k < held ? a.table[static_cast<long long>(b0 + i) * a.stride + k] : page_at(s_top[i] + k - held);
+        page = page < a.num_pages ? page : -1;
+        bad = bad || page < 0;
+        return page;
+      };
       int k_last = -1, i_last = -1, page = -1;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -174,15 +183,12 @@ __global__ void __launch_bounds__(kTableThreads, 1) fa_paged_extend_kernel(const
         pos[e] = s_old[i] + (t - s_row[i]);
         const int k = pos[e] >> a.ps_log2;
         if (k != k_last || i != i_last) {
-          const int held = pages_of(s_old[i], a.ps_log2);
-          page = k < held ? a.table[static_cast<long long>(b0 + i) * a.stride + k] : page_at(s_top[i] + k - held);
-          page = page < a.num_pages ? page : -1;
-          bad = bad || page < 0;
+          page = page_of(pos[e]);
           k_last = k;
           i_last = i;
         }
         if (page >= 0)
-          slot[e] = (static_cast<long long>(page) << a.ps_log2) + (pos[e] & ((1 << a.ps_log2) - 1));
+          slot[e] = (static_cast<long long>(page) << a.ps_log2) + (pos[e] & mask);
       }
       if (t0 >= first && t0 + 4 <= last) {
         if (a.slots) {
@@ -224,27 +230,41 @@ __global__ void __launch_bounds__(kTableThreads, 1) fa_paged_release_kernel(cons
   auto valid = [&](int page) { return page >= 0 && page < a.num_pages; };
   long long base = free;
   for (long long u0 = 0; u0 < units; u0 += kTableThreads) {
-    for (int i = rank * kTableWarps + warp; i < kTableThreads; i += ctas * kTableWarps) {
-      int count = 0;
-      int2 part = make_int2(0, 0);
-      if (u0 + i < units) {
-        const int b = static_cast<int>((u0 + i) >> a.parts_log2), p = i & ((1 << a.parts_log2) - 1);
-        if (a.done[b]) {
-          const long long len = a.lens[b], most = static_cast<long long>(a.max_pages) << a.ps_log2;
-          bad = bad || len < 0 || len > most;
-          const int held = pages_of(min(max(len, 0ll), most), a.ps_log2);
-          const int each = (held + (1 << a.parts_log2) - 1) >> a.parts_log2;
-          part = make_int2(min(p * each, held), min((p + 1) * each, held));
-          const int* from = a.table + b * a.stride;
-          int mine = 0;
-#pragma unroll 8
-          for (int k = part.x + lane; k < part.y; k += 32) mine += valid(from[k]) ? 1 : 0;
-          count = __reduce_add_sync(0xffffffffu, mine);
-          bad = bad || count != part.y - part.x;
-        }
+    // (A warp's parts together, so that their loads are on their way together.)
+    constexpr int PARTS = kTableThreads / (kTableCtas * kTableWarps);
+    for (int i0 = rank * kTableWarps + warp; i0 < kTableThreads; i0 += PARTS * ctas * kTableWarps) {
+      bool on[PARTS];
+      int2 part[PARTS];
+      int count[PARTS];
+      long long len[PARTS];
+#pragma unroll
+      for (int e = 0; e < PARTS; ++e) {
+        const long long u = u0 + i0 + e * ctas * kTableWarps;
+        on[e] = u < units && a.done[u >> a.parts_log2];
+        len[e] = u < units ? a.lens[u >> a.parts_log2] : 0;
       }
-      if (lane == 0) s_part[i] = part;
-      if (lane < ctas) st_cluster(mapa_shared(smem_u32(&s_count[i]), lane), count);
+#pragma unroll
+      for (int e = 0; e < PARTS; ++e) {
+        const long long u = u0 + i0 + e * ctas * kTableWarps;
+        const int p = static_cast<int>(u) & ((1 << a.parts_log2) - 1);
+        const long long most = static_cast<long long>(a.max_pages) << a.ps_log2;
+        bad = bad || (on[e] && (len[e] < 0 || len[e] > most));
+        const int held = on[e] ? pages_of(min(max(len[e], 0ll), most), a.ps_log2) : 0;
+        const int each = (held + (1 << a.parts_log2) - 1) >> a.parts_log2;
+        part[e] = make_int2(min(p * each, held), min((p + 1) * each, held));
+        const int* from = a.table + (u >> a.parts_log2) * a.stride;
+        int mine = 0;
+#pragma unroll 8
+        for (int k = part[e].x + lane; k < part[e].y; k += 32) mine += valid(from[k]) ? 1 : 0;
+        count[e] = __reduce_add_sync(0xffffffffu, mine);
+        bad = bad || count[e] != part[e].y - part[e].x;
+      }
+#pragma unroll
+      for (int e = 0; e < PARTS; ++e) {
+        const int i = i0 + e * ctas * kTableWarps;
+        if (lane == 0) s_part[i] = part[e];
+        if (lane < ctas) st_cluster(mapa_shared(smem_u32(&s_count[i]), lane), count[e]);
+      }
     }
     cluster_sync_all();
     long long x[1] = {s_count[threadIdx.x]}, sum[1];
@@ -282,18 +302,37 @@ __global__ void __launch_bounds__(kTableThreads, 1) fa_paged_release_kernel(cons
   if (bad) atomicOr(a.status, kBadBatchBit);
 }
 
-int launch_cluster(void (*kernel)(const TableArgs), const TableArgs& a, int ctas, cudaStream_t stream) {
+// One cluster of kTableCtas CTAs: 16 is more than every device has to take, so it is asked once (`fit`: 0 not asked, else the
+// CTAs).  With 16 (8, 1) CTAs 200 thousand slots took 12 (17, 85) us, the pages of 128 long sequences 11 (17, 89), a step's 256 rows 6.7
+// with any: a launch, a barrier and the dependent reads of lengths, stack and table.
+int launch_cluster(void (*kernel)(const TableArgs), const TableArgs& a, std::atomic<int> (&fit)[64], cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kTableThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  auto ctas = [&](int n) {
+    cfg.gridDim = dim3(n);
+    attr[0].val.clusterDim.x = n;
+  };
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  std::atomic<int>& known = fit[dev & 63];
+  int n = known.load(std::memory_order_relaxed);
+  if (n == 0) {
+    ctas(kTableCtas);
+    int clusters = 0;
+    const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0;
+    if (!ok) cudaGetLastError();  // (an answer, not an error)
+    n = ok ? kTableCtas : kTableCtas / 2;
+    known.store(n, std::memory_order_relaxed);
+  }
+  ctas(n);
   return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -346,7 +385,8 @@ int fa_paged_extend(const fa_page_pool* pool, int* page_table, long long table_s
   a.positions = positions;
   a.rows = rows;
   a.status = ctx.status;
-  return fa::launch_cluster(fa::fa_paged_extend_kernel, a, 8, ctx.stream);
+  static std::atomic<int> fit[64];
+  return fa::launch_cluster(fa::fa_paged_extend_kernel, a, fit, ctx.stream);
 }
 
 int fa_paged_release(const fa_page_pool* pool, int* page_table, long long table_stride, int max_pages, int* kv_lens,
@@ -360,10 +400,12 @@ int fa_paged_release(const fa_page_pool* pool, int* page_table, long long table_
   if (rc != FA_OK) return rc;
   a.done = done;
   a.status = ctx.status;
-  // Long rows of few sequences are shared out until every warp of the cluster has some.
-  while (a.parts_log2 < 5 && (static_cast<long long>(B) << a.parts_log2) < 8 * fa::kTableWarps && (max_pages >> a.parts_log2) > 64)
+  // Long rows of few sequences are shared out until every warp of the cluster has two parts (the pages of 17 of 256 sequences of up to
+  // 512: 6.3 us; with one part a warp 7.2).
+  while (a.parts_log2 < 10 && (static_cast<long long>(B) << a.parts_log2) < 32 * fa::kTableWarps && (max_pages >> a.parts_log2) > 64)
     ++a.parts_log2;
-  return fa::launch_cluster(fa::fa_paged_release_kernel, a, 8, ctx.stream);
+  static std::atomic<int> fit[64];
+  return fa::launch_cluster(fa::fa_paged_release_kernel, a, fit, ctx.stream);
 }
 
 }  // extern "C"
