@@ -184,3 +184,25 @@ def test_pages_taken_and_given_back_are_a_permutation():
         if rng.random() < 0.6:
             count, fine = tables.release(table, lens, stack, count, (rng.random(4) < 0.5).tolist(), ps)
             assert fine
+
+
+def test_cross_kernels_fit_their_registers():
+    """The chunk kernels' register split (d <= 128) is sized for exactly 128 a thread at launch; the gradients' kernels hold a
+    tile's S and dP in registers (the one-pass kernel with 16 warps at the limit of 128)."""
+    from tiled_attention_fwd_gb300 import build
+
+    rep = build.ptxas_report({f"fa_cross_{k}_d{d}.cu" for k in ("few", "chunk", "bwd") for d in (32, 64, 128, 256)})
+    pick = lambda name: {k: r for k, r in rep.items() if name in k}
+    chunk, few, short = pick("fa_paged_chunk_kernel"), pick("fa_paged_few_kernel"), pick("fa_cross_bwd_short_kernel")
+    long, prep, join = pick("19fa_cross_bwd_kernel"), pick("fa_cross_prep_kernel"), pick("fa_cross_bwd_join_kernel")
+    # dK and dV, dQ; d = 256: dV, dK, dQ.
+    assert (len(chunk), len(few), len(short), len(long), len(prep), len(join)) == (4, 11, 3, 9, 4, 4)
+    for name, r in chunk.items():
+        if "ILi256E" in name:
+            assert r["registers"] <= 168, (name, r)
+        else:
+            assert r["registers"] == 128, (name, r)
+    for name, r in short.items():
+        assert r["registers"] <= 128 and r["spill_stores"] <= 16, (name, r)
+    for name, r in {**few, **long, **prep, **join}.items():
+        assert r["spill_stores"] == 0, (name, r)

@@ -1,5 +1,5 @@
-"""The barriers of the one-pass gradient kernel (csrc/fa_cross_bwd_short.cuh), stepped on the CPU: its warps as coroutines that
-run in any order, the tensor core's completions late but in the order of each issuing warp.  A wait is for a phase's
+"""The barriers of cross attention's gradient kernels (csrc/fa_cross_bwd_short.cuh, csrc/fa_cross_bwd.cuh), stepped on the CPU: their
+warps as coroutines that run in any order, the tensor core's completions late but in the order of each issuing warp.  A wait is for a phase's
 parity, so it must never be made two phases early or late: every wait that passes is checked to be for the phase meant, and
 no order may leave every warp waiting."""
 import random
@@ -45,6 +45,32 @@ class Items:
         self.slot0 += -(-self.items // self.subs)
         self.k += 1
         return False
+
+
+def schedule(rng, bars, commits, warps):
+    """Steps the warps in a random order until all have ended."""
+    waits = {}
+
+    def step(name):
+        try:
+            waits[name] = next(warps[name])
+        except StopIteration:
+            del warps[name]
+            waits.pop(name, None)
+
+    for name in list(warps):
+        step(name)
+    while warps:
+        pending = [q for q in commits.values() if q]
+        ready = [w for w in warps if (bars[waits[w][0]].phase & 1) != (waits[w][1] & 1)]
+        assert ready or pending, {w: waits[w] for w in warps}  # a deadlock
+        if pending and (not ready or rng.random() < 0.3):
+            bars[rng.choice(pending).pop(0)].arrive()
+            continue
+        name = rng.choice(ready)
+        bar, phase = waits[name]
+        assert bars[bar].phase == phase + 1, (name, bar, phase, bars[bar].phase)
+        step(name)
 
 
 def run(units, stages, slots, subs, seed):
@@ -182,28 +208,7 @@ def run(units, stages, slots, subs, seed):
     warps = {"load": load(), "s": mma_s(), "kv": mma_kv(), "ew0": elementwise(0), "ew1": elementwise(1), "out": output()}
     if apart:
         warps["dq"] = mma_dq()
-    waits = {}
-
-    def step(name):
-        try:
-            waits[name] = next(warps[name])
-        except StopIteration:
-            del warps[name]
-            waits.pop(name, None)
-
-    for name in list(warps):
-        step(name)
-    while warps:
-        pending = [q for q in commits.values() if q]
-        ready = [w for w in warps if (bars[waits[w][0]].phase & 1) != (waits[w][1] & 1)]
-        assert ready or pending, {w: waits[w] for w in warps}  # a deadlock
-        if pending and (not ready or rng.random() < 0.3):
-            bars[rng.choice(pending).pop(0)].arrive()
-            continue
-        name = rng.choice(ready)
-        bar, phase = waits[name]
-        assert bars[bar].phase == phase + 1, (name, bar, phase, bars[bar].phase)
-        step(name)
+    schedule(rng, bars, commits, warps)
 
 
 # (stages, slots, items to a row tile, row tiles of a unit at most) at d = 32, 64, 128, and other rings.
@@ -213,3 +218,111 @@ def test_every_order_ends_and_no_wait_is_for_another_phase(stages, slots, subs, 
         rng = random.Random(seed)
         units = [(rng.randint(1, 4), [128] * rng.randint(0, most - 1) + [rng.randint(1, 128)]) for _ in range(rng.randint(0, 12))]
         run(units, stages, slots, subs, seed)
+
+
+def run_long(segments, stages, apart, dp, seed):
+    """fa_cross_bwd_kernel over segments of so many streamed tiles: one issuing warp, or (d = 256) the accumulations apart and
+    (`dp`) dP, too."""
+    rng = random.Random(seed)
+    names = ["fix_full", "out_done", "drain"] + [(x, b) for x in ("p", "free") for b in range(2)]
+    bars = {x: Barrier(1) for x in names + [("st_full", i) for i in range(stages)] + [("st_empty", i) for i in range(stages)]}
+    first = 2 if dp else 1  # warps whose products make a tile's S and dP
+    bars.update({"fix_empty": Barrier(first), ("s", 0): Barrier(first), ("s", 1): Barrier(first), "out_free": Barrier(2)})
+    for i in range(RING):
+        bars[("seg_full", i)], bars[("seg_empty", i)] = Barrier(1), Barrier(2 + first + apart)
+    ring = [None] * RING
+    commits = {0: [], 1: [], "acc": []}
+
+    def load():
+        pos = 0
+        for k, n in enumerate(segments + [None]):
+            yield ("seg_empty", k % RING), k // RING - 1
+            ring[k % RING] = n
+            bars[("seg_full", k % RING)].arrive()
+            if n is None:
+                return
+            yield "fix_empty", k - 1
+            bars["fix_full"].arrive()
+            for _ in range(n):
+                yield ("st_empty", pos % stages), pos // stages - 1
+                bars[("st_full", pos % stages)].arrive()
+                pos += 1
+
+    def segment(k):
+        yield ("seg_full", k % RING), k // RING
+        bars[("seg_empty", k % RING)].arrive()
+        return ring[k % RING]
+
+    def one():
+        pos, ready = 0, [0, 0]
+        queue, k = commits["acc"], 0
+        while (n := (yield from segment(k))) is not None:
+            yield "fix_full", k
+            for t in range(-2, n):
+                if t >= 0:
+                    yield ("p", t & 1), ready[t & 1]
+                    ready[t & 1] += 1
+                    if t == 0 and k > 0:
+                        yield "out_free", k - 1
+                    queue.append(("st_empty", (pos + t) % stages))
+                if t + 2 < n:
+                    yield ("st_full", (pos + t + 2) % stages), (pos + t + 2) // stages
+                    queue.append(("s", t & 1))
+                    if t + 2 == n - 1:
+                        queue.append("fix_empty")
+            pos, k = pos + n, k + 1
+            queue.append("out_done")
+
+    def sdp(x):
+        pos, used, k = 0, [0, 0], 0
+        while (n := (yield from segment(k))) is not None:
+            yield "fix_full", k
+            for t in range(n):
+                yield ("st_full", pos % stages), pos // stages
+                if used[t & 1]:
+                    yield ("free", t & 1), used[t & 1] - 1
+                used[t & 1] += 1
+                commits[x].append(("s", t & 1))
+                if t == n - 1:
+                    commits[x].append("fix_empty")
+                pos += 1
+            k += 1
+
+    def acc():
+        pos, ready, k = 0, [0, 0], 0
+        while (n := (yield from segment(k))) is not None:
+            for t in range(n):
+                yield ("p", t & 1), ready[t & 1]
+                ready[t & 1] += 1
+                if t == 0 and k > 0:
+                    yield "out_free", k - 1
+                commits["acc"] += [("free", t & 1), ("st_empty", pos % stages)]
+                pos += 1
+            commits["acc"].append("out_done")
+            k += 1
+
+    def elementwise(b):
+        pos, done, k = 0, 0, 0
+        while (n := (yield from segment(k))) is not None:
+            for t in range(b, n, 2):
+                yield ("s", b), done
+                done += 1
+                yield ("st_full", (pos + t) % stages), (pos + t) // stages
+                bars[("p", b)].arrive()
+            pos += n
+            yield "out_done", k
+            bars["out_free"].arrive()
+            k += 1
+
+    warps = {"load": load(), "ew0": elementwise(0), "ew1": elementwise(1)}
+    warps.update({"s": sdp(0), "acc": acc()} if apart else {"mma": one()})
+    if dp:
+        warps["dp"] = sdp(1)
+    schedule(rng, bars, commits, warps)
+
+
+@pytest.mark.parametrize("stages,apart,dp", [(2, False, False), (3, False, False), (4, False, False), (4, True, False), (3, True, True)])
+def test_the_kernel_of_longer_sequences(stages, apart, dp):
+    for seed in range(400):
+        rng = random.Random(seed)
+        run_long([rng.choice((1, 1, 2, 3, 4, 7)) for _ in range(rng.randint(0, 12))], stages, apart, dp, seed)
