@@ -391,3 +391,84 @@ def test_python_refusals():
     with pytest.raises(ValueError):
         fa.cross_backward(q, k, v, o, lse, dout, cu_rows, cu_keys, out=(q, k, v[:1]))
     fa.check_status()
+
+
+# ------------------------------------------------------------------ paddings, wide heads, first calls
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("rows,keys", [([2], [3]), ([300], [3]), ([0], [5]), ([4, 0, 90], [0, 7, 2000])])
+def test_long_paddings_are_cleared(rows, keys, d):
+    """Many blocks clear one sequence's places."""
+    s = Ragged(rows, keys, 2, 2, d, padded=True, lead=2, pad=3, seed=d)
+    s.cu_keys = np.cumsum([2] + [6001] * len(rows))
+    s.K = int(s.cu_keys[-1]) + 3
+    g = torch.Generator().manual_seed(d)
+    s.wide_k = torch.full((s.K, 4, d), float("nan"), dtype=torch.bfloat16)
+    s.mine_k = (np.arange(s.K) >= 2) & (np.arange(s.K) < s.K - 3)
+    for _, _, key0, _, length in s.sequences():
+        s.wide_k[key0:key0 + length] = torch.randn(length, 4, d, generator=g).bfloat16()
+    check(s)
+
+
+def test_many_padded_sequences_are_cleared():
+    """Each block clears several sequences' places."""
+    rng = np.random.default_rng(5)
+    rows, keys = rng.integers(0, 6, 500).tolist(), rng.integers(0, 40, 500).tolist()
+    check(Ragged(rows, keys, 1, 2, 32, padded=True, pad=4, seed=5))
+
+
+@pytest.mark.parametrize("d", [32, 256])
+def test_same_inputs_give_the_same_bits_captured_or_not(d):
+    s = Ragged([700, 81, 3], [500, 1700, 900], 2, 4, d, seed=22, padded=True)
+    tensors, batch = s.tensors(), s.batch()
+    q, dout, k, v = tensors
+    o, lse = forward(s, tensors=tensors)
+    grads = backward(s, o, lse, tensors=tensors)
+    ws = fa.cross_backward_workspace(q, k, 3)
+    out = [torch.empty_like(t) for t in (q, k, v)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]  # with one workspace
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            fa.cross_backward(q, k, v, o, lse, dout, *batch, out=out, workspace=ws)
+    for graph in graphs * 2:
+        ws.fill_(255)
+        for t, x in zip(out, grads):
+            t.copy_(torch.full_like(t, 7.0))
+        graph.replay()
+        fa.check_status()
+        assert all(torch.equal(a, b) for a, b in zip(out, grads))
+
+
+def test_first_calls_may_be_captured():
+    """Kernels' attributes and cluster sizes are set by a first call of theirs; it may be a captured one (the device's own state is made
+    by the process' first call of any, which may not: include/fa_gb300.h)."""
+    import subprocess
+    import sys
+
+    code = """
+import torch
+import tiled_attention_fwd_gb300 as fa
+i32 = dict(dtype=torch.int32, device="cuda")
+pool = fa.PagePool.full(40, 16)
+table, lens, new = torch.full((3, 8), -1, **i32), torch.zeros(3, **i32), torch.tensor([5, 0, 33], **i32)
+done = torch.tensor([False, True, True], device="cuda")
+out = torch.zeros(4, **i32), torch.full((38,), -1, dtype=torch.int64, device="cuda"), torch.full((38,), -1, **i32)
+cu = torch.tensor([0, 5, 40], **i32)
+q, k = (torch.randn(40, 4, d, device="cuda").bfloat16() for d in (64, 64))
+o, dq, dk, dv = (torch.empty_like(q) for _ in range(4))
+lse = torch.empty(4, 40, device="cuda")
+ws, wsb = fa.cross_workspace(k), fa.cross_backward_workspace(q, k, 2)
+fa.check_status()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    fa.paged_extend(pool, table, lens, new, out=out)
+    fa.paged_release(pool, table, lens, done)
+    fa.cross_forward(q, k, k, cu, cu, out=o, lse=lse, workspace=ws)
+    fa.cross_backward(q, k, k, o, lse, o, cu, cu, out=(dq, dk, dv), workspace=wsb)
+graph.replay()
+fa.check_status()
+assert lens.tolist() == [5, 0, 0] and out[0].tolist() == [0, 5, 5, 38] and pool.free_count.tolist() == [39]
+x, l = fa.cross_forward(q, k, k, cu, cu)
+assert torch.equal(o, x) and torch.equal(lse, l)
+assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), fa.cross_backward(q, k, k, o, lse, o, cu, cu)))
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300, cwd=str(__import__("pathlib").Path(__file__).parent.parent))
