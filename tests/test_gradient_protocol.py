@@ -221,11 +221,13 @@ def test_every_order_ends_and_no_wait_is_for_another_phase(stages, slots, subs, 
 
 
 def run_long(segments, stages, apart, dp, seed):
-    """fa_cross_bwd_kernel over segments of so many streamed tiles: one issuing warp, or (d = 256) the accumulations apart and
-    (`dp`) dP, too."""
+    """fa_cross_bwd_kernel over segments of so many streamed tiles: one issuing warp and one ring of `stages`; or (d = 256, `apart`) the
+    accumulations by a warp of their own, (`dp`) dP, too, and `stages` slots of the rings A and B."""
     rng = random.Random(seed)
     names = ["fix_full", "out_done", "drain"] + [(x, b) for x in ("p", "free") for b in range(2)]
-    bars = {x: Barrier(1) for x in names + [("st_full", i) for i in range(stages)] + [("st_empty", i) for i in range(stages)]}
+    rings = {"a": stages[0], "b": stages[1]} if apart else {"a": stages}
+    acc_ring = "a" if dp or not apart else "b"  # what the accumulations read
+    bars = {x: Barrier(1) for x in names + [(r, e, i) for r in rings for e in ("full", "empty") for i in range(rings[r])]}
     first = 2 if dp else 1  # warps whose products make a tile's S and dP
     bars.update({"fix_empty": Barrier(first), ("s", 0): Barrier(first), ("s", 1): Barrier(first), "out_free": Barrier(2)})
     for i in range(RING):
@@ -244,8 +246,9 @@ def run_long(segments, stages, apart, dp, seed):
             yield "fix_empty", k - 1
             bars["fix_full"].arrive()
             for _ in range(n):
-                yield ("st_empty", pos % stages), pos // stages - 1
-                bars[("st_full", pos % stages)].arrive()
+                for r in rings:
+                    yield (r, "empty", pos % rings[r]), pos // rings[r] - 1
+                    bars[(r, "full", pos % rings[r])].arrive()
                 pos += 1
 
     def segment(k):
@@ -264,9 +267,9 @@ def run_long(segments, stages, apart, dp, seed):
                     ready[t & 1] += 1
                     if t == 0 and k > 0:
                         yield "out_free", k - 1
-                    queue.append(("st_empty", (pos + t) % stages))
+                    queue.append(("a", "empty", (pos + t) % stages))
                 if t + 2 < n:
-                    yield ("st_full", (pos + t + 2) % stages), (pos + t + 2) // stages
+                    yield ("a", "full", (pos + t + 2) % stages), (pos + t + 2) // stages
                     queue.append(("s", t & 1))
                     if t + 2 == n - 1:
                         queue.append("fix_empty")
@@ -278,11 +281,14 @@ def run_long(segments, stages, apart, dp, seed):
         while (n := (yield from segment(k))) is not None:
             yield "fix_full", k
             for t in range(n):
-                yield ("st_full", pos % stages), pos // stages
+                r = "ab"[x]
+                yield (r, "full", pos % rings[r]), pos // rings[r]
                 if used[t & 1]:
                     yield ("free", t & 1), used[t & 1] - 1
                 used[t & 1] += 1
                 commits[x].append(("s", t & 1))
+                if r != acc_ring:
+                    commits[x].append((r, "empty", pos % rings[r]))
                 if t == n - 1:
                     commits[x].append("fix_empty")
                 pos += 1
@@ -292,11 +298,13 @@ def run_long(segments, stages, apart, dp, seed):
         pos, ready, k = 0, [0, 0], 0
         while (n := (yield from segment(k))) is not None:
             for t in range(n):
+                slot = pos % rings[acc_ring]
+                yield (acc_ring, "full", slot), pos // rings[acc_ring]
                 yield ("p", t & 1), ready[t & 1]
                 ready[t & 1] += 1
                 if t == 0 and k > 0:
                     yield "out_free", k - 1
-                commits["acc"] += [("free", t & 1), ("st_empty", pos % stages)]
+                commits["acc"] += [("free", t & 1), (acc_ring, "empty", slot)]
                 pos += 1
             commits["acc"].append("out_done")
             k += 1
@@ -307,7 +315,7 @@ def run_long(segments, stages, apart, dp, seed):
             for t in range(b, n, 2):
                 yield ("s", b), done
                 done += 1
-                yield ("st_full", (pos + t) % stages), (pos + t) // stages
+                yield (acc_ring, "full", (pos + t) % rings[acc_ring]), (pos + t) // rings[acc_ring]
                 bars[("p", b)].arrive()
             pos += n
             yield "out_done", k
@@ -321,7 +329,7 @@ def run_long(segments, stages, apart, dp, seed):
     schedule(rng, bars, commits, warps)
 
 
-@pytest.mark.parametrize("stages,apart,dp", [(2, False, False), (3, False, False), (4, False, False), (4, True, False), (3, True, True)])
+@pytest.mark.parametrize("stages,apart,dp", [(2, False, False), (3, False, False), (4, False, False), ((2, 3), True, False), ((2, 1), True, True)])
 def test_the_kernel_of_longer_sequences(stages, apart, dp):
     for seed in range(400):
         rng = random.Random(seed)

@@ -32,13 +32,14 @@ namespace fa {
 
 constexpr int kBwdSegRing = 4;
 
-// dV or dK of d = 256: TMEM columns S' buffers, (dK) dP's buffers, the accumulator; the vectors of the streamed rows lie
-// behind everything else, where they leave room for one more stage.
+// d = 256 (MODE 1, 3, 4).  The streamed tensors have a ring each: A holds what S is made of (Q, or K), B the other.  The
+// accumulations read A, too (dV's: B); the one that only a first product reads needs fewer slots, and 64 rows a tile
+// fit where pairs of tiles left room for 32 (half as many products; 6 sequences of 100 to 700 rows: ROWS64).
 template <int MODE>
 struct BwdWideCfg {
-  static constexpr bool KV = false;
+  static constexpr bool DP = MODE != 3;
   static constexpr int BM = 128;
-  static constexpr int BS = 32;
+  static constexpr int BS = 64;
   static constexpr int OUTW = 256, NOUT = 1;
   static constexpr int SWB = 128;
   static constexpr uint32_t SWZ = 2u;
@@ -46,25 +47,38 @@ struct BwdWideCfg {
   static constexpr int FIX_REGION = BM * SWB, S_REGION = BS * SWB;
   static constexpr int FIX_TILE = BM * 512, S_TILE = BS * 512;
   static constexpr int VEC_BYTES = BS * 4;
-  static constexpr int STAGE = 2 * S_TILE;
+  static constexpr int NA = 2, NB = DP ? 1 : 3;  // slots
   static constexpr int OFF_FIX = 0;
-  static constexpr int OFF_ST = (MODE == 3 ? 1 : 2) * FIX_TILE;  // dV: K alone
-  static constexpr int NST = MODE == 3 ? 4 : 3;
-  static constexpr int OFF_MISC = OFF_ST + NST * STAGE;
-  static constexpr int MISC = 1024 + NST * 2 * VEC_BYTES;
+  static constexpr int OFF_A = (DP ? 2 : 1) * FIX_TILE;  // dV: K alone
+  static constexpr int OFF_B = OFF_A + NA * S_TILE;
+  static constexpr int OFF_MISC = OFF_B + NB * S_TILE;
+  // The ring that the accumulations read; the vectors come with its tiles.
+  static constexpr int NST = DP ? NA : NB;
+  static constexpr int STAGE = S_TILE;
+  static constexpr int OFF_ST = DP ? OFF_A : OFF_B;
+  static constexpr int VECS = MODE == 1 ? 0 : DP ? 2 : 1;  // -L log2e, -D
+  static constexpr int MISC = 1024 + NST * VECS * VEC_BYTES;
   static constexpr int OFF_TMEM_SLOT = OFF_MISC + 512;
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
   static constexpr int SMEM_ALLOC = OFF_MISC + MISC + 1024;  // + slack for 1024-byte alignment
   static constexpr int TM_S = 0, TM_DP = 2 * BS, TM_OUT = 4 * BS, TM_COLS = 512;
-  static constexpr bool RUNS = true;
   static constexpr int MMA_WARP = 8, LOAD_WARP = 9;
-  static constexpr int THREADS = 320;
   static_assert(TM_OUT + OUTW <= TM_COLS && SMEM_ALLOC <= 227 * 1024, "TMEM and shared memory budgets");
 };
-template <>
-struct BwdCfg<256, 3> : BwdWideCfg<3> {};
-template <>
-struct BwdCfg<256, 4> : BwdWideCfg<4> {};
+template <int D, int MODE>
+struct BwdBaseOf {
+  using type = BwdCfg<D, MODE>;
+};
+template <int MODE>
+struct BwdBaseOf<256, MODE> {
+  using type = BwdWideCfg<MODE>;
+};
+template <int D, int MODE>
+using BwdBase = typename BwdBaseOf<D, MODE>::type;
+
+// Rows of a streamed tile where K and V stay, and of a tile of the vectors.
+template <int D>
+constexpr __host__ __device__ int bwd_rows0() { return BwdBase<D, D == 256 ? 3 : 0>::BS; }
 
 // Whether a unit is 128 keys (else 128 rows), and which of the workspace's three records and parts are a mode's.
 constexpr __host__ __device__ bool bwd_by_key(int mode) { return mode == 0 || mode >= 3; }
@@ -72,7 +86,7 @@ constexpr __host__ __device__ int bwd_place(int mode) { return mode == 3 ? 0 : m
 
 // Tokens of a streamed tile of MODE 0 and of a fixed tile of MODE 1.
 template <int D>
-constexpr __host__ __device__ int bwd_tokens0(int group) { return BwdCfg<D, 0>::BS / group; }
+constexpr __host__ __device__ int bwd_tokens0(int group) { return bwd_rows0<D>() / group; }
 constexpr __host__ __device__ int bwd_tokens1(int group) { return 128 / group; }
 
 // -L log2e and -D of the rows, as MODE 0 streams them: BS values a tile of tokens, [heads][tiles][BS]; sequence b's tiles
@@ -96,8 +110,8 @@ __host__ __device__ __forceinline__ bool bwd_short(const CrossSeq& s, int group)
 // Units, fixed and streamed tiles of a kernel.
 template <int D, int MODE>
 struct BwdWork {
-  static constexpr int STR = BwdCfg<D, MODE>::BS;
-  static constexpr size_t PART = static_cast<size_t>(128) * BwdCfg<D, MODE>::NOUT * BwdCfg<D, MODE>::OUTW;  // floats of a part
+  static constexpr int STR = BwdBase<D, MODE>::BS;
+  static constexpr size_t PART = static_cast<size_t>(128) * BwdBase<D, MODE>::NOUT * BwdBase<D, MODE>::OUTW;  // floats of a part
   // Streamed tiles that a unit costs besides its own (loading the fixed tiles, the output).
   static constexpr int UNIT_COST = 2;  // (of places on the line, as a streamed tile is one)
 };
@@ -127,7 +141,7 @@ size_t cross_bwd_ws(char* p, int B, int rows, int heads, int group, CrossBwdWs* 
     return x;
   };
   CrossBwdWs x;
-  const size_t vec = static_cast<size_t>(heads) * bwd_tiles<D>(rows, B, group) * BwdCfg<D, 0>::BS * sizeof(float);
+  const size_t vec = static_cast<size_t>(heads) * bwd_tiles<D>(rows, B, group) * bwd_rows0<D>() * sizeof(float);
   for (int i = 0; i < 3; ++i) x.rec[i] = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
   x.part0 = reinterpret_cast<int*>(take(kPlanCtas * sizeof(int)));
   x.l2 = reinterpret_cast<float*>(take(vec));
@@ -165,16 +179,16 @@ struct alignas(16) BwdSeg {
 static_assert(sizeof(BwdSeg) == 48, "segment size");
 
 template <int D, int MODE>
-struct CrossBwdCfg : BwdCfg<D, MODE> {
-  using C = BwdCfg<D, MODE>;
+struct CrossBwdCfg : BwdBase<D, MODE> {
+  using C = BwdBase<D, MODE>;
   static constexpr int OFF_SEG = C::OFF_MISC + 576;
   static constexpr int OFF_PLAN = OFF_SEG + kBwdSegRing * static_cast<int>(sizeof(BwdSeg));
   static constexpr bool BY_KEY = bwd_by_key(MODE);      // K and V stay, Q and dO stream past, with the vectors
   static constexpr bool DV = MODE == 0 || MODE == 3;
   static constexpr bool DP = MODE != 3;                 // dP is formed, and dK or dQ
-  // Warps: 0-7 elementwise, 8 MMA, 9 load; d = 256: 10 MMA of the accumulators.  One warp takes some 65 cycles for each
-  // product, which of 32 streamed rows is more than the tensor core takes (6 sequences of 100 to 700 rows, d = 256: 242 us with one, 203 with
-  // two); with more rows it is not, and the warps' signals to each other cost more (d = 128, 1 to 4 K rows: 1.27 ms with one, 1.41 with two).
+  // Warps: 0-7 elementwise, 8 MMA, 9 load; d = 256: 10 MMA of the accumulators, 11 of dP.  One warp takes some 65 cycles for each
+  // product, which of few streamed rows is more than the tensor core takes (6 sequences of 100 to 700 rows, d = 256, 32 rows a tile: 242 us
+  // with one, 203 with two); else the warps' signals to each other cost more (d = 128, 1 to 4 K rows: 1.27 ms with one, 1.41 with two).
   static constexpr bool ACC_APART = D == 256;
   static constexpr int ACC_WARP = C::LOAD_WARP + 1;
   static constexpr bool DP_APART = ACC_APART && DP;
@@ -183,34 +197,9 @@ struct CrossBwdCfg : BwdCfg<D, MODE> {
   static constexpr int READERS = THREADS / 32 - 1;
   // A stage's vectors.
   static __device__ __forceinline__ int off_vec(int st) {
-    return MODE == 0 ? C::OFF_ST + st * C::STAGE + 2 * C::S_TILE : C::OFF_MISC + 1024 + st * 2 * C::VEC_BYTES;
+    return MODE == 0 ? C::OFF_ST + st * C::STAGE + 2 * C::S_TILE : C::OFF_MISC + 1024 + st * (DP ? 2 : 1) * C::VEC_BYTES;
   }
   static_assert(C::OFF_ABORT + 4 <= OFF_SEG && OFF_PLAN + sizeof(PlanScratch) <= C::OFF_MISC + 1024, "misc area");
-};
-
-template <int D, int MODE>
-struct CrossBwdMma : BwdMma<D, MODE> {
-  using Base = BwdMma<D, MODE>;
-  using C = BwdCfg<D, MODE>;
-  using Base::BwdMma;
-  // d = 256, X = 0: S, 1: dP of the tile in stage st, into buffer b.
-  template <int X>
-  __device__ __forceinline__ void first(uint32_t st, int b) const {
-    using S0 = typename Base::template SdpSteps<0>;
-    using S8 = typename Base::template SdpSteps<8>;
-    const uint32_t d = this->tmem + (X ? C::TM_DP : C::TM_S) + b * C::BS;
-    const uint32_t x = X ? this->a2 : this->a1, y = (X ? this->b2 : this->b1) + st * Base::STAGE_STEP;
-    mma_ss_run<8, S0>(d, x, Base::DESC_HI, y, Base::DESC_HI, Base::IDESC_S, 0u);
-    mma_ss_run<8, S8>(d, x + Base::a_step(8), Base::DESC_HI, y + Base::b_step(8), Base::DESC_HI, Base::IDESC_S, 1u);
-  }
-  // MODE 0: dK (+)= dS^T Q, dV (+)= P^T dO; 1: dQ (+)= dS K; 3: dV; 4: dK.
-  __device__ __forceinline__ void add(uint32_t st, int b, bool acc) const {
-    if constexpr (MODE == 3)
-      mma_ts_run<C::BS / 16, typename Base::AccSteps>(this->tmem + C::TM_OUT, this->tmem + C::TM_S + b * C::BS,
-                                                      this->b2_mn + st * Base::STAGE_STEP, Base::DESC_HI, Base::IDESC_O, acc ? 1u : 0u);
-    else
-      this->accumulate(st, b, acc, 0);
-  }
 };
 
 template <int D, int MODE>
@@ -218,11 +207,69 @@ struct CrossBwdBars : BwdBars<D, MODE> {
   using Base = BwdBars<D, MODE>;
   __device__ __forceinline__ uint32_t seg_full(int i) const { return this->b0 + 256 + 8u * i; }
   __device__ __forceinline__ uint32_t seg_empty(int i) const { return this->b0 + 288 + 8u * i; }
-  // The accumulations that read P and dS in buffer b are complete.
-  __device__ __forceinline__ uint32_t buf_free(int b) const { return this->b0 + 240 + 8u * b; }
-  __device__ __forceinline__ uint32_t drain_acc() const { return this->b0 + 232; }
-  __device__ __forceinline__ uint32_t drain_dp() const { return this->b0 + 224; }
-  static_assert(Base::COUNT * 8 <= 224, "barrier area");
+  static_assert(Base::COUNT * 8 <= 256, "barrier area");
+};
+template <int MODE>
+struct CrossBwdBars<256, MODE> {
+  using C = BwdWideCfg<MODE>;
+  uint32_t b0;
+  __device__ __forceinline__ uint32_t fix_full() const { return b0; }
+  __device__ __forceinline__ uint32_t fix_empty() const { return b0 + 8; }
+  __device__ __forceinline__ uint32_t a_full(int i) const { return b0 + 16 + 8u * i; }
+  __device__ __forceinline__ uint32_t a_empty(int i) const { return b0 + 32 + 8u * i; }
+  __device__ __forceinline__ uint32_t b_full(int i) const { return b0 + 48 + 8u * i; }
+  __device__ __forceinline__ uint32_t b_empty(int i) const { return b0 + 72 + 8u * i; }
+  __device__ __forceinline__ uint32_t st_full(int i) const { return C::DP ? a_full(i) : b_full(i); }
+  __device__ __forceinline__ uint32_t st_empty(int i) const { return C::DP ? a_empty(i) : b_empty(i); }
+  __device__ __forceinline__ uint32_t s_full(int b) const { return b0 + 96 + 8u * b; }
+  __device__ __forceinline__ uint32_t p_ready(int b) const { return b0 + 112 + 8u * b; }
+  // The accumulations that read P or dS in buffer b are complete.
+  __device__ __forceinline__ uint32_t buf_free(int b) const { return b0 + 128 + 8u * b; }
+  __device__ __forceinline__ uint32_t out_done() const { return b0 + 144; }
+  __device__ __forceinline__ uint32_t out_free() const { return b0 + 152; }
+  __device__ __forceinline__ uint32_t drain() const { return b0 + 160; }
+  __device__ __forceinline__ uint32_t drain_acc() const { return b0 + 168; }
+  __device__ __forceinline__ uint32_t drain_dp() const { return b0 + 176; }
+  __device__ __forceinline__ uint32_t seg_full(int i) const { return b0 + 256 + 8u * i; }
+  __device__ __forceinline__ uint32_t seg_empty(int i) const { return b0 + 288 + 8u * i; }
+  static_assert(C::NA <= 2 && C::NB <= 3, "barrier area");
+};
+
+// Products of d = 256.
+template <int MODE>
+struct BwdWideMma {
+  using C = BwdWideCfg<MODE>;
+  static constexpr uint32_t IDESC_S = make_idesc_bf16(128, C::BS, 0);
+  static constexpr uint32_t IDESC_O = make_idesc_bf16(128, C::OUTW, 1);
+  static constexpr uint32_t HI = sdesc_hi(8 * C::SWB, C::SWZ);
+  template <int REGION>
+  static constexpr __host__ __device__ uint32_t k_step(int kk) {
+    return ((kk * 16 / C::RC) * REGION + (kk * 16 % C::RC) * 2) >> 4;
+  }
+  template <int OFF>
+  struct Steps {  // runs that start at K step OFF
+    static constexpr __host__ __device__ uint32_t da(int k) { return k_step<C::FIX_REGION>(OFF + k) - k_step<C::FIX_REGION>(OFF + k - 1); }
+    static constexpr __host__ __device__ uint32_t db(int k) { return k_step<C::S_REGION>(OFF + k) - k_step<C::S_REGION>(OFF + k - 1); }
+  };
+  struct AccSteps {
+    static constexpr __host__ __device__ uint32_t ta(int) { return 8; }
+    static constexpr __host__ __device__ uint32_t db(int) { return 16 * C::SWB >> 4; }
+  };
+  uint32_t tmem, base;
+  // X = 0: S = A1 A^T, 1: dP = A2 B^T, with the tile in `slot` of its ring, into buffer b.
+  template <int X>
+  __device__ __forceinline__ void first(uint32_t slot, int b) const {
+    const uint32_t d = tmem + (X ? C::TM_DP : C::TM_S) + b * C::BS;
+    const uint32_t x = sdesc_lo(base + C::OFF_FIX + X * C::FIX_TILE, 16);
+    const uint32_t y = sdesc_lo(base + (X ? C::OFF_B : C::OFF_A), 16) + slot * (C::S_TILE >> 4);
+    mma_ss_run<8, Steps<0>>(d, x, HI, y, HI, IDESC_S, 0u);
+    mma_ss_run<8, Steps<8>>(d, x + k_step<C::FIX_REGION>(8), HI, y + k_step<C::S_REGION>(8), HI, IDESC_S, 1u);
+  }
+  // dQ (+)= dS K, dV (+)= P^T dO, dK (+)= dS^T Q.
+  __device__ __forceinline__ void add(uint32_t slot, int b, bool acc) const {
+    mma_ts_run<C::BS / 16, AccSteps>(tmem + C::TM_OUT, tmem + (C::DP ? C::TM_DP : C::TM_S) + b * C::BS,
+                                     sdesc_lo(base + C::OFF_ST, C::S_REGION) + slot * (C::S_TILE >> 4), HI, IDESC_O, acc ? 1u : 0u);
+  }
 };
 
 // The units of a sequence.
@@ -402,38 +449,74 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
     }
     last_fix = k;
     for (int t = 0; t < w.n; ++t) {
-      const int st = pos % C::NST;
-      const uint32_t par = (pos / C::NST) & 1;
-      if (!(ok = warp_wait_bar(bar.st_empty(st), par ^ 1, g, kStatusTimeoutLoad))) break;
-      if (lane == 0) {
-        const uint32_t s0 = base + C::OFF_ST + st * C::STAGE;
-        const uint32_t full = bar.st_full(st);
+      if constexpr (D == 256) {
+        // A tile of ring A, then one of ring B.
         const int rows = C::BY_KEY ? t0 * group : C::BS;
-        mbar_arrive_expect_tx(full, 2 * C::NR * rows * C::SWB + (C::BY_KEY ? (C::DP ? 2 : 1) * C::VEC_BYTES : 0));
         const int s = w.s0 + t, h = C::BY_KEY ? w.head * group : w.head;
         const int row = w.str0 + s * (C::BY_KEY ? t0 : C::BS);
-        for (int r = 0; r < C::NR; ++r) {
-          tma_load_3d(s0 + r * C::S_REGION, tm_b1, full, r * C::RC, h, row, pol_str);
-          tma_load_3d(s0 + C::S_TILE + r * C::S_REGION, tm_b2, full, r * C::RC, h, row, pol_str);
+#pragma unroll
+        for (int x = 0; ok && x < 2; ++x) {
+          const int n = x ? C::NB : C::NA;
+          const int slot = pos % n;
+          const uint32_t par = (pos / n) & 1;
+          if (!(ok = warp_wait_bar(x ? bar.b_empty(slot) : bar.a_empty(slot), par ^ 1, g, kStatusTimeoutLoad))) break;
+          if (lane == 0) {
+            const bool vecs = C::BY_KEY && (x == 0) == C::DP;
+            const uint32_t full = x ? bar.b_full(slot) : bar.a_full(slot);
+            const uint32_t dst = base + (x ? C::OFF_B : C::OFF_A) + slot * C::S_TILE;
+            mbar_arrive_expect_tx(full, C::NR * rows * C::SWB + (vecs ? (C::DP ? 2 : 1) * C::VEC_BYTES : 0));
+            for (int r = 0; r < C::NR; ++r) tma_load_3d(dst + r * C::S_REGION, x ? tm_b2 : tm_b1, full, r * C::RC, h, row, pol_str);
+            if (vecs) {
+              const long long off = (w.head * p.tiles + w.vec0 + s) * C::BS;
+              bulk_load(base + C::off_vec(slot), p.ws.l2 + off, C::VEC_BYTES, full);
+              if (C::DP) bulk_load(base + C::off_vec(slot) + C::VEC_BYTES, p.ws.dsum + off, C::VEC_BYTES, full);
+            }
+          }
+          const int bit = x * 4 + slot;
+          issued |= 1u << bit;
+          last_par = (last_par & ~(1u << bit)) | (par << bit);
         }
-        if constexpr (C::BY_KEY) {
-          // (BS * 4 is a multiple of 16.)
-          const long long off = (w.head * p.tiles + w.vec0 + s) * C::BS;
-          const uint32_t vec = base + C::off_vec(st);
-          bulk_load(vec, p.ws.l2 + off, C::VEC_BYTES, full);
-          if (C::DP) bulk_load(vec + C::VEC_BYTES, p.ws.dsum + off, C::VEC_BYTES, full);
+        if (!ok) break;
+        ++pos;
+      } else {
+        const int st = pos % C::NST;
+        const uint32_t par = (pos / C::NST) & 1;
+        if (!(ok = warp_wait_bar(bar.st_empty(st), par ^ 1, g, kStatusTimeoutLoad))) break;
+        if (lane == 0) {
+          const uint32_t s0 = base + C::OFF_ST + st * C::STAGE;
+          const uint32_t full = bar.st_full(st);
+          const int rows = C::BY_KEY ? t0 * group : C::BS;
+          mbar_arrive_expect_tx(full, 2 * C::NR * rows * C::SWB + (C::BY_KEY ? (C::DP ? 2 : 1) * C::VEC_BYTES : 0));
+          const int s = w.s0 + t, h = C::BY_KEY ? w.head * group : w.head;
+          const int row = w.str0 + s * (C::BY_KEY ? t0 : C::BS);
+          for (int r = 0; r < C::NR; ++r) {
+            tma_load_3d(s0 + r * C::S_REGION, tm_b1, full, r * C::RC, h, row, pol_str);
+            tma_load_3d(s0 + C::S_TILE + r * C::S_REGION, tm_b2, full, r * C::RC, h, row, pol_str);
+          }
+          if constexpr (C::BY_KEY) {
+            // (BS * 4 is a multiple of 16.)
+            const long long off = (w.head * p.tiles + w.vec0 + s) * C::BS;
+            const uint32_t vec = base + C::off_vec(st);
+            bulk_load(vec, p.ws.l2 + off, C::VEC_BYTES, full);
+            if (C::DP) bulk_load(vec + C::VEC_BYTES, p.ws.dsum + off, C::VEC_BYTES, full);
+          }
         }
+        issued |= 1u << st;
+        last_par = (last_par & ~(1u << st)) | (par << st);
+        ++pos;
       }
-      issued |= 1u << st;
-      last_par = (last_par & ~(1u << st)) | (par << st);
-      ++pos;
     }
     if (!ok) break;
   }
   if (lane == 0 && !recorded) p.ws.rec[bwd_place(MODE)][blockIdx.x].b = -1;
   // Every issued copy must land before the CTA may exit.
-  for (int i = 0; i < C::NST; ++i)
-    if (issued & (1u << i)) bwd_wait_drain(bar.st_full(i), (last_par >> i) & 1, g);
+  if constexpr (D == 256) {
+    for (int i = 0; i < 8; ++i)
+      if (issued & (1u << i)) bwd_wait_drain(i < 4 ? bar.a_full(i) : bar.b_full(i - 4), (last_par >> i) & 1, g);
+  } else {
+    for (int i = 0; i < C::NST; ++i)
+      if (issued & (1u << i)) bwd_wait_drain(bar.st_full(i), (last_par >> i) & 1, g);
+  }
   if (last_fix >= 0) bwd_wait_drain(bar.fix_full(), last_fix & 1, g);
   __syncwarp();
 }
@@ -458,7 +541,7 @@ template <int D, int MODE>
 __device__ __forceinline__ void cross_bwd_mma(const CrossBwdBars<D, MODE>& bar, uint32_t base,
                                               uint8_t* gbase, uint32_t tmem, const WaitGuard& g) {
   using C = CrossBwdCfg<D, MODE>;
-  const CrossBwdMma<D, MODE> M(tmem, base);
+  const BwdMma<D, MODE> M(tmem, base);
   const CrossIssuer is{g};
   uint32_t pos = 0;            // streamed stages consumed before the current segment
   uint32_t pr0 = 0, pr1 = 0;   // p_ready phases consumed, per buffer
@@ -492,7 +575,7 @@ __device__ __forceinline__ void cross_bwd_mma(const CrossBwdBars<D, MODE>& bar, 
         if (!(ok = is.wait(bar.out_free(), (k - 1) & 1))) break;
         tc_fence_after();
       }
-      M.add(stage_of(t), b, t > 0);
+      M.accumulate(stage_of(t), b, t > 0, 0);
       mma_commit_elect(bar.st_empty(stage_of(t)));
       if (t + 2 < n) {
         if (!(ok = acquire(t + 2))) break;
@@ -508,15 +591,16 @@ __device__ __forceinline__ void cross_bwd_mma(const CrossBwdBars<D, MODE>& bar, 
   is.finish(bar.drain());
 }
 
-// ACC_APART: S (X = 0) or dP, segment by segment.
-template <int D, int MODE, int X>
-__device__ __forceinline__ void cross_bwd_sdp(const CrossBwdBars<D, MODE>& bar, uint32_t base, uint8_t* gbase, uint32_t tmem,
-                                              const WaitGuard& g) {
-  using C = CrossBwdCfg<D, MODE>;
-  const CrossBwdMma<D, MODE> M(tmem, base);
+// d = 256: S (X = 0) or dP, segment by segment, up to two tiles ahead of the accumulations.
+template <int MODE, int X>
+__device__ __forceinline__ void cross_bwd_first(const CrossBwdBars<256, MODE>& bar, uint32_t base, uint8_t* gbase, uint32_t tmem,
+                                                const WaitGuard& g) {
+  using C = CrossBwdCfg<256, MODE>;
+  constexpr int N = X ? C::NB : C::NA;
+  const BwdWideMma<MODE> M{tmem, base};
   const CrossIssuer is{g};
-  uint32_t pos = 0;                // streamed stages issued
-  uint32_t used[2] = {0, 0};       // tiles issued into the buffers
+  uint32_t pos = 0;                // streamed tiles issued
+  uint32_t used[2] = {0, 0};       // into the buffers
   bool ok = true;
   for (int k = 0; ok; ++k) {
     BwdSeg w;
@@ -524,27 +608,29 @@ __device__ __forceinline__ void cross_bwd_sdp(const CrossBwdBars<D, MODE>& bar, 
     if (!(ok = is.wait(bar.fix_full(), k & 1))) break;
     for (int t = 0; t < w.n; ++t, ++pos) {
       const int b = t & 1;
+      const uint32_t slot = pos % N;
       uint32_t& u = b ? used[1] : used[0];
-      if (!(ok = is.wait(bar.st_full(pos % C::NST), (pos / C::NST) & 1))) break;
+      if (!(ok = is.wait(X ? bar.b_full(slot) : bar.a_full(slot), (pos / N) & 1))) break;
       if (u > 0 && !(ok = is.wait(bar.buf_free(b), (u - 1) & 1))) break;
       ++u;
       tc_fence_after();
-      M.template first<X>(pos % C::NST, b);
+      M.template first<X>(slot, b);
       mma_commit_elect(bar.s_full(b));
+      if (X || !C::DP) mma_commit_elect(X ? bar.b_empty(slot) : bar.a_empty(slot));  // (no other product reads the tile)
       if (t == w.n - 1) mma_commit_elect(bar.fix_empty());
     }
   }
   is.finish(X ? bar.drain_dp() : bar.drain());
 }
 
-// The accumulations.
-template <int D, int MODE>
-__device__ __forceinline__ void cross_bwd_acc(const CrossBwdBars<D, MODE>& bar, uint32_t base, uint8_t* gbase, uint32_t tmem,
+// d = 256: the accumulations.
+template <int MODE>
+__device__ __forceinline__ void cross_bwd_acc(const CrossBwdBars<256, MODE>& bar, uint32_t base, uint8_t* gbase, uint32_t tmem,
                                               const WaitGuard& g) {
-  using C = CrossBwdCfg<D, MODE>;
-  const CrossBwdMma<D, MODE> M(tmem, base);
+  using C = CrossBwdCfg<256, MODE>;
+  const BwdWideMma<MODE> M{tmem, base};
   const CrossIssuer is{g};
-  uint32_t pos = 0;            // streamed stages consumed
+  uint32_t pos = 0;            // streamed tiles consumed
   uint32_t pr0 = 0, pr1 = 0;   // p_ready phases consumed, per buffer
   bool ok = true;
   for (int k = 0; ok; ++k) {
@@ -552,14 +638,16 @@ __device__ __forceinline__ void cross_bwd_acc(const CrossBwdBars<D, MODE>& bar, 
     if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
     for (int t = 0; t < w.n; ++t, ++pos) {
       const int b = t & 1;
+      const uint32_t slot = pos % C::NST;
       uint32_t& pr = b ? pr1 : pr0;
+      if (!(ok = is.wait(bar.st_full(slot), (pos / C::NST) & 1))) break;
       if (!(ok = is.wait(bar.p_ready(b), pr & 1))) break;
       ++pr;
       if (t == 0 && k > 0 && !(ok = is.wait(bar.out_free(), (k - 1) & 1))) break;
       tc_fence_after();
-      M.add(pos % C::NST, b, t > 0);
+      M.add(slot, b, t > 0);
       mma_commit_elect(bar.buf_free(b));
-      mma_commit_elect(bar.st_empty(pos % C::NST));
+      mma_commit_elect(bar.st_empty(slot));
     }
     if (!ok) break;
     mma_commit_elect(bar.out_done());
@@ -594,7 +682,7 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
       float l2 = -INFINITY, dsum = 0.f;
       if (mine) {
         const int t0 = bwd_tokens0<D>(p.a.group), tok = w.tok0 + tok_r;
-        const long long at = (w.head * p.tiles + w.vec0 + tok / t0) * BwdCfg<D, 0>::BS + tok % t0 * p.a.group + head_r;
+        const long long at = (w.head * p.tiles + w.vec0 + tok / t0) * bwd_rows0<D>() + tok % t0 * p.a.group + head_r;
         // (Written by a kernel that is not the one before: past L1.)
         l2 = __ldcg(p.ws.l2 + at);
         dsum = __ldcg(p.ws.dsum + at);
@@ -619,8 +707,8 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
       const int there = C::BY_KEY ? min(w.str_n - (w.s0 + t) * per, per) * p.a.group : w.str_n - (w.s0 + t) * per;
       const bool need_mask = there < C::BS;
       if (need_mask) {
-        // (MODE 0: both tiles; dV alone: dO's; else the first one's.)
-        const uint32_t tile = smem_u32(gbase + C::OFF_ST + st * C::STAGE) + (MODE == 3 ? C::S_TILE : 0);
+        // (Of the tiles that the accumulations read: MODE 0 both.)
+        const uint32_t tile = smem_u32(gbase + C::OFF_ST + st * C::STAGE);
         for (int x = r; x < (MODE == 0 ? 2 : 1) * C::BS; x += 128) {
           const int row = x % C::BS;
           if (row < there) continue;
@@ -769,20 +857,31 @@ __global__ void __launch_bounds__(CrossBwdCfg<D, MODE>::THREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(bar.fix_full(), 1);
     mbar_init(bar.fix_empty(), C::DP_APART ? 2 : 1);
-    for (int i = 0; i < C::NST; ++i) {
-      mbar_init(bar.st_full(i), 1);
-      mbar_init(bar.st_empty(i), 1);
-    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar.s_full(b), C::DP_APART ? 2 : 1);
       mbar_init(bar.p_ready(b), 4);
-      if (C::ACC_APART) mbar_init(bar.buf_free(b), 1);
+    }
+    if constexpr (C::ACC_APART) {
+      for (int i = 0; i < C::NA; ++i) {
+        mbar_init(bar.a_full(i), 1);
+        mbar_init(bar.a_empty(i), 1);
+      }
+      for (int i = 0; i < C::NB; ++i) {
+        mbar_init(bar.b_full(i), 1);
+        mbar_init(bar.b_empty(i), 1);
+      }
+      for (int b = 0; b < 2; ++b) mbar_init(bar.buf_free(b), 1);
+      mbar_init(bar.drain_acc(), 1);
+      mbar_init(bar.drain_dp(), 1);
+    } else {
+      for (int i = 0; i < C::NST; ++i) {
+        mbar_init(bar.st_full(i), 1);
+        mbar_init(bar.st_empty(i), 1);
+      }
     }
     mbar_init(bar.out_done(), 1);
     mbar_init(bar.out_free(), 8);
     mbar_init(bar.drain(), 1);
-    if (C::ACC_APART) mbar_init(bar.drain_acc(), 1);
-    if (C::DP_APART) mbar_init(bar.drain_dp(), 1);
     for (int i = 0; i < kBwdSegRing; ++i) {
       mbar_init(bar.seg_full(i), 1);
       mbar_init(bar.seg_empty(i), C::READERS);
@@ -812,15 +911,15 @@ __global__ void __launch_bounds__(CrossBwdCfg<D, MODE>::THREADS, 1)
     cross_bwd_elementwise<D, MODE>(p, bar, gbase, tmem, warp >> 2, warp & 3, lane, g);
   } else if (warp == C::MMA_WARP) {
     if constexpr (C::ACC_APART)
-      cross_bwd_sdp<D, MODE, 0>(bar, base, gbase, tmem, g);
+      cross_bwd_first<MODE, 0>(bar, base, gbase, tmem, g);
     else
       cross_bwd_mma<D, MODE>(bar, base, gbase, tmem, g);
   } else if (warp == C::LOAD_WARP) {
     cross_bwd_load<D, MODE>(&tm_a1, &tm_a2, &tm_b1, &tm_b2, p, bar, base, gbase, share, g);
   } else if (C::ACC_APART && warp == C::ACC_WARP) {
-    if constexpr (C::ACC_APART) cross_bwd_acc<D, MODE>(bar, base, gbase, tmem, g);
+    if constexpr (C::ACC_APART) cross_bwd_acc<MODE>(bar, base, gbase, tmem, g);
   } else {
-    if constexpr (C::DP_APART) cross_bwd_sdp<D, MODE, 1>(bar, base, gbase, tmem, g);
+    if constexpr (C::DP_APART) cross_bwd_first<MODE, 1>(bar, base, gbase, tmem, g);
   }
 
   __syncwarp();
@@ -878,7 +977,7 @@ struct BwdZeros {
 // (`zeros`: the kernel for short sequences, which writes them else, is not launched behind this one.)
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __grid_constant__ CrossBwdParams p, bool zeros) {
-  constexpr int BS = BwdCfg<D, 0>::BS;
+  constexpr int BS = bwd_rows0<D>();
   constexpr int CPR = D / 8;     // 16-byte chunks per row
   constexpr int RPW = 32 / CPR;  // rows per warp step
   constexpr int WARPS = kPrepThreads / 32;

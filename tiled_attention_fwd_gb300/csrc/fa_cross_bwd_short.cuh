@@ -226,7 +226,7 @@ __device__ __forceinline__ void short_load(const CUtensorMap* tm_q, const CUtens
         l2[e] = -INFINITY;
         dsum[e] = 0.f;
         if (r < t1 * group && tok < w.fix_n) {
-          const long long at = (w.head * p.tiles + w.vec0 + tok / t0) * BwdCfg<D, 0>::BS + tok % t0 * group + h;
+          const long long at = (w.head * p.tiles + w.vec0 + tok / t0) * bwd_rows0<D>() + tok % t0 * group + h;
           l2[e] = __ldcg(p.ws.l2 + at);
           dsum[e] = __ldcg(p.ws.dsum + at);
         }
