@@ -222,7 +222,7 @@ def test_every_order_ends_and_no_wait_is_for_another_phase(stages, slots, subs, 
 
 def run_long(segments, stages, apart, dp, seed):
     """fa_cross_bwd_kernel over segments of so many streamed tiles: one issuing warp and one ring of `stages`; or (d = 256, `apart`) the
-    accumulations by a warp of their own, (`dp`) dP, too, and `stages` slots of the rings A and B."""
+    accumulations by a warp of their own, (`dp`) dP, too, and `stages` slots of the rings A and B (`dp`: a tile's regions, each slot holds its own)."""
     rng = random.Random(seed)
     names = ["fix_full", "out_done", "drain"] + [(x, b) for x in ("p", "free") for b in range(2)]
     rings = {"a": stages[0], "b": stages[1]} if apart else {"a": stages}
@@ -235,6 +235,10 @@ def run_long(segments, stages, apart, dp, seed):
     ring = [None] * RING
     commits = {0: [], 1: [], "acc": []}
 
+    def regions(r, pos):
+        """Slots of tile `pos` and their phases."""
+        return [(i, pos) for i in range(rings[r])] if dp and r == "b" else [(pos % rings[r], pos // rings[r])]
+
     def load():
         pos = 0
         for k, n in enumerate(segments + [None]):
@@ -246,9 +250,10 @@ def run_long(segments, stages, apart, dp, seed):
             yield "fix_empty", k - 1
             bars["fix_full"].arrive()
             for _ in range(n):
-                for r in rings:
-                    yield (r, "empty", pos % rings[r]), pos // rings[r] - 1
-                    bars[(r, "full", pos % rings[r])].arrive()
+                for r in sorted(rings, reverse=dp):
+                    for slot, phase in regions(r, pos):
+                        yield (r, "empty", slot), phase - 1
+                        bars[(r, "full", slot)].arrive()
                 pos += 1
 
     def segment(k):
@@ -282,13 +287,14 @@ def run_long(segments, stages, apart, dp, seed):
             yield "fix_full", k
             for t in range(n):
                 r = "ab"[x]
-                yield (r, "full", pos % rings[r]), pos // rings[r]
                 if used[t & 1]:
                     yield ("free", t & 1), used[t & 1] - 1
                 used[t & 1] += 1
+                for slot, phase in regions(r, pos):
+                    yield (r, "full", slot), phase
+                    if r != acc_ring:
+                        commits[x].append((r, "empty", slot))
                 commits[x].append(("s", t & 1))
-                if r != acc_ring:
-                    commits[x].append((r, "empty", pos % rings[r]))
                 if t == n - 1:
                     commits[x].append("fix_empty")
                 pos += 1
@@ -329,7 +335,7 @@ def run_long(segments, stages, apart, dp, seed):
     schedule(rng, bars, commits, warps)
 
 
-@pytest.mark.parametrize("stages,apart,dp", [(2, False, False), (3, False, False), (4, False, False), ((2, 3), True, False), ((2, 1), True, True)])
+@pytest.mark.parametrize("stages,apart,dp", [(2, False, False), (3, False, False), (4, False, False), ((2, 3), True, False), ((2, 4), True, True)])
 def test_the_kernel_of_longer_sequences(stages, apart, dp):
     for seed in range(400):
         rng = random.Random(seed)

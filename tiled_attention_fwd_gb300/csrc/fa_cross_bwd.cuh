@@ -34,7 +34,7 @@ constexpr int kBwdSegRing = 4;
 
 // d = 256 (MODE 1, 3, 4).  The streamed tensors have a ring each: A holds what S is made of (Q, or K), B the other.  The
 // accumulations read A, too (dV's: B); the one that only a first product reads needs fewer slots, and 64 rows a tile
-// fit where pairs of tiles left room for 32 (half as many products; 6 sequences of 100 to 700 rows: ROWS64).
+// fit where pairs of tiles left room for 32 (half as many products; 6 sequences of 100 to 700 rows: 172 to 160 us, and 157 with regions).
 template <int MODE>
 struct BwdWideCfg {
   static constexpr bool DP = MODE != 3;
@@ -47,11 +47,15 @@ struct BwdWideCfg {
   static constexpr int FIX_REGION = BM * SWB, S_REGION = BS * SWB;
   static constexpr int FIX_TILE = BM * 512, S_TILE = BS * 512;
   static constexpr int VEC_BYTES = BS * 4;
-  static constexpr int NA = 2, NB = DP ? 1 : 3;  // slots
+  static constexpr int NA = 2;            // slots
+  // dQ, dK: one slot for what dP alone reads, loaded and freed region by region (64 columns, four products), so that most of a tile is on
+  // its way again while the rest is multiplied; dV: whole tiles.
+  static constexpr int NB = DP ? NR : 3;
+  static constexpr int B_BYTES = DP ? S_REGION : S_TILE;
   static constexpr int OFF_FIX = 0;
   static constexpr int OFF_A = (DP ? 2 : 1) * FIX_TILE;  // dV: K alone
   static constexpr int OFF_B = OFF_A + NA * S_TILE;
-  static constexpr int OFF_MISC = OFF_B + NB * S_TILE;
+  static constexpr int OFF_MISC = OFF_B + NB * B_BYTES;
   // The ring that the accumulations read; the vectors come with its tiles.
   static constexpr int NST = DP ? NA : NB;
   static constexpr int STAGE = S_TILE;
@@ -218,7 +222,7 @@ struct CrossBwdBars<256, MODE> {
   __device__ __forceinline__ uint32_t a_full(int i) const { return b0 + 16 + 8u * i; }
   __device__ __forceinline__ uint32_t a_empty(int i) const { return b0 + 32 + 8u * i; }
   __device__ __forceinline__ uint32_t b_full(int i) const { return b0 + 48 + 8u * i; }
-  __device__ __forceinline__ uint32_t b_empty(int i) const { return b0 + 72 + 8u * i; }
+  __device__ __forceinline__ uint32_t b_empty(int i) const { return b0 + 184 + 8u * i; }
   __device__ __forceinline__ uint32_t st_full(int i) const { return C::DP ? a_full(i) : b_full(i); }
   __device__ __forceinline__ uint32_t st_empty(int i) const { return C::DP ? a_empty(i) : b_empty(i); }
   __device__ __forceinline__ uint32_t s_full(int b) const { return b0 + 96 + 8u * b; }
@@ -232,7 +236,7 @@ struct CrossBwdBars<256, MODE> {
   __device__ __forceinline__ uint32_t drain_dp() const { return b0 + 176; }
   __device__ __forceinline__ uint32_t seg_full(int i) const { return b0 + 256 + 8u * i; }
   __device__ __forceinline__ uint32_t seg_empty(int i) const { return b0 + 288 + 8u * i; }
-  static_assert(C::NA <= 2 && C::NB <= 3, "barrier area");
+  static_assert(C::NA <= 2 && C::NB <= 4, "barrier area");
 };
 
 // Products of d = 256.
@@ -256,14 +260,17 @@ struct BwdWideMma {
     static constexpr __host__ __device__ uint32_t db(int) { return 16 * C::SWB >> 4; }
   };
   uint32_t tmem, base;
-  // X = 0: S = A1 A^T, 1: dP = A2 B^T, with the tile in `slot` of its ring, into buffer b.
-  template <int X>
-  __device__ __forceinline__ void first(uint32_t slot, int b) const {
-    const uint32_t d = tmem + (X ? C::TM_DP : C::TM_S) + b * C::BS;
-    const uint32_t x = sdesc_lo(base + C::OFF_FIX + X * C::FIX_TILE, 16);
-    const uint32_t y = sdesc_lo(base + (X ? C::OFF_B : C::OFF_A), 16) + slot * (C::S_TILE >> 4);
+  // S = A1 A^T with the tile in `slot` of ring A, into buffer b.
+  __device__ __forceinline__ void s(uint32_t slot, int b) const {
+    const uint32_t d = tmem + C::TM_S + b * C::BS, x = sdesc_lo(base + C::OFF_FIX, 16);
+    const uint32_t y = sdesc_lo(base + C::OFF_A, 16) + slot * (C::S_TILE >> 4);
     mma_ss_run<8, Steps<0>>(d, x, HI, y, HI, IDESC_S, 0u);
     mma_ss_run<8, Steps<8>>(d, x + k_step<C::FIX_REGION>(8), HI, y + k_step<C::S_REGION>(8), HI, IDESC_S, 1u);
+  }
+  // Region r of dP = A2 B^T, into buffer b.
+  __device__ __forceinline__ void dp(uint32_t r, int b) const {
+    mma_ss_run<4, Steps<0>>(tmem + C::TM_DP + b * C::BS, sdesc_lo(base + C::OFF_FIX + C::FIX_TILE, 16) + r * (C::FIX_REGION >> 4), HI,
+                            sdesc_lo(base + C::OFF_B, 16) + r * (C::S_REGION >> 4), HI, IDESC_S, r > 0 ? 1u : 0u);
   }
   // dQ (+)= dS K, dV (+)= P^T dO, dK (+)= dS^T Q.
   __device__ __forceinline__ void add(uint32_t slot, int b, bool acc) const {
@@ -450,22 +457,18 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
     last_fix = k;
     for (int t = 0; t < w.n; ++t) {
       if constexpr (D == 256) {
-        // A tile of ring A, then one of ring B.
         const int rows = C::BY_KEY ? t0 * group : C::BS;
         const int s = w.s0 + t, h = C::BY_KEY ? w.head * group : w.head;
         const int row = w.str0 + s * (C::BY_KEY ? t0 : C::BS);
-#pragma unroll
-        for (int x = 0; ok && x < 2; ++x) {
-          const int n = x ? C::NB : C::NA;
-          const int slot = pos % n;
-          const uint32_t par = (pos / n) & 1;
-          if (!(ok = warp_wait_bar(x ? bar.b_empty(slot) : bar.a_empty(slot), par ^ 1, g, kStatusTimeoutLoad))) break;
+        // Into slot `slot` of a ring (A: x = 0): the regions [r0, r1), and the vectors.
+        auto load = [&](int x, int slot, uint32_t par, int r0, int r1, bool vecs) -> bool {
+          if (!warp_wait_bar(x ? bar.b_empty(slot) : bar.a_empty(slot), par ^ 1, g, kStatusTimeoutLoad)) return false;
           if (lane == 0) {
-            const bool vecs = C::BY_KEY && (x == 0) == C::DP;
             const uint32_t full = x ? bar.b_full(slot) : bar.a_full(slot);
-            const uint32_t dst = base + (x ? C::OFF_B : C::OFF_A) + slot * C::S_TILE;
-            mbar_arrive_expect_tx(full, C::NR * rows * C::SWB + (vecs ? (C::DP ? 2 : 1) * C::VEC_BYTES : 0));
-            for (int r = 0; r < C::NR; ++r) tma_load_3d(dst + r * C::S_REGION, x ? tm_b2 : tm_b1, full, r * C::RC, h, row, pol_str);
+            const uint32_t dst = base + (x ? C::OFF_B + slot * C::B_BYTES : C::OFF_A + slot * C::S_TILE);
+            mbar_arrive_expect_tx(full, (r1 - r0) * rows * C::SWB + (vecs ? (C::DP ? 2 : 1) * C::VEC_BYTES : 0));
+            for (int r = r0; r < r1; ++r)
+              tma_load_3d(dst + (r - r0) * C::S_REGION, x ? tm_b2 : tm_b1, full, r * C::RC, h, row, pol_str);
             if (vecs) {
               const long long off = (w.head * p.tiles + w.vec0 + s) * C::BS;
               bulk_load(base + C::off_vec(slot), p.ws.l2 + off, C::VEC_BYTES, full);
@@ -475,7 +478,13 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
           const int bit = x * 4 + slot;
           issued |= 1u << bit;
           last_par = (last_par & ~(1u << bit)) | (par << bit);
-        }
+          return true;
+        };
+        // (What dP alone reads is free first.)
+        if constexpr (C::DP)
+          for (int r = 0; ok && r < C::NR; ++r) ok = load(1, r, pos & 1, r, r + 1, false);
+        ok = ok && load(0, pos % C::NA, (pos / C::NA) & 1, 0, C::NR, C::BY_KEY && C::DP);
+        if constexpr (!C::DP) ok = ok && load(1, pos % C::NB, (pos / C::NB) & 1, 0, C::NR, true);
         if (!ok) break;
         ++pos;
       } else {
@@ -596,7 +605,6 @@ template <int MODE, int X>
 __device__ __forceinline__ void cross_bwd_first(const CrossBwdBars<256, MODE>& bar, uint32_t base, uint8_t* gbase, uint32_t tmem,
                                                 const WaitGuard& g) {
   using C = CrossBwdCfg<256, MODE>;
-  constexpr int N = X ? C::NB : C::NA;
   const BwdWideMma<MODE> M{tmem, base};
   const CrossIssuer is{g};
   uint32_t pos = 0;                // streamed tiles issued
@@ -606,17 +614,29 @@ __device__ __forceinline__ void cross_bwd_first(const CrossBwdBars<256, MODE>& b
     BwdSeg w;
     if (!(ok = bwd_seg_read(w, k, gbase + C::OFF_SEG, bar, g)) || !w.valid) break;
     if (!(ok = is.wait(bar.fix_full(), k & 1))) break;
-    for (int t = 0; t < w.n; ++t, ++pos) {
+    for (int t = 0; ok && t < w.n; ++t, ++pos) {
       const int b = t & 1;
-      const uint32_t slot = pos % N;
       uint32_t& u = b ? used[1] : used[0];
-      if (!(ok = is.wait(X ? bar.b_full(slot) : bar.a_full(slot), (pos / N) & 1))) break;
       if (u > 0 && !(ok = is.wait(bar.buf_free(b), (u - 1) & 1))) break;
       ++u;
-      tc_fence_after();
-      M.template first<X>(slot, b);
-      mma_commit_elect(bar.s_full(b));
-      if (X || !C::DP) mma_commit_elect(X ? bar.b_empty(slot) : bar.a_empty(slot));  // (no other product reads the tile)
+      if constexpr (X == 0) {
+        const uint32_t slot = pos % C::NA;
+        if (!(ok = is.wait(bar.a_full(slot), (pos / C::NA) & 1))) break;
+        tc_fence_after();
+        M.s(slot, b);
+        mma_commit_elect(bar.s_full(b));
+        if (!C::DP) mma_commit_elect(bar.a_empty(slot));  // (no other product reads the tile)
+      } else {
+#pragma unroll 1
+        for (int r = 0; r < C::NR; ++r) {
+          if (!(ok = is.wait(bar.b_full(r), pos & 1))) break;
+          tc_fence_after();
+          M.dp(r, b);
+          mma_commit_elect(bar.b_empty(r));
+        }
+        if (!ok) break;
+        mma_commit_elect(bar.s_full(b));
+      }
       if (t == w.n - 1) mma_commit_elect(bar.fix_empty());
     }
   }
