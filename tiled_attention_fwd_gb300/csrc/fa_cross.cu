@@ -9,8 +9,12 @@
 namespace fa {
 namespace {
 
-// The forward pass is the paged attention's kernels on keys that lie packed: longer sequences (unless max_rows says that there are
-// none), then those of few rows, then what CTAs left in parts.
+// The forward pass is the paged attention's kernels on keys that lie packed (PACKED: a key tile is one TMA box of a sequence's rows, boxes
+// may reach into the next sequence's, whose keys are masked and whose values are cleared): longer sequences (unless max_rows says that
+// there are none), then those of few rows, then what CTAs left in parts.  64 sequences of 1 to 5 rows over 512 to 4096 keys, 32 over 8 heads,
+// d = 128: 110 us, 0.83 of the memory's rate (5.6 TB/s); 4 of 1 to 4 K rows over 2 to 8 K keys, d = 128: 355 us, 1.42 PFLOP/s, 0.74;
+// 32 of 17 to 200 rows over 100 to 1024 keys, d = 64: 54 us, bound by tiles of which half the rows, and one of two softmax
+// warpgroups, have nothing to do (letting the two share such a tile's keys made the kernel larger and slower: 66 us).
 template <int D>
 int launch_fwd_d(PagedFwdArgs& a, const LaunchCtx& ctx) {
   const long long most = static_cast<long long>(a.max_rows) * a.group;

@@ -1,6 +1,7 @@
 // Gradients of cross attention over ragged batches: the backward pass's two
 // kernels (fa_bwd_tc.cuh: a key-parallel one for dK and dV, a query-parallel
-// one for dQ, no atomics on results) on work that is found on the device.
+// one for dQ, no atomics on results) on work that is found on the device, and
+// the kernels before and behind them.
 //
 //   P = 2^(scale log2e q k^T - L log2e),  D = sum_c dO O,  dS = P (dO v^T - D),
 //   dV = P^T dO,  dK = scale dS^T Q (both summed over the heads of a group),  dQ = scale dS K.
@@ -22,6 +23,13 @@
 //    streamed tiles) to the other warps through a ring in shared memory.
 //  * Output.  A unit held whole is written as it is finished; parts of others go to
 //    the workspace in fp32 and the joining kernel adds them up in the order of their CTAs.
+//  * Roundings.  P and dS are rounded to bf16 for the products (half a step, 2^-8, of each term), as in the contiguous
+//    pass; S, dP, D, L and all sums are fp32, gradients are rounded once.
+//
+// Bound: at d <= 128 by a tile's way through products and elementwise step (4 of 1 to 4 K rows over 2 to 8 K keys, d = 128: dK and
+// dV 714 us, dQ 479 of 1.28 ms, 0.51 of the tensor cores for the five products that there must be and 0.71 for the seven that
+// this split makes); at d = 256 by the latency of the streamed tiles, of which two fit (6 of 100 to 700 rows: 36 + 46 + 49 of 155 us),
+// then by parts (120 MB through L2, 20 us).  All modes in one launch, CTAs dealt by work, took longer: 1.37 ms and 210 us (then 173).
 #pragma once
 
 #include "fa_bwd_tc.cuh"
@@ -104,7 +112,9 @@ __host__ __device__ __forceinline__ long long bwd_tiles(int rows, int B, int gro
   return rows / bwd_tokens0<D>(group) + static_cast<long long>(B);
 }
 
-// 128-row tiles of a sequence's rows (all heads of a group) that MODE 2 takes at most (d = 256: none).
+// 128-row tiles of a sequence's rows (all heads of a group) that MODE 2 takes at most (d = 256: none): as many as tensor memory holds dQ
+// of.  There it is the faster one up to this bound (32 sequences over 1000 keys, 8 heads, at the bound and at half of it, us, against the
+// kernels of longer sequences: d = 32 119 and 73 against 183 and 115, d = 64 90 and 62 against 145 and 111, d = 128 114 and 94 against 138 and 121).
 constexpr __host__ __device__ int bwd_short_tiles(int d) { return d == 32 ? 4 : d == 64 ? 2 : d == 128 ? 1 : 0; }
 template <int D>
 __host__ __device__ __forceinline__ bool bwd_short(const CrossSeq& s, int group) {
@@ -117,14 +127,18 @@ struct BwdWork {
   static constexpr int STR = BwdBase<D, MODE>::BS;
   static constexpr size_t PART = static_cast<size_t>(128) * BwdBase<D, MODE>::NOUT * BwdBase<D, MODE>::OUTW;  // floats of a part
   // Streamed tiles that a unit costs besides its own (loading the fixed tiles, the output).
-  static constexpr int UNIT_COST = 2;  // (of places on the line, as a streamed tile is one)
+  // (6 sequences of 100 to 700 rows, d = 256, with 1/2/4/6/8/12: 162/157/155/156/156/159 us; of 1 to 4 K rows, d = 128, 1290
+  // with 1 or 2, 1260 to 1280 with more.)
+  static constexpr int UNIT_COST = 4;  // (of places on the line, as a streamed tile is one)
 };
 template <int D>
 struct BwdWork<D, 2> {
   static constexpr int STR = 128;
   static constexpr size_t PART = static_cast<size_t>(128) * bwd_short_tiles(D) * D;
   static constexpr int QT = D <= 64 ? 64 : 32;  // rows of an item (fa_cross_bwd_short.cuh), which is a place on the line
-  static constexpr int TILE_COST = 2;  // items that a streamed tile costs besides its own (its loads, its dK and dV)
+  // Items that a streamed tile costs besides its own (its loads, its dK and dV), and a unit (32 sequences of 17 to 200 rows, d = 64,
+  // with 1/2/4 of the one: 101.4/102.7/106.8 us, with 1/3/6 of the other 108.5/102.7/102.0).
+  static constexpr int TILE_COST = 1;
   static constexpr int UNIT_COST = 3;
 };
 

@@ -122,7 +122,8 @@ struct ChunkCfg : TcCfg<D> {
   static constexpr int ROWS = T::NQT * 128;
   // Key tiles that a unit costs besides its own (its beginning, its end, its output).  Measured on ragged batches, us with
   // 0/1/2/3: prompts, bf16, d = 128: 202/186/190/195; d = 256: 438/387/353/349; chunks, e4m3, with 2/4/5/7: d = 128:
-  // 313/305/303/309, d = 64: 277/261/263/259, d = 256: 567/572/575/581.
+  // 313/305/303/309, d = 64: 277/261/263/259, d = 256: 567/572/575/581; packed keys, with 1/2/3/5: 32 sequences of 17 to 200 rows,
+  // d = 64: 54.2/53.4/53.2/53.1, of 1 to 4 K rows, d = 128: 357/354/357/356.
   static constexpr int UNIT_COST = E4M3 ? (D == 256 ? 2 : 5) : (D == 256 ? 2 : 1);
   static_assert(T::OFF_ABORT + 4 <= OFF_SEG && OFF_SEG % 16 == 0, "misc area");
   static_assert(OFF_SEG + kSegRing * static_cast<int>(sizeof(ChunkSeg)) <= T::OFF_MISC + T::MISC, "misc area");
