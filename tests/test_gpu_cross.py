@@ -472,3 +472,44 @@ assert torch.equal(o, x) and torch.equal(lse, l)
 assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), fa.cross_backward(q, k, k, o, lse, o, cu, cu)))
 """
     subprocess.run([sys.executable, "-c", code], check=True, timeout=300, cwd=str(__import__("pathlib").Path(__file__).parent.parent))
+
+
+# ------------------------------------------------------------------ heads in pairs (d <= 64)
+@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("heads,group", [(2, 1), (3, 1), (5, 3), (3, 32), (7, 5)])
+def test_heads_in_pairs_and_the_odd_one(heads, group, d):
+    s = Ragged([40, 1, 0, 150, 17, 3], [100, 333, 50, 129, 0, 64], heads, group, d, padded=True, fused=True, lead=2, pad=3, seed=heads)
+    o, lse = forward(s)
+    check_forward(s, o, lse)
+
+
+@pytest.mark.parametrize("rows,keys", [([1, 20], [20000, 9001]), ([130], [9001]), ([3001], [200])])
+def test_pairs_that_are_split_and_joined(rows, keys):
+    s = Ragged(rows, keys, 3, 2, 64, seed=rows[0])
+    o, lse = forward(s)
+    check_forward(s, o, lse)
+    for _ in range(2):
+        again = forward(s)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
+def test_pairs_leave_and_report_what_is_not_there():
+    s = Ragged([18, 40, 2], [70, 90, 33], 3, 1, 64, seed=4)
+    q, _, k, v = s.tensors()
+    cu_rows, cu_keys, _ = s.batch()
+    o = torch.full((s.T, 3, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((3, s.T), 7.0, device="cuda")
+    fa.cross_forward(q, k, v, cu_rows, cu_keys, max_rows=39, out=o, lse=lse)
+    with pytest.raises(fa.FAError):
+        fa.check_status()
+    want, want_lse = forward(s)
+    mine = torch.ones(s.T, dtype=torch.bool, device="cuda")
+    mine[18:58] = False
+    assert torch.equal(o[mine], want[mine]) and torch.equal(lse[:, mine], want_lse[:, mine])
+    assert (o[~mine] == 7.0).all() and (lse[:, ~mine] == 7.0).all()
+    bad = cu_keys.clone()
+    bad[-1] = s.K + 1
+    fa.cross_forward(q, k, v, cu_rows, bad, max_rows=40, out=o, lse=lse)
+    with pytest.raises(fa.FAError):
+        fa.check_status()
+    assert torch.equal(o[:58], want[:58]) and (o[58:] == 0).all() and torch.isneginf(lse[:, 58:]).all()

@@ -12,12 +12,21 @@ namespace {
 // The forward pass is the paged attention's kernels on keys that lie packed (PACKED: a key tile is one TMA box of a sequence's rows, boxes
 // may reach into the next sequence's, whose keys are masked and whose values are cleared): longer sequences (unless max_rows says that
 // there are none), then those of few rows, then what CTAs left in parts.  64 sequences of 1 to 5 rows over 512 to 4096 keys, 32 over 8 heads,
-// d = 128: 110 us, 0.83 of the memory's rate (5.6 TB/s); 4 of 1 to 4 K rows over 2 to 8 K keys, d = 128: 355 us, 1.42 PFLOP/s, 0.74;
-// 32 of 17 to 200 rows over 100 to 1024 keys, d = 64: 54 us, bound by tiles of which half the rows, and one of two softmax
-// warpgroups, have nothing to do (letting the two share such a tile's keys made the kernel larger and slower: 66 us).
+// d = 128: 110 us, 0.83 of the memory's rate (5.6 TB/s); 4 of 1 to 4 K rows over 2 to 8 K keys, d = 128: 355 us, 1.42 PFLOP/s, 0.74.
+//
+// d <= 64: the chunk kernel takes the heads in pairs (PAIRED), and all sequences, for its stages hold tiles of two heads then and single tiles read
+// keys as fast as they come: 32 sequences of 17 to 200 rows over 100 to 1024 keys, d = 64, 16 heads: 39 us instead of 57.  Against the
+// others in us, 16 heads, d = 64 (d = 32, 8 heads): 32 sequences of 40 rows over 600 keys 29 against 38 (26, 34: 16 heads), of 256 46 and 52 (27 and 29), 4
+// of 2048 over 4096 147 and 154 (75 and 77); 63 of one row and one of 100 over 2000 98 and 153.  Up to 16 rows the few-row kernel alone is
+// the faster one: 32 of 16 over 1000 34 and 39, of 5 28 and 39 (of 17 to 32 it is not: 41 and 29).
 template <int D>
 int launch_fwd_d(PagedFwdArgs& a, const LaunchCtx& ctx) {
   const long long most = static_cast<long long>(a.max_rows) * a.group;
+  a.paired = D <= 64 && a.kv.heads > 1 && most > 16;
+  if (a.paired) {
+    const int e = launch_paged_chunk<D, true>(a, ctx);
+    return e != 0 ? e : launch_paged_join<D, true>(a, true, ctx);
+  }
   // 8 or 16 rows where that is all there can be, else 32 (d = 256: 16), as fa_paged_fwd.
   a.few_rows = most <= 8 ? 8 : most <= 16 || D == 256 ? 16 : kFewMost;
   a.few_sets = 1;

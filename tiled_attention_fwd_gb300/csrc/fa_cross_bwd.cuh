@@ -191,7 +191,7 @@ struct alignas(16) BwdSeg {
   int vec0;   // its first tile of the vectors
   int s0;     // first streamed tile
   int n;      // streamed tiles
-  int unused;
+  int pad;
   int out;    // 0: the unit is whole; 1, 2: part 0, part 1 of this CTA
 };
 static_assert(sizeof(BwdSeg) == 48, "segment size");
@@ -210,7 +210,6 @@ struct CrossBwdCfg : BwdBase<D, MODE> {
   static constexpr bool ACC_APART = D == 256;
   static constexpr int ACC_WARP = C::LOAD_WARP + 1;
   static constexpr bool DP_APART = ACC_APART && DP;
-  static constexpr int DP_WARP = ACC_WARP + 1;
   static constexpr int THREADS = DP_APART ? 384 : ACC_APART ? 352 : 320;
   static constexpr int READERS = THREADS / 32 - 1;
   // A stage's vectors.

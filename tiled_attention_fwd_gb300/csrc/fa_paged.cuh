@@ -128,6 +128,7 @@ struct PagedFwdArgs {
   int max_rows;
   int few_rows;  // rows (tokens x group) of a sequence that the few-row kernel takes at most
   int few_sets;  // its launches (1 or 2)
+  bool paired;   // blocks of the chunk kernel are one tile of two key/value heads
   float scale;
   bool causal;
   bool e4m3;

@@ -21,6 +21,8 @@
 //    two more turn them (d >= 128: in place) into the bf16 tiles that the tensor
 //    core reads (exact: a code has 4 significant bits and a scale is a power of
 //    two), so the rest of the pipeline is the same.
+//  * Short sequences over packed keys (PAIRED, d <= 64).  A query block is one tile, and the two tiles in flight are those of two
+//    key/value heads, each with a K and a V tile in the stage: alone, a tile waits for its products and they for it.
 //  * Output.  A unit held whole is written as it is finished; of others O and
 //    the log-sum (base 2) go to the workspace in fp32 and the joining kernel
 //    adds them up: O = sum 2^(L_i - L) O_i, L = log2 sum 2^L_i.
@@ -76,7 +78,7 @@ __device__ __forceinline__ uint32_t mbar_try_wait_ns(uint32_t bar, uint32_t pari
 struct alignas(16) ChunkSeg {
   int valid;
   int b;
-  int head;   // key/value head
+  int head;   // key/value head; PAIRED: of tile 0, the next one is tile 1's
   int row0;   // row of the block's first token
   int ntok;   // tokens of the block
   int pos0;   // position of its first token; packed keys: row of the sequence's first key
@@ -122,8 +124,8 @@ struct ChunkCfg : TcCfg<D> {
   static constexpr int ROWS = T::NQT * 128;
   // Key tiles that a unit costs besides its own (its beginning, its end, its output).  Measured on ragged batches, us with
   // 0/1/2/3: prompts, bf16, d = 128: 202/186/190/195; d = 256: 438/387/353/349; chunks, e4m3, with 2/4/5/7: d = 128:
-  // 313/305/303/309, d = 64: 277/261/263/259, d = 256: 567/572/575/581; packed keys, with 1/2/3/5: 32 sequences of 17 to 200 rows,
-  // d = 64: 54.2/53.4/53.2/53.1, of 1 to 4 K rows, d = 128: 357/354/357/356.
+  // 313/305/303/309, d = 64: 277/261/263/259, d = 256: 567/572/575/581; packed keys, d = 128, 4 of
+  // 1 to 4 K rows, with 1/2/3/5: 357/354/357/356.
   static constexpr int UNIT_COST = E4M3 ? (D == 256 ? 2 : 5) : (D == 256 ? 2 : 1);
   static_assert(T::OFF_ABORT + 4 <= OFF_SEG && OFF_SEG % 16 == 0, "misc area");
   static_assert(OFF_SEG + kSegRing * static_cast<int>(sizeof(ChunkSeg)) <= T::OFF_MISC + T::MISC, "misc area");
@@ -210,22 +212,30 @@ struct ChunkBlocks {
   }
 };
 
-template <int D, bool E4M3>
+// Units of a query block: its heads, or pairs of them.
+template <bool PAIRED>
+__host__ __device__ __forceinline__ int chunk_heads(const ChunkParams& p) { return PAIRED ? (p.a.kv.heads + 1) / 2 : p.a.kv.heads; }
+
+// What a unit costs besides its key tiles (PAIRED, with 0/1/2/3/5: 32 sequences of 17 to 200 rows, d = 64: 45.7/41.0/39.4/40.2/41.1 us).
+template <int D, bool E4M3, bool PAIRED>
+constexpr __host__ __device__ int chunk_unit() { return PAIRED ? 2 : ChunkCfg<D, E4M3>::UNIT_COST; }
+
+template <int D, bool E4M3, bool PAIRED>
 __host__ __device__ __forceinline__ ChunkBlocks chunk_blocks(const ChunkParams& p, const PagedSeq& s) {
   ChunkBlocks c;
   const bool mine = s.n >= 1 && s.n <= p.a.max_rows && (s.n > kFewMost || s.n * p.a.group > p.a.few_rows);
   c.n = mine ? s.n : 0;
   c.len = s.len;
-  c.tq = p.tpt * TcCfg<D>::NQT;
+  c.tq = p.tpt * (PAIRED ? 1 : TcCfg<D>::NQT);
   c.bk = TcCfg<D>::BK;
-  c.unit = ChunkCfg<D, E4M3>::UNIT_COST;
+  c.unit = chunk_unit<D, E4M3, PAIRED>();
   c.causal = p.a.causal;
   return c;
 }
 
 // ------------------------------------------------------------------ segments
 // The load warp's walk over its CTA's share.
-template <int D, bool E4M3, bool PACKED>
+template <int D, bool E4M3, bool PACKED, bool PAIRED>
 struct ChunkWalk {
   using C = ChunkCfg<D, E4M3>;
   int b, q, head, j, nt;
@@ -237,14 +247,14 @@ struct ChunkWalk {
   __host__ __device__ __forceinline__ void load(const ChunkParams& p) {
     bool bad;
     s = attn_seq<PACKED>(p.a.pb, p.a.cb, p.a.kv.ps_log2, b, bad);
-    c = chunk_blocks<D, E4M3>(p, s);
+    c = chunk_blocks<D, E4M3, PAIRED>(p, s);
   }
   // On to the next unit, if the share reaches it.
   __host__ __device__ __forceinline__ void advance(const ChunkParams& p) {
-    pos += nt - j + C::UNIT_COST;
+    pos += nt - j + chunk_unit<D, E4M3, PAIRED>();
     j = 0;
     if (pos >= end) return;
-    if (++head == p.a.kv.heads) {
+    if (++head == chunk_heads<PAIRED>(p)) {
       head = 0;
       ++q;
       while (q == c.count()) {
@@ -262,7 +272,7 @@ struct ChunkWalk {
     const int n = end - pos < nt - j ? static_cast<int>(end - pos) : nt - j;
     g.valid = 1;
     g.b = b;
-    g.head = head;
+    g.head = PAIRED ? 2 * head : head;
     g.row0 = s.row0 + q * c.tq;
     g.ntok = ntok;
     g.pos0 = PACKED ? s.key0 : s.len - s.n + q * c.tq;
@@ -270,7 +280,9 @@ struct ChunkWalk {
     g.j0 = j;
     g.nmax = n;
     g.n0 = n;
-    if (ntok > p.tpt) {
+    if (PAIRED) {
+      g.n1 = g.head + 1 < p.a.kv.heads ? n : 0;
+    } else if (ntok > p.tpt) {
       // Tile 0's tokens come first: they may be done with their keys before tile 1's.
       const int first = c.tiles(q, p.tpt) - j;
       g.n0 = first < 0 ? 0 : first < n ? first : n;
@@ -438,7 +450,7 @@ __device__ __forceinline__ bool chunk_load_stage(const CUtensorMap* tm_k, const 
 
 // The same of packed keys: whole tiles (behind the last key: the next sequence's, or zeros behind the tensor); lane i loads
 // position i.
-template <int D>
+template <int D, bool PAIRED>
 __device__ __forceinline__ bool chunk_load_packed(const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                                   const ChunkBars<D, false>& bar, uint32_t base, uint32_t pos, int which,
                                                   const ChunkTile& t0, const ChunkTile& t1, ChunkLoaded& done,
@@ -446,17 +458,19 @@ __device__ __forceinline__ bool chunk_load_packed(const CUtensorMap* tm_k, const
   using C = ChunkCfg<D, false>;
   const int lane = threadIdx.x & 31;
   const uint64_t pol_kv = policy_evict_last();
-  const int st = pos % C::NST;
-  const uint32_t full = bar.kv_full(st), par = (pos / C::NST) & 1;
+  constexpr int NST = PAIRED ? C::NST / 2 : C::NST, HEADS = PAIRED ? 2 : 1;  // PAIRED: stages of four tiles, {V, K} of each head
+  const int st = pos % NST;
+  const uint32_t full = bar.kv_full(st), par = (pos / NST) & 1;
   const bool has0 = which & 1, has1 = (which & 2) && t1.kind;
   if (!chunk_wait(bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
-  if (lane == 0) mbar_arrive_expect_tx(full, (has0 + has1) * C::KV_TILE);
+  if (lane == 0) mbar_arrive_expect_tx(full, HEADS * (has0 + has1) * C::KV_TILE);
   __syncwarp();
-  if (lane == 0 ? has0 : lane == 1 && has1) {
-    const ChunkTile& t = lane == 0 ? t0 : t1;
-    const uint32_t dst = base + C::OFF_KV + st * C::STAGE + lane * C::KV_TILE;
+  // (A lane a tile.  PAIRED: of an odd number of heads the last pair's second head lies outside the tensor and reads as zeros.)
+  if (lane < 2 * HEADS && (lane % 2 == 0 ? has0 : has1)) {
+    const ChunkTile& t = lane % 2 == 0 ? t0 : t1;
+    const uint32_t dst = base + C::OFF_KV + st * HEADS * C::STAGE + lane * C::KV_TILE;
     for (int r = 0; r < C::NR; ++r)
-      tma_load_3d(dst + r * C::K_REGION, t.kind == 1 ? tm_k : tm_v, full, r * C::RC, t.head, t.base + t.key0, pol_kv);
+      tma_load_3d(dst + r * C::K_REGION, t.kind == 1 ? tm_k : tm_v, full, r * C::RC, t.head + lane / 2, t.base + t.key0, pol_kv);
   }
   done.issued |= 1u << st;
   done.last_par = (done.last_par & ~(1u << st)) | (par << st);
@@ -465,7 +479,7 @@ __device__ __forceinline__ bool chunk_load_packed(const CUtensorMap* tm_k, const
 
 // The load warp, or the second one (bf16), which reads the segments that the first finds and loads the tiles at
 // position 1.
-template <int D, bool E4M3, bool PACKED>
+template <int D, bool E4M3, bool PACKED, bool PAIRED>
 __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                            const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint32_t base,
                                            uint8_t* gbase, const PlanShare& share, bool second, const WaitGuard& g) {
@@ -477,7 +491,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
   int last_q = -1;           // latest segment whose Q tiles were loaded
   bool recorded = false;
 
-  ChunkWalk<D, E4M3, PACKED> walk;
+  ChunkWalk<D, E4M3, PACKED, PAIRED> walk;
   walk.pos = share.start;
   walk.end = share.end;
   if (walk.pos < walk.end && !second) {
@@ -491,8 +505,8 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
       int nt = 0;
       if (q < walk.c.count()) {
         nt = walk.c.tiles(q, walk.c.tokens(q));
-        first = p.a.kv.heads * walk.c.before(q);
-        here = first <= share.offset && share.offset < first + static_cast<long long>(p.a.kv.heads) * (nt + C::UNIT_COST);
+        first = chunk_heads<PAIRED>(p) * walk.c.before(q);
+        here = first <= share.offset && share.offset < first + static_cast<long long>(chunk_heads<PAIRED>(p)) * (nt + chunk_unit<D, E4M3, PAIRED>());
       }
       const uint32_t who = __ballot_sync(0xffffffffu, here);
       if (who != 0) {
@@ -500,8 +514,8 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
         walk.q = q0 + from;
         walk.nt = __shfl_sync(0xffffffffu, nt, from);
         const long long in = share.offset - __shfl_sync(0xffffffffu, first, from);
-        walk.head = static_cast<int>(in / (walk.nt + C::UNIT_COST));
-        walk.j = static_cast<int>(in - static_cast<long long>(walk.head) * (walk.nt + C::UNIT_COST));
+        walk.head = static_cast<int>(in / (walk.nt + chunk_unit<D, E4M3, PAIRED>()));
+        walk.j = static_cast<int>(in - static_cast<long long>(walk.head) * (walk.nt + chunk_unit<D, E4M3, PAIRED>()));
         if (walk.j >= walk.nt) walk.advance(p);  // behind a unit's tiles: its first tile is the next unit's
         break;
       }
@@ -536,7 +550,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
         mbar_arrive_expect_tx(bar.q_full(t), p.tpt * p.a.group * D * 2);
         for (int r = 0; r < C::NR; ++r)
           tma_load_3d(base + C::OFF_Q + t * C::Q_TILE + r * C::Q_REGION, tm_q, bar.q_full(t), r * C::RC,
-                      w.head * p.a.group, w.row0 + t * p.tpt, pol_q);
+                      (w.head + (PAIRED ? t : 0)) * p.a.group, w.row0 + (PAIRED ? 0 : t * p.tpt), pol_q);
       }
     }
     last_q = k;
@@ -546,7 +560,7 @@ __device__ __forceinline__ void chunk_load(const CUtensorMap* tm_q, const CUtens
     const int which = C::LOADERS == 1 ? 3 : second ? 2 : 1;
     bool ok;
     if constexpr (PACKED)
-      ok = chunk_load_packed<D>(tm_k, tm_v, bar, base, pos, which, t0, t1, done, g);
+      ok = chunk_load_packed<D, PAIRED>(tm_k, tm_v, bar, base, pos, which, t0, t1, done, g);
     else
       ok = chunk_load_stage<D, E4M3>(tm_k, tm_v, p, bar, base, pos, which, t0, t1, done, g);
     ++pos;
@@ -685,7 +699,7 @@ __device__ __forceinline__ bool chunk_convert(const ChunkParams& p, const ChunkB
 
 // ------------------------------------------------------------------ MMA issuer
 // tc_mma's order of products, segment by segment.
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool PAIRED>
 __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint32_t base,
                                           uint8_t* gbase, uint32_t tmem, const WaitGuard& g) {
   using C = ChunkCfg<D, E4M3>;
@@ -698,12 +712,15 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<
   uint32_t go0 = 0;
   bool ok = true;
   auto stage_acquire = [&](uint32_t& st) -> bool {
-    st = pos % C::NST;
-    const bool r = wait(bar.kv_full(st), (pos / C::NST) & 1);
+    constexpr int NST = PAIRED ? C::NST / 2 : C::NST;
+    st = pos % NST;
+    const bool r = wait(bar.kv_full(st), (pos / NST) & 1);
     ++pos;
     if (r) tc_fence_after();
     return r;
   };
+  // Position of query tile t's first tile of stage st (its second is the next one).
+  auto at = [](int t, uint32_t st) -> uint32_t { return PAIRED ? 4 * st + 2 * t : 2 * st; };
   // V rows behind the sequence's end in the tile at stage st (key tile j of w): zeros.
   auto clear_tail = [&](const ChunkSeg& w, int j, uint32_t st) {
     if constexpr (!E4M3) {
@@ -711,9 +728,11 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<
       if (end >= C::BK) return;
       const int from = end < 0 ? 0 : end;
       constexpr int UR = C::SWB / 16;
-      const uint32_t vt = base + C::OFF_KV + 2 * st * C::KV_TILE;
-      for (int r = 0; r < C::NR; ++r)
-        for (int i = from * UR + lane; i < C::BK * UR; i += 32) st_shared_v4(vt + r * C::V_REGION + i * 16, 0, 0, 0, 0);
+      for (int h = 0; h < (PAIRED ? 2 : 1); ++h) {
+        const uint32_t vt = base + C::OFF_KV + at(h, st) * C::KV_TILE;
+        for (int r = 0; r < C::NR; ++r)
+          for (int i = from * UR + lane; i < C::BK * UR; i += 32) st_shared_v4(vt + r * C::V_REGION + i * 16, 0, 0, 0, 0);
+      }
       fence_proxy_async_smem();
       __syncwarp();
     }
@@ -724,13 +743,13 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<
   ok = get(0, w);
   if constexpr (C::NQT == 2) {
     auto tiles_of = [](const ChunkSeg& x, int t) -> int { return t == 0 ? x.n0 : x.n1; };
-    // S of key tile 0 of segment k for both tiles, K_0 at position kpos.
-    auto first_qk = [&](const ChunkSeg& x, int k, uint32_t kpos) -> bool {
+    // S of key tile 0 of segment k for both tiles, K_0 at position `second` of stage st.
+    auto first_qk = [&](const ChunkSeg& x, int k, uint32_t st, int second) -> bool {
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
         if (!wait(bar.q_full(t), k & 1)) return false;
         tc_fence_after();
-        if (tiles_of(x, t) > 0) M.qk(t, t, kpos, bar.s_full(t));
+        if (tiles_of(x, t) > 0) M.qk(t, t, at(t, st) + second, bar.s_full(t));
         if (tiles_of(x, t) <= 1) M.commit(bar.q_empty(t));
       }
       return true;
@@ -761,25 +780,25 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<
             if (!(ok = wait(bar.pv_go(t, 0), par))) break;
             tc_fence_after();
             if constexpr (C::PV_SPLIT) {
-              M.pv_half(t, t, 2 * st, 0, j > 0);
+              M.pv_half(t, t, at(t, st), 0, j > 0);
               if (!(ok = wait(bar.pv_go(t, 1), par))) break;
               tc_fence_after();
-              M.pv_half(t, t, 2 * st, 1, true);
+              M.pv_half(t, t, at(t, st), 1, true);
             } else {
-              M.pv(t, t, 2 * st, j > 0);
+              M.pv(t, t, at(t, st), j > 0);
             }
             go ^= 1u << t;
             if (j == n - 1) {
               M.commit(bar.o_done(t));
             } else {
-              M.qk(t, t, 2 * st + 1, bar.s_full(t));
+              M.qk(t, t, at(t, st) + 1, bar.s_full(t));
               if (j + 1 == n - 1) M.commit(bar.q_empty(t));
             }
           }
         }
         // The next segment's first products (in the stage of this one's last V; the very first K_0 stands alone).
         if (ok && (j < 0 || (j == w.nmax - 1 && wn.valid)))
-          ok = first_qk(j < 0 ? w : wn, j < 0 ? k : k + 1, j < 0 ? 2 * st : 2 * st + 1);
+          ok = first_qk(j < 0 ? w : wn, j < 0 ? k : k + 1, st, j < 0 ? 0 : 1);
         if (ok) M.commit(bar.kv_empty(st));
       }
       begun = true;
@@ -826,7 +845,7 @@ __device__ __forceinline__ void chunk_mma(const ChunkParams& p, const ChunkBars<
 
 // ------------------------------------------------------------------ softmax
 // tc_softmax with the rows' limits taken from the segment.
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool PAIRED>
 __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkBars<D, E4M3>& bar, uint8_t* gbase,
                                               uint32_t tmem, int wg, int quarter, int lane, const WaitGuard& g) {
   using C = ChunkCfg<D, E4M3>;
@@ -842,7 +861,8 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
   uint32_t s_waits = 0;
   int fin = 0;  // units finished by this warpgroup
   bool ok = true;
-  const int tok_r = min(wg * p.tpt + r / p.a.group, (wg + 1) * p.tpt - 1);  // this row's token within the block
+  const int w0 = PAIRED ? 0 : wg * p.tpt;  // the tile's first token
+  const int tok_r = min(w0 + r / p.a.group, w0 + p.tpt - 1);  // this row's token within the block
 
   for (int uk = 0; ok; ++uk) {
     int n, j0, lim0, min_lim, len;
@@ -855,7 +875,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
       len = w.len;
       // Rows behind the block's last token take that one's limit (they are not written).
       lim0 = p.a.causal ? w.pos0 + min(tok_r, w.ntok - 1) : w.len - 1;
-      min_lim = p.a.causal ? w.pos0 + wg * p.tpt : w.len - 1;
+      min_lim = p.a.causal ? w.pos0 + w0 : w.len - 1;
     }
     if (n == 0) continue;
     lim0 = min(lim0, len - 1);
@@ -1010,7 +1030,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkParams& p, const ChunkB
 }
 
 // ------------------------------------------------------------------ correction + output
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool PAIRED>
 __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUtensorMap* tm_o,
                                                  const ChunkBars<D, E4M3>& bar, uint32_t base, uint8_t* gbase,
                                                  uint32_t tmem, int quarter, int lane, const WaitGuard& g) {
@@ -1092,10 +1112,11 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUt
     const float lrow = stat_l[su * 256 + t * 128 + r];
     const float inv_l = lrow == 0.f ? 0.f : 1.f / lrow;
     const uint64_t il2 = f2_pack(inv_l, inv_l);
-    const int tok = t * p.tpt + tok_r;
+    const int w0 = PAIRED ? 0 : t * p.tpt, kv_head = PAIRED ? w.head + t : w.head;  // the tile's first token, its head
+    const int tok = w0 + tok_r;
     const bool mine = tok_r < p.tpt && tok < w.ntok;
     const uint32_t to = tmem + lane_off + C::TM_O + t * D;
-    const int hq = w.head * p.a.group + head_r;
+    const int hq = kv_head * p.a.group + head_r;
     // Where this row of O is (-1: it is no row).
     const long long row_off =
         mine ? static_cast<long long>(w.row0 + tok) * p.a.os[0] + static_cast<long long>(hq) * p.a.os[1] : -1ll;
@@ -1103,8 +1124,8 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUt
     float4* pblk = reinterpret_cast<float4*>(part + C::ROWS + static_cast<size_t>(t) * 128 * D) + r;
     // All 32 rows of this warp are rows of O: a box of min(G, 32) heads.
     const int in = quarter * 32 / p.a.group;
-    const bool boxed = p.tma_o && t * p.tpt + (quarter * 32 + 31) / p.a.group < w.ntok;
-    const int box_head = w.head * p.a.group + (quarter * 32 - in * p.a.group), box_row = w.row0 + t * p.tpt + in;
+    const bool boxed = p.tma_o && w0 + (quarter * 32 + 31) / p.a.group < w.ntok;
+    const int box_head = kv_head * p.a.group + (quarter * 32 - in * p.a.group), box_row = w.row0 + w0 + in;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t v[32];
@@ -1250,7 +1271,7 @@ __device__ __forceinline__ void chunk_correction(const ChunkParams& p, const CUt
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, bool E4M3, bool PACKED = false>
+template <int D, bool E4M3, bool PACKED = false, bool PAIRED = false>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     fa_paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -1309,14 +1330,23 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
     tmem_relinquish();
   }
+  if (PAIRED && blockIdx.x == 0) {  // (else the few-row kernel behind this one looks)
+    bool any = false;
+    for (int b = threadIdx.x; b < p.a.pb.B; b += C::THREADS) {
+      bool bad;
+      const PagedSeq s = attn_seq<PACKED>(p.a.pb, p.a.cb, p.a.kv.ps_log2, b, bad);
+      any = any || bad || s.n > p.a.max_rows;
+    }
+    if (any) atomicOr(p.status, kStatusBadBatch);
+  }
   const PlanShare share = plan_share<C::THREADS>(
       p.a.pb.B, gridDim.x, blockIdx.x,
       [&](int b) -> long long {
         bool bad;
-        const ChunkBlocks c = chunk_blocks<D, E4M3>(p, attn_seq<PACKED>(p.a.pb, p.a.cb, p.a.kv.ps_log2, b, bad));
-        return c.n == 0 ? 0 : p.a.kv.heads * c.before(c.count());
+        const ChunkBlocks c = chunk_blocks<D, E4M3, PAIRED>(p, attn_seq<PACKED>(p.a.pb, p.a.cb, p.a.kv.ps_log2, b, bad));
+        return c.n == 0 ? 0 : chunk_heads<PAIRED>(p) * c.before(c.count());
       },
-      1 + C::UNIT_COST,
+      1 + chunk_unit<D, E4M3, PAIRED>(),
       *reinterpret_cast<PlanScratch*>(gbase + C::OFF_PLAN));
   tc_fence_before();
   __syncthreads();
@@ -1326,15 +1356,15 @@ __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 
   if (warp < C::SOFTMAX_WARPS) {
     if constexpr (C::SPLIT_REGS) regs_increase<C::REG_SOFTMAX>();
-    chunk_softmax<D, E4M3>(p, bar, gbase, tmem, warp >> 2, warp & 3, lane, g);
+    chunk_softmax<D, E4M3, PAIRED>(p, bar, gbase, tmem, warp >> 2, warp & 3, lane, g);
   } else if (warp < C::SOFTMAX_WARPS + 4) {
     if constexpr (C::SPLIT_REGS) regs_decrease<C::reg_corr(false)>();
-    chunk_correction<D, E4M3>(p, &tm_o, bar, base, gbase, tmem, warp & 3, lane, g);
+    chunk_correction<D, E4M3, PAIRED>(p, &tm_o, bar, base, gbase, tmem, warp & 3, lane, g);
   } else {
     if constexpr (C::SPLIT_REGS) regs_decrease<C::REG_CORR_OTHER - C::reg_corr(false)>();
     if (warp >= C::LOAD_WARP && warp < C::LOAD_WARP + C::LOADERS)
-      chunk_load<D, E4M3, PACKED>(&tm_q, &tm_k, &tm_v, p, bar, base, gbase, share, warp > C::LOAD_WARP, g);
-    if (warp == C::MMA_WARP) chunk_mma<D, E4M3>(p, bar, base, gbase, tmem, g);
+      chunk_load<D, E4M3, PACKED, PAIRED>(&tm_q, &tm_k, &tm_v, p, bar, base, gbase, share, warp > C::LOAD_WARP, g);
+    if (warp == C::MMA_WARP) chunk_mma<D, E4M3, PAIRED>(p, bar, base, gbase, tmem, g);
     if constexpr (E4M3)
       if (warp >= C::CONV_WARP0)
         chunk_convert<D, E4M3>(
@@ -1358,6 +1388,7 @@ struct JoinParams {
   bool chunks;   // the chunk kernel has run
   int few_sets;  // launches of the few-row kernel
   int tpt;
+  bool paired;   // the chunk kernel's blocks are one tile of two heads
 };
 
 // Joins the parts of the units that several CTAs held; blocks (c, .) those of the unit that CTA c began.
@@ -1381,8 +1412,9 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
       for (int job = blockIdx.y * 4 + warp; job < ROWS / 32 * (D / 16); job += gridDim.y * 4) {
         const int r = job % (ROWS / 32) * 32 + lane, c16 = job / (ROWS / 32);
         const int tr = (r & 127) / a.group, head = (r & 127) % a.group;
-        const int tok = (rec.qb * (ROWS / 128) + (r >> 7)) * p.tpt + tr;
-        if (tr >= p.tpt || tok >= s.n) continue;
+        const int kv_head = p.paired ? rec.head + (r >> 7) : rec.head;
+        const int tok = (p.paired ? rec.qb : rec.qb * (ROWS / 128) + (r >> 7)) * p.tpt + tr;
+        if (tr >= p.tpt || tok >= s.n || kv_head >= a.kv.heads) continue;
         float m = -INFINITY;
 #pragma unroll 4
         for (int i = 0; i < n; ++i) m = fmaxf(m, (i == 0 ? first : rest + i * stride)[r]);
@@ -1405,7 +1437,7 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
             o[k].w = fmaf(y.w, f, o[k].w);
           }
         }
-        const int row = s.row0 + tok, hq = rec.head * a.group + head;
+        const int row = s.row0 + tok, hq = kv_head * a.group + head;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         uint4* dst = reinterpret_cast<uint4*>(a.o + static_cast<long long>(row) * a.os[0] +
                                               static_cast<long long>(hq) * a.os[1] + c16 * 16);
@@ -1486,15 +1518,15 @@ __global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constan
 template <int D, bool PACKED>
 int launch_paged_join(const PagedFwdArgs& a, bool chunks, const LaunchCtx& ctx) {
   const int ctas = ctx.num_sms < kPlanCtas ? ctx.num_sms : kPlanCtas;
-  const JoinParams p{a, paged_ws(a.workspace, D), chunks, a.few_sets, 128 / a.group};
+  const JoinParams p{a, paged_ws(a.workspace, D), chunks, a.few_sets, 128 / a.group, a.paired};
   return launch_dependent(fa_paged_join_kernel<D, PACKED>, dim3(ctas, 16), 128, 0, ctx.stream, p);
 }
 
 // ------------------------------------------------------------------ launch
-template <int D, bool E4M3, bool PACKED>
+template <int D, bool E4M3, bool PACKED, bool PAIRED = false>
 int launch_paged_chunk_impl(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   using C = ChunkCfg<D, E4M3>;
-  auto kernel = fa_paged_chunk_kernel<D, E4M3, PACKED>;
+  auto kernel = fa_paged_chunk_kernel<D, E4M3, PACKED, PAIRED>;
   if constexpr (C::SPLIT_REGS) {
     // The register split is sized for exactly LAUNCH_REGS a thread (see launch_tc_impl).
     static std::atomic<int> checked_regs{-1};
@@ -1552,6 +1584,8 @@ template <int D, bool PACKED>
 int launch_paged_chunk(const PagedFwdArgs& a, const LaunchCtx& ctx) {
   if constexpr (!PACKED)
     if (a.e4m3) return launch_paged_chunk_impl<D, true, false>(a, ctx);
+  if constexpr (PACKED && D <= 64)
+    if (a.paired) return launch_paged_chunk_impl<D, false, true, true>(a, ctx);
   return launch_paged_chunk_impl<D, false, PACKED>(a, ctx);
 }
 
