@@ -28,7 +28,7 @@
 //
 // Bound: at d <= 128 by a tile's way through products and elementwise step (4 of 1 to 4 K rows over 2 to 8 K keys, d = 128: dK and
 // dV 714 us, dQ 479 of 1.28 ms, 0.51 of the tensor cores for the five products that there must be and 0.71 for the seven that
-// this split makes); at d = 256 by the latency of the streamed tiles, of which two fit (6 of 100 to 700 rows: 36 + 46 + 49 of 155 us),
+// this split makes); at d = 256 by the latency of the streamed tiles, of which two fit (6 of 100 to 700 rows: some 36 + 46 + 49 under a profiler, of 150.5 us),
 // then by parts (120 MB through L2, 20 us).  All modes in one launch, CTAs dealt by work, took longer: 1.37 ms and 210 us (then 173).
 #pragma once
 
@@ -410,6 +410,19 @@ struct CrossBwdWalk {
   }
 };
 
+// warp_wait_bar; d = 256: all but the first try out of line (with five or six roles and less code 150.5 us instead of 155 at 6 sequences of 100
+// to 700 rows; in the kernels of d <= 128 it costs 1 to 5 %).
+static __device__ __noinline__ bool bwd_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns, int code) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, WaitGuard{abort, status, limit_ns}, code));
+}
+template <int D>
+__device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, const WaitGuard& g, int code) {
+  if constexpr (D == 256)
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || bwd_wait_slow(bar, parity, g.abort, g.status, g.limit_ns, code);
+  else
+    return warp_wait_bar(bar, parity, g, code);
+}
+
 // Segment k of the ring at `ring`, read by a whole warp of a role other than the load warp.
 template <class Bars>
 __device__ __forceinline__ bool bwd_seg_read(BwdSeg& g, int k, const uint8_t* ring, const Bars& bar, const WaitGuard& guard) {
@@ -443,7 +456,7 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
   walk.start(p, share);
   for (int k = 0;; ++k) {
     const int i = k % kBwdSegRing;
-    if (!(ok = warp_wait_bar(bar.seg_empty(i), ((k / kBwdSegRing) & 1) ^ 1, g, kStatusTimeoutLoad))) break;
+    if (!(ok = bwd_wait<D>(bar.seg_empty(i), ((k / kBwdSegRing) & 1) ^ 1, g, kStatusTimeoutLoad))) break;
     const BwdSeg w = walk.next(p);
     if (lane == 0) {
       reinterpret_cast<BwdSeg*>(gbase + C::OFF_SEG)[i] = w;
@@ -456,7 +469,7 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
     warp_arrive(bar.seg_full(i));
     if (!w.valid) break;
     // The fixed tiles: K, V (128 keys of a head), or Q, dO (a group's heads of 128 / G tokens).
-    if (!(ok = warp_wait_bar(bar.fix_empty(), (k & 1) ^ 1, g, kStatusTimeoutLoad))) break;
+    if (!(ok = bwd_wait<D>(bar.fix_empty(), (k & 1) ^ 1, g, kStatusTimeoutLoad))) break;
     if (lane == 0) {
       const int rows = C::BY_KEY ? 128 : t1 * group;
       mbar_arrive_expect_tx(bar.fix_full(), (C::DP ? 2 : 1) * C::NR * rows * C::SWB);
@@ -475,7 +488,7 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
         const int row = w.str0 + s * (C::BY_KEY ? t0 : C::BS);
         // Into slot `slot` of a ring (A: x = 0): the regions [r0, r1), and the vectors.
         auto load = [&](int x, int slot, uint32_t par, int r0, int r1, bool vecs) -> bool {
-          if (!warp_wait_bar(x ? bar.b_empty(slot) : bar.a_empty(slot), par ^ 1, g, kStatusTimeoutLoad)) return false;
+          if (!bwd_wait<D>(x ? bar.b_empty(slot) : bar.a_empty(slot), par ^ 1, g, kStatusTimeoutLoad)) return false;
           if (lane == 0) {
             const uint32_t full = x ? bar.b_full(slot) : bar.a_full(slot);
             const uint32_t dst = base + (x ? C::OFF_B + slot * C::B_BYTES : C::OFF_A + slot * C::S_TILE);
@@ -503,7 +516,7 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
       } else {
         const int st = pos % C::NST;
         const uint32_t par = (pos / C::NST) & 1;
-        if (!(ok = warp_wait_bar(bar.st_empty(st), par ^ 1, g, kStatusTimeoutLoad))) break;
+        if (!(ok = bwd_wait<D>(bar.st_empty(st), par ^ 1, g, kStatusTimeoutLoad))) break;
         if (lane == 0) {
           const uint32_t s0 = base + C::OFF_ST + st * C::STAGE;
           const uint32_t full = bar.st_full(st);
@@ -544,9 +557,11 @@ __device__ __forceinline__ void cross_bwd_load(const CUtensorMap* tm_a1, const C
 }
 
 // ------------------------------------------------------------------ MMA issuer
+template <int D>
 struct CrossIssuer {
   const WaitGuard& g;
   __device__ __forceinline__ bool wait(uint32_t b, uint32_t par) const {
+    if constexpr (D == 256) return bwd_wait<D>(b, par, g, kStatusTimeoutMma);
     const bool r = mbar_test_wait(b, par) || wait_bar(b, par, g, kStatusTimeoutMma);
     return __all_sync(0xffffffffu, r);
   }
@@ -564,7 +579,7 @@ __device__ __forceinline__ void cross_bwd_mma(const CrossBwdBars<D, MODE>& bar, 
                                               uint8_t* gbase, uint32_t tmem, const WaitGuard& g) {
   using C = CrossBwdCfg<D, MODE>;
   const BwdMma<D, MODE> M(tmem, base);
-  const CrossIssuer is{g};
+  const CrossIssuer<D> is{g};
   uint32_t pos = 0;            // streamed stages consumed before the current segment
   uint32_t pr0 = 0, pr1 = 0;   // p_ready phases consumed, per buffer
   bool ok = true;
@@ -619,7 +634,7 @@ __device__ __forceinline__ void cross_bwd_first(const CrossBwdBars<256, MODE>& b
                                                 const WaitGuard& g) {
   using C = CrossBwdCfg<256, MODE>;
   const BwdWideMma<MODE> M{tmem, base};
-  const CrossIssuer is{g};
+  const CrossIssuer<256> is{g};
   uint32_t pos = 0;                // streamed tiles issued
   uint32_t used[2] = {0, 0};       // into the buffers
   bool ok = true;
@@ -662,7 +677,7 @@ __device__ __forceinline__ void cross_bwd_acc(const CrossBwdBars<256, MODE>& bar
                                               const WaitGuard& g) {
   using C = CrossBwdCfg<256, MODE>;
   const BwdWideMma<MODE> M{tmem, base};
-  const CrossIssuer is{g};
+  const CrossIssuer<256> is{g};
   uint32_t pos = 0;            // streamed tiles consumed
   uint32_t pr0 = 0, pr1 = 0;   // p_ready phases consumed, per buffer
   bool ok = true;
@@ -724,14 +739,14 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
       d_row = f2_pack(dsum, dsum);
     }
     for (int t = b; ok && t < n; t += 2) {
-      ok = warp_wait_bar(bar.s_full(b), sf & 1, g, kStatusTimeoutSoftmax);
+      ok = bwd_wait<D>(bar.s_full(b), sf & 1, g, kStatusTimeoutSoftmax);
       if (!ok) break;
       ++sf;
       const uint32_t q = pos + t;
       const int st = q % C::NST;
       if constexpr (C::BY_KEY) {
         // The stage's vectors were written by TMA; observe that completion here too.
-        ok = warp_wait_bar(bar.st_full(st), (q / C::NST) & 1, g, kStatusTimeoutSoftmax);
+        ok = bwd_wait<D>(bar.st_full(st), (q / C::NST) & 1, g, kStatusTimeoutSoftmax);
         if (!ok) break;
       }
       tc_fence_after();
@@ -806,7 +821,7 @@ __device__ __forceinline__ void cross_bwd_elementwise(const CrossBwdParams& p, c
     if (!ok) break;
     pos += n;
     // Read the unit's accumulators out.
-    ok = warp_wait_bar(bar.out_done(), k & 1, g, kStatusTimeoutSoftmax);
+    ok = bwd_wait<D>(bar.out_done(), k & 1, g, kStatusTimeoutSoftmax);
     if (!ok) break;
     tc_fence_after();
     const bool second = MODE == 0 && b == 1;
@@ -977,8 +992,9 @@ struct BwdZeros {
   int per, x, grid, warp, warps;  // blocks of a sequence; this block's next (sequence, share); ..
   int at = 0, to = 0, q_to = 0;   // the sequence's next row of this warp's; behind its places; behind its rows without keys
   CrossSeq s;
-  __device__ __forceinline__ BwdZeros(const CrossArgs& a, int block, int grid_, int warp_, int warps_)
-      : per(max(grid_ / a.cb.B, 1)), x(block), grid(grid_), warp(warp_), warps(warps_) {}
+  // `shares`: of different sequences, that a block has where there are fewer sequences than blocks.
+  __device__ __forceinline__ BwdZeros(const CrossArgs& a, int block, int grid_, int warp_, int warps_, int shares)
+      : per(max(grid_ * shares / a.cb.B, 1)), x(block), grid(grid_), warp(warp_), warps(warps_) {}
   // One row of dK and dV, or of dQ; false behind the last.
   __device__ __forceinline__ bool row(const CrossBwdParams& p) {
     const CrossArgs& a = p.a;
@@ -1076,7 +1092,7 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
     }
   }
   if (zeros) {
-    BwdZeros<D> z(a, blockIdx.x, gridDim.x, warp, WARPS);
+    BwdZeros<D> z(a, blockIdx.x, gridDim.x, warp, WARPS, 1);
     while (z.row(p)) {
     }
   }

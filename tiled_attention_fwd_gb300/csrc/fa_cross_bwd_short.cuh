@@ -16,7 +16,7 @@
 // tiles through a ring of their own, so that the next unit's are there when this one ends.
 //
 // Bound by an item's chain of products, elementwise step and products (some 4000 cycles, two in flight), not by memory or the tensor
-// cores: 32 sequences of 17 to 200 rows over 100 to 1024 keys, 16 heads, d = 64: 101.5 us with the other kernels (180 MB: 0.26 of the
+// cores: 32 sequences of 17 to 200 rows over 100 to 1024 keys, 16 heads, d = 64: 100 us with the other kernels (180 MB: 0.26 of the
 // memory's rate).  Other shapes of it that were measured there, whole calls: 128 rows an item, single-buffered, 16 elementwise warps 116; S and dV
 // issued by one warp, dP and dK by another 132; both warpgroups on every item 116.
 #pragma once
@@ -341,7 +341,7 @@ __device__ __forceinline__ void short_mma_s(const CrossBwdParams& p, const Short
                                             uint32_t tmem, const WaitGuard& g) {
   using C = ShortCfg<D>;
   const ShortMma<D> M(tmem, base);
-  const CrossIssuer is{g};
+  const CrossIssuer<D> is{g};
   const int group = p.a.group, t1 = bwd_tokens1(group);
   ShortItem<D> it;
   int k = 0;
@@ -370,7 +370,7 @@ __device__ __forceinline__ void short_mma_kv(const CrossBwdParams& p, const Shor
                                              uint32_t tmem, const WaitGuard& g) {
   using C = ShortCfg<D>;
   const ShortMma<D> M(tmem, base);
-  const CrossIssuer is{g};
+  const CrossIssuer<D> is{g};
   const int group = p.a.group, t1 = bwd_tokens1(group);
   ShortItem<D> it;
   int k = 0;
@@ -420,7 +420,7 @@ __device__ __forceinline__ void short_mma_dq(const CrossBwdParams& p, const Shor
                                              uint32_t tmem, const WaitGuard& g) {
   using C = ShortCfg<D>;
   const ShortMma<D> M(tmem, base);
-  const CrossIssuer is{g};
+  const CrossIssuer<D> is{g};
   const int group = p.a.group, t1 = bwd_tokens1(group);
   ShortItem<D> it;
   int k = 0;
@@ -572,9 +572,9 @@ __device__ __forceinline__ void short_output(const CrossBwdParams& p, const Shor
   const int tok_r = r / group, head_r = r - tok_r * group;
   uint32_t tiles = 0;  // key tiles read out
   bool ok = true;
-  // The zeros of dK and dV, a few rows behind each key tile: they cost nothing here (written before, 32 padded sequences of 100 to
-  // 1024 places: 9 us).
-  BwdZeros<D> zeros(p.a, blockIdx.x, gridDim.x, quarter, 4);
+  // The zeros of dK and dV, a few rows behind each key tile (32 padded sequences of 100 to 1024 places, with 2/4/8/12/16 of them or all
+  // behind the first: 109/105/100/100/101/103 us; written by the kernel before, one share of a sequence a block: 106 and 101).
+  BwdZeros<D> zeros(p.a, blockIdx.x, gridDim.x, quarter, 4, 8);
   bool more = true;
   // 32 columns of TMEM.
   auto chunk = [&](uint32_t at, uint32_t (&v)[32]) {
