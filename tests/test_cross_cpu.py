@@ -206,3 +206,9 @@ def test_cross_kernels_fit_their_registers():
         assert r["registers"] <= 128 and r["spill_stores"] <= 16, (name, r)
     for name, r in {**few, **long, **prep, **join}.items():
         assert r["spill_stores"] == 0, (name, r)
+
+
+def test_what_stands_in_for_missing_keys_lies_in_the_workspace():
+    """Without keys the forward's tensor maps are of the workspace, with dense heads: 65535 of them at most."""
+    for d in (32, 64, 128, 256):
+        assert fa.fa_cross_fwd_workspace_bytes(d) >= 65535 * d * 2

@@ -96,13 +96,15 @@ int fa_cross_fwd(const void* q, const long long* q_stride, const void* k, const 
   rc = fa::current_ctx(&ctx, stream);
   if (rc != FA_OK || batch->rows == 0) return rc;
   fa::PagedFwdArgs p = {};
-  // (Without keys the tensor maps are made of something that is there; nothing is read through them.)
-  p.kv.k = const_cast<void*>(batch->keys > 0 ? k : workspace);
-  p.kv.v = const_cast<void*>(batch->keys > 0 ? v : workspace);
+  // Without keys the tensor maps are made of something that is there (65535 dense heads, at most 34 MB, are less than the workspace's
+  // parts at every d; the caller's head stride may lead out of it).  Nothing is read through them: no kernel loads a tile without keys.
+  const bool none = batch->keys == 0;
+  p.kv.k = const_cast<void*>(none ? workspace : k);
+  p.kv.v = const_cast<void*>(none ? workspace : v);
   for (int i = 0; i < 2; ++i) {
     p.qs[i] = q_stride[i];
-    p.kv.ks[i] = k_stride[i];
-    p.kv.vs[i] = v_stride[i];
+    p.kv.ks[i] = none ? d : k_stride[i];
+    p.kv.vs[i] = none ? d : v_stride[i];
     p.os[i] = o_stride[i];
   }
   p.kv.heads = heads;

@@ -449,7 +449,7 @@ __device__ __forceinline__ bool chunk_load_stage(const CUtensorMap* tm_k, const 
 }
 
 // The same of packed keys: whole tiles (behind the last key: the next sequence's, or zeros behind the tensor); lane i loads
-// position i.
+// position i.  Nothing is loaded for a sequence without keys, whose unit is one tile all the same: there may be no tensor to read it from.
 template <int D, bool PAIRED>
 __device__ __forceinline__ bool chunk_load_packed(const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                                   const ChunkBars<D, false>& bar, uint32_t base, uint32_t pos, int which,
@@ -461,7 +461,7 @@ __device__ __forceinline__ bool chunk_load_packed(const CUtensorMap* tm_k, const
   constexpr int NST = PAIRED ? C::NST / 2 : C::NST, HEADS = PAIRED ? 2 : 1;  // PAIRED: stages of four tiles, {V, K} of each head
   const int st = pos % NST;
   const uint32_t full = bar.kv_full(st), par = (pos / NST) & 1;
-  const bool has0 = which & 1, has1 = (which & 2) && t1.kind;
+  const bool has0 = (which & 1) && t0.key0 < t0.len, has1 = (which & 2) && t1.kind && t1.key0 < t1.len;
   if (!chunk_wait(bar.kv_empty(st), par ^ 1, g, kStatusTimeoutLoad)) return false;
   if (lane == 0) mbar_arrive_expect_tx(full, HEADS * (has0 + has1) * C::KV_TILE);
   __syncwarp();
