@@ -225,6 +225,9 @@ __global__ void __launch_bounds__(kTableThreads, 1) fa_paged_release_kernel(cons
   const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_ctas());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool bad = false;
+  // A CTA's shared memory may be written by another one when it has started: all arrive here and wait before their first such store.
+  cluster_arrive();
+  bool all_started = false;
   const int free = free_count(a, bad);
   const long long units = static_cast<long long>(a.B) << a.parts_log2;
   auto valid = [&](int page) { return page >= 0 && page < a.num_pages; };
@@ -259,6 +262,8 @@ __global__ void __launch_bounds__(kTableThreads, 1) fa_paged_release_kernel(cons
         count[e] = __reduce_add_sync(0xffffffffu, mine);
         bad = bad || count[e] != part[e].y - part[e].x;
       }
+      if (!all_started) cluster_wait();
+      all_started = true;
 #pragma unroll
       for (int e = 0; e < PARTS; ++e) {
         const int i = i0 + e * ctas * kTableWarps;
