@@ -101,12 +101,9 @@ template <int D>
 constexpr __host__ __device__ int bwd_tokens0(int group) { return bwd_rows0<D>() / group; }
 constexpr __host__ __device__ int bwd_tokens1(int group) { return 128 / group; }
 
-// -L log2e and -D of the rows, as MODE 0 streams them: BS values a tile of tokens, [heads][tiles][BS]; sequence b's tiles
-// begin at tile row0 / tokens + b (its n rows need no more than what is left up to the next sequence's).
-template <int D>
-__host__ __device__ __forceinline__ long long bwd_tile0(const CrossSeq& s, int b, int group) {
-  return s.row0 / bwd_tokens0<D>(group) + static_cast<long long>(b);
-}
+// -L log2e and -D of the rows, as MODE 0 streams them: BS values a tile of tokens, [heads][tiles][BS]; the tiles of sequences with
+// rows and keys lie one behind another, in the sequences' order (CrossBwdWs::tile0).  As many as there can be: ranges that share no
+// rows have rows / t0 whole tiles together at most, and B others.
 template <int D>
 __host__ __device__ __forceinline__ long long bwd_tiles(int rows, int B, int group) {
   return rows / bwd_tokens0<D>(group) + static_cast<long long>(B);
@@ -146,6 +143,7 @@ struct BwdWork<D, 2> {
 struct CrossBwdWs {
   PlanRecord* rec[3];  // of the kernels (bwd_place): [kPlanCtas]
   int* part0;          // [kPlanCtas]: MODE 2's CTA has written its part 0
+  int* tile0;          // [B]: first tile of a sequence's vectors (written where it has rows and keys)
   float* l2;           // [heads][tiles][BS]
   float* dsum;
   float* part[3];      // [kPlanCtas][2][part floats]
@@ -162,6 +160,7 @@ size_t cross_bwd_ws(char* p, int B, int rows, int heads, int group, CrossBwdWs* 
   const size_t vec = static_cast<size_t>(heads) * bwd_tiles<D>(rows, B, group) * bwd_rows0<D>() * sizeof(float);
   for (int i = 0; i < 3; ++i) x.rec[i] = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
   x.part0 = reinterpret_cast<int*>(take(kPlanCtas * sizeof(int)));
+  x.tile0 = reinterpret_cast<int*>(take(static_cast<size_t>(B) * sizeof(int)));
   x.l2 = reinterpret_cast<float*>(take(vec));
   x.dsum = reinterpret_cast<float*>(take(vec));
   x.part[0] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, D == 256 ? 3 : 0>::PART * sizeof(float)));
@@ -333,6 +332,7 @@ template <int D, int MODE>
 struct CrossBwdWalk {
   using C = BwdWork<D, MODE>;
   int b, u, j;
+  int vec0;  // the sequence's first tile of the vectors
   CrossSeq s;
   BwdUnits c;
   long long pos, end;   // on the line
@@ -342,6 +342,8 @@ struct CrossBwdWalk {
   __device__ __forceinline__ void load(const CrossBwdParams& p) {
     bool bad;
     s = cross_seq(p.a.cb, b, bad);
+    // (Written by a kernel that is not the one before: past L1.  Anything where there are no units.)
+    vec0 = __ldcg(p.ws.tile0 + b);
     c = bwd_units<D, MODE>(p.a, s);
   }
   __device__ __forceinline__ void start(const CrossBwdParams& p, const PlanShare& w) {
@@ -393,7 +395,7 @@ struct CrossBwdWalk {
       g.str0 = s.key0;
       g.str_n = s.len;
     }
-    g.vec0 = static_cast<int>(bwd_tile0<D>(s, b, p.a.group));
+    g.vec0 = vec0;
     g.s0 = j;
     g.n = n;
     g.out = n == c.str ? 0 : j == 0 ? 2 : 1;
@@ -1030,6 +1032,7 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
   constexpr int CPR = D / 8;     // 16-byte chunks per row
   constexpr int RPW = 32 / CPR;  // rows per warp step
   constexpr int WARPS = kPrepThreads / 32;
+  __shared__ PlanScratch scratch;
   const CrossArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -1044,32 +1047,37 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
   }
   const int t0 = bwd_tokens0<D>(a.group);
   const int sub = lane / CPR, chunk = lane % CPR;
-  // A tile of one key/value head's rows at a time.
-  for (long long x = blockIdx.x; x < p.tiles * a.heads; x += gridDim.x) {
-    const long long tile = x / a.heads;
-    const int head = static_cast<int>(x % a.heads);
-    // The last sequence whose tiles begin at `tile` or before, found in steps of 32 sub-ranges (every warp for itself).
-    int lo = 0, count = a.cb.B;
-    while (count > 1) {
-      const int step = (count + 31) / 32;
-      const int at = lo + lane * step;
-      const bool here = at < lo + count && a.cb.cu_rows[at] / t0 + static_cast<long long>(at) <= tile;
-      const int k = __popc(__ballot_sync(0xffffffffu, here));  // (lane 0 always, where the offsets do not decrease)
-      const int from = lo + (k > 0 ? k - 1 : 0) * step;
-      count = min(step, lo + count - from);
-      lo = from;
-    }
+  // The tiles of one key/value head's rows, dealt out in equal shares like the products (a search among the offsets would lead
+  // astray where one of them names what is not there).
+  auto tiles_of = [&](const CrossSeq& s) -> int { return s.len == 0 ? 0 : (s.n + t0 - 1) / t0; };
+  const PlanShare share = plan_share<kPrepThreads>(
+      a.cb.B, gridDim.x, blockIdx.x,
+      [&](int b) -> long long {
+        bool bad;
+        return static_cast<long long>(tiles_of(cross_seq(a.cb, b, bad))) * a.heads;
+      },
+      1, scratch);
+  int b = share.b, tile = static_cast<int>(share.offset / a.heads), head = static_cast<int>(share.offset % a.heads);
+  long long before = (share.start - share.offset) / a.heads;  // tiles of the sequences before b
+  int tiles = 0, tile0 = 0;
+  CrossSeq s = {};
+  auto load = [&]() {
     bool bad;
-    const CrossSeq s = cross_seq(a.cb, lo, bad);
-    const long long first = (tile - bwd_tile0<D>(s, lo, a.group)) * t0;  // token of the tile's first row
-    if (first < 0 || first >= s.n || s.len == 0) continue;               // nobody reads it
+    s = cross_seq(a.cb, b, bad);
+    tiles = tiles_of(s);
+    tile0 = static_cast<int>(min(before, p.tiles - tiles));  // (ranges that share rows may have more tiles than there are places)
+  };
+  if (share.start < share.end) load();
+  for (long long x = share.start; x < share.end; ++x) {
+    if (tile == 0 && head == 0 && threadIdx.x == 0) p.ws.tile0[b] = tile0;
+    const int first = tile * t0;  // token of the tile's first row
 #pragma unroll 1
     for (int r = warp * RPW + sub; r < BS; r += WARPS * RPW) {
       const int tok = r / a.group, hq = head * a.group + r % a.group;
       const bool valid = tok < t0 && first + tok < s.n;
       float acc = 0.f, lse = 0.f;
       if (valid) {
-        const long long row = s.row0 + first + tok;
+        const long long row = static_cast<long long>(s.row0) + first + tok;
         if (chunk == 0) lse = a.lse[static_cast<long long>(hq) * a.cb.rows + row];
         const uint4 u4 = *reinterpret_cast<const uint4*>(a.o + row * a.st[3][0] + hq * a.st[3][1] + chunk * 8);
         const uint4 v4 = *reinterpret_cast<const uint4*>(a.dout + row * a.st[4][0] + hq * a.st[4][1] + chunk * 8);
@@ -1085,11 +1093,21 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
 #pragma unroll
       for (int m = CPR / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
       if (chunk == 0) {
-        const long long at = (head * p.tiles + tile) * BS + r;
+        const long long at = (head * p.tiles + tile0 + tile) * BS + r;
         p.ws.dsum[at] = valid ? -acc : 0.f;
         p.ws.l2[at] = valid ? -lse * 1.4426950408889634f : -INFINITY;
       }
     }
+    if (++head < a.heads) continue;
+    head = 0;
+    if (++tile < tiles) continue;
+    tile = 0;
+    before += tiles;
+    if (x + 1 == share.end) break;
+    do {
+      ++b;
+      load();
+    } while (tiles == 0);
   }
   if (zeros) {
     BwdZeros<D> z(a, blockIdx.x, gridDim.x, warp, WARPS, 1);
