@@ -53,6 +53,15 @@ def test_a_bad_row_offset_leaves_the_others_right(B, n, d):
         passes(s, cu_rows, cu_keys, None, [b for b in range(B) if b not in (at - 1, at)])
 
 
+def test_a_bad_row_offset_among_thousands():
+    """More sequences than a block of the preparing kernel sums up in one go (32 times its threads)."""
+    B, rng = 9000, np.random.default_rng(1)
+    s = Ragged(rng.integers(0, 3, B).tolist(), rng.integers(0, 4, B).tolist(), 1, 1, 32, seed=1, pad=3)
+    cu_rows, cu_keys, _ = s.batch()
+    cu_rows[5000] = -3
+    passes(s, cu_rows, cu_keys, None, set(range(B)) - {4999, 5000})
+
+
 @pytest.mark.parametrize("d", [64, 256])
 @pytest.mark.parametrize("n", [3, 300])
 def test_a_bad_key_offset_or_length_leaves_the_others_right(n, d):

@@ -1050,15 +1050,39 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
   // The tiles of one key/value head's rows, dealt out in equal shares like the products (a search among the offsets would lead
   // astray where one of them names what is not there).
   auto tiles_of = [&](const CrossSeq& s) -> int { return s.len == 0 ? 0 : (s.n + t0 - 1) / t0; };
+  auto places_of = [&](int b) -> long long {  // of sequence b on the line
+    bool bad;
+    return static_cast<long long>(tiles_of(cross_seq(a.cb, b, bad))) * a.heads;
+  };
+  // A thread adds up `per` sequences, so that the CTA, of which there are several on an SM, goes through its threads' sums but once
+  // (2000 sequences of 3 rows, whole calls: 292 us; scanned 256 at a time 314).
+  const int per = (a.cb.B + kPrepThreads - 1) / kPrepThreads;
   const PlanShare share = plan_share<kPrepThreads>(
-      a.cb.B, gridDim.x, blockIdx.x,
-      [&](int b) -> long long {
-        bool bad;
-        return static_cast<long long>(tiles_of(cross_seq(a.cb, b, bad))) * a.heads;
+      (a.cb.B + per - 1) / per, gridDim.x, blockIdx.x,
+      [&](int group) -> long long {
+        long long sum = 0;
+        for (int b = group * per; b < min((group + 1) * per, a.cb.B); ++b) sum += places_of(b);
+        return sum;
       },
       1, scratch);
-  int b = share.b, tile = static_cast<int>(share.offset / a.heads), head = static_cast<int>(share.offset % a.heads);
-  long long before = (share.start - share.offset) / a.heads;  // tiles of the sequences before b
+  int b = share.b * per;
+  long long offset = share.offset;
+  for (bool found = per == 1 || share.start >= share.end; !found;) {  // the sequence of these that holds the share's first tile
+    const long long w = b + lane < a.cb.B ? places_of(b + lane) : 0;
+    long long upto = w;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, k);
+      if (lane >= k) upto += y;
+    }
+    const uint32_t behind = __ballot_sync(0xffffffffu, upto > offset);
+    found = behind != 0 || b >= a.cb.B;
+    const int at = behind != 0 ? __ffs(behind) - 1 : 31;
+    offset -= __shfl_sync(0xffffffffu, behind != 0 ? upto - w : upto, at);
+    b += behind != 0 ? at : 32;
+  }
+  int tile = static_cast<int>(offset / a.heads), head = static_cast<int>(offset % a.heads);
+  long long before = (share.start - offset) / a.heads;  // tiles of the sequences before b
   int tiles = 0, tile0 = 0;
   CrossSeq s = {};
   auto load = [&]() {
