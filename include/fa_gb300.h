@@ -331,7 +331,7 @@ typedef struct fa_paged_batch {
   const int* kv_lens;       /* device, [B], >= 0                                                     */
   long long table_stride;
   int max_pages;            /* entries of a row of page_table, >= 1, times page_size <= 2^31 - 4096  */
-  int B;                    /* sequences, >= 1                                                       */
+  int B;                    /* sequences, 1 .. 2^31 - 4096                                           */
   int rows;                 /* rows of the token-major tensors, >= 0 (0: nothing is done)            */
 } fa_paged_batch;
 
@@ -426,7 +426,7 @@ typedef struct fa_page_pool {
  *   page_table : device, [B] rows of max_pages entries, table_stride ints apart.
  *   kv_lens, new_rows : device, [B].    cu_rows : device, [B + 1].
  *   slots      : device, long long [rows], positions : device, int [rows]; 16-byte aligned.  Either may be NULL (not written).
- *   rows       : most new rows that the arrays hold, >= 0.
+ *   rows       : most new rows that the arrays hold, 0 .. 2^31 - 4096.  B : 1 .. 2^31 - 4096.
  *   An entry of free_pages that is no page (outside [0, num_pages)) is entered as -1 and reported as
  *   FA_ERR_BAD_BATCH, and so is an entry of page_table that a new row needs and that is none: its slot is -1.
  */
@@ -467,7 +467,7 @@ typedef struct fa_cross_batch {
   const int* cu_rows;       /* device, [B + 1], cu_rows[0] >= 0, not decreasing                      */
   const int* cu_keys;       /* device, [B + 1], cu_keys[0] >= 0, not decreasing                      */
   const int* key_lens;      /* device, [B], or NULL                                                  */
-  int B;                    /* sequences, >= 1                                                       */
+  int B;                    /* sequences, 1 .. 2^31 - 4096                                           */
   int rows;                 /* rows of q, 0 <= rows, rows + B <= 2^31 - 4096                          */
   int keys;                 /* rows of k and v, 0 .. 2^31 - 4096 (0: k and v may be NULL)             */
 } fa_cross_batch;

@@ -212,3 +212,15 @@ def test_what_stands_in_for_missing_keys_lies_in_the_workspace():
     """Without keys the forward's tensor maps are of the workspace, with dense heads: 65535 of them at most."""
     for d in (32, 64, 128, 256):
         assert fa.fa_cross_fwd_workspace_bytes(d) >= 65535 * d * 2
+
+
+def test_more_sequences_than_the_kernels_count():
+    """They step through the sequences 1024 at a time in 32 bits: beyond 2^31 - 4096 a step would pass the last and wrap."""
+    for B in (MAX + 1, 2 ** 31 - 1):
+        assert fwd(batch(B=B, rows=0)) == -2 and bwd(batch(B=B, rows=0)) == -2
+        assert fa.fa_paged_extend(pool(), FAKE, 4, 4, FAKE, FAKE, FAKE, FAKE, FAKE, B, 4, None) == -2
+        assert fa.fa_paged_release(pool(), FAKE, 4, 4, FAKE, FAKE, B, None) == -2
+        cache = fa.CPagedCache(FAKE, FAKE, 0, 0, (1024, 512, 64), (1024, 512, 64), 8, 16, 2, 64)
+        pages = fa.CPagedBatch(FAKE, FAKE, FAKE, 4, 4, B, 10)
+        assert fa.fa_paged_write(cache, pages, FAKE, ST, FAKE, ST, None) == -2
+        assert fa.fa_paged_fwd(FAKE, ST, cache, pages, FAKE, ST, FAKE, 4, 1, 0.1, 0, FAKE, 1 << 40, None) == -2

@@ -440,7 +440,8 @@ int take(const fa_paged_cache* c, const fa_paged_batch* b, PagedKv* kv, PagedBat
   int log2 = 4;
   while (log2 < 10 && (1 << log2) != c->page_size) ++log2;
   if ((1 << log2) != c->page_size) return FA_ERR_BAD_SHAPE;
-  if (b->B < 1 || b->rows < 0 || b->max_pages < 1 || b->table_stride < b->max_pages) return FA_ERR_BAD_SHAPE;
+  // (The kernels take up to 1024 sequences at a time, counted in 32 bits.)
+  if (b->B < 1 || b->B > 0x7ffff000 || b->rows < 0 || b->max_pages < 1 || b->table_stride < b->max_pages) return FA_ERR_BAD_SHAPE;
   if (c->d != 32 && c->d != 64 && c->d != 128 && c->d != 256) return FA_ERR_UNSUPPORTED_D;
   // Positions are 32-bit, those at the end of a tile (512 keys at most) and of the batch of tiles behind it, too.
   if ((static_cast<long long>(b->max_pages) << log2) > 0x7ffff000LL) return FA_ERR_BAD_SHAPE;

@@ -349,7 +349,8 @@ int take(const fa_page_pool* pool, int* table, long long stride, int max_pages, 
   int log2 = 4;
   while (log2 < 10 && (1 << log2) != pool->page_size) ++log2;
   if ((1 << log2) != pool->page_size || pool->num_pages < 1) return FA_ERR_BAD_SHAPE;
-  if (B < 1 || max_pages < 1 || stride < max_pages) return FA_ERR_BAD_SHAPE;
+  // (The kernels take 1024 sequences at a time, counted in 32 bits.)
+  if (B < 1 || B > 0x7ffff000 || max_pages < 1 || stride < max_pages) return FA_ERR_BAD_SHAPE;
   // As fa_paged_batch: positions are 32-bit, those at the end of a tile, too.
   if ((static_cast<long long>(max_pages) << log2) > 0x7ffff000LL) return FA_ERR_BAD_SHAPE;
   if (misaligned(pool->free_pages, 4) || misaligned(pool->free_count, 4) || misaligned(table, 4) || misaligned(lens, 4))
