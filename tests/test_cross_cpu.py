@@ -224,3 +224,27 @@ def test_more_sequences_than_the_kernels_count():
         pages = fa.CPagedBatch(FAKE, FAKE, FAKE, 4, 4, B, 10)
         assert fa.fa_paged_write(cache, pages, FAKE, ST, FAKE, ST, None) == -2
         assert fa.fa_paged_fwd(FAKE, ST, cache, pages, FAKE, ST, FAKE, 4, 1, 0.1, 0, FAKE, 1 << 40, None) == -2
+
+
+def test_sizes_that_pass_32_bits_stay_too_large():
+    """A C int would keep their low bits."""
+    from tiled_attention_fwd_gb300 import _lib
+
+    class Tensor:  # as much of one as the batch is made of
+        is_cuda, dtype = True, torch.bfloat16
+
+        def __init__(self, *shape, dtype=torch.bfloat16):
+            self.shape, self.dtype = shape, dtype
+
+        dim = lambda self: len(self.shape)
+        get_device = lambda self: 0
+        data_ptr = lambda self: FAKE
+        is_contiguous = lambda self: True
+
+    cu = Tensor(3, dtype=torch.int32)
+    for n in (2 ** 31, 2 ** 32 + 50):
+        b = _lib._cross_batch(Tensor(50, 2, 64), Tensor(n, 2, 64), cu, cu, None)
+        assert (b.B, b.rows) == (2, 50) and fwd(b) == -2 and bwd(b) == -2
+        b = _lib._cross_batch(Tensor(n, 2, 64), Tensor(50, 2, 64), cu, cu, None)
+        assert fwd(b) == -2 and bwd(b) == -2
+    assert [_lib._most_rows(n, 7) for n in (None, 3, 2 ** 32 + 1, 2 ** 70, -1, -2 ** 32 + 5)] == [7, 3, 2 ** 31 - 1, 2 ** 31 - 1, -1, -1]

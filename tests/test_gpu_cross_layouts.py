@@ -25,3 +25,26 @@ def test_no_keys_at_all_with_heads_far_apart(rows, d):
     dq, dk, dv = fa.cross_backward(q, k, v, o, lse, q, at, none, out=(torch.full_like(q, 7.0), k, v))
     assert not dq.any()
     fa.check_status()
+
+
+def test_bounds_of_rows_that_pass_32_bits():
+    """They are no bounds, whatever their low bits say."""
+    q, k = (torch.randn(n, 2, 64, device="cuda").bfloat16() for n in (40, 50))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu, ck = torch.tensor([0, 7, 40], **i32), torch.tensor([0, 30, 50], **i32)
+    o, lse = fa.cross_forward(q, k, k, cu, ck, max_rows=2 ** 31 - 1)
+    for most in (2 ** 32, 2 ** 32 + 1, 2 ** 40, 2 ** 63 - 1, 2 ** 70):
+        again = fa.cross_forward(q, k, k, cu, ck, max_rows=most)
+        fa.check_status()
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+    for most in (-1, -2 ** 32 + 33):
+        with pytest.raises(fa.FAError):
+            fa.cross_forward(q, k, k, cu, ck, max_rows=most)
+    cache = fa.PagedCache.empty(4, 2, 16, 64)
+    cache.k.copy_(torch.randn(cache.k.shape, device="cuda")), cache.v.copy_(torch.randn(cache.v.shape, device="cuda"))
+    table, lens = torch.tensor([[0, 1], [2, 3]], **i32), torch.tensor([20, 32], **i32)
+    cu = torch.tensor([0, 10, 40], **i32)
+    want = fa.paged_forward(q, cache, table, cu, lens, max_rows=2 ** 31 - 1)
+    got = fa.paged_forward(q, cache, table, cu, lens, max_rows=2 ** 32 + 1)
+    fa.check_status()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -530,6 +530,11 @@ def _call_on(index, fn, name, *args):
         raise FAError(rc, name)
 
 
+def _most_rows(max_rows, rows):
+    """max_rows (default: all rows) as a C int, which ctypes would cut to 32 bits: a larger bound says no more than the largest."""
+    return rows if max_rows is None else max(min(int(max_rows), 0x7fffffff), -1)
+
+
 def _paged_call(cache, fn, name, *args):
     """fn(*args, stream) on the cache's device."""
     _call_on(cache._index, fn, name, *args)
@@ -615,7 +620,7 @@ def paged_forward(q, cache, page_table, cu_rows, kv_lens, max_rows=None, causal:
     elif workspace.get_device() != cache._index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     _paged_call(cache, fa_paged_fwd, "fa_paged_fwd", q.data_ptr(), qs, cache._c, batch, o.data_ptr(), os_, l.data_ptr(),
-                heads, rows if max_rows is None else int(max_rows), d ** -0.5 if scale is None else float(scale), causal,
+                heads, _most_rows(max_rows, rows), d ** -0.5 if scale is None else float(scale), causal,
                 workspace.data_ptr(), workspace.nbytes)
     return o, l
 
@@ -728,8 +733,9 @@ def _cross_batch(q, k, cu_rows, cu_keys, key_lens):
     for t in ts:
         if t.dtype is not torch.int32 or t.get_device() != q.get_device() or not t.is_contiguous():
             raise ValueError("cu_rows, cu_keys and key_lens must be contiguous int32 tensors on q's device")
+    # (What passes 32 bits stays too large, for the library to refuse.)
     return CCrossBatch(cu_rows.data_ptr(), cu_keys.data_ptr(), None if key_lens is None else key_lens.data_ptr(), n[0] - 1,
-                       q.shape[0], k.shape[0])
+                       min(q.shape[0], 0x7fffffff), min(k.shape[0], 0x7fffffff))
 
 
 def _cross_ws(workspace, q):
@@ -772,7 +778,7 @@ def cross_forward(q, k, v, cu_rows, cu_keys, key_lens=None, max_rows=None, scale
         return o, l
     ws = _cross_ws(cross_workspace(q) if workspace is None else workspace, q)
     _call_on(q.get_device(), fa_cross_fwd, "fa_cross_fwd", q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, batch,
-             o.data_ptr(), os_, l.data_ptr(), heads, k.shape[1], d, rows if max_rows is None else int(max_rows),
+             o.data_ptr(), os_, l.data_ptr(), heads, k.shape[1], d, _most_rows(max_rows, rows),
              d ** -0.5 if scale is None else float(scale), *ws)
     return o, l
 
