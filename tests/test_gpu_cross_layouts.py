@@ -3,8 +3,33 @@ import pytest
 import torch
 
 import tiled_attention_fwd_gb300 as fa
+from cross_util import Ragged, check_backward, check_forward
 
 pytestmark = pytest.mark.gpu
+
+
+def heads_first(t):
+    """The same values, laid out [heads, rows, d]."""
+    return t.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+@pytest.mark.parametrize("rows,keys", [([1, 5, 0, 2], [333, 60, 9, 1000]), ([17, 120, 40], [100, 33, 260]), ([300, 700, 3], [500, 129, 0])])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("heads,group", [(3, 1), (2, 4), (1, 3)])
+def test_heads_before_rows(rows, keys, heads, group, d):
+    """Every tensor of both passes, results too, with its heads farther apart than its rows."""
+    s = Ragged(rows, keys, heads, group, d, padded=d != 128, lead=2, pad=3, seed=d + group)
+    q, dout, k, v = (heads_first(t) for t in s.tensors())
+    assert k.stride(0) == d and k.stride(1) == s.K * d or heads == 1
+    o, lse = torch.full_like(q, 7.0), torch.full((heads * group, s.T), 7.0, device="cuda")
+    assert o.stride() == q.stride()
+    fa.cross_forward(q, k, v, *s.batch(), max_rows=max(rows), out=o, lse=lse)
+    fa.check_status()
+    check_forward(s, o, lse)
+    grads = [torch.full_like(t, 7.0) for t in (q, k, v)]
+    fa.cross_backward(q, k, v, o, lse, dout, *s.batch(), out=grads)
+    fa.check_status()
+    check_backward(s, o, lse, grads)
 
 
 @pytest.mark.parametrize("rows", [[1, 0, 2], [20, 3, 40], [300, 0, 1]])

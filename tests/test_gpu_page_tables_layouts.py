@@ -1,0 +1,57 @@
+"""Page tables whose rows lie farther apart than they are wide, and calls that want no slots or no positions."""
+import pytest
+import torch
+
+import oracle.tables as ref
+import tiled_attention_fwd_gb300 as fa
+from test_gpu_page_tables import Pool
+
+pytestmark = pytest.mark.gpu
+
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+def widen(p, left, right):
+    """p's table as columns of a wider one, whose others hold 12345."""
+    B, width = p.d_table.shape
+    wide = torch.full((B, left + width + right), 12345, **I32)
+    wide[:, left:left + width] = p.d_table
+    p.d_table = wide[:, left:left + width]
+    return lambda: (wide[:, :left] == 12345).all() and (wide[:, left + width:] == 12345).all()
+
+
+@pytest.mark.parametrize("B", [1, 2, 37, 1030])
+@pytest.mark.parametrize("left,right", [(0, 3), (2, 0), (5, 20)])
+def test_rows_farther_apart_than_they_are_wide(B, left, right):
+    p = Pool([(7 * b) % 70 for b in range(B)], 12, 16, spare=B * 7, seed=B)
+    others_are_left = widen(p, left, right)
+    assert p.d_table.stride(0) == 12 + left + right
+    new = [(11 * b) % 60 for b in range(B)]
+    p.extend(new, sum(new) + 1)
+    p.extend([1] * B, B)
+    assert others_are_left()
+    p.release([b % 3 != 1 for b in range(B)])
+    p.extend(new, sum(new) + 1)
+    p.release([True] * B)
+    assert others_are_left()
+
+
+@pytest.mark.parametrize("wanted", [(True, False), (False, True), (False, False)])
+def test_slots_and_positions_that_are_not_wanted(wanted):
+    """The library takes NULL for either; the rest of the call is the same, what it reports too."""
+    p = Pool([5, 20, 7, 0], 6, 16, spare=9)
+    for new, code in (([1, 20, 0, 33], 0), ([1, 1, 1, 1], 0), ([30, 90, 2, 1], -11)):
+        rows = 64
+        slots, positions = torch.full((rows,), -7, dtype=torch.int64, device="cuda"), torch.full((rows,), -7, **I32)
+        cu, counts = torch.zeros(5, **I32), torch.tensor(new, **I32)
+        stream = torch.cuda.current_stream().cuda_stream
+        p.count, want_cu, want_slots, want_positions, _ = ref.extend(p.table, p.lens, p.stack, p.count, new, 16, rows)
+        assert fa.fa_paged_extend(p.pool._c, p.d_table.data_ptr(), 6, 6, p.d_lens.data_ptr(), counts.data_ptr(), cu.data_ptr(),
+                                  slots.data_ptr() if wanted[0] else None, positions.data_ptr() if wanted[1] else None, 4, rows,
+                                  stream) == 0
+        assert fa.fa_status(stream) == code
+        p.same()
+        assert cu.tolist() == want_cu
+        n = want_cu[-1]
+        assert slots.tolist() == (want_slots + [-7] * (rows - n) if wanted[0] else [-7] * rows)
+        assert positions.tolist() == (want_positions + [-7] * (rows - n) if wanted[1] else [-7] * rows)
