@@ -1,4 +1,5 @@
 """Cross attention on layouts where heads lie farther apart than rows ([heads, keys, d] seen as [keys, heads, d])."""
+import numpy as np
 import pytest
 import torch
 
@@ -58,7 +59,7 @@ def test_bounds_of_rows_that_pass_32_bits():
     i32 = dict(dtype=torch.int32, device="cuda")
     cu, ck = torch.tensor([0, 7, 40], **i32), torch.tensor([0, 30, 50], **i32)
     o, lse = fa.cross_forward(q, k, k, cu, ck, max_rows=2 ** 31 - 1)
-    for most in (2 ** 32, 2 ** 32 + 1, 2 ** 40, 2 ** 63 - 1, 2 ** 70):
+    for most in (2 ** 32, 2 ** 32 + 1, 2 ** 40, 2 ** 63 - 1, 2 ** 70, torch.tensor(2 ** 40), np.int64(2 ** 40)):
         again = fa.cross_forward(q, k, k, cu, ck, max_rows=most)
         fa.check_status()
         assert torch.equal(again[0], o) and torch.equal(again[1], lse)

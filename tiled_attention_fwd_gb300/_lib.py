@@ -530,14 +530,8 @@ def _call_on(index, fn, name, *args):
         raise FAError(rc, name)
 
 
-def _most_rows(max_rows, rows):
-    """max_rows (default: all rows) as a C int, which ctypes would cut to 32 bits: a larger bound says no more than the largest."""
-    return rows if max_rows is None else max(min(int(max_rows), 0x7fffffff), -1)
-
-
-def _paged_call(cache, fn, name, *args):
-    """fn(*args, stream) on the cache's device."""
-    _call_on(cache._index, fn, name, *args)
+# The largest bound of rows that a C int holds (ctypes would cut a larger one to its low bits).
+_MOST = 0x7fffffff
 
 
 def paged_write(cache, k, v, page_table, cu_rows, kv_lens):
@@ -554,7 +548,7 @@ def paged_write(cache, k, v, page_table, cu_rows, kv_lens):
     batch = _paged_batch(cache, page_table, cu_rows, kv_lens, k.shape[0])
     if k.shape[0] == 0:
         return cache
-    _paged_call(cache, fa_paged_write, "fa_paged_write", cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs)
+    _call_on(cache._index, fa_paged_write, "fa_paged_write", cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs)
     return cache
 
 
@@ -576,7 +570,7 @@ def paged_read(cache, page_table, cu_rows, kv_lens, rows=None, out=None):
     batch = _paged_batch(cache, page_table, cu_rows, kv_lens, k.shape[0])
     if k.shape[0] == 0:
         return k, v
-    _paged_call(cache, fa_paged_read, "fa_paged_read", cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs)
+    _call_on(cache._index, fa_paged_read, "fa_paged_read", cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs)
     return k, v
 
 
@@ -619,8 +613,8 @@ def paged_forward(q, cache, page_table, cu_rows, kv_lens, max_rows=None, causal:
         workspace = paged_workspace(cache, batch.B)
     elif workspace.get_device() != cache._index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
-    _paged_call(cache, fa_paged_fwd, "fa_paged_fwd", q.data_ptr(), qs, cache._c, batch, o.data_ptr(), os_, l.data_ptr(),
-                heads, _most_rows(max_rows, rows), d ** -0.5 if scale is None else float(scale), causal,
+    _call_on(cache._index, fa_paged_fwd, "fa_paged_fwd", q.data_ptr(), qs, cache._c, batch, o.data_ptr(), os_, l.data_ptr(),
+                heads, rows if max_rows is None else max(-1, min(int(max_rows), _MOST)), d ** -0.5 if scale is None else float(scale), causal,
                 workspace.data_ptr(), workspace.nbytes)
     return o, l
 
@@ -778,7 +772,7 @@ def cross_forward(q, k, v, cu_rows, cu_keys, key_lens=None, max_rows=None, scale
         return o, l
     ws = _cross_ws(cross_workspace(q) if workspace is None else workspace, q)
     _call_on(q.get_device(), fa_cross_fwd, "fa_cross_fwd", q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, batch,
-             o.data_ptr(), os_, l.data_ptr(), heads, k.shape[1], d, _most_rows(max_rows, rows),
+             o.data_ptr(), os_, l.data_ptr(), heads, k.shape[1], d, rows if max_rows is None else max(-1, min(int(max_rows), _MOST)),
              d ** -0.5 if scale is None else float(scale), *ws)
     return o, l
 
