@@ -399,8 +399,11 @@ int fa_paged_fwd(const void* q, const long long* q_stride, const fa_paged_cache*
  * *free_count entries of free_pages are page numbers, the last of them is taken
  * first.  (free_pages = num_pages - 1 .. 0 and *free_count = num_pages: all
  * free.)  A sequence of len tokens has the first ceil(len / page_size) entries
- * of its row of page_table.  The arrays are the caller's; calls on the same
- * ones are ordered by a stream.
+ * of its row of page_table; those behind are nobody's, and fa_paged_extend
+ * overwrites them.  So a caller that lowers kv_lens across a page's border (a
+ * rejected draft) gives the pages behind the new length back itself, for
+ * instance with fa_paged_release on a table of theirs, or they are lost.  The
+ * arrays are the caller's; calls on the same ones are ordered by a stream.
  */
 typedef struct fa_page_pool {
   int* free_pages;          /* device, [num_pages]                                                   */

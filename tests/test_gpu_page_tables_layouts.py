@@ -55,3 +55,48 @@ def test_slots_and_positions_that_are_not_wanted(wanted):
         n = want_cu[-1]
         assert slots.tolist() == (want_slots + [-7] * (rows - n) if wanted[0] else [-7] * rows)
         assert positions.tolist() == (want_positions + [-7] * (rows - n) if wanted[1] else [-7] * rows)
+
+
+def shorten(pool, table, lens, new_lens):
+    """Sequences lose their last tokens (a rejected draft): the pages behind the new length go back as a table of their own, on the GPU."""
+    ps, width = pool.page_size, table.shape[1]
+    held, kept = (lens + ps - 1) // ps, (new_lens + ps - 1) // ps
+    k = torch.arange(width, device=table.device)
+    behind = table.gather(1, (kept.view(-1, 1) + k).clamp(max=width - 1).long()).contiguous()
+    table.masked_fill_(k >= kept.view(-1, 1), -1)
+    fa.paged_release(pool, behind, ((held - kept) * ps).int(), torch.ones_like(lens, dtype=torch.bool))
+    lens.copy_(new_lens)
+
+
+def test_shortened_sequences_give_their_pages_back():
+    """As the header says: whoever lowers a length across a page's border gives the pages behind it back; none is lost then, in a captured
+    loop either."""
+    ps, width, total = 16, 6, 20
+    pool = fa.PagePool.full(total, ps)
+    table, lens = torch.full((3, width), -1, **I32), torch.zeros(3, **I32)
+    counts, keep = torch.zeros(3, **I32), torch.zeros(3, **I32)
+    cu, slots, positions = torch.zeros(4, **I32), torch.full((64,), -1, dtype=torch.int64, device="cuda"), torch.full((64,), -1, **I32)
+
+    def step():
+        fa.paged_extend(pool, table, lens, counts, out=(cu, slots, positions))
+        shorten(pool, table, lens, lens - keep)
+
+    step()  # (of no tokens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    want = [0] * 3
+    for new, dropped in (([17, 5, 30], [0, 0, 0]), ([8, 30, 1], [7, 28, 1]), ([16, 16, 1], [16, 1, 0]), ([2, 2, 18], [0, 0, 17]),
+                         ([0, 16, 4], [0, 16, 4])):
+        counts.copy_(torch.tensor(new)), keep.copy_(torch.tensor(dropped))
+        graph.replay()
+        fa.check_status()
+        want = [a + b - c for a, b, c in zip(want, new, dropped)]
+        assert lens.tolist() == want
+        free = pool.free_pages[:pool.free_count.item()].tolist()
+        used = [x for row, n in zip(table.tolist(), want) for x in row[:-(-n // ps)]]
+        assert sorted(used + free) == list(range(total))
+        assert all(x == -1 for row, n in zip(table.tolist(), want) for x in row[-(-n // ps):])
+    fa.paged_release(pool, table, lens, torch.ones(3, dtype=torch.bool, device="cuda"))
+    fa.check_status()
+    assert sorted(pool.free_pages.tolist()) == list(range(total)) and pool.free_count.item() == total

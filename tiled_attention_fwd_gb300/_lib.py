@@ -621,7 +621,11 @@ def paged_forward(q, cache, page_table, cu_rows, kv_lens, max_rows=None, causal:
 
 class PagePool:
     """The pages of a cache that no sequence has, as a stack on the GPU: the first free_count[0] entries of free_pages
-    (int32 [num_pages]) are free, the last of them is taken first.  ``PagePool.full`` makes one of all pages."""
+    (int32 [num_pages]) are free, the last of them is taken first.  ``PagePool.full`` makes one of all pages.
+
+    A sequence has the first ceil(length / page_size) entries of its row of page_table; those behind are nobody's.  Whoever lowers a
+    length across a page's border (a rejected draft) gives the pages behind it back, or they are lost: paged_release on a table
+    of those entries and (pages x page_size) as lengths does it."""
 
     def __init__(self, free_pages, free_count, page_size):
         import torch
@@ -751,7 +755,7 @@ def cross_forward(q, k, v, cu_rows, cu_keys, key_lens=None, max_rows=None, scale
 
     Sequence b has the rows cu_rows[b] .. cu_rows[b + 1] and the places cu_keys[b] .. cu_keys[b + 1] (int32 [B + 1]), of which
     the first key_lens[b] (int32 [B]; default: all) are keys; all three are read on the device.  q_heads is a multiple of
-    heads, 32 times as many at most.  Any strides with a contiguous last dimension.  ``max_rows``: an upper bound of a sequence's rows (default: all rows of q; a
+    heads, 32 times as many at most.  Any strides that are multiples of 8 (not 0) with a contiguous last dimension.  ``max_rows``: an upper bound of a sequence's rows (default: all rows of q; a
     serving step passes 1).  Returns O (like q, contiguous unless ``out`` is given) and L fp32 [q_heads, rows]; rows of no
     sequence are left as they are (zero in new tensors), rows without keys get O = 0 and L = -inf.  ``workspace``
     (cross_workspace) is allocated here if not given.  Enqueued on the current stream.
