@@ -49,7 +49,7 @@
 namespace fa {
 
 // NT: tiles of 8 rows (1, 2 or 4).
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, bool PACKED = false>
 struct FewCfg {
   static constexpr int EB = E4M3 ? 1 : 2;
   static constexpr int ROWB = D * EB;                     // bytes of a K or V row
@@ -89,6 +89,12 @@ struct FewCfg {
   // sequences, d = 128: 178 us instead of 183, d = 64: 122 and 138; bf16 and d = 256 the same; four row tiles have no
   // registers left).
   static constexpr bool EARLY = E4M3 && NT <= 2 && D <= 128;
+  // Packed keys: the reference is the row's largest logit of the warp's keys, so that the key of the largest weight has p = 1, which bf16 holds: a
+  // late key within kFewSlack of an early one would be off by up to half a step of bf16 alone, and a row that all but copies that key's
+  // v with it (single rows of ordinary batches: O up to 1.65 times as far from 64 bits as its own rounding, 1.25 so).  It moves more often, which
+  // costs nothing with up to 16 rows (64 sequences of one row over 604 MB, 4 heads to a key/value head: 110.6 us either way; of 2 111 and 112.6)
+  // but 10 % with 32 (of 1 to 5 rows: 121 us instead of 111), whose errors average out over more rows.
+  static constexpr bool EXACT = PACKED && NT <= 2;
   static constexpr int KS = D / 16;                       // K steps of S^T = 16-column tiles of O^T
 };
 
@@ -207,7 +213,7 @@ template <int D, bool E4M3, int NT, bool PACKED = false>
 __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
     fa_paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ FewParams p) {
-  using C = FewCfg<D, E4M3, NT>;
+  using C = FewCfg<D, E4M3, NT, PACKED>;
   constexpr int NG = C::NG;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -523,7 +529,7 @@ __global__ void __launch_bounds__(FewCfg<D, E4M3, NT>::THREADS, 1)
       }
       const bool edge = key0 + C::KG - 1 > lim_all;  // some row does not see some key
       float pf[NG][2];  // e4m3: 2^6 times V's scales of keys 16 sg + g, + 8, in units of 2^(vbase - 127)
-      float slack = kFewSlack;  // e4m3: less by the log2 of the largest of these scales (without the 2^6)
+      float slack = C::EXACT ? 0.f : kFewSlack;  // e4m3: less by the log2 of the largest of these scales (without the 2^6)
       if constexpr (E4M3) {
         // A lane turns the scales of keys 32 r + lane into factors; a fragment's come by shuffle.
         constexpr int KPL = C::KG / 32;
