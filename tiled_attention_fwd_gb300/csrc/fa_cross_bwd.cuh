@@ -143,7 +143,7 @@ struct BwdWork<D, 2> {
 struct CrossBwdWs {
   PlanRecord* rec[3];  // of the kernels (bwd_place): [kPlanCtas]
   int* part0;          // [kPlanCtas]: MODE 2's CTA has written its part 0
-  int* tile0;          // [B]: first tile of a sequence's vectors (written where it has rows and keys)
+  uint32_t* tile0;     // [B]: first tile of a sequence's vectors (written where it has rows and keys)
   float* l2;           // [heads][tiles][BS]
   float* dsum;
   float* part[3];      // [kPlanCtas][2][part floats]
@@ -157,10 +157,11 @@ size_t cross_bwd_ws(char* p, int B, int rows, int heads, int group, CrossBwdWs* 
     return x;
   };
   CrossBwdWs x;
-  const size_t vec = static_cast<size_t>(heads) * bwd_tiles<D>(rows, B, group) * bwd_rows0<D>() * sizeof(float);
+  // (One head more than there are: see CrossBwdWalk::load.)
+  const size_t vec = (static_cast<size_t>(heads) + 1) * bwd_tiles<D>(rows, B, group) * bwd_rows0<D>() * sizeof(float);
   for (int i = 0; i < 3; ++i) x.rec[i] = reinterpret_cast<PlanRecord*>(take(kPlanCtas * sizeof(PlanRecord)));
   x.part0 = reinterpret_cast<int*>(take(kPlanCtas * sizeof(int)));
-  x.tile0 = reinterpret_cast<int*>(take(static_cast<size_t>(B) * sizeof(int)));
+  x.tile0 = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(B) * sizeof(uint32_t)));
   x.l2 = reinterpret_cast<float*>(take(vec));
   x.dsum = reinterpret_cast<float*>(take(vec));
   x.part[0] = reinterpret_cast<float*>(take(kPlanCtas * 2 * BwdWork<D, D == 256 ? 3 : 0>::PART * sizeof(float)));
@@ -342,9 +343,10 @@ struct CrossBwdWalk {
   __device__ __forceinline__ void load(const CrossBwdParams& p) {
     bool bad;
     s = cross_seq(p.a.cb, b, bad);
-    // (Written by a kernel that is not the one before: past L1.  Anything where there are no units.)
-    vec0 = __ldcg(p.ws.tile0 + b);
     c = bwd_units<D, MODE>(p.a, s);
+    // (Written by a kernel that is not the one before: past L1.  Not written where there is nothing to multiply, nor for what ranges that share
+    // rows have too much: there it is anything, cut so that a sequence's tiles from there on are the workspace's.)
+    vec0 = static_cast<int>(min(__ldcg(p.ws.tile0 + b), static_cast<uint32_t>(p.tiles)));
   }
   __device__ __forceinline__ void start(const CrossBwdParams& p, const PlanShare& w) {
     pos = w.start;
@@ -1032,7 +1034,7 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
   constexpr int CPR = D / 8;     // 16-byte chunks per row
   constexpr int RPW = 32 / CPR;  // rows per warp step
   constexpr int WARPS = kPrepThreads / 32;
-  __shared__ PlanScratch scratch;
+  __shared__ uint32_t s_warp[kPrepThreads / 32], s_first, s_group;
   const CrossArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -1047,52 +1049,79 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
   }
   const int t0 = bwd_tokens0<D>(a.group);
   const int sub = lane / CPR, chunk = lane % CPR;
-  // The tiles of one key/value head's rows, dealt out in equal shares like the products (a search among the offsets would lead
-  // astray where one of them names what is not there).
+  // The tiles of all sequences lie on a line, one behind another and heads fastest, that is cut into equal shares.  (A search for a tile's
+  // sequence among the offsets would lead astray where one of them names what is not there.)  All is counted in 32 bits and divided
+  // so where it fits, with two barriers, for this is the way to a small batch's first product (one sequence of 20 rows, in a graph: 15.4
+  // us, with the plan of the products' kernels 17.8).
   auto tiles_of = [&](const CrossSeq& s) -> int { return s.len == 0 ? 0 : (s.n + t0 - 1) / t0; };
-  auto places_of = [&](int b) -> long long {  // of sequence b on the line
+  auto tiles_at = [&](int b) -> int {
     bool bad;
-    return static_cast<long long>(tiles_of(cross_seq(a.cb, b, bad))) * a.heads;
+    return tiles_of(cross_seq(a.cb, b, bad));
   };
-  // A thread adds up `per` sequences, so that the CTA, of which there are several on an SM, goes through its threads' sums but once
-  // (2000 sequences of 3 rows, whole calls: 292 us; scanned 256 at a time 314).
-  const int per = (a.cb.B + kPrepThreads - 1) / kPrepThreads;
-  const PlanShare share = plan_share<kPrepThreads>(
-      (a.cb.B + per - 1) / per, gridDim.x, blockIdx.x,
-      [&](int group) -> long long {
-        long long sum = 0;
-        for (int b = group * per; b < min((group + 1) * per, a.cb.B); ++b) sum += places_of(b);
-        return sum;
-      },
-      1, scratch);
-  int b = share.b * per;
-  long long offset = share.offset;
-  for (bool found = per == 1 || share.start >= share.end; !found;) {  // the sequence of these that holds the share's first tile
-    const long long w = b + lane < a.cb.B ? places_of(b + lane) : 0;
-    long long upto = w;
+  // Sums end at `most`: ranges that share rows may have more tiles than there are places (those behind are left out then).
+  const uint32_t most = static_cast<uint32_t>(p.tiles);
+  auto add = [&](uint32_t x, uint32_t y) -> uint32_t { return min(x + y, most); };
+  auto scan = [&](uint32_t x) -> uint32_t {
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, k);
-      if (lane >= k) upto += y;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, k);
+      if (lane >= k) x = add(x, y);
     }
-    const uint32_t behind = __ballot_sync(0xffffffffu, upto > offset);
-    found = behind != 0 || b >= a.cb.B;
-    const int at = behind != 0 ? __ffs(behind) - 1 : 31;
-    offset -= __shfl_sync(0xffffffffu, behind != 0 ? upto - w : upto, at);
-    b += behind != 0 ? at : 32;
+    return x;
+  };
+  // A thread adds up `per` sequences (2000 sequences of 3 rows, whole calls: 292 us; scanned 256 at a time 314).
+  const int per = (a.cb.B + kPrepThreads - 1) / kPrepThreads;
+  uint32_t mine = 0;
+  for (int b = static_cast<int>(threadIdx.x) * per; b < min((static_cast<int>(threadIdx.x) + 1) * per, a.cb.B); ++b) mine = add(mine, tiles_at(b));
+  mine = scan(mine);
+  auto behind_last = [&](uint32_t x) -> uint32_t {  // of the lane before
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, 1);
+    return lane > 0 ? y : 0;
+  };
+  uint32_t first_of = behind_last(mine);
+  if (lane == 31) s_warp[warp] = mine;
+  if (threadIdx.x == 0) s_group = s_first = 0;
+  __syncthreads();
+  uint32_t sum = 0, below = 0;
+#pragma unroll
+  for (int k = 0; k < WARPS; ++k) {
+    if (k == warp) below = sum;
+    sum = add(sum, s_warp[k]);
   }
-  int tile = static_cast<int>(offset / a.heads), head = static_cast<int>(offset % a.heads);
-  long long before = (share.start - offset) / a.heads;  // tiles of the sequences before b
-  int tiles = 0, tile0 = 0;
+  const uint64_t places = static_cast<uint64_t>(sum) * a.heads;
+  auto over = [](uint64_t x, uint32_t y) -> uint64_t { return x >> 32 ? x / y : static_cast<uint32_t>(x) / y; };
+  const uint64_t share = places <= gridDim.x ? 1 : over(places + gridDim.x - 1, gridDim.x);
+  const uint64_t start = share * blockIdx.x, end = min(start + share, places);
+  const uint32_t tile_at = static_cast<uint32_t>(over(start, a.heads));  // of all sequences'
+  first_of = add(first_of, below);
+  if (first_of <= tile_at && tile_at < add(mine, below)) {
+    s_group = threadIdx.x;
+    s_first = first_of;
+  }
+  __syncthreads();
+  int b = static_cast<int>(s_group) * per;
+  uint32_t before = s_first;  // tiles of the sequences before b
+  for (bool found = per == 1 || start >= end; !found && b < a.cb.B;) {  // the sequence of these that holds the share's first tile
+    const uint32_t y = scan(b + lane < a.cb.B ? tiles_at(b + lane) : 0u), y0 = behind_last(y);
+    const uint32_t behind = __ballot_sync(0xffffffffu, add(before, y) > tile_at);
+    found = behind != 0;
+    const int at = found ? __ffs(behind) - 1 : 31;
+    before = add(before, __shfl_sync(0xffffffffu, found ? y0 : y, at));
+    b += found ? at : 32;
+  }
+  int tile = static_cast<int>(tile_at - before), head = static_cast<int>(start - static_cast<uint64_t>(tile_at) * a.heads);
+  int tiles = 0;
+  uint32_t tile0 = 0;
   CrossSeq s = {};
   auto load = [&]() {
     bool bad;
     s = cross_seq(a.cb, b, bad);
     tiles = tiles_of(s);
-    tile0 = static_cast<int>(min(before, p.tiles - tiles));  // (ranges that share rows may have more tiles than there are places)
+    tile0 = min(before, most - tiles);
   };
-  if (share.start < share.end) load();
-  for (long long x = share.start; x < share.end; ++x) {
+  uint32_t left = start < end ? static_cast<uint32_t>(end - start) : 0u;
+  if (left > 0) load();
+  for (; left > 0; --left) {
     if (tile == 0 && head == 0 && threadIdx.x == 0) p.ws.tile0[b] = tile0;
     const int first = tile * t0;  // token of the tile's first row
 #pragma unroll 1
@@ -1117,7 +1146,7 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
 #pragma unroll
       for (int m = CPR / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
       if (chunk == 0) {
-        const long long at = (head * p.tiles + tile0 + tile) * BS + r;
+        const long long at = (head * p.tiles + static_cast<int>(tile0) + tile) * BS + r;
         p.ws.dsum[at] = valid ? -acc : 0.f;
         p.ws.l2[at] = valid ? -lse * 1.4426950408889634f : -INFINITY;
       }
@@ -1126,8 +1155,8 @@ __global__ void __launch_bounds__(kPrepThreads) fa_cross_prep_kernel(const __gri
     head = 0;
     if (++tile < tiles) continue;
     tile = 0;
-    before += tiles;
-    if (x + 1 == share.end) break;
+    before = add(before, tiles);
+    if (left == 1) break;
     do {
       ++b;
       load();
