@@ -495,7 +495,8 @@ size_t fa_cross_fwd_workspace_bytes(int d);
  *   Rows of a sequence without keys have o = 0 and L = -infinity; rows of no sequence are left as they are.
  *   o and lse must not overlap each other or the inputs.
  *
- * Arithmetic: as fa_paged_fwd's on bf16 pages.  Results do not depend on what else runs.
+ * Arithmetic: as fa_paged_fwd's on bf16 pages (P rounded to bf16 before P v: in the 2-norm O is some 1.1 to 1.25 times
+ * as far from the definition as its own rounding).  Results do not depend on what else runs.
  */
 int fa_cross_fwd(const void* q, const long long* q_stride, const void* k, const long long* k_stride, const void* v,
                  const long long* v_stride, const fa_cross_batch* batch, void* o, const long long* o_stride, float* lse,
@@ -520,7 +521,8 @@ size_t fa_cross_bwd_workspace_bytes(int B, int rows, int q_heads, int heads, int
  *   workspace  : 256-byte aligned, at least fa_cross_bwd_workspace_bytes bytes, as in fa_cross_fwd.
  *   Other arguments as fa_cross_fwd's.  The outputs must not overlap each other or the inputs.
  *
- * Arithmetic: as fa_bwd's (P and dS rounded to bf16 before their products, fp32 sums); deterministic.
+ * Arithmetic: as fa_bwd's (P and dS rounded to bf16 before their products, fp32 sums: in the 2-norm 1.4 times as
+ * far from the definition as the results' own rounding, twice in batches of a few rows); deterministic.
  */
 int fa_cross_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
                  void* dq, void* dk, void* dv, const long long* strides, const fa_cross_batch* batch, int q_heads,

@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kTableThreads, 1) fa_paged_release_kernel(cons
 }
 
 // One cluster of kTableCtas CTAs: 16 is more than every device has to take, so it is asked once (`fit`: 0 not asked, else the
-// CTAs).  With 16 (8, 1) CTAs 200 thousand slots took 12 (17, 85) us, the pages of 128 long sequences 11 (17, 89), a step's 256 rows 6.7
-// with any: a launch, a barrier and the dependent reads of lengths, stack and table.
+// CTAs).  In a graph with 16 (8, 1) CTAs 200 thousand slots take 12.5 (17, 85) us, the pages of 128 long sequences 11.2 (17, 89), a step's 256
+// rows 6.6 with any: a launch, a barrier and the dependent reads of lengths, stack and table.
 int launch_cluster(void (*kernel)(const TableArgs), const TableArgs& a, std::atomic<int> (&fit)[64], cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kTableThreads);
@@ -407,7 +407,7 @@ int fa_paged_release(const fa_page_pool* pool, int* page_table, long long table_
   a.done = done;
   a.status = ctx.status;
   // Long rows of few sequences are shared out until every warp of the cluster has two parts (the pages of 17 of 256 sequences of up to
-  // 512: 6.3 us; with one part a warp 7.2).
+  // 512: 6.5 us; with one part a warp 7.2).
   while (a.parts_log2 < 10 && (static_cast<long long>(B) << a.parts_log2) < 32 * fa::kTableWarps && (max_pages >> a.parts_log2) > 64)
     ++a.parts_log2;
   static std::atomic<int> fit[64];
